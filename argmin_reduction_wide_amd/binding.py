@@ -46,7 +46,10 @@ EXPORTS = ("argreduce_scratch_bytes", "argreduce_lastaxis", "argreduce_plan",
            "argreduce_scan_scratch_bytes", "argreduce_scan_lastaxis", "argreduce_scan_plan",
            "argreduce_debug_set_window", "argreduce_debug_launch_store",
            "argreduce_debug_set_spin_limit", "argreduce_debug_launch_read",
-           "argreduce_wait_timeouts", "argreduce_lastaxis_noalloc")
+           "argreduce_wait_timeouts", "argreduce_lastaxis_noalloc",
+           "argreduce_logprobs_scratch_bytes", "argreduce_logprobs", "argreduce_logprobs_plan",
+           "argreduce_logprobs_grad", "argreduce_distill_scratch_bytes", "argreduce_distill",
+           "argreduce_distill_plan", "argreduce_distill_grad", "argreduce_distill_step")
 
 
 class ArgreduceError(RuntimeError):
@@ -132,6 +135,24 @@ def lib() -> ctypes.CDLL:
                 h.argreduce_debug_launch_empty.restype = c_int
                 h.argreduce_debug_set_kernel_events.argtypes = [vp, vp]
                 h.argreduce_debug_set_kernel_events.restype = c_int
+                i32, f32 = ctypes.c_int32, ctypes.c_float
+                logits = [vp, c_int, i64, i64, i64]  # x, dtype, rows, cols, row_stride
+                teacher = [i32, vp, vp, f32]  # k, teacher_tokens, teacher_logits, temperature
+                for name in ("logprobs", "distill"):
+                    f = getattr(h, f"argreduce_{name}_scratch_bytes")
+                    f.argtypes, f.restype = [i64, i64, c_int], sz
+                    f = getattr(h, f"argreduce_{name}_plan")
+                    f.argtypes, f.restype = [i64, i64, c_int, ctypes.POINTER(argreduce_plan_t)], c_int
+                h.argreduce_logprobs.argtypes = logits + [vp, f32, i32, i32, vp, vp, vp, vp, sz, vp]
+                h.argreduce_logprobs.restype = c_int
+                h.argreduce_logprobs_grad.argtypes = logits + [vp, f32, vp, vp, vp, vp, vp]
+                h.argreduce_logprobs_grad.restype = c_int
+                h.argreduce_distill.argtypes = logits + teacher + [vp, vp, sz, vp]
+                h.argreduce_distill.restype = c_int
+                h.argreduce_distill_grad.argtypes = logits + teacher + [vp, vp, vp, vp]
+                h.argreduce_distill_grad.restype = c_int
+                h.argreduce_distill_step.argtypes = logits + teacher + [vp, vp, vp, vp, sz, vp]
+                h.argreduce_distill_step.restype = c_int
                 _bind_fast(h)
                 _lib = h
     return _lib
@@ -153,6 +174,10 @@ def _bind_fast(h: ctypes.CDLL) -> None:
     m.bind(addr(h.argreduce_lastaxis), addr(h.argreduce_axis), addr(h.argreduce_scan_lastaxis),
            addr(h.argreduce_debug_launch_empty), addr(h.argreduce_debug_launch_store),
            addr(h.argreduce_debug_launch_read))
+    m.bind_logits(addr(h.argreduce_logprobs_scratch_bytes), addr(h.argreduce_distill_scratch_bytes),
+                  addr(h.argreduce_logprobs), addr(h.argreduce_logprobs_grad),
+                  addr(h.argreduce_distill), addr(h.argreduce_distill_grad),
+                  addr(h.argreduce_distill_step))
     _fast = m
 
 
@@ -248,6 +273,74 @@ def argreduce_scan_plan(rows: int, cols: int, dtype) -> dict:
     if rc != OK:
         raise ArgreduceError(rc, "argreduce_scan_plan")
     return p.as_dict()
+
+
+def argreduce_logprobs_scratch_bytes(rows: int, cols: int, dtype) -> int:
+    return entry_point("argreduce_logprobs_scratch_bytes")(rows, cols, _dtype_code(dtype))
+
+
+def argreduce_logprobs(x_ptr: int, dtype, rows: int, cols: int, row_stride: int, tokens_ptr: int,
+                       temperature: float, entropy: int, top: int, stats_ptr: int,
+                       top_logprobs_ptr: int, top_tokens_ptr: int, scratch_ptr: int,
+                       scratch_bytes: int, stream: int) -> int:
+    return entry_point("argreduce_logprobs")(
+        x_ptr, _dtype_code(dtype), rows, cols, row_stride, tokens_ptr, temperature, entropy, top,
+        stats_ptr, top_logprobs_ptr, top_tokens_ptr, scratch_ptr, scratch_bytes, stream)
+
+
+def argreduce_logprobs_grad(x_ptr: int, dtype, rows: int, cols: int, row_stride: int,
+                            tokens_ptr: int, temperature: float, stats_ptr: int,
+                            grad_logprob_ptr: int, grad_entropy_ptr: int, grad_ptr: int,
+                            stream: int) -> int:
+    return entry_point("argreduce_logprobs_grad")(
+        x_ptr, _dtype_code(dtype), rows, cols, row_stride, tokens_ptr, temperature, stats_ptr,
+        grad_logprob_ptr, grad_entropy_ptr, grad_ptr, stream)
+
+
+def _logits_plan(name: str, rows: int, cols: int, dtype) -> dict:
+    p = argreduce_plan_t()
+    rc = getattr(lib(), name)(rows, cols, _dtype_code(dtype), ctypes.byref(p))
+    if rc != OK:
+        raise ArgreduceError(rc, name)
+    return p.as_dict()
+
+
+def argreduce_logprobs_plan(rows: int, cols: int, dtype) -> dict:
+    return _logits_plan("argreduce_logprobs_plan", rows, cols, dtype)
+
+
+def argreduce_distill_plan(rows: int, cols: int, dtype) -> dict:
+    return _logits_plan("argreduce_distill_plan", rows, cols, dtype)
+
+
+def argreduce_distill_scratch_bytes(rows: int, cols: int, dtype) -> int:
+    return entry_point("argreduce_distill_scratch_bytes")(rows, cols, _dtype_code(dtype))
+
+
+def argreduce_distill(x_ptr: int, dtype, rows: int, cols: int, row_stride: int, k: int,
+                      teacher_tokens_ptr: int, teacher_logits_ptr: int, temperature: float,
+                      stats_ptr: int, scratch_ptr: int, scratch_bytes: int, stream: int) -> int:
+    return entry_point("argreduce_distill")(
+        x_ptr, _dtype_code(dtype), rows, cols, row_stride, k, teacher_tokens_ptr,
+        teacher_logits_ptr, temperature, stats_ptr, scratch_ptr, scratch_bytes, stream)
+
+
+def argreduce_distill_grad(x_ptr: int, dtype, rows: int, cols: int, row_stride: int, k: int,
+                           teacher_tokens_ptr: int, teacher_logits_ptr: int, temperature: float,
+                           stats_ptr: int, grad_loss_ptr: int, grad_ptr: int, stream: int) -> int:
+    return entry_point("argreduce_distill_grad")(
+        x_ptr, _dtype_code(dtype), rows, cols, row_stride, k, teacher_tokens_ptr,
+        teacher_logits_ptr, temperature, stats_ptr, grad_loss_ptr, grad_ptr, stream)
+
+
+def argreduce_distill_step(x_ptr: int, dtype, rows: int, cols: int, row_stride: int, k: int,
+                           teacher_tokens_ptr: int, teacher_logits_ptr: int, temperature: float,
+                           weights_ptr: int, stats_ptr: int, grad_ptr: int, scratch_ptr: int,
+                           scratch_bytes: int, stream: int) -> int:
+    return entry_point("argreduce_distill_step")(
+        x_ptr, _dtype_code(dtype), rows, cols, row_stride, k, teacher_tokens_ptr,
+        teacher_logits_ptr, temperature, weights_ptr, stats_ptr, grad_ptr, scratch_ptr,
+        scratch_bytes, stream)
 
 
 def argreduce_debug_set_capacity(threads: int) -> int:

@@ -16,6 +16,7 @@
 
 #include "argreduce.h"
 #include "argreduce_internal.hpp"
+#include "argreduce_logits.hpp"
 
 #define ARGREDUCE_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -464,6 +465,9 @@ int make_scan_plan(int64_t rows, int64_t cols, int dtype, bool aligned, ScanPlan
 }
 
 }  // namespace
+
+int plan_device_threads(int64_t* threads) { return device_threads(threads); }
+
 }  // namespace argreduce
 
 using argreduce::AxisPlan;

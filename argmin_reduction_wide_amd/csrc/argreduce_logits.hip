@@ -1,0 +1,1211 @@
+// Logits operators for gfx950: log probabilities of given tokens with entropy and top
+// alternatives, and distillation from a teacher's top logits, each with its gradient.
+//
+// Mathematics. For a row x of logits, m = max x, k = log2(e) / T:
+//   z_j = (x_j - m) k        (base-2 exponents, <= 0)
+//   s   = sum 2^z_j,  h = sum 2^z_j z_j,  p_j = 2^(z_j - log2 s)
+//   logprob of t  = ln 2 (z_t - log2 s)
+//   entropy       = ln 2 (log2 s - h / s)
+// (m, s, h) of two parts of a row merge exactly as in an online softmax: moving a part from
+// its own maximum m' to m = m' + d / k turns s into 2^-d s and h into 2^-d (h - d s). Every
+// statistic is held in binary32; the one rounding to the logits' type is a gradient's store.
+//
+// What bounds the forward kernels is the read of the logits: per element one subtraction, one
+// multiplication, one exponential and one addition (two more operations with the entropy),
+// which the vector units do about as fast as HBM delivers 16-bit elements.
+//
+// Masked logits are -inf: 2^-inf = 0 and the h term is cut off at z = -16384, where 2^z is 0
+// already, so that 0 * inf does not arise. A running maximum starts at the lowest finite
+// number, never at -inf, so that x - m is never inf - inf; a row whose every element is -inf
+// ends with s = 0. NaN and +inf make s NaN.
+#include <hip/hip_runtime.h>
+
+#include "argreduce_device.hpp"
+#include "argreduce_launch.hpp"
+#include "argreduce_logits.hpp"
+
+namespace argreduce {
+namespace {
+
+constexpr float kLowest = -3.402823466e+38f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kZFloor = -16384.0f;
+constexpr uint32_t kNoVec = 0xffffffffu;
+
+// ---------------------------------------------------------------------------------------
+// Kernel arguments. All of a kernel's arguments have to fit the 14 dwords that the hardware
+// preloads into SGPRs at wave launch; the kernels with six pointers get there by carrying
+// 16-bit values in the unused upper bits of 48-bit device addresses.
+
+constexpr int kAddrBits = 48;
+template <typename T>
+__device__ inline T* addr(uint64_t a) {
+    return reinterpret_cast<T*>(a & ((uint64_t{1} << kAddrBits) - 1));
+}
+__device__ inline uint32_t tag(uint64_t a) { return static_cast<uint32_t>(a >> kAddrBits); }
+__device__ inline uint32_t tags(uint64_t lo, uint64_t hi) { return tag(lo) | (tag(hi) << 16); }
+
+inline uint64_t tagged(const void* p, uint32_t t) {
+    return reinterpret_cast<uintptr_t>(p) | (static_cast<uint64_t>(t & 0xffffu) << kAddrBits);
+}
+inline uint32_t bits_of(float f) { return __builtin_bit_cast(uint32_t, f); }
+
+// ---------------------------------------------------------------------------------------
+// Arithmetic and lanes
+
+__device__ inline float exp2_f(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ inline float log2_f(float v) { return __builtin_amdgcn_logf(v); }
+// One instruction each; the C functions add a canonicalisation of every operand.
+__device__ inline float max_f(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ inline float max3_f(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+// Reduction over aligned groups of G lanes; every lane gets the result, and the same one:
+// each step combines two values that all lanes of a half share.
+template <int G, typename Op>
+__device__ inline float lanes_all(float v, Op op) {
+    if constexpr (G >= 2) v = op(v, dpp_val<0xB1, 0xf>(v));
+    if constexpr (G >= 4) v = op(v, dpp_val<0x4E, 0xf>(v));
+    if constexpr (G >= 8) v = op(v, dpp_val<0x141, 0xf>(v));
+    if constexpr (G >= 16) v = op(v, dpp_val<0x140, 0xf>(v));
+    if constexpr (G >= 32) v = op(v, __shfl_xor(v, 16));
+    if constexpr (G >= 64) v = op(v, __shfl_xor(v, 32));
+    return v;
+}
+template <int G>
+__device__ inline float lanes_max(float v) {
+    return lanes_all<G>(v, [](float a, float b) { return max_f(a, b); });
+}
+template <int G>
+__device__ inline float lanes_sum(float v) {
+    return lanes_all<G>(v, [](float a, float b) { return a + b; });
+}
+
+// A team is one wavefront (T == 64, four teams to a workgroup) or one workgroup of T threads.
+template <int T>
+__device__ inline void team_sync() {
+    if constexpr (T == kWave) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    } else {
+        __syncthreads();
+    }
+}
+
+template <int T>
+constexpr int kTeamsPerBlock = T == kWave ? kBlockThreads / kWave : 1;
+template <int T>
+constexpr int kTeamBlock = T == kWave ? kBlockThreads : T;
+
+// ln p of a logit v in a row of maximum m: in units of e, not of 2, since (v - m) k can leave
+// binary32's range where (v - m) / T does not (v the lowest finite value, as some masks have it).
+__device__ inline float ln_p(float v, float m, float l2, float scale) {
+    return (v - m) * (scale * kLn2) - l2 * kLn2;
+}
+
+struct Stat {
+    float m, s, h;
+    __device__ void init() {
+        m = kLowest;
+        s = 0.0f;
+        h = 0.0f;
+    }
+    // Expresses the part relative to the maximum `to` >= m.
+    template <bool ENT>
+    __device__ void move(float to, float k) {
+        const float d = (to - m) * k;
+        const float r = exp2_f(-d);
+        if constexpr (ENT) h = r * (h - fminf(d, -kZFloor) * s);
+        s *= r;
+        m = to;
+    }
+};
+
+// Merges the lanes' parts; every thread of the team gets the row's.
+template <bool ENT, int T>
+__device__ inline void team_merge(Stat& a, float k, int lane, float (*sh)[4]) {
+    a.move<ENT>(lanes_max<kWave>(a.m), k);
+    a.s = lanes_sum<kWave>(a.s);
+    if constexpr (ENT) a.h = lanes_sum<kWave>(a.h);
+    if constexpr (T > kWave) {
+        constexpr int kWaves = T / kWave;
+        const int wave = lane / kWave;
+        if (lane % kWave == 0) {
+            sh[wave][0] = a.m;
+            sh[wave][1] = a.s;
+            sh[wave][2] = a.h;
+        }
+        __syncthreads();
+        float m = sh[0][0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) m = max_f(m, sh[w][0]);
+        Stat all{m, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            Stat b{sh[w][0], sh[w][1], ENT ? sh[w][2] : 0.0f};
+            b.move<ENT>(m, k);
+            all.s += b.s;
+            all.h += b.h;
+        }
+        a = all;
+        __syncthreads();
+    }
+}
+
+template <int T, bool MAX>
+__device__ inline float team_reduce(float v, int lane, float (*sh)[4]) {
+    v = MAX ? lanes_max<kWave>(v) : lanes_sum<kWave>(v);
+    if constexpr (T > kWave) {
+        if (lane % kWave == 0) sh[lane / kWave][3] = v;
+        __syncthreads();
+        v = sh[0][3];
+#pragma unroll
+        for (int w = 1; w < T / kWave; ++w) v = MAX ? max_f(v, sh[w][3]) : v + sh[w][3];
+        __syncthreads();
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------------------
+// A row as the aligned 16-byte vectors that its bytes lie in. Vector v holds the elements
+// v * VW - off .. + VW - 1; vectors [va, vb) lie wholly in the row, the first and the last may
+// not ("edges", lanes 0 and 1). An edge vector is read whole: it holds a byte of the row, so
+// it lies in a mapped page.
+
+template <typename Fmt>
+struct Span {
+    const uint8_t* base;
+    uint32_t off, cols, vs, va, vb;
+    __device__ Span(const uint8_t* row, uint32_t n) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(row);
+        base = row - (a & 15);
+        off = static_cast<uint32_t>(a & 15) / Fmt::kSize;
+        cols = n;
+        const uint32_t end = off + n;  // n <= INT32_MAX
+        vs = (end + Fmt::VW - 1) / Fmt::VW;
+        va = off ? 1 : 0;
+        vb = end % Fmt::VW ? vs - 1 : vs;
+        vb = vb < va ? va : vb;
+    }
+    // The edge vector of lane 0 or 1, or kNoVec.
+    __device__ uint32_t edge(int lane) const {
+        if (lane == 0) return off ? 0u : kNoVec;
+        return (lane == 1 && (off + cols) % Fmt::VW && (vs > 1 || !off)) ? vs - 1 : kNoVec;
+    }
+    __device__ const uint8_t* at(uint32_t v) const { return base + static_cast<size_t>(v) * 16; }
+    // Position of element 0 of vector v (wraps for elements before the row).
+    __device__ uint32_t pos(uint32_t v) const { return v * Fmt::VW - off; }
+};
+
+template <typename Fmt>
+__device__ inline typename Fmt::Vec load16(const uint8_t* p) {
+    return *reinterpret_cast<const typename Fmt::Vec*>(p);
+}
+
+// Takes N elements into the running part.
+template <bool ENT, int N>
+__device__ inline void take(const float (&e)[N], float k, Stat& a) {
+    float m = a.m;
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) m = max3_f(m, e[i], e[i + 1]);
+    if constexpr (N % 2) m = max_f(m, e[N - 1]);
+    a.move<ENT>(m, k);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float z = (e[i] - m) * k;
+        const float p = exp2_f(z);
+        a.s += p;
+        if constexpr (ENT) a.h = fmaf(p, max_f(z, kZFloor), a.h);
+    }
+}
+
+// One lane's share of a row: its edge vector, then vectors first + lane, + T, ... below last.
+template <typename Fmt, bool ENT, int T, int U>
+__device__ inline void scan_span(const Span<Fmt>& sp, bool edges, uint32_t first, uint32_t last,
+                                 int lane, float k, Stat& a) {
+    constexpr int VW = Fmt::VW;
+    a.init();
+    if (edges) {
+        const uint32_t ev = sp.edge(lane);
+        if (ev != kNoVec) {
+            float e[VW];
+            Fmt::unpack(load16<Fmt>(sp.at(ev)), e);
+            const uint32_t p0 = sp.pos(ev);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) e[i] = p0 + i < sp.cols ? e[i] : -__builtin_huge_valf();
+            take<ENT>(e, k, a);
+        }
+    }
+    uint32_t v = first + lane;
+    for (; v + (U - 1) * T < last; v += U * T) {
+        typename Fmt::Vec q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = load16<Fmt>(sp.at(v + u * T));
+        float e[U * VW];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[VW];
+            Fmt::unpack(q[u], f);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) e[u * VW + i] = f[i];
+        }
+        take<ENT>(e, k, a);
+    }
+    for (; v < last; v += T) {
+        float e[VW];
+        Fmt::unpack(load16<Fmt>(sp.at(v)), e);
+        take<ENT>(e, k, a);
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// The k best elements of a row, by (value descending, position ascending).
+//
+// A pass over the row leaves the maximum of each of S segments (a lane's or a wavefront's
+// share). With tau the k-th largest of those maxima, the k best elements are all >= tau and
+// lie in segments whose maximum is >= tau: only these are read again, from the caches, and
+// their elements >= tau collected in LDS as 64-bit keys (value above complemented position).
+// Ranking the keys by counting gives the sorted result. Ties may put more keys into the
+// buffer than it holds; the collection then starts again in steps that cannot overflow it, the
+// buffer cut to its k best in between.
+
+__device__ inline uint64_t key_of(float v, uint32_t pos) { return Key32<kMax>::make(v, pos); }
+
+template <int T, int S>
+struct TopLds {
+    static constexpr int kCap = 4 * T + kTopMax;
+    uint64_t buf[kCap];
+    uint64_t best[T];
+    float seg[S];
+    uint16_t list[S];
+    uint32_t count, listed;
+    uint64_t least;  // keys at or below it cannot be among the k best
+    float tau;
+};
+
+// Cuts the buffer to its k best keys, sorted. Called by the whole team after a team_sync.
+template <int T, int S>
+__device__ inline void top_cut(TopLds<T, S>& L, int lane, uint32_t k) {
+    constexpr int kPer = (TopLds<T, S>::kCap + T - 1) / T;
+    uint32_t n = L.count;
+    if (n > 2 * kTopMax + 64) {
+        // the k-th largest of the threads' own maxima bounds the k-th best key from below
+        uint64_t mine[kPer], top = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const uint32_t i = lane + j * T;
+            mine[j] = i < n ? L.buf[i] : 0;
+            top = mine[j] > top ? mine[j] : top;
+        }
+        L.best[lane] = top;
+        if (lane == 0) L.least = 0;
+        team_sync<T>();
+        uint32_t above = 0;
+        for (int j = 0; j < T; ++j) above += L.best[j] > top ? 1 : 0;
+        if (top != 0 && above == k - 1) L.least = top;
+        if (lane == 0) L.count = 0;
+        team_sync<T>();
+        const uint64_t least = L.least;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (mine[j] != 0 && mine[j] >= least) L.buf[atomicAdd(&L.count, 1u)] = mine[j];
+        team_sync<T>();
+        n = L.count;
+    }
+    for (uint32_t i = lane; i < n; i += T) {
+        const uint64_t key = L.buf[i];
+        uint32_t above = 0;
+        for (uint32_t j = 0; j < n; ++j) above += L.buf[j] > key ? 1 : 0;
+        if (above < k) L.best[above] = key;
+    }
+    team_sync<T>();
+    const uint32_t kept = n < k ? n : k;
+    if (static_cast<uint32_t>(lane) < kept) L.buf[lane] = L.best[lane];
+    if (lane == 0) {
+        L.count = kept;
+        L.least = kept == k ? L.best[k - 1] : 0;
+    }
+    team_sync<T>();
+}
+
+// Four elements of a vector: half of one of 16-bit elements.
+template <typename Fmt>
+__device__ inline void load4(const uint8_t* p, float (&e)[4]) {
+    if constexpr (Fmt::kSize == 4) {
+        F32::unpack(load16<F32>(p), e);
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        e[0] = Fmt::from_bits(static_cast<uint16_t>(w.x));
+        e[1] = Fmt::from_bits(static_cast<uint16_t>(w.x >> 16));
+        e[2] = Fmt::from_bits(static_cast<uint16_t>(w.y));
+        e[3] = Fmt::from_bits(static_cast<uint16_t>(w.y >> 16));
+    }
+}
+
+// segs maxima are in L.seg. `vec(seg, i)` names vector i (of per_seg) of a segment, or kNoVec.
+// Leaves the k best (fewer if the row has fewer) in L.buf, their number in L.count.
+template <typename Fmt, int T, int S, typename VecOf>
+__device__ inline void top_select(TopLds<T, S>& L, const Span<Fmt>& sp, uint32_t segs,
+                                  uint32_t per_seg, uint32_t k, int lane, VecOf vec) {
+    constexpr uint32_t kParts = Fmt::VW / 4;  // 4-element parts of a vector
+    if (lane == 0) {
+        L.count = 0;
+        L.listed = 0;
+        L.least = 0;
+        L.tau = kLowest;
+    }
+    team_sync<T>();
+    for (uint32_t s = lane; s < segs; s += T) {
+        const float m = L.seg[s];
+        uint32_t above = 0, reach = 0;
+        for (uint32_t j = 0; j < segs; ++j) {
+            const float o = L.seg[j];
+            above += o > m ? 1 : 0;
+            reach += o >= m ? 1 : 0;
+        }
+        if (above < k) {
+            L.list[atomicAdd(&L.listed, 1u)] = static_cast<uint16_t>(s);
+            if (reach >= k) L.tau = m;  // every segment that gets here holds the same value
+        }
+    }
+    team_sync<T>();
+    const float tau = L.tau;
+    const uint32_t main_items = L.listed * per_seg * kParts;
+    const uint32_t items = main_items + 2 * kParts;  // and the edges
+    const auto visit = [&](uint32_t it, uint64_t least, bool bounded) {
+        const uint32_t part = it % kParts;
+        uint32_t v;
+        if (it < main_items) {
+            const uint32_t u = it / kParts;
+            v = vec(L.list[u / per_seg], u % per_seg);
+        } else {
+            v = sp.edge(static_cast<int>((it - main_items) / kParts));
+        }
+        if (v == kNoVec) return;
+        float e[4];
+        load4<Fmt>(sp.at(v) + part * 4 * Fmt::kSize, e);
+        const uint32_t p0 = sp.pos(v) + part * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (e[i] >= tau && p0 + i < sp.cols) {
+                const uint64_t key = key_of(e[i], p0 + i);
+                if (key > least) {
+                    const uint32_t at = atomicAdd(&L.count, 1u);
+                    if (!bounded || at < TopLds<T, S>::kCap) L.buf[at] = key;
+                }
+            }
+        }
+    };
+    for (uint32_t it = lane; it < items; it += T) visit(it, 0, true);
+    team_sync<T>();
+    if (L.count > TopLds<T, S>::kCap) {
+        team_sync<T>();
+        if (lane == 0) L.count = 0;
+        for (uint32_t base = 0; base < items; base += T) {
+            team_sync<T>();
+            if (L.count > kTopMax) top_cut(L, lane, k);  // at most 4 T more keys fit
+            const uint64_t least = L.least;
+            team_sync<T>();
+            if (base + lane < items) visit(base + lane, least, false);
+        }
+        team_sync<T>();
+    }
+    top_cut(L, lane, k);
+}
+
+// Writes a row's alternatives from L.buf, or k empty ones.
+template <int T, int S>
+__device__ inline void top_store(const TopLds<T, S>& L, uint32_t k, int lane, const Stat& a,
+                                 float scale, float l2, float* lp, int64_t* tok) {
+    if (static_cast<uint32_t>(lane) < k) {
+        if (static_cast<uint32_t>(lane) < L.count) {
+            float v;
+            uint32_t i;
+            Key32<kMax>::split(L.buf[lane], v, i);
+            lp[lane] = ln_p(v, a.m, l2, scale);
+            tok[lane] = i;
+        } else {
+            lp[lane] = -__builtin_huge_valf();
+            tok[lane] = -1;
+        }
+    }
+}
+__device__ inline void top_none(uint32_t k, int lane, int step, float v, float* lp, int64_t* tok) {
+    for (uint32_t i = lane; i < k; i += step) {
+        lp[i] = v;
+        tok[i] = -1;
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// Log probabilities: outputs of one row.
+
+struct RowOut {
+    float logprob, entropy, m, l2;
+};
+// stats is [4, rows]: log probability, entropy, maximum, log2 of the sum.
+__device__ inline void store_stats(float* stats, uint32_t rows, uint32_t r, const RowOut& o) {
+    stats[r] = o.logprob;
+    stats[static_cast<size_t>(rows) + r] = o.entropy;
+    stats[2 * static_cast<size_t>(rows) + r] = o.m;
+    stats[3 * static_cast<size_t>(rows) + r] = o.l2;
+}
+template <bool ENT>
+__device__ inline RowOut row_out(const Stat& a, float xt, float scale) {
+    RowOut o;
+    o.m = a.m;
+    o.l2 = log2_f(a.s);
+    o.logprob = ln_p(xt, a.m, o.l2, scale);
+    o.entropy = ENT ? (o.l2 - a.h / a.s) * kLn2 : __builtin_nanf("");
+    if (a.s == 0.0f) {  // every logit is -inf, and xt too unless its token is none of the row's
+        o.logprob = xt != xt ? xt : -__builtin_huge_valf();
+        if (ENT) o.entropy = 0.0f;
+    }
+    return o;
+}
+template <bool ENT>
+__device__ inline RowOut row_left_out() {
+    return {0.0f, ENT ? 0.0f : __builtin_nanf(""), 0.0f, 0.0f};
+}
+template <typename Fmt>
+__device__ inline float load_at(const uint8_t* row, int64_t t, uint32_t cols) {
+    return t < static_cast<int64_t>(cols) ? Fmt::load1(row + t * Fmt::kSize) : __builtin_nanf("");
+}
+template <typename Fmt>
+__device__ inline const uint8_t* row_ptr(const void* x, uint32_t r, uint32_t stride) {
+    return static_cast<const uint8_t*>(x) + static_cast<size_t>(r) * stride * Fmt::kSize;
+}
+
+// Rows of at most G vectors, G lanes each, the row held in registers: maximum first, then the
+// exponentials. Alternatives are taken one by one, as the largest key left.
+template <typename Fmt, bool ENT, int G>
+__global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint32_t cols,
+                                                            uint32_t stride, float scale,
+                                                            uint32_t rows, const int64_t* tokens,
+                                                            float* stats, uint64_t top_lp,
+                                                            int64_t* top_tok) {
+    constexpr int VW = Fmt::VW;
+    const uint32_t k = tag(top_lp);
+    const uint32_t want = blockIdx.x * (kBlockThreads / G) + threadIdx.x / G;
+    const uint32_t r = want < rows ? want : rows - 1;  // lanes past the end repeat the last row
+    const int lane = threadIdx.x % G;
+    const uint8_t* row = row_ptr<Fmt>(x, r, stride);
+    const int64_t t = tokens[r];
+    const bool live = t >= 0;
+    const Span<Fmt> sp(row, cols);
+    float e[VW];
+#pragma unroll
+    for (int i = 0; i < VW; ++i) e[i] = -__builtin_huge_valf();
+    if (live && static_cast<uint32_t>(lane) < sp.vs) {
+        Fmt::unpack(load16<Fmt>(sp.at(lane)), e);
+        const uint32_t p0 = sp.pos(lane);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) e[i] = p0 + i < cols ? e[i] : -__builtin_huge_valf();
+    }
+    const float xt = live ? load_at<Fmt>(row, t, cols) : 0.0f;
+    Stat a;
+    a.init();
+    float m = a.m;
+#pragma unroll
+    for (int i = 0; i < VW; i += 2) m = max3_f(m, e[i], e[i + 1]);
+    a.m = lanes_max<G>(m);
+    take<ENT>(e, scale, a);
+    a.s = lanes_sum<G>(a.s);
+    if constexpr (ENT) a.h = lanes_sum<G>(a.h);
+    const RowOut o = live ? row_out<ENT>(a, xt, scale) : row_left_out<ENT>();
+    if (lane == 0 && want < rows) store_stats(stats, rows, r, o);
+    if (k == 0) return;
+    float* lp = addr<float>(top_lp) + static_cast<size_t>(r) * k;
+    int64_t* tok = top_tok + static_cast<size_t>(r) * k;
+    uint64_t key[VW];
+    const uint32_t p0 = sp.pos(lane);
+    const bool ok = a.s == a.s;  // a row with NaN or +inf has no alternatives
+#pragma unroll
+    for (int i = 0; i < VW; ++i) key[i] = (ok && e[i] >= kLowest) ? key_of(e[i], p0 + i) : 0;
+    for (uint32_t j = 0; j < k; ++j) {
+        uint64_t b = 0;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) b = key[i] > b ? key[i] : b;
+        if constexpr (G >= 2) b = dpp_max_key<0xB1, 0xf>(b);
+        if constexpr (G >= 4) b = dpp_max_key<0x4E, 0xf>(b);
+        if constexpr (G >= 8) b = dpp_max_key<0x141, 0xf>(b);
+        if constexpr (G >= 16) b = dpp_max_key<0x140, 0xf>(b);
+        if constexpr (G >= 32) {
+            const uint64_t other = __shfl_xor(static_cast<unsigned long long>(b), 16);
+            b = other > b ? other : b;
+        }
+#pragma unroll
+        for (int i = 0; i < VW; ++i) key[i] = key[i] == b ? 0 : key[i];
+        if (lane == 0 && want < rows) {
+            float v;
+            uint32_t i;
+            Key32<kMax>::split(b, v, i);
+            lp[j] = b != 0 ? ln_p(v, a.m, o.l2, scale)
+                           : (ok ? -__builtin_huge_valf() : __builtin_nanf(""));
+            tok[j] = b != 0 ? static_cast<int64_t>(i) : -1;
+        }
+    }
+}
+
+// A team of T lanes per row.
+template <typename Fmt, bool ENT, bool TOP, int T>
+__global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32_t cols,
+                                                           uint32_t stride, float scale,
+                                                           uint32_t rows, const int64_t* tokens,
+                                                           float* stats, uint64_t top_lp,
+                                                           int64_t* top_tok) {
+    constexpr int kTeams = kTeamsPerBlock<T>;
+    constexpr int kSegs = T < 256 ? T : 256;  // segments of a row: a lane's share, or a few lanes'
+    constexpr int kSub = T / kSegs;
+    constexpr int U = 16 / Fmt::VW;
+    __shared__ float sh[T / kWave][4];
+    __shared__ TopLds<TOP ? T : 1, TOP ? kSegs : 1> lds[TOP ? kTeams : 1];
+    const uint32_t team = threadIdx.x / T;
+    const uint32_t r = blockIdx.x * kTeams + team;
+    const int lane = threadIdx.x % T;
+    if (r >= rows) return;  // whole teams, and never one of several wavefronts
+    const int64_t t = tokens[r];
+    const uint32_t k = tag(top_lp);
+    float* lp = addr<float>(top_lp) + static_cast<size_t>(r) * k;
+    int64_t* tok = top_tok + static_cast<size_t>(r) * k;
+    if (t < 0) {
+        if (lane == 0) store_stats(stats, rows, r, row_left_out<ENT>());
+        if constexpr (TOP) top_none(k, lane, T, -__builtin_huge_valf(), lp, tok);
+        return;
+    }
+    const uint8_t* row = row_ptr<Fmt>(x, r, stride);
+    const float xt = load_at<Fmt>(row, t, cols);
+    const Span<Fmt> sp(row, cols);
+    Stat a;
+    scan_span<Fmt, ENT, T, U>(sp, true, sp.va, sp.vb, lane, scale, a);
+    const float mine = a.m;
+    team_merge<ENT, T>(a, scale, lane, sh);
+    const RowOut o = row_out<ENT>(a, xt, scale);
+    if (lane == 0) store_stats(stats, rows, r, o);
+    if constexpr (TOP) {
+        if (!(a.s > 0.0f)) {
+            top_none(k, lane, T, a.s == 0.0f ? -__builtin_huge_valf() : __builtin_nanf(""), lp, tok);
+            return;
+        }
+        auto& L = lds[team];
+        const float seg = lanes_max<kSub>(mine);
+        if (lane % kSub == 0) L.seg[lane / kSub] = seg;
+        const uint32_t per_lane = (sp.vb - sp.va + T - 1) / T;
+        top_select<Fmt, T, kSegs>(L, sp, kSegs, per_lane * kSub, k, lane, [&](uint32_t s, uint32_t i) {
+            const uint32_t v = sp.va + s * kSub + i % kSub + (i / kSub) * T;
+            return v < sp.vb ? v : kNoVec;
+        });
+        top_store(L, k, lane, a, scale, o.l2, lp, tok);
+    }
+}
+
+// Slice b of a row split over `parts` workgroups: vectors [first, last).
+__device__ inline uint32_t part_vecs(uint32_t span_max, uint32_t parts) {
+    return (span_max + parts - 1) / parts;
+}
+template <typename Fmt>
+__device__ inline uint32_t span_max(uint32_t cols) {  // vectors of the worst aligned row
+    return cols / Fmt::VW + 2;
+}
+struct Part {  // what a slice leaves in scratch
+    float m, s, h, pad;
+    float wave_max[kPartThreads / kWave];
+};
+
+template <typename Fmt, bool ENT>
+__global__ __launch_bounds__(kPartThreads) void k_part(const void* x, uint32_t cols, uint32_t stride,
+                                                       float scale, uint32_t parts,
+                                                       const int64_t* tokens, Part* out) {
+    __shared__ float sh[kPartThreads / kWave][4];
+    const uint32_t r = blockIdx.x / parts;
+    const uint32_t b = blockIdx.x - r * parts;
+    if (tokens != nullptr && tokens[r] < 0) return;
+    const Span<Fmt> sp(row_ptr<Fmt>(x, r, stride), cols);
+    const uint32_t n = part_vecs(span_max<Fmt>(cols), parts);
+    uint32_t first = sp.va + b * n;
+    first = first < sp.vb ? first : sp.vb;
+    const uint32_t last = sp.vb - first < n ? sp.vb : first + n;
+    const int lane = threadIdx.x;
+    Stat a;
+    scan_span<Fmt, ENT, kPartThreads, kPartUnroll>(sp, b == 0, first, last, lane, scale, a);
+    const float wave_max = lanes_max<kWave>(a.m);
+    team_merge<ENT, kPartThreads>(a, scale, lane, sh);
+    if (lane % kWave == 0) out[blockIdx.x].wave_max[lane / kWave] = wave_max;
+    if (lane == 0) {
+        out[blockIdx.x].m = a.m;
+        out[blockIdx.x].s = a.s;
+        out[blockIdx.x].h = a.h;
+    }
+}
+
+constexpr int kMergeThreads = 256;
+
+// The merged statistics of a split row, in every thread.
+template <bool ENT>
+__device__ inline Stat merge_parts(const Part* p, uint32_t parts, float scale, int lane,
+                                   float (*sh)[4]) {
+    Stat a;
+    a.init();
+    for (uint32_t b = lane; b < parts; b += kMergeThreads) {
+        Stat o{p[b].m, p[b].s, ENT ? p[b].h : 0.0f};
+        const float m = max_f(a.m, o.m);
+        a.move<ENT>(m, scale);
+        o.move<ENT>(m, scale);
+        a.s += o.s;
+        a.h += o.h;
+    }
+    team_merge<ENT, kMergeThreads>(a, scale, lane, sh);
+    return a;
+}
+
+// One workgroup per split row. Tags: columns in (x, tokens), slices, alternatives, scale.
+template <typename Fmt, bool ENT, bool TOP>
+__global__ __launch_bounds__(kMergeThreads) void k_lp_merge(uint64_t x, uint64_t tokens,
+                                                            uint64_t part, uint64_t stats_,
+                                                            uint64_t top_lp, uint64_t top_tok,
+                                                            uint32_t stride, uint32_t rows) {
+    constexpr int kWaves = kPartThreads / kWave;
+    constexpr int kSegs = kMaxParts * kWaves;
+    __shared__ float sh[kMergeThreads / kWave][4];
+    __shared__ TopLds<TOP ? kMergeThreads : 1, TOP ? kSegs : 1> L;
+    const uint32_t cols = tags(x, tokens);
+    const uint32_t parts = tag(part), k = tag(stats_);
+    const float scale = __uint_as_float(tags(top_lp, top_tok));
+    float* stats = addr<float>(stats_);
+    const uint32_t r = blockIdx.x;
+    const int lane = threadIdx.x;
+    const int64_t t = addr<const int64_t>(tokens)[r];
+    float* lp = addr<float>(top_lp) + static_cast<size_t>(r) * k;
+    int64_t* tok = addr<int64_t>(top_tok) + static_cast<size_t>(r) * k;
+    if (t < 0) {
+        if (lane == 0) store_stats(stats, rows, r, row_left_out<ENT>());
+        if constexpr (TOP) top_none(k, lane, kMergeThreads, -__builtin_huge_valf(), lp, tok);
+        return;
+    }
+    const uint8_t* row = row_ptr<Fmt>(addr<const void>(x), r, stride);
+    const float xt = load_at<Fmt>(row, t, cols);
+    const Part* p = addr<const Part>(part) + static_cast<size_t>(r) * parts;
+    const Stat a = merge_parts<ENT>(p, parts, scale, lane, sh);
+    const RowOut o = row_out<ENT>(a, xt, scale);
+    if (lane == 0) store_stats(stats, rows, r, o);
+    if constexpr (TOP) {
+        if (!(a.s > 0.0f)) {
+            top_none(k, lane, kMergeThreads, a.s == 0.0f ? -__builtin_huge_valf() : __builtin_nanf(""),
+                     lp, tok);
+            return;
+        }
+        for (uint32_t s = lane; s < parts * kWaves; s += kMergeThreads)
+            L.seg[s] = p[s / kWaves].wave_max[s % kWaves];
+        const Span<Fmt> sp(row, cols);
+        const uint32_t n = part_vecs(span_max<Fmt>(cols), parts);
+        const uint32_t steps = (n + kPartThreads - 1) / kPartThreads;
+        top_select<Fmt, kMergeThreads, kSegs>(
+            L, sp, parts * kWaves, steps * kWave, k, lane, [&](uint32_t s, uint32_t i) {
+                const uint32_t in = (i / kWave) * kPartThreads + (s % kWaves) * kWave + i % kWave;
+                const uint32_t v = sp.va + (s / kWaves) * n + in;
+                return in < n && v < sp.vb ? v : kNoVec;
+            });
+        top_store(L, k, lane, a, scale, o.l2, lp, tok);
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// Gradients. A slice of a row is written as the aligned vectors of the gradient's row; the
+// logits are read at the same positions, aligned or not (the hardware reads a vector at any
+// element's address). f(element, position) gives the gradient of one element.
+
+template <typename Fmt>
+struct Unaligned {
+    typename Fmt::Vec v;
+} __attribute__((packed, aligned(2)));
+
+template <typename Fmt>
+__device__ inline typename Fmt::Vec load16_any(const uint8_t* p) {
+    return reinterpret_cast<const Unaligned<Fmt>*>(p)->v;
+}
+
+// Rounds to nearest even.
+template <typename Fmt>
+__device__ inline typename Fmt::Bits round_to(float v) {
+    if constexpr (Fmt::kSize == 4) {
+        return __float_as_uint(v);
+    } else if constexpr (std::is_same<Fmt, F16>::value) {
+        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+    } else {
+        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+    }
+}
+template <typename Fmt>
+__device__ inline typename Fmt::Vec pack(const float (&g)[Fmt::VW]) {
+    typename Fmt::Bits b[Fmt::VW];
+#pragma unroll
+    for (int i = 0; i < Fmt::VW; ++i) b[i] = round_to<Fmt>(g[i]);
+    return __builtin_bit_cast(typename Fmt::Vec, b);
+}
+
+template <typename Fmt>
+struct GradSlice {
+    const uint8_t* x;  // the row's logits
+    uint8_t* g;        // the row's gradient
+    Span<Fmt> sp;      // of the gradient's row
+    uint32_t first, last;
+    __device__ GradSlice(const uint8_t* xr, uint8_t* gr, uint32_t cols, uint32_t slice, uint32_t slices)
+        : x(xr), g(gr), sp(gr, cols) {
+        const uint32_t n = part_vecs(span_max<Fmt>(cols), slices);
+        first = slice * n < sp.vs ? slice * n : sp.vs;
+        last = sp.vs - first < n ? sp.vs : first + n;
+    }
+    __device__ bool holds(int64_t i) const {
+        const int64_t v = (i + sp.off) / Fmt::VW;
+        return v >= first && v < last;
+    }
+    // take(values, position of the first, out): the gradients of VW elements.
+    template <typename Take>
+    __device__ void write(int lane, int team, bool zero, Take take) const {
+        constexpr int VW = Fmt::VW;
+        for (uint32_t v = first + lane; v < last; v += team) {
+            const uint32_t p0 = sp.pos(v);
+            float e[VW], d[VW];
+            if (v >= sp.va && v < sp.vb) {
+#pragma unroll
+                for (int i = 0; i < VW; ++i) d[i] = 0.0f;
+                if (!zero) {
+                    Fmt::unpack(load16_any<Fmt>(x + static_cast<size_t>(p0) * Fmt::kSize), e);
+                    take(e, p0, d);
+                }
+                *reinterpret_cast<typename Fmt::Vec*>(g + static_cast<size_t>(p0) * Fmt::kSize) =
+                    pack<Fmt>(d);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    d[i] = 0.0f;
+                    e[i] = (!zero && p0 + i < sp.cols)
+                               ? Fmt::load1(x + static_cast<size_t>(p0 + i) * Fmt::kSize)
+                               : 0.0f;
+                }
+                if (!zero) take(e, p0, d);
+#pragma unroll
+                for (int i = 0; i < VW; ++i)
+                    if (p0 + i < sp.cols)
+                        reinterpret_cast<typename Fmt::Bits*>(g)[p0 + i] = round_to<Fmt>(d[i]);
+            }
+        }
+    }
+};
+
+// d logprob and d entropy: dx_j = [ g (delta_jt - p_j) - e p_j (ln p_j + H) ] / T.
+// Tags: columns in (x, tokens), scale in (stats, g_lp), slices in g_ent, log2 of the team's
+// lanes in grad.
+template <typename Fmt, bool ENT>
+__global__ __launch_bounds__(kBlockThreads) void k_lp_grad(uint64_t x, uint64_t tokens,
+                                                           uint64_t stats_, uint64_t g_lp,
+                                                           uint64_t g_ent, uint64_t grad,
+                                                           uint32_t stride, uint32_t rows) {
+    constexpr int VW = Fmt::VW;
+    const uint32_t cols = tags(x, tokens), lg = tag(grad), slices = tag(g_ent);
+    const float scale = __uint_as_float(tags(stats_, g_lp));
+    const uint32_t unit = (blockIdx.x << (8 - lg)) + (threadIdx.x >> lg);
+    const uint32_t r = unit / slices;
+    if (r >= rows) return;
+    const int lane = threadIdx.x & ((1u << lg) - 1);
+    const float* stats = addr<const float>(stats_);
+    const int64_t t = addr<const int64_t>(tokens)[r];
+    const float h = ENT ? stats[static_cast<size_t>(rows) + r] : 0.0f;
+    const float m = stats[2 * static_cast<size_t>(rows) + r];
+    const float l2 = stats[3 * static_cast<size_t>(rows) + r];
+    const float inv_t = scale * kLn2;
+    float a = addr<const float>(g_lp)[r] * inv_t;
+    if (t >= static_cast<int64_t>(cols)) a = __builtin_nanf("");
+    const float b = ENT ? addr<const float>(g_ent)[r] * inv_t * kLn2 : 0.0f;
+    const float h2 = h * (1.0f / kLn2);
+    const bool zero = t < 0 || l2 == -__builtin_huge_valf();
+    const GradSlice<Fmt> gs(row_ptr<Fmt>(addr<const void>(x), r, stride),
+                            const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad), r, cols)), cols,
+                            unit - r * slices, slices);
+    gs.write(lane, 1 << lg, zero, [&](const float (&e)[VW], uint32_t p0, float (&d)[VW]) {
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            const float z = (e[i] - m) * scale - l2;
+            const float p = exp2_f(z);
+            d[i] = ENT ? -p * fmaf(b, max_f(z, kZFloor) + h2, a) : -p * a;
+        }
+        const uint32_t at = static_cast<uint32_t>(t) - p0;
+        if (at < VW) {
+#pragma unroll
+            for (int i = 0; i < VW; ++i) d[i] += at == static_cast<uint32_t>(i) ? a : 0.0f;
+        }
+    });
+}
+
+// ---------------------------------------------------------------------------------------
+// Distillation. The teacher's distribution q is the softmax of its k values over the entries
+// with an id >= 0; loss = sum q_i (ln q_i - ln p_i).
+// stats is [5, rows]: loss, maximum, log2 of the sum, and the same two of the teacher's row.
+
+struct Teacher {
+    float m, l2;
+    __device__ float weight(float v, float scale) const { return exp2_f((v - m) * scale - l2); }
+};
+__device__ inline float teacher_value(const int64_t* ids, const float* values, uint32_t i) {
+    return ids[i] >= 0 ? values[i] : -__builtin_huge_valf();
+}
+template <int T>
+__device__ inline Teacher teacher_row(const int64_t* ids, const float* values, uint32_t k, float scale,
+                                      int lane, float (*sh)[4]) {
+    float m = -__builtin_huge_valf(), s = 0.0f;
+    bool bad = false;
+    for (uint32_t i = lane; i < k; i += T) {
+        const float v = teacher_value(ids, values, i);
+        m = max_f(m, v);
+        bad |= v != v;
+    }
+    m = team_reduce<T, true>(m, lane, sh);
+    if (m > -__builtin_huge_valf())
+        for (uint32_t i = lane; i < k; i += T)
+            s += exp2_f((teacher_value(ids, values, i) - m) * scale);
+    else if (bad)
+        s = __builtin_nanf("");
+    s = team_reduce<T, false>(s, lane, sh);
+    return {s == s ? m : __builtin_nanf(""), log2_f(s)};
+}
+
+__device__ inline void store_distill(float* stats, uint32_t rows, uint32_t r, float loss, float m,
+                                     float l2, const Teacher& q) {
+    const size_t n = rows;
+    stats[r] = loss;
+    stats[n + r] = m;
+    stats[2 * n + r] = l2;
+    stats[3 * n + r] = q.m;
+    stats[4 * n + r] = q.l2;
+}
+
+// The loss of a row from its merged statistics; *l2 becomes NaN when an id with weight lies
+// beyond the row or a weight is NaN, so that the whole gradient is NaN too.
+template <typename Fmt, int T>
+__device__ inline float distill_loss(const uint8_t* row, uint32_t cols, const int64_t* ids,
+                                     const float* values, uint32_t k, float scale, const Teacher& q,
+                                     const Stat& a, float* l2, int lane, float (*sh)[4]) {
+    *l2 = log2_f(a.s);
+    float sum = 0.0f, bad = 0.0f;
+    for (uint32_t i = lane; i < k; i += T) {
+        const int64_t id = ids[i];
+        if (id < 0) continue;
+        const float lq = (values[i] - q.m) * scale - q.l2;
+        const float w = exp2_f(lq);
+        if (w == 0.0f) continue;
+        const float xi = load_at<Fmt>(row, id, cols);
+        if (id >= static_cast<int64_t>(cols) || w != w) bad = 1.0f;
+        const float lp = a.s == 0.0f ? -__builtin_huge_valf() : ln_p(xi, a.m, *l2, scale);
+        sum = fmaf(w, lq * kLn2 - lp, sum);
+    }
+    sum = team_reduce<T, false>(sum, lane, sh);
+    bad = team_reduce<T, true>(bad, lane, sh);
+    if (bad > 0.0f) *l2 = __builtin_nanf("");
+    return sum;
+}
+
+// Gradient of a row's slice: g (p_j - q_j) / T. The dense part g p_j / T is stored first; after
+// it each teacher entry's element is stored again with its weight taken off (the sum of the
+// weights of equal ids, which every one of them computes in the same order).
+template <typename Fmt, int T>
+__device__ inline void distill_grad_slice(const GradSlice<Fmt>& gs, const int64_t* ids,
+                                          const float* values, uint32_t k, float scale, float coef,
+                                          float m, float l2, const Teacher& q, bool zero, int lane,
+                                          int team) {
+    constexpr int VW = Fmt::VW;
+    gs.write(lane, team, zero, [&](const float (&e)[VW], uint32_t, float (&d)[VW]) {
+#pragma unroll
+        for (int i = 0; i < VW; ++i) d[i] = coef * exp2_f((e[i] - m) * scale - l2);
+    });
+    team_sync<T>();
+    if (zero) return;
+    for (uint32_t i = lane; i < k; i += team) {
+        const int64_t id = ids[i];
+        if (id < 0 || id >= static_cast<int64_t>(gs.sp.cols) || !gs.holds(id)) continue;
+        float w = 0.0f;
+        for (uint32_t j = 0; j < k; ++j)
+            if (ids[j] == id) w += q.weight(values[j], scale);
+        const float p = exp2_f((Fmt::load1(gs.x + id * Fmt::kSize) - m) * scale - l2);
+        reinterpret_cast<typename Fmt::Bits*>(gs.g)[id] = round_to<Fmt>(coef * (p - w));
+    }
+}
+
+template <typename Fmt, int T>
+__global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32_t cols,
+                                                           uint32_t stride, float scale,
+                                                           uint32_t rows, uint32_t k,
+                                                           const int64_t* ids_, const float* values_,
+                                                           float* stats) {
+    constexpr int U = 16 / Fmt::VW;
+    __shared__ float sh[T / kWave][4];
+    const uint32_t r = blockIdx.x * kTeamsPerBlock<T> + threadIdx.x / T;
+    const int lane = threadIdx.x % T;
+    if (r >= rows) return;
+    const int64_t* ids = ids_ + static_cast<size_t>(r) * k;
+    const float* values = values_ + static_cast<size_t>(r) * k;
+    const Teacher q = teacher_row<T>(ids, values, k, scale, lane, sh);
+    if (q.m == -__builtin_huge_valf()) {
+        if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
+        return;
+    }
+    const uint8_t* row = row_ptr<Fmt>(x, r, stride);
+    const Span<Fmt> sp(row, cols);
+    Stat a;
+    scan_span<Fmt, false, T, U>(sp, true, sp.va, sp.vb, lane, scale, a);
+    team_merge<false, T>(a, scale, lane, sh);
+    float l2;
+    const float loss = distill_loss<Fmt, T>(row, cols, ids, values, k, scale, q, a, &l2, lane, sh);
+    if (lane == 0) store_distill(stats, rows, r, loss, a.m, l2, q);
+}
+
+// Tags: teacher entries in ids, slices of the row in values.
+template <typename Fmt>
+__global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint32_t cols,
+                                                            uint32_t stride, float scale,
+                                                            uint32_t rows, uint64_t ids_,
+                                                            uint64_t values_, const Part* part,
+                                                            float* stats) {
+    constexpr int T = kMergeThreads;
+    __shared__ float sh[T / kWave][4];
+    const uint32_t k = tag(ids_), parts = tag(values_);
+    const uint32_t r = blockIdx.x;
+    const int lane = threadIdx.x;
+    const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
+    const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
+    const Teacher q = teacher_row<T>(ids, values, k, scale, lane, sh);
+    if (q.m == -__builtin_huge_valf()) {
+        if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
+        return;
+    }
+    const Stat a = merge_parts<false>(part + static_cast<size_t>(r) * parts, parts, scale, lane, sh);
+    float l2;
+    const float loss = distill_loss<Fmt, T>(row_ptr<Fmt>(x, r, stride), cols, ids, values, k, scale, q,
+                                            a, &l2, lane, sh);
+    if (lane == 0) store_distill(stats, rows, r, loss, a.m, l2, q);
+}
+
+// Tags: columns in (x, ids), teacher entries in values, scale in (stats, g), log2 of the team's
+// lanes and the slices (12 bits above 4) in grad.
+template <typename Fmt>
+__global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t ids_, uint64_t values_,
+                                                           uint64_t stats_, uint64_t g, uint64_t grad,
+                                                           uint32_t stride, uint32_t rows) {
+    const uint32_t cols = tags(x, ids_), k = tag(values_);
+    const float scale = __uint_as_float(tags(stats_, g));
+    const uint32_t lg = tag(grad) & 15, slices = tag(grad) >> 4;
+    const uint32_t unit = (blockIdx.x << (8 - lg)) + (threadIdx.x >> lg);
+    const uint32_t want = unit / slices;
+    const bool extra = want >= rows;  // keeps the workgroup's barrier whole
+    const uint32_t r = extra ? rows - 1 : want;
+    const int lane = threadIdx.x & ((1u << lg) - 1);
+    const float* stats = addr<const float>(stats_);
+    const size_t n = rows;
+    const float m = stats[n + r], l2 = stats[2 * n + r];
+    const Teacher q{stats[3 * n + r], stats[4 * n + r]};
+    const float coef = addr<const float>(g)[r] * scale * kLn2;
+    GradSlice<Fmt> gs(row_ptr<Fmt>(addr<const void>(x), r, stride),
+                      const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad), r, cols)), cols,
+                      unit - want * slices, slices);
+    if (extra) gs.first = gs.last = 0;
+    const bool zero = q.m == -__builtin_huge_valf() || l2 == -__builtin_huge_valf();
+    distill_grad_slice<Fmt, kBlockThreads>(gs, addr<const int64_t>(ids_) + static_cast<size_t>(r) * k,
+                                           addr<const float>(values_) + static_cast<size_t>(r) * k, k,
+                                           scale, coef, m, l2, q, zero, lane, 1 << lg);
+}
+
+// Loss and gradient of a row in one kernel: the second reading of the logits comes from the
+// caches. Tags as for k_ds_grad (none in grad).
+template <typename Fmt, int T>
+__global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t ids_, uint64_t values_,
+                                                           uint64_t stats_, uint64_t w, uint64_t grad,
+                                                           uint32_t stride, uint32_t rows) {
+    constexpr int U = 16 / Fmt::VW;
+    __shared__ float sh[T / kWave][4];
+    const uint32_t cols = tags(x, ids_), k = tag(values_);
+    const float scale = __uint_as_float(tags(stats_, w));
+    const uint32_t r = blockIdx.x * kTeamsPerBlock<T> + threadIdx.x / T;
+    const int lane = threadIdx.x % T;
+    if (r >= rows) return;
+    const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
+    const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
+    const uint8_t* row = row_ptr<Fmt>(addr<const void>(x), r, stride);
+    const GradSlice<Fmt> gs(row, const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad), r, cols)), cols, 0, 1);
+    const Teacher q = teacher_row<T>(ids, values, k, scale, lane, sh);
+    float loss = 0.0f, l2 = 0.0f;
+    Stat a{0.0f, 0.0f, 0.0f};
+    const bool absent = q.m == -__builtin_huge_valf();
+    if (!absent) {
+        const Span<Fmt> sp(row, cols);
+        scan_span<Fmt, false, T, U>(sp, true, sp.va, sp.vb, lane, scale, a);
+        team_merge<false, T>(a, scale, lane, sh);
+        loss = distill_loss<Fmt, T>(row, cols, ids, values, k, scale, q, a, &l2, lane, sh);
+    }
+    if (lane == 0) store_distill(addr<float>(stats_), rows, r, loss, a.m, l2, q);
+    const float coef = addr<const float>(w)[r] * scale * kLn2;
+    distill_grad_slice<Fmt, T>(gs, ids, values, k, scale, coef, a.m, l2, q,
+                               absent || l2 == -__builtin_huge_valf(), lane, T);
+}
+
+// ---------------------------------------------------------------------------------------
+// Launch
+
+template <typename F>
+void with_format(int dtype, F f) {
+    switch (dtype) {
+        case ARGREDUCE_F32: f(F32{}); break;
+        case ARGREDUCE_F16: f(F16{}); break;
+        default: f(BF16{}); break;
+    }
+}
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+template <typename F>
+void with_team(int team, F f) {
+    switch (team) {
+        case 64: f(Int<64>{}); break;
+        case 256: f(Int<256>{}); break;
+        default: f(Int<1024>{}); break;
+    }
+}
+template <typename F>
+void with_bool(bool b, F f) {
+    if (b)
+        f(Int<1>{});
+    else
+        f(Int<0>{});
+}
+
+uint32_t team_blocks(int64_t rows, int team) {
+    const int64_t per = team == kWave ? kBlockThreads / kWave : 1;
+    return static_cast<uint32_t>((rows + per - 1) / per);
+}
+uint32_t log2_of(int v) { return static_cast<uint32_t>(__builtin_ctz(static_cast<unsigned>(v))); }
+
+template <typename... KArgs, typename... Args>
+void launch(void (*kernel)(KArgs...), uint32_t grid, int block, hipStream_t s, Args... args) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, s, args...);
+}
+
+}  // namespace
+
+size_t part_bytes() { return sizeof(Part); }
+
+hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const int64_t* tokens,
+                           bool entropy, int top, float* stats, float* top_logprobs,
+                           int64_t* top_tokens, uint8_t* scratch16, hipStream_t s) {
+    const uint32_t cols = static_cast<uint32_t>(a.cols), stride = static_cast<uint32_t>(a.row_stride);
+    const uint32_t rows = static_cast<uint32_t>(a.rows);
+    const uint32_t grid = static_cast<uint32_t>(plan.grid_blocks);
+    with_format(a.dtype, [&](auto fmt) {
+        using Fmt = decltype(fmt);
+        with_bool(entropy, [&](auto ent) {
+            constexpr bool ENT = decltype(ent)::value;
+            if (plan.path == ARGREDUCE_PATH_SUBWAVE && plan.team < kWave) {
+                const auto go = [&](auto g) {
+                    launch(k_lp_group<Fmt, ENT, decltype(g)::value>, grid, kBlockThreads, s, a.x, cols,
+                           stride, a.scale, rows, tokens, stats, tagged(top_logprobs, top), top_tokens);
+                };
+                switch (plan.team) {
+                    case 4: go(Int<4>{}); break;
+                    case 8: go(Int<8>{}); break;
+                    case 16: go(Int<16>{}); break;
+                    default: go(Int<32>{}); break;
+                }
+                return;
+            }
+            with_bool(top > 0, [&](auto tp) {
+                constexpr bool TOP = decltype(tp)::value;
+                if (plan.path == ARGREDUCE_PATH_SPLIT) {
+                    Part* part = reinterpret_cast<Part*>(scratch16);
+                    launch(k_part<Fmt, ENT>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
+                           static_cast<uint32_t>(plan.parts), tokens, part);
+                    const uint32_t sc = bits_of(a.scale);
+                    launch(k_lp_merge<Fmt, ENT, TOP>, rows, kMergeThreads, s, tagged(a.x, cols),
+                           tagged(tokens, cols >> 16), tagged(part, plan.parts), tagged(stats, top),
+                           tagged(top_logprobs, sc), tagged(top_tokens, sc >> 16), stride, rows);
+                    return;
+                }
+                with_team(plan.team, [&](auto team) {
+                    constexpr int T = decltype(team)::value;
+                    launch(k_lp_team<Fmt, ENT, TOP, T>, grid, kTeamBlock<T>, s, a.x, cols, stride,
+                           a.scale, rows, tokens, stats, tagged(top_logprobs, top), top_tokens);
+                });
+            });
+        });
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_logprobs_grad(const GradPlan& plan, const LogitsArgs& a, const int64_t* tokens,
+                                const float* stats, const float* g_logprob, const float* g_entropy,
+                                void* grad, hipStream_t s) {
+    const uint32_t cols = static_cast<uint32_t>(a.cols), sc = bits_of(a.scale);
+    with_format(a.dtype, [&](auto fmt) {
+        using Fmt = decltype(fmt);
+        with_bool(g_entropy != nullptr, [&](auto ent) {
+            launch(k_lp_grad<Fmt, decltype(ent)::value>, static_cast<uint32_t>(plan.grid_blocks),
+                   kBlockThreads, s, tagged(a.x, cols), tagged(tokens, cols >> 16), tagged(stats, sc),
+                   tagged(g_logprob, sc >> 16), tagged(g_entropy, plan.slices),
+                   tagged(grad, log2_of(plan.team)), static_cast<uint32_t>(a.row_stride),
+                   static_cast<uint32_t>(a.rows));
+        });
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_distill_grad(const GradPlan& plan, const LogitsArgs& a, int k, const int64_t* ids,
+                               const float* values, const float* stats, const float* g_loss,
+                               void* grad, hipStream_t s) {
+    const uint32_t cols = static_cast<uint32_t>(a.cols), sc = bits_of(a.scale);
+    with_format(a.dtype, [&](auto fmt) {
+        using Fmt = decltype(fmt);
+        launch(k_ds_grad<Fmt>, static_cast<uint32_t>(plan.grid_blocks), kBlockThreads, s,
+               tagged(a.x, cols), tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
+               tagged(g_loss, sc >> 16), tagged(grad, log2_of(plan.team) | (plan.slices << 4)),
+               static_cast<uint32_t>(a.row_stride), static_cast<uint32_t>(a.rows));
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const LogitsArgs& a, int k,
+                          const int64_t* ids, const float* values, float* stats,
+                          const float* weights, void* grad, uint8_t* scratch16, hipStream_t s) {
+    const uint32_t cols = static_cast<uint32_t>(a.cols), stride = static_cast<uint32_t>(a.row_stride);
+    const uint32_t rows = static_cast<uint32_t>(a.rows), sc = bits_of(a.scale);
+    const uint32_t grid = static_cast<uint32_t>(plan.grid_blocks);
+    with_format(a.dtype, [&](auto fmt) {
+        using Fmt = decltype(fmt);
+        if (plan.path == ARGREDUCE_PATH_SPLIT) {
+            Part* part = reinterpret_cast<Part*>(scratch16);
+            launch(k_part<Fmt, false>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
+                   static_cast<uint32_t>(plan.parts), static_cast<const int64_t*>(nullptr), part);
+            launch(k_ds_merge<Fmt>, rows, kMergeThreads, s, a.x, cols, stride, a.scale, rows,
+                   tagged(ids, k), tagged(values, plan.parts), static_cast<const Part*>(part), stats);
+            return;
+        }
+        with_team(plan.team, [&](auto team) {
+            constexpr int T = decltype(team)::value;
+            if (grad != nullptr)
+                launch(k_ds_step<Fmt, T>, grid, kTeamBlock<T>, s, tagged(a.x, cols),
+                       tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
+                       tagged(weights, sc >> 16), tagged(grad, 0), stride, rows);
+            else
+                launch(k_ds_team<Fmt, T>, grid, kTeamBlock<T>, s, a.x, cols, stride, a.scale, rows,
+                       static_cast<uint32_t>(k), ids, values, stats);
+        });
+    });
+    if (plan.path == ARGREDUCE_PATH_SPLIT && grad != nullptr)
+        return launch_distill_grad(gplan, a, k, ids, values, stats, weights, grad, s);
+    return hipGetLastError();
+}
+
+}  // namespace argreduce

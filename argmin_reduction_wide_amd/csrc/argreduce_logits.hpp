@@ -1,0 +1,64 @@
+// Plans and launchers of the logits operators (argreduce_logits.hip), shared with their C ABI
+// (argreduce_logits_api.cpp).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "argreduce.h"
+
+namespace argreduce {
+
+constexpr int kTopMax = 64;            // alternatives per row (ARGREDUCE_TOP_MAX)
+constexpr int kTeacherMax = 1024;      // teacher entries per row (ARGREDUCE_TEACHER_MAX)
+constexpr int kPartThreads = 256;      // threads of a workgroup that scans a slice of a row
+constexpr int kPartUnroll = 4;         // 16-byte loads each of its lanes keeps in flight
+constexpr int kMaxParts = 256;         // slices of a row
+
+// How the rows of one forward call are scanned.
+struct LogitsPlan {
+    int path;             // argreduce_path_t: SUBWAVE, BLOCK or SPLIT
+    int team;             // lanes that scan one row (SUBWAVE, BLOCK), else kPartThreads
+    int parts;            // SPLIT: workgroups per row
+    int64_t grid_blocks;  // workgroups of the scanning kernel
+    int64_t device_threads;
+    size_t scratch_bytes; // including 15 bytes of alignment slack; 0 if none needed
+};
+
+// How the rows of one gradient call are cut: `team` lanes per slice of a row.
+struct GradPlan {
+    int team;             // 1 .. 256, a power of two
+    int slices;           // slices per row (1 unless team == 256)
+    int64_t grid_blocks;
+};
+
+// Logits of one call. `scale` is log2(e) / temperature.
+struct LogitsArgs {
+    const void* x;
+    int dtype;
+    int64_t rows, cols, row_stride;
+    float scale;
+};
+
+size_t part_bytes();  // scratch of one slice of a split row
+
+hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const int64_t* tokens,
+                           bool entropy, int top, float* stats, float* top_logprobs,
+                           int64_t* top_tokens, uint8_t* scratch16, hipStream_t stream);
+hipError_t launch_logprobs_grad(const GradPlan& plan, const LogitsArgs& a, const int64_t* tokens,
+                                const float* stats, const float* g_logprob, const float* g_entropy,
+                                void* grad, hipStream_t stream);
+// With `weights` and `grad` the gradient too (argreduce_distill_step), by `gplan` where the
+// plan splits rows.
+hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const LogitsArgs& a, int k,
+                          const int64_t* ids, const float* values, float* stats,
+                          const float* weights, void* grad, uint8_t* scratch16, hipStream_t stream);
+hipError_t launch_distill_grad(const GradPlan& plan, const LogitsArgs& a, int k, const int64_t* ids,
+                               const float* values, const float* stats, const float* g_loss,
+                               void* grad, hipStream_t stream);
+
+// Thread capacity plans are made for (the simulated one if set); an ARGREDUCE_* status.
+int plan_device_threads(int64_t* threads);
+
+}  // namespace argreduce

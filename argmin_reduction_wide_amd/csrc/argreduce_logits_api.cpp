@@ -1,0 +1,332 @@
+// C ABI of the logits operators: argument checks, launch plans and scratch sizes. Declarations
+// and the contract are in include/argreduce.h, the kernels in argreduce_logits.hip.
+#include <hip/hip_runtime_api.h>
+
+#include <cmath>
+#include <limits>
+
+#include "argreduce.h"
+#include "argreduce_logits.hpp"
+
+#define ARGREDUCE_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace argreduce {
+namespace {
+
+constexpr int64_t kBlock = 256;
+constexpr int64_t kMaxGridThreads = int64_t{1} << 32;  // threads a launch's grid may hold
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t next_pow2(int64_t v) {
+    int64_t p = 1;
+    while (p < v) p <<= 1;
+    return p;
+}
+
+int64_t logits_elem_size(int dtype) {
+    switch (dtype) {
+        case ARGREDUCE_F32: return 4;
+        case ARGREDUCE_F16: return 2;
+        case ARGREDUCE_BF16: return 2;
+        default: return 0;
+    }
+}
+
+// 16-byte vectors that a row's bytes lie in, for the worst aligned row.
+int64_t span_vecs(int64_t cols, int64_t es) { return cols * es / 16 + 2; }
+
+int check_logits_shape(int dtype, int64_t rows, int64_t cols) {
+    if (logits_elem_size(dtype) == 0) return ARGREDUCE_ERR_UNSUPPORTED_DTYPE;
+    if (rows < 0 || cols < 1) return ARGREDUCE_ERR_INVALID_ARG;
+    if (cols > std::numeric_limits<int32_t>::max() || rows > std::numeric_limits<int32_t>::max())
+        return ARGREDUCE_ERR_TOO_WIDE;
+    return ARGREDUCE_OK;
+}
+
+// Checks of the arguments that every call takes; fills *a. Row stride: see the header.
+int check_logits(const void* x, int dtype, int64_t rows, int64_t cols, int64_t stride,
+                 float temperature, LogitsArgs* a) {
+    const int rc = check_logits_shape(dtype, rows, cols);
+    if (rc != ARGREDUCE_OK) return rc;
+    if (stride > std::numeric_limits<uint32_t>::max()) return ARGREDUCE_ERR_TOO_WIDE;
+    if (rows > 1 && stride < cols) return ARGREDUCE_ERR_INVALID_ARG;
+    // powers of two far inside the range of a float: log2(e) / T and its products stay normal
+    if (!(temperature >= 0x1p-60f && temperature <= 0x1p60f)) return ARGREDUCE_ERR_INVALID_ARG;
+    if (rows > 0 && (x == nullptr || reinterpret_cast<uintptr_t>(x) % logits_elem_size(dtype) != 0))
+        return ARGREDUCE_ERR_INVALID_ARG;
+    *a = LogitsArgs{x, dtype, rows, cols, rows > 1 ? stride : cols,
+                    static_cast<float>(1.4426950408889634 / static_cast<double>(temperature))};
+    return ARGREDUCE_OK;
+}
+
+// Device addresses carry 16 bits of other arguments in their upper bits (argreduce_logits.hip).
+bool fits48(const void* p) { return (reinterpret_cast<uintptr_t>(p) >> 48) == 0; }
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// A device array of `n`-byte elements that a call with rows > 0 needs.
+bool usable(const void* p, uintptr_t n) { return p != nullptr && aligned(p, n) && fits48(p); }
+
+// Scratch depends on the shape alone, so only the choices among plans without any go by
+// `vec_rows` (every row starts on a 16-byte boundary).
+int make_logits_plan(int dtype, int64_t rows, int64_t cols, bool groups, bool vec_rows,
+                     LogitsPlan* p) {
+    int rc = check_logits_shape(dtype, rows, cols);
+    if (rc != ARGREDUCE_OK) return rc;
+    int64_t cap = 0;
+    rc = plan_device_threads(&cap);
+    if (rc != ARGREDUCE_OK) return rc;
+    const int64_t es = logits_elem_size(dtype);
+    const int64_t rows1 = rows > 0 ? rows : 1;
+    const int64_t vecs = span_vecs(cols, es);
+    const int64_t cap_blocks = cap / kBlock > 0 ? cap / kBlock : 1;
+    *p = LogitsPlan{};
+    p->device_threads = cap;
+    p->parts = 1;
+    const int64_t held = vec_rows ? ceil_div(cols * es, 16) : vecs;  // vectors a row lies in
+    if (held <= 32 && groups) {
+        p->path = ARGREDUCE_PATH_SUBWAVE;
+        p->team = static_cast<int>(next_pow2(held < 4 ? 4 : held));
+        p->grid_blocks = ceil_div(rows1, kBlock / p->team);
+        if (rows1 * p->team >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
+        return ARGREDUCE_OK;
+    }
+    if (vecs <= 256) {
+        p->path = ARGREDUCE_PATH_SUBWAVE;
+        p->team = 64;
+        p->grid_blocks = ceil_div(rows1, kBlock / 64);
+        if (rows1 * 64 >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
+        return ARGREDUCE_OK;
+    }
+    int64_t parts = ceil_div(vecs, kPartThreads * kPartUnroll);
+    const int64_t most = cap_blocks / rows1;
+    parts = parts < most ? parts : most;
+    parts = parts < kMaxParts ? parts : kMaxParts;
+    if (parts >= 4) {
+        p->path = ARGREDUCE_PATH_SPLIT;
+        p->team = kPartThreads;
+        p->parts = static_cast<int>(parts);
+        p->grid_blocks = rows1 * parts;
+        p->scratch_bytes = 15 + static_cast<size_t>(rows1) * static_cast<size_t>(parts) * part_bytes();
+        return ARGREDUCE_OK;
+    }
+    p->path = ARGREDUCE_PATH_BLOCK;
+    p->team = vecs > 4096 ? 1024 : 256;
+    p->grid_blocks = rows1;
+    if (rows1 * p->team >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
+    return ARGREDUCE_OK;
+}
+
+int make_grad_plan(int dtype, int64_t rows, int64_t cols, GradPlan* p) {
+    const int64_t vecs = span_vecs(cols, logits_elem_size(dtype));
+    const int64_t rows1 = rows > 0 ? rows : 1;
+    const int64_t team = next_pow2(vecs);
+    p->team = static_cast<int>(team < kBlock ? team : kBlock);
+    p->slices = 1;
+    if (team > kBlock) {
+        // four vectors to a thread
+        int64_t slices = ceil_div(vecs, kBlock * 4);
+        p->slices = static_cast<int>(slices < 4095 ? slices : 4095);
+    }
+    p->grid_blocks = ceil_div(rows1 * p->slices, kBlock / p->team);
+    if (p->grid_blocks * kBlock >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
+    return ARGREDUCE_OK;
+}
+
+// The caller's scratch aligned up to 16 bytes in *out; an ARGREDUCE_* status.
+int scratch_of(const LogitsPlan& p, void* scratch, size_t bytes, uint8_t** out) {
+    *out = nullptr;
+    if (p.scratch_bytes == 0) return ARGREDUCE_OK;
+    if (scratch == nullptr || bytes < p.scratch_bytes) return ARGREDUCE_ERR_SCRATCH_TOO_SMALL;
+    if (!fits48(scratch)) return ARGREDUCE_ERR_INVALID_ARG;
+    *out = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(scratch) + 15u) &
+                                      ~static_cast<uintptr_t>(15u));
+    return ARGREDUCE_OK;
+}
+
+bool vec_rows(const LogitsArgs& a) {
+    return aligned(a.x, 16) && a.row_stride * logits_elem_size(a.dtype) % 16 == 0;
+}
+
+int status_of(hipError_t e) { return e == hipSuccess ? ARGREDUCE_OK : ARGREDUCE_ERR_HIP; }
+
+void fill_logits_plan(const LogitsPlan& p, int dispatches, argreduce_plan_t* out) {
+    *out = argreduce_plan_t{};
+    out->path = p.path;
+    out->lanes_per_row = p.team * p.parts;
+    out->blocks_per_row = p.parts;
+    out->block_threads = p.path == ARGREDUCE_PATH_BLOCK ? p.team : static_cast<int32_t>(kBlock);
+    out->grid_blocks = p.grid_blocks;
+    out->grid_rows = p.path == ARGREDUCE_PATH_SUBWAVE ? p.grid_blocks * (kBlock / p.team)
+                                                      : p.grid_blocks / p.parts;
+    out->unroll = kPartUnroll;
+    out->outputs_per_block = p.path == ARGREDUCE_PATH_SUBWAVE ? static_cast<int32_t>(kBlock / p.team) : 1;
+    out->device_threads = p.device_threads;
+    out->scratch_bytes = p.scratch_bytes;
+    out->load_bytes = 16;
+    out->dispatches = dispatches;
+}
+
+// Checks of the teacher's arguments.
+int check_teacher(const LogitsArgs& a, int32_t k, const int64_t* ids, const float* values,
+                  const float* stats) {
+    if (k < 1 || k > kTeacherMax) return ARGREDUCE_ERR_INVALID_ARG;
+    if (a.rows == 0) return ARGREDUCE_OK;
+    if (!fits48(a.x) || !usable(ids, 8) || !usable(values, 4) || !usable(stats, 4))
+        return ARGREDUCE_ERR_INVALID_ARG;
+    return ARGREDUCE_OK;
+}
+
+int distill(const LogitsArgs& a, int32_t k, const int64_t* ids, const float* values, float* stats,
+            const float* weights, void* grad, void* scratch, size_t scratch_bytes, void* stream) {
+    LogitsPlan p;
+    GradPlan g;
+    int rc = make_logits_plan(a.dtype, a.rows, a.cols, false, vec_rows(a), &p);
+    if (rc != ARGREDUCE_OK) return rc;
+    rc = make_grad_plan(a.dtype, a.rows, a.cols, &g);
+    if (rc != ARGREDUCE_OK) return rc;
+    uint8_t* scratch16 = nullptr;
+    rc = scratch_of(p, scratch, scratch_bytes, &scratch16);
+    if (rc != ARGREDUCE_OK) return rc;
+    return status_of(launch_distill(p, g, a, k, ids, values, stats, weights, grad, scratch16,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+}  // namespace argreduce
+
+using argreduce::GradPlan;
+using argreduce::LogitsArgs;
+using argreduce::LogitsPlan;
+
+ARGREDUCE_EXPORT size_t argreduce_logprobs_scratch_bytes(int64_t rows, int64_t cols,
+                                                         argreduce_dtype_t dtype) {
+    LogitsPlan p;
+    if (argreduce::make_logits_plan(dtype, rows, cols, true, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p) != ARGREDUCE_OK)
+        return std::numeric_limits<size_t>::max();
+    return p.scratch_bytes;
+}
+
+ARGREDUCE_EXPORT int argreduce_logprobs_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
+                                             argreduce_plan_t* out) {
+    if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
+    LogitsPlan p;
+    const int rc = argreduce::make_logits_plan(dtype, rows, cols, true, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p);
+    if (rc != ARGREDUCE_OK) return rc;
+    argreduce::fill_logits_plan(p, p.parts > 1 ? 2 : 1, out);
+    return ARGREDUCE_OK;
+}
+
+ARGREDUCE_EXPORT int argreduce_logprobs(const void* x, argreduce_dtype_t dtype, int64_t rows,
+                                        int64_t cols, int64_t row_stride, const int64_t* tokens,
+                                        float temperature, int32_t entropy, int32_t top, float* stats,
+                                        float* top_logprobs, int64_t* top_tokens, void* scratch,
+                                        size_t scratch_bytes, void* stream) {
+    using namespace argreduce;
+    LogitsArgs a;
+    int rc = check_logits(x, dtype, rows, cols, row_stride, temperature, &a);
+    if (rc != ARGREDUCE_OK) return rc;
+    if (top < 0 || top > kTopMax) return ARGREDUCE_ERR_INVALID_ARG;
+    if (rows == 0) return ARGREDUCE_OK;
+    if (!fits48(x) || !usable(tokens, 8) || !usable(stats, 4)) return ARGREDUCE_ERR_INVALID_ARG;
+    if (top > 0 && (!usable(top_logprobs, 4) || !usable(top_tokens, 8))) return ARGREDUCE_ERR_INVALID_ARG;
+    LogitsPlan p;
+    rc = make_logits_plan(dtype, rows, cols, true, vec_rows(a), &p);
+    if (rc != ARGREDUCE_OK) return rc;
+    uint8_t* scratch16 = nullptr;
+    rc = scratch_of(p, scratch, scratch_bytes, &scratch16);
+    if (rc != ARGREDUCE_OK) return rc;
+    return status_of(launch_logprobs(p, a, tokens, entropy != 0, top, stats, top > 0 ? top_logprobs : nullptr,
+                                     top > 0 ? top_tokens : nullptr, scratch16,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+ARGREDUCE_EXPORT int argreduce_logprobs_grad(const void* x, argreduce_dtype_t dtype, int64_t rows,
+                                             int64_t cols, int64_t row_stride, const int64_t* tokens,
+                                             float temperature, const float* stats,
+                                             const float* grad_logprob, const float* grad_entropy,
+                                             void* grad, void* stream) {
+    using namespace argreduce;
+    LogitsArgs a;
+    int rc = check_logits(x, dtype, rows, cols, row_stride, temperature, &a);
+    if (rc != ARGREDUCE_OK) return rc;
+    if (rows == 0) return ARGREDUCE_OK;
+    if (!fits48(x) || !usable(tokens, 8) || !usable(stats, 4) || !usable(grad_logprob, 4) ||
+        !usable(grad, static_cast<uintptr_t>(logits_elem_size(dtype))) ||
+        (grad_entropy != nullptr && !usable(grad_entropy, 4)))
+        return ARGREDUCE_ERR_INVALID_ARG;
+    GradPlan g;
+    rc = make_grad_plan(dtype, rows, cols, &g);
+    if (rc != ARGREDUCE_OK) return rc;
+    return status_of(launch_logprobs_grad(g, a, tokens, stats, grad_logprob, grad_entropy, grad,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+ARGREDUCE_EXPORT size_t argreduce_distill_scratch_bytes(int64_t rows, int64_t cols,
+                                                        argreduce_dtype_t dtype) {
+    LogitsPlan p;
+    if (argreduce::make_logits_plan(dtype, rows, cols, false, false, &p) != ARGREDUCE_OK)
+        return std::numeric_limits<size_t>::max();
+    return p.scratch_bytes;
+}
+
+ARGREDUCE_EXPORT int argreduce_distill_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
+                                            argreduce_plan_t* out) {
+    if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
+    LogitsPlan p;
+    const int rc = argreduce::make_logits_plan(dtype, rows, cols, false, false, &p);
+    if (rc != ARGREDUCE_OK) return rc;
+    argreduce::fill_logits_plan(p, p.parts > 1 ? 2 : 1, out);
+    return ARGREDUCE_OK;
+}
+
+ARGREDUCE_EXPORT int argreduce_distill(const void* x, argreduce_dtype_t dtype, int64_t rows,
+                                       int64_t cols, int64_t row_stride, int32_t k,
+                                       const int64_t* teacher_tokens, const float* teacher_logits,
+                                       float temperature, float* stats, void* scratch,
+                                       size_t scratch_bytes, void* stream) {
+    using namespace argreduce;
+    LogitsArgs a;
+    int rc = check_logits(x, dtype, rows, cols, row_stride, temperature, &a);
+    if (rc != ARGREDUCE_OK) return rc;
+    rc = check_teacher(a, k, teacher_tokens, teacher_logits, stats);
+    if (rc != ARGREDUCE_OK || rows == 0) return rc;
+    return distill(a, k, teacher_tokens, teacher_logits, stats, nullptr, nullptr, scratch, scratch_bytes,
+                   stream);
+}
+
+ARGREDUCE_EXPORT int argreduce_distill_grad(const void* x, argreduce_dtype_t dtype, int64_t rows,
+                                            int64_t cols, int64_t row_stride, int32_t k,
+                                            const int64_t* teacher_tokens, const float* teacher_logits,
+                                            float temperature, const float* stats,
+                                            const float* grad_loss, void* grad, void* stream) {
+    using namespace argreduce;
+    LogitsArgs a;
+    int rc = check_logits(x, dtype, rows, cols, row_stride, temperature, &a);
+    if (rc != ARGREDUCE_OK) return rc;
+    rc = check_teacher(a, k, teacher_tokens, teacher_logits, stats);
+    if (rc != ARGREDUCE_OK || rows == 0) return rc;
+    if (!usable(grad_loss, 4) || !usable(grad, static_cast<uintptr_t>(logits_elem_size(dtype))))
+        return ARGREDUCE_ERR_INVALID_ARG;
+    GradPlan g;
+    rc = make_grad_plan(dtype, rows, cols, &g);
+    if (rc != ARGREDUCE_OK) return rc;
+    return status_of(launch_distill_grad(g, a, k, teacher_tokens, teacher_logits, stats, grad_loss, grad,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+ARGREDUCE_EXPORT int argreduce_distill_step(const void* x, argreduce_dtype_t dtype, int64_t rows,
+                                            int64_t cols, int64_t row_stride, int32_t k,
+                                            const int64_t* teacher_tokens, const float* teacher_logits,
+                                            float temperature, const float* weights, float* stats,
+                                            void* grad, void* scratch, size_t scratch_bytes,
+                                            void* stream) {
+    using namespace argreduce;
+    LogitsArgs a;
+    int rc = check_logits(x, dtype, rows, cols, row_stride, temperature, &a);
+    if (rc != ARGREDUCE_OK) return rc;
+    rc = check_teacher(a, k, teacher_tokens, teacher_logits, stats);
+    if (rc != ARGREDUCE_OK || rows == 0) return rc;
+    if (!usable(weights, 4) || !usable(grad, static_cast<uintptr_t>(logits_elem_size(dtype))))
+        return ARGREDUCE_ERR_INVALID_ARG;
+    return distill(a, k, teacher_tokens, teacher_logits, stats, weights, grad, scratch, scratch_bytes,
+                   stream);
+}

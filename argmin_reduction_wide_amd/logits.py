@@ -1,0 +1,367 @@
+"""Logits operators for torch tensors: log probabilities of given tokens with entropy and top
+alternatives, and distillation from a teacher's top logits, each with its gradient.
+
+torch supplies device memory, the current stream and, where asked for, autograd; every step of
+the arithmetic runs in the library's kernels (include/argreduce.h states the semantics). Logits
+are float32, float16 or bfloat16 on the GPU, shape [..., cols]; the leading dimensions are rows,
+and rows may be further apart than cols (a slice of a padded vocabulary, or of one position per
+sequence, needs no copy).
+
+``token_logprobs`` and ``distill_loss`` take part in autograd when the logits require a
+gradient. ``token_logprobs_grad``, ``distill_loss_grad`` and ``distill_step`` are the same
+gradients as plain calls, which can also be captured into a graph.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import binding as B
+
+TOP_MAX = 64         # alternatives per row (ARGREDUCE_TOP_MAX)
+TEACHER_MAX = 1024   # teacher entries per row (ARGREDUCE_TEACHER_MAX)
+
+_CODES = {torch.float32: B.F32, torch.float16: B.F16, torch.bfloat16: B.BF16}
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns. ``stats`` (float32 [4, rows]) is what token_logprobs_grad
+    takes; logprob and entropy are its first two rows in the logits' leading shape."""
+
+    logprob: torch.Tensor
+    entropy: Optional[torch.Tensor]
+    top_logprobs: Optional[torch.Tensor]
+    top_tokens: Optional[torch.Tensor]
+    stats: torch.Tensor
+
+
+class DistillLoss(NamedTuple):
+    """What distill_loss returns. ``stats`` (float32 [5, rows]) is what distill_loss_grad takes;
+    the loss is its first row in the logits' leading shape."""
+
+    loss: torch.Tensor
+    stats: torch.Tensor
+
+
+class _Rows(NamedTuple):
+    code: int
+    rows: int
+    cols: int
+    stride: int
+
+
+def _rows(logits) -> _Rows:
+    """The logits as rows of one stride, or a refusal."""
+    if not logits.is_cuda:
+        raise ValueError("the logits operators run on the GPU only; got a CPU tensor")
+    code = _CODES.get(logits.dtype)
+    if code is None:
+        raise B.ArgreduceError(-2, f"logits of {logits.dtype}")
+    shape, strides = logits.shape, logits.stride()
+    if len(shape) == 0:
+        raise ValueError("logits need at least one dimension")
+    cols = shape[-1]
+    if cols == 0:
+        raise ValueError("logits need at least one column")
+    if strides[-1] != 1 and cols != 1:
+        raise ValueError("the last dimension of the logits must be contiguous")
+    if len(shape) == 2:
+        return _Rows(code, shape[0], cols, strides[0])
+    rows, stride = 1, None
+    for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = s
+        elif rows > 0 and s != stride * rows:
+            raise ValueError("the leading dimensions of the logits must be rows of one stride")
+        rows *= n
+    return _Rows(code, rows, cols, cols if stride is None else stride)
+
+
+def _same(t, name: str, like, dtype, shape) -> None:
+    """An input array: contiguous, of this type and shape, on the logits' device."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}; got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}; got {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}; got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _temperature(t) -> float:
+    t = float(t)
+    if not 2.0 ** -60 <= t <= 2.0 ** 60:
+        raise ValueError(f"temperature must lie in [2^-60, 2^60]; got {t}")
+    return t
+
+
+class _On:
+    """Makes the logits' device current for the library (its plans and launches go by the
+    current device), where it is not already."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self) -> int:
+        self.before = torch._C._cuda_getDevice()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _scratch(need: int, what: str, given, device):
+    if need == B.SIZE_MAX:
+        raise B.ArgreduceError(-3, what)
+    if given is not None:
+        B._check_buffer(given, "scratch", device)
+    if need == 0:
+        return None, 0, 0
+    if given is None or given.numel() * given.element_size() < need:
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def _done(rc: int, what: str, r: _Rows) -> None:
+    if rc != B.OK:
+        raise B.ArgreduceError(rc, f"{what}(rows={r.rows}, cols={r.cols}, row_stride={r.stride})")
+
+
+def _refuse_captured_autograd(logits) -> None:
+    """An autograd graph recorded while a HIP graph is captured can share gradient accumulators
+    with an eager one, which ends the process when the engine joins their streams."""
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("autograd through the logits operators cannot be captured: call "
+                           "token_logprobs_grad, distill_loss_grad or distill_step in the capture")
+
+
+# ---------------------------------------------------------------------------------------
+# token_logprobs
+
+
+def _logprobs(logits, tokens, temperature, entropy, top, scratch):
+    r = _rows(logits)
+    lead = logits.shape[:-1]
+    _same(tokens, "tokens", logits, torch.int64, lead)
+    temperature = _temperature(temperature)
+    if not 0 <= top <= TOP_MAX:
+        raise ValueError(f"top must lie in 0..{TOP_MAX}; got {top}")
+    device = logits.device
+    stats = torch.empty((4, r.rows), dtype=torch.float32, device=device)
+    lp = tok = None
+    if top:
+        lp = torch.empty(lead + (top,), dtype=torch.float32, device=device)
+        tok = torch.empty(lead + (top,), dtype=torch.int64, device=device)
+    with _On(device) as stream:
+        need = B.argreduce_logprobs_scratch_bytes(r.rows, r.cols, r.code)
+        scratch, sptr, sbytes = _scratch(need, "argreduce_logprobs", scratch, device)
+        rc = B.argreduce_logprobs(logits.data_ptr(), r.code, r.rows, r.cols, r.stride,
+                                  tokens.data_ptr(), temperature, 1 if entropy else 0, top,
+                                  stats.data_ptr(), lp.data_ptr() if top else 0,
+                                  tok.data_ptr() if top else 0, sptr, sbytes, stream)
+    _done(rc, "argreduce_logprobs", r)
+    return stats, lp, tok
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, temperature, entropy, top, scratch):
+        stats, lp, tok = _logprobs(logits, tokens, temperature, entropy, top, scratch)
+        ctx.save_for_backward(logits, tokens, stats)
+        ctx.temperature, ctx.entropy = temperature, entropy
+        # outputs of their own: a view of stats would carry its gradient to the other rows
+        lead = logits.shape[:-1]
+        logprob = stats[0].view(lead).clone()
+        ent = stats[1].view(lead).clone() if entropy else None
+        ctx.mark_non_differentiable(*[t for t in (lp, tok, stats) if t is not None])
+        ctx.set_materialize_grads(False)
+        return logprob, ent, lp, tok, stats
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_logprob, g_entropy, *_):
+        logits, tokens, stats = ctx.saved_tensors
+        if g_logprob is None and g_entropy is None:
+            return (None,) * 6
+        lead = logits.shape[:-1]
+        if g_logprob is None:
+            g_logprob = torch.zeros(lead, dtype=torch.float32, device=logits.device)
+        grad = token_logprobs_grad(logits, tokens, stats, g_logprob.contiguous(),
+                                   None if g_entropy is None else g_entropy.contiguous(),
+                                   temperature=ctx.temperature)
+        return grad, None, None, None, None, None
+
+
+def token_logprobs(logits, tokens, *, temperature: float = 1.0, entropy: bool = False, top: int = 0,
+                   scratch=None) -> TokenLogprobs:
+    """Log probability of one given token per row, ``ln softmax(logits / temperature)[token]``.
+
+    logits [..., cols] (float32, float16, bfloat16); tokens int64, the logits' leading shape. A
+    negative token leaves its row out (0, no gradient). entropy: also the entropy of each row's
+    distribution. top: also the ``top`` most likely tokens and their log probabilities, most
+    likely first, ties to the lower token; rows with fewer unmasked logits end in token -1.
+
+    Differentiable in logprob and entropy (float32) when the logits require a gradient."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        _refuse_captured_autograd(logits)
+        return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, bool(entropy), top,
+                                                   scratch))
+    stats, lp, tok = _logprobs(logits, tokens, temperature, entropy, top, scratch)
+    if logits.dim() == 2:
+        return TokenLogprobs(stats[0], stats[1] if entropy else None, lp, tok, stats)
+    lead = logits.shape[:-1]
+    return TokenLogprobs(stats[0].view(lead), stats[1].view(lead) if entropy else None, lp, tok, stats)
+
+
+def _grad_out(logits, out):
+    if out is None:
+        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    B._check_buffer(out, "out", logits.device, logits.dtype, logits.numel())
+    if out.shape != logits.shape:
+        raise ValueError(f"out must have shape {tuple(logits.shape)}; got {tuple(out.shape)}")
+    return out
+
+
+def token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy=None, *,
+                        temperature: float = 1.0, out=None):
+    """Gradient of ``(grad_logprob * logprob + grad_entropy * entropy).sum()`` with respect to the
+    logits, in their type and shape (contiguous; ``out``, if given, is such a tensor). stats is
+    that of the forward call on the same logits, tokens and temperature, made with
+    ``entropy=True`` if grad_entropy is given; grad_logprob and grad_entropy are float32 in the
+    logits' leading shape."""
+    r = _rows(logits)
+    lead = logits.shape[:-1]
+    _same(tokens, "tokens", logits, torch.int64, lead)
+    _same(stats, "stats", logits, torch.float32, (4, r.rows))
+    _same(grad_logprob, "grad_logprob", logits, torch.float32, lead)
+    if grad_entropy is not None:
+        _same(grad_entropy, "grad_entropy", logits, torch.float32, lead)
+    temperature = _temperature(temperature)
+    out = _grad_out(logits, out)
+    with _On(logits.device) as stream:
+        rc = B.argreduce_logprobs_grad(logits.data_ptr(), r.code, r.rows, r.cols, r.stride,
+                                       tokens.data_ptr(), temperature, stats.data_ptr(),
+                                       grad_logprob.data_ptr(),
+                                       0 if grad_entropy is None else grad_entropy.data_ptr(),
+                                       out.data_ptr(), stream)
+    _done(rc, "argreduce_logprobs_grad", r)
+    return out
+
+
+# ---------------------------------------------------------------------------------------
+# distill_loss
+
+
+def _teacher(logits, teacher_tokens, teacher_logits) -> int:
+    k = teacher_tokens.shape[-1] if teacher_tokens.dim() else 0
+    if not 1 <= k <= TEACHER_MAX:
+        raise ValueError(f"a row must have 1..{TEACHER_MAX} teacher entries; got {k}")
+    shape = logits.shape[:-1] + (k,)
+    _same(teacher_tokens, "teacher_tokens", logits, torch.int64, shape)
+    _same(teacher_logits, "teacher_logits", logits, torch.float32, shape)
+    return k
+
+
+def _distill(logits, teacher_tokens, teacher_logits, temperature, scratch):
+    r = _rows(logits)
+    k = _teacher(logits, teacher_tokens, teacher_logits)
+    temperature = _temperature(temperature)
+    stats = torch.empty((5, r.rows), dtype=torch.float32, device=logits.device)
+    with _On(logits.device) as stream:
+        need = B.argreduce_distill_scratch_bytes(r.rows, r.cols, r.code)
+        scratch, sptr, sbytes = _scratch(need, "argreduce_distill", scratch, logits.device)
+        rc = B.argreduce_distill(logits.data_ptr(), r.code, r.rows, r.cols, r.stride, k,
+                                 teacher_tokens.data_ptr(), teacher_logits.data_ptr(), temperature,
+                                 stats.data_ptr(), sptr, sbytes, stream)
+    _done(rc, "argreduce_distill", r)
+    return stats
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, teacher_tokens, teacher_logits, temperature, scratch):
+        stats = _distill(logits, teacher_tokens, teacher_logits, temperature, scratch)
+        ctx.save_for_backward(logits, teacher_tokens, teacher_logits, stats)
+        ctx.temperature = temperature
+        ctx.mark_non_differentiable(stats)
+        ctx.set_materialize_grads(False)
+        return stats[0].view(logits.shape[:-1]).clone(), stats
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_loss, _):
+        if g_loss is None:
+            return (None,) * 5
+        logits, teacher_tokens, teacher_logits, stats = ctx.saved_tensors
+        grad = distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, g_loss.contiguous(),
+                                 temperature=ctx.temperature)
+        return grad, None, None, None, None
+
+
+def distill_loss(logits, teacher_tokens, teacher_logits, *, temperature: float = 1.0,
+                 scratch=None) -> DistillLoss:
+    """Divergence KL(q || p) per row of the student's distribution p = softmax(logits /
+    temperature) from the teacher's q, the softmax at the same temperature over its k entries.
+
+    teacher_tokens [..., k] int64 (negative: absent) and teacher_logits [..., k] float32 (logits or
+    log probabilities; -inf: no weight), such as token_logprobs(teacher, ..., top=k) returns. A row
+    without an entry of weight has loss 0. The loss is not multiplied by temperature ** 2.
+
+    Differentiable in the loss when the logits require a gradient; the teacher is a constant."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        _refuse_captured_autograd(logits)
+        return DistillLoss(*_DistillLoss.apply(logits, teacher_tokens, teacher_logits, temperature,
+                                               scratch))
+    stats = _distill(logits, teacher_tokens, teacher_logits, temperature, scratch)
+    return DistillLoss(stats[0] if logits.dim() == 2 else stats[0].view(logits.shape[:-1]), stats)
+
+
+def distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss, *,
+                      temperature: float = 1.0, out=None):
+    """Gradient of ``(grad_loss * loss).sum()`` with respect to the logits, in their type and shape
+    (contiguous; ``out``, if given, is such a tensor). stats is that of the forward call on the
+    same inputs; grad_loss is float32 in the logits' leading shape."""
+    r = _rows(logits)
+    k = _teacher(logits, teacher_tokens, teacher_logits)
+    _same(stats, "stats", logits, torch.float32, (5, r.rows))
+    _same(grad_loss, "grad_loss", logits, torch.float32, logits.shape[:-1])
+    temperature = _temperature(temperature)
+    out = _grad_out(logits, out)
+    with _On(logits.device) as stream:
+        rc = B.argreduce_distill_grad(logits.data_ptr(), r.code, r.rows, r.cols, r.stride, k,
+                                      teacher_tokens.data_ptr(), teacher_logits.data_ptr(),
+                                      temperature, stats.data_ptr(), grad_loss.data_ptr(),
+                                      out.data_ptr(), stream)
+    _done(rc, "argreduce_distill_grad", r)
+    return out
+
+
+def distill_step(logits, teacher_tokens, teacher_logits, weights, *, temperature: float = 1.0,
+                 out=None, scratch=None):
+    """(loss, grad): the loss of every row, and the gradient of ``(weights * loss).sum()`` with
+    respect to the logits, in one call that reads the logits from memory once. For a training step
+    whose row weights (float32, the logits' leading shape) do not depend on the loss."""
+    r = _rows(logits)
+    k = _teacher(logits, teacher_tokens, teacher_logits)
+    _same(weights, "weights", logits, torch.float32, logits.shape[:-1])
+    temperature = _temperature(temperature)
+    out = _grad_out(logits, out)
+    stats = torch.empty((5, r.rows), dtype=torch.float32, device=logits.device)
+    with _On(logits.device) as stream:
+        need = B.argreduce_distill_scratch_bytes(r.rows, r.cols, r.code)
+        scratch, sptr, sbytes = _scratch(need, "argreduce_distill_step", scratch, logits.device)
+        rc = B.argreduce_distill_step(logits.data_ptr(), r.code, r.rows, r.cols, r.stride, k,
+                                      teacher_tokens.data_ptr(), teacher_logits.data_ptr(),
+                                      temperature, weights.data_ptr(), stats.data_ptr(),
+                                      out.data_ptr(), sptr, sbytes, stream)
+    _done(rc, "argreduce_distill_step", r)
+    return (stats[0] if logits.dim() == 2 else stats[0].view(logits.shape[:-1])), out

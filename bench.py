@@ -65,6 +65,9 @@ KERNEL_SOURCES = ("argmin_reduction_wide_amd/csrc/argreduce_kernels.hip",
                   "argmin_reduction_wide_amd/csrc/argreduce_device.hpp",
                   "argmin_reduction_wide_amd/csrc/argreduce_api.cpp",
                   "argmin_reduction_wide_amd/csrc/argreduce_internal.hpp",
+                  "argmin_reduction_wide_amd/csrc/argreduce_logits.hip",
+                  "argmin_reduction_wide_amd/csrc/argreduce_logits.hpp",
+                  "argmin_reduction_wide_amd/csrc/argreduce_logits_api.cpp",
                   "include/argreduce.h")
 ROTATE_BYTES = 1 << 29  # 512 MiB of rotated inputs, twice the Infinity Cache
 PAGES_US_1x202048 = 6.4  # ArgMax fp32 [1,202048] per call on the pages' H200

@@ -295,6 +295,120 @@ int argreduce_scan_lastaxis(const void *x, argreduce_dtype_t dtype, int64_t rows
 int argreduce_scan_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
                         argreduce_plan_t *plan);
 
+/* ----------------------------------------------------------------------------------------
+ * Logits operators: a softmax over the same last axis that ArgMax answers from. Logits are a
+ * [rows, cols] tensor of f32, f16 or bf16 (other formats: ARGREDUCE_ERR_UNSUPPORTED_DTYPE), row
+ * r starting at element r * row_stride (row_stride >= cols; ignored for rows <= 1), so a padded
+ * vocabulary or a slice of a sequence needs no copy. With temperature T > 0:
+ *
+ *     p_j = exp(x_j / T) / sum_i exp(x_i / T)
+ *
+ * Statistics, sums and outputs are binary32 (a log probability below its range is -inf); a gradient is computed in binary32 and rounded
+ * once, to the nearest even value of the logits' format. Results do not depend on the order in
+ * which workgroups run: the same call gives the same bits.
+ *
+ *   - A logit of -inf is masked: probability 0, no gradient, never an alternative. The lowest
+ *     finite value is an ordinary value.
+ *   - A row whose every logit is -inf has log probabilities -inf, entropy 0, no alternatives
+ *     and gradient 0.
+ *   - A row with a NaN or +inf has NaN log probabilities, entropy and gradient and no
+ *     alternatives.
+ *   - Rows are independent: a row's contents change no other row's results.
+ *
+ * rows >= 0 (0 is a no-op); 1 <= cols <= INT32_MAX, rows <= INT32_MAX, row_stride <= UINT32_MAX
+ * (else ARGREDUCE_ERR_TOO_WIDE); 2^-60 <= T <= 2^60. x is aligned to its elements, int64 arrays
+ * to 8 and float arrays to 4 bytes. Inputs, outputs and scratch must not overlap. Scratch
+ * (argreduce_*_scratch_bytes, which depends on the shape only) is as for argreduce_lastaxis: any
+ * contents, any byte alignment, not shared by calls that can run at the same time. Token ids are
+ * read on the device and cannot be refused by the call: no id makes a kernel read or write out
+ * of range (what each gives is stated below). Everything else as for argreduce_lastaxis: the
+ * caller's stream, status codes before anything is enqueued, calls may be captured.
+ */
+#define ARGREDUCE_TOP_MAX 64        /* alternatives per row */
+#define ARGREDUCE_TEACHER_MAX 1024  /* teacher entries per row */
+
+/*
+ * Log probabilities of given tokens, with entropy and the top alternatives.
+ *
+ *   tokens        [rows]: the token of each row. A negative one leaves the row out: its logits
+ *                 do not matter, log probability and entropy are 0, and it has no alternatives.
+ *                 One >= cols gives a NaN log probability (and a NaN gradient, unless every
+ *                 logit of the row is -inf).
+ *   entropy       non-zero: compute the entropy; 0: row 1 of stats is NaN.
+ *   top           alternatives per row, 0 .. ARGREDUCE_TOP_MAX.
+ *   stats         [4, rows] out: ln p of the token; entropy -sum p ln p; and two rows for
+ *                 argreduce_logprobs_grad (the row's maximum, and log2 sum exp((x - max) / T)).
+ *   top_logprobs  [rows, top] out, top_tokens [rows, top] out (NULL if top is 0): the largest
+ *                 logits' ln p and positions, largest first, equal logits by position (-0 and +0
+ *                 are equal). Entries past the row's unmasked logits are -inf and -1 (NaN and
+ *                 -1 in a row with NaN or +inf).
+ */
+size_t argreduce_logprobs_scratch_bytes(int64_t rows, int64_t cols, argreduce_dtype_t dtype);
+int argreduce_logprobs(const void *x, argreduce_dtype_t dtype, int64_t rows, int64_t cols,
+                       int64_t row_stride, const int64_t *tokens, float temperature, int32_t entropy,
+                       int32_t top, float *stats, float *top_logprobs, int64_t *top_tokens,
+                       void *scratch, size_t scratch_bytes, void *stream);
+/* The plan of argreduce_logprobs: SUBWAVE (a group of lanes or a wavefront per row), BLOCK (a
+ * workgroup per row) or SPLIT (several workgroups per row, merged by a second dispatch; no
+ * workgroup waits on another). */
+int argreduce_logprobs_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
+                            argreduce_plan_t *plan);
+
+/*
+ * Gradient of sum_r (grad_logprob[r] * ln p of the token + grad_entropy[r] * entropy) with
+ * respect to the logits: grad is [rows, cols], contiguous, in the logits' format, every element
+ * written; 0 in rows left out and in rows of -inf. x, tokens and temperature are those of the
+ * forward call, stats what it wrote (with entropy if grad_entropy is not NULL).
+ */
+int argreduce_logprobs_grad(const void *x, argreduce_dtype_t dtype, int64_t rows, int64_t cols,
+                            int64_t row_stride, const int64_t *tokens, float temperature,
+                            const float *stats, const float *grad_logprob, const float *grad_entropy,
+                            void *grad, void *stream);
+
+/*
+ * Distillation from a teacher's top logits: per row the divergence KL(q || p) of the student's
+ * p (over all cols) from the teacher's q, the softmax at the same temperature over the row's k
+ * teacher entries,
+ *
+ *     q_i = exp(v_i / T) / sum_l exp(v_l / T),   loss = sum_i q_i (ln q_i - ln p_{id_i}).
+ *
+ *   teacher_tokens  [rows, k]: ids. A negative one marks an absent entry (its value does not
+ *                   matter). The same id twice: both entries count. An id >= cols with weight
+ *                   makes the row's loss and gradient NaN.
+ *   teacher_logits  [rows, k] f32: logits or log probabilities; -inf has no weight. The outputs
+ *                   of argreduce_logprobs (top_tokens, top_logprobs) can be passed as they are.
+ *                   A NaN (or +inf) of a present entry makes loss and gradient NaN.
+ *   k               1 .. ARGREDUCE_TEACHER_MAX.
+ *   stats           [5, rows] out: the loss, and four rows for argreduce_distill_grad.
+ *
+ * A row without an entry of weight has loss 0 and gradient 0, its logits do not matter. A row
+ * of -inf has loss +inf and gradient 0; a masked logit at an id with weight gives loss +inf.
+ */
+size_t argreduce_distill_scratch_bytes(int64_t rows, int64_t cols, argreduce_dtype_t dtype);
+int argreduce_distill(const void *x, argreduce_dtype_t dtype, int64_t rows, int64_t cols,
+                      int64_t row_stride, int32_t k, const int64_t *teacher_tokens,
+                      const float *teacher_logits, float temperature, float *stats, void *scratch,
+                      size_t scratch_bytes, void *stream);
+int argreduce_distill_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
+                           argreduce_plan_t *plan);
+
+/* Gradient of sum_r grad_loss[r] * loss[r]: grad[r][j] = grad_loss[r] (p_j - q_j) / T, [rows,
+ * cols], contiguous, in the logits' format, every element written. Inputs as in the forward
+ * call, stats what it wrote. */
+int argreduce_distill_grad(const void *x, argreduce_dtype_t dtype, int64_t rows, int64_t cols,
+                           int64_t row_stride, int32_t k, const int64_t *teacher_tokens,
+                           const float *teacher_logits, float temperature, const float *stats,
+                           const float *grad_loss, void *grad, void *stream);
+
+/* Both at once, for weights known before the loss: stats as argreduce_distill, grad as
+ * argreduce_distill_grad with grad_loss = weights. The logits are read from HBM once. Scratch as
+ * for argreduce_distill. */
+int argreduce_distill_step(const void *x, argreduce_dtype_t dtype, int64_t rows, int64_t cols,
+                           int64_t row_stride, int32_t k, const int64_t *teacher_tokens,
+                           const float *teacher_logits, float temperature, const float *weights,
+                           float *stats, void *grad, void *scratch, size_t scratch_bytes,
+                           void *stream);
+
 /* Measurement hook: the launch floor. Enqueues one empty kernel (one workgroup of 64
  * threads) on `stream`, the same way argreduce_lastaxis enqueues its kernels, so that a
  * benchmark can time bare launch latency in the same harness ("[CUDA] Parallelize

@@ -1,0 +1,610 @@
+"""The logits operators on the GPU against the plain 64-bit reference (logits_reference.py), whose
+error bounds are derived there; special rows, ties, layouts, streams, graphs, autograd and a run of
+the operators together."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import argmin_reduction_wide_amd as ar
+import argmin_reduction_wide_amd.binding as B
+import logits_reference as R
+from gpu_helpers import announce
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+INF = math.inf
+
+
+@pytest.fixture
+def capacity():
+    yield B.argreduce_debug_set_capacity
+    B.argreduce_debug_set_capacity(0)
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def make_rows(rng, rows, cols, dtype, std=2.0):
+    """Ordinary rows, and among them: masked, empty, constant, the lowest value throughout, one
+    that the lowest value masks, NaN, +inf, ascending, a few values only."""
+    x = rng.normal(size=(rows, cols)) * std
+    low = torch.finfo(DT[dtype]).min
+    for r in range(rows):
+        kind = r % 11
+        if kind == 1:
+            x[r, rng.random(cols) < 0.4] = -INF
+        elif kind == 2 and rows > 3:
+            x[r] = -INF
+        elif kind == 3:
+            x[r] = 0.25
+        elif kind == 4:
+            x[r] = low
+        elif kind == 5:
+            x[r, rng.random(cols) < 0.5] = low
+        elif kind == 6 and rows > 8:
+            x[r, int(rng.integers(cols))] = math.nan
+        elif kind == 7 and rows > 8:
+            x[r, int(rng.integers(cols))] = INF
+        elif kind == 8:
+            x[r] = np.arange(cols) % 97
+        elif kind == 9:
+            x[r] = rng.integers(0, 3, size=cols)
+        elif kind == 10:
+            x[r] = -INF
+            x[r, int(rng.integers(cols))] = -3.0
+    return torch.from_numpy(x).to(DT[dtype]).cuda()
+
+
+def check_logprobs(x, tokens, dtype, temperature=1.0, entropy=True, top=0, **kw):
+    r = ar.token_logprobs(x, tokens, temperature=temperature, entropy=entropy, top=top, **kw)
+    torch.cuda.synchronize()
+    xs, ts = host(x).reshape(-1, x.shape[-1]), tokens.cpu().numpy().reshape(-1)
+    lps, ents = host(r.logprob).reshape(-1), host(r.entropy).reshape(-1) if entropy else None
+    rows = []
+    for i in range(len(xs)):
+        want = R.logprobs_row(xs[i], int(ts[i]), temperature, top)
+        what = f"row {i} ({want['kind']})"
+        ok = want["kind"] == "ok"
+        R.agree(lps[i], want["logprob"], R.tol_logprob(want, want["logprob"]) if ok else 0, what)
+        if entropy:
+            R.agree(ents[i], want["entropy"], want["tol_entropy"] if ok else 0, what + " entropy")
+        if top:
+            got_t = r.top_tokens.reshape(-1, top)[i].cpu().numpy()
+            got_l = host(r.top_logprobs).reshape(-1, top)[i]
+            assert got_t.tolist() == [t for _, t in want["top"]], what
+            wl = np.array([v for v, _ in want["top"]])
+            tol = R.tol_logprob(want, np.where(np.isfinite(wl), wl, 0)) if ok else 0
+            R.agree(got_l, wl, tol, what + " alternatives")
+        rows.append(want)
+    return r, xs, ts, rows
+
+
+def check_logprobs_grad(x, tokens, dtype, temperature, entropy, r, xs, ts, rows, rng):
+    lead = x.shape[:-1]
+    g = torch.from_numpy(rng.normal(size=lead)).float().cuda()
+    e = torch.from_numpy(rng.normal(size=lead)).float().cuda() if entropy else None
+    grad = ar.token_logprobs_grad(x, tokens, r.stats, g, e, temperature=temperature)
+    torch.cuda.synchronize()
+    assert grad.dtype == x.dtype and grad.shape == x.shape and grad.is_contiguous()
+    got, gs = host(grad).reshape(xs.shape), host(g).reshape(-1)
+    es = host(e).reshape(-1) if entropy else [None] * len(xs)
+    for i in range(len(xs)):
+        d, tol = R.logprobs_grad_row(rows[i], xs[i], int(ts[i]), temperature, gs[i], es[i], dtype)
+        R.agree(got[i], d, tol, f"gradient of row {i} ({rows[i]['kind']})")
+
+
+def make_tokens(rng, rows, cols):
+    t = rng.integers(0, cols, size=rows)
+    if rows > 3:
+        t[rows // 2] = -100
+    if rows > 12:
+        t[11] = cols       # the first id beyond the row
+        t[0] = cols - 1
+        t[12] = 2 ** 40    # far beyond
+    return torch.from_numpy(t).cuda()
+
+
+# Widths round the borders between lane groups, wavefronts, workgroups and splits, odd ones among
+# them; with fewer columns than alternatives too.
+SHAPES = [(1, 1), (4, 2), (13, 3), (13, 8), (14, 31), (23, 64), (13, 65), (13, 127), (13, 129),
+          (13, 256), (14, 257), (13, 511), (13, 1000), (13, 1025), (13, 2047), (13, 2049), (12, 4100),
+          (11, 8200), (11, 16411)]
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_logprobs_and_gradient(dtype, rows, cols):
+    rng = np.random.default_rng(rows * 1000 + cols)
+    temperature = [1.0, 0.7, 3.0][cols % 3]
+    top = min(64, [0, 1, 5, 20, 64][(rows + cols) % 5])
+    entropy = (rows + cols) % 4 != 0
+    announce(f"logprobs {dtype} [{rows},{cols}] T={temperature} top={top} entropy={entropy}")
+    x = make_rows(rng, rows, cols, dtype)
+    tokens = make_tokens(rng, rows, cols)
+    got = check_logprobs(x, tokens, dtype, temperature, entropy, top)
+    check_logprobs_grad(x, tokens, dtype, temperature, entropy, *got, rng)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("cap", [2048, 256 * 2048])
+@pytest.mark.parametrize("rows,cols", [(11, 6000), (11, 20001), (3, 70001), (2, 262144)])
+def test_every_path(capacity, dtype, cap, rows, cols):
+    """A small simulated device takes a workgroup per row where the real one splits the row."""
+    rng = np.random.default_rng(cols)
+    assert capacity(cap) == 0
+    plan = B.argreduce_logprobs_plan(rows, cols, dtype)
+    announce(f"logprobs {dtype} [{rows},{cols}] capacity {cap}: path {plan['path']} "
+             f"lanes {plan['lanes_per_row']}")
+    x = make_rows(rng, rows, cols, dtype)
+    tokens = make_tokens(rng, rows, cols)
+    for top in (0, 7, 64):
+        got = check_logprobs(x, tokens, dtype, 1.0, top != 0, top)
+    check_logprobs_grad(x, tokens, dtype, 1.0, True, *got, rng)
+
+
+@pytest.mark.parametrize("cap", [2048, 256 * 2048])
+@pytest.mark.parametrize("cols", [40, 500, 1500, 30000, 140000])
+def test_alternatives_of_tied_rows(capacity, cap, cols):
+    """Rows whose ties put far more elements at the threshold than any buffer holds."""
+    capacity(cap)
+    announce(f"ties cols={cols} capacity {cap}")
+    rng = np.random.default_rng(7)
+    x = np.zeros((8, cols))
+    x[1] = np.arange(cols)            # ascending: every element beats those before it
+    x[2] = -np.arange(cols)
+    x[3] = np.arange(cols) // 64
+    x[4] = rng.integers(0, 2, size=cols)
+    x[5, cols // 2:] = -INF
+    x[6] = (np.arange(cols) % 256) // 32
+    x[7, 0::2] = -0.0                 # equal to +0
+    for dtype in sorted(DT):
+        t = torch.from_numpy(x).to(DT[dtype]).cuda()
+        check_logprobs(t, torch.zeros(8, dtype=torch.int64).cuda(), dtype, 1.0, True, 64)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("offset", [1, 3, 5])
+@pytest.mark.parametrize("cols,pad", [(50, 14), (64, 0), (1000, 1), (3001, 7), (9001, 8)])
+def test_strides_and_alignment(dtype, offset, cols, pad):
+    """Rows further apart than their length, starting at any element's address."""
+    rows = 13
+    rng = np.random.default_rng(offset * cols)
+    announce(f"strides {dtype} cols={cols} pad={pad} offset={offset}")
+    buf = torch.full((rows * (cols + pad) + offset + 16,), 1e4, dtype=DT[dtype], device="cuda")
+    x = buf[offset:offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    x.copy_(make_rows(rng, rows, cols, dtype))
+    tokens = make_tokens(rng, rows, cols)
+    got = check_logprobs(x, tokens, dtype, 1.0, True, 5)
+    check_logprobs_grad(x, tokens, dtype, 1.0, True, *got, rng)
+    ids, v = make_teacher(rng, rows, cols, 9)
+    check_distill(x, ids, v, dtype, 1.0, rng)
+    # a gradient buffer at any element's address
+    out = torch.full((rows * cols + offset + 8,), 7.0, dtype=DT[dtype], device="cuda")
+    view = out[offset:offset + rows * cols].view(rows, cols)
+    g = torch.ones(rows, device="cuda")
+    want = ar.token_logprobs_grad(x, tokens, got[0].stats, g)
+    ar.token_logprobs_grad(x, tokens, got[0].stats, g, out=view)
+    assert torch.equal(view.nan_to_num(9.0), want.nan_to_num(9.0))
+    assert (out[:offset] == 7).all() and (out[offset + rows * cols:] == 7).all()
+    loss, want = ar.distill_step(x, ids, v, g)
+    out.fill_(7.0)
+    ar.distill_step(x, ids, v, g, out=view)
+    assert torch.equal(view.nan_to_num(9.0), want.nan_to_num(9.0))
+    assert (out[:offset] == 7).all() and (out[offset + rows * cols:] == 7).all()
+
+
+def make_teacher(rng, rows, cols, k):
+    ids = rng.integers(0, cols, size=(rows, k))  # equal ids among them
+    v = rng.normal(size=(rows, k)) * 3
+    ids[rng.random((rows, k)) < 0.1] = -1
+    v[rng.random((rows, k)) < 0.05] = -INF
+    if rows > 2:
+        ids[1] = -1                   # no entry
+        v[2] = -INF                   # no weight
+    if rows > 10:
+        ids[8, 0], v[8, 0] = cols, 1.0
+        ids[9, 0], v[9, 0] = 0, math.nan
+        ids[10] = int(rng.integers(cols))  # one id only
+        v[10] = 1.0
+        ids[3, 0], v[3, 0] = -1, math.nan  # an absent entry's value does not matter
+    return torch.from_numpy(ids).cuda(), torch.from_numpy(v).float().cuda()
+
+
+def check_distill(x, ids, v, dtype, temperature, rng):
+    lead, cols = x.shape[:-1], x.shape[-1]
+    w = torch.from_numpy(rng.normal(size=lead)).float().cuda()
+    got = ar.distill_loss(x, ids, v, temperature=temperature)
+    grad = ar.distill_loss_grad(x, ids, v, got.stats, w, temperature=temperature)
+    loss, step_grad = ar.distill_step(x, ids, v, w, temperature=temperature)
+    torch.cuda.synchronize()
+    k = ids.shape[-1]
+    xs, ws = host(x).reshape(-1, cols), host(w).reshape(-1)
+    i_s, vs = ids.cpu().numpy().reshape(-1, k), host(v).reshape(-1, k)
+    for i in range(len(xs)):
+        want = R.distill_row(xs[i], i_s[i], vs[i], temperature)
+        what = f"row {i} ({want['kind']})"
+        tol = want.get("tol", 0)
+        R.agree(host(got.loss).reshape(-1)[i], want["loss"], tol, what)
+        R.agree(host(loss).reshape(-1)[i], want["loss"], tol, what + " step")
+        d, tol = R.distill_grad_row(want, xs[i], temperature, ws[i], dtype)
+        R.agree(host(grad).reshape(-1, cols)[i], d, tol, what + " gradient")
+        R.agree(host(step_grad).reshape(-1, cols)[i], d, tol, what + " step's gradient")
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("rows,cols,k", [(1, 1, 1), (3, 2, 3), (12, 7, 5), (13, 64, 64), (13, 65, 1),
+                                         (13, 500, 33), (12, 1030, 300), (12, 2050, 1024), (11, 4099, 8),
+                                         (11, 9000, 257), (3, 40001, 64)])
+def test_distill(dtype, rows, cols, k):
+    rng = np.random.default_rng(rows * 100 + cols + k)
+    temperature = [1.0, 2.0, 0.8][cols % 3]
+    announce(f"distill {dtype} [{rows},{cols}] k={k} T={temperature}")
+    x = make_rows(rng, rows, cols, dtype)
+    ids, v = make_teacher(rng, rows, cols, k)
+    check_distill(x, ids, v, dtype, temperature, rng)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("cap", [2048, 256 * 2048])
+def test_distill_every_path(capacity, dtype, cap):
+    capacity(cap)
+    rng = np.random.default_rng(5)
+    for rows, cols in [(11, 6000), (3, 70001)]:
+        announce(f"distill {dtype} [{rows},{cols}] capacity {cap}: "
+                 f"path {B.argreduce_distill_plan(rows, cols, dtype)['path']}")
+        x = make_rows(rng, rows, cols, dtype)
+        ids, v = make_teacher(rng, rows, cols, 40)
+        check_distill(x, ids, v, dtype, 1.5, rng)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows 2^31 + 8 elements apart: the last starts past 2^32 elements."""
+    stride, cols = 2 ** 31 + 8, 1000
+    announce("offsets beyond 32 bits")
+    buf = torch.empty(2 * stride + cols, dtype=torch.float16, device="cuda")
+    x = buf.as_strided((3, cols), (stride, 1))
+    rng = np.random.default_rng(3)
+    x.copy_(torch.from_numpy(rng.normal(size=(3, cols))).half().cuda())
+    tokens = torch.tensor([5, 999, 0], device="cuda")
+    got = check_logprobs(x, tokens, "f16", 1.0, True, 5)
+    check_logprobs_grad(x, tokens, "f16", 1.0, True, *got, rng)
+    check_distill(x, *make_teacher(rng, 3, cols, 7), "f16", 1.0, rng)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 3_000_001), (2, 1_000_003)])
+def test_very_wide_rows(rows, cols):
+    announce(f"wide [{rows},{cols}]")
+    rng = np.random.default_rng(1)
+    x = torch.from_numpy(rng.normal(size=(rows, cols)) * 3).float().cuda()
+    tokens = torch.tensor([cols - 1, 17][:rows], device="cuda")
+    got = check_logprobs(x, tokens, "f32", 1.0, True, 64)
+    check_logprobs_grad(x, tokens, "f32", 1.0, True, *got, rng)
+    check_distill(x, *make_teacher(rng, rows, cols, 64), "f32", 1.0, rng)
+
+
+def test_many_rows():
+    """More rows than a device wave, short ones."""
+    announce("many rows")
+    rng = np.random.default_rng(2)
+    x = torch.from_numpy(rng.normal(size=(70000, 24)) * 2).half().cuda()
+    tokens = torch.from_numpy(rng.integers(-1, 24, size=70000)).cuda()
+    r = ar.token_logprobs(x, tokens, entropy=True, top=3)
+    y = torch.log_softmax(x.double(), 1)
+    live = tokens >= 0
+    want = torch.where(live, y.gather(1, tokens.clamp(min=0)[:, None])[:, 0], 0.0)
+    # rows of 24: E|z| below 30 and 81 additions (see logits_reference), log probabilities below 20
+    assert (r.logprob.double() - want).abs().max() < R.U * (3 * 30 + 83 + 8 * 24)
+    v, i = x.float().sort(dim=1, descending=True, stable=True)
+    assert torch.equal(r.top_tokens, torch.where(live[:, None], i[:, :3], -1))
+
+
+@pytest.mark.parametrize("value", [1e4, -1e4, 6e4])
+def test_large_common_offset(value):
+    """A constant added to a row changes nothing but the rounding of the stored logits."""
+    announce(f"offset {value}")
+    rng = np.random.default_rng(4)
+    x = torch.from_numpy(rng.normal(size=(11, 3000)) * 2 + value).float().cuda()
+    tokens = make_tokens(rng, 11, 3000)
+    got = check_logprobs(x, tokens, "f32", 1.0, True, 20)
+    check_logprobs_grad(x, tokens, "f32", 1.0, True, *got, rng)
+
+
+@pytest.mark.parametrize("temperature", [2.0 ** -60, 1e-3, 1e3, 2.0 ** 60])
+def test_extreme_temperatures(temperature):
+    announce(f"temperature {temperature}")
+    rng = np.random.default_rng(6)
+    for cols in (40, 700, 9000):
+        x = torch.from_numpy(np.round(rng.normal(size=(5, cols)) * 4) / 4).float().cuda()
+        tokens = torch.from_numpy(rng.integers(0, cols, size=5)).cuda()
+        r = ar.token_logprobs(x, tokens, temperature=temperature, entropy=True)
+        torch.cuda.synchronize()
+        xs = host(x)
+        for i in range(5):
+            want = R.logprobs_row(xs[i], int(tokens[i]), temperature, 0)
+            lp = want["logprob"]
+            # beyond the range of a float the log probability is -inf
+            if lp < -3e38:
+                assert r.logprob[i] == -INF
+            else:
+                R.agree(host(r.logprob[i]), lp, R.tol_logprob(want, lp) + 3 * R.U * abs(lp), f"row {i}")
+            R.agree(host(r.entropy[i]), want["entropy"], want["tol_entropy"], f"row {i} entropy")
+
+
+def test_leading_dimensions_and_slices():
+    announce("leading dimensions")
+    rng = np.random.default_rng(8)
+    full = torch.from_numpy(rng.normal(size=(3, 5, 640))).float().cuda()
+    x = full[:, :, :600]
+    tokens = torch.from_numpy(rng.integers(0, 600, size=(3, 5))).cuda()
+    got = check_logprobs(x, tokens, "f32", 1.0, True, 4)
+    assert got[0].logprob.shape == (3, 5) and got[0].top_tokens.shape == (3, 5, 4)
+    check_logprobs_grad(x, tokens, "f32", 1.0, True, *got, rng)
+    last = full[:, -1]  # one position of every sequence: rows 5 * 640 apart
+    check_logprobs(last, tokens[:, -1].contiguous(), "f32", 1.0, True, 4)
+    one = full[0, 0]
+    r = ar.token_logprobs(one, tokens[0, 0], entropy=True, top=2)
+    assert r.logprob.shape == () and r.top_tokens.shape == (2,)
+    assert torch.equal(r.logprob, ar.token_logprobs(full[0], tokens[0], entropy=True).logprob[0]) or \
+        abs(float(r.logprob) - float(torch.log_softmax(one.double(), 0)[tokens[0, 0]])) < 1e-5
+    empty = ar.token_logprobs(full[:0, 0], tokens[:0, 0].contiguous(), entropy=True, top=2)
+    assert empty.logprob.shape == (0,) and empty.top_tokens.shape == (0, 2)
+    loss, grad = ar.distill_step(full[:0, 0], torch.zeros(0, 3, dtype=torch.int64, device="cuda"),
+                                 torch.zeros(0, 3, device="cuda"), torch.zeros(0, device="cuda"))
+    assert loss.shape == (0,) and grad.shape == (0, 640)
+
+
+def test_refusals():
+    announce("refusals")
+    x = torch.zeros(4, 8, device="cuda")
+    t = torch.zeros(4, dtype=torch.int64, device="cuda")
+    ids, v = torch.zeros(4, 3, dtype=torch.int64, device="cuda"), torch.zeros(4, 3, device="cuda")
+    w = torch.zeros(4, device="cuda")
+    bad = [lambda: ar.token_logprobs(x.double(), t), lambda: ar.token_logprobs(x.t(), t),
+           lambda: ar.token_logprobs(x, t.int()), lambda: ar.token_logprobs(x, t[:3]),
+           lambda: ar.token_logprobs(x, t.cpu()), lambda: ar.token_logprobs(x, t, temperature=0.0),
+           lambda: ar.token_logprobs(x, t, temperature=math.nan),
+           lambda: ar.token_logprobs(x, t, top=65), lambda: ar.token_logprobs(x, t, top=-1),
+           lambda: ar.token_logprobs(x[:, :0], t), lambda: ar.token_logprobs(x[0, 0], t[0]),
+           lambda: ar.token_logprobs(x[:1].expand(4, 8), t),
+           lambda: ar.token_logprobs(x.view(2, 2, 8).transpose(0, 1), t.view(2, 2)),
+           lambda: ar.token_logprobs(x, torch.zeros(8, dtype=torch.int64, device="cuda")[::2]),
+           lambda: ar.token_logprobs(x, t, scratch=torch.empty(64)),
+           lambda: ar.token_logprobs_grad(x, t, torch.zeros(5, 4, device="cuda"), w),
+           lambda: ar.token_logprobs_grad(x, t, torch.zeros(4, 4, device="cuda"), w.double()),
+           lambda: ar.token_logprobs_grad(x, t, torch.zeros(4, 4, device="cuda"), w, w[:2]),
+           lambda: ar.token_logprobs_grad(x, t, torch.zeros(4, 4, device="cuda"), w, out=x.half()),
+           lambda: ar.token_logprobs_grad(x, t, torch.zeros(4, 4, device="cuda"), w, out=x.view(8, 4)),
+           lambda: ar.distill_loss(x, ids, v.double()), lambda: ar.distill_loss(x, ids[:, :2], v),
+           lambda: ar.distill_loss(x, ids[:, :0], v[:, :0]), lambda: ar.distill_loss(x, ids.int(), v),
+           lambda: ar.distill_loss(x, torch.zeros(4, 1025, dtype=torch.int64, device="cuda"),
+                                   torch.zeros(4, 1025, device="cuda")),
+           lambda: ar.distill_loss_grad(x, ids, v, torch.zeros(4, 4, device="cuda"), w),
+           lambda: ar.distill_step(x, ids, v, w[:2]),
+           lambda: ar.distill_step(x, ids, v, w, out=torch.zeros(4, 16, device="cuda")[:, ::2])]
+    for n, f in enumerate(bad):
+        with pytest.raises((ValueError, ar.ArgreduceError)):
+            f()
+            pytest.fail(f"call {n} was not refused")
+
+
+def raw_logprobs(x, tokens, top, stats, lp, tok, scratch, soff, sbytes):
+    return B.argreduce_logprobs(x.data_ptr(), B.F32, x.shape[0], x.shape[1], x.stride(0), tokens.data_ptr(),
+                                1.0, 1, top, stats.data_ptr(), lp.data_ptr(), tok.data_ptr(),
+                                scratch.data_ptr() + soff, sbytes, torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("soff", [0, 1, 13])
+def test_scratch_and_output_bounds(soff):
+    """Nothing outside the outputs and the scratch's stated size is written; the scratch may start
+    anywhere and hold anything."""
+    announce(f"bounds, scratch offset {soff}")
+    rows, cols, top = 3, 202048, 20
+    rng = np.random.default_rng(9)
+    x = torch.from_numpy(rng.normal(size=(rows, cols))).float().cuda()
+    tokens = torch.tensor([0, -1, cols - 1], device="cuda")
+    need = B.argreduce_logprobs_scratch_bytes(rows, cols, B.F32)
+    assert need > 0
+    want = ar.token_logprobs(x, tokens, entropy=True, top=top)
+    for fill in (0, 255, 0x7f):
+        scratch = torch.full((need + 64,), fill, dtype=torch.uint8, device="cuda")
+        stats = torch.full((4 * rows + 8,), 5.0, device="cuda")
+        lp = torch.full((rows * top + 8,), 5.0, device="cuda")
+        tok = torch.full((rows * top + 8,), 5, dtype=torch.int64, device="cuda")
+        assert raw_logprobs(x, tokens, top, stats, lp, tok, scratch, soff, need) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(stats[:4 * rows], want.stats.reshape(-1)) and (stats[4 * rows:] == 5).all()
+        assert torch.equal(lp[:rows * top], want.top_logprobs.reshape(-1)) and (lp[rows * top:] == 5).all()
+        assert torch.equal(tok[:rows * top], want.top_tokens.reshape(-1)) and (tok[rows * top:] == 5).all()
+        assert (scratch[:soff] == fill).all() and (scratch[soff + need:] == fill).all()
+
+
+SAME = [(3, 50), (40, 900), (5, 5000), (2, 202048), (700, 40000)]
+
+
+@pytest.mark.parametrize("rows,cols", SAME)
+def test_same_bits_every_time(rows, cols):
+    announce(f"same bits [{rows},{cols}]")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, cols, device="cuda", generator=g).bfloat16()
+    tokens = torch.randint(0, cols, (rows,), device="cuda", generator=g)
+    ids = torch.randint(0, cols, (rows, 40), device="cuda", generator=g)
+    v, w = torch.randn(rows, 40, device="cuda", generator=g), torch.rand(rows, device="cuda", generator=g)
+
+    def once():
+        r = ar.token_logprobs(x, tokens, entropy=True, top=9)
+        return [r.stats, r.top_logprobs, r.top_tokens, ar.token_logprobs_grad(x, tokens, r.stats, w, w),
+                *ar.distill_step(x, ids, v, w)]
+
+    first = once()
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(first, once()))
+
+
+def test_streams():
+    """Calls side by side on two streams, each with scratch of its own, on tensors made on another."""
+    announce("streams")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    xs = [torch.randn(4, 202048, device="cuda", generator=g) for _ in range(2)]
+    tokens = torch.randint(0, 202048, (4,), device="cuda", generator=g)
+    want = [ar.token_logprobs(x, tokens, entropy=True, top=20) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for n, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[n].append(ar.token_logprobs(xs[n], tokens, entropy=True, top=20))
+    torch.cuda.synchronize()
+    for n in range(2):
+        for r in got[n]:
+            assert torch.equal(r.stats, want[n].stats) and torch.equal(r.top_tokens, want[n].top_tokens)
+
+
+@pytest.mark.parametrize("rows,cols", [(6, 100), (3, 202048), (600, 20000)])
+def test_graph_replay(rows, cols):
+    """A captured run replayed on new inputs, with eager work between the replays."""
+    announce(f"graph [{rows},{cols}]")
+    x = torch.randn(rows, cols, device="cuda").half()
+    tokens = torch.randint(0, cols, (rows,), device="cuda")
+    ids, v = torch.randint(0, cols, (rows, 12), device="cuda"), torch.randn(rows, 12, device="cuda")
+    w = torch.rand(rows, device="cuda")
+
+    def work():
+        r = ar.token_logprobs(x, tokens, entropy=True, top=6)
+        g = ar.token_logprobs_grad(x, tokens, r.stats, w, w)
+        return [r.stats, r.top_logprobs, r.top_tokens, g, *ar.distill_step(x, ids, v, w)]
+
+    work()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):  # two graphs alive at once
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = work()
+        graphs.append((graph, outs))
+    for n in range(4):
+        x.copy_(torch.randn(rows, cols, device="cuda").half())
+        tokens.copy_(torch.randint(-1, cols, (rows,), device="cuda"))
+        graph, outs = graphs[n % 2]
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        want = work()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), f"replay {n}"
+
+
+def test_autograd():
+    announce("autograd")
+    rng = np.random.default_rng(11)
+    for dtype in sorted(DT):
+        x = torch.from_numpy(rng.normal(size=(3, 4, 700))).to(DT[dtype]).cuda().requires_grad_()
+        tokens = torch.from_numpy(rng.integers(0, 700, size=(3, 4))).cuda()
+        g, e = torch.randn(3, 4, device="cuda"), torch.randn(3, 4, device="cuda")
+        r = ar.token_logprobs(x, tokens, temperature=0.9, entropy=True, top=3)
+        assert r.logprob.requires_grad and r.entropy.requires_grad
+        assert not r.top_logprobs.requires_grad and not r.stats.requires_grad
+        (r.logprob * g + r.entropy * e).sum().backward()
+        want = ar.token_logprobs_grad(x.detach(), tokens, r.stats, g, e, temperature=0.9)
+        assert torch.equal(x.grad, want)
+        for pick in ("logprob", "entropy"):  # one output alone
+            x.grad = None
+            r = ar.token_logprobs(x, tokens, entropy=True)
+            (getattr(r, pick) * g).sum().backward()
+            z = torch.zeros_like(g)
+            want = ar.token_logprobs_grad(x.detach(), tokens, r.stats, *((g, z) if pick == "logprob" else (z, g)))
+            assert torch.allclose(x.grad, want, rtol=2 * R.HALF_STEP[dtype], atol=1e-6)
+        ids, v = torch.randint(0, 700, (3, 4, 5), device="cuda"), torch.randn(3, 4, 5, device="cuda")
+        x.grad = None
+        d = ar.distill_loss(x, ids, v, temperature=1.5)
+        d.loss.backward(g)
+        _, want = ar.distill_step(x.detach(), ids, v, g, temperature=1.5)
+        assert torch.equal(x.grad, want)
+        # an expanded gradient, and through a view of padded logits
+        big = torch.zeros(6, 704, dtype=DT[dtype], device="cuda", requires_grad=True)
+        ar.token_logprobs(big[:, :700], torch.zeros(6, dtype=torch.int64, device="cuda")).logprob.sum().backward()
+        assert (big.grad[:, 700:] == 0).all() and (big.grad[:, 0] > 0).all() and (big.grad[:, 1:700] < 0).all()
+        with torch.no_grad():
+            assert not ar.token_logprobs(x, tokens).logprob.requires_grad
+
+
+def test_gradient_is_the_difference():
+    """The kernels' gradients against central differences of the 64-bit values."""
+    announce("differences")
+    rng = np.random.default_rng(12)
+    cols, step = 37, 1e-4
+    x = torch.from_numpy(rng.normal(size=(1, cols))).float().cuda()
+    tokens = torch.tensor([5], device="cuda")
+    ids, v = torch.tensor([[3, 9, 3, -1]], device="cuda"), torch.tensor([[1.0, 0.5, -1.0, 9.0]], device="cuda")
+    one = torch.ones(1, device="cuda")
+    r = ar.token_logprobs(x, tokens, entropy=True)
+    g = host(ar.token_logprobs_grad(x, tokens, r.stats, one, one))[0]
+    dg = host(ar.distill_step(x, ids, v, one)[1])[0]
+    y = host(x)[0]
+    for j in range(cols):
+        a, b = y.copy(), y.copy()
+        a[j] += step
+        b[j] -= step
+        f = [R.logprobs_row(t, 5, 1.0, 0) for t in (a, b)]
+        diff = (f[0]["logprob"] + f[0]["entropy"] - f[1]["logprob"] - f[1]["entropy"]) / (2 * step)
+        assert abs(diff - g[j]) < 30 * step ** 2 + 1e-5  # third derivative, and 32-bit arithmetic
+        d = [R.distill_row(t, host(ids)[0].astype(int), host(v)[0], 1.0)["loss"] for t in (a, b)]
+        assert abs((d[0] - d[1]) / (2 * step) - dg[j]) < 30 * step ** 2 + 1e-5
+
+
+def test_captured_autograd_is_refused():
+    announce("captured autograd")
+    x = torch.randn(4, 100, device="cuda", requires_grad=True)
+    tokens = torch.zeros(4, dtype=torch.int64, device="cuda")
+    ids, v = torch.zeros(4, 2, dtype=torch.int64, device="cuda"), torch.zeros(4, 2, device="cuda")
+    ar.token_logprobs(x, tokens).logprob.sum().backward()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="captured"):
+            ar.token_logprobs(x, tokens)
+        with pytest.raises(RuntimeError, match="captured"):
+            ar.distill_loss(x, ids, v)
+        with torch.no_grad():
+            r = ar.token_logprobs(x, tokens)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(r.logprob, ar.token_logprobs(x.detach(), tokens).logprob)
+
+
+def test_run_together():
+    """A teacher's top alternatives go straight into the student's loss; the greedy answer of the
+    library is the first alternative; an eager autograd step, the single call and a captured step
+    agree."""
+    announce("run together")
+    g = torch.Generator(device="cuda").manual_seed(13)
+    rows, cols, k = 24, 32003, 16
+    hidden = torch.randn(rows, 64, device="cuda", generator=g)
+    teacher = hidden @ torch.randn(64, cols, device="cuda", generator=g) * 0.4
+    weight = (torch.randn(64, cols, device="cuda", generator=g) * 0.1).requires_grad_()
+    tokens = torch.full((rows,), -1, dtype=torch.int64, device="cuda")
+    greedy = ar.argmax(teacher)
+    t = ar.token_logprobs(teacher, greedy, top=k)
+    assert torch.equal(t.top_tokens[:, 0], greedy) and torch.equal(t.top_logprobs[:, 0], t.logprob)
+    skipped = ar.token_logprobs(teacher, tokens, top=k)  # rows left out: no teacher
+    ids, v = t.top_tokens.clone(), t.top_logprobs.clone()
+    ids[::4], v[::4] = skipped.top_tokens[::4], skipped.top_logprobs[::4]
+    logits = hidden @ weight
+    d = ar.distill_loss(logits, ids, v, temperature=2.0)
+    assert (d.loss[::4] == 0).all() and (d.loss[1::4] > 0).all()
+    share = torch.full((rows,), 1.0 / rows, device="cuda")
+    (d.loss * share).sum().backward()
+    loss, grad = ar.distill_step(logits.detach(), ids, v, share, temperature=2.0)
+    assert torch.equal(loss, d.loss.detach())
+    # the product of the same gradient: the same call, so the same rounding
+    assert torch.equal(weight.grad, hidden.t() @ grad)
+    # against 64 bits: the share, q and p of each row
+    p = torch.softmax(logits.detach().double() / 2, 1)
+    q = torch.zeros_like(p)
+    live = ids[:, 0] >= 0
+    q.scatter_add_(1, ids.clamp(min=0), torch.where(live[:, None], torch.softmax(v.double() / 2, 1), 0.0).nan_to_num(0.0))
+    want = (p * live[:, None] - q) / 2 / rows
+    # |logits| < 40 / 2: z is off by 3 u 60, the sums by 600 u (logits_reference), times p or q <= 1
+    assert (grad.double() - want).abs().max() < R.U * 1000 / rows
