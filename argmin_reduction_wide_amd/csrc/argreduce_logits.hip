@@ -24,6 +24,10 @@
 #include "argreduce_launch.hpp"
 #include "argreduce_logits.hpp"
 
+// Products and sums are fused where the source says so and nowhere else, so that two kernels
+// that compute the same quantity from the same inputs get the same bits.
+#pragma clang fp contract(off)
+
 namespace argreduce {
 namespace {
 
@@ -107,7 +111,7 @@ constexpr int kTeamBlock = T == kWave ? kBlockThreads : T;
 // ln p of a logit v in a row of maximum m: in units of e, not of 2, since (v - m) k can leave
 // binary32's range where (v - m) / T does not (v the lowest finite value, as some masks have it).
 __device__ inline float ln_p(float v, float m, float l2, float scale) {
-    return (v - m) * (scale * kLn2) - l2 * kLn2;
+    return fmaf(v - m, scale * kLn2, -l2 * kLn2);
 }
 
 struct Stat {
@@ -122,7 +126,7 @@ struct Stat {
     __device__ void move(float to, float k) {
         const float d = (to - m) * k;
         const float r = exp2_f(-d);
-        if constexpr (ENT) h = r * (h - fminf(d, -kZFloor) * s);
+        if constexpr (ENT) h = r * fmaf(-fminf(d, -kZFloor), s, h);
         s *= r;
         m = to;
     }
@@ -209,85 +213,177 @@ __device__ inline typename Fmt::Vec load16(const uint8_t* p) {
     return *reinterpret_cast<const typename Fmt::Vec*>(p);
 }
 
-// Takes N elements into the running part.
+// Takes N (even) elements into the running part; returns the larger of `m` and their maximum.
 template <bool ENT, int N>
-__device__ inline void take(const float (&e)[N], float k, Stat& a) {
-    float m = a.m;
+__device__ inline float take(const float (&e)[N], float k, Stat& a, float m = kLowest) {
 #pragma unroll
-    for (int i = 0; i + 1 < N; i += 2) m = max3_f(m, e[i], e[i + 1]);
-    if constexpr (N % 2) m = max_f(m, e[N - 1]);
-    a.move<ENT>(m, k);
+    for (int i = 0; i < N; i += 2) m = max3_f(m, e[i], e[i + 1]);
+    a.move<ENT>(max_f(a.m, m), k);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float z = (e[i] - m) * k;
+        const float z = (e[i] - a.m) * k;
         const float p = exp2_f(z);
         a.s += p;
         if constexpr (ENT) a.h = fmaf(p, max_f(z, kZFloor), a.h);
     }
+    return m;
 }
 
-// One lane's share of a row: its edge vector, then vectors first + lane, + T, ... below last.
-template <typename Fmt, bool ENT, int T, int U>
+// Loads vectors v, v + T, ... (U of them) as floats; those at or past `last` as -inf.
+template <typename Fmt, int T, int U>
+__device__ inline void load_step(const Span<Fmt>& sp, uint32_t v, uint32_t last, bool full,
+                                 float (&e)[U * Fmt::VW]) {
+    constexpr int VW = Fmt::VW;
+    typename Fmt::Vec q[U];
+    if (full) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = load16<Fmt>(sp.at(v + u * T));
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = load16<Fmt>(sp.at(v + u * T < last ? v + u * T : last - 1));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float f[VW];
+        Fmt::unpack(q[u], f);
+        const bool in = full || v + u * T < last;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) e[u * VW + i] = in ? f[i] : -__builtin_huge_valf();
+    }
+}
+
+// The edge vector of lane 0 or 1.
+template <typename Fmt, bool ENT>
+__device__ inline void scan_edge(const Span<Fmt>& sp, int lane, float k, Stat& a) {
+    const uint32_t v = sp.edge(lane);
+    if (v == kNoVec) return;
+    float e[Fmt::VW];
+    Fmt::unpack(load16<Fmt>(sp.at(v)), e);
+    const uint32_t p0 = sp.pos(v);
+#pragma unroll
+    for (int i = 0; i < Fmt::VW; ++i) e[i] = p0 + i < sp.cols ? e[i] : -__builtin_huge_valf();
+    take<ENT>(e, k, a);
+}
+
+// The segments of vectors [first, last) whose maxima a scan by T lanes in steps of U vectors per
+// lane leaves for top_select, at most `most` of them: single vectors, or eight neighbouring ones
+// (whole 128-byte lines), or eight lanes' vectors of `group` steps.
+struct Segments {
+    uint32_t first, last, lg_vecs, group, row;  // row: vectors between two of a lane's
+    int oct;
+    template <int T, int U>
+    __device__ static Segments cut(uint32_t first, uint32_t last, uint32_t most) {
+        const uint32_t n = last - first, steps = (n + U * T - 1) / (U * T);
+        Segments g{first, last, 0, 0, T, T / 8};
+        if (n > most) {
+            g.lg_vecs = 3;
+            if (n > 8 * most) {
+                g.group = (steps * g.oct + most - 1) / most;
+                g.lg_vecs = 32 - __clz(8 * U * g.group - 1);
+            }
+        }
+        g.group *= U;
+        return g;
+    }
+    __device__ uint32_t count() const {
+        const uint32_t n = last - first;
+        return group == 0 ? (n + (1u << lg_vecs) - 1) >> lg_vecs : (n + group * row - 1) / (group * row) * oct;
+    }
+    // Vector i (of 2^lg_vecs) of segment s, or kNoVec.
+    __device__ uint32_t vec(uint32_t s, uint32_t i) const {
+        uint32_t v;
+        if (group == 0) {
+            v = first + (s << lg_vecs) + i;
+        } else {
+            if (i / 8 >= group) return kNoVec;
+            v = first + (s / oct * group + i / 8) * row + s % oct * 8 + i % 8;
+        }
+        return v < last ? v : kNoVec;
+    }
+};
+
+// One lane's share of a row: its edge vector, then vectors first + lane, + T, ... below last in
+// steps of U, the last step filled up with -inf. With SEG the maxima of g's segments go to seg[].
+template <typename Fmt, bool ENT, int T, int U, bool SEG = false>
 __device__ inline void scan_span(const Span<Fmt>& sp, bool edges, uint32_t first, uint32_t last,
-                                 int lane, float k, Stat& a) {
+                                 int lane, float k, Stat& a, const Segments& g = Segments{},
+                                 float* seg = nullptr) {
     constexpr int VW = Fmt::VW;
     a.init();
-    if (edges) {
-        const uint32_t ev = sp.edge(lane);
-        if (ev != kNoVec) {
-            float e[VW];
-            Fmt::unpack(load16<Fmt>(sp.at(ev)), e);
-            const uint32_t p0 = sp.pos(ev);
+    if (edges && lane < 2) scan_edge<Fmt, ENT>(sp, lane, k, a);
+    float m = kLowest;
+    uint32_t left = g.group, at = lane / 8;
+    for (uint32_t base = first; base < last; base += U * T) {
+        float e[U * VW];
+        const bool full = last - base >= U * T;
+        load_step<Fmt, T, U>(sp, base + lane, last, full, e);
+        if constexpr (SEG) {
+            if (g.group == 0) {
 #pragma unroll
-            for (int i = 0; i < VW; ++i) e[i] = p0 + i < sp.cols ? e[i] : -__builtin_huge_valf();
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t i = base - first + lane + u * T;
+                    float v = e[u * VW];
+#pragma unroll
+                    for (int j = 1; j + 1 < VW; j += 2) v = max3_f(v, e[u * VW + j], e[u * VW + j + 1]);
+                    v = max_f(v, e[u * VW + VW - 1]);
+                    if (g.lg_vecs) v = lanes_max<8>(v);
+                    if (i < last - first && (i & ((1u << g.lg_vecs) - 1)) == 0) seg[i >> g.lg_vecs] = v;
+                }
+                take<ENT>(e, k, a);
+            } else {
+                m = take<ENT>(e, k, a, m);
+                left -= U;
+                if (left == 0) {
+                    m = lanes_max<8>(m);
+                    if (lane % 8 == 0) seg[at] = m;
+                    m = kLowest;
+                    left = g.group;
+                    at += T / 8;
+                }
+            }
+        } else {
             take<ENT>(e, k, a);
         }
     }
-    uint32_t v = first + lane;
-    for (; v + (U - 1) * T < last; v += U * T) {
-        typename Fmt::Vec q[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = load16<Fmt>(sp.at(v + u * T));
-        float e[U * VW];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float f[VW];
-            Fmt::unpack(q[u], f);
-#pragma unroll
-            for (int i = 0; i < VW; ++i) e[u * VW + i] = f[i];
+    if constexpr (SEG)
+        if (left != g.group) {
+            m = lanes_max<8>(m);
+            if (lane % 8 == 0) seg[at] = m;
         }
-        take<ENT>(e, k, a);
-    }
-    for (; v < last; v += T) {
-        float e[VW];
-        Fmt::unpack(load16<Fmt>(sp.at(v)), e);
-        take<ENT>(e, k, a);
-    }
 }
 
 // ---------------------------------------------------------------------------------------
 // The k best elements of a row, by (value descending, position ascending).
 //
-// A pass over the row leaves the maximum of each of S segments (a lane's or a wavefront's
-// share). With tau the k-th largest of those maxima, the k best elements are all >= tau and
-// lie in segments whose maximum is >= tau: only these are read again, from the caches, and
+// A pass over the row leaves the maximum of each of S segments (struct Segments). For a tau that at least k of these maxima reach, the k best elements are all >= tau
+// and lie in segments whose maximum is >= tau: only these are read again, from the caches, and
 // their elements >= tau collected in LDS as 64-bit keys (value above complemented position).
-// Ranking the keys by counting gives the sorted result. Ties may put more keys into the
-// buffer than it holds; the collection then starts again in steps that cannot overflow it, the
-// buffer cut to its k best in between.
+// Ranking the keys by counting gives the sorted result. tau comes from a bisection that stops
+// when few more than k maxima reach it. Ties may put more keys into the buffer than it holds;
+// the collection then starts again in steps that cannot overflow it, the buffer cut to its k
+// best in between.
 
 __device__ inline uint64_t key_of(float v, uint32_t pos) { return Key32<kMax>::make(v, pos); }
+// Unsigned integers in the order of the floats, and back.
+__device__ inline uint32_t order_of(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ inline float value_of(uint32_t o) {
+    return __uint_as_float((o >> 31) ? (o & 0x7fffffffu) : ~o);
+}
 
 template <int T, int S>
 struct TopLds {
-    static constexpr int kCap = 4 * T + kTopMax;
+    static constexpr int kStep = T / 4;  // vectors per step of the bounded collection
+    static constexpr int kCap = 8 * kStep + kTopMax;
     uint64_t buf[kCap];
     uint64_t best[T];
     float seg[S];
     uint16_t list[S];
     uint32_t count, listed;
-    uint64_t least;  // keys at or below it cannot be among the k best
     float tau;
+    uint64_t least;  // keys at or below it cannot be among the k best
 };
 
 // Cuts the buffer to its k best keys, sorted. Called by the whole team after a team_sync.
@@ -319,10 +415,15 @@ __device__ inline void top_cut(TopLds<T, S>& L, int lane, uint32_t k) {
         team_sync<T>();
         n = L.count;
     }
-    for (uint32_t i = lane; i < n; i += T) {
+    // ranks: kShare lanes count for a key, each over every kShare-th of the others
+    constexpr int kShare = T >= 512 ? 4 : (T >= 256 ? 2 : 1);
+    for (uint32_t i = lane / kShare; i < n; i += T / kShare) {
         const uint64_t key = L.buf[i];
         uint32_t above = 0;
-        for (uint32_t j = 0; j < n; ++j) above += L.buf[j] > key ? 1 : 0;
+#pragma unroll 4
+        for (uint32_t j = lane % kShare; j < n; j += kShare) above += L.buf[j] > key ? 1 : 0;
+        if constexpr (kShare >= 2) above += dpp_u32<0xB1, 0xf>(above);
+        if constexpr (kShare >= 4) above += dpp_u32<0x4E, 0xf>(above);
         if (above < k) L.best[above] = key;
     }
     team_sync<T>();
@@ -335,65 +436,109 @@ __device__ inline void top_cut(TopLds<T, S>& L, int lane, uint32_t k) {
     team_sync<T>();
 }
 
-// Four elements of a vector: half of one of 16-bit elements.
+// The low bits that every value of a format, as an ordered integer, has alike.
 template <typename Fmt>
-__device__ inline void load4(const uint8_t* p, float (&e)[4]) {
-    if constexpr (Fmt::kSize == 4) {
-        F32::unpack(load16<F32>(p), e);
-    } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        e[0] = Fmt::from_bits(static_cast<uint16_t>(w.x));
-        e[1] = Fmt::from_bits(static_cast<uint16_t>(w.x >> 16));
-        e[2] = Fmt::from_bits(static_cast<uint16_t>(w.y));
-        e[3] = Fmt::from_bits(static_cast<uint16_t>(w.y >> 16));
+constexpr int kLowBits = std::is_same<Fmt, F32>::value ? 0 : std::is_same<Fmt, F16>::value ? 13 : 16;
+
+// Bisection for kth_bound over N maxima per lane: N comparisons a step, the counts from lane masks.
+template <int N>
+__device__ inline uint32_t bisect(const uint32_t (&o)[N], uint32_t k) {
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        hi = o[j] > hi ? o[j] : hi;
+        lo = o[j] != 0 && ~o[j] > lo ? ~o[j] : lo;
     }
+    hi = wave_max_u32(hi) + 1;
+    lo = ~wave_max_u32(lo);
+    const uint32_t enough = k + k / 8 + 2;
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        uint32_t n = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) n += __popcll(__ballot(o[j] >= mid));
+        if (n >= k) {
+            lo = mid;
+            if (n <= enough) break;
+        } else {
+            hi = mid;
+        }
+    }
+    return lo;
 }
 
-// segs maxima are in L.seg. `vec(seg, i)` names vector i (of per_seg) of a segment, or kNoVec.
+// A value that at least k, and if the values allow few more, of the `segs` maxima reach (the
+// lowest finite value if there are fewer than k). One wavefront computes it, from the maxima of
+// 64 N groups of segments: with k / (64 N) = 1/4 groups above it, about 11% more segments than
+// groups are. N = 4, or 1 for few alternatives; all 16 or 32 maxima of a lane in each step
+// measured 2.5 to 5.9 us here, a third of the time that the alternatives cost.
+template <typename Fmt, int S>
+__device__ inline float kth_bound(const float* seg, uint32_t segs, uint32_t k, int lane) {
+    constexpr int kPer = (S + kWave - 1) / kWave, N = kPer < 4 ? kPer : 4;
+    if (segs < k) return kLowest;
+    float m[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) m[j] = -__builtin_huge_valf();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const uint32_t s = lane + j * kWave;
+        if (s < segs) m[j % N] = max_f(m[j % N], seg[s]);
+    }
+    uint32_t o[N], bound;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        o[j] = lane + static_cast<uint32_t>(j) * kWave < segs ? order_of(m[j]) >> kLowBits<Fmt> : 0;
+    if (k <= kWave / 4) {
+        uint32_t top[1] = {o[0]};
+#pragma unroll
+        for (int j = 1; j < N; ++j) top[0] = o[j] > top[0] ? o[j] : top[0];
+        bound = bisect(top, k);
+    } else {
+        bound = bisect(o, k);
+    }
+    bound <<= kLowBits<Fmt>;  // below the lowest finite value: segments of masked elements alone
+    return bound > order_of(kLowest) ? value_of(bound) : kLowest;
+}
+
+// `segs` maxima are in L.seg. `vec(seg, i)` names vector i (of 2^lg_seg) of a segment, or kNoVec.
 // Leaves the k best (fewer if the row has fewer) in L.buf, their number in L.count.
 template <typename Fmt, int T, int S, typename VecOf>
 __device__ inline void top_select(TopLds<T, S>& L, const Span<Fmt>& sp, uint32_t segs,
-                                  uint32_t per_seg, uint32_t k, int lane, VecOf vec) {
-    constexpr uint32_t kParts = Fmt::VW / 4;  // 4-element parts of a vector
+                                  uint32_t lg_seg, uint32_t k, int lane, VecOf vec) {
+    constexpr int VW = Fmt::VW;
+    constexpr int U = 4;  // vectors a thread reads at once
     if (lane == 0) {
         L.count = 0;
         L.listed = 0;
         L.least = 0;
-        L.tau = kLowest;
     }
     team_sync<T>();
-    for (uint32_t s = lane; s < segs; s += T) {
-        const float m = L.seg[s];
-        uint32_t above = 0, reach = 0;
-        for (uint32_t j = 0; j < segs; ++j) {
-            const float o = L.seg[j];
-            above += o > m ? 1 : 0;
-            reach += o >= m ? 1 : 0;
-        }
-        if (above < k) {
-            L.list[atomicAdd(&L.listed, 1u)] = static_cast<uint16_t>(s);
-            if (reach >= k) L.tau = m;  // every segment that gets here holds the same value
-        }
+    if (lane < kWave) {
+        const float t = kth_bound<Fmt, S>(L.seg, segs, k, lane);
+        if (lane == 0) L.tau = t;
     }
     team_sync<T>();
     const float tau = L.tau;
-    const uint32_t main_items = L.listed * per_seg * kParts;
-    const uint32_t items = main_items + 2 * kParts;  // and the edges
-    const auto visit = [&](uint32_t it, uint64_t least, bool bounded) {
-        const uint32_t part = it % kParts;
-        uint32_t v;
-        if (it < main_items) {
-            const uint32_t u = it / kParts;
-            v = vec(L.list[u / per_seg], u % per_seg);
-        } else {
-            v = sp.edge(static_cast<int>((it - main_items) / kParts));
-        }
-        if (v == kNoVec) return;
-        float e[4];
-        load4<Fmt>(sp.at(v) + part * 4 * Fmt::kSize, e);
-        const uint32_t p0 = sp.pos(v) + part * 4;
+    for (uint32_t s = lane; s < segs; s += T)
+        if (L.seg[s] >= tau) L.list[atomicAdd(&L.listed, 1u)] = static_cast<uint16_t>(s);
+    team_sync<T>();
+    const uint32_t main_items = L.listed << lg_seg;
+    const uint32_t items = main_items + 2;  // and the edges
+    const auto item_vec = [&](uint32_t it) {
+        if (it < main_items) return vec(L.list[it >> lg_seg], it & ((1u << lg_seg) - 1));
+        return it < items ? sp.edge(static_cast<int>(it - main_items)) : kNoVec;
+    };
+    const auto visit = [&](const typename Fmt::Vec& q, uint32_t v, uint64_t least, bool bounded) {
+        float e[VW];
+        Fmt::unpack(q, e);
+        float m = e[0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 1; i + 1 < VW; i += 2) m = max3_f(m, e[i], e[i + 1]);
+        m = max_f(m, e[VW - 1]);
+        if (v == kNoVec || !(m >= tau)) return;
+        const uint32_t p0 = sp.pos(v);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
             if (e[i] >= tau && p0 + i < sp.cols) {
                 const uint64_t key = key_of(e[i], p0 + i);
                 if (key > least) {
@@ -403,17 +548,32 @@ __device__ inline void top_select(TopLds<T, S>& L, const Span<Fmt>& sp, uint32_t
             }
         }
     };
-    for (uint32_t it = lane; it < items; it += T) visit(it, 0, true);
+    for (uint32_t it = lane; it < items; it += U * T) {
+        typename Fmt::Vec q[U];
+        uint32_t v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            v[u] = item_vec(it + u * T);
+            q[u] = load16<Fmt>(sp.at(v[u] == kNoVec ? 0 : v[u]));  // vector 0 can always be read
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (it + u * T < items) visit(q[u], v[u], 0, true);
+    }
     team_sync<T>();
     if (L.count > TopLds<T, S>::kCap) {
+        constexpr uint32_t kStep = TopLds<T, S>::kStep;
         team_sync<T>();
         if (lane == 0) L.count = 0;
-        for (uint32_t base = 0; base < items; base += T) {
+        for (uint32_t base = 0; base < items; base += kStep) {
             team_sync<T>();
-            if (L.count > kTopMax) top_cut(L, lane, k);  // at most 4 T more keys fit
+            if (L.count > kTopMax) top_cut(L, lane, k);  // then 8 kStep more keys fit
             const uint64_t least = L.least;
             team_sync<T>();
-            if (base + lane < items) visit(base + lane, least, false);
+            if (static_cast<uint32_t>(lane) < kStep) {
+                const uint32_t v = item_vec(base + lane);
+                visit(load16<Fmt>(sp.at(v == kNoVec ? 0 : v)), v, least, false);
+            }
         }
         team_sync<T>();
     }
@@ -478,6 +638,7 @@ template <typename Fmt>
 __device__ inline float load_at(const uint8_t* row, int64_t t, uint32_t cols) {
     return t < static_cast<int64_t>(cols) ? Fmt::load1(row + t * Fmt::kSize) : __builtin_nanf("");
 }
+__device__ inline uint32_t ceil_log2(uint32_t v) { return v <= 1 ? 0 : 32 - __clz(v - 1); }
 template <typename Fmt>
 __device__ inline const uint8_t* row_ptr(const void* x, uint32_t r, uint32_t stride) {
     return static_cast<const uint8_t*>(x) + static_cast<size_t>(r) * stride * Fmt::kSize;
@@ -554,6 +715,10 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint3
     }
 }
 
+// Segments of a row with alternatives, at most.
+template <int T>
+constexpr int kSegs = T == kWave ? 256 : 1024;
+
 // A team of T lanes per row.
 template <typename Fmt, bool ENT, bool TOP, int T>
 __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32_t cols,
@@ -562,11 +727,9 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32
                                                            float* stats, uint64_t top_lp,
                                                            int64_t* top_tok) {
     constexpr int kTeams = kTeamsPerBlock<T>;
-    constexpr int kSegs = T < 256 ? T : 256;  // segments of a row: a lane's share, or a few lanes'
-    constexpr int kSub = T / kSegs;
     constexpr int U = 16 / Fmt::VW;
     __shared__ float sh[T / kWave][4];
-    __shared__ TopLds<TOP ? T : 1, TOP ? kSegs : 1> lds[TOP ? kTeams : 1];
+    __shared__ TopLds<TOP ? T : 64, TOP ? kSegs<T> : 1> lds[TOP ? kTeams : 1];
     const uint32_t team = threadIdx.x / T;
     const uint32_t r = blockIdx.x * kTeams + team;
     const int lane = threadIdx.x % T;
@@ -584,8 +747,9 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32
     const float xt = load_at<Fmt>(row, t, cols);
     const Span<Fmt> sp(row, cols);
     Stat a;
-    scan_span<Fmt, ENT, T, U>(sp, true, sp.va, sp.vb, lane, scale, a);
-    const float mine = a.m;
+    auto& L = lds[TOP ? team : 0];
+    const Segments g = Segments::cut<T, U>(sp.va, sp.vb, kSegs<T>);
+    scan_span<Fmt, ENT, T, U, TOP>(sp, true, sp.va, sp.vb, lane, scale, a, g, L.seg);
     team_merge<ENT, T>(a, scale, lane, sh);
     const RowOut o = row_out<ENT>(a, xt, scale);
     if (lane == 0) store_stats(stats, rows, r, o);
@@ -594,14 +758,8 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32
             top_none(k, lane, T, a.s == 0.0f ? -__builtin_huge_valf() : __builtin_nanf(""), lp, tok);
             return;
         }
-        auto& L = lds[team];
-        const float seg = lanes_max<kSub>(mine);
-        if (lane % kSub == 0) L.seg[lane / kSub] = seg;
-        const uint32_t per_lane = (sp.vb - sp.va + T - 1) / T;
-        top_select<Fmt, T, kSegs>(L, sp, kSegs, per_lane * kSub, k, lane, [&](uint32_t s, uint32_t i) {
-            const uint32_t v = sp.va + s * kSub + i % kSub + (i / kSub) * T;
-            return v < sp.vb ? v : kNoVec;
-        });
+        top_select<Fmt, T, kSegs<T>>(L, sp, g.count(), g.lg_vecs, k, lane,
+                                     [&](uint32_t s, uint32_t i) { return g.vec(s, i); });
         top_store(L, k, lane, a, scale, o.l2, lp, tok);
     }
 }
@@ -616,7 +774,7 @@ __device__ inline uint32_t span_max(uint32_t cols) {  // vectors of the worst al
 }
 struct Part {  // what a slice leaves in scratch
     float m, s, h, pad;
-    float wave_max[kPartThreads / kWave];
+    float oct_max[kPartThreads / 8];  // of every eight lanes
 };
 
 template <typename Fmt, bool ENT>
@@ -635,9 +793,9 @@ __global__ __launch_bounds__(kPartThreads) void k_part(const void* x, uint32_t c
     const int lane = threadIdx.x;
     Stat a;
     scan_span<Fmt, ENT, kPartThreads, kPartUnroll>(sp, b == 0, first, last, lane, scale, a);
-    const float wave_max = lanes_max<kWave>(a.m);
+    const float oct_max = lanes_max<8>(a.m);  // with the edges': a bound is all that is needed
     team_merge<ENT, kPartThreads>(a, scale, lane, sh);
-    if (lane % kWave == 0) out[blockIdx.x].wave_max[lane / kWave] = wave_max;
+    if (lane % 8 == 0) out[blockIdx.x].oct_max[lane / 8] = oct_max;
     if (lane == 0) {
         out[blockIdx.x].m = a.m;
         out[blockIdx.x].s = a.s;
@@ -646,14 +804,16 @@ __global__ __launch_bounds__(kPartThreads) void k_part(const void* x, uint32_t c
 }
 
 constexpr int kMergeThreads = 256;
+constexpr int kMergeTopThreads = 1024;  // with alternatives: vectors to read again in one step
+constexpr int kMergeSegs = 2048;
 
 // The merged statistics of a split row, in every thread.
-template <bool ENT>
+template <bool ENT, int T>
 __device__ inline Stat merge_parts(const Part* p, uint32_t parts, float scale, int lane,
                                    float (*sh)[4]) {
     Stat a;
     a.init();
-    for (uint32_t b = lane; b < parts; b += kMergeThreads) {
+    for (uint32_t b = lane; b < parts; b += T) {
         Stat o{p[b].m, p[b].s, ENT ? p[b].h : 0.0f};
         const float m = max_f(a.m, o.m);
         a.move<ENT>(m, scale);
@@ -661,20 +821,18 @@ __device__ inline Stat merge_parts(const Part* p, uint32_t parts, float scale, i
         a.s += o.s;
         a.h += o.h;
     }
-    team_merge<ENT, kMergeThreads>(a, scale, lane, sh);
+    team_merge<ENT, T>(a, scale, lane, sh);
     return a;
 }
 
 // One workgroup per split row. Tags: columns in (x, tokens), slices, alternatives, scale.
-template <typename Fmt, bool ENT, bool TOP>
-__global__ __launch_bounds__(kMergeThreads) void k_lp_merge(uint64_t x, uint64_t tokens,
+template <typename Fmt, bool ENT, bool TOP, int T = TOP ? kMergeTopThreads : kMergeThreads>
+__global__ __launch_bounds__(T) void k_lp_merge(uint64_t x, uint64_t tokens,
                                                             uint64_t part, uint64_t stats_,
                                                             uint64_t top_lp, uint64_t top_tok,
                                                             uint32_t stride, uint32_t rows) {
-    constexpr int kWaves = kPartThreads / kWave;
-    constexpr int kSegs = kMaxParts * kWaves;
-    __shared__ float sh[kMergeThreads / kWave][4];
-    __shared__ TopLds<TOP ? kMergeThreads : 1, TOP ? kSegs : 1> L;
+    __shared__ float sh[T / kWave][4];
+    __shared__ TopLds<TOP ? T : 64, TOP ? kMergeSegs : 1> L;
     const uint32_t cols = tags(x, tokens);
     const uint32_t parts = tag(part), k = tag(stats_);
     const float scale = __uint_as_float(tags(top_lp, top_tok));
@@ -686,30 +844,37 @@ __global__ __launch_bounds__(kMergeThreads) void k_lp_merge(uint64_t x, uint64_t
     int64_t* tok = addr<int64_t>(top_tok) + static_cast<size_t>(r) * k;
     if (t < 0) {
         if (lane == 0) store_stats(stats, rows, r, row_left_out<ENT>());
-        if constexpr (TOP) top_none(k, lane, kMergeThreads, -__builtin_huge_valf(), lp, tok);
+        if constexpr (TOP) top_none(k, lane, T, -__builtin_huge_valf(), lp, tok);
         return;
     }
     const uint8_t* row = row_ptr<Fmt>(addr<const void>(x), r, stride);
     const float xt = load_at<Fmt>(row, t, cols);
     const Part* p = addr<const Part>(part) + static_cast<size_t>(r) * parts;
-    const Stat a = merge_parts<ENT>(p, parts, scale, lane, sh);
+    const Stat a = merge_parts<ENT, T>(p, parts, scale, lane, sh);
     const RowOut o = row_out<ENT>(a, xt, scale);
     if (lane == 0) store_stats(stats, rows, r, o);
     if constexpr (TOP) {
         if (!(a.s > 0.0f)) {
-            top_none(k, lane, kMergeThreads, a.s == 0.0f ? -__builtin_huge_valf() : __builtin_nanf(""),
-                     lp, tok);
+            top_none(k, lane, T, a.s == 0.0f ? -__builtin_huge_valf() : __builtin_nanf(""), lp, tok);
             return;
         }
-        for (uint32_t s = lane; s < parts * kWaves; s += kMergeThreads)
-            L.seg[s] = p[s / kWaves].wave_max[s % kWaves];
+        // a slice's 32 maxima as they are, or two, four, ... together so that kMergeSegs hold them
+        constexpr uint32_t kOct = kPartThreads / 8;
+        const uint32_t lg = ceil_log2((parts * kOct + kMergeSegs - 1) / kMergeSegs);
+        const uint32_t per = kOct >> lg, segs = parts * per, lanes = 8u << lg;
+        for (uint32_t s = lane; s < segs; s += T) {
+            const float* o = p[s / per].oct_max + (s % per << lg);
+            float m = o[0];
+            for (uint32_t i = 1; i < 1u << lg; ++i) m = max_f(m, o[i]);
+            L.seg[s] = m;
+        }
         const Span<Fmt> sp(row, cols);
         const uint32_t n = part_vecs(span_max<Fmt>(cols), parts);
         const uint32_t steps = (n + kPartThreads - 1) / kPartThreads;
-        top_select<Fmt, kMergeThreads, kSegs>(
-            L, sp, parts * kWaves, steps * kWave, k, lane, [&](uint32_t s, uint32_t i) {
-                const uint32_t in = (i / kWave) * kPartThreads + (s % kWaves) * kWave + i % kWave;
-                const uint32_t v = sp.va + (s / kWaves) * n + in;
+        top_select<Fmt, T, kMergeSegs>(
+            L, sp, segs, ceil_log2(steps * lanes), k, lane, [&](uint32_t s, uint32_t i) {
+                const uint32_t in = i / lanes * kPartThreads + s % per * lanes + i % lanes;
+                const uint32_t v = sp.va + s / per * n + in;
                 return in < n && v < sp.vb ? v : kNoVec;
             });
         top_store(L, k, lane, a, scale, o.l2, lp, tok);
@@ -832,7 +997,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_grad(uint64_t x, uint64_t 
     gs.write(lane, 1 << lg, zero, [&](const float (&e)[VW], uint32_t p0, float (&d)[VW]) {
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
-            const float z = (e[i] - m) * scale - l2;
+            const float z = fmaf(e[i] - m, scale, -l2);
             const float p = exp2_f(z);
             d[i] = ENT ? -p * fmaf(b, max_f(z, kZFloor) + h2, a) : -p * a;
         }
@@ -851,7 +1016,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_grad(uint64_t x, uint64_t 
 
 struct Teacher {
     float m, l2;
-    __device__ float weight(float v, float scale) const { return exp2_f((v - m) * scale - l2); }
+    __device__ float weight(float v, float scale) const { return exp2_f(fmaf(v - m, scale, -l2)); }
 };
 __device__ inline float teacher_value(const int64_t* ids, const float* values, uint32_t i) {
     return ids[i] >= 0 ? values[i] : -__builtin_huge_valf();
@@ -897,13 +1062,13 @@ __device__ inline float distill_loss(const uint8_t* row, uint32_t cols, const in
     for (uint32_t i = lane; i < k; i += T) {
         const int64_t id = ids[i];
         if (id < 0) continue;
-        const float lq = (values[i] - q.m) * scale - q.l2;
+        const float lq = fmaf(values[i] - q.m, scale, -q.l2);
         const float w = exp2_f(lq);
         if (w == 0.0f) continue;
         const float xi = load_at<Fmt>(row, id, cols);
         if (id >= static_cast<int64_t>(cols) || w != w) bad = 1.0f;
         const float lp = a.s == 0.0f ? -__builtin_huge_valf() : ln_p(xi, a.m, *l2, scale);
-        sum = fmaf(w, lq * kLn2 - lp, sum);
+        sum = fmaf(w, fmaf(lq, kLn2, -lp), sum);
     }
     sum = team_reduce<T, false>(sum, lane, sh);
     bad = team_reduce<T, true>(bad, lane, sh);
@@ -922,7 +1087,7 @@ __device__ inline void distill_grad_slice(const GradSlice<Fmt>& gs, const int64_
     constexpr int VW = Fmt::VW;
     gs.write(lane, team, zero, [&](const float (&e)[VW], uint32_t, float (&d)[VW]) {
 #pragma unroll
-        for (int i = 0; i < VW; ++i) d[i] = coef * exp2_f((e[i] - m) * scale - l2);
+        for (int i = 0; i < VW; ++i) d[i] = coef * exp2_f(fmaf(e[i] - m, scale, -l2));
     });
     team_sync<T>();
     if (zero) return;
@@ -932,7 +1097,7 @@ __device__ inline void distill_grad_slice(const GradSlice<Fmt>& gs, const int64_
         float w = 0.0f;
         for (uint32_t j = 0; j < k; ++j)
             if (ids[j] == id) w += q.weight(values[j], scale);
-        const float p = exp2_f((Fmt::load1(gs.x + id * Fmt::kSize) - m) * scale - l2);
+        const float p = exp2_f(fmaf(Fmt::load1(gs.x + id * Fmt::kSize) - m, scale, -l2));
         reinterpret_cast<typename Fmt::Bits*>(gs.g)[id] = round_to<Fmt>(coef * (p - w));
     }
 }
@@ -984,7 +1149,7 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
     }
-    const Stat a = merge_parts<false>(part + static_cast<size_t>(r) * parts, parts, scale, lane, sh);
+    const Stat a = merge_parts<false, T>(part + static_cast<size_t>(r) * parts, parts, scale, lane, sh);
     float l2;
     const float loss = distill_loss<Fmt, T>(row_ptr<Fmt>(x, r, stride), cols, ids, values, k, scale, q,
                                             a, &l2, lane, sh);
@@ -1073,7 +1238,7 @@ void with_team(int team, F f) {
     switch (team) {
         case 64: f(Int<64>{}); break;
         case 256: f(Int<256>{}); break;
-        default: f(Int<1024>{}); break;
+        default: f(Int<512>{}); break;
     }
 }
 template <typename F>
@@ -1129,7 +1294,7 @@ hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const in
                     launch(k_part<Fmt, ENT>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
                            static_cast<uint32_t>(plan.parts), tokens, part);
                     const uint32_t sc = bits_of(a.scale);
-                    launch(k_lp_merge<Fmt, ENT, TOP>, rows, kMergeThreads, s, tagged(a.x, cols),
+                    launch(k_lp_merge<Fmt, ENT, TOP>, rows, TOP ? kMergeTopThreads : kMergeThreads, s, tagged(a.x, cols),
                            tagged(tokens, cols >> 16), tagged(part, plan.parts), tagged(stats, top),
                            tagged(top_logprobs, sc), tagged(top_tokens, sc >> 16), stride, rows);
                     return;

@@ -109,7 +109,7 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, bool groups, bool ve
         return ARGREDUCE_OK;
     }
     p->path = ARGREDUCE_PATH_BLOCK;
-    p->team = vecs > 4096 ? 1024 : 256;
+    p->team = vecs > 4096 ? 512 : 256;
     p->grid_blocks = rows1;
     if (rows1 * p->team >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
     return ARGREDUCE_OK;
