@@ -42,9 +42,11 @@ constexpr uint32_t kNoVec = 0xffffffffu;
 // 16-bit values in the unused upper bits of 48-bit device addresses.
 
 constexpr int kAddrBits = 48;
+// (Through a pointer to global memory, so that the accesses are global ones, not flat ones.)
 template <typename T>
 __device__ inline T* addr(uint64_t a) {
-    return reinterpret_cast<T*>(a & ((uint64_t{1} << kAddrBits) - 1));
+    typedef __attribute__((address_space(1))) uint8_t Global;
+    return (T*)(Global*)(a & ((uint64_t{1} << kAddrBits) - 1));
 }
 __device__ inline uint32_t tag(uint64_t a) { return static_cast<uint32_t>(a >> kAddrBits); }
 __device__ inline uint32_t tags(uint64_t lo, uint64_t hi) { return tag(lo) | (tag(hi) << 16); }
@@ -208,10 +210,32 @@ struct Span {
     __device__ uint32_t pos(uint32_t v) const { return v * Fmt::VW - off; }
 };
 
+// Nontemporal: [2048,128256] bf16 took 94-96 us with ordinary loads, 86 with these (T = 512).
 template <typename Fmt>
 __device__ inline typename Fmt::Vec load16(const uint8_t* p) {
-    return *reinterpret_cast<const typename Fmt::Vec*>(p);
+    return __builtin_nontemporal_load(reinterpret_cast<const typename Fmt::Vec*>(p));
 }
+
+// A vector of -inf.
+template <typename Fmt>
+__device__ inline typename Fmt::Vec masked16() {
+    constexpr uint32_t w = std::is_same<Fmt, F32>::value   ? 0xff800000u
+                           : std::is_same<Fmt, F16>::value ? 0xfc00fc00u
+                                                           : 0xff80ff80u;
+    return __builtin_bit_cast(typename Fmt::Vec, u32x4{w, w, w, w});
+}
+template <typename Fmt>
+__device__ inline typename Fmt::Vec masked_unless(bool in, const typename Fmt::Vec& v) {
+    const u32x4 a = __builtin_bit_cast(u32x4, v), b = __builtin_bit_cast(u32x4, masked16<Fmt>());
+    return __builtin_bit_cast(typename Fmt::Vec,
+                              u32x4{in ? a.x : b.x, in ? a.y : b.y, in ? a.z : b.z, in ? a.w : b.w});
+}
+
+// Vectors a lane reads per step of a scan: four, or 16 elements where the alternatives' segments
+// take registers too ([2048,128256] bf16, T = 512, four and two vectors: 87 and 93 us without
+// alternatives, 107 and 98 with 64 of them).
+template <typename Fmt, bool TOP>
+constexpr int kUnroll = TOP ? 16 / Fmt::VW : 4;
 
 // Takes N (even) elements into the running part; returns the larger of `m` and their maximum.
 template <bool ENT, int N>
@@ -229,26 +253,21 @@ __device__ inline float take(const float (&e)[N], float k, Stat& a, float m = kL
     return m;
 }
 
-// Loads vectors v, v + T, ... (U of them) as floats; those at or past `last` as -inf.
-template <typename Fmt, int T, int U>
-__device__ inline void load_step(const Span<Fmt>& sp, uint32_t v, uint32_t last, bool full,
+// Loads vectors v, v + T, ... (U of them) as floats; unless FULL, those at or past `last` as -inf.
+template <typename Fmt, int T, int U, bool FULL>
+__device__ inline void load_step(const Span<Fmt>& sp, uint32_t v, uint32_t last,
                                  float (&e)[U * Fmt::VW]) {
     constexpr int VW = Fmt::VW;
     typename Fmt::Vec q[U];
-    if (full) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = load16<Fmt>(sp.at(v + u * T));
-    } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = load16<Fmt>(sp.at(v + u * T < last ? v + u * T : last - 1));
-    }
+    for (int u = 0; u < U; ++u) q[u] = load16<Fmt>(sp.at(FULL || v + u * T < last ? v + u * T : last - 1));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        if constexpr (!FULL) q[u] = masked_unless<Fmt>(v + u * T < last, q[u]);
         float f[VW];
         Fmt::unpack(q[u], f);
-        const bool in = full || v + u * T < last;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) e[u * VW + i] = in ? f[i] : -__builtin_huge_valf();
+        for (int i = 0; i < VW; ++i) e[u * VW + i] = f[i];
     }
 }
 
@@ -302,21 +321,16 @@ struct Segments {
     }
 };
 
-// One lane's share of a row: its edge vector, then vectors first + lane, + T, ... below last in
-// steps of U, the last step filled up with -inf. With SEG the maxima of g's segments go to seg[].
+// One lane's share of a row: its edge vector (scan_span), then vectors first + lane, + T, ... below
+// last in steps of U, the last step filled up with -inf. With SEG the maxima of g's segments go to
+// seg[].
 template <typename Fmt, bool ENT, int T, int U, bool SEG = false>
-__device__ inline void scan_span(const Span<Fmt>& sp, bool edges, uint32_t first, uint32_t last,
-                                 int lane, float k, Stat& a, const Segments& g = Segments{},
-                                 float* seg = nullptr) {
+__device__ inline void scan_on(const Span<Fmt>& sp, uint32_t first, uint32_t last, int lane, float k,
+                               Stat& a, const Segments& g = Segments{}, float* seg = nullptr) {
     constexpr int VW = Fmt::VW;
-    a.init();
-    if (edges && lane < 2) scan_edge<Fmt, ENT>(sp, lane, k, a);
     float m = kLowest;
     uint32_t left = g.group, at = lane / 8;
-    for (uint32_t base = first; base < last; base += U * T) {
-        float e[U * VW];
-        const bool full = last - base >= U * T;
-        load_step<Fmt, T, U>(sp, base + lane, last, full, e);
+    const auto step = [&](const float (&e)[U * VW], uint32_t base) {
         if constexpr (SEG) {
             if (g.group == 0) {
 #pragma unroll
@@ -344,12 +358,30 @@ __device__ inline void scan_span(const Span<Fmt>& sp, bool edges, uint32_t first
         } else {
             take<ENT>(e, k, a);
         }
+    };
+    const uint32_t whole = first + (last - first) / (U * T) * (U * T);
+    float e[U * VW];
+    for (uint32_t base = first; base < whole; base += U * T) {
+        load_step<Fmt, T, U, true>(sp, base + lane, last, e);
+        step(e, base);
+    }
+    if (whole < last) {
+        load_step<Fmt, T, U, false>(sp, whole + lane, last, e);
+        step(e, whole);
     }
     if constexpr (SEG)
         if (left != g.group) {
             m = lanes_max<8>(m);
             if (lane % 8 == 0) seg[at] = m;
         }
+}
+template <typename Fmt, bool ENT, int T, int U, bool SEG = false>
+__device__ inline void scan_span(const Span<Fmt>& sp, bool edges, uint32_t first, uint32_t last,
+                                 int lane, float k, Stat& a, const Segments& g = Segments{},
+                                 float* seg = nullptr) {
+    a.init();
+    if (edges && lane < 2) scan_edge<Fmt, ENT>(sp, lane, k, a);
+    scan_on<Fmt, ENT, T, U, SEG>(sp, first, last, lane, k, a, g, seg);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -727,7 +759,7 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32
                                                            float* stats, uint64_t top_lp,
                                                            int64_t* top_tok) {
     constexpr int kTeams = kTeamsPerBlock<T>;
-    constexpr int U = 16 / Fmt::VW;
+    constexpr int U = kUnroll<Fmt, TOP>;
     __shared__ float sh[T / kWave][4];
     __shared__ TopLds<TOP ? T : 64, TOP ? kSegs<T> : 1> lds[TOP ? kTeams : 1];
     const uint32_t team = threadIdx.x / T;
@@ -896,13 +928,21 @@ __device__ inline typename Fmt::Vec load16_any(const uint8_t* p) {
     return reinterpret_cast<const Unaligned<Fmt>*>(p)->v;
 }
 
-// Rounds to nearest even.
+template <typename Fmt>
+__device__ inline void store16_any(uint8_t* p, const typename Fmt::Vec& v) {
+    reinterpret_cast<Unaligned<Fmt>*>(p)->v = v;
+}
+
+// Rounds to nearest even. binary16 by the instruction: the compiler may join the conversion with
+// the product before it, in one kernel and not in another.
 template <typename Fmt>
 __device__ inline typename Fmt::Bits round_to(float v) {
     if constexpr (Fmt::kSize == 4) {
         return __float_as_uint(v);
     } else if constexpr (std::is_same<Fmt, F16>::value) {
-        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+        uint32_t h;
+        asm("v_cvt_f16_f32 %0, %1" : "=v"(h) : "v"(v));
+        return static_cast<uint16_t>(h);
     } else {
         return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
     }
@@ -1018,27 +1058,84 @@ struct Teacher {
     float m, l2;
     __device__ float weight(float v, float scale) const { return exp2_f(fmaf(v - m, scale, -l2)); }
 };
-__device__ inline float teacher_value(const int64_t* ids, const float* values, uint32_t i) {
-    return ids[i] >= 0 ? values[i] : -__builtin_huge_valf();
-}
-template <int T>
-__device__ inline Teacher teacher_row(const int64_t* ids, const float* values, uint32_t k, float scale,
-                                      int lane, float (*sh)[4]) {
+// An entry of the teacher's row in LDS: id (-1: absent, cols: beyond the row), value (-inf if
+// absent), the student's logit there, and the weight of all entries with this id. Entry i belongs
+// to the lanes i mod T; only id and v are read by others.
+struct Entry {
+    int32_t id;
+    float v, x, w;
+};
+extern __shared__ Entry s_entries[];
+
+// The teacher's row: its entries into `ent`, the normaliser to every thread. *bad: the whole
+// gradient is NaN (a weight is NaN, or an id with weight lies beyond the row). Up to 64 entries
+// every wavefront finds the normaliser for itself, without a barrier.
+template <typename Fmt, int T>
+__device__ inline Teacher teacher_row(Entry* ent, const uint8_t* row, uint32_t cols, const int64_t* ids,
+                                      const float* values, uint32_t k, float scale, int lane,
+                                      float (*sh)[4], bool* bad) {
+    const auto get = [&](uint32_t i, float* v) {
+        const int64_t id = ids[i];
+        *v = id >= 0 ? values[i] : -__builtin_huge_valf();
+        return id < 0 ? -1 : static_cast<int32_t>(id < static_cast<int64_t>(cols) ? id : cols);
+    };
     float m = -__builtin_huge_valf(), s = 0.0f;
-    bool bad = false;
-    for (uint32_t i = lane; i < k; i += T) {
-        const float v = teacher_value(ids, values, i);
-        m = max_f(m, v);
-        bad |= v != v;
+    Teacher q;
+    if (k <= kWave) {
+        const uint32_t i = lane % kWave;
+        int32_t id = -1;
+        float v = -__builtin_huge_valf();
+        if (i < k) id = get(i, &v);
+        float x = __builtin_nanf("");
+        if (static_cast<uint32_t>(lane) < k && id >= 0 && static_cast<uint32_t>(id) < cols)
+            x = Fmt::load1(row + static_cast<size_t>(id) * Fmt::kSize);
+        m = lanes_max<kWave>(v);
+        if (m > -__builtin_huge_valf()) s = exp2_f((v - m) * scale);
+        if (v != v) s = v;
+        s = lanes_sum<kWave>(s);
+        q = {s == s ? m : __builtin_nanf(""), log2_f(s)};
+        *bad = __any(s != s || (id == static_cast<int32_t>(cols) && q.weight(v, scale) != 0.0f));
+        if (static_cast<uint32_t>(lane) < k) ent[lane] = {id, v, x, 0.0f};
+        team_sync<kWave>();
+    } else {
+        bool nan = false, beyond = false;
+        for (uint32_t i = lane; i < k; i += T) {
+            float v;
+            const int32_t id = get(i, &v);
+            ent[i].id = id;
+            ent[i].v = v;
+            m = max_f(m, v);
+            nan |= v != v;
+        }
+        m = team_reduce<T, true>(m, lane, sh);
+        if (m > -__builtin_huge_valf())
+            for (uint32_t i = lane; i < k; i += T) s += exp2_f((ent[i].v - m) * scale);
+        if (nan) s = __builtin_nanf("");
+        s = team_reduce<T, false>(s, lane, sh);  // also makes the entries visible
+        q = {s == s ? m : __builtin_nanf(""), log2_f(s)};
+        for (uint32_t i = lane; i < k; i += T) {
+            const int32_t id = ent[i].id;
+            beyond |= id == static_cast<int32_t>(cols) && q.weight(ent[i].v, scale) != 0.0f;
+            ent[i].x = id >= 0 && static_cast<uint32_t>(id) < cols
+                           ? Fmt::load1(row + static_cast<size_t>(id) * Fmt::kSize)
+                           : __builtin_nanf("");
+        }
+        *bad = s != s || team_reduce<T, true>(beyond ? 1.0f : 0.0f, lane, sh) > 0.0f;
     }
-    m = team_reduce<T, true>(m, lane, sh);
-    if (m > -__builtin_huge_valf())
-        for (uint32_t i = lane; i < k; i += T)
-            s += exp2_f((teacher_value(ids, values, i) - m) * scale);
-    else if (bad)
-        s = __builtin_nanf("");
-    s = team_reduce<T, false>(s, lane, sh);
-    return {s == s ? m : __builtin_nanf(""), log2_f(s)};
+    return q;
+}
+
+// The weight of each entry's id: the sum over the entries with that id, in their order.
+template <int T>
+__device__ inline void teacher_weights(Entry* ent, uint32_t k, float scale, const Teacher& q, int lane) {
+    for (uint32_t i = lane; i < k; i += T) {
+        const int32_t id = ent[i].id;
+        float w = 0.0f;
+#pragma unroll 8
+        for (uint32_t j = 0; j < k; ++j)
+            if (ent[j].id == id) w += q.weight(ent[j].v, scale);
+        ent[i].w = w;
+    }
 }
 
 __device__ inline void store_distill(float* stats, uint32_t rows, uint32_t r, float loss, float m,
@@ -1051,54 +1148,38 @@ __device__ inline void store_distill(float* stats, uint32_t rows, uint32_t r, fl
     stats[4 * n + r] = q.l2;
 }
 
-// The loss of a row from its merged statistics; *l2 becomes NaN when an id with weight lies
-// beyond the row or a weight is NaN, so that the whole gradient is NaN too.
-template <typename Fmt, int T>
-__device__ inline float distill_loss(const uint8_t* row, uint32_t cols, const int64_t* ids,
-                                     const float* values, uint32_t k, float scale, const Teacher& q,
-                                     const Stat& a, float* l2, int lane, float (*sh)[4]) {
-    *l2 = log2_f(a.s);
-    float sum = 0.0f, bad = 0.0f;
+// The loss of a row from its merged statistics (in lane 0 of the team) and log2 of the sum.
+template <int T>
+__device__ inline float distill_loss(const Entry* ent, uint32_t k, float scale, const Teacher& q,
+                                     const Stat& a, float l2, int lane, float (*sh)[4]) {
+    float sum = 0.0f;
     for (uint32_t i = lane; i < k; i += T) {
-        const int64_t id = ids[i];
-        if (id < 0) continue;
-        const float lq = fmaf(values[i] - q.m, scale, -q.l2);
+        const float lq = fmaf(ent[i].v - q.m, scale, -q.l2);
         const float w = exp2_f(lq);
-        if (w == 0.0f) continue;
-        const float xi = load_at<Fmt>(row, id, cols);
-        if (id >= static_cast<int64_t>(cols) || w != w) bad = 1.0f;
-        const float lp = a.s == 0.0f ? -__builtin_huge_valf() : ln_p(xi, a.m, *l2, scale);
+        if (ent[i].id < 0 || w == 0.0f) continue;
+        const float lp = a.s == 0.0f ? -__builtin_huge_valf() : ln_p(ent[i].x, a.m, l2, scale);
         sum = fmaf(w, fmaf(lq, kLn2, -lp), sum);
     }
-    sum = team_reduce<T, false>(sum, lane, sh);
-    bad = team_reduce<T, true>(bad, lane, sh);
-    if (bad > 0.0f) *l2 = __builtin_nanf("");
-    return sum;
+    return k <= kWave ? lanes_sum<kWave>(sum) : team_reduce<T, false>(sum, lane, sh);
 }
 
-// Gradient of a row's slice: g (p_j - q_j) / T. The dense part g p_j / T is stored first; after
-// it each teacher entry's element is stored again with its weight taken off (the sum of the
-// weights of equal ids, which every one of them computes in the same order).
-template <typename Fmt, int T>
-__device__ inline void distill_grad_slice(const GradSlice<Fmt>& gs, const int64_t* ids,
-                                          const float* values, uint32_t k, float scale, float coef,
-                                          float m, float l2, const Teacher& q, bool zero, int lane,
-                                          int team) {
-    constexpr int VW = Fmt::VW;
-    gs.write(lane, team, zero, [&](const float (&e)[VW], uint32_t, float (&d)[VW]) {
-#pragma unroll
-        for (int i = 0; i < VW; ++i) d[i] = coef * exp2_f(fmaf(e[i] - m, scale, -l2));
-    });
-    team_sync<T>();
-    if (zero) return;
+// The gradient of a row is g (p_j - q_j) / T. The dense part g p_j / T is stored first; after it
+// (and a barrier) each teacher entry's element is stored again with its weight taken off: the sum
+// of the weights of equal ids, which every one of them computes in the same order.
+template <typename Fmt, typename Holds>
+__device__ inline void distill_take_off(const uint8_t* x, uint8_t* g, uint32_t cols, const int64_t* ids,
+                                        const float* values, uint32_t k, float scale, float coef,
+                                        float m, float l2, const Teacher& q, int lane, int team,
+                                        Holds holds) {
     for (uint32_t i = lane; i < k; i += team) {
         const int64_t id = ids[i];
-        if (id < 0 || id >= static_cast<int64_t>(gs.sp.cols) || !gs.holds(id)) continue;
+        if (id < 0 || id >= static_cast<int64_t>(cols) || !holds(id)) continue;
         float w = 0.0f;
+#pragma unroll 8
         for (uint32_t j = 0; j < k; ++j)
             if (ids[j] == id) w += q.weight(values[j], scale);
-        const float p = exp2_f(fmaf(Fmt::load1(gs.x + id * Fmt::kSize) - m, scale, -l2));
-        reinterpret_cast<typename Fmt::Bits*>(gs.g)[id] = round_to<Fmt>(coef * (p - w));
+        const float p = exp2_f(fmaf(Fmt::load1(x + id * Fmt::kSize) - m, scale, -l2));
+        reinterpret_cast<typename Fmt::Bits*>(g)[id] = round_to<Fmt>(coef * (p - w));
     }
 }
 
@@ -1108,25 +1189,26 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32
                                                            uint32_t rows, uint32_t k,
                                                            const int64_t* ids_, const float* values_,
                                                            float* stats) {
-    constexpr int U = 16 / Fmt::VW;
     __shared__ float sh[T / kWave][4];
     const uint32_t r = blockIdx.x * kTeamsPerBlock<T> + threadIdx.x / T;
     const int lane = threadIdx.x % T;
     if (r >= rows) return;
     const int64_t* ids = ids_ + static_cast<size_t>(r) * k;
     const float* values = values_ + static_cast<size_t>(r) * k;
-    const Teacher q = teacher_row<T>(ids, values, k, scale, lane, sh);
+    const uint8_t* row = row_ptr<Fmt>(x, r, stride);
+    Entry* ent = s_entries + threadIdx.x / T * k;
+    bool bad;
+    const Teacher q = teacher_row<Fmt, T>(ent, row, cols, ids, values, k, scale, lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
     }
-    const uint8_t* row = row_ptr<Fmt>(x, r, stride);
     const Span<Fmt> sp(row, cols);
     Stat a;
-    scan_span<Fmt, false, T, U>(sp, true, sp.va, sp.vb, lane, scale, a);
+    scan_span<Fmt, false, T, kUnroll<Fmt, false>>(sp, true, sp.va, sp.vb, lane, scale, a);
     team_merge<false, T>(a, scale, lane, sh);
-    float l2;
-    const float loss = distill_loss<Fmt, T>(row, cols, ids, values, k, scale, q, a, &l2, lane, sh);
+    const float l2 = bad ? __builtin_nanf("") : log2_f(a.s);
+    const float loss = distill_loss<T>(ent, k, scale, q, a, l2, lane, sh);
     if (lane == 0) store_distill(stats, rows, r, loss, a.m, l2, q);
 }
 
@@ -1144,15 +1226,16 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
     const int lane = threadIdx.x;
     const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
     const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
-    const Teacher q = teacher_row<T>(ids, values, k, scale, lane, sh);
+    bool bad;
+    const Teacher q = teacher_row<Fmt, T>(s_entries, row_ptr<Fmt>(x, r, stride), cols, ids, values, k,
+                                          scale, lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
     }
     const Stat a = merge_parts<false, T>(part + static_cast<size_t>(r) * parts, parts, scale, lane, sh);
-    float l2;
-    const float loss = distill_loss<Fmt, T>(row_ptr<Fmt>(x, r, stride), cols, ids, values, k, scale, q,
-                                            a, &l2, lane, sh);
+    const float l2 = bad ? __builtin_nanf("") : log2_f(a.s);
+    const float loss = distill_loss<T>(s_entries, k, scale, q, a, l2, lane, sh);
     if (lane == 0) store_distill(stats, rows, r, loss, a.m, l2, q);
 }
 
@@ -1180,42 +1263,134 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t 
                       unit - want * slices, slices);
     if (extra) gs.first = gs.last = 0;
     const bool zero = q.m == -__builtin_huge_valf() || l2 == -__builtin_huge_valf();
-    distill_grad_slice<Fmt, kBlockThreads>(gs, addr<const int64_t>(ids_) + static_cast<size_t>(r) * k,
-                                           addr<const float>(values_) + static_cast<size_t>(r) * k, k,
-                                           scale, coef, m, l2, q, zero, lane, 1 << lg);
-}
-
-// Loss and gradient of a row in one kernel: the second reading of the logits comes from the
-// caches. Tags as for k_ds_grad (none in grad).
-template <typename Fmt, int T>
-__global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t ids_, uint64_t values_,
-                                                           uint64_t stats_, uint64_t w, uint64_t grad,
-                                                           uint32_t stride, uint32_t rows) {
-    constexpr int U = 16 / Fmt::VW;
-    __shared__ float sh[T / kWave][4];
-    const uint32_t cols = tags(x, ids_), k = tag(values_);
-    const float scale = __uint_as_float(tags(stats_, w));
-    const uint32_t r = blockIdx.x * kTeamsPerBlock<T> + threadIdx.x / T;
-    const int lane = threadIdx.x % T;
-    if (r >= rows) return;
     const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
     const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
-    const uint8_t* row = row_ptr<Fmt>(addr<const void>(x), r, stride);
-    const GradSlice<Fmt> gs(row, const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad), r, cols)), cols, 0, 1);
-    const Teacher q = teacher_row<T>(ids, values, k, scale, lane, sh);
-    float loss = 0.0f, l2 = 0.0f;
-    Stat a{0.0f, 0.0f, 0.0f};
-    const bool absent = q.m == -__builtin_huge_valf();
-    if (!absent) {
-        const Span<Fmt> sp(row, cols);
-        scan_span<Fmt, false, T, U>(sp, true, sp.va, sp.vb, lane, scale, a);
-        team_merge<false, T>(a, scale, lane, sh);
-        loss = distill_loss<Fmt, T>(row, cols, ids, values, k, scale, q, a, &l2, lane, sh);
+    constexpr int VW = Fmt::VW;
+    gs.write(lane, 1 << lg, zero, [&](const float (&e)[VW], uint32_t, float (&d)[VW]) {
+#pragma unroll
+        for (int i = 0; i < VW; ++i) d[i] = coef * exp2_f(fmaf(e[i] - m, scale, -l2));
+    });
+    __syncthreads();
+    if (!zero)
+        distill_take_off<Fmt>(gs.x, gs.g, cols, ids, values, k, scale, coef, m, l2, q, lane, 1 << lg,
+                              [&](int64_t id) { return gs.holds(id); });
+}
+
+// Loss and gradient of a row in one kernel. A lane keeps its first NV vectors in registers from
+// the pass that takes the maximum and the sum to the pass that writes the gradient, so that the
+// logits are read from memory once; vectors beyond them are read again, mostly from the caches.
+// The registers of a CU hold few rows, so a team goes through several, and as soon as a vector's
+// gradient is stored, the vector of the team's next row is loaded in its place: the loads run
+// beside the second pass's arithmetic and stores. [4096,128256] bf16: 535 us when all vectors were
+// read again, 597 held without that overlap. Tags as for k_ds_grad, but the workgroups of the grid
+// in grad.
+template <typename Fmt, int T, int NV>
+__global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t ids_, uint64_t values_,
+                                                           uint64_t stats_, uint64_t w, uint64_t grad_,
+                                                           uint32_t stride, uint32_t rows) {
+    constexpr int VW = Fmt::VW, U = kUnroll<Fmt, false>;
+    static_assert(NV % U == 0, "whole steps");
+    __shared__ float sh[T / kWave][4];
+    const uint32_t cols = tags(x, ids_), k = tag(values_), teams = tag(grad_) * kTeamsPerBlock<T>;
+    const float scale = __uint_as_float(tags(stats_, w));
+    const int lane = threadIdx.x % T;
+    uint32_t r = blockIdx.x * kTeamsPerBlock<T> + threadIdx.x / T;
+    if (r >= rows) return;
+    Entry* ent = s_entries + threadIdx.x / T * k;
+    const auto row_at = [&](uint32_t n) { return row_ptr<Fmt>(addr<const void>(x), n, stride); };
+    typename Fmt::Vec held[NV];
+    const auto load = [&](const Span<Fmt>& sp, int i) {
+        const uint32_t v = sp.va + lane + i * T;
+        held[i] = load16<Fmt>(sp.at(v < sp.vb ? v : sp.vs - 1));  // of any row a readable vector
+    };
+    {
+        const Span<Fmt> sp(row_at(r), cols);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) load(sp, i);
     }
-    if (lane == 0) store_distill(addr<float>(stats_), rows, r, loss, a.m, l2, q);
-    const float coef = addr<const float>(w)[r] * scale * kLn2;
-    distill_grad_slice<Fmt, T>(gs, ids, values, k, scale, coef, a.m, l2, q,
-                               absent || l2 == -__builtin_huge_valf(), lane, T);
+    while (true) {
+        const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
+        const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
+        const uint8_t* row = row_at(r);
+        uint8_t* out = const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad_), r, cols));
+        const Span<Fmt> sp(row, cols);
+        bool bad;
+        const Teacher q = teacher_row<Fmt, T>(ent, row, cols, ids, values, k, scale, lane, sh, &bad);
+        const bool absent = q.m == -__builtin_huge_valf();
+        float loss = 0.0f, l2 = 0.0f;
+        Stat a{0.0f, 0.0f, 0.0f};
+        const uint32_t rest = sp.vb - sp.va > NV * T ? sp.va + NV * T : sp.vb;  // first vector not held
+        if (!absent) {
+            // the steps of scan_span, the first of them from registers
+            a.init();
+            if (lane < 2) scan_edge<Fmt, false>(sp, lane, scale, a);
+#pragma unroll
+            for (int i = 0; i < NV; i += U) {
+                if (sp.va + i * T < sp.vb) {
+                    float e[U * VW];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        typename Fmt::Vec h = held[i + u];
+                        if (sp.va + (i + U) * T > sp.vb)
+                            h = masked_unless<Fmt>(sp.va + lane + (i + u) * T < sp.vb, h);
+                        float f[VW];
+                        Fmt::unpack(h, f);
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) e[u * VW + j] = f[j];
+                    }
+                    take<false>(e, scale, a);
+                }
+            }
+            teacher_weights<T>(ent, k, scale, q, lane);
+            if (rest < sp.vb) scan_on<Fmt, false, T, U>(sp, rest, sp.vb, lane, scale, a);
+            team_merge<false, T>(a, scale, lane, sh);
+            l2 = bad ? __builtin_nanf("") : log2_f(a.s);
+            loss = distill_loss<T>(ent, k, scale, q, a, l2, lane, sh);
+        }
+        if (lane == 0) store_distill(addr<float>(stats_), rows, r, loss, a.m, l2, q);
+        const bool zero = absent || l2 == -__builtin_huge_valf();
+        const float coef = addr<const float>(w)[r] * scale * kLn2;
+        const auto write = [&](const typename Fmt::Vec& v16, uint32_t v) {
+            float e[VW], d[VW];
+            Fmt::unpack(v16, e);
+#pragma unroll
+            for (int j = 0; j < VW; ++j) d[j] = coef * exp2_f(fmaf(e[j] - a.m, scale, -l2));
+            typename Fmt::Vec g = pack<Fmt>(d);
+            if (zero) g = __builtin_bit_cast(typename Fmt::Vec, u32x4{0, 0, 0, 0});
+            store16_any<Fmt>(out + static_cast<size_t>(sp.pos(v)) * Fmt::kSize, g);
+        };
+        const uint32_t next = r + teams;
+        const Span<Fmt> np(row_at(next < rows ? next : r), cols);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t v = sp.va + lane + i * T;
+            if (v < sp.vb) write(held[i], v);
+            if (next < rows) load(np, i);
+        }
+        for (uint32_t v = rest + lane; v < sp.vb; v += T) write(load16<Fmt>(sp.at(v)), v);
+        const uint32_t ev = sp.edge(lane);
+        if (ev != kNoVec) {
+            const uint32_t p0 = sp.pos(ev);
+            for (uint32_t p = p0; p != p0 + VW; ++p) {
+                if (p >= cols) continue;
+                const float e = Fmt::load1(row + static_cast<size_t>(p) * Fmt::kSize);
+                reinterpret_cast<typename Fmt::Bits*>(out)[p] =
+                    round_to<Fmt>(zero ? 0.0f : coef * exp2_f(fmaf(e - a.m, scale, -l2)));
+            }
+        }
+        team_sync<T>();
+        if (!zero) {
+            for (uint32_t i = lane; i < k; i += T) {
+                const Entry e = ent[i];
+                if (e.id < 0 || static_cast<uint32_t>(e.id) >= cols) continue;
+                const float p = exp2_f(fmaf(e.x - a.m, scale, -l2));
+                reinterpret_cast<typename Fmt::Bits*>(out)[e.id] = round_to<Fmt>(coef * (p - e.w));
+            }
+        }
+        if (next >= rows) return;
+        team_sync<T>();  // the entries are written anew
+        r = next;
+    }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1238,7 +1413,8 @@ void with_team(int team, F f) {
     switch (team) {
         case 64: f(Int<64>{}); break;
         case 256: f(Int<256>{}); break;
-        default: f(Int<512>{}); break;
+        case 512: f(Int<512>{}); break;
+        default: f(Int<1024>{}); break;
     }
 }
 template <typename F>
@@ -1258,6 +1434,12 @@ uint32_t log2_of(int v) { return static_cast<uint32_t>(__builtin_ctz(static_cast
 template <typename... KArgs, typename... Args>
 void launch(void (*kernel)(KArgs...), uint32_t grid, int block, hipStream_t s, Args... args) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, s, args...);
+}
+// With LDS for the teacher's entries of the workgroup's rows.
+template <typename... KArgs, typename... Args>
+void launch_entries(void (*kernel)(KArgs...), uint32_t grid, int block, int entries, hipStream_t s,
+                    Args... args) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), entries * sizeof(Entry), s, args...);
 }
 
 }  // namespace
@@ -1353,18 +1535,25 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
             Part* part = reinterpret_cast<Part*>(scratch16);
             launch(k_part<Fmt, false>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
                    static_cast<uint32_t>(plan.parts), static_cast<const int64_t*>(nullptr), part);
-            launch(k_ds_merge<Fmt>, rows, kMergeThreads, s, a.x, cols, stride, a.scale, rows,
+            launch_entries(k_ds_merge<Fmt>, rows, kMergeThreads, k, s, a.x, cols, stride, a.scale, rows,
                    tagged(ids, k), tagged(values, plan.parts), static_cast<const Part*>(part), stats);
             return;
         }
         with_team(plan.team, [&](auto team) {
             constexpr int T = decltype(team)::value;
-            if (grad != nullptr)
-                launch(k_ds_step<Fmt, T>, grid, kTeamBlock<T>, s, tagged(a.x, cols),
+            const auto step = [&](auto held) {
+                launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k,
+                               s, tagged(a.x, cols),
                        tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
-                       tagged(weights, sc >> 16), tagged(grad, 0), stride, rows);
+                       tagged(weights, sc >> 16), tagged(grad, grid), stride, rows);
+            };
+            // 8 vectors per lane, or 16 for the rows that do not fit (T = 1024 alone has such)
+            if (grad != nullptr && T == 1024 && plan.held > 8)
+                step(Int<T == 1024 ? 16 : 8>{});
+            else if (grad != nullptr)
+                step(Int<8>{});
             else
-                launch(k_ds_team<Fmt, T>, grid, kTeamBlock<T>, s, a.x, cols, stride, a.scale, rows,
+                launch_entries(k_ds_team<Fmt, T>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k, s, a.x, cols, stride, a.scale, rows,
                        static_cast<uint32_t>(k), ids, values, stats);
         });
     });

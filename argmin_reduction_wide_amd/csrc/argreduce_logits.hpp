@@ -21,6 +21,7 @@ struct LogitsPlan {
     int path;             // argreduce_path_t: SUBWAVE, BLOCK or SPLIT
     int team;             // lanes that scan one row (SUBWAVE, BLOCK), else kPartThreads
     int parts;            // SPLIT: workgroups per row
+    int held;             // distillation step: vectors per lane kept in registers, 8 or 16
     int64_t grid_blocks;  // workgroups of the scanning kernel
     int64_t device_threads;
     size_t scratch_bytes; // including 15 bytes of alignment slack; 0 if none needed

@@ -14,6 +14,7 @@ namespace argreduce {
 namespace {
 
 constexpr int64_t kBlock = 256;
+constexpr int64_t kThreadsPerCu = 2048;
 constexpr int64_t kMaxGridThreads = int64_t{1} << 32;  // threads a launch's grid may hold
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -65,10 +66,25 @@ bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p)
 // A device array of `n`-byte elements that a call with rows > 0 needs.
 bool usable(const void* p, uintptr_t n) { return p != nullptr && aligned(p, n) && fits48(p); }
 
+// Workgroups of the distillation step: as many as its registers (at most 128 per lane) let the
+// CUs hold at once; each goes through several rows. The kernel takes the number in 16 bits.
+int64_t step_blocks(int64_t cap, int team) {
+    const int64_t per_cu = team == 1024 ? 1 : team == 512 ? 2 : 4;
+    const int64_t cus = cap / kThreadsPerCu > 0 ? cap / kThreadsPerCu : 1;
+    return per_cu * cus < 65535 ? per_cu * cus : 65535;
+}
+
+// What a plan is for.
+enum Use { kLogprobs, kLogprobsTop, kDistill, kDistillStep };
+
+// Rows of up to this many vectors (160 KiB, in a distillation step 256 KiB) are left to one
+// workgroup each, however few they are.
+constexpr int64_t kOneBlockVecs = 10240;
+constexpr int64_t kOneBlockStepVecs = 16384;
+
 // Scratch depends on the shape alone, so only the choices among plans without any go by
 // `vec_rows` (every row starts on a 16-byte boundary).
-int make_logits_plan(int dtype, int64_t rows, int64_t cols, bool groups, bool vec_rows,
-                     LogitsPlan* p) {
+int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, bool vec_rows, LogitsPlan* p) {
     int rc = check_logits_shape(dtype, rows, cols);
     if (rc != ARGREDUCE_OK) return rc;
     int64_t cap = 0;
@@ -81,8 +97,10 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, bool groups, bool ve
     *p = LogitsPlan{};
     p->device_threads = cap;
     p->parts = 1;
+    p->held = vecs > 8 * 1024 ? 16 : 8;
+    const bool logprobs = use == kLogprobs || use == kLogprobsTop;
     const int64_t held = vec_rows ? ceil_div(cols * es, 16) : vecs;  // vectors a row lies in
-    if (held <= 32 && groups) {
+    if (held <= 32 && logprobs) {
         p->path = ARGREDUCE_PATH_SUBWAVE;
         p->team = static_cast<int>(next_pow2(held < 4 ? 4 : held));
         p->grid_blocks = ceil_div(rows1, kBlock / p->team);
@@ -94,13 +112,19 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, bool groups, bool ve
         p->team = 64;
         p->grid_blocks = ceil_div(rows1, kBlock / 64);
         if (rows1 * 64 >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
+        if (use == kDistillStep) {
+            const int64_t most = step_blocks(cap, p->team);
+            p->grid_blocks = p->grid_blocks < most ? p->grid_blocks : most;
+        }
         return ARGREDUCE_OK;
     }
-    int64_t parts = ceil_div(vecs, kPartThreads * kPartUnroll);
-    const int64_t most = cap_blocks / rows1;
-    parts = parts < most ? parts : most;
-    parts = parts < kMaxParts ? parts : kMaxParts;
-    if (parts >= 4) {
+    // Long rows too few to give every second CU one: split, in one device wave.
+    const int64_t one_block = use == kDistillStep ? kOneBlockStepVecs : kOneBlockVecs;
+    if (vecs > one_block && rows1 <= cap / kThreadsPerCu / 2) {
+        int64_t parts = ceil_div(vecs, kPartThreads * kPartUnroll);
+        const int64_t most = cap_blocks / rows1;
+        parts = parts < most ? parts : most;
+        parts = parts < kMaxParts ? parts : kMaxParts;
         p->path = ARGREDUCE_PATH_SPLIT;
         p->team = kPartThreads;
         p->parts = static_cast<int>(parts);
@@ -109,9 +133,18 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, bool groups, bool ve
         return ARGREDUCE_OK;
     }
     p->path = ARGREDUCE_PATH_BLOCK;
-    p->team = vecs > 4096 ? 512 : 256;
+    if (use == kDistillStep)
+        p->team = vecs <= 8 * 256 ? 256 : vecs <= 8 * 512 ? 512 : 1024;  // what the registers hold
+    else if (vecs > 2048 && rows1 * 1024 <= cap)
+        p->team = 1024;  // the whole device in one wave of workgroups
+    else
+        p->team = vecs > (use == kLogprobsTop ? 4096 : 3000) ? 512 : 256;
     p->grid_blocks = rows1;
     if (rows1 * p->team >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
+    if (use == kDistillStep) {
+        const int64_t most = step_blocks(cap, p->team);
+        p->grid_blocks = rows1 < most ? rows1 : most;
+    }
     return ARGREDUCE_OK;
 }
 
@@ -179,7 +212,7 @@ int distill(const LogitsArgs& a, int32_t k, const int64_t* ids, const float* val
             const float* weights, void* grad, void* scratch, size_t scratch_bytes, void* stream) {
     LogitsPlan p;
     GradPlan g;
-    int rc = make_logits_plan(a.dtype, a.rows, a.cols, false, vec_rows(a), &p);
+    int rc = make_logits_plan(a.dtype, a.rows, a.cols, grad != nullptr ? kDistillStep : kDistill, vec_rows(a), &p);
     if (rc != ARGREDUCE_OK) return rc;
     rc = make_grad_plan(a.dtype, a.rows, a.cols, &g);
     if (rc != ARGREDUCE_OK) return rc;
@@ -200,7 +233,7 @@ using argreduce::LogitsPlan;
 ARGREDUCE_EXPORT size_t argreduce_logprobs_scratch_bytes(int64_t rows, int64_t cols,
                                                          argreduce_dtype_t dtype) {
     LogitsPlan p;
-    if (argreduce::make_logits_plan(dtype, rows, cols, true, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p) != ARGREDUCE_OK)
+    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p) != ARGREDUCE_OK)
         return std::numeric_limits<size_t>::max();
     return p.scratch_bytes;
 }
@@ -209,7 +242,7 @@ ARGREDUCE_EXPORT int argreduce_logprobs_plan(int64_t rows, int64_t cols, argredu
                                              argreduce_plan_t* out) {
     if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
     LogitsPlan p;
-    const int rc = argreduce::make_logits_plan(dtype, rows, cols, true, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p);
+    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p);
     if (rc != ARGREDUCE_OK) return rc;
     argreduce::fill_logits_plan(p, p.parts > 1 ? 2 : 1, out);
     return ARGREDUCE_OK;
@@ -229,7 +262,7 @@ ARGREDUCE_EXPORT int argreduce_logprobs(const void* x, argreduce_dtype_t dtype, 
     if (!fits48(x) || !usable(tokens, 8) || !usable(stats, 4)) return ARGREDUCE_ERR_INVALID_ARG;
     if (top > 0 && (!usable(top_logprobs, 4) || !usable(top_tokens, 8))) return ARGREDUCE_ERR_INVALID_ARG;
     LogitsPlan p;
-    rc = make_logits_plan(dtype, rows, cols, true, vec_rows(a), &p);
+    rc = make_logits_plan(dtype, rows, cols, top > 0 ? kLogprobsTop : kLogprobs, vec_rows(a), &p);
     if (rc != ARGREDUCE_OK) return rc;
     uint8_t* scratch16 = nullptr;
     rc = scratch_of(p, scratch, scratch_bytes, &scratch16);
@@ -263,7 +296,7 @@ ARGREDUCE_EXPORT int argreduce_logprobs_grad(const void* x, argreduce_dtype_t dt
 ARGREDUCE_EXPORT size_t argreduce_distill_scratch_bytes(int64_t rows, int64_t cols,
                                                         argreduce_dtype_t dtype) {
     LogitsPlan p;
-    if (argreduce::make_logits_plan(dtype, rows, cols, false, false, &p) != ARGREDUCE_OK)
+    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, false, &p) != ARGREDUCE_OK)
         return std::numeric_limits<size_t>::max();
     return p.scratch_bytes;
 }
@@ -272,7 +305,7 @@ ARGREDUCE_EXPORT int argreduce_distill_plan(int64_t rows, int64_t cols, argreduc
                                             argreduce_plan_t* out) {
     if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
     LogitsPlan p;
-    const int rc = argreduce::make_logits_plan(dtype, rows, cols, false, false, &p);
+    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, false, &p);
     if (rc != ARGREDUCE_OK) return rc;
     argreduce::fill_logits_plan(p, p.parts > 1 ? 2 : 1, out);
     return ARGREDUCE_OK;

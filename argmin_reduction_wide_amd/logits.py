@@ -99,36 +99,29 @@ def _temperature(t) -> float:
     return t
 
 
-class _On:
-    """Makes the logits' device current for the library (its plans and launches go by the
-    current device), where it is not already."""
+# The current device and its current stream's handle, as cheaply as torch gives them
+# (torch.cuda.current_stream(...).cuda_stream takes 2 us, a tenth of a small call).
+_device = torch._C._cuda_getDevice
+_stream = torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("index", "before")
 
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self) -> int:
-        self.before = torch._C._cuda_getDevice()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _elsewhere(logits) -> bool:
+    """Whether the logits are on another device than the current one. Plans and launches go by the
+    current device: such a call is made again with the logits' device current."""
+    return logits.device.index != _device()
 
 
 def _scratch(need: int, what: str, given, device):
-    if need == B.SIZE_MAX:
-        raise B.ArgreduceError(-3, what)
+    """(address, bytes, owner) of scratch for a call."""
     if given is not None:
         B._check_buffer(given, "scratch", device)
     if need == 0:
-        return None, 0, 0
+        return 0, 0, None
+    if need == B.SIZE_MAX:
+        raise B.ArgreduceError(-3, what)
     if given is None or given.numel() * given.element_size() < need:
         given = torch.empty(need, dtype=torch.uint8, device=device)
-    return given, given.data_ptr(), given.numel() * given.element_size()
+    return given.data_ptr(), given.numel() * given.element_size(), given
 
 
 def _done(rc: int, what: str, r: _Rows) -> None:
@@ -150,24 +143,30 @@ def _refuse_captured_autograd(logits) -> None:
 
 def _logprobs(logits, tokens, temperature, entropy, top, scratch):
     r = _rows(logits)
-    lead = logits.shape[:-1]
+    shape = logits.shape
+    lead = shape[:-1]
     _same(tokens, "tokens", logits, torch.int64, lead)
     temperature = _temperature(temperature)
     if not 0 <= top <= TOP_MAX:
         raise ValueError(f"top must lie in 0..{TOP_MAX}; got {top}")
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return _logprobs(logits, tokens, temperature, entropy, top, scratch)
     device = logits.device
-    stats = torch.empty((4, r.rows), dtype=torch.float32, device=device)
+    code, rows, cols, stride = r
+    stats = torch.empty(4, rows, dtype=torch.float32, device=device)
     lp = tok = None
+    lp_ptr = tok_ptr = 0
     if top:
-        lp = torch.empty(lead + (top,), dtype=torch.float32, device=device)
-        tok = torch.empty(lead + (top,), dtype=torch.int64, device=device)
-    with _On(device) as stream:
-        need = B.argreduce_logprobs_scratch_bytes(r.rows, r.cols, r.code)
-        scratch, sptr, sbytes = _scratch(need, "argreduce_logprobs", scratch, device)
-        rc = B.argreduce_logprobs(logits.data_ptr(), r.code, r.rows, r.cols, r.stride,
-                                  tokens.data_ptr(), temperature, 1 if entropy else 0, top,
-                                  stats.data_ptr(), lp.data_ptr() if top else 0,
-                                  tok.data_ptr() if top else 0, sptr, sbytes, stream)
+        lp = torch.empty(*lead, top, dtype=torch.float32, device=device)
+        tok = torch.empty(*lead, top, dtype=torch.int64, device=device)
+        lp_ptr, tok_ptr = lp.data_ptr(), tok.data_ptr()
+    need = B.entry_point("argreduce_logprobs_scratch_bytes")(rows, cols, code)
+    sptr, sbytes, scratch = _scratch(need, "argreduce_logprobs", scratch, device)
+    rc = B.entry_point("argreduce_logprobs")(logits.data_ptr(), code, rows, cols, stride,
+                                             tokens.data_ptr(), temperature, 1 if entropy else 0,
+                                             top, stats.data_ptr(), lp_ptr, tok_ptr, sptr, sbytes,
+                                             _stream(device.index))
     _done(rc, "argreduce_logprobs", r)
     return stats, lp, tok
 
@@ -224,7 +223,7 @@ def token_logprobs(logits, tokens, *, temperature: float = 1.0, entropy: bool = 
 
 def _grad_out(logits, out):
     if out is None:
-        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        return torch.empty(*logits.shape, dtype=logits.dtype, device=logits.device)
     B._check_buffer(out, "out", logits.device, logits.dtype, logits.numel())
     if out.shape != logits.shape:
         raise ValueError(f"out must have shape {tuple(logits.shape)}; got {tuple(out.shape)}")
@@ -247,12 +246,16 @@ def token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy=None, 
         _same(grad_entropy, "grad_entropy", logits, torch.float32, lead)
     temperature = _temperature(temperature)
     out = _grad_out(logits, out)
-    with _On(logits.device) as stream:
-        rc = B.argreduce_logprobs_grad(logits.data_ptr(), r.code, r.rows, r.cols, r.stride,
-                                       tokens.data_ptr(), temperature, stats.data_ptr(),
-                                       grad_logprob.data_ptr(),
-                                       0 if grad_entropy is None else grad_entropy.data_ptr(),
-                                       out.data_ptr(), stream)
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy,
+                                       temperature=temperature, out=out)
+    code, rows, cols, stride = r
+    rc = B.entry_point("argreduce_logprobs_grad")(
+        logits.data_ptr(), code, rows, cols, stride, tokens.data_ptr(), temperature,
+        stats.data_ptr(), grad_logprob.data_ptr(),
+        0 if grad_entropy is None else grad_entropy.data_ptr(), out.data_ptr(),
+        _stream(logits.device.index))
     _done(rc, "argreduce_logprobs_grad", r)
     return out
 
@@ -275,13 +278,18 @@ def _distill(logits, teacher_tokens, teacher_logits, temperature, scratch):
     r = _rows(logits)
     k = _teacher(logits, teacher_tokens, teacher_logits)
     temperature = _temperature(temperature)
-    stats = torch.empty((5, r.rows), dtype=torch.float32, device=logits.device)
-    with _On(logits.device) as stream:
-        need = B.argreduce_distill_scratch_bytes(r.rows, r.cols, r.code)
-        scratch, sptr, sbytes = _scratch(need, "argreduce_distill", scratch, logits.device)
-        rc = B.argreduce_distill(logits.data_ptr(), r.code, r.rows, r.cols, r.stride, k,
-                                 teacher_tokens.data_ptr(), teacher_logits.data_ptr(), temperature,
-                                 stats.data_ptr(), sptr, sbytes, stream)
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return _distill(logits, teacher_tokens, teacher_logits, temperature, scratch)
+    code, rows, cols, stride = r
+    device = logits.device
+    stats = torch.empty(5, rows, dtype=torch.float32, device=device)
+    need = B.entry_point("argreduce_distill_scratch_bytes")(rows, cols, code)
+    sptr, sbytes, scratch = _scratch(need, "argreduce_distill", scratch, device)
+    rc = B.entry_point("argreduce_distill")(logits.data_ptr(), code, rows, cols, stride, k,
+                                            teacher_tokens.data_ptr(), teacher_logits.data_ptr(),
+                                            temperature, stats.data_ptr(), sptr, sbytes,
+                                            _stream(device.index))
     _done(rc, "argreduce_distill", r)
     return stats
 
@@ -336,11 +344,15 @@ def distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss, 
     _same(grad_loss, "grad_loss", logits, torch.float32, logits.shape[:-1])
     temperature = _temperature(temperature)
     out = _grad_out(logits, out)
-    with _On(logits.device) as stream:
-        rc = B.argreduce_distill_grad(logits.data_ptr(), r.code, r.rows, r.cols, r.stride, k,
-                                      teacher_tokens.data_ptr(), teacher_logits.data_ptr(),
-                                      temperature, stats.data_ptr(), grad_loss.data_ptr(),
-                                      out.data_ptr(), stream)
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss,
+                                     temperature=temperature, out=out)
+    code, rows, cols, stride = r
+    rc = B.entry_point("argreduce_distill_grad")(
+        logits.data_ptr(), code, rows, cols, stride, k, teacher_tokens.data_ptr(),
+        teacher_logits.data_ptr(), temperature, stats.data_ptr(), grad_loss.data_ptr(),
+        out.data_ptr(), _stream(logits.device.index))
     _done(rc, "argreduce_distill_grad", r)
     return out
 
@@ -355,13 +367,18 @@ def distill_step(logits, teacher_tokens, teacher_logits, weights, *, temperature
     _same(weights, "weights", logits, torch.float32, logits.shape[:-1])
     temperature = _temperature(temperature)
     out = _grad_out(logits, out)
-    stats = torch.empty((5, r.rows), dtype=torch.float32, device=logits.device)
-    with _On(logits.device) as stream:
-        need = B.argreduce_distill_scratch_bytes(r.rows, r.cols, r.code)
-        scratch, sptr, sbytes = _scratch(need, "argreduce_distill_step", scratch, logits.device)
-        rc = B.argreduce_distill_step(logits.data_ptr(), r.code, r.rows, r.cols, r.stride, k,
-                                      teacher_tokens.data_ptr(), teacher_logits.data_ptr(),
-                                      temperature, weights.data_ptr(), stats.data_ptr(),
-                                      out.data_ptr(), sptr, sbytes, stream)
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return distill_step(logits, teacher_tokens, teacher_logits, weights,
+                                temperature=temperature, out=out, scratch=scratch)
+    code, rows, cols, stride = r
+    device = logits.device
+    stats = torch.empty(5, rows, dtype=torch.float32, device=device)
+    need = B.entry_point("argreduce_distill_scratch_bytes")(rows, cols, code)
+    sptr, sbytes, scratch = _scratch(need, "argreduce_distill_step", scratch, device)
+    rc = B.entry_point("argreduce_distill_step")(
+        logits.data_ptr(), code, rows, cols, stride, k, teacher_tokens.data_ptr(),
+        teacher_logits.data_ptr(), temperature, weights.data_ptr(), stats.data_ptr(),
+        out.data_ptr(), sptr, sbytes, _stream(device.index))
     _done(rc, "argreduce_distill_step", r)
     return (stats[0] if logits.dim() == 2 else stats[0].view(logits.shape[:-1])), out
