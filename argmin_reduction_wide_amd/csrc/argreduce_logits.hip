@@ -95,13 +95,17 @@ __device__ inline float lanes_sum(float v) {
 }
 
 // A team is one wavefront (T == 64, four teams to a workgroup) or one workgroup of T threads.
+// The barrier orders LDS accesses only: __syncthreads() would also wait for every load and store
+// to global memory under way, which no team exchanges anything through.
 template <int T>
 __device__ inline void team_sync() {
     if constexpr (T == kWave) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     } else {
-        __syncthreads();
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     }
 }
 
@@ -148,7 +152,7 @@ __device__ inline void team_merge(Stat& a, float k, int lane, float (*sh)[4]) {
             sh[wave][1] = a.s;
             sh[wave][2] = a.h;
         }
-        __syncthreads();
+        team_sync<T>();
         float m = sh[0][0];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) m = max_f(m, sh[w][0]);
@@ -161,7 +165,7 @@ __device__ inline void team_merge(Stat& a, float k, int lane, float (*sh)[4]) {
             all.h += b.h;
         }
         a = all;
-        __syncthreads();
+        team_sync<T>();
     }
 }
 
@@ -170,11 +174,11 @@ __device__ inline float team_reduce(float v, int lane, float (*sh)[4]) {
     v = MAX ? lanes_max<kWave>(v) : lanes_sum<kWave>(v);
     if constexpr (T > kWave) {
         if (lane % kWave == 0) sh[lane / kWave][3] = v;
-        __syncthreads();
+        team_sync<T>();
         v = sh[0][3];
 #pragma unroll
         for (int w = 1; w < T / kWave; ++w) v = MAX ? max_f(v, sh[w][3]) : v + sh[w][3];
-        __syncthreads();
+        team_sync<T>();
     }
     return v;
 }
@@ -1067,45 +1071,51 @@ struct Entry {
 };
 extern __shared__ Entry s_entries[];
 
+template <typename Fmt>
+__device__ inline float student_at(const uint8_t* row, int32_t id, uint32_t cols) {
+    return id >= 0 && static_cast<uint32_t>(id) < cols
+               ? Fmt::load1(row + static_cast<size_t>(id) * Fmt::kSize)
+               : __builtin_nanf("");
+}
+__device__ inline Entry entry_at(const int64_t* ids, const float* values, uint32_t i, uint32_t cols) {
+    const int64_t id = ids[i];
+    return {static_cast<int32_t>(id < 0 ? -1 : id < static_cast<int64_t>(cols) ? id : cols),
+            id >= 0 ? values[i] : -__builtin_huge_valf(), __builtin_nanf(""), 0.0f};
+}
+// Up to 64 entries: every wavefront's own copy of them, one per lane (x in the team's first).
+__device__ inline Entry wave_entry(const int64_t* ids, const float* values, uint32_t k, int lane,
+                                   uint32_t cols) {
+    const uint32_t i = lane % kWave;
+    if (k <= kWave && i < k) return entry_at(ids, values, i, cols);
+    return {-1, -__builtin_huge_valf(), __builtin_nanf(""), 0.0f};
+}
+
 // The teacher's row: its entries into `ent`, the normaliser to every thread. *bad: the whole
 // gradient is NaN (a weight is NaN, or an id with weight lies beyond the row). Up to 64 entries
-// every wavefront finds the normaliser for itself, without a barrier.
+// (`mine`) every wavefront finds the normaliser for itself, without a barrier.
 template <typename Fmt, int T>
-__device__ inline Teacher teacher_row(Entry* ent, const uint8_t* row, uint32_t cols, const int64_t* ids,
-                                      const float* values, uint32_t k, float scale, int lane,
-                                      float (*sh)[4], bool* bad) {
-    const auto get = [&](uint32_t i, float* v) {
-        const int64_t id = ids[i];
-        *v = id >= 0 ? values[i] : -__builtin_huge_valf();
-        return id < 0 ? -1 : static_cast<int32_t>(id < static_cast<int64_t>(cols) ? id : cols);
-    };
+__device__ inline Teacher teacher_row(Entry* ent, const Entry& mine, const uint8_t* row, uint32_t cols,
+                                      const int64_t* ids, const float* values, uint32_t k, float scale,
+                                      int lane, float (*sh)[4], bool* bad) {
     float m = -__builtin_huge_valf(), s = 0.0f;
     Teacher q;
     if (k <= kWave) {
-        const uint32_t i = lane % kWave;
-        int32_t id = -1;
-        float v = -__builtin_huge_valf();
-        if (i < k) id = get(i, &v);
-        float x = __builtin_nanf("");
-        if (static_cast<uint32_t>(lane) < k && id >= 0 && static_cast<uint32_t>(id) < cols)
-            x = Fmt::load1(row + static_cast<size_t>(id) * Fmt::kSize);
-        m = lanes_max<kWave>(v);
-        if (m > -__builtin_huge_valf()) s = exp2_f((v - m) * scale);
-        if (v != v) s = v;
+        m = lanes_max<kWave>(mine.v);
+        if (m > -__builtin_huge_valf()) s = exp2_f((mine.v - m) * scale);
+        if (mine.v != mine.v) s = mine.v;
         s = lanes_sum<kWave>(s);
         q = {s == s ? m : __builtin_nanf(""), log2_f(s)};
-        *bad = __any(s != s || (id == static_cast<int32_t>(cols) && q.weight(v, scale) != 0.0f));
-        if (static_cast<uint32_t>(lane) < k) ent[lane] = {id, v, x, 0.0f};
+        *bad = __any(s != s || (mine.id == static_cast<int32_t>(cols) && q.weight(mine.v, scale) != 0.0f));
+        if (static_cast<uint32_t>(lane) < k) ent[lane] = mine;
         team_sync<kWave>();
     } else {
         bool nan = false, beyond = false;
         for (uint32_t i = lane; i < k; i += T) {
-            float v;
-            const int32_t id = get(i, &v);
-            ent[i].id = id;
-            ent[i].v = v;
-            m = max_f(m, v);
-            nan |= v != v;
+            const Entry e = entry_at(ids, values, i, cols);
+            ent[i].id = e.id;
+            ent[i].v = e.v;
+            m = max_f(m, e.v);
+            nan |= e.v != e.v;
         }
         m = team_reduce<T, true>(m, lane, sh);
         if (m > -__builtin_huge_valf())
@@ -1116,9 +1126,7 @@ __device__ inline Teacher teacher_row(Entry* ent, const uint8_t* row, uint32_t c
         for (uint32_t i = lane; i < k; i += T) {
             const int32_t id = ent[i].id;
             beyond |= id == static_cast<int32_t>(cols) && q.weight(ent[i].v, scale) != 0.0f;
-            ent[i].x = id >= 0 && static_cast<uint32_t>(id) < cols
-                           ? Fmt::load1(row + static_cast<size_t>(id) * Fmt::kSize)
-                           : __builtin_nanf("");
+            ent[i].x = student_at<Fmt>(row, id, cols);
         }
         *bad = s != s || team_reduce<T, true>(beyond ? 1.0f : 0.0f, lane, sh) > 0.0f;
     }
@@ -1198,7 +1206,9 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32
     const uint8_t* row = row_ptr<Fmt>(x, r, stride);
     Entry* ent = s_entries + threadIdx.x / T * k;
     bool bad;
-    const Teacher q = teacher_row<Fmt, T>(ent, row, cols, ids, values, k, scale, lane, sh, &bad);
+    Entry mine = wave_entry(ids, values, k, lane, cols);
+    if (lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
+    const Teacher q = teacher_row<Fmt, T>(ent, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
@@ -1226,9 +1236,11 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
     const int lane = threadIdx.x;
     const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
     const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
+    const uint8_t* row = row_ptr<Fmt>(x, r, stride);
     bool bad;
-    const Teacher q = teacher_row<Fmt, T>(s_entries, row_ptr<Fmt>(x, r, stride), cols, ids, values, k,
-                                          scale, lane, sh, &bad);
+    Entry mine = wave_entry(ids, values, k, lane, cols);
+    if (lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
+    const Teacher q = teacher_row<Fmt, T>(s_entries, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
@@ -1296,26 +1308,31 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t 
     const int lane = threadIdx.x % T;
     uint32_t r = blockIdx.x * kTeamsPerBlock<T> + threadIdx.x / T;
     if (r >= rows) return;
-    Entry* ent = s_entries + threadIdx.x / T * k;
+    // the entries of two rows: a wavefront may be one row ahead of another
+    Entry* ent = s_entries + threadIdx.x / T * 2 * k;
+    Entry* other = ent + k;
+    const auto ids_at = [&](uint32_t n) { return addr<const int64_t>(ids_) + static_cast<size_t>(n) * k; };
+    const auto values_at = [&](uint32_t n) { return addr<const float>(values_) + static_cast<size_t>(n) * k; };
     const auto row_at = [&](uint32_t n) { return row_ptr<Fmt>(addr<const void>(x), n, stride); };
     typename Fmt::Vec held[NV];
     const auto load = [&](const Span<Fmt>& sp, int i) {
         const uint32_t v = sp.va + lane + i * T;
         held[i] = load16<Fmt>(sp.at(v < sp.vb ? v : sp.vs - 1));  // of any row a readable vector
     };
+    Entry mine = wave_entry(ids_at(r), values_at(r), k, lane, cols);
     {
         const Span<Fmt> sp(row_at(r), cols);
 #pragma unroll
         for (int i = 0; i < NV; ++i) load(sp, i);
     }
     while (true) {
-        const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
-        const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
         const uint8_t* row = row_at(r);
+        if (lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
         uint8_t* out = const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad_), r, cols));
         const Span<Fmt> sp(row, cols);
         bool bad;
-        const Teacher q = teacher_row<Fmt, T>(ent, row, cols, ids, values, k, scale, lane, sh, &bad);
+        const Teacher q = teacher_row<Fmt, T>(ent, mine, row, cols, ids_at(r), values_at(r), k, scale, lane,
+                                              sh, &bad);
         const bool absent = q.m == -__builtin_huge_valf();
         float loss = 0.0f, l2 = 0.0f;
         Stat a{0.0f, 0.0f, 0.0f};
@@ -1346,6 +1363,8 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t 
             team_merge<false, T>(a, scale, lane, sh);
             l2 = bad ? __builtin_nanf("") : log2_f(a.s);
             loss = distill_loss<T>(ent, k, scale, q, a, l2, lane, sh);
+        } else {
+            team_sync<T>();  // every row has a barrier: none gets two rows ahead of another
         }
         if (lane == 0) store_distill(addr<float>(stats_), rows, r, loss, a.m, l2, q);
         const bool zero = absent || l2 == -__builtin_huge_valf();
@@ -1360,7 +1379,9 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t 
             store16_any<Fmt>(out + static_cast<size_t>(sp.pos(v)) * Fmt::kSize, g);
         };
         const uint32_t next = r + teams;
-        const Span<Fmt> np(row_at(next < rows ? next : r), cols);
+        const uint32_t nr = next < rows ? next : r;
+        const Span<Fmt> np(row_at(nr), cols);
+        mine = wave_entry(ids_at(nr), values_at(nr), k, lane, cols);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const uint32_t v = sp.va + lane + i * T;
@@ -1378,17 +1399,24 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t 
                     round_to<Fmt>(zero ? 0.0f : coef * exp2_f(fmaf(e - a.m, scale, -l2)));
             }
         }
-        team_sync<T>();
+        // Each wavefront stores again the elements at the teacher's ids that it has just stored: its
+        // own stores to an address keep their order, so no barrier is needed.
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (!zero) {
-            for (uint32_t i = lane; i < k; i += T) {
+            for (uint32_t i = lane % kWave; i < k; i += kWave) {
                 const Entry e = ent[i];
                 if (e.id < 0 || static_cast<uint32_t>(e.id) >= cols) continue;
+                const uint32_t v = (static_cast<uint32_t>(e.id) + sp.off) / VW;
+                const uint32_t owner = v >= sp.va && v < sp.vb ? (v - sp.va) % T / kWave : 0;
+                if (owner != static_cast<uint32_t>(lane) / kWave) continue;
                 const float p = exp2_f(fmaf(e.x - a.m, scale, -l2));
                 reinterpret_cast<typename Fmt::Bits*>(out)[e.id] = round_to<Fmt>(coef * (p - e.w));
             }
         }
         if (next >= rows) return;
-        team_sync<T>();  // the entries are written anew
+        Entry* const t = ent;
+        ent = other;
+        other = t;
         r = next;
     }
 }
@@ -1542,7 +1570,7 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
         with_team(plan.team, [&](auto team) {
             constexpr int T = decltype(team)::value;
             const auto step = [&](auto held) {
-                launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k,
+                launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * 2 * k,
                                s, tagged(a.x, cols),
                        tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
                        tagged(weights, sc >> 16), tagged(grad, grid), stride, rows);
