@@ -109,6 +109,20 @@ __device__ inline void team_sync() {
     }
 }
 
+// A thread's team in its workgroup and its lane in the team; the team as a wave-uniform value, so
+// that row addresses stay in scalar registers.
+template <int T>
+__device__ inline uint32_t team_of() {
+    if constexpr (T == kWave)
+        return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    else
+        return 0;
+}
+template <int T>
+__device__ inline int lane_of() {
+    return T == kWave ? threadIdx.x % kWave : threadIdx.x;
+}
+
 template <int T>
 constexpr int kTeamsPerBlock = T == kWave ? kBlockThreads / kWave : 1;
 template <int T>
@@ -138,7 +152,13 @@ struct Stat {
     }
 };
 
-// Merges the lanes' parts; every thread of the team gets the row's.
+// A value that every lane of the wavefront holds, as a scalar.
+__device__ inline float uniform(float v) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
+// Merges the lanes' parts; every thread of the team gets the row's. The wavefronts' parts go
+// through LDS; each wavefront then merges them all, one per lane of each group of T / 64 lanes.
 template <bool ENT, int T>
 __device__ inline void team_merge(Stat& a, float k, int lane, float (*sh)[4]) {
     a.move<ENT>(lanes_max<kWave>(a.m), k);
@@ -146,27 +166,20 @@ __device__ inline void team_merge(Stat& a, float k, int lane, float (*sh)[4]) {
     if constexpr (ENT) a.h = lanes_sum<kWave>(a.h);
     if constexpr (T > kWave) {
         constexpr int kWaves = T / kWave;
-        const int wave = lane / kWave;
         if (lane % kWave == 0) {
-            sh[wave][0] = a.m;
-            sh[wave][1] = a.s;
-            sh[wave][2] = a.h;
+            sh[lane / kWave][0] = a.m;
+            sh[lane / kWave][1] = a.s;
+            sh[lane / kWave][2] = a.h;
         }
         team_sync<T>();
-        float m = sh[0][0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) m = max_f(m, sh[w][0]);
-        Stat all{m, 0.0f, 0.0f};
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            Stat b{sh[w][0], sh[w][1], ENT ? sh[w][2] : 0.0f};
-            b.move<ENT>(m, k);
-            all.s += b.s;
-            all.h += b.h;
-        }
-        a = all;
+        const float* w = sh[lane % kWaves];
+        a = {w[0], w[1], ENT ? w[2] : 0.0f};
+        a.move<ENT>(lanes_max<kWaves>(a.m), k);
+        a.s = lanes_sum<kWaves>(a.s);
+        if constexpr (ENT) a.h = lanes_sum<kWaves>(a.h);
         team_sync<T>();
     }
+    a = {uniform(a.m), uniform(a.s), uniform(a.h)};
 }
 
 template <int T, bool MAX>
@@ -175,12 +188,11 @@ __device__ inline float team_reduce(float v, int lane, float (*sh)[4]) {
     if constexpr (T > kWave) {
         if (lane % kWave == 0) sh[lane / kWave][3] = v;
         team_sync<T>();
-        v = sh[0][3];
-#pragma unroll
-        for (int w = 1; w < T / kWave; ++w) v = MAX ? max_f(v, sh[w][3]) : v + sh[w][3];
+        v = sh[lane % (T / kWave)][3];
+        v = MAX ? lanes_max<T / kWave>(v) : lanes_sum<T / kWave>(v);
         team_sync<T>();
     }
-    return v;
+    return uniform(v);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -766,9 +778,9 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32
     constexpr int U = kUnroll<Fmt, TOP>;
     __shared__ float sh[T / kWave][4];
     __shared__ TopLds<TOP ? T : 64, TOP ? kSegs<T> : 1> lds[TOP ? kTeams : 1];
-    const uint32_t team = threadIdx.x / T;
+    const uint32_t team = team_of<T>();
     const uint32_t r = blockIdx.x * kTeams + team;
-    const int lane = threadIdx.x % T;
+    const int lane = lane_of<T>();
     if (r >= rows) return;  // whole teams, and never one of several wavefronts
     const int64_t t = tokens[r];
     const uint32_t k = tag(top_lp);
@@ -1012,16 +1024,17 @@ struct GradSlice {
 // d logprob and d entropy: dx_j = [ g (delta_jt - p_j) - e p_j (ln p_j + H) ] / T.
 // Tags: columns in (x, tokens), scale in (stats, g_lp), slices in g_ent, log2 of the team's
 // lanes in grad.
-template <typename Fmt, bool ENT>
+template <typename Fmt, bool ENT, bool WIDE>
 __global__ __launch_bounds__(kBlockThreads) void k_lp_grad(uint64_t x, uint64_t tokens,
                                                            uint64_t stats_, uint64_t g_lp,
                                                            uint64_t g_ent, uint64_t grad,
                                                            uint32_t stride, uint32_t rows) {
     constexpr int VW = Fmt::VW;
-    const uint32_t cols = tags(x, tokens), lg = tag(grad), slices = tag(g_ent);
+    const uint32_t cols = tags(x, tokens), slices = tag(g_ent);
+    const uint32_t lg = WIDE ? 8 : tag(grad);  // WIDE: a slice per workgroup, wave-uniform addresses
     const float scale = __uint_as_float(tags(stats_, g_lp));
-    const uint32_t unit = (blockIdx.x << (8 - lg)) + (threadIdx.x >> lg);
-    const uint32_t r = unit / slices;
+    const uint32_t unit = WIDE ? blockIdx.x : (blockIdx.x << (8 - lg)) + (threadIdx.x >> lg);
+    const uint32_t r = WIDE ? unit / slices : unit;
     if (r >= rows) return;
     const int lane = threadIdx.x & ((1u << lg) - 1);
     const float* stats = addr<const float>(stats_);
@@ -1037,7 +1050,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_grad(uint64_t x, uint64_t 
     const bool zero = t < 0 || l2 == -__builtin_huge_valf();
     const GradSlice<Fmt> gs(row_ptr<Fmt>(addr<const void>(x), r, stride),
                             const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad), r, cols)), cols,
-                            unit - r * slices, slices);
+                            WIDE ? unit - r * slices : 0, slices);
     gs.write(lane, 1 << lg, zero, [&](const float (&e)[VW], uint32_t p0, float (&d)[VW]) {
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
@@ -1055,19 +1068,21 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_grad(uint64_t x, uint64_t 
 
 // ---------------------------------------------------------------------------------------
 // Distillation. The teacher's distribution q is the softmax of its k values over the entries
-// with an id >= 0; loss = sum q_i (ln q_i - ln p_i).
+// with an id >= 0; loss = sum q_i (ln q_i - ln p_i), the first part known before the student's.
 // stats is [5, rows]: loss, maximum, log2 of the sum, and the same two of the teacher's row.
 
 struct Teacher {
-    float m, l2;
-    __device__ float weight(float v, float scale) const { return exp2_f(fmaf(v - m, scale, -l2)); }
+    float m, l2;    // log2 q_i = (v_i - m) scale - l2
+    float entropy;  // -sum q_i ln q_i
+    __device__ float log_weight(float v, float scale) const { return fmaf(v - m, scale, -l2); }
+    __device__ float weight(float v, float scale) const { return exp2_f(log_weight(v, scale)); }
 };
-// An entry of the teacher's row in LDS: id (-1: absent, cols: beyond the row), value (-inf if
-// absent), the student's logit there, and the weight of all entries with this id. Entry i belongs
-// to the lanes i mod T; only id and v are read by others.
+// An entry of the teacher's row in LDS: id (-1: absent, cols: beyond the row), weight (first the
+// value), the weight of all entries with this id, and the student's logit there. Entry i belongs to
+// the lanes i mod T.
 struct Entry {
     int32_t id;
-    float v, x, w;
+    float w, total, x;
 };
 extern __shared__ Entry s_entries[];
 
@@ -1080,70 +1095,86 @@ __device__ inline float student_at(const uint8_t* row, int32_t id, uint32_t cols
 __device__ inline Entry entry_at(const int64_t* ids, const float* values, uint32_t i, uint32_t cols) {
     const int64_t id = ids[i];
     return {static_cast<int32_t>(id < 0 ? -1 : id < static_cast<int64_t>(cols) ? id : cols),
-            id >= 0 ? values[i] : -__builtin_huge_valf(), __builtin_nanf(""), 0.0f};
+            id >= 0 ? values[i] : -__builtin_huge_valf(), 0.0f, __builtin_nanf("")};
 }
 // Up to 64 entries: every wavefront's own copy of them, one per lane (x in the team's first).
 __device__ inline Entry wave_entry(const int64_t* ids, const float* values, uint32_t k, int lane,
                                    uint32_t cols) {
     const uint32_t i = lane % kWave;
     if (k <= kWave && i < k) return entry_at(ids, values, i, cols);
-    return {-1, -__builtin_huge_valf(), __builtin_nanf(""), 0.0f};
+    return {-1, -__builtin_huge_valf(), 0.0f, __builtin_nanf("")};
 }
 
-// The teacher's row: its entries into `ent`, the normaliser to every thread. *bad: the whole
-// gradient is NaN (a weight is NaN, or an id with weight lies beyond the row). Up to 64 entries
-// (`mine`) every wavefront finds the normaliser for itself, without a barrier.
-template <typename Fmt, int T>
-__device__ inline Teacher teacher_row(Entry* ent, const Entry& mine, const uint8_t* row, uint32_t cols,
+// The teacher's row: its entries into `ent`, the distribution's numbers to every thread. *bad: the
+// whole gradient is NaN (a weight is NaN, or an id with weight lies beyond the row). Up to 64
+// entries (`mine`) every wavefront finds the numbers for itself, without a barrier. With TOTALS
+// the totals too: each the sum of the weights with its id, in the entries' order.
+template <typename Fmt, int T, bool TOTALS>
+__device__ inline Teacher teacher_row(Entry* ent, Entry mine, const uint8_t* row, uint32_t cols,
                                       const int64_t* ids, const float* values, uint32_t k, float scale,
                                       int lane, float (*sh)[4], bool* bad) {
-    float m = -__builtin_huge_valf(), s = 0.0f;
+    const auto beyond = [&](int32_t id, float w) { return id == static_cast<int32_t>(cols) && w != 0.0f; };
+    const auto spread = [](float w, float lw) { return w > 0.0f ? -w * (lw * kLn2) : 0.0f; };
+    float m = -__builtin_huge_valf(), s = 0.0f, h = 0.0f;
     Teacher q;
     if (k <= kWave) {
-        m = lanes_max<kWave>(mine.v);
-        if (m > -__builtin_huge_valf()) s = exp2_f((mine.v - m) * scale);
-        if (mine.v != mine.v) s = mine.v;
+        m = lanes_max<kWave>(mine.w);
+        if (m > -__builtin_huge_valf()) s = exp2_f((mine.w - m) * scale);
+        if (mine.w != mine.w) s = mine.w;
         s = lanes_sum<kWave>(s);
-        q = {s == s ? m : __builtin_nanf(""), log2_f(s)};
-        *bad = __any(s != s || (mine.id == static_cast<int32_t>(cols) && q.weight(mine.v, scale) != 0.0f));
+        q = {s == s ? m : __builtin_nanf(""), log2_f(s), 0.0f};
+        const float lw = q.log_weight(mine.w, scale);
+        mine.w = exp2_f(lw);
+        q.entropy = lanes_sum<kWave>(mine.id < 0 ? 0.0f : spread(mine.w, lw));
+        *bad = __any(s != s || beyond(mine.id, mine.w));
+        if (TOTALS && lane < kWave) {
+#pragma unroll 8
+            for (uint32_t j = 0; j < k; ++j) {
+                const int32_t id = __builtin_amdgcn_readlane(mine.id, static_cast<int>(j));
+                const float w = __uint_as_float(
+                    __builtin_amdgcn_readlane(__float_as_uint(mine.w), static_cast<int>(j)));
+                mine.total += id == mine.id ? w : 0.0f;
+            }
+        }
         if (static_cast<uint32_t>(lane) < k) ent[lane] = mine;
         team_sync<kWave>();
     } else {
-        bool nan = false, beyond = false;
+        bool nan = false, out = false;
         for (uint32_t i = lane; i < k; i += T) {
             const Entry e = entry_at(ids, values, i, cols);
-            ent[i].id = e.id;
-            ent[i].v = e.v;
-            m = max_f(m, e.v);
-            nan |= e.v != e.v;
+            ent[i] = e;
+            m = max_f(m, e.w);
+            nan |= e.w != e.w;
         }
         m = team_reduce<T, true>(m, lane, sh);
         if (m > -__builtin_huge_valf())
-            for (uint32_t i = lane; i < k; i += T) s += exp2_f((ent[i].v - m) * scale);
+            for (uint32_t i = lane; i < k; i += T) s += exp2_f((ent[i].w - m) * scale);
         if (nan) s = __builtin_nanf("");
-        s = team_reduce<T, false>(s, lane, sh);  // also makes the entries visible
-        q = {s == s ? m : __builtin_nanf(""), log2_f(s)};
+        s = team_reduce<T, false>(s, lane, sh);
+        q = {s == s ? m : __builtin_nanf(""), log2_f(s), 0.0f};
         for (uint32_t i = lane; i < k; i += T) {
             const int32_t id = ent[i].id;
-            beyond |= id == static_cast<int32_t>(cols) && q.weight(ent[i].v, scale) != 0.0f;
+            const float lw = q.log_weight(ent[i].w, scale);
+            const float w = exp2_f(lw);
+            ent[i].w = w;
+            out |= beyond(id, w);
+            if (id >= 0) h += spread(w, lw);
             ent[i].x = student_at<Fmt>(row, id, cols);
         }
-        *bad = s != s || team_reduce<T, true>(beyond ? 1.0f : 0.0f, lane, sh) > 0.0f;
+        q.entropy = team_reduce<T, false>(h, lane, sh);
+        // (also makes the weights visible)
+        *bad = s != s || team_reduce<T, true>(out ? 1.0f : 0.0f, lane, sh) > 0.0f;
+        if constexpr (TOTALS) {
+            for (uint32_t i = lane; i < k; i += T) {
+                const int32_t id = ent[i].id;
+                float w = 0.0f;
+#pragma unroll 8
+                for (uint32_t j = 0; j < k; ++j) w += ent[j].id == id ? ent[j].w : 0.0f;
+                ent[i].total = w;
+            }
+        }
     }
     return q;
-}
-
-// The weight of each entry's id: the sum over the entries with that id, in their order.
-template <int T>
-__device__ inline void teacher_weights(Entry* ent, uint32_t k, float scale, const Teacher& q, int lane) {
-    for (uint32_t i = lane; i < k; i += T) {
-        const int32_t id = ent[i].id;
-        float w = 0.0f;
-#pragma unroll 8
-        for (uint32_t j = 0; j < k; ++j)
-            if (ent[j].id == id) w += q.weight(ent[j].v, scale);
-        ent[i].w = w;
-    }
 }
 
 __device__ inline void store_distill(float* stats, uint32_t rows, uint32_t r, float loss, float m,
@@ -1156,19 +1187,19 @@ __device__ inline void store_distill(float* stats, uint32_t rows, uint32_t r, fl
     stats[4 * n + r] = q.l2;
 }
 
-// The loss of a row from its merged statistics (in lane 0 of the team) and log2 of the sum.
+// The loss of a row from its merged statistics and log2 of their sum (in lane 0 of the team).
 template <int T>
 __device__ inline float distill_loss(const Entry* ent, uint32_t k, float scale, const Teacher& q,
                                      const Stat& a, float l2, int lane, float (*sh)[4]) {
     float sum = 0.0f;
     for (uint32_t i = lane; i < k; i += T) {
-        const float lq = fmaf(ent[i].v - q.m, scale, -q.l2);
-        const float w = exp2_f(lq);
-        if (ent[i].id < 0 || w == 0.0f) continue;
-        const float lp = a.s == 0.0f ? -__builtin_huge_valf() : ln_p(ent[i].x, a.m, l2, scale);
-        sum = fmaf(w, fmaf(lq, kLn2, -lp), sum);
+        const Entry e = ent[i];
+        if (e.id < 0 || e.w == 0.0f) continue;
+        const float lp = a.s == 0.0f ? -__builtin_huge_valf() : ln_p(e.x, a.m, l2, scale);
+        sum = fmaf(e.w, lp, sum);
     }
-    return k <= kWave ? lanes_sum<kWave>(sum) : team_reduce<T, false>(sum, lane, sh);
+    sum = k <= kWave ? lanes_sum<kWave>(sum) : team_reduce<T, false>(sum, lane, sh);
+    return -q.entropy - sum;
 }
 
 // The gradient of a row is g (p_j - q_j) / T. The dense part g p_j / T is stored first; after it
@@ -1198,17 +1229,17 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32
                                                            const int64_t* ids_, const float* values_,
                                                            float* stats) {
     __shared__ float sh[T / kWave][4];
-    const uint32_t r = blockIdx.x * kTeamsPerBlock<T> + threadIdx.x / T;
-    const int lane = threadIdx.x % T;
+    const uint32_t r = blockIdx.x * kTeamsPerBlock<T> + team_of<T>();
+    const int lane = lane_of<T>();
     if (r >= rows) return;
     const int64_t* ids = ids_ + static_cast<size_t>(r) * k;
     const float* values = values_ + static_cast<size_t>(r) * k;
     const uint8_t* row = row_ptr<Fmt>(x, r, stride);
-    Entry* ent = s_entries + threadIdx.x / T * k;
+    Entry* ent = s_entries + team_of<T>() * k;
     bool bad;
     Entry mine = wave_entry(ids, values, k, lane, cols);
     if (lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
-    const Teacher q = teacher_row<Fmt, T>(ent, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
+    const Teacher q = teacher_row<Fmt, T, false>(ent, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
@@ -1240,7 +1271,7 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
     bool bad;
     Entry mine = wave_entry(ids, values, k, lane, cols);
     if (lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
-    const Teacher q = teacher_row<Fmt, T>(s_entries, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
+    const Teacher q = teacher_row<Fmt, T, false>(s_entries, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
@@ -1253,26 +1284,26 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
 
 // Tags: columns in (x, ids), teacher entries in values, scale in (stats, g), log2 of the team's
 // lanes and the slices (12 bits above 4) in grad.
-template <typename Fmt>
+template <typename Fmt, bool WIDE>
 __global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t ids_, uint64_t values_,
                                                            uint64_t stats_, uint64_t g, uint64_t grad,
                                                            uint32_t stride, uint32_t rows) {
     const uint32_t cols = tags(x, ids_), k = tag(values_);
     const float scale = __uint_as_float(tags(stats_, g));
-    const uint32_t lg = tag(grad) & 15, slices = tag(grad) >> 4;
-    const uint32_t unit = (blockIdx.x << (8 - lg)) + (threadIdx.x >> lg);
-    const uint32_t want = unit / slices;
+    const uint32_t lg = WIDE ? 8 : tag(grad) & 15, slices = tag(grad) >> 4;
+    const uint32_t unit = WIDE ? blockIdx.x : (blockIdx.x << (8 - lg)) + (threadIdx.x >> lg);
+    const uint32_t want = WIDE ? unit / slices : unit;
     const bool extra = want >= rows;  // keeps the workgroup's barrier whole
     const uint32_t r = extra ? rows - 1 : want;
     const int lane = threadIdx.x & ((1u << lg) - 1);
     const float* stats = addr<const float>(stats_);
     const size_t n = rows;
     const float m = stats[n + r], l2 = stats[2 * n + r];
-    const Teacher q{stats[3 * n + r], stats[4 * n + r]};
+    const Teacher q{stats[3 * n + r], stats[4 * n + r], 0.0f};
     const float coef = addr<const float>(g)[r] * scale * kLn2;
     GradSlice<Fmt> gs(row_ptr<Fmt>(addr<const void>(x), r, stride),
                       const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad), r, cols)), cols,
-                      unit - want * slices, slices);
+                      WIDE ? unit - want * slices : 0, slices);
     if (extra) gs.first = gs.last = 0;
     const bool zero = q.m == -__builtin_huge_valf() || l2 == -__builtin_huge_valf();
     const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
@@ -1297,19 +1328,20 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t 
 // read again, 597 held without that overlap. Tags as for k_ds_grad, but the workgroups of the grid
 // in grad.
 template <typename Fmt, int T, int NV>
-__global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t ids_, uint64_t values_,
+__global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64_t ids_, uint64_t values_,
                                                            uint64_t stats_, uint64_t w, uint64_t grad_,
                                                            uint32_t stride, uint32_t rows) {
-    constexpr int VW = Fmt::VW, U = kUnroll<Fmt, false>;
+    constexpr int VW = Fmt::VW;
+    constexpr int U = NV > 8 ? kUnroll<Fmt, false> / 2 : kUnroll<Fmt, false>;  // 128 registers suffice
     static_assert(NV % U == 0, "whole steps");
     __shared__ float sh[T / kWave][4];
     const uint32_t cols = tags(x, ids_), k = tag(values_), teams = tag(grad_) * kTeamsPerBlock<T>;
     const float scale = __uint_as_float(tags(stats_, w));
-    const int lane = threadIdx.x % T;
-    uint32_t r = blockIdx.x * kTeamsPerBlock<T> + threadIdx.x / T;
+    const int lane = lane_of<T>();
+    uint32_t r = blockIdx.x * kTeamsPerBlock<T> + team_of<T>();
     if (r >= rows) return;
     // the entries of two rows: a wavefront may be one row ahead of another
-    Entry* ent = s_entries + threadIdx.x / T * 2 * k;
+    Entry* ent = s_entries + team_of<T>() * 2 * k;
     Entry* other = ent + k;
     const auto ids_at = [&](uint32_t n) { return addr<const int64_t>(ids_) + static_cast<size_t>(n) * k; };
     const auto values_at = [&](uint32_t n) { return addr<const float>(values_) + static_cast<size_t>(n) * k; };
@@ -1331,8 +1363,8 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t 
         uint8_t* out = const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad_), r, cols));
         const Span<Fmt> sp(row, cols);
         bool bad;
-        const Teacher q = teacher_row<Fmt, T>(ent, mine, row, cols, ids_at(r), values_at(r), k, scale, lane,
-                                              sh, &bad);
+        const Teacher q = teacher_row<Fmt, T, true>(ent, mine, row, cols, ids_at(r), values_at(r), k, scale,
+                                                    lane, sh, &bad);
         const bool absent = q.m == -__builtin_huge_valf();
         float loss = 0.0f, l2 = 0.0f;
         Stat a{0.0f, 0.0f, 0.0f};
@@ -1358,7 +1390,6 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t 
                     take<false>(e, scale, a);
                 }
             }
-            teacher_weights<T>(ent, k, scale, q, lane);
             if (rest < sp.vb) scan_on<Fmt, false, T, U>(sp, rest, sp.vb, lane, scale, a);
             team_merge<false, T>(a, scale, lane, sh);
             l2 = bad ? __builtin_nanf("") : log2_f(a.s);
@@ -1410,7 +1441,7 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_step(uint64_t x, uint64_t 
                 const uint32_t owner = v >= sp.va && v < sp.vb ? (v - sp.va) % T / kWave : 0;
                 if (owner != static_cast<uint32_t>(lane) / kWave) continue;
                 const float p = exp2_f(fmaf(e.x - a.m, scale, -l2));
-                reinterpret_cast<typename Fmt::Bits*>(out)[e.id] = round_to<Fmt>(coef * (p - e.w));
+                reinterpret_cast<typename Fmt::Bits*>(out)[e.id] = round_to<Fmt>(coef * (p - e.total));
             }
         }
         if (next >= rows) return;
@@ -1527,11 +1558,13 @@ hipError_t launch_logprobs_grad(const GradPlan& plan, const LogitsArgs& a, const
     with_format(a.dtype, [&](auto fmt) {
         using Fmt = decltype(fmt);
         with_bool(g_entropy != nullptr, [&](auto ent) {
-            launch(k_lp_grad<Fmt, decltype(ent)::value>, static_cast<uint32_t>(plan.grid_blocks),
-                   kBlockThreads, s, tagged(a.x, cols), tagged(tokens, cols >> 16), tagged(stats, sc),
-                   tagged(g_logprob, sc >> 16), tagged(g_entropy, plan.slices),
-                   tagged(grad, log2_of(plan.team)), static_cast<uint32_t>(a.row_stride),
-                   static_cast<uint32_t>(a.rows));
+            with_bool(plan.team == kBlockThreads, [&](auto wide) {
+                launch(k_lp_grad<Fmt, decltype(ent)::value, decltype(wide)::value>,
+                       static_cast<uint32_t>(plan.grid_blocks), kBlockThreads, s, tagged(a.x, cols),
+                       tagged(tokens, cols >> 16), tagged(stats, sc), tagged(g_logprob, sc >> 16),
+                       tagged(g_entropy, plan.slices), tagged(grad, log2_of(plan.team)),
+                       static_cast<uint32_t>(a.row_stride), static_cast<uint32_t>(a.rows));
+            });
         });
     });
     return hipGetLastError();
@@ -1543,10 +1576,13 @@ hipError_t launch_distill_grad(const GradPlan& plan, const LogitsArgs& a, int k,
     const uint32_t cols = static_cast<uint32_t>(a.cols), sc = bits_of(a.scale);
     with_format(a.dtype, [&](auto fmt) {
         using Fmt = decltype(fmt);
-        launch(k_ds_grad<Fmt>, static_cast<uint32_t>(plan.grid_blocks), kBlockThreads, s,
-               tagged(a.x, cols), tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
-               tagged(g_loss, sc >> 16), tagged(grad, log2_of(plan.team) | (plan.slices << 4)),
-               static_cast<uint32_t>(a.row_stride), static_cast<uint32_t>(a.rows));
+        with_bool(plan.team == kBlockThreads, [&](auto wide) {
+            launch(k_ds_grad<Fmt, decltype(wide)::value>, static_cast<uint32_t>(plan.grid_blocks),
+                   kBlockThreads, s, tagged(a.x, cols), tagged(ids, cols >> 16), tagged(values, k),
+                   tagged(stats, sc), tagged(g_loss, sc >> 16),
+                   tagged(grad, log2_of(plan.team) | (plan.slices << 4)),
+                   static_cast<uint32_t>(a.row_stride), static_cast<uint32_t>(a.rows));
+        });
     });
     return hipGetLastError();
 }
@@ -1575,9 +1611,8 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
                        tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
                        tagged(weights, sc >> 16), tagged(grad, grid), stride, rows);
             };
-            // 8 vectors per lane, or 16 for the rows that do not fit (T = 1024 alone has such)
-            if (grad != nullptr && T == 1024 && plan.held > 8)
-                step(Int<T == 1024 ? 16 : 8>{});
+            if (grad != nullptr && T >= 512 && plan.held > 8)
+                step(Int<T >= 512 ? 16 : 8>{});
             else if (grad != nullptr)
                 step(Int<8>{});
             else

@@ -97,7 +97,6 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, bool vec_ro
     *p = LogitsPlan{};
     p->device_threads = cap;
     p->parts = 1;
-    p->held = vecs > 8 * 1024 ? 16 : 8;
     const bool logprobs = use == kLogprobs || use == kLogprobsTop;
     const int64_t held = vec_rows ? ceil_div(cols * es, 16) : vecs;  // vectors a row lies in
     if (held <= 32 && logprobs) {
@@ -134,7 +133,14 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, bool vec_ro
     }
     p->path = ARGREDUCE_PATH_BLOCK;
     if (use == kDistillStep)
-        p->team = vecs <= 8 * 256 ? 256 : vecs <= 8 * 512 ? 512 : 1024;  // what the registers hold
+        // One workgroup per CU where there are no more rows than CUs; else 8 vectors per lane of the
+        // fewest lanes that hold the row, then 16. Measured with 64 entries, lanes x vectors: [4096,
+        // 16000] bf16 256 x 8 59 us, 512 x 8 83; [8192,30000] 512 x 8 255, 256 x 16 264, 1024 x 8
+        // 381; [4096,60000] 512 x 16 245, 1024 x 8 263; [4096,128256] 1024 x 16 477, 512 x 16 544.
+        p->team = rows1 * kThreadsPerCu <= cap && vecs > 8 * 256 ? 1024
+                  : vecs <= 8 * 256                             ? 256
+                  : vecs <= 16 * 512                            ? 512
+                                                                : 1024;
     else if (vecs > 2048 && rows1 * 1024 <= cap)
         p->team = 1024;  // the whole device in one wave of workgroups
     else
@@ -143,6 +149,7 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, bool vec_ro
     if (rows1 * p->team >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
     if (use == kDistillStep) {
         const int64_t most = step_blocks(cap, p->team);
+        p->held = vecs > 8 * p->team ? 16 : 8;
         p->grid_blocks = rows1 < most ? rows1 : most;
     }
     return ARGREDUCE_OK;
