@@ -201,7 +201,10 @@ __device__ inline float team_reduce(float v, int lane, float (*sh)[4]) {
 // not ("edges", lanes 0 and 1). An edge vector is read whole: it holds a byte of the row, so
 // it lies in a mapped page.
 
-template <typename Fmt>
+// KEEP: ordinary loads, which leave the logits in the Infinity Cache for a gradient call to read;
+// else nontemporal ones, for logits too large for it. [257,32003] f32, forward and gradient: 7.2 +
+// 10.7 us kept, 7.2 + 14.1 not; [2048,128256] bf16: 136 + 178 kept, 97 + 193 not.
+template <typename Fmt, bool KEEP = false>
 struct Span {
     const uint8_t* base;
     uint32_t off, cols, vs, va, vb;
@@ -222,15 +225,16 @@ struct Span {
         return (lane == 1 && (off + cols) % Fmt::VW && (vs > 1 || !off)) ? vs - 1 : kNoVec;
     }
     __device__ const uint8_t* at(uint32_t v) const { return base + static_cast<size_t>(v) * 16; }
+    __device__ typename Fmt::Vec load(uint32_t v) const {
+        const auto* p = reinterpret_cast<const typename Fmt::Vec*>(at(v));
+        if constexpr (KEEP)
+            return *p;
+        else
+            return __builtin_nontemporal_load(p);
+    }
     // Position of element 0 of vector v (wraps for elements before the row).
     __device__ uint32_t pos(uint32_t v) const { return v * Fmt::VW - off; }
 };
-
-// Nontemporal: [2048,128256] bf16 took 94-96 us with ordinary loads, 86 with these (T = 512).
-template <typename Fmt>
-__device__ inline typename Fmt::Vec load16(const uint8_t* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const typename Fmt::Vec*>(p));
-}
 
 // A vector of -inf.
 template <typename Fmt>
@@ -269,31 +273,31 @@ __device__ inline float take(const float (&e)[N], float k, Stat& a, float m = kL
     return m;
 }
 
-// Loads vectors v, v + T, ... (U of them) as floats; unless FULL, those at or past `last` as -inf.
-template <typename Fmt, int T, int U, bool FULL>
-__device__ inline void load_step(const Span<Fmt>& sp, uint32_t v, uint32_t last,
-                                 float (&e)[U * Fmt::VW]) {
-    constexpr int VW = Fmt::VW;
-    typename Fmt::Vec q[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) q[u] = load16<Fmt>(sp.at(FULL || v + u * T < last ? v + u * T : last - 1));
+template <typename Fmt, int U>
+__device__ inline void unpack_all(const typename Fmt::Vec (&q)[U], float (&e)[U * Fmt::VW]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if constexpr (!FULL) q[u] = masked_unless<Fmt>(v + u * T < last, q[u]);
-        float f[VW];
+        float f[Fmt::VW];
         Fmt::unpack(q[u], f);
 #pragma unroll
-        for (int i = 0; i < VW; ++i) e[u * VW + i] = f[i];
+        for (int i = 0; i < Fmt::VW; ++i) e[u * Fmt::VW + i] = f[i];
     }
+}
+template <int N>
+__device__ inline float max_of(const float (&e)[N]) {
+    float m = e[0];
+#pragma unroll
+    for (int i = 1; i + 1 < N; i += 2) m = max3_f(m, e[i], e[i + 1]);
+    return N % 2 ? m : max_f(m, e[N - 1]);
 }
 
 // The edge vector of lane 0 or 1.
-template <typename Fmt, bool ENT>
-__device__ inline void scan_edge(const Span<Fmt>& sp, int lane, float k, Stat& a) {
+template <typename Fmt, bool ENT, typename Sp>
+__device__ inline void scan_edge(const Sp& sp, int lane, float k, Stat& a) {
     const uint32_t v = sp.edge(lane);
     if (v == kNoVec) return;
     float e[Fmt::VW];
-    Fmt::unpack(load16<Fmt>(sp.at(v)), e);
+    Fmt::unpack(sp.load(v), e);
     const uint32_t p0 = sp.pos(v);
 #pragma unroll
     for (int i = 0; i < Fmt::VW; ++i) e[i] = p0 + i < sp.cols ? e[i] : -__builtin_huge_valf();
@@ -338,63 +342,80 @@ struct Segments {
 };
 
 // One lane's share of a row: its edge vector (scan_span), then vectors first + lane, + T, ... below
-// last in steps of U, the last step filled up with -inf. With SEG the maxima of g's segments go to
-// seg[].
-template <typename Fmt, bool ENT, int T, int U, bool SEG = false>
-__device__ inline void scan_on(const Span<Fmt>& sp, uint32_t first, uint32_t last, int lane, float k,
-                               Stat& a, const Segments& g = Segments{}, float* seg = nullptr) {
+// last: in steps of U vectors, and the last, incomplete step one by one, lanes past the end with
+// -inf. With SEG the maxima of g's segments go to seg[].
+template <typename Fmt, bool ENT, int T, int U, bool SEG = false, typename Sp>
+__device__ inline void scan_on(const Sp& sp, uint32_t first, uint32_t last, int lane, float k, Stat& a,
+                               const Segments& g = Segments{}, float* seg = nullptr) {
     constexpr int VW = Fmt::VW;
-    float m = kLowest;
+    using Vec = typename Fmt::Vec;
+    float m = kLowest;  // of the running group of segments
     uint32_t left = g.group, at = lane / 8;
-    const auto step = [&](const float (&e)[U * VW], uint32_t base) {
+    const auto vector_max = [&](const float(&f)[VW], uint32_t i) {  // segments of one or eight vectors
+        float v = max_of(f);
+        if (g.lg_vecs) v = lanes_max<8>(v);
+        if (i < last - first && (i & ((1u << g.lg_vecs) - 1)) == 0) seg[i >> g.lg_vecs] = v;
+    };
+    const auto group_max = [&] {
+        m = lanes_max<8>(m);
+        if (lane % 8 == 0) seg[at] = m;
+        m = kLowest;
+        left = g.group;
+        at += T / 8;
+    };
+    uint32_t base = first;
+    for (; last - base >= U * T; base += U * T) {
+        Vec q[U];
+        float e[U * VW];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = sp.load(base + lane + u * T);
+        unpack_all<Fmt, U>(q, e);
         if constexpr (SEG) {
             if (g.group == 0) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const uint32_t i = base - first + lane + u * T;
-                    float v = e[u * VW];
-#pragma unroll
-                    for (int j = 1; j + 1 < VW; j += 2) v = max3_f(v, e[u * VW + j], e[u * VW + j + 1]);
-                    v = max_f(v, e[u * VW + VW - 1]);
-                    if (g.lg_vecs) v = lanes_max<8>(v);
-                    if (i < last - first && (i & ((1u << g.lg_vecs) - 1)) == 0) seg[i >> g.lg_vecs] = v;
+                    float f[VW];
+                    Fmt::unpack(q[u], f);
+                    vector_max(f, base - first + lane + u * T);
                 }
                 take<ENT>(e, k, a);
             } else {
                 m = take<ENT>(e, k, a, m);
                 left -= U;
-                if (left == 0) {
-                    m = lanes_max<8>(m);
-                    if (lane % 8 == 0) seg[at] = m;
-                    m = kLowest;
-                    left = g.group;
-                    at += T / 8;
-                }
+                if (left == 0) group_max();
             }
         } else {
             take<ENT>(e, k, a);
         }
-    };
-    const uint32_t whole = first + (last - first) / (U * T) * (U * T);
-    float e[U * VW];
-    for (uint32_t base = first; base < whole; base += U * T) {
-        load_step<Fmt, T, U, true>(sp, base + lane, last, e);
-        step(e, base);
     }
-    if (whole < last) {
-        load_step<Fmt, T, U, false>(sp, whole + lane, last, e);
-        step(e, whole);
+    if (base < last) {
+        Vec q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t v = base + lane + u * T;
+            if (base + u * T < last) q[u] = sp.load(v < last ? v : last - 1);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (base + u * T < last) {
+                float f[VW];
+                Fmt::unpack(masked_unless<Fmt>(base + lane + u * T < last, q[u]), f);
+                if constexpr (SEG) {
+                    if (g.group == 0) vector_max(f, base - first + lane + u * T);
+                    m = take<ENT>(f, k, a, g.group ? m : kLowest);
+                } else {
+                    take<ENT>(f, k, a);
+                }
+            }
+        }
+        if constexpr (SEG) left = 0;
     }
     if constexpr (SEG)
-        if (left != g.group) {
-            m = lanes_max<8>(m);
-            if (lane % 8 == 0) seg[at] = m;
-        }
+        if (g.group != 0 && left != g.group) group_max();
 }
-template <typename Fmt, bool ENT, int T, int U, bool SEG = false>
-__device__ inline void scan_span(const Span<Fmt>& sp, bool edges, uint32_t first, uint32_t last,
-                                 int lane, float k, Stat& a, const Segments& g = Segments{},
-                                 float* seg = nullptr) {
+template <typename Fmt, bool ENT, int T, int U, bool SEG = false, typename Sp>
+__device__ inline void scan_span(const Sp& sp, bool edges, uint32_t first, uint32_t last, int lane,
+                                 float k, Stat& a, const Segments& g = Segments{}, float* seg = nullptr) {
     a.init();
     if (edges && lane < 2) scan_edge<Fmt, ENT>(sp, lane, k, a);
     scan_on<Fmt, ENT, T, U, SEG>(sp, first, last, lane, k, a, g, seg);
@@ -550,8 +571,8 @@ __device__ inline float kth_bound(const float* seg, uint32_t segs, uint32_t k, i
 
 // `segs` maxima are in L.seg. `vec(seg, i)` names vector i (of 2^lg_seg) of a segment, or kNoVec.
 // Leaves the k best (fewer if the row has fewer) in L.buf, their number in L.count.
-template <typename Fmt, int T, int S, typename VecOf>
-__device__ inline void top_select(TopLds<T, S>& L, const Span<Fmt>& sp, uint32_t segs,
+template <typename Fmt, int T, int S, typename Sp, typename VecOf>
+__device__ inline void top_select(TopLds<T, S>& L, const Sp& sp, uint32_t segs,
                                   uint32_t lg_seg, uint32_t k, int lane, VecOf vec) {
     constexpr int VW = Fmt::VW;
     constexpr int U = 4;  // vectors a thread reads at once
@@ -579,11 +600,7 @@ __device__ inline void top_select(TopLds<T, S>& L, const Span<Fmt>& sp, uint32_t
     const auto visit = [&](const typename Fmt::Vec& q, uint32_t v, uint64_t least, bool bounded) {
         float e[VW];
         Fmt::unpack(q, e);
-        float m = e[0];
-#pragma unroll
-        for (int i = 1; i + 1 < VW; i += 2) m = max3_f(m, e[i], e[i + 1]);
-        m = max_f(m, e[VW - 1]);
-        if (v == kNoVec || !(m >= tau)) return;
+        if (v == kNoVec || !(max_of(e) >= tau)) return;
         const uint32_t p0 = sp.pos(v);
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
@@ -602,7 +619,7 @@ __device__ inline void top_select(TopLds<T, S>& L, const Span<Fmt>& sp, uint32_t
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             v[u] = item_vec(it + u * T);
-            q[u] = load16<Fmt>(sp.at(v[u] == kNoVec ? 0 : v[u]));  // vector 0 can always be read
+            q[u] = sp.load(v[u] == kNoVec ? 0 : v[u]);  // vector 0 can always be read
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -620,7 +637,7 @@ __device__ inline void top_select(TopLds<T, S>& L, const Span<Fmt>& sp, uint32_t
             team_sync<T>();
             if (static_cast<uint32_t>(lane) < kStep) {
                 const uint32_t v = item_vec(base + lane);
-                visit(load16<Fmt>(sp.at(v == kNoVec ? 0 : v)), v, least, false);
+                visit(sp.load(v == kNoVec ? 0 : v), v, least, false);
             }
         }
         team_sync<T>();
@@ -694,7 +711,7 @@ __device__ inline const uint8_t* row_ptr(const void* x, uint32_t r, uint32_t str
 
 // Rows of at most G vectors, G lanes each, the row held in registers: maximum first, then the
 // exponentials. Alternatives are taken one by one, as the largest key left.
-template <typename Fmt, bool ENT, int G>
+template <typename Fmt, bool KEEP, bool ENT, int G>
 __global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint32_t cols,
                                                             uint32_t stride, float scale,
                                                             uint32_t rows, const int64_t* tokens,
@@ -708,12 +725,12 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint3
     const uint8_t* row = row_ptr<Fmt>(x, r, stride);
     const int64_t t = tokens[r];
     const bool live = t >= 0;
-    const Span<Fmt> sp(row, cols);
+    const Span<Fmt, KEEP> sp(row, cols);
     float e[VW];
 #pragma unroll
     for (int i = 0; i < VW; ++i) e[i] = -__builtin_huge_valf();
     if (live && static_cast<uint32_t>(lane) < sp.vs) {
-        Fmt::unpack(load16<Fmt>(sp.at(lane)), e);
+        Fmt::unpack(sp.load(lane), e);
         const uint32_t p0 = sp.pos(lane);
 #pragma unroll
         for (int i = 0; i < VW; ++i) e[i] = p0 + i < cols ? e[i] : -__builtin_huge_valf();
@@ -768,7 +785,7 @@ template <int T>
 constexpr int kSegs = T == kWave ? 256 : 1024;
 
 // A team of T lanes per row.
-template <typename Fmt, bool ENT, bool TOP, int T>
+template <typename Fmt, bool KEEP, bool ENT, bool TOP, int T>
 __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32_t cols,
                                                            uint32_t stride, float scale,
                                                            uint32_t rows, const int64_t* tokens,
@@ -793,7 +810,7 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32
     }
     const uint8_t* row = row_ptr<Fmt>(x, r, stride);
     const float xt = load_at<Fmt>(row, t, cols);
-    const Span<Fmt> sp(row, cols);
+    const Span<Fmt, KEEP> sp(row, cols);
     Stat a;
     auto& L = lds[TOP ? team : 0];
     const Segments g = Segments::cut<T, U>(sp.va, sp.vb, kSegs<T>);
@@ -825,7 +842,7 @@ struct Part {  // what a slice leaves in scratch
     float oct_max[kPartThreads / 8];  // of every eight lanes
 };
 
-template <typename Fmt, bool ENT>
+template <typename Fmt, bool KEEP, bool ENT>
 __global__ __launch_bounds__(kPartThreads) void k_part(const void* x, uint32_t cols, uint32_t stride,
                                                        float scale, uint32_t parts,
                                                        const int64_t* tokens, Part* out) {
@@ -833,7 +850,7 @@ __global__ __launch_bounds__(kPartThreads) void k_part(const void* x, uint32_t c
     const uint32_t r = blockIdx.x / parts;
     const uint32_t b = blockIdx.x - r * parts;
     if (tokens != nullptr && tokens[r] < 0) return;
-    const Span<Fmt> sp(row_ptr<Fmt>(x, r, stride), cols);
+    const Span<Fmt, KEEP> sp(row_ptr<Fmt>(x, r, stride), cols);
     const uint32_t n = part_vecs(span_max<Fmt>(cols), parts);
     uint32_t first = sp.va + b * n;
     first = first < sp.vb ? first : sp.vb;
@@ -1222,7 +1239,7 @@ __device__ inline void distill_take_off(const uint8_t* x, uint8_t* g, uint32_t c
     }
 }
 
-template <typename Fmt, int T>
+template <typename Fmt, bool KEEP, int T>
 __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32_t cols,
                                                            uint32_t stride, float scale,
                                                            uint32_t rows, uint32_t k,
@@ -1244,7 +1261,7 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
     }
-    const Span<Fmt> sp(row, cols);
+    const Span<Fmt, KEEP> sp(row, cols);
     Stat a;
     scan_span<Fmt, false, T, kUnroll<Fmt, false>>(sp, true, sp.va, sp.vb, lane, scale, a);
     team_merge<false, T>(a, scale, lane, sh);
@@ -1349,7 +1366,7 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
     typename Fmt::Vec held[NV];
     const auto load = [&](const Span<Fmt>& sp, int i) {
         const uint32_t v = sp.va + lane + i * T;
-        held[i] = load16<Fmt>(sp.at(v < sp.vb ? v : sp.vs - 1));  // of any row a readable vector
+        if (sp.va + i * T < sp.vb) held[i] = sp.load(v < sp.vb ? v : sp.vb - 1);
     };
     Entry mine = wave_entry(ids_at(r), values_at(r), k, lane, cols);
     {
@@ -1375,19 +1392,22 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
             if (lane < 2) scan_edge<Fmt, false>(sp, lane, scale, a);
 #pragma unroll
             for (int i = 0; i < NV; i += U) {
-                if (sp.va + i * T < sp.vb) {
+                if (sp.vb - sp.va >= (i + U) * T) {
+                    typename Fmt::Vec h[U];
                     float e[U * VW];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        typename Fmt::Vec h = held[i + u];
-                        if (sp.va + (i + U) * T > sp.vb)
-                            h = masked_unless<Fmt>(sp.va + lane + (i + u) * T < sp.vb, h);
-                        float f[VW];
-                        Fmt::unpack(h, f);
-#pragma unroll
-                        for (int j = 0; j < VW; ++j) e[u * VW + j] = f[j];
-                    }
+                    for (int u = 0; u < U; ++u) h[u] = held[i + u];
+                    unpack_all<Fmt, U>(h, e);
                     take<false>(e, scale, a);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (sp.va + (i + u) * T < sp.vb) {
+                            float f[VW];
+                            Fmt::unpack(masked_unless<Fmt>(sp.va + lane + (i + u) * T < sp.vb, held[i + u]), f);
+                            take<false>(f, scale, a);
+                        }
+                    }
                 }
             }
             if (rest < sp.vb) scan_on<Fmt, false, T, U>(sp, rest, sp.vb, lane, scale, a);
@@ -1419,7 +1439,7 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
             if (v < sp.vb) write(held[i], v);
             if (next < rows) load(np, i);
         }
-        for (uint32_t v = rest + lane; v < sp.vb; v += T) write(load16<Fmt>(sp.at(v)), v);
+        for (uint32_t v = rest + lane; v < sp.vb; v += T) write(sp.load(v), v);
         const uint32_t ev = sp.edge(lane);
         if (ev != kNoVec) {
             const uint32_t p0 = sp.pos(ev);
@@ -1484,10 +1504,11 @@ void with_bool(bool b, F f) {
         f(Int<0>{});
 }
 
-uint32_t team_blocks(int64_t rows, int team) {
-    const int64_t per = team == kWave ? kBlockThreads / kWave : 1;
-    return static_cast<uint32_t>((rows + per - 1) / per);
+template <typename F>
+void with_format_and_keep(const LogitsArgs& a, F f) {
+    with_format(a.dtype, [&](auto fmt) { with_bool(a.keep, [&](auto keep) { f(fmt, keep); }); });
 }
+
 uint32_t log2_of(int v) { return static_cast<uint32_t>(__builtin_ctz(static_cast<unsigned>(v))); }
 
 template <typename... KArgs, typename... Args>
@@ -1511,13 +1532,14 @@ hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const in
     const uint32_t cols = static_cast<uint32_t>(a.cols), stride = static_cast<uint32_t>(a.row_stride);
     const uint32_t rows = static_cast<uint32_t>(a.rows);
     const uint32_t grid = static_cast<uint32_t>(plan.grid_blocks);
-    with_format(a.dtype, [&](auto fmt) {
+    with_format_and_keep(a, [&](auto fmt, auto keep) {
         using Fmt = decltype(fmt);
+        constexpr bool KEEP = decltype(keep)::value;
         with_bool(entropy, [&](auto ent) {
             constexpr bool ENT = decltype(ent)::value;
             if (plan.path == ARGREDUCE_PATH_SUBWAVE && plan.team < kWave) {
                 const auto go = [&](auto g) {
-                    launch(k_lp_group<Fmt, ENT, decltype(g)::value>, grid, kBlockThreads, s, a.x, cols,
+                    launch(k_lp_group<Fmt, KEEP, ENT, decltype(g)::value>, grid, kBlockThreads, s, a.x, cols,
                            stride, a.scale, rows, tokens, stats, tagged(top_logprobs, top), top_tokens);
                 };
                 switch (plan.team) {
@@ -1532,7 +1554,7 @@ hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const in
                 constexpr bool TOP = decltype(tp)::value;
                 if (plan.path == ARGREDUCE_PATH_SPLIT) {
                     Part* part = reinterpret_cast<Part*>(scratch16);
-                    launch(k_part<Fmt, ENT>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
+                    launch(k_part<Fmt, KEEP, ENT>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
                            static_cast<uint32_t>(plan.parts), tokens, part);
                     const uint32_t sc = bits_of(a.scale);
                     launch(k_lp_merge<Fmt, ENT, TOP>, rows, TOP ? kMergeTopThreads : kMergeThreads, s, tagged(a.x, cols),
@@ -1542,7 +1564,7 @@ hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const in
                 }
                 with_team(plan.team, [&](auto team) {
                     constexpr int T = decltype(team)::value;
-                    launch(k_lp_team<Fmt, ENT, TOP, T>, grid, kTeamBlock<T>, s, a.x, cols, stride,
+                    launch(k_lp_team<Fmt, KEEP, ENT, TOP, T>, grid, kTeamBlock<T>, s, a.x, cols, stride,
                            a.scale, rows, tokens, stats, tagged(top_logprobs, top), top_tokens);
                 });
             });
@@ -1593,11 +1615,12 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
     const uint32_t cols = static_cast<uint32_t>(a.cols), stride = static_cast<uint32_t>(a.row_stride);
     const uint32_t rows = static_cast<uint32_t>(a.rows), sc = bits_of(a.scale);
     const uint32_t grid = static_cast<uint32_t>(plan.grid_blocks);
-    with_format(a.dtype, [&](auto fmt) {
+    with_format_and_keep(a, [&](auto fmt, auto keep) {
         using Fmt = decltype(fmt);
+        constexpr bool KEEP = decltype(keep)::value;
         if (plan.path == ARGREDUCE_PATH_SPLIT) {
             Part* part = reinterpret_cast<Part*>(scratch16);
-            launch(k_part<Fmt, false>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
+            launch(k_part<Fmt, KEEP, false>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
                    static_cast<uint32_t>(plan.parts), static_cast<const int64_t*>(nullptr), part);
             launch_entries(k_ds_merge<Fmt>, rows, kMergeThreads, k, s, a.x, cols, stride, a.scale, rows,
                    tagged(ids, k), tagged(values, plan.parts), static_cast<const Part*>(part), stats);
@@ -1616,7 +1639,7 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
             else if (grad != nullptr)
                 step(Int<8>{});
             else
-                launch_entries(k_ds_team<Fmt, T>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k, s, a.x, cols, stride, a.scale, rows,
+                launch_entries(k_ds_team<Fmt, KEEP, T>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k, s, a.x, cols, stride, a.scale, rows,
                        static_cast<uint32_t>(k), ids, values, stats);
         });
     });

@@ -34,12 +34,14 @@ struct GradPlan {
     int64_t grid_blocks;
 };
 
-// Logits of one call. `scale` is log2(e) / temperature.
+// Logits of one call. `scale` is log2(e) / temperature; `keep`: read them so that they stay in the
+// Infinity Cache.
 struct LogitsArgs {
     const void* x;
     int dtype;
     int64_t rows, cols, row_stride;
     float scale;
+    bool keep;
 };
 
 size_t part_bytes();  // scratch of one slice of a split row

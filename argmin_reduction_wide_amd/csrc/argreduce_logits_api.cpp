@@ -15,6 +15,9 @@ namespace {
 
 constexpr int64_t kBlock = 256;
 constexpr int64_t kThreadsPerCu = 2048;
+// Logits of up to this size are left in the 256 MiB Infinity Cache (struct Span; at 125 MiB, [512,128256]
+// f16, the forward pass takes 25.7 us with them left there, 23.0 without).
+constexpr int64_t kKeepBytes = int64_t{64} << 20;
 constexpr int64_t kMaxGridThreads = int64_t{1} << 32;  // threads a launch's grid may hold
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -56,7 +59,8 @@ int check_logits(const void* x, int dtype, int64_t rows, int64_t cols, int64_t s
     if (rows > 0 && (x == nullptr || reinterpret_cast<uintptr_t>(x) % logits_elem_size(dtype) != 0))
         return ARGREDUCE_ERR_INVALID_ARG;
     *a = LogitsArgs{x, dtype, rows, cols, rows > 1 ? stride : cols,
-                    static_cast<float>(1.4426950408889634 / static_cast<double>(temperature))};
+                    static_cast<float>(1.4426950408889634 / static_cast<double>(temperature)),
+                    rows * cols * logits_elem_size(dtype) <= kKeepBytes};
     return ARGREDUCE_OK;
 }
 
@@ -74,6 +78,9 @@ int64_t step_blocks(int64_t cap, int team) {
     return per_cu * cus < 65535 ? per_cu * cus : 65535;
 }
 
+// Teacher entries, at most, of a row left to one wavefront.
+constexpr int kWaveEntries = 256;
+
 // What a plan is for.
 enum Use { kLogprobs, kLogprobsTop, kDistill, kDistillStep };
 
@@ -84,7 +91,8 @@ constexpr int64_t kOneBlockStepVecs = 16384;
 
 // Scratch depends on the shape alone, so only the choices among plans without any go by
 // `vec_rows` (every row starts on a 16-byte boundary).
-int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, bool vec_rows, LogitsPlan* p) {
+// `k`: teacher entries (0: none).
+int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool vec_rows, LogitsPlan* p) {
     int rc = check_logits_shape(dtype, rows, cols);
     if (rc != ARGREDUCE_OK) return rc;
     int64_t cap = 0;
@@ -106,13 +114,17 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, bool vec_ro
         if (rows1 * p->team >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
         return ARGREDUCE_OK;
     }
-    if (vecs <= 256) {
+    // a wavefront per row: up to four vectors per lane; in a distillation step up to the eight that
+    // it holds ([19940,2312] f16, 291 vectors: 256 lanes 152 us, see the step's figures below)
+    // (not with so many entries that four rows' would fill the LDS)
+    if (vecs <= (use == kDistillStep ? 512 : 256) && k <= kWaveEntries) {
         p->path = ARGREDUCE_PATH_SUBWAVE;
         p->team = 64;
         p->grid_blocks = ceil_div(rows1, kBlock / 64);
         if (rows1 * 64 >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
         if (use == kDistillStep) {
             const int64_t most = step_blocks(cap, p->team);
+            p->held = 8;
             p->grid_blocks = p->grid_blocks < most ? p->grid_blocks : most;
         }
         return ARGREDUCE_OK;
@@ -219,7 +231,7 @@ int distill(const LogitsArgs& a, int32_t k, const int64_t* ids, const float* val
             const float* weights, void* grad, void* scratch, size_t scratch_bytes, void* stream) {
     LogitsPlan p;
     GradPlan g;
-    int rc = make_logits_plan(a.dtype, a.rows, a.cols, grad != nullptr ? kDistillStep : kDistill, vec_rows(a), &p);
+    int rc = make_logits_plan(a.dtype, a.rows, a.cols, grad != nullptr ? kDistillStep : kDistill, k, vec_rows(a), &p);
     if (rc != ARGREDUCE_OK) return rc;
     rc = make_grad_plan(a.dtype, a.rows, a.cols, &g);
     if (rc != ARGREDUCE_OK) return rc;
@@ -240,7 +252,7 @@ using argreduce::LogitsPlan;
 ARGREDUCE_EXPORT size_t argreduce_logprobs_scratch_bytes(int64_t rows, int64_t cols,
                                                          argreduce_dtype_t dtype) {
     LogitsPlan p;
-    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p) != ARGREDUCE_OK)
+    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, 0, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p) != ARGREDUCE_OK)
         return std::numeric_limits<size_t>::max();
     return p.scratch_bytes;
 }
@@ -249,7 +261,7 @@ ARGREDUCE_EXPORT int argreduce_logprobs_plan(int64_t rows, int64_t cols, argredu
                                              argreduce_plan_t* out) {
     if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
     LogitsPlan p;
-    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p);
+    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, 0, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p);
     if (rc != ARGREDUCE_OK) return rc;
     argreduce::fill_logits_plan(p, p.parts > 1 ? 2 : 1, out);
     return ARGREDUCE_OK;
@@ -269,7 +281,7 @@ ARGREDUCE_EXPORT int argreduce_logprobs(const void* x, argreduce_dtype_t dtype, 
     if (!fits48(x) || !usable(tokens, 8) || !usable(stats, 4)) return ARGREDUCE_ERR_INVALID_ARG;
     if (top > 0 && (!usable(top_logprobs, 4) || !usable(top_tokens, 8))) return ARGREDUCE_ERR_INVALID_ARG;
     LogitsPlan p;
-    rc = make_logits_plan(dtype, rows, cols, top > 0 ? kLogprobsTop : kLogprobs, vec_rows(a), &p);
+    rc = make_logits_plan(dtype, rows, cols, top > 0 ? kLogprobsTop : kLogprobs, 0, vec_rows(a), &p);
     if (rc != ARGREDUCE_OK) return rc;
     uint8_t* scratch16 = nullptr;
     rc = scratch_of(p, scratch, scratch_bytes, &scratch16);
@@ -303,7 +315,7 @@ ARGREDUCE_EXPORT int argreduce_logprobs_grad(const void* x, argreduce_dtype_t dt
 ARGREDUCE_EXPORT size_t argreduce_distill_scratch_bytes(int64_t rows, int64_t cols,
                                                         argreduce_dtype_t dtype) {
     LogitsPlan p;
-    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, false, &p) != ARGREDUCE_OK)
+    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1, false, &p) != ARGREDUCE_OK)
         return std::numeric_limits<size_t>::max();
     return p.scratch_bytes;
 }
@@ -312,7 +324,7 @@ ARGREDUCE_EXPORT int argreduce_distill_plan(int64_t rows, int64_t cols, argreduc
                                             argreduce_plan_t* out) {
     if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
     LogitsPlan p;
-    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, false, &p);
+    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1, false, &p);
     if (rc != ARGREDUCE_OK) return rc;
     argreduce::fill_logits_plan(p, p.parts > 1 ? 2 : 1, out);
     return ARGREDUCE_OK;

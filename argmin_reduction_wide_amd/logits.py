@@ -44,15 +44,8 @@ class DistillLoss(NamedTuple):
     stats: torch.Tensor
 
 
-class _Rows(NamedTuple):
-    code: int
-    rows: int
-    cols: int
-    stride: int
-
-
-def _rows(logits) -> _Rows:
-    """The logits as rows of one stride, or a refusal."""
+def _rows(logits):
+    """(format code, rows, cols, row stride) of the logits, or a refusal."""
     if not logits.is_cuda:
         raise ValueError("the logits operators run on the GPU only; got a CPU tensor")
     code = _CODES.get(logits.dtype)
@@ -67,7 +60,7 @@ def _rows(logits) -> _Rows:
     if strides[-1] != 1 and cols != 1:
         raise ValueError("the last dimension of the logits must be contiguous")
     if len(shape) == 2:
-        return _Rows(code, shape[0], cols, strides[0])
+        return code, shape[0], cols, strides[0]
     rows, stride = 1, None
     for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
@@ -77,19 +70,20 @@ def _rows(logits) -> _Rows:
         elif rows > 0 and s != stride * rows:
             raise ValueError("the leading dimensions of the logits must be rows of one stride")
         rows *= n
-    return _Rows(code, rows, cols, cols if stride is None else stride)
+    return code, rows, cols, cols if stride is None else stride
 
 
 def _same(t, name: str, like, dtype, shape) -> None:
     """An input array: contiguous, of this type and shape, on the logits' device."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == like.device:
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}; got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}; got {tuple(t.shape)}")
     if t.device != like.device:
         raise ValueError(f"{name} must be on {like.device}; got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _temperature(t) -> float:
@@ -124,9 +118,20 @@ def _scratch(need: int, what: str, given, device):
     return given.data_ptr(), given.numel() * given.element_size(), given
 
 
-def _done(rc: int, what: str, r: _Rows) -> None:
-    if rc != B.OK:
-        raise B.ArgreduceError(rc, f"{what}(rows={r.rows}, cols={r.cols}, row_stride={r.stride})")
+class _Calls:
+    """The library's logits entry points, looked up when the first of them is needed."""
+
+    def __getattr__(self, name):
+        f = B.entry_point("argreduce_" + name)
+        setattr(self, name, f)
+        return f
+
+
+_call = _Calls()
+
+
+def _failed(rc: int, what: str, rows, cols, stride):
+    return B.ArgreduceError(rc, f"argreduce_{what}(rows={rows}, cols={cols}, row_stride={stride})")
 
 
 def _refuse_captured_autograd(logits) -> None:
@@ -142,7 +147,7 @@ def _refuse_captured_autograd(logits) -> None:
 
 
 def _logprobs(logits, tokens, temperature, entropy, top, scratch):
-    r = _rows(logits)
+    code, rows, cols, stride = _rows(logits)
     shape = logits.shape
     lead = shape[:-1]
     _same(tokens, "tokens", logits, torch.int64, lead)
@@ -153,7 +158,6 @@ def _logprobs(logits, tokens, temperature, entropy, top, scratch):
         with torch.cuda.device(logits.device):
             return _logprobs(logits, tokens, temperature, entropy, top, scratch)
     device = logits.device
-    code, rows, cols, stride = r
     stats = torch.empty(4, rows, dtype=torch.float32, device=device)
     lp = tok = None
     lp_ptr = tok_ptr = 0
@@ -161,13 +165,13 @@ def _logprobs(logits, tokens, temperature, entropy, top, scratch):
         lp = torch.empty(*lead, top, dtype=torch.float32, device=device)
         tok = torch.empty(*lead, top, dtype=torch.int64, device=device)
         lp_ptr, tok_ptr = lp.data_ptr(), tok.data_ptr()
-    need = B.entry_point("argreduce_logprobs_scratch_bytes")(rows, cols, code)
+    need = _call.logprobs_scratch_bytes(rows, cols, code)
     sptr, sbytes, scratch = _scratch(need, "argreduce_logprobs", scratch, device)
-    rc = B.entry_point("argreduce_logprobs")(logits.data_ptr(), code, rows, cols, stride,
-                                             tokens.data_ptr(), temperature, 1 if entropy else 0,
-                                             top, stats.data_ptr(), lp_ptr, tok_ptr, sptr, sbytes,
-                                             _stream(device.index))
-    _done(rc, "argreduce_logprobs", r)
+    rc = _call.logprobs(logits.data_ptr(), code, rows, cols, stride, tokens.data_ptr(), temperature,
+                        1 if entropy else 0, top, stats.data_ptr(), lp_ptr, tok_ptr, sptr, sbytes,
+                        _stream(device.index))
+    if rc:
+        raise _failed(rc, "logprobs", rows, cols, stride)
     return stats, lp, tok
 
 
@@ -237,10 +241,10 @@ def token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy=None, 
     that of the forward call on the same logits, tokens and temperature, made with
     ``entropy=True`` if grad_entropy is given; grad_logprob and grad_entropy are float32 in the
     logits' leading shape."""
-    r = _rows(logits)
+    code, rows, cols, stride = _rows(logits)
     lead = logits.shape[:-1]
     _same(tokens, "tokens", logits, torch.int64, lead)
-    _same(stats, "stats", logits, torch.float32, (4, r.rows))
+    _same(stats, "stats", logits, torch.float32, (4, rows))
     _same(grad_logprob, "grad_logprob", logits, torch.float32, lead)
     if grad_entropy is not None:
         _same(grad_entropy, "grad_entropy", logits, torch.float32, lead)
@@ -250,13 +254,13 @@ def token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy=None, 
         with torch.cuda.device(logits.device):
             return token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy,
                                        temperature=temperature, out=out)
-    code, rows, cols, stride = r
-    rc = B.entry_point("argreduce_logprobs_grad")(
+    rc = _call.logprobs_grad(
         logits.data_ptr(), code, rows, cols, stride, tokens.data_ptr(), temperature,
         stats.data_ptr(), grad_logprob.data_ptr(),
         0 if grad_entropy is None else grad_entropy.data_ptr(), out.data_ptr(),
         _stream(logits.device.index))
-    _done(rc, "argreduce_logprobs_grad", r)
+    if rc:
+        raise _failed(rc, "logprobs_grad", rows, cols, stride)
     return out
 
 
@@ -275,22 +279,21 @@ def _teacher(logits, teacher_tokens, teacher_logits) -> int:
 
 
 def _distill(logits, teacher_tokens, teacher_logits, temperature, scratch):
-    r = _rows(logits)
+    code, rows, cols, stride = _rows(logits)
     k = _teacher(logits, teacher_tokens, teacher_logits)
     temperature = _temperature(temperature)
     if _elsewhere(logits):
         with torch.cuda.device(logits.device):
             return _distill(logits, teacher_tokens, teacher_logits, temperature, scratch)
-    code, rows, cols, stride = r
     device = logits.device
     stats = torch.empty(5, rows, dtype=torch.float32, device=device)
-    need = B.entry_point("argreduce_distill_scratch_bytes")(rows, cols, code)
+    need = _call.distill_scratch_bytes(rows, cols, code)
     sptr, sbytes, scratch = _scratch(need, "argreduce_distill", scratch, device)
-    rc = B.entry_point("argreduce_distill")(logits.data_ptr(), code, rows, cols, stride, k,
-                                            teacher_tokens.data_ptr(), teacher_logits.data_ptr(),
-                                            temperature, stats.data_ptr(), sptr, sbytes,
-                                            _stream(device.index))
-    _done(rc, "argreduce_distill", r)
+    rc = _call.distill(logits.data_ptr(), code, rows, cols, stride, k, teacher_tokens.data_ptr(),
+                       teacher_logits.data_ptr(), temperature, stats.data_ptr(), sptr, sbytes,
+                       _stream(device.index))
+    if rc:
+        raise _failed(rc, "distill", rows, cols, stride)
     return stats
 
 
@@ -338,9 +341,9 @@ def distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss, 
     """Gradient of ``(grad_loss * loss).sum()`` with respect to the logits, in their type and shape
     (contiguous; ``out``, if given, is such a tensor). stats is that of the forward call on the
     same inputs; grad_loss is float32 in the logits' leading shape."""
-    r = _rows(logits)
+    code, rows, cols, stride = _rows(logits)
     k = _teacher(logits, teacher_tokens, teacher_logits)
-    _same(stats, "stats", logits, torch.float32, (5, r.rows))
+    _same(stats, "stats", logits, torch.float32, (5, rows))
     _same(grad_loss, "grad_loss", logits, torch.float32, logits.shape[:-1])
     temperature = _temperature(temperature)
     out = _grad_out(logits, out)
@@ -348,12 +351,12 @@ def distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss, 
         with torch.cuda.device(logits.device):
             return distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss,
                                      temperature=temperature, out=out)
-    code, rows, cols, stride = r
-    rc = B.entry_point("argreduce_distill_grad")(
+    rc = _call.distill_grad(
         logits.data_ptr(), code, rows, cols, stride, k, teacher_tokens.data_ptr(),
         teacher_logits.data_ptr(), temperature, stats.data_ptr(), grad_loss.data_ptr(),
         out.data_ptr(), _stream(logits.device.index))
-    _done(rc, "argreduce_distill_grad", r)
+    if rc:
+        raise _failed(rc, "distill_grad", rows, cols, stride)
     return out
 
 
@@ -362,7 +365,7 @@ def distill_step(logits, teacher_tokens, teacher_logits, weights, *, temperature
     """(loss, grad): the loss of every row, and the gradient of ``(weights * loss).sum()`` with
     respect to the logits, in one call that reads the logits from memory once. For a training step
     whose row weights (float32, the logits' leading shape) do not depend on the loss."""
-    r = _rows(logits)
+    code, rows, cols, stride = _rows(logits)
     k = _teacher(logits, teacher_tokens, teacher_logits)
     _same(weights, "weights", logits, torch.float32, logits.shape[:-1])
     temperature = _temperature(temperature)
@@ -371,14 +374,14 @@ def distill_step(logits, teacher_tokens, teacher_logits, weights, *, temperature
         with torch.cuda.device(logits.device):
             return distill_step(logits, teacher_tokens, teacher_logits, weights,
                                 temperature=temperature, out=out, scratch=scratch)
-    code, rows, cols, stride = r
     device = logits.device
     stats = torch.empty(5, rows, dtype=torch.float32, device=device)
-    need = B.entry_point("argreduce_distill_scratch_bytes")(rows, cols, code)
+    need = _call.distill_scratch_bytes(rows, cols, code)
     sptr, sbytes, scratch = _scratch(need, "argreduce_distill_step", scratch, device)
-    rc = B.entry_point("argreduce_distill_step")(
+    rc = _call.distill_step(
         logits.data_ptr(), code, rows, cols, stride, k, teacher_tokens.data_ptr(),
         teacher_logits.data_ptr(), temperature, weights.data_ptr(), stats.data_ptr(),
         out.data_ptr(), sptr, sbytes, _stream(device.index))
-    _done(rc, "argreduce_distill_step", r)
+    if rc:
+        raise _failed(rc, "distill_step", rows, cols, stride)
     return (stats[0] if logits.dim() == 2 else stats[0].view(logits.shape[:-1])), out

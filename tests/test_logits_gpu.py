@@ -260,6 +260,65 @@ def test_distill_every_path(capacity, dtype, cap):
         check_distill(x, ids, v, dtype, 1.5, rng)
 
 
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("rows,cols,k", [(23, 300, 7), (23, 90, 100), (13, 90, 1024), (23, 3000, 64),
+                                         (13, 3000, 65), (9, 9001, 200), (9, 33000, 33), (7, 33000, 300),
+                                         (5, 70001, 64)])
+def test_distill_teams_go_through_several_rows(capacity, dtype, rows, cols, k):
+    """One CU's worth of workgroups: each takes several rows of every kind, one after another."""
+    capacity(2048)
+    announce(f"distill {dtype} [{rows},{cols}] k={k} on one CU")
+    rng = np.random.default_rng(rows * cols + k)
+    x = make_rows(rng, rows, cols, dtype)
+    ids, v = make_teacher(rng, rows, cols, k)
+    ids[3:6] = -1  # three rows without a teacher in a row
+    check_distill(x, ids, v, dtype, 1.0, rng)
+
+
+@pytest.mark.parametrize("dtype,rows,cols", [("f32", 600, 30011), ("f16", 700, 50021), ("bf16", 9000, 4096),
+                                             ("bf16", 70000, 520)])
+def test_logits_too_large_for_the_cache(dtype, rows, cols):
+    """Logits over 64 MiB, which are read past the caches, and more rows than are in flight at once;
+    every row against 64-bit torch, a sample of rows against the reference and its bounds."""
+    announce(f"large {dtype} [{rows},{cols}]")
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = (torch.randn(rows, cols, device="cuda", generator=g) * 2).to(DT[dtype])
+    tokens = torch.randint(0, cols, (rows,), device="cuda", generator=g)
+    tokens[::17] = -1
+    ids = torch.randint(0, cols, (rows, 12), device="cuda", generator=g)
+    ids[::13] = -1
+    v = torch.randn(rows, 12, device="cuda", generator=g) * 2
+    w, e = torch.rand(rows, device="cuda", generator=g), torch.rand(rows, device="cuda", generator=g)
+    r = ar.token_logprobs(x, tokens, entropy=True, top=3)
+    grad = ar.token_logprobs_grad(x, tokens, r.stats, w, e)
+    loss, dgrad = ar.distill_step(x, ids, v, w)
+    d = ar.distill_loss(x, ids, v)
+    dgrad2 = ar.distill_loss_grad(x, ids, v, d.stats, w)
+    torch.cuda.synchronize()
+    live = tokens >= 0
+    for a in range(0, rows, 1000):
+        cut = slice(a, a + 1000)
+        lp = torch.log_softmax(x[cut].double(), 1)
+        want = torch.where(live[cut], lp.gather(1, tokens[cut].clamp(min=0)[:, None])[:, 0], 0.0)
+        # randn * 2: E|z| < 30 and |ln p| < 40; the bounds are logits_reference's
+        assert (r.logprob[cut].double() - want).abs().max() < R.U * (3 * 30 + R.adds(cols) + 2 + 8 * 60)
+        best, at = x[cut].float().sort(dim=1, descending=True, stable=True)
+        assert torch.equal(r.top_tokens[cut], torch.where(live[cut, None], at[:, :3], -1))
+        q = torch.where(ids[cut] >= 0, torch.softmax(v[cut].double(), 1), 0.0)
+        want = (q * (torch.log_softmax(v[cut].double(), 1) - lp.gather(1, ids[cut].clamp(min=0)))).sum(1)
+        assert (loss[cut].double() - want).abs().max() < R.U * (3 * 30 + R.adds(cols) + 8 * 100)
+        assert torch.equal(loss[cut] == 0, (ids[cut] < 0).all(1))
+    xs, ts, i_s = host(x[::97]), tokens[::97].cpu().numpy(), ids[::97].cpu().numpy()
+    vs, ws, es = host(v[::97]), host(w[::97]), host(e[::97])
+    got = [host(t[::97]) for t in (grad, dgrad, dgrad2)]
+    for n in range(len(xs)):
+        row = R.logprobs_row(xs[n], int(ts[n]), 1.0, 0)
+        R.agree(got[0][n], *R.logprobs_grad_row(row, xs[n], int(ts[n]), 1.0, ws[n], es[n], dtype), f"row {n}")
+        row = R.distill_row(xs[n], i_s[n], vs[n], 1.0)
+        for t in got[1:]:
+            R.agree(t[n], *R.distill_grad_row(row, xs[n], 1.0, ws[n], dtype), f"distill row {n}")
+
+
 def test_offsets_beyond_32_bits():
     """Rows 2^31 + 8 elements apart: the last starts past 2^32 elements."""
     stride, cols = 2 ** 31 + 8, 1000
