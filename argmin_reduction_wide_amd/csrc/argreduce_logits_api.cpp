@@ -2,7 +2,7 @@
 // and the contract are in include/argreduce.h, the kernels in argreduce_logits.hip.
 #include <hip/hip_runtime_api.h>
 
-#include <cmath>
+#include <algorithm>
 #include <limits>
 
 #include "argreduce.h"
@@ -105,13 +105,16 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
     *p = LogitsPlan{};
     p->device_threads = cap;
     p->parts = 1;
-    const bool logprobs = use == kLogprobs || use == kLogprobsTop;
+    // Rows held by a group of lanes, a vector each, and at most four teacher entries per lane.
+    // (Alternatives too, though they are taken one by one there: [65536,64] f16 16 us with 4 of
+    // them, 39 with 30, and 61 and 70 with a wavefront per row and its selection.)
     const int64_t held = vec_rows ? ceil_div(cols * es, 16) : vecs;  // vectors a row lies in
-    if (held <= 32 && logprobs) {
+    const int64_t lanes = next_pow2(std::max<int64_t>({held, ceil_div(k, 4), 4}));
+    if (lanes <= 32) {
         p->path = ARGREDUCE_PATH_SUBWAVE;
-        p->team = static_cast<int>(next_pow2(held < 4 ? 4 : held));
-        p->grid_blocks = ceil_div(rows1, kBlock / p->team);
-        if (rows1 * p->team >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
+        p->team = static_cast<int>(lanes);
+        p->grid_blocks = ceil_div(rows1, kBlock / lanes);
+        if (rows1 * lanes >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
         return ARGREDUCE_OK;
     }
     // a wavefront per row: up to four vectors per lane; in a distillation step up to the eight that
@@ -315,7 +318,7 @@ ARGREDUCE_EXPORT int argreduce_logprobs_grad(const void* x, argreduce_dtype_t dt
 ARGREDUCE_EXPORT size_t argreduce_distill_scratch_bytes(int64_t rows, int64_t cols,
                                                         argreduce_dtype_t dtype) {
     LogitsPlan p;
-    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1, false, &p) != ARGREDUCE_OK)
+    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p) != ARGREDUCE_OK)
         return std::numeric_limits<size_t>::max();
     return p.scratch_bytes;
 }
@@ -324,7 +327,7 @@ ARGREDUCE_EXPORT int argreduce_distill_plan(int64_t rows, int64_t cols, argreduc
                                             argreduce_plan_t* out) {
     if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
     LogitsPlan p;
-    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1, false, &p);
+    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p);
     if (rc != ARGREDUCE_OK) return rc;
     argreduce::fill_logits_plan(p, p.parts > 1 ? 2 : 1, out);
     return ARGREDUCE_OK;
