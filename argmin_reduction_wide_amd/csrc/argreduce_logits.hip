@@ -152,6 +152,9 @@ struct Stat {
     }
 };
 
+// A team's LDS words per wavefront: three for team_merge, and one for each reduction of a row.
+enum Slot { kSlotMax = 3, kSlotSum, kSlotEntropy, kSlotLoss, kShared = 8 };
+
 // A value that every lane of the wavefront holds, as a scalar.
 __device__ inline float uniform(float v) {
     return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
@@ -160,7 +163,7 @@ __device__ inline float uniform(float v) {
 // Merges the lanes' parts; every thread of the team gets the row's. The wavefronts' parts go
 // through LDS; each wavefront then merges them all, one per lane of each group of T / 64 lanes.
 template <bool ENT, int T>
-__device__ inline void team_merge(Stat& a, float k, int lane, float (*sh)[4]) {
+__device__ inline void team_merge(Stat& a, float k, int lane, float (*sh)[kShared]) {
     a.move<ENT>(lanes_max<kWave>(a.m), k);
     a.s = lanes_sum<kWave>(a.s);
     if constexpr (ENT) a.h = lanes_sum<kWave>(a.h);
@@ -182,15 +185,15 @@ __device__ inline void team_merge(Stat& a, float k, int lane, float (*sh)[4]) {
     a = {uniform(a.m), uniform(a.s), uniform(a.h)};
 }
 
+// One barrier: a slot is written again only for the team's next row, and other barriers lie between.
 template <int T, bool MAX>
-__device__ inline float team_reduce(float v, int lane, float (*sh)[4]) {
+__device__ inline float team_reduce(float v, int lane, float (*sh)[kShared], Slot slot) {
     v = MAX ? lanes_max<kWave>(v) : lanes_sum<kWave>(v);
     if constexpr (T > kWave) {
-        if (lane % kWave == 0) sh[lane / kWave][3] = v;
+        if (lane % kWave == 0) sh[lane / kWave][slot] = v;
         team_sync<T>();
-        v = sh[lane % (T / kWave)][3];
+        v = sh[lane % (T / kWave)][slot];
         v = MAX ? lanes_max<T / kWave>(v) : lanes_sum<T / kWave>(v);
-        team_sync<T>();
     }
     return uniform(v);
 }
@@ -793,7 +796,7 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32
                                                            int64_t* top_tok) {
     constexpr int kTeams = kTeamsPerBlock<T>;
     constexpr int U = kUnroll<Fmt, TOP>;
-    __shared__ float sh[T / kWave][4];
+    __shared__ float sh[T / kWave][kShared];
     __shared__ TopLds<TOP ? T : 64, TOP ? kSegs<T> : 1> lds[TOP ? kTeams : 1];
     const uint32_t team = team_of<T>();
     const uint32_t r = blockIdx.x * kTeams + team;
@@ -846,7 +849,7 @@ template <typename Fmt, bool KEEP, bool ENT>
 __global__ __launch_bounds__(kPartThreads) void k_part(const void* x, uint32_t cols, uint32_t stride,
                                                        float scale, uint32_t parts,
                                                        const int64_t* tokens, Part* out) {
-    __shared__ float sh[kPartThreads / kWave][4];
+    __shared__ float sh[kPartThreads / kWave][kShared];
     const uint32_t r = blockIdx.x / parts;
     const uint32_t b = blockIdx.x - r * parts;
     if (tokens != nullptr && tokens[r] < 0) return;
@@ -875,7 +878,7 @@ constexpr int kMergeSegs = 2048;
 // The merged statistics of a split row, in every thread.
 template <bool ENT, int T>
 __device__ inline Stat merge_parts(const Part* p, uint32_t parts, float scale, int lane,
-                                   float (*sh)[4]) {
+                                   float (*sh)[kShared]) {
     Stat a;
     a.init();
     for (uint32_t b = lane; b < parts; b += T) {
@@ -896,7 +899,7 @@ __global__ __launch_bounds__(T) void k_lp_merge(uint64_t x, uint64_t tokens,
                                                             uint64_t part, uint64_t stats_,
                                                             uint64_t top_lp, uint64_t top_tok,
                                                             uint32_t stride, uint32_t rows) {
-    __shared__ float sh[T / kWave][4];
+    __shared__ float sh[T / kWave][kShared];
     __shared__ TopLds<TOP ? T : 64, TOP ? kMergeSegs : 1> L;
     const uint32_t cols = tags(x, tokens);
     const uint32_t parts = tag(part), k = tag(stats_);
@@ -1114,36 +1117,82 @@ __device__ inline Entry entry_at(const int64_t* ids, const float* values, uint32
     return {static_cast<int32_t>(id < 0 ? -1 : id < static_cast<int64_t>(cols) ? id : cols),
             id >= 0 ? values[i] : -__builtin_huge_valf(), 0.0f, __builtin_nanf("")};
 }
-// Up to 64 entries: every wavefront's own copy of them, one per lane (x in the team's first).
-__device__ inline Entry wave_entry(const int64_t* ids, const float* values, uint32_t k, int lane,
-                                   uint32_t cols) {
-    const uint32_t i = lane % kWave;
-    if (k <= kWave && i < k) return entry_at(ids, values, i, cols);
+// A lane's entry where there are no more entries than lanes, read ahead of its use: up to 64 of them
+// every wavefront has its own copy (the student's logits in the team's first alone), beyond that
+// the team has one.
+template <int T>
+__device__ inline Entry own_entry(const int64_t* ids, const float* values, uint32_t k, int lane,
+                                  uint32_t cols) {
+    const uint32_t i = k <= kWave ? lane % kWave : lane;
+    if (k <= T && i < k) return entry_at(ids, values, i, cols);
     return {-1, -__builtin_huge_valf(), 0.0f, __builtin_nanf("")};
 }
+template <typename Fmt>
+__device__ inline void own_student(Entry& mine, const uint8_t* row, uint32_t k, int lane, uint32_t cols) {
+    if (k > kWave || lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
+}
+
+// How often each id occurs in a row of more than 64 entries: an open hash table in LDS of at least
+// twice as many places. Comparing every entry with every other took most of the time instead:
+// [11266,617] f16 229 us with 256 entries.
+struct IdTable {
+    struct Place {
+        int32_t id;
+        uint32_t count;
+    };
+    Place* place;
+    uint32_t mask;
+    __device__ static uint32_t size(uint32_t k) { return k <= kWave ? 0 : 2u << (32 - __clz(k - 1)); }
+    __device__ void clear(int lane, int team) const {
+        for (uint32_t i = lane; i <= mask; i += team) place[i] = {-1, 0};
+    }
+    __device__ uint32_t first(int32_t id) const { return (static_cast<uint32_t>(id) * 0x9e3779b1u) >> 8 & mask; }
+    __device__ void add(int32_t id) const {
+        if (id < 0) return;
+        uint32_t i = first(id);
+        while (true) {  // ends: there are more places than ids
+            const int32_t old = atomicCAS(&place[i].id, -1, id);
+            if (old == -1 || old == id) break;
+            i = (i + 1) & mask;
+        }
+        atomicAdd(&place[i].count, 1u);
+    }
+    __device__ bool once(int32_t id) const {
+        if (id < 0) return true;
+        uint32_t i = first(id);
+        while (place[i].id != id) i = (i + 1) & mask;
+        return place[i].count == 1;
+    }
+};
 
 // The teacher's row: its entries into `ent`, the distribution's numbers to every thread. *bad: the
-// whole gradient is NaN (a weight is NaN, or an id with weight lies beyond the row). Up to 64
-// entries (`mine`) every wavefront finds the numbers for itself, without a barrier. With TOTALS
-// the totals too: each the sum of the weights with its id, in the entries' order.
+// whole gradient is NaN (a weight is NaN, or an id with weight lies beyond the row). With TOTALS the
+// totals too: each the sum of the weights with its id, in the entries' order. Up to 64 entries take
+// no barrier, up to T (`mine`) three; more are read here and worked off in turns.
 template <typename Fmt, int T, bool TOTALS>
-__device__ inline Teacher teacher_row(Entry* ent, Entry mine, const uint8_t* row, uint32_t cols,
+__device__ inline Teacher teacher_row(Entry* ent, const IdTable& table, Entry mine, const uint8_t* row, uint32_t cols,
                                       const int64_t* ids, const float* values, uint32_t k, float scale,
-                                      int lane, float (*sh)[4], bool* bad) {
-    const auto beyond = [&](int32_t id, float w) { return id == static_cast<int32_t>(cols) && w != 0.0f; };
-    const auto spread = [](float w, float lw) { return w > 0.0f ? -w * (lw * kLn2) : 0.0f; };
+                                      int lane, float (*sh)[kShared], bool* bad) {
+    // an entry's part of the entropy; NaN for an id with weight beyond the row
+    const auto spread = [&](int32_t id, float w, float lw) {
+        if (id == static_cast<int32_t>(cols) && w != 0.0f) return __builtin_nanf("");
+        return id >= 0 && w > 0.0f ? -w * (lw * kLn2) : 0.0f;
+    };
+    const auto numbers = [&](float m, float s) {
+        return Teacher{s == s ? m : __builtin_nanf(""), log2_f(s), 0.0f};
+    };
+    // a value's part of the sum; NaN for NaN, which a maximum passes over
+    const auto part = [&](float v, float m) {
+        return v != v ? v : (m > -__builtin_huge_valf() ? exp2_f((v - m) * scale) : 0.0f);
+    };
     float m = -__builtin_huge_valf(), s = 0.0f, h = 0.0f;
     Teacher q;
     if (k <= kWave) {
-        m = lanes_max<kWave>(mine.w);
-        if (m > -__builtin_huge_valf()) s = exp2_f((mine.w - m) * scale);
-        if (mine.w != mine.w) s = mine.w;
-        s = lanes_sum<kWave>(s);
-        q = {s == s ? m : __builtin_nanf(""), log2_f(s), 0.0f};
+        m = lanes_max<kWave>(max_f(mine.w, m));
+        q = numbers(m, s = lanes_sum<kWave>(part(mine.w, m)));
         const float lw = q.log_weight(mine.w, scale);
         mine.w = exp2_f(lw);
-        q.entropy = lanes_sum<kWave>(mine.id < 0 ? 0.0f : spread(mine.w, lw));
-        *bad = __any(s != s || beyond(mine.id, mine.w));
+        q.entropy = lanes_sum<kWave>(spread(mine.id, mine.w, lw));
         if (TOTALS && lane < kWave) {
 #pragma unroll 8
             for (uint32_t j = 0; j < k; ++j) {
@@ -1155,42 +1204,55 @@ __device__ inline Teacher teacher_row(Entry* ent, Entry mine, const uint8_t* row
         }
         if (static_cast<uint32_t>(lane) < k) ent[lane] = mine;
         team_sync<kWave>();
+    } else if (k <= T) {
+        if constexpr (TOTALS) table.clear(lane, T);
+        m = team_reduce<T, true>(max_f(mine.w, m), lane, sh, kSlotMax);
+        if constexpr (TOTALS) table.add(mine.id);
+        q = numbers(m, s = team_reduce<T, false>(part(mine.w, m), lane, sh, kSlotSum));
+        const float lw = q.log_weight(mine.w, scale);
+        mine.w = exp2_f(lw);
+        if (static_cast<uint32_t>(lane) < k) ent[lane] = mine;
+        q.entropy = team_reduce<T, false>(spread(mine.id, mine.w, lw), lane, sh, kSlotEntropy);
     } else {
-        bool nan = false, out = false;
+        if constexpr (TOTALS) table.clear(lane, T);
         for (uint32_t i = lane; i < k; i += T) {
             const Entry e = entry_at(ids, values, i, cols);
             ent[i] = e;
             m = max_f(m, e.w);
-            nan |= e.w != e.w;
         }
-        m = team_reduce<T, true>(m, lane, sh);
-        if (m > -__builtin_huge_valf())
-            for (uint32_t i = lane; i < k; i += T) s += exp2_f((ent[i].w - m) * scale);
-        if (nan) s = __builtin_nanf("");
-        s = team_reduce<T, false>(s, lane, sh);
-        q = {s == s ? m : __builtin_nanf(""), log2_f(s), 0.0f};
+        m = team_reduce<T, true>(m, lane, sh, kSlotMax);
+        if constexpr (T == kWave) team_sync<T>();
+        for (uint32_t i = lane; i < k; i += T) {
+            s += part(ent[i].w, m);
+            if constexpr (TOTALS) table.add(ent[i].id);
+        }
+        q = numbers(m, s = team_reduce<T, false>(s, lane, sh, kSlotSum));
         for (uint32_t i = lane; i < k; i += T) {
             const int32_t id = ent[i].id;
             const float lw = q.log_weight(ent[i].w, scale);
             const float w = exp2_f(lw);
             ent[i].w = w;
-            out |= beyond(id, w);
-            if (id >= 0) h += spread(w, lw);
+            h += spread(id, w, lw);
             ent[i].x = student_at<Fmt>(row, id, cols);
         }
-        q.entropy = team_reduce<T, false>(h, lane, sh);
-        // (also makes the weights visible)
-        *bad = s != s || team_reduce<T, true>(out ? 1.0f : 0.0f, lane, sh) > 0.0f;
-        if constexpr (TOTALS) {
+        q.entropy = team_reduce<T, false>(h, lane, sh, kSlotEntropy);
+    }
+    if constexpr (TOTALS) {
+        if (k > kWave) {  // (the last reduction's barrier has made the table and the weights visible)
+            if constexpr (T == kWave) team_sync<T>();
             for (uint32_t i = lane; i < k; i += T) {
                 const int32_t id = ent[i].id;
-                float w = 0.0f;
-#pragma unroll 8
-                for (uint32_t j = 0; j < k; ++j) w += ent[j].id == id ? ent[j].w : 0.0f;
+                float w = ent[i].w;
+                if (!table.once(id)) {
+                    w = 0.0f;
+#pragma unroll 4
+                    for (uint32_t j = 0; j < k; ++j) w += ent[j].id == id ? ent[j].w : 0.0f;
+                }
                 ent[i].total = w;
             }
         }
     }
+    *bad = s != s || q.entropy != q.entropy;
     return q;
 }
 
@@ -1207,7 +1269,7 @@ __device__ inline void store_distill(float* stats, uint32_t rows, uint32_t r, fl
 // The loss of a row from its merged statistics and log2 of their sum (in lane 0 of the team).
 template <int T>
 __device__ inline float distill_loss(const Entry* ent, uint32_t k, float scale, const Teacher& q,
-                                     const Stat& a, float l2, int lane, float (*sh)[4]) {
+                                     const Stat& a, float l2, int lane, float (*sh)[kShared]) {
     float sum = 0.0f;
     for (uint32_t i = lane; i < k; i += T) {
         const Entry e = ent[i];
@@ -1215,7 +1277,7 @@ __device__ inline float distill_loss(const Entry* ent, uint32_t k, float scale, 
         const float lp = a.s == 0.0f ? -__builtin_huge_valf() : ln_p(e.x, a.m, l2, scale);
         sum = fmaf(e.w, lp, sum);
     }
-    sum = k <= kWave ? lanes_sum<kWave>(sum) : team_reduce<T, false>(sum, lane, sh);
+    sum = k <= kWave ? lanes_sum<kWave>(sum) : team_reduce<T, false>(sum, lane, sh, kSlotLoss);
     return -q.entropy - sum;
 }
 
@@ -1245,7 +1307,7 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32
                                                            uint32_t rows, uint32_t k,
                                                            const int64_t* ids_, const float* values_,
                                                            float* stats) {
-    __shared__ float sh[T / kWave][4];
+    __shared__ float sh[T / kWave][kShared];
     const uint32_t r = blockIdx.x * kTeamsPerBlock<T> + team_of<T>();
     const int lane = lane_of<T>();
     if (r >= rows) return;
@@ -1254,9 +1316,9 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32
     const uint8_t* row = row_ptr<Fmt>(x, r, stride);
     Entry* ent = s_entries + team_of<T>() * k;
     bool bad;
-    Entry mine = wave_entry(ids, values, k, lane, cols);
-    if (lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
-    const Teacher q = teacher_row<Fmt, T, false>(ent, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
+    Entry mine = own_entry<T>(ids, values, k, lane, cols);
+    own_student<Fmt>(mine, row, k, lane, cols);
+    const Teacher q = teacher_row<Fmt, T, false>(ent, IdTable{}, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
@@ -1389,7 +1451,7 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
                                                             uint64_t values_, const Part* part,
                                                             float* stats) {
     constexpr int T = kMergeThreads;
-    __shared__ float sh[T / kWave][4];
+    __shared__ float sh[T / kWave][kShared];
     const uint32_t k = tag(ids_), parts = tag(values_);
     const uint32_t r = blockIdx.x;
     const int lane = threadIdx.x;
@@ -1397,9 +1459,9 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
     const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
     const uint8_t* row = row_ptr<Fmt>(x, r, stride);
     bool bad;
-    Entry mine = wave_entry(ids, values, k, lane, cols);
-    if (lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
-    const Teacher q = teacher_row<Fmt, T, false>(s_entries, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
+    Entry mine = own_entry<T>(ids, values, k, lane, cols);
+    own_student<Fmt>(mine, row, k, lane, cols);
+    const Teacher q = teacher_row<Fmt, T, false>(s_entries, IdTable{}, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
@@ -1462,7 +1524,7 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
     constexpr int VW = Fmt::VW;
     constexpr int U = NV > 8 ? kUnroll<Fmt, false> / 2 : kUnroll<Fmt, false>;  // 128 registers suffice
     static_assert(NV % U == 0, "whole steps");
-    __shared__ float sh[T / kWave][4];
+    __shared__ float sh[T / kWave][kShared];
     const uint32_t cols = tags(x, ids_), k = tag(values_), teams = tag(grad_) * kTeamsPerBlock<T>;
     const float scale = __uint_as_float(tags(stats_, w));
     const int lane = lane_of<T>();
@@ -1471,6 +1533,10 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
     // the entries of two rows: a wavefront may be one row ahead of another
     Entry* ent = s_entries + team_of<T>() * 2 * k;
     Entry* other = ent + k;
+    const uint32_t places = IdTable::size(k);  // the tables lie behind all teams' entries
+    const IdTable table{reinterpret_cast<IdTable::Place*>(s_entries + kTeamsPerBlock<T> * 2 * k) +
+                            team_of<T>() * places,
+                        places - 1};
     const auto ids_at = [&](uint32_t n) { return addr<const int64_t>(ids_) + static_cast<size_t>(n) * k; };
     const auto values_at = [&](uint32_t n) { return addr<const float>(values_) + static_cast<size_t>(n) * k; };
     const auto row_at = [&](uint32_t n) { return row_ptr<Fmt>(addr<const void>(x), n, stride); };
@@ -1479,7 +1545,7 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
         const uint32_t v = sp.va + lane + i * T;
         if (sp.va + i * T < sp.vb) held[i] = sp.load(v < sp.vb ? v : sp.vb - 1);
     };
-    Entry mine = wave_entry(ids_at(r), values_at(r), k, lane, cols);
+    Entry mine = own_entry<T>(ids_at(r), values_at(r), k, lane, cols);
     {
         const Span<Fmt> sp(row_at(r), cols);
 #pragma unroll
@@ -1487,12 +1553,12 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
     }
     while (true) {
         const uint8_t* row = row_at(r);
-        if (lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
+        own_student<Fmt>(mine, row, k, lane, cols);
         uint8_t* out = const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad_), r, cols));
         const Span<Fmt> sp(row, cols);
         bool bad;
-        const Teacher q = teacher_row<Fmt, T, true>(ent, mine, row, cols, ids_at(r), values_at(r), k, scale,
-                                                    lane, sh, &bad);
+        const Teacher q = teacher_row<Fmt, T, true>(ent, table, mine, row, cols, ids_at(r), values_at(r), k,
+                                                    scale, lane, sh, &bad);
         const bool absent = q.m == -__builtin_huge_valf();
         float loss = 0.0f, l2 = 0.0f;
         Stat a{0.0f, 0.0f, 0.0f};
@@ -1543,7 +1609,7 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
         const uint32_t next = r + teams;
         const uint32_t nr = next < rows ? next : r;
         const Span<Fmt> np(row_at(nr), cols);
-        mine = wave_entry(ids_at(nr), values_at(nr), k, lane, cols);
+        mine = own_entry<T>(ids_at(nr), values_at(nr), k, lane, cols);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const uint32_t v = sp.va + lane + i * T;
@@ -1635,11 +1701,18 @@ template <typename... KArgs, typename... Args>
 void launch(void (*kernel)(KArgs...), uint32_t grid, int block, hipStream_t s, Args... args) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, s, args...);
 }
-// With LDS for the teacher's entries of the workgroup's rows.
+// With LDS for the teacher's entries of the workgroup's rows, and their hash tables.
 template <typename... KArgs, typename... Args>
-void launch_entries(void (*kernel)(KArgs...), uint32_t grid, int block, int entries, hipStream_t s,
-                    Args... args) {
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), entries * sizeof(Entry), s, args...);
+void launch_entries(void (*kernel)(KArgs...), uint32_t grid, int block, int entries, int places,
+                    hipStream_t s, Args... args) {
+    const size_t bytes = entries * sizeof(Entry) + places * sizeof(IdTable::Place);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), bytes, s, args...);
+}
+int table_places(int k) {
+    if (k <= kWave) return 0;
+    int places = 2;
+    while (places < 2 * k) places *= 2;
+    return places;
 }
 
 }  // namespace
@@ -1737,7 +1810,7 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
             Part* part = reinterpret_cast<Part*>(scratch16);
             launch(k_part<Fmt, KEEP, false>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
                    static_cast<uint32_t>(plan.parts), static_cast<const int64_t*>(nullptr), part);
-            launch_entries(k_ds_merge<Fmt>, rows, kMergeThreads, k, s, a.x, cols, stride, a.scale, rows,
+            launch_entries(k_ds_merge<Fmt>, rows, kMergeThreads, k, 0, s, a.x, cols, stride, a.scale, rows,
                    tagged(ids, k), tagged(values, plan.parts), static_cast<const Part*>(part), stats);
             return;
         }
@@ -1746,7 +1819,7 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
                 const auto go = [&](auto g) {
                     constexpr int G = decltype(g)::value;
                     launch_entries(k_ds_group<Fmt, decltype(gr)::value, G>, grid, kBlockThreads,
-                                   kBlockThreads / G * k, s, tagged(a.x, cols), tagged(ids, cols >> 16),
+                                   kBlockThreads / G * k, 0, s, tagged(a.x, cols), tagged(ids, cols >> 16),
                                    tagged(values, k), tagged(stats, sc), tagged(weights, sc >> 16),
                                    tagged(grad, 0), stride, rows);
                 };
@@ -1758,7 +1831,7 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
             constexpr int T = decltype(team)::value;
             const auto step = [&](auto held) {
                 launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * 2 * k,
-                               s, tagged(a.x, cols),
+                               kTeamsPerBlock<T> * table_places(k), s, tagged(a.x, cols),
                        tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
                        tagged(weights, sc >> 16), tagged(grad, grid), stride, rows);
             };
@@ -1767,7 +1840,7 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
             else if (grad != nullptr)
                 step(Int<8>{});
             else
-                launch_entries(k_ds_team<Fmt, KEEP, T>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k, s, a.x, cols, stride, a.scale, rows,
+                launch_entries(k_ds_team<Fmt, KEEP, T>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k, 0, s, a.x, cols, stride, a.scale, rows,
                        static_cast<uint32_t>(k), ids, values, stats);
         });
     });

@@ -78,7 +78,8 @@ int64_t step_blocks(int64_t cap, int team) {
     return per_cu * cus < 65535 ? per_cu * cus : 65535;
 }
 
-// Teacher entries, at most, of a row left to one wavefront.
+// Teacher entries, at most, of a row left to one wavefront: four rows' entries and tables then take
+// 48 KiB of LDS.
 constexpr int kWaveEntries = 256;
 
 // What a plan is for.
@@ -119,7 +120,6 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
     }
     // a wavefront per row: up to four vectors per lane; in a distillation step up to the eight that
     // it holds ([19940,2312] f16, 291 vectors: 256 lanes 152 us, see the step's figures below)
-    // (not with so many entries that four rows' would fill the LDS)
     if (vecs <= (use == kDistillStep ? 512 : 256) && k <= kWaveEntries) {
         p->path = ARGREDUCE_PATH_SUBWAVE;
         p->team = 64;
