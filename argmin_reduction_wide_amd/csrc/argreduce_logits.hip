@@ -1132,9 +1132,10 @@ __device__ inline void own_student(Entry& mine, const uint8_t* row, uint32_t k, 
     if (k > kWave || lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
 }
 
-// How often each id occurs in a row of more than 64 entries: an open hash table in LDS of at least
-// twice as many places. Comparing every entry with every other took most of the time instead:
-// [11266,617] f16 229 us with 256 entries.
+// How often each id occurs in a row of more than kCompared entries: an open hash table in LDS of at
+// least twice as many places. Comparing every entry with every other took most of the time instead:
+// [11266,617] f16 with 256 entries 229 us, with the table 71.
+constexpr uint32_t kCompared = 16;
 struct IdTable {
     struct Place {
         int32_t id;
@@ -1142,7 +1143,7 @@ struct IdTable {
     };
     Place* place;
     uint32_t mask;
-    __device__ static uint32_t size(uint32_t k) { return k <= kWave ? 0 : 2u << (32 - __clz(k - 1)); }
+    __device__ static uint32_t size(uint32_t k) { return k <= kCompared ? 0 : 2u << (32 - __clz(k - 1)); }
     __device__ void clear(int lane, int team) const {
         for (uint32_t i = lane; i <= mask; i += team) place[i] = {-1, 0};
     }
@@ -1194,12 +1195,24 @@ __device__ inline Teacher teacher_row(Entry* ent, const IdTable& table, Entry mi
         mine.w = exp2_f(lw);
         q.entropy = lanes_sum<kWave>(spread(mine.id, mine.w, lw));
         if (TOTALS && lane < kWave) {
+            bool alone = false;
+            if (k > kCompared) {
+                table.clear(lane, kWave);
+                team_sync<kWave>();
+                table.add(mine.id);
+                team_sync<kWave>();
+                alone = table.once(mine.id);
+            }
+            mine.total = mine.w;
+            if (__any(!alone)) {
+                mine.total = 0.0f;
 #pragma unroll 8
-            for (uint32_t j = 0; j < k; ++j) {
-                const int32_t id = __builtin_amdgcn_readlane(mine.id, static_cast<int>(j));
-                const float w = __uint_as_float(
-                    __builtin_amdgcn_readlane(__float_as_uint(mine.w), static_cast<int>(j)));
-                mine.total += id == mine.id ? w : 0.0f;
+                for (uint32_t j = 0; j < k; ++j) {
+                    const int32_t id = __builtin_amdgcn_readlane(mine.id, static_cast<int>(j));
+                    const float w = __uint_as_float(
+                        __builtin_amdgcn_readlane(__float_as_uint(mine.w), static_cast<int>(j)));
+                    mine.total += id == mine.id ? w : 0.0f;
+                }
             }
         }
         if (static_cast<uint32_t>(lane) < k) ent[lane] = mine;
@@ -1709,7 +1722,7 @@ void launch_entries(void (*kernel)(KArgs...), uint32_t grid, int block, int entr
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), bytes, s, args...);
 }
 int table_places(int k) {
-    if (k <= kWave) return 0;
+    if (k <= static_cast<int>(kCompared)) return 0;
     int places = 2;
     while (places < 2 * k) places *= 2;
     return places;
