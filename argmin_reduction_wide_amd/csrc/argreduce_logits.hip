@@ -1132,37 +1132,40 @@ __device__ inline void own_student(Entry& mine, const uint8_t* row, uint32_t k, 
     if (k > kWave || lane < kWave) mine.x = student_at<Fmt>(row, mine.id, cols);
 }
 
-// How often each id occurs in a row of more than kCompared entries: an open hash table in LDS of at
-// least twice as many places. Comparing every entry with every other took most of the time instead:
-// [11266,617] f16 with 256 entries 229 us, with the table 71.
-constexpr uint32_t kCompared = 16;
+// Which ids of a row of more than kTeacherCompared entries occur more than once: an open hash table
+// in LDS of at least twice as many places. Comparing every entry with every other took most of the
+// time instead: [11266,617] f16 with 256 entries 229 us, with the table 71. A place holds an id, its
+// top bit set once the id has come again. (No id has all 31 bits set: ids are below cols <=
+// INT32_MAX, and cols itself, for ids beyond the row, is not entered.)
 struct IdTable {
-    struct Place {
-        int32_t id;
-        uint32_t count;
-    };
-    Place* place;
+    uint32_t* place;
     uint32_t mask;
-    __device__ static uint32_t size(uint32_t k) { return k <= kCompared ? 0 : 2u << (32 - __clz(k - 1)); }
-    __device__ void clear(int lane, int team) const {
-        for (uint32_t i = lane; i <= mask; i += team) place[i] = {-1, 0};
+    int32_t cols;
+    static constexpr uint32_t kFree = 0xffffffffu, kAgain = 0x80000000u;
+    __device__ static uint32_t size(uint32_t k) {
+        return k <= kTeacherCompared ? 0 : 2u << (32 - __clz(k - 1));  // as teacher_places
     }
+    __device__ void clear(int lane, int team) const {
+        for (uint32_t i = lane; i <= mask; i += team) place[i] = kFree;
+    }
+    __device__ bool entered(int32_t id) const { return id >= 0 && id < cols; }
     __device__ uint32_t first(int32_t id) const { return (static_cast<uint32_t>(id) * 0x9e3779b1u) >> 8 & mask; }
     __device__ void add(int32_t id) const {
-        if (id < 0) return;
-        uint32_t i = first(id);
-        while (true) {  // ends: there are more places than ids
-            const int32_t old = atomicCAS(&place[i].id, -1, id);
-            if (old == -1 || old == id) break;
-            i = (i + 1) & mask;
+        if (!entered(id)) return;
+        for (uint32_t i = first(id);; i = (i + 1) & mask) {  // ends: there are more places than ids
+            const uint32_t old = atomicCAS(&place[i], kFree, static_cast<uint32_t>(id));
+            if (old == kFree) return;
+            if ((old & ~kAgain) == static_cast<uint32_t>(id)) {
+                atomicOr(&place[i], kAgain);
+                return;
+            }
         }
-        atomicAdd(&place[i].count, 1u);
     }
     __device__ bool once(int32_t id) const {
-        if (id < 0) return true;
+        if (!entered(id)) return true;
         uint32_t i = first(id);
-        while (place[i].id != id) i = (i + 1) & mask;
-        return place[i].count == 1;
+        while ((place[i] & ~kAgain) != static_cast<uint32_t>(id)) i = (i + 1) & mask;
+        return place[i] < kAgain;
     }
 };
 
@@ -1196,7 +1199,7 @@ __device__ inline Teacher teacher_row(Entry* ent, const IdTable& table, Entry mi
         q.entropy = lanes_sum<kWave>(spread(mine.id, mine.w, lw));
         if (TOTALS && lane < kWave) {
             bool alone = false;
-            if (k > kCompared) {
+            if (k > kTeacherCompared) {
                 table.clear(lane, kWave);
                 team_sync<kWave>();
                 table.add(mine.id);
@@ -1547,9 +1550,9 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
     Entry* ent = s_entries + team_of<T>() * 2 * k;
     Entry* other = ent + k;
     const uint32_t places = IdTable::size(k);  // the tables lie behind all teams' entries
-    const IdTable table{reinterpret_cast<IdTable::Place*>(s_entries + kTeamsPerBlock<T> * 2 * k) +
+    const IdTable table{reinterpret_cast<uint32_t*>(s_entries + kTeamsPerBlock<T> * 2 * k) +
                             team_of<T>() * places,
-                        places - 1};
+                        places - 1, static_cast<int32_t>(cols)};
     const auto ids_at = [&](uint32_t n) { return addr<const int64_t>(ids_) + static_cast<size_t>(n) * k; };
     const auto values_at = [&](uint32_t n) { return addr<const float>(values_) + static_cast<size_t>(n) * k; };
     const auto row_at = [&](uint32_t n) { return row_ptr<Fmt>(addr<const void>(x), n, stride); };
@@ -1714,18 +1717,12 @@ template <typename... KArgs, typename... Args>
 void launch(void (*kernel)(KArgs...), uint32_t grid, int block, hipStream_t s, Args... args) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, s, args...);
 }
-// With LDS for the teacher's entries of the workgroup's rows, and their hash tables.
+// With LDS for the teacher's entries of the workgroup's rows, and a hash table for each.
+static_assert(sizeof(Entry) == kEntryBytes, "the plans count with it");
 template <typename... KArgs, typename... Args>
-void launch_entries(void (*kernel)(KArgs...), uint32_t grid, int block, int entries, int places,
-                    hipStream_t s, Args... args) {
-    const size_t bytes = entries * sizeof(Entry) + places * sizeof(IdTable::Place);
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), bytes, s, args...);
-}
-int table_places(int k) {
-    if (k <= static_cast<int>(kCompared)) return 0;
-    int places = 2;
-    while (places < 2 * k) places *= 2;
-    return places;
+void launch_entries(void (*kernel)(KArgs...), uint32_t grid, int block, size_t lds, hipStream_t s,
+                    Args... args) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), lds, s, args...);
 }
 
 }  // namespace
@@ -1823,7 +1820,7 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
             Part* part = reinterpret_cast<Part*>(scratch16);
             launch(k_part<Fmt, KEEP, false>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
                    static_cast<uint32_t>(plan.parts), static_cast<const int64_t*>(nullptr), part);
-            launch_entries(k_ds_merge<Fmt>, rows, kMergeThreads, k, 0, s, a.x, cols, stride, a.scale, rows,
+            launch_entries(k_ds_merge<Fmt>, rows, kMergeThreads, k * kEntryBytes, s, a.x, cols, stride, a.scale, rows,
                    tagged(ids, k), tagged(values, plan.parts), static_cast<const Part*>(part), stats);
             return;
         }
@@ -1832,7 +1829,7 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
                 const auto go = [&](auto g) {
                     constexpr int G = decltype(g)::value;
                     launch_entries(k_ds_group<Fmt, decltype(gr)::value, G>, grid, kBlockThreads,
-                                   kBlockThreads / G * k, 0, s, tagged(a.x, cols), tagged(ids, cols >> 16),
+                                   kBlockThreads / G * k * kEntryBytes, s, tagged(a.x, cols), tagged(ids, cols >> 16),
                                    tagged(values, k), tagged(stats, sc), tagged(weights, sc >> 16),
                                    tagged(grad, 0), stride, rows);
                 };
@@ -1843,8 +1840,8 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
         with_team(plan.team, [&](auto team) {
             constexpr int T = decltype(team)::value;
             const auto step = [&](auto held) {
-                launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * 2 * k,
-                               kTeamsPerBlock<T> * table_places(k), s, tagged(a.x, cols),
+                launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>, step_lds(kTeamsPerBlock<T>, k),
+                               s, tagged(a.x, cols),
                        tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
                        tagged(weights, sc >> 16), tagged(grad, grid), stride, rows);
             };
@@ -1853,7 +1850,8 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
             else if (grad != nullptr)
                 step(Int<8>{});
             else
-                launch_entries(k_ds_team<Fmt, KEEP, T>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k, 0, s, a.x, cols, stride, a.scale, rows,
+                launch_entries(k_ds_team<Fmt, KEEP, T>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k * kEntryBytes,
+                               s, a.x, cols, stride, a.scale, rows,
                        static_cast<uint32_t>(k), ids, values, stats);
         });
     });

@@ -15,6 +15,17 @@ constexpr int kTeacherMax = 1024;      // teacher entries per row (ARGREDUCE_TEA
 constexpr int kPartThreads = 256;      // threads of a workgroup that scans a slice of a row
 constexpr int kPartUnroll = 4;         // 16-byte loads each of its lanes keeps in flight
 constexpr int kMaxParts = 256;         // slices of a row
+constexpr size_t kEntryBytes = 16;     // LDS of one teacher entry
+constexpr int kTeacherCompared = 16;   // more teacher entries than this get a hash table in LDS
+inline int teacher_places(int k) {
+    int n = 2;
+    while (n < 2 * k) n *= 2;
+    return k <= kTeacherCompared ? 0 : n;
+}
+// LDS of a workgroup of the distillation step: the entries of two rows and a table for each team.
+inline size_t step_lds(int teams, int k) {
+    return teams * (2 * k * kEntryBytes + teacher_places(k) * sizeof(uint32_t));
+}
 
 // How the rows of one forward call are scanned.
 struct LogitsPlan {

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int64_t kBlock = 256;
 constexpr int64_t kThreadsPerCu = 2048;
+constexpr int64_t kLdsPerCu = 160 * 1024;
 // Logits of up to this size are left in the 256 MiB Infinity Cache (struct Span; at 125 MiB, [512,128256]
 // f16, the forward pass takes 25.7 us with them left there, 23.0 without).
 constexpr int64_t kKeepBytes = int64_t{64} << 20;
@@ -70,16 +71,19 @@ bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p)
 // A device array of `n`-byte elements that a call with rows > 0 needs.
 bool usable(const void* p, uintptr_t n) { return p != nullptr && aligned(p, n) && fits48(p); }
 
-// Workgroups of the distillation step: as many as its registers (at most 128 per lane) let the
-// CUs hold at once; each goes through several rows. The kernel takes the number in 16 bits.
-int64_t step_blocks(int64_t cap, int team) {
-    const int64_t per_cu = team == 1024 ? 1 : team == 512 ? 2 : 4;
+// Workgroups of the distillation step: as many as its registers (at most 128 per lane) and LDS let
+// the CUs hold at once; each goes through several rows. The kernel takes the number in 16 bits.
+int64_t step_blocks(int64_t cap, int team, int k) {
+    int64_t per_cu = team == 1024 ? 1 : team == 512 ? 2 : 4;
+    const int64_t lds = static_cast<int64_t>(step_lds(team == 64 ? kBlock / 64 : 1, k)) + 1024;
+    per_cu = std::min(per_cu, kLdsPerCu / lds);
     const int64_t cus = cap / kThreadsPerCu > 0 ? cap / kThreadsPerCu : 1;
     return per_cu * cus < 65535 ? per_cu * cus : 65535;
 }
 
 // Teacher entries, at most, of a row left to one wavefront: four rows' entries and tables then take
-// 48 KiB of LDS.
+// 40 KiB of LDS. (A workgroup per row has a lane for each entry, and is slower: [21454,251] f16 with
+// 130 entries, loss and gradient, 64 us by a wavefront, 153 by 256 lanes.)
 constexpr int kWaveEntries = 256;
 
 // What a plan is for.
@@ -126,7 +130,7 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
         p->grid_blocks = ceil_div(rows1, kBlock / 64);
         if (rows1 * 64 >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
         if (use == kDistillStep) {
-            const int64_t most = step_blocks(cap, p->team);
+            const int64_t most = step_blocks(cap, p->team, k);
             p->held = 8;
             p->grid_blocks = p->grid_blocks < most ? p->grid_blocks : most;
         }
@@ -163,7 +167,7 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
     p->grid_blocks = rows1;
     if (rows1 * p->team >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
     if (use == kDistillStep) {
-        const int64_t most = step_blocks(cap, p->team);
+        const int64_t most = step_blocks(cap, p->team, k);
         p->held = vecs > 8 * p->team ? 16 : 8;
         p->grid_blocks = rows1 < most ? rows1 : most;
     }
