@@ -1169,6 +1169,36 @@ struct IdTable {
     }
 };
 
+// The totals of a row's entries in LDS, each the sum in the entries' order. Few ids are there twice:
+// a wavefront takes those of its entries one after the other and looks the row through for them,
+// 64 entries at a time. ([4096,32000] bf16 with 1024 random ids, about 16 of them there already, loss
+// and gradient: 1036 us with a lane per entry adding its row up, 301 so.)
+template <int T>
+__device__ inline void entry_totals(Entry* ent, const IdTable& table, uint32_t k, int lane) {
+    const uint32_t l = lane % kWave;
+    for (uint32_t base = lane - l; base < k; base += T) {
+        const uint32_t i = base + l;
+        const int32_t id = i < k ? ent[i].id : -1;
+        float total = i < k ? ent[i].w : 0.0f;
+        uint64_t todo = __ballot(table.entered(id) && (k <= kTeacherCompared || !table.once(id)));
+        while (todo != 0) {
+            const int32_t one = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+            float sum = 0.0f;
+            for (uint32_t c = 0; c < k; c += kWave) {
+                const uint32_t j = c + l < k ? c + l : k - 1;
+                const float w = ent[j].w;
+                uint64_t hits = __ballot(c + l < k && ent[j].id == one);
+                for (; hits != 0; hits &= hits - 1)
+                    sum += __uint_as_float(
+                        __builtin_amdgcn_readlane(__float_as_uint(w), __builtin_ctzll(hits)));
+            }
+            if (id == one) total = sum;
+            todo &= ~__ballot(id == one);
+        }
+        if (i < k) ent[i].total = total;
+    }
+}
+
 // The teacher's row: its entries into `ent`, the distribution's numbers to every thread. *bad: the
 // whole gradient is NaN (a weight is NaN, or an id with weight lies beyond the row). With TOTALS the
 // totals too: each the sum of the weights with its id, in the entries' order. Up to 64 entries take
@@ -1256,16 +1286,7 @@ __device__ inline Teacher teacher_row(Entry* ent, const IdTable& table, Entry mi
     if constexpr (TOTALS) {
         if (k > kWave) {  // (the last reduction's barrier has made the table and the weights visible)
             if constexpr (T == kWave) team_sync<T>();
-            for (uint32_t i = lane; i < k; i += T) {
-                const int32_t id = ent[i].id;
-                float w = ent[i].w;
-                if (!table.once(id)) {
-                    w = 0.0f;
-#pragma unroll 4
-                    for (uint32_t j = 0; j < k; ++j) w += ent[j].id == id ? ent[j].w : 0.0f;
-                }
-                ent[i].total = w;
-            }
+            entry_totals<T>(ent, table, k, lane);
         }
     }
     *bad = s != s || q.entropy != q.entropy;
@@ -1282,6 +1303,15 @@ __device__ inline void store_distill(float* stats, uint32_t rows, uint32_t r, fl
     stats[4 * n + r] = q.l2;
 }
 
+// sum q ln p is added up in units of 2^8: weights that add up to a little more than 1 would take a
+// row whose every weight lies on logits of the lowest finite value (a mask) out of range. Infinite
+// is only the loss of a row with a logit of -inf at a weight.
+constexpr float kLossUnit = 0x1p-8f;
+__device__ inline float loss_of(const Teacher& q, float sum) {
+    const float v = sum * (1.0f / kLossUnit);
+    return -q.entropy - (sum > -__builtin_huge_valf() ? max_f(v, kLowest) : v);
+}
+
 // The loss of a row from its merged statistics and log2 of their sum (in lane 0 of the team).
 template <int T>
 __device__ inline float distill_loss(const Entry* ent, uint32_t k, float scale, const Teacher& q,
@@ -1291,30 +1321,10 @@ __device__ inline float distill_loss(const Entry* ent, uint32_t k, float scale, 
         const Entry e = ent[i];
         if (e.id < 0 || e.w == 0.0f) continue;
         const float lp = a.s == 0.0f ? -__builtin_huge_valf() : ln_p(e.x, a.m, l2, scale);
-        sum = fmaf(e.w, lp, sum);
+        sum = fmaf(e.w, lp * kLossUnit, sum);
     }
     sum = k <= kWave ? lanes_sum<kWave>(sum) : team_reduce<T, false>(sum, lane, sh, kSlotLoss);
-    return -q.entropy - sum;
-}
-
-// The gradient of a row is g (p_j - q_j) / T. The dense part g p_j / T is stored first; after it
-// (and a barrier) each teacher entry's element is stored again with its weight taken off: the sum
-// of the weights of equal ids, which every one of them computes in the same order.
-template <typename Fmt, typename Holds>
-__device__ inline void distill_take_off(const uint8_t* x, uint8_t* g, uint32_t cols, const int64_t* ids,
-                                        const float* values, uint32_t k, float scale, float coef,
-                                        float m, float l2, const Teacher& q, int lane, int team,
-                                        Holds holds) {
-    for (uint32_t i = lane; i < k; i += team) {
-        const int64_t id = ids[i];
-        if (id < 0 || id >= static_cast<int64_t>(cols) || !holds(id)) continue;
-        float w = 0.0f;
-#pragma unroll 8
-        for (uint32_t j = 0; j < k; ++j)
-            if (ids[j] == id) w += q.weight(values[j], scale);
-        const float p = exp2_f(fmaf(Fmt::load1(x + id * Fmt::kSize) - m, scale, -l2));
-        reinterpret_cast<typename Fmt::Bits*>(g)[id] = round_to<Fmt>(coef * (p - w));
-    }
+    return loss_of(q, sum);
 }
 
 template <typename Fmt, bool KEEP, int T>
@@ -1421,11 +1431,11 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_group(uint64_t x, uint64_t
         const Entry t = ent[i];
         if (t.id < 0 || t.w == 0.0f) continue;
         const float lp = a.s == 0.0f ? -__builtin_huge_valf() : ln_p(t.x, a.m, l2, scale);
-        sum = fmaf(t.w, lp, sum);
+        sum = fmaf(t.w, lp * kLossUnit, sum);
     }
     sum = lanes_sum<G>(sum);
     if (lane == 0 && !extra)
-        store_distill(addr<float>(stats_), rows, r, absent ? 0.0f : -q.entropy - sum, absent ? 0.0f : a.m,
+        store_distill(addr<float>(stats_), rows, r, absent ? 0.0f : loss_of(q, sum), absent ? 0.0f : a.m,
                       absent ? 0.0f : l2, q);
     if constexpr (GRAD) {
         if (extra) return;
@@ -1488,41 +1498,81 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
     if (lane == 0) store_distill(stats, rows, r, loss, a.m, l2, q);
 }
 
-// Tags: columns in (x, ids), teacher entries in values, scale in (stats, g), log2 of the team's
-// lanes and the slices (12 bits above 4) in grad.
-template <typename Fmt, bool WIDE>
+// The gradient of a row: g (p_j - q_j) / T. The dense part g p_j / T is stored first; after it each
+// teacher entry's element is stored again with its weight taken off: the sum of the weights of equal
+// ids, which every one of them stores. A team of T lanes (32: of 2^lg, up to 32) for a slice of a
+// row has the slice's entries in LDS. [4096,128256] bf16 with 64 entries: 421 us, 5.0 TB/s read and
+// written, bound by that; [4096,32000] with 1024 268 us, bound by the entries (553 and 7958 us with
+// each entry compared with all others from global memory). Tags: columns in (x, ids), teacher entries in values, scale in
+// (stats, g), lg and the slices (12 bits above 4) in grad.
+template <typename Fmt, int T>
 __global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t ids_, uint64_t values_,
                                                            uint64_t stats_, uint64_t g, uint64_t grad,
                                                            uint32_t stride, uint32_t rows) {
+    constexpr int VW = Fmt::VW;
+    constexpr bool kWide = T == kBlockThreads;
     const uint32_t cols = tags(x, ids_), k = tag(values_);
     const float scale = __uint_as_float(tags(stats_, g));
-    const uint32_t lg = WIDE ? 8 : tag(grad) & 15, slices = tag(grad) >> 4;
-    const uint32_t unit = WIDE ? blockIdx.x : (blockIdx.x << (8 - lg)) + (threadIdx.x >> lg);
-    const uint32_t want = WIDE ? unit / slices : unit;
-    const bool extra = want >= rows;  // keeps the workgroup's barrier whole
-    const uint32_t r = extra ? rows - 1 : want;
-    const int lane = threadIdx.x & ((1u << lg) - 1);
+    const uint32_t lg = kWide ? 8 : T == kWave ? 6 : tag(grad) & 15, slices = kWide ? tag(grad) >> 4 : 1;
+    const uint32_t team = kWide ? 0 : T == kWave ? team_of<kWave>() : threadIdx.x >> lg;
+    const uint32_t unit = kWide ? blockIdx.x : (blockIdx.x << (8 - lg)) + team;
+    const uint32_t r = kWide ? unit / slices : unit;
+    if (r >= rows) return;  // whole teams, and never one of several wavefronts
+    const uint32_t lanes = 1u << lg;
+    const int lane = threadIdx.x & (lanes - 1);
     const float* stats = addr<const float>(stats_);
     const size_t n = rows;
     const float m = stats[n + r], l2 = stats[2 * n + r];
     const Teacher q{stats[3 * n + r], stats[4 * n + r], 0.0f};
     const float coef = addr<const float>(g)[r] * scale * kLn2;
-    GradSlice<Fmt> gs(row_ptr<Fmt>(addr<const void>(x), r, stride),
-                      const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad), r, cols)), cols,
-                      WIDE ? unit - want * slices : 0, slices);
-    if (extra) gs.first = gs.last = 0;
+    const GradSlice<Fmt> gs(row_ptr<Fmt>(addr<const void>(x), r, stride),
+                            const_cast<uint8_t*>(row_ptr<Fmt>(addr<void>(grad), r, cols)), cols,
+                            kWide ? unit - r * slices : 0, slices);
     const bool zero = q.m == -__builtin_huge_valf() || l2 == -__builtin_huge_valf();
-    const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
-    const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
-    constexpr int VW = Fmt::VW;
-    gs.write(lane, 1 << lg, zero, [&](const float (&e)[VW], uint32_t, float (&d)[VW]) {
+    Entry* ent = s_entries + team * k;
+    const uint32_t places = T == 32 ? 0 : IdTable::size(k);  // the tables lie behind all teams' entries
+    const IdTable table{reinterpret_cast<uint32_t*>(s_entries + (kBlockThreads >> lg) * k) + team * places,
+                        places - 1, static_cast<int32_t>(cols)};
+    if (!zero) {
+        const int64_t* ids = addr<const int64_t>(ids_) + static_cast<size_t>(r) * k;
+        const float* values = addr<const float>(values_) + static_cast<size_t>(r) * k;
+        if (places != 0) {
+            table.clear(lane, lanes);
+            if constexpr (T > 32) team_sync<T>();
+        }
+        for (uint32_t i = lane; i < k; i += lanes) {
+            const int64_t id = ids[i];
+            const bool in = id >= 0 && id < static_cast<int64_t>(cols) && gs.holds(id);
+            Entry t{in ? static_cast<int32_t>(id) : -1, 0.0f, 0.0f, 0.0f};
+            if (in) {
+                t.w = q.weight(values[i], scale);
+                t.x = Fmt::load1(gs.x + id * Fmt::kSize);
+            }
+            ent[i] = t;
+            if (places != 0) table.add(t.id);
+        }
+    }
+    gs.write(lane, lanes, zero, [&](const float (&e)[VW], uint32_t, float (&d)[VW]) {
 #pragma unroll
         for (int i = 0; i < VW; ++i) d[i] = coef * exp2_f(fmaf(e[i] - m, scale, -l2));
     });
-    __syncthreads();
-    if (!zero)
-        distill_take_off<Fmt>(gs.x, gs.g, cols, ids, values, k, scale, coef, m, l2, q, lane, 1 << lg,
-                              [&](int64_t id) { return gs.holds(id); });
+    // the dense stores before those of the entries: a wavefront's own keep their order
+    if constexpr (kWide)
+        __syncthreads();
+    else
+        team_sync<kWave>();
+    if (zero) return;
+    if constexpr (T > 32) entry_totals<T>(ent, table, k, lane);
+    for (uint32_t i = lane; i < k; i += lanes) {
+        Entry t = ent[i];
+        if (t.id < 0) continue;
+        if constexpr (T == 32) {
+#pragma unroll 4
+            for (uint32_t j = 0; j < k; ++j) t.total += ent[j].id == t.id ? ent[j].w : 0.0f;
+        }
+        const float p = exp2_f(fmaf(t.x - m, scale, -l2));
+        reinterpret_cast<typename Fmt::Bits*>(gs.g)[t.id] = round_to<Fmt>(coef * (p - t.total));
+    }
 }
 
 // Loss and gradient of a row in one kernel. A lane keeps its first NV vectors in registers from
@@ -1796,13 +1846,21 @@ hipError_t launch_distill_grad(const GradPlan& plan, const LogitsArgs& a, int k,
     const uint32_t cols = static_cast<uint32_t>(a.cols), sc = bits_of(a.scale);
     with_format(a.dtype, [&](auto fmt) {
         using Fmt = decltype(fmt);
-        with_bool(plan.team == kBlockThreads, [&](auto wide) {
-            launch(k_ds_grad<Fmt, decltype(wide)::value>, static_cast<uint32_t>(plan.grid_blocks),
-                   kBlockThreads, s, tagged(a.x, cols), tagged(ids, cols >> 16), tagged(values, k),
-                   tagged(stats, sc), tagged(g_loss, sc >> 16),
-                   tagged(grad, log2_of(plan.team) | (plan.slices << 4)),
-                   static_cast<uint32_t>(a.row_stride), static_cast<uint32_t>(a.rows));
-        });
+        const auto go = [&](auto team) {
+            constexpr int T = decltype(team)::value;
+            const int teams = kBlockThreads / plan.team;
+            launch_entries(k_ds_grad<Fmt, T>, static_cast<uint32_t>(plan.grid_blocks), kBlockThreads,
+                           entries_lds(teams, 1, k, T > 32), s, tagged(a.x, cols), tagged(ids, cols >> 16),
+                           tagged(values, k), tagged(stats, sc), tagged(g_loss, sc >> 16),
+                           tagged(grad, log2_of(plan.team) | (plan.slices << 4)),
+                           static_cast<uint32_t>(a.row_stride), static_cast<uint32_t>(a.rows));
+        };
+        if (plan.team == kBlockThreads)
+            go(Int<kBlockThreads>{});
+        else if (plan.team == kWave)
+            go(Int<kWave>{});
+        else
+            go(Int<32>{});
     });
     return hipGetLastError();
 }
@@ -1840,7 +1898,7 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
         with_team(plan.team, [&](auto team) {
             constexpr int T = decltype(team)::value;
             const auto step = [&](auto held) {
-                launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>, step_lds(kTeamsPerBlock<T>, k),
+                launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>, entries_lds(kTeamsPerBlock<T>, 2, k, true),
                                s, tagged(a.x, cols),
                        tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
                        tagged(weights, sc >> 16), tagged(grad, grid), stride, rows);

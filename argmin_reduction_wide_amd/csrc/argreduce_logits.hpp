@@ -22,9 +22,10 @@ inline int teacher_places(int k) {
     while (n < 2 * k) n *= 2;
     return k <= kTeacherCompared ? 0 : n;
 }
-// LDS of a workgroup of the distillation step: the entries of two rows and a table for each team.
-inline size_t step_lds(int teams, int k) {
-    return teams * (2 * k * kEntryBytes + teacher_places(k) * sizeof(uint32_t));
+// LDS of a workgroup for the entries of `rows` teacher rows of each of its teams, and for a table
+// of each team.
+inline size_t entries_lds(int teams, int rows, int k, bool tables) {
+    return teams * (rows * k * kEntryBytes + (tables ? teacher_places(k) * sizeof(uint32_t) : 0));
 }
 
 // How the rows of one forward call are scanned.

@@ -53,7 +53,7 @@ int check_logits(const void* x, int dtype, int64_t rows, int64_t cols, int64_t s
                  float temperature, LogitsArgs* a) {
     const int rc = check_logits_shape(dtype, rows, cols);
     if (rc != ARGREDUCE_OK) return rc;
-    if (stride > std::numeric_limits<uint32_t>::max()) return ARGREDUCE_ERR_TOO_WIDE;
+    if (rows > 1 && stride > std::numeric_limits<uint32_t>::max()) return ARGREDUCE_ERR_TOO_WIDE;
     if (rows > 1 && stride < cols) return ARGREDUCE_ERR_INVALID_ARG;
     // powers of two far inside the range of a float: log2(e) / T and its products stay normal
     if (!(temperature >= 0x1p-60f && temperature <= 0x1p60f)) return ARGREDUCE_ERR_INVALID_ARG;
@@ -61,7 +61,7 @@ int check_logits(const void* x, int dtype, int64_t rows, int64_t cols, int64_t s
         return ARGREDUCE_ERR_INVALID_ARG;
     *a = LogitsArgs{x, dtype, rows, cols, rows > 1 ? stride : cols,
                     static_cast<float>(1.4426950408889634 / static_cast<double>(temperature)),
-                    rows * cols * logits_elem_size(dtype) <= kKeepBytes};
+                    rows <= kKeepBytes / logits_elem_size(dtype) / cols};
     return ARGREDUCE_OK;
 }
 
@@ -75,7 +75,7 @@ bool usable(const void* p, uintptr_t n) { return p != nullptr && aligned(p, n) &
 // the CUs hold at once; each goes through several rows. The kernel takes the number in 16 bits.
 int64_t step_blocks(int64_t cap, int team, int k) {
     int64_t per_cu = team == 1024 ? 1 : team == 512 ? 2 : 4;
-    const int64_t lds = static_cast<int64_t>(step_lds(team == 64 ? kBlock / 64 : 1, k)) + 1024;
+    const int64_t lds = static_cast<int64_t>(entries_lds(team == 64 ? kBlock / 64 : 1, 2, k, true)) + 1024;
     per_cu = std::min(per_cu, kLdsPerCu / lds);
     const int64_t cus = cap / kThreadsPerCu > 0 ? cap / kThreadsPerCu : 1;
     return per_cu * cus < 65535 ? per_cu * cus : 65535;
@@ -174,16 +174,23 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
     return ARGREDUCE_OK;
 }
 
-int make_grad_plan(int dtype, int64_t rows, int64_t cols, GradPlan* p) {
+// `k`: teacher entries (0: none).
+int make_grad_plan(int dtype, int64_t rows, int64_t cols, int k, GradPlan* p) {
     const int64_t vecs = span_vecs(cols, logits_elem_size(dtype));
     const int64_t rows1 = rows > 0 ? rows : 1;
-    const int64_t team = next_pow2(vecs);
+    int64_t team = next_pow2(vecs);
+    if (k > 0) {
+        // the team's LDS holds the entries: at most four to a lane, and beyond 32 lanes a wavefront
+        // or a workgroup, by the forward pass's rules
+        team = std::max<int64_t>(team, next_pow2(ceil_div(k, 4)));
+        if (team > 32) team = vecs <= 256 && k <= kWaveEntries ? 64 : kBlock;
+    }
     p->team = static_cast<int>(team < kBlock ? team : kBlock);
     p->slices = 1;
-    if (team > kBlock) {
-        // four vectors to a thread
-        int64_t slices = ceil_div(vecs, kBlock * 4);
-        p->slices = static_cast<int>(slices < 4095 ? slices : 4095);
+    if (p->team == kBlock) {
+        // four vectors to a thread, with many teacher entries more: every slice goes through them
+        const int64_t each = std::max(4, k / 64);
+        p->slices = static_cast<int>(std::min<int64_t>(ceil_div(vecs, kBlock * each), 4095));
     }
     p->grid_blocks = ceil_div(rows1 * p->slices, kBlock / p->team);
     if (p->grid_blocks * kBlock >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
@@ -240,7 +247,7 @@ int distill(const LogitsArgs& a, int32_t k, const int64_t* ids, const float* val
     GradPlan g;
     int rc = make_logits_plan(a.dtype, a.rows, a.cols, grad != nullptr ? kDistillStep : kDistill, k, vec_rows(a), &p);
     if (rc != ARGREDUCE_OK) return rc;
-    rc = make_grad_plan(a.dtype, a.rows, a.cols, &g);
+    rc = make_grad_plan(a.dtype, a.rows, a.cols, k, &g);
     if (rc != ARGREDUCE_OK) return rc;
     uint8_t* scratch16 = nullptr;
     rc = scratch_of(p, scratch, scratch_bytes, &scratch16);
@@ -313,7 +320,7 @@ ARGREDUCE_EXPORT int argreduce_logprobs_grad(const void* x, argreduce_dtype_t dt
         (grad_entropy != nullptr && !usable(grad_entropy, 4)))
         return ARGREDUCE_ERR_INVALID_ARG;
     GradPlan g;
-    rc = make_grad_plan(dtype, rows, cols, &g);
+    rc = make_grad_plan(dtype, rows, cols, 0, &g);
     if (rc != ARGREDUCE_OK) return rc;
     return status_of(launch_logprobs_grad(g, a, tokens, stats, grad_logprob, grad_entropy, grad,
                                           static_cast<hipStream_t>(stream)));
@@ -366,7 +373,7 @@ ARGREDUCE_EXPORT int argreduce_distill_grad(const void* x, argreduce_dtype_t dty
     if (!usable(grad_loss, 4) || !usable(grad, static_cast<uintptr_t>(logits_elem_size(dtype))))
         return ARGREDUCE_ERR_INVALID_ARG;
     GradPlan g;
-    rc = make_grad_plan(dtype, rows, cols, &g);
+    rc = make_grad_plan(dtype, rows, cols, k, &g);
     if (rc != ARGREDUCE_OK) return rc;
     return status_of(launch_distill_grad(g, a, k, teacher_tokens, teacher_logits, stats, grad_loss, grad,
                                          static_cast<hipStream_t>(stream)));

@@ -134,7 +134,7 @@ def _failed(rc: int, what: str, rows, cols, stride):
     return B.ArgreduceError(rc, f"argreduce_{what}(rows={rows}, cols={cols}, row_stride={stride})")
 
 
-def _refuse_captured_autograd(logits) -> None:
+def _refuse_captured_autograd() -> None:
     """An autograd graph recorded while a HIP graph is captured can share gradient accumulators
     with an eager one, which ends the process when the engine joins their streams."""
     if torch.cuda.is_current_stream_capturing():
@@ -193,6 +193,7 @@ class _TokenLogprobs(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, g_logprob, g_entropy, *_):
         logits, tokens, stats = ctx.saved_tensors
+        _refuse_captured_autograd()
         if g_logprob is None and g_entropy is None:
             return (None,) * 6
         lead = logits.shape[:-1]
@@ -215,7 +216,7 @@ def token_logprobs(logits, tokens, *, temperature: float = 1.0, entropy: bool = 
 
     Differentiable in logprob and entropy (float32) when the logits require a gradient."""
     if logits.requires_grad and torch.is_grad_enabled():
-        _refuse_captured_autograd(logits)
+        _refuse_captured_autograd()
         return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, bool(entropy), top,
                                                    scratch))
     stats, lp, tok = _logprobs(logits, tokens, temperature, entropy, top, scratch)
@@ -225,12 +226,15 @@ def token_logprobs(logits, tokens, *, temperature: float = 1.0, entropy: bool = 
     return TokenLogprobs(stats[0].view(lead), stats[1].view(lead) if entropy else None, lp, tok, stats)
 
 
-def _grad_out(logits, out):
+def _grad_out(logits, rows, cols, stride, out):
     if out is None:
         return torch.empty(*logits.shape, dtype=logits.dtype, device=logits.device)
     B._check_buffer(out, "out", logits.device, logits.dtype, logits.numel())
     if out.shape != logits.shape:
         raise ValueError(f"out must have shape {tuple(logits.shape)}; got {tuple(out.shape)}")
+    size, x, g = logits.element_size(), logits.data_ptr(), out.data_ptr()
+    if rows > 0 and g < x + ((rows - 1) * stride + cols) * size and x < g + rows * cols * size:
+        raise ValueError("out must not overlap the logits")
     return out
 
 
@@ -249,7 +253,7 @@ def token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy=None, 
     if grad_entropy is not None:
         _same(grad_entropy, "grad_entropy", logits, torch.float32, lead)
     temperature = _temperature(temperature)
-    out = _grad_out(logits, out)
+    out = _grad_out(logits, rows, cols, stride, out)
     if _elsewhere(logits):
         with torch.cuda.device(logits.device):
             return token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy,
@@ -313,6 +317,7 @@ class _DistillLoss(torch.autograd.Function):
         if g_loss is None:
             return (None,) * 5
         logits, teacher_tokens, teacher_logits, stats = ctx.saved_tensors
+        _refuse_captured_autograd()
         grad = distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, g_loss.contiguous(),
                                  temperature=ctx.temperature)
         return grad, None, None, None, None
@@ -329,7 +334,7 @@ def distill_loss(logits, teacher_tokens, teacher_logits, *, temperature: float =
 
     Differentiable in the loss when the logits require a gradient; the teacher is a constant."""
     if logits.requires_grad and torch.is_grad_enabled():
-        _refuse_captured_autograd(logits)
+        _refuse_captured_autograd()
         return DistillLoss(*_DistillLoss.apply(logits, teacher_tokens, teacher_logits, temperature,
                                                scratch))
     stats = _distill(logits, teacher_tokens, teacher_logits, temperature, scratch)
@@ -346,7 +351,7 @@ def distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss, 
     _same(stats, "stats", logits, torch.float32, (5, rows))
     _same(grad_loss, "grad_loss", logits, torch.float32, logits.shape[:-1])
     temperature = _temperature(temperature)
-    out = _grad_out(logits, out)
+    out = _grad_out(logits, rows, cols, stride, out)
     if _elsewhere(logits):
         with torch.cuda.device(logits.device):
             return distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss,
@@ -369,7 +374,7 @@ def distill_step(logits, teacher_tokens, teacher_logits, weights, *, temperature
     k = _teacher(logits, teacher_tokens, teacher_logits)
     _same(weights, "weights", logits, torch.float32, logits.shape[:-1])
     temperature = _temperature(temperature)
-    out = _grad_out(logits, out)
+    out = _grad_out(logits, rows, cols, stride, out)
     if _elsewhere(logits):
         with torch.cuda.device(logits.device):
             return distill_step(logits, teacher_tokens, teacher_logits, weights,

@@ -667,3 +667,140 @@ def test_run_together():
     want = (p * live[:, None] - q) / 2 / rows
     # |logits| < 40 / 2: z is off by 3 u 60, the sums by 600 u (logits_reference), times p or q <= 1
     assert (grad.double() - want).abs().max() < R.U * 1000 / rows
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("rows,cols,k", [(40, 17, 128), (70, 17, 8), (9, 150, 256), (9, 2000, 200), (12, 2000, 257),
+                                         (30, 600, 300), (5, 33000, 1024), (5, 33000, 17), (3, 150001, 1000)])
+def test_distill_with_many_equal_ids(dtype, rows, cols, k):
+    """Ids from a small part of the row, every one of them there several times, some absent."""
+    announce(f"equal ids {dtype} [{rows},{cols}] k={k}")
+    rng = np.random.default_rng(rows + cols + k)
+    x = make_rows(rng, rows, cols, dtype)
+    ids = rng.integers(0, max(1, min(cols, k) // 5), size=(rows, k)) + rng.integers(0, cols - min(cols, k) // 5 + 1)
+    ids[rng.random(size=ids.shape) < 0.1] = -1
+    ids = torch.from_numpy(np.minimum(ids, cols - 1)).cuda()
+    ids[0] = cols - 1  # one id alone
+    v = torch.from_numpy(rng.normal(size=(rows, k))).float().cuda()
+    check_distill(x, ids, v, dtype, 1.0, rng)
+
+
+def test_single_row_and_single_dimension():
+    announce("one row")
+    rng = np.random.default_rng(31)
+    buf = torch.from_numpy(rng.normal(size=(1, 5000)) * 2).float().cuda()
+    x = buf.as_strided((1, 5000), (2 ** 33, 1))  # the stride of a row that has no next one
+    tokens = torch.tensor([17], device="cuda")
+    got = check_logprobs(x, tokens, "f32", 1.0, True, 3)
+    check_logprobs_grad(x, tokens, "f32", 1.0, True, *got, rng)
+    ids, v = make_teacher(rng, 1, 5000, 70)
+    check_distill(x, ids, v, "f32", 1.0, rng)
+    loss, grad = ar.distill_step(x, ids, v, torch.ones(1, device="cuda"))
+    loss1, grad1 = ar.distill_step(buf[0], ids[0], v[0], torch.ones((), device="cuda"))
+    assert loss1.shape == () and grad1.shape == (5000,)
+    assert loss1 == loss[0] and torch.equal(grad1, grad[0])
+
+
+def test_gradient_over_the_logits_is_refused():
+    announce("overlap")
+    buf = torch.zeros(100, device="cuda")
+    x, t = buf[:32].view(4, 8), torch.zeros(4, dtype=torch.int64, device="cuda")
+    ids, v, w = t.view(4, 1), torch.zeros(4, 1, device="cuda"), torch.zeros(4, device="cuda")
+    for out in (x, buf[31:63].view(4, 8)):
+        with pytest.raises(ValueError, match="overlap"):
+            ar.token_logprobs_grad(x, t, torch.zeros(4, 4, device="cuda"), w, out=out)
+        with pytest.raises(ValueError, match="overlap"):
+            ar.distill_loss_grad(x, ids, v, torch.zeros(5, 4, device="cuda"), w, out=out)
+        with pytest.raises(ValueError, match="overlap"):
+            ar.distill_step(x, ids, v, w, out=out)
+    ar.distill_step(x, ids, v, w, out=buf[32:64].view(4, 8))
+
+
+def test_backward_in_a_capture_is_refused(monkeypatch):
+    """(The capture is feigned: what torch does with one whose graph was recorded eagerly is its own.)"""
+    announce("backward while capturing")
+    x = torch.randn(3, 100, device="cuda", requires_grad=True)
+    ids = torch.zeros(3, 2, dtype=torch.int64, device="cuda")
+    lp = ar.token_logprobs(x, ids[:, 0].contiguous()).logprob.sum()
+    loss = ar.distill_loss(x, ids, torch.zeros(3, 2, device="cuda")).loss.sum()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    for y in (lp, loss):
+        with pytest.raises(RuntimeError, match="captured"):
+            y.backward()
+
+
+@pytest.mark.parametrize("rows,cols,k", [(50, 200, 100), (300, 2000, 200), (300, 20000, 100), (4, 202048, 300)])
+def test_distill_on_two_streams_and_captured(rows, cols, k):
+    """distill_step with tables of ids: calls side by side, and replays on new teachers."""
+    announce(f"distill streams [{rows},{cols}] k={k}")
+    g = torch.Generator(device="cuda").manual_seed(k)
+    xs = [torch.randn(rows, cols, device="cuda", generator=g).half() for _ in range(2)]
+    ids = torch.randint(-1, min(cols, 3 * k), (rows, k), device="cuda", generator=g)
+    v, w = torch.randn(rows, k, device="cuda", generator=g), torch.rand(rows, device="cuda", generator=g)
+
+    def work(x):
+        d = ar.distill_loss(x, ids, v)
+        return [*ar.distill_step(x, ids, v, w), d.stats, ar.distill_loss_grad(x, ids, v, d.stats, w)]
+
+    want = [work(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(5):
+        for n, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[n].append(work(xs[n]))
+    torch.cuda.synchronize()
+    for n in range(2):
+        assert all(torch.equal(a, b) for outs in got[n] for a, b in zip(outs, want[n]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = work(xs[0])
+    for n in range(3):
+        ids.copy_(torch.randint(-1, min(cols, (n + 1) * k), (rows, k), device="cuda", generator=g))
+        v.copy_(torch.randn(rows, k, device="cuda", generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, work(xs[0]))), f"replay {n}"
+
+
+def test_the_longest_row():
+    """2^31 - 1 columns. At the temperature log2 e the exponents are the logits' differences, integers
+    here, so that every term is a power of two or an integer times one and the lanes' sums (of 2^15
+    terms) are exact; the merges of the 2^16 lanes' sums and of the slices round at most 24 times."""
+    cols = 2 ** 31 - 1
+    announce("longest row")
+    t = float(np.float32(math.log2(math.e)))  # log2(e) / t rounds to 1
+    x = torch.zeros(1, cols, dtype=torch.float16, device="cuda")
+    spikes = {0: 20.0, 5: 21.0, 2 ** 30 + 3: 22.0, cols - 2: 21.0, cols - 1: 23.0}
+    for at, value in spikes.items():
+        x[0, at] = value
+    best = sorted(spikes, key=lambda at: (-spikes[at], at)) + [1]
+    total = (cols - len(spikes)) + sum(math.exp(s / t) for s in spikes.values())
+    lse = math.log(total)
+    lps = {at: spikes.get(at, 0.0) / t - lse for at in best + [7, 8, cols - 3]}
+    entropy = lse - sum(math.exp(s / t) * s / t for s in spikes.values()) / total
+    token = torch.tensor([cols - 1], device="cuda")
+    r = ar.token_logprobs(x, token, temperature=t, entropy=True, top=6)
+    # 24 roundings of the sum; the exponents, the logarithm and the last steps as in logits_reference
+    # (|z| < 30); the entropy's quotient has twice the sum's roundings, times |z|
+    tol, tol_entropy = R.U * (24 + 3 * 30 + 8 * 30), R.U * (2 * 24 * 30 + 3 * 30 + 8 * 30)
+    assert r.top_tokens[0].tolist() == best
+    for got, at in zip(r.top_logprobs[0].tolist(), best):
+        assert abs(got - lps[at]) < tol
+    assert abs(float(r.logprob) - lps[cols - 1]) < tol
+    assert abs(float(r.entropy) - entropy) < tol_entropy
+    w = torch.ones(1, device="cuda")
+    grad = ar.token_logprobs_grad(x, token, r.stats, w, temperature=t)
+    ids = torch.tensor([[cols - 1, 0, 7, cols - 1]], device="cuda")
+    loss, dgrad = ar.distill_step(x, ids, torch.zeros(1, 4, device="cuda"), w, temperature=t)
+    want = sum(0.25 * (math.log(0.25) - lps[at]) for at in ids[0].tolist())
+    assert abs(float(loss) - want) < tol
+    eps = torch.finfo(torch.float16).eps / 2
+    q = {cols - 1: 0.5, 0: 0.25, 7: 0.25}
+    for at, lp in lps.items():
+        p = math.exp(lp)
+        for got, exact in [(grad[0, at], ((at == cols - 1) - p) / t), (dgrad[0, at], (p - q.get(at, 0.0)) / t)]:
+            # half a step of the type (2^-25 below its normal range), and the binary32 errors of p and q
+            assert abs(float(got) - exact) <= abs(exact) * eps + 2.0 ** -25 + 2 * tol * (p + q.get(at, 0.0))

@@ -167,3 +167,15 @@ def test_package_names():
     assert f"#define ARGREDUCE_TOP_MAX {ar.logits.TOP_MAX} " in text
     assert f"#define ARGREDUCE_TEACHER_MAX {ar.logits.TEACHER_MAX} " in text
     assert ctypes.sizeof(B.argreduce_plan_t) > 0
+
+
+def test_the_stride_of_a_single_row_does_not_matter(lib):
+    """Refused for what follows it (too many alternatives), not for a stride that nothing reads."""
+    args = list((FAKE, B.F32, 1, 8, 1 << 40) + CALLS["argreduce_logprobs"])
+    args[8] = 65
+    assert lib.argreduce_logprobs(*args) == -1
+
+
+def test_rows_times_columns_past_64_bits(lib):
+    args = (FAKE, B.F32, INT32_MAX, INT32_MAX, INT32_MAX) + CALLS["argreduce_logprobs"]
+    assert lib.argreduce_logprobs(*args) == -3
