@@ -1,9 +1,10 @@
 """Python binding of the HIP library ``libargreduce.so`` (argument marshalling only).
 
-ctypes loads the library and serves every entry point; the three reduction calls go
-through a small CPython fast-call module (``_argreduce_fast``, built beside the library)
-when it is present, because a ctypes call with nine converted arguments costs about as
-much host time as the GPU spends on a small reduction.
+ctypes loads the library and serves every entry point; the three reduction calls and the
+logits operators (torch functions in ``logits.py``) go through a small CPython fast-call
+module (``_argreduce_fast``, built beside the library) when it is present, because a ctypes
+call with nine converted arguments costs about as much host time as the GPU spends on a
+small reduction.
 
 The functions carry the names of the C ABI in include/argreduce.h and take the same
 arguments (device pointers as Python ints). ``argmax`` / ``argmin`` are conveniences for

@@ -427,13 +427,13 @@ __device__ inline void scan_span(const Sp& sp, bool edges, uint32_t first, uint3
 // ---------------------------------------------------------------------------------------
 // The k best elements of a row, by (value descending, position ascending).
 //
-// A pass over the row leaves the maximum of each of S segments (struct Segments). For a tau that at least k of these maxima reach, the k best elements are all >= tau
-// and lie in segments whose maximum is >= tau: only these are read again, from the caches, and
-// their elements >= tau collected in LDS as 64-bit keys (value above complemented position).
-// Ranking the keys by counting gives the sorted result. tau comes from a bisection that stops
-// when few more than k maxima reach it. Ties may put more keys into the buffer than it holds;
-// the collection then starts again in steps that cannot overflow it, the buffer cut to its k
-// best in between.
+// A pass over the row leaves the maximum of each of S segments (struct Segments). For a tau that at
+// least k of these maxima reach, the k best elements are all >= tau and lie in segments whose
+// maximum is >= tau: only these are read again, from the caches, and their elements >= tau collected
+// in LDS as 64-bit keys (value above complemented position). Ranking the keys by counting gives the
+// sorted result. tau comes from a bisection that stops when few more than k maxima reach it. Ties
+// may put more keys into the buffer than it holds; the collection then starts again in steps that
+// cannot overflow it, the buffer cut to its k best in between.
 
 __device__ inline uint64_t key_of(float v, uint32_t pos) { return Key32<kMax>::make(v, pos); }
 // Unsigned integers in the order of the floats, and back.
@@ -713,7 +713,9 @@ __device__ inline const uint8_t* row_ptr(const void* x, uint32_t r, uint32_t str
 }
 
 // Rows of at most G vectors, G lanes each, the row held in registers: maximum first, then the
-// exponentials. Alternatives are taken one by one, as the largest key left.
+// exponentials. Alternatives are taken one by one, as the largest key left. [65536,64] f16 with
+// entropy and 2 alternatives: 7.8 us (8 lanes; 11 MB, 1.4 TB/s), bound by the latency of one load and
+// the chain of reductions after it: a wavefront has eight rows and no work beside them.
 template <typename Fmt, bool KEEP, bool ENT, int G>
 __global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint32_t cols,
                                                             uint32_t stride, float scale,
@@ -787,7 +789,11 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint3
 template <int T>
 constexpr int kSegs = T == kWave ? 256 : 1024;
 
-// A team of T lanes per row.
+// A team of T lanes per row, in one pass. [4001,32001] f16: 38.0 us, 6.7 TB/s, bound by the read;
+// [2048,128256] bf16 with entropy 89 us, 5.9 TB/s, with 64 alternatives and no entropy 96 us, 5.4 TB/s:
+// the read, and the alternatives' selection (about 10 us a row) as far as the CU's other rows do not
+// hide it. [1,32000] f32 with entropy and 5 alternatives: 8.2 us, the latency of the read and of the
+// selection's barriers (split over 8 workgroups: 10, and a second launch).
 template <typename Fmt, bool KEEP, bool ENT, bool TOP, int T>
 __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32_t cols,
                                                            uint32_t stride, float scale,
@@ -845,6 +851,8 @@ struct Part {  // what a slice leaves in scratch
     float oct_max[kPartThreads / 8];  // of every eight lanes
 };
 
+// A slice per workgroup. [32,202048] bf16 with entropy: 6.4 us (12.9 MB, 2 TB/s), [1,202048] f32 3.3 us:
+// a launch and the latency of four loads per lane.
 template <typename Fmt, bool KEEP, bool ENT>
 __global__ __launch_bounds__(kPartThreads) void k_part(const void* x, uint32_t cols, uint32_t stride,
                                                        float scale, uint32_t parts,
@@ -893,7 +901,11 @@ __device__ inline Stat merge_parts(const Part* p, uint32_t parts, float scale, i
     return a;
 }
 
-// One workgroup per split row. Tags: columns in (x, tokens), slices, alternatives, scale.
+// One workgroup per split row; with 20 alternatives 6.6 us ([1,202048] f32), with 8 7.6 us
+// ([32,202048] bf16): chained latencies, of the slices' statistics, the bisection, and the segments'
+// second read. A kernel of its own, since the last workgroup of k_part to arrive could do it only
+// with a counter that something has to clear for every call. Tags: columns in (x, tokens), slices,
+// alternatives, scale.
 template <typename Fmt, bool ENT, bool TOP, int T = TOP ? kMergeTopThreads : kMergeThreads>
 __global__ __launch_bounds__(T) void k_lp_merge(uint64_t x, uint64_t tokens,
                                                             uint64_t part, uint64_t stats_,
@@ -1042,8 +1054,11 @@ struct GradSlice {
 };
 
 // d logprob and d entropy: dx_j = [ g (delta_jt - p_j) - e p_j (ln p_j + H) ] / T.
-// Tags: columns in (x, tokens), scale in (stats, g_lp), slices in g_ent, log2 of the team's
-// lanes in grad.
+// One exponential per element: bound by the read and the store. [2048,128256] bf16 with the entropy's
+// gradient 194 us, 5.4 TB/s read and written; [257,32003] f32 10.6 us, 6.2 TB/s, the logits from the
+// Infinity Cache. Slices of 1024 vectors, so that few rows occupy every CU and a workgroup's loads
+// are all under way at once. Tags: columns in (x, tokens), scale in (stats, g_lp), slices in g_ent,
+// log2 of the team's lanes in grad.
 template <typename Fmt, bool ENT, bool WIDE>
 __global__ __launch_bounds__(kBlockThreads) void k_lp_grad(uint64_t x, uint64_t tokens,
                                                            uint64_t stats_, uint64_t g_lp,
@@ -1149,7 +1164,9 @@ struct IdTable {
         for (uint32_t i = lane; i <= mask; i += team) place[i] = kFree;
     }
     __device__ bool entered(int32_t id) const { return id >= 0 && id < cols; }
-    __device__ uint32_t first(int32_t id) const { return (static_cast<uint32_t>(id) * 0x9e3779b1u) >> 8 & mask; }
+    __device__ uint32_t first(int32_t id) const {
+        return (static_cast<uint32_t>(id) * 0x9e3779b1u) >> 8 & mask;
+    }
     __device__ void add(int32_t id) const {
         if (!entered(id)) return;
         for (uint32_t i = first(id);; i = (i + 1) & mask) {  // ends: there are more places than ids
@@ -1204,9 +1221,9 @@ __device__ inline void entry_totals(Entry* ent, const IdTable& table, uint32_t k
 // totals too: each the sum of the weights with its id, in the entries' order. Up to 64 entries take
 // no barrier, up to T (`mine`) three; more are read here and worked off in turns.
 template <typename Fmt, int T, bool TOTALS>
-__device__ inline Teacher teacher_row(Entry* ent, const IdTable& table, Entry mine, const uint8_t* row, uint32_t cols,
-                                      const int64_t* ids, const float* values, uint32_t k, float scale,
-                                      int lane, float (*sh)[kShared], bool* bad) {
+__device__ inline Teacher teacher_row(Entry* ent, const IdTable& table, Entry mine, const uint8_t* row,
+                                      uint32_t cols, const int64_t* ids, const float* values, uint32_t k,
+                                      float scale, int lane, float (*sh)[kShared], bool* bad) {
     // an entry's part of the entropy; NaN for an id with weight beyond the row
     const auto spread = [&](int32_t id, float w, float lw) {
         if (id == static_cast<int32_t>(cols) && w != 0.0f) return __builtin_nanf("");
@@ -1327,6 +1344,8 @@ __device__ inline float distill_loss(const Entry* ent, uint32_t k, float scale, 
     return loss_of(q, sum);
 }
 
+// The loss alone, a team of T lanes per row. [512,128256] f16 with 32 entries: 22.9-24.5 us, 5.4-5.7
+// TB/s, bound by the read of two rows per CU one after the other, with the tail of each exposed.
 template <typename Fmt, bool KEEP, int T>
 __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32_t cols,
                                                            uint32_t stride, float scale,
@@ -1344,7 +1363,8 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32
     bool bad;
     Entry mine = own_entry<T>(ids, values, k, lane, cols);
     own_student<Fmt>(mine, row, k, lane, cols);
-    const Teacher q = teacher_row<Fmt, T, false>(ent, IdTable{}, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
+    const Teacher q = teacher_row<Fmt, T, false>(ent, IdTable{}, mine, row, cols, ids, values, k, scale,
+                                                 lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
@@ -1487,7 +1507,8 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
     bool bad;
     Entry mine = own_entry<T>(ids, values, k, lane, cols);
     own_student<Fmt>(mine, row, k, lane, cols);
-    const Teacher q = teacher_row<Fmt, T, false>(s_entries, IdTable{}, mine, row, cols, ids, values, k, scale, lane, sh, &bad);
+    const Teacher q = teacher_row<Fmt, T, false>(s_entries, IdTable{}, mine, row, cols, ids, values, k, scale,
+                                                 lane, sh, &bad);
     if (q.m == -__builtin_huge_valf()) {
         if (lane == 0) store_distill(stats, rows, r, 0.0f, 0.0f, 0.0f, q);
         return;
@@ -1503,8 +1524,8 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
 // ids, which every one of them stores. A team of T lanes (32: of 2^lg, up to 32) for a slice of a
 // row has the slice's entries in LDS. [4096,128256] bf16 with 64 entries: 421 us, 5.0 TB/s read and
 // written, bound by that; [4096,32000] with 1024 268 us, bound by the entries (553 and 7958 us with
-// each entry compared with all others from global memory). Tags: columns in (x, ids), teacher entries in values, scale in
-// (stats, g), lg and the slices (12 bits above 4) in grad.
+// each entry compared with all others from global memory). Tags: columns in (x, ids), teacher entries
+// in values, scale in (stats, g), lg and the slices (12 bits above 4) in grad.
 template <typename Fmt, int T>
 __global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t ids_, uint64_t values_,
                                                            uint64_t stats_, uint64_t g, uint64_t grad,
@@ -1580,9 +1601,10 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t 
 // logits are read from memory once; vectors beyond them are read again, mostly from the caches.
 // The registers of a CU hold few rows, so a team goes through several, and as soon as a vector's
 // gradient is stored, the vector of the team's next row is loaded in its place: the loads run
-// beside the second pass's arithmetic and stores. [4096,128256] bf16: 535 us when all vectors were
-// read again, 597 held without that overlap. Tags as for k_ds_grad, but the workgroups of the grid
-// in grad.
+// beside the second pass's arithmetic and stores. [4096,128256] bf16 with 64 entries: 439 us, 4.8 TB/s
+// read and written, the rate of a device copy (535 when all vectors were read again, 597 held without
+// that overlap); [1003,50001] f16 43 us, 4.6 TB/s; [16,32000] f32 8.7 us, a row's latency from end to
+// end. Tags as for k_ds_grad, but the workgroups of the grid in grad.
 template <typename Fmt, int T, int NV>
 __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64_t ids_, uint64_t values_,
                                                            uint64_t stats_, uint64_t w, uint64_t grad_,
@@ -1805,9 +1827,9 @@ hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const in
                     launch(k_part<Fmt, KEEP, ENT>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
                            static_cast<uint32_t>(plan.parts), tokens, part);
                     const uint32_t sc = bits_of(a.scale);
-                    launch(k_lp_merge<Fmt, ENT, TOP>, rows, TOP ? kMergeTopThreads : kMergeThreads, s, tagged(a.x, cols),
-                           tagged(tokens, cols >> 16), tagged(part, plan.parts), tagged(stats, top),
-                           tagged(top_logprobs, sc), tagged(top_tokens, sc >> 16), stride, rows);
+                    launch(k_lp_merge<Fmt, ENT, TOP>, rows, TOP ? kMergeTopThreads : kMergeThreads, s,
+                           tagged(a.x, cols), tagged(tokens, cols >> 16), tagged(part, plan.parts),
+                           tagged(stats, top), tagged(top_logprobs, sc), tagged(top_tokens, sc >> 16), stride, rows);
                     return;
                 }
                 with_team(plan.team, [&](auto team) {
@@ -1878,8 +1900,8 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
             Part* part = reinterpret_cast<Part*>(scratch16);
             launch(k_part<Fmt, KEEP, false>, grid, kPartThreads, s, a.x, cols, stride, a.scale,
                    static_cast<uint32_t>(plan.parts), static_cast<const int64_t*>(nullptr), part);
-            launch_entries(k_ds_merge<Fmt>, rows, kMergeThreads, k * kEntryBytes, s, a.x, cols, stride, a.scale, rows,
-                   tagged(ids, k), tagged(values, plan.parts), static_cast<const Part*>(part), stats);
+            launch_entries(k_ds_merge<Fmt>, rows, kMergeThreads, k * kEntryBytes, s, a.x, cols, stride, a.scale,
+                           rows, tagged(ids, k), tagged(values, plan.parts), static_cast<const Part*>(part), stats);
             return;
         }
         if (plan.team < kWave) {
@@ -1887,8 +1909,8 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
                 const auto go = [&](auto g) {
                     constexpr int G = decltype(g)::value;
                     launch_entries(k_ds_group<Fmt, decltype(gr)::value, G>, grid, kBlockThreads,
-                                   kBlockThreads / G * k * kEntryBytes, s, tagged(a.x, cols), tagged(ids, cols >> 16),
-                                   tagged(values, k), tagged(stats, sc), tagged(weights, sc >> 16),
+                                   entries_lds(kBlockThreads / G, 1, k, false), s, tagged(a.x, cols),
+                                   tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc), tagged(weights, sc >> 16),
                                    tagged(grad, 0), stride, rows);
                 };
                 with_group(plan.team, go);
@@ -1898,19 +1920,19 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
         with_team(plan.team, [&](auto team) {
             constexpr int T = decltype(team)::value;
             const auto step = [&](auto held) {
-                launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>, entries_lds(kTeamsPerBlock<T>, 2, k, true),
-                               s, tagged(a.x, cols),
-                       tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
-                       tagged(weights, sc >> 16), tagged(grad, grid), stride, rows);
+                launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>,
+                               entries_lds(kTeamsPerBlock<T>, 2, k, true), s, tagged(a.x, cols),
+                               tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
+                               tagged(weights, sc >> 16), tagged(grad, grid), stride, rows);
             };
             if (grad != nullptr && T >= 512 && plan.held > 8)
                 step(Int<T >= 512 ? 16 : 8>{});
             else if (grad != nullptr)
                 step(Int<8>{});
             else
-                launch_entries(k_ds_team<Fmt, KEEP, T>, grid, kTeamBlock<T>, kTeamsPerBlock<T> * k * kEntryBytes,
-                               s, a.x, cols, stride, a.scale, rows,
-                       static_cast<uint32_t>(k), ids, values, stats);
+                launch_entries(k_ds_team<Fmt, KEEP, T>, grid, kTeamBlock<T>,
+                               entries_lds(kTeamsPerBlock<T>, 1, k, false), s, a.x, cols, stride, a.scale, rows,
+                               static_cast<uint32_t>(k), ids, values, stats);
         });
     });
     if (plan.path == ARGREDUCE_PATH_SPLIT && grad != nullptr)

@@ -16,8 +16,8 @@ namespace {
 constexpr int64_t kBlock = 256;
 constexpr int64_t kThreadsPerCu = 2048;
 constexpr int64_t kLdsPerCu = 160 * 1024;
-// Logits of up to this size are left in the 256 MiB Infinity Cache (struct Span; at 125 MiB, [512,128256]
-// f16, the forward pass takes 25.7 us with them left there, 23.0 without).
+// Logits of up to this size are left in the 256 MiB Infinity Cache (struct Span; at 125 MiB,
+// [512,128256] f16, the forward pass takes 25.7 us with them left there, 23.0 without).
 constexpr int64_t kKeepBytes = int64_t{64} << 20;
 constexpr int64_t kMaxGridThreads = int64_t{1} << 32;  // threads a launch's grid may hold
 
@@ -97,7 +97,8 @@ constexpr int64_t kOneBlockStepVecs = 16384;
 // Scratch depends on the shape alone, so only the choices among plans without any go by
 // `vec_rows` (every row starts on a 16-byte boundary).
 // `k`: teacher entries (0: none).
-int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool vec_rows, LogitsPlan* p) {
+int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool vec_rows,
+                     LogitsPlan* p) {
     int rc = check_logits_shape(dtype, rows, cols);
     if (rc != ARGREDUCE_OK) return rc;
     int64_t cap = 0;
@@ -208,9 +209,11 @@ int scratch_of(const LogitsPlan& p, void* scratch, size_t bytes, uint8_t** out) 
     return ARGREDUCE_OK;
 }
 
+// Whether every row starts on a 16-byte boundary; of contiguous rows in an aligned tensor.
 bool vec_rows(const LogitsArgs& a) {
     return aligned(a.x, 16) && a.row_stride * logits_elem_size(a.dtype) % 16 == 0;
 }
+bool vec_rows(int dtype, int64_t cols) { return cols * logits_elem_size(dtype) % 16 == 0; }
 
 int status_of(hipError_t e) { return e == hipSuccess ? ARGREDUCE_OK : ARGREDUCE_ERR_HIP; }
 
@@ -245,7 +248,8 @@ int distill(const LogitsArgs& a, int32_t k, const int64_t* ids, const float* val
             const float* weights, void* grad, void* scratch, size_t scratch_bytes, void* stream) {
     LogitsPlan p;
     GradPlan g;
-    int rc = make_logits_plan(a.dtype, a.rows, a.cols, grad != nullptr ? kDistillStep : kDistill, k, vec_rows(a), &p);
+    int rc = make_logits_plan(a.dtype, a.rows, a.cols, grad != nullptr ? kDistillStep : kDistill, k,
+                              vec_rows(a), &p);
     if (rc != ARGREDUCE_OK) return rc;
     rc = make_grad_plan(a.dtype, a.rows, a.cols, k, &g);
     if (rc != ARGREDUCE_OK) return rc;
@@ -266,7 +270,8 @@ using argreduce::LogitsPlan;
 ARGREDUCE_EXPORT size_t argreduce_logprobs_scratch_bytes(int64_t rows, int64_t cols,
                                                          argreduce_dtype_t dtype) {
     LogitsPlan p;
-    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, 0, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p) != ARGREDUCE_OK)
+    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, 0,
+                                    argreduce::vec_rows(dtype, cols), &p) != ARGREDUCE_OK)
         return std::numeric_limits<size_t>::max();
     return p.scratch_bytes;
 }
@@ -275,7 +280,8 @@ ARGREDUCE_EXPORT int argreduce_logprobs_plan(int64_t rows, int64_t cols, argredu
                                              argreduce_plan_t* out) {
     if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
     LogitsPlan p;
-    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, 0, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p);
+    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kLogprobs, 0,
+                                               argreduce::vec_rows(dtype, cols), &p);
     if (rc != ARGREDUCE_OK) return rc;
     argreduce::fill_logits_plan(p, p.parts > 1 ? 2 : 1, out);
     return ARGREDUCE_OK;
@@ -329,7 +335,8 @@ ARGREDUCE_EXPORT int argreduce_logprobs_grad(const void* x, argreduce_dtype_t dt
 ARGREDUCE_EXPORT size_t argreduce_distill_scratch_bytes(int64_t rows, int64_t cols,
                                                         argreduce_dtype_t dtype) {
     LogitsPlan p;
-    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p) != ARGREDUCE_OK)
+    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1,
+                                    argreduce::vec_rows(dtype, cols), &p) != ARGREDUCE_OK)
         return std::numeric_limits<size_t>::max();
     return p.scratch_bytes;
 }
@@ -338,7 +345,8 @@ ARGREDUCE_EXPORT int argreduce_distill_plan(int64_t rows, int64_t cols, argreduc
                                             argreduce_plan_t* out) {
     if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
     LogitsPlan p;
-    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1, cols * argreduce::logits_elem_size(dtype) % 16 == 0, &p);
+    const int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1,
+                                               argreduce::vec_rows(dtype, cols), &p);
     if (rc != ARGREDUCE_OK) return rc;
     argreduce::fill_logits_plan(p, p.parts > 1 ? 2 : 1, out);
     return ARGREDUCE_OK;

@@ -303,9 +303,10 @@ int argreduce_scan_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
  *
  *     p_j = exp(x_j / T) / sum_i exp(x_i / T)
  *
- * Statistics, sums and outputs are binary32 (a log probability below its range is -inf); a gradient is computed in binary32 and rounded
- * once, to the nearest even value of the logits' format. Results do not depend on the order in
- * which workgroups run: the same call gives the same bits.
+ * Statistics, sums and outputs are binary32 (a log probability below its range is -inf); a
+ * gradient is computed in binary32 and rounded once, to the nearest even value of the logits'
+ * format. Results do not depend on the order in which workgroups run: the same call gives the
+ * same bits.
  *
  *   - A logit of -inf is masked: probability 0, no gradient, never an alternative. The lowest
  *     finite value is an ordinary value.
@@ -316,8 +317,9 @@ int argreduce_scan_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
  *   - Rows are independent: a row's contents change no other row's results.
  *
  * rows >= 0 (0 is a no-op); 1 <= cols <= INT32_MAX, rows <= INT32_MAX, row_stride <= UINT32_MAX
- * (else ARGREDUCE_ERR_TOO_WIDE); 2^-60 <= T <= 2^60. x is aligned to its elements, int64 arrays
- * to 8 and float arrays to 4 bytes. Inputs, outputs and scratch must not overlap. Scratch
+ * (else ARGREDUCE_ERR_TOO_WIDE, also where a launch would hold 2^32 threads or more, which takes at
+ * least 2^23 rows); 2^-60 <= T <= 2^60. x is aligned to its elements, int64 arrays to 8 and float
+ * arrays to 4 bytes. Inputs, outputs and scratch must not overlap. Scratch
  * (argreduce_*_scratch_bytes, which depends on the shape only) is as for argreduce_lastaxis: any
  * contents, any byte alignment, not shared by calls that can run at the same time. Token ids are
  * read on the device and cannot be refused by the call: no id makes a kernel read or write out
@@ -348,9 +350,9 @@ int argreduce_logprobs(const void *x, argreduce_dtype_t dtype, int64_t rows, int
                        int64_t row_stride, const int64_t *tokens, float temperature, int32_t entropy,
                        int32_t top, float *stats, float *top_logprobs, int64_t *top_tokens,
                        void *scratch, size_t scratch_bytes, void *stream);
-/* The plan of argreduce_logprobs: SUBWAVE (a group of lanes or a wavefront per row), BLOCK (a
- * workgroup per row) or SPLIT (several workgroups per row, merged by a second dispatch; no
- * workgroup waits on another). */
+/* The plan of argreduce_logprobs without alternatives, for contiguous rows in an aligned tensor:
+ * SUBWAVE (a group of lanes or a wavefront per row), BLOCK (a workgroup per row) or SPLIT (several
+ * workgroups per row, merged by a second dispatch; no workgroup waits on another). */
 int argreduce_logprobs_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
                             argreduce_plan_t *plan);
 
@@ -389,6 +391,7 @@ int argreduce_distill(const void *x, argreduce_dtype_t dtype, int64_t rows, int6
                       int64_t row_stride, int32_t k, const int64_t *teacher_tokens,
                       const float *teacher_logits, float temperature, float *stats, void *scratch,
                       size_t scratch_bytes, void *stream);
+/* The plan of argreduce_distill with one entry, likewise. */
 int argreduce_distill_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
                            argreduce_plan_t *plan);
 
