@@ -1127,10 +1127,12 @@ __device__ inline float student_at(const uint8_t* row, int32_t id, uint32_t cols
                ? Fmt::load1(row + static_cast<size_t>(id) * Fmt::kSize)
                : __builtin_nanf("");
 }
-__device__ inline Entry entry_at(const int64_t* ids, const float* values, uint32_t i, uint32_t cols) {
-    const int64_t id = ids[i];
+__device__ inline Entry entry_of(int64_t id, float value, uint32_t cols) {
     return {static_cast<int32_t>(id < 0 ? -1 : id < static_cast<int64_t>(cols) ? id : cols),
-            id >= 0 ? values[i] : -__builtin_huge_valf(), 0.0f, __builtin_nanf("")};
+            id >= 0 ? value : -__builtin_huge_valf(), 0.0f, __builtin_nanf("")};
+}
+__device__ inline Entry entry_at(const int64_t* ids, const float* values, uint32_t i, uint32_t cols) {
+    return entry_of(ids[i], values[i], cols);
 }
 // A lane's entry where there are no more entries than lanes, read ahead of its use: up to 64 of them
 // every wavefront has its own copy (the student's logits in the team's first alone), beyond that
@@ -1149,7 +1151,8 @@ __device__ inline void own_student(Entry& mine, const uint8_t* row, uint32_t k, 
 
 // Which ids of a row of more than kTeacherCompared entries occur more than once: an open hash table
 // in LDS of at least twice as many places. Comparing every entry with every other took most of the
-// time instead: [11266,617] f16 with 256 entries 229 us, with the table 71. A place holds an id, its
+// time instead: [11266,617] f16 with 256 entries 229 us, with the table 36 (71 before the table's
+// places were 4 bytes and such rows held two vectors per lane). A place holds an id, its
 // top bit set once the id has come again. (No id has all 31 bits set: ids are below cols <=
 // INT32_MAX, and cols itself, for ids beyond the row, is not entered.)
 struct IdTable {
@@ -1278,10 +1281,26 @@ __device__ inline Teacher teacher_row(Entry* ent, const IdTable& table, Entry mi
         q.entropy = team_reduce<T, false>(spread(mine.id, mine.w, lw), lane, sh, kSlotEntropy);
     } else {
         if constexpr (TOTALS) table.clear(lane, T);
-        for (uint32_t i = lane; i < k; i += T) {
-            const Entry e = entry_at(ids, values, i, cols);
-            ent[i] = e;
-            m = max_f(m, e.w);
+        constexpr uint32_t N = 4;  // entries a lane loads at once
+        for (uint32_t base = lane; base < k; base += N * T) {
+            int64_t id[N];
+            float v[N];
+            Entry e[N];
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j) {
+                const uint32_t i = base + j * T < k ? base + j * T : base;
+                id[j] = ids[i];
+                v[j] = values[i];
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j) {
+                e[j] = entry_of(id[j], v[j], cols);
+                if constexpr (TOTALS) e[j].x = student_at<Fmt>(row, e[j].id, cols);
+                m = max_f(m, e[j].w);
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < N; ++j)
+                if (base + j * T < k) ent[base + j * T] = e[j];
         }
         m = team_reduce<T, true>(m, lane, sh, kSlotMax);
         if constexpr (T == kWave) team_sync<T>();
@@ -1296,7 +1315,9 @@ __device__ inline Teacher teacher_row(Entry* ent, const IdTable& table, Entry mi
             const float w = exp2_f(lw);
             ent[i].w = w;
             h += spread(id, w, lw);
-            ent[i].x = student_at<Fmt>(row, id, cols);
+            // (the loss alone: [4096,32000] bf16 with 1024 entries 72 us, 86 with them above; the step
+            // [8192,16000] f16 with 1000 the other way round, 216 and 188)
+            if constexpr (!TOTALS) ent[i].x = student_at<Fmt>(row, id, cols);
         }
         q.entropy = team_reduce<T, false>(h, lane, sh, kSlotEntropy);
     }
@@ -1604,13 +1625,18 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t 
 // beside the second pass's arithmetic and stores. [4096,128256] bf16 with 64 entries: 439 us, 4.8 TB/s
 // read and written, the rate of a device copy (535 when all vectors were read again, 597 held without
 // that overlap); [1003,50001] f16 43 us, 4.6 TB/s; [16,32000] f32 8.7 us, a row's latency from end to
-// end. Tags as for k_ds_grad, but the workgroups of the grid in grad.
+// end. Rows of up to 128 vectors hold two per lane, in half the registers, so that twice the wavefronts
+// hide their latency: [21454,251] f16 with 251 entries 57 us, 100 with eight. Tags as for k_ds_grad,
+// but the workgroups of the grid in grad.
+template <int T>
+constexpr int kStepRows = step_rows(T);
 template <typename Fmt, int T, int NV>
-__global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64_t ids_, uint64_t values_,
+__global__ __launch_bounds__(kTeamBlock<T>, NV > 2 ? 4 : 8) void k_ds_step(uint64_t x, uint64_t ids_, uint64_t values_,
                                                            uint64_t stats_, uint64_t w, uint64_t grad_,
                                                            uint32_t stride, uint32_t rows) {
     constexpr int VW = Fmt::VW;
-    constexpr int U = NV > 8 ? kUnroll<Fmt, false> / 2 : kUnroll<Fmt, false>;  // 128 registers suffice
+    // 128 registers suffice, 64 for two vectors
+    constexpr int U = NV == 8 ? kUnroll<Fmt, false> : kUnroll<Fmt, false> / 2;
     static_assert(NV % U == 0, "whole steps");
     __shared__ float sh[T / kWave][kShared];
     const uint32_t cols = tags(x, ids_), k = tag(values_), teams = tag(grad_) * kTeamsPerBlock<T>;
@@ -1618,11 +1644,12 @@ __global__ __launch_bounds__(kTeamBlock<T>, 4) void k_ds_step(uint64_t x, uint64
     const int lane = lane_of<T>();
     uint32_t r = blockIdx.x * kTeamsPerBlock<T> + team_of<T>();
     if (r >= rows) return;
-    // the entries of two rows: a wavefront may be one row ahead of another
-    Entry* ent = s_entries + team_of<T>() * 2 * k;
-    Entry* other = ent + k;
+    // the entries of two rows if a wavefront may be one row ahead of another
+    constexpr uint32_t kBuffers = kStepRows<T>;
+    Entry* ent = s_entries + team_of<T>() * kBuffers * k;
+    Entry* other = ent + (kBuffers - 1) * k;
     const uint32_t places = IdTable::size(k);  // the tables lie behind all teams' entries
-    const IdTable table{reinterpret_cast<uint32_t*>(s_entries + kTeamsPerBlock<T> * 2 * k) +
+    const IdTable table{reinterpret_cast<uint32_t*>(s_entries + kTeamsPerBlock<T> * kBuffers * k) +
                             team_of<T>() * places,
                         places - 1, static_cast<int32_t>(cols)};
     const auto ids_at = [&](uint32_t n) { return addr<const int64_t>(ids_) + static_cast<size_t>(n) * k; };
@@ -1921,12 +1948,14 @@ hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const L
             constexpr int T = decltype(team)::value;
             const auto step = [&](auto held) {
                 launch_entries(k_ds_step<Fmt, T, decltype(held)::value>, grid, kTeamBlock<T>,
-                               entries_lds(kTeamsPerBlock<T>, 2, k, true), s, tagged(a.x, cols),
+                               entries_lds(kTeamsPerBlock<T>, kStepRows<T>, k, true), s, tagged(a.x, cols),
                                tagged(ids, cols >> 16), tagged(values, k), tagged(stats, sc),
                                tagged(weights, sc >> 16), tagged(grad, grid), stride, rows);
             };
             if (grad != nullptr && T >= 512 && plan.held > 8)
                 step(Int<T >= 512 ? 16 : 8>{});
+            else if (grad != nullptr && T == kWave && plan.held < 8)
+                step(Int<T == kWave ? 2 : 8>{});
             else if (grad != nullptr)
                 step(Int<8>{});
             else

@@ -28,12 +28,16 @@ inline size_t entries_lds(int teams, int rows, int k, bool tables) {
     return teams * (rows * k * kEntryBytes + (tables ? teacher_places(k) * sizeof(uint32_t) : 0));
 }
 
+// Teacher rows that a team of the distillation step has in LDS: wavefronts of one team may work on
+// two rows at a time.
+constexpr int step_rows(int team) { return team == 64 ? 1 : 2; }
+
 // How the rows of one forward call are scanned.
 struct LogitsPlan {
     int path;             // argreduce_path_t: SUBWAVE, BLOCK or SPLIT
     int team;             // lanes that scan one row (SUBWAVE, BLOCK), else kPartThreads
     int parts;            // SPLIT: workgroups per row
-    int held;             // distillation step: vectors per lane kept in registers, 8 or 16
+    int held;             // distillation step: vectors per lane kept in registers, 2, 8 or 16
     int64_t grid_blocks;  // workgroups of the scanning kernel
     int64_t device_threads;
     size_t scratch_bytes; // including 15 bytes of alignment slack; 0 if none needed

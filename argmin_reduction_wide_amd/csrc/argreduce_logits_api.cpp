@@ -71,19 +71,21 @@ bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p)
 // A device array of `n`-byte elements that a call with rows > 0 needs.
 bool usable(const void* p, uintptr_t n) { return p != nullptr && aligned(p, n) && fits48(p); }
 
-// Workgroups of the distillation step: as many as its registers (at most 128 per lane) and LDS let
-// the CUs hold at once; each goes through several rows. The kernel takes the number in 16 bits.
-int64_t step_blocks(int64_t cap, int team, int k) {
-    int64_t per_cu = team == 1024 ? 1 : team == 512 ? 2 : 4;
-    const int64_t lds = static_cast<int64_t>(entries_lds(team == 64 ? kBlock / 64 : 1, 2, k, true)) + 1024;
+// Workgroups of the distillation step: as many as its registers (at most 128 per lane, 64 if it
+// holds two vectors) and LDS let the CUs hold at once; each goes through several rows. The kernel
+// takes the number in 16 bits.
+int64_t step_blocks(int64_t cap, int team, int held, int k) {
+    int64_t per_cu = team == 1024 ? 1 : team == 512 ? 2 : held > 2 ? 4 : 8;
+    const size_t entries = entries_lds(team == 64 ? kBlock / 64 : 1, step_rows(team), k, true);
+    const int64_t lds = static_cast<int64_t>(entries) + 1024;
     per_cu = std::min(per_cu, kLdsPerCu / lds);
     const int64_t cus = cap / kThreadsPerCu > 0 ? cap / kThreadsPerCu : 1;
     return per_cu * cus < 65535 ? per_cu * cus : 65535;
 }
 
 // Teacher entries, at most, of a row left to one wavefront: four rows' entries and tables then take
-// 40 KiB of LDS. (A workgroup per row has a lane for each entry, and is slower: [21454,251] f16 with
-// 130 entries, loss and gradient, 64 us by a wavefront, 153 by 256 lanes.)
+// 24 KiB of LDS. (A workgroup per row has a lane for each entry, and is slower: [21454,251] f16 with
+// 130 entries, loss and gradient, 41 us by a wavefront, 153 by 256 lanes.)
 constexpr int kWaveEntries = 256;
 
 // What a plan is for.
@@ -131,8 +133,8 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
         p->grid_blocks = ceil_div(rows1, kBlock / 64);
         if (rows1 * 64 >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
         if (use == kDistillStep) {
-            const int64_t most = step_blocks(cap, p->team, k);
-            p->held = 8;
+            p->held = vecs <= 128 ? 2 : 8;
+            const int64_t most = step_blocks(cap, p->team, p->held, k);
             p->grid_blocks = p->grid_blocks < most ? p->grid_blocks : most;
         }
         return ARGREDUCE_OK;
@@ -168,8 +170,8 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
     p->grid_blocks = rows1;
     if (rows1 * p->team >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
     if (use == kDistillStep) {
-        const int64_t most = step_blocks(cap, p->team, k);
         p->held = vecs > 8 * p->team ? 16 : 8;
+        const int64_t most = step_blocks(cap, p->team, p->held, k);
         p->grid_blocks = rows1 < most ? rows1 : most;
     }
     return ARGREDUCE_OK;
