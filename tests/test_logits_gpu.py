@@ -804,3 +804,46 @@ def test_the_longest_row():
         for got, exact in [(grad[0, at], ((at == cols - 1) - p) / t), (dgrad[0, at], (p - q.get(at, 0.0)) / t)]:
             # half a step of the type (2^-25 below its normal range), and the binary32 errors of p and q
             assert abs(float(got) - exact) <= abs(exact) * eps + 2.0 ** -25 + 2 * tol * (p + q.get(at, 0.0))
+
+
+@pytest.mark.parametrize("dtype,top", [("f16", 64), ("f32", 1)])
+def test_very_wide_rows_by_one_workgroup(capacity, dtype, top):
+    """Rows far longer than a workgroup's registers and segments, left to one workgroup each."""
+    capacity(2048)
+    rows, cols = 2, 3_000_001
+    announce(f"wide by one workgroup {dtype}")
+    assert B.argreduce_logprobs_plan(rows, cols, dtype)["path"] == B.PATH_BLOCK
+    rng = np.random.default_rng(41)
+    x = torch.from_numpy(rng.normal(size=(rows, cols)) * 3).to(DT[dtype]).cuda()
+    tokens = torch.tensor([cols - 1, 0], device="cuda")
+    got = check_logprobs(x, tokens, dtype, 1.0, True, top)
+    check_logprobs_grad(x, tokens, dtype, 1.0, True, *got, rng)
+    check_distill(x, *make_teacher(rng, rows, cols, 300), dtype, 1.0, rng)
+
+
+def test_calls_without_the_fast_module(monkeypatch):
+    """The same bits through ctypes alone."""
+    announce("ctypes")
+    import argmin_reduction_wide_amd.logits as L
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(5, 60001, device="cuda", generator=g)
+    tokens = torch.randint(0, 60001, (5,), device="cuda", generator=g)
+    w = torch.rand(5, device="cuda", generator=g)
+
+    def work():
+        r = ar.token_logprobs(x, tokens, temperature=0.7, entropy=True, top=5)
+        d = ar.distill_loss(x, r.top_tokens, r.top_logprobs, temperature=0.7)
+        return [r.stats, r.top_logprobs, r.top_tokens, d.stats,
+                ar.token_logprobs_grad(x, tokens, r.stats, w, w, temperature=0.7),
+                ar.distill_loss_grad(x, r.top_tokens, r.top_logprobs, d.stats, w, temperature=0.7),
+                *ar.distill_step(x, r.top_tokens, r.top_logprobs, w, temperature=0.7)]
+
+    fast = work()
+
+    class Ctypes:
+        def __getattr__(self, name):
+            return getattr(B.lib(), "argreduce_" + name)
+
+    monkeypatch.setattr(L, "_call", Ctypes())
+    for a, b in zip(fast, work()):
+        assert torch.equal(a, b)
