@@ -1428,7 +1428,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_group(uint64_t x, uint64_t
         for (int i = 0; i < VW; ++i) e[i] = p0 + i < cols ? e[i] : -__builtin_huge_valf();
     }
     // the teacher's row
-    float m = -__builtin_huge_valf(), s = 0.0f, h = 0.0f, bad = 0.0f;
+    float m = -__builtin_huge_valf(), s = 0.0f, h = 0.0f;
     for (uint32_t i = lane; i < k; i += G) {
         Entry t = entry_at(ids, values, i, cols);
         t.x = student_at<Fmt>(row, t.id, cols);
@@ -1443,12 +1443,13 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_group(uint64_t x, uint64_t
     Teacher q{s == s ? m : __builtin_nanf(""), log2_f(s), 0.0f};
     for (uint32_t i = lane; i < k; i += G) {
         const float lw = q.log_weight(ent[i].w, scale), wt = exp2_f(lw);
-        if (ent[i].id == static_cast<int32_t>(cols) && wt != 0.0f) bad = 1.0f;
+        // NaN for an id with weight beyond the row, so that the loss is NaN whatever the logits are
+        if (ent[i].id == static_cast<int32_t>(cols) && wt != 0.0f) h = __builtin_nanf("");
         if (ent[i].id >= 0 && wt > 0.0f) h -= wt * (lw * kLn2);
         ent[i].w = wt;
     }
     q.entropy = lanes_sum<G>(h);
-    bad = s != s ? 1.0f : lanes_max<G>(bad);
+    const bool bad = s != s || q.entropy != q.entropy;
     team_sync<kWave>();
     if constexpr (GRAD) {
         for (uint32_t i = lane; i < k; i += G) {
@@ -1466,7 +1467,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_group(uint64_t x, uint64_t
     a.m = lanes_max<G>(max_f(a.m, max_of(e)));
     take<false>(e, scale, a);
     a.s = lanes_sum<G>(a.s);
-    const float l2 = bad > 0.0f ? __builtin_nanf("") : log2_f(a.s);
+    const float l2 = bad ? __builtin_nanf("") : log2_f(a.s);
     float sum = 0.0f;
     for (uint32_t i = lane; i < k; i += G) {
         const Entry t = ent[i];

@@ -847,3 +847,20 @@ def test_calls_without_the_fast_module(monkeypatch):
     monkeypatch.setattr(L, "_call", Ctypes())
     for a, b in zip(fast, work()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("rows,cols", [(5, 4), (5, 24), (5, 100), (5, 700), (5, 9000), (5, 140001)])
+def test_an_id_beyond_an_empty_row(dtype, rows, cols):
+    """A weight beyond the row makes loss and gradient NaN, also where every logit is -inf: by a group
+    of lanes, a wavefront, a workgroup and split."""
+    announce(f"beyond an empty row {dtype} [{rows},{cols}]")
+    rng = np.random.default_rng(cols)
+    x = torch.from_numpy(rng.normal(size=(rows, cols))).to(DT[dtype]).cuda()
+    x[:3] = -INF
+    ids = torch.tensor([[cols, 1], [1, cols + 7], [1, 2], [cols, 1], [2 ** 40, -1]], device="cuda")
+    v = torch.zeros(rows, 2, device="cuda")
+    v[3, 0] = -INF  # beyond the row, but without weight
+    check_distill(x, ids, v, dtype, 1.0, rng)
+    loss = ar.distill_loss(x, ids, v).loss
+    assert loss.isnan().tolist() == [True, True, False, False, True] and loss[2] == INF
