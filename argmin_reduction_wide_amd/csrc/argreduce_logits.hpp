@@ -69,7 +69,7 @@ hipError_t launch_logprobs_grad(const GradPlan& plan, const LogitsArgs& a, const
                                 const float* stats, const float* g_logprob, const float* g_entropy,
                                 void* grad, hipStream_t stream);
 // With `weights` and `grad` the gradient too (argreduce_distill_step), by `gplan` where the
-// plan splits rows.
+// plan splits rows (else it is not read).
 hipError_t launch_distill(const LogitsPlan& plan, const GradPlan& gplan, const LogitsArgs& a, int k,
                           const int64_t* ids, const float* values, float* stats,
                           const float* weights, void* grad, uint8_t* scratch16, hipStream_t stream);

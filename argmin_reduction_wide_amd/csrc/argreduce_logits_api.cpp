@@ -19,7 +19,8 @@ constexpr int64_t kLdsPerCu = 160 * 1024;
 // Logits of up to this size are left in the 256 MiB Infinity Cache (struct Span; at 125 MiB,
 // [512,128256] f16, the forward pass takes 25.7 us with them left there, 23.0 without).
 constexpr int64_t kKeepBytes = int64_t{64} << 20;
-constexpr int64_t kMaxGridThreads = int64_t{1} << 32;  // threads a launch's grid may hold
+constexpr int64_t kMaxGridThreads = int64_t{1} << 32;  // a launch's grid holds fewer threads
+constexpr int64_t kMaxBytes = int64_t{1} << 48;        // a device address is below it
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t next_pow2(int64_t v) {
@@ -59,6 +60,7 @@ int check_logits(const void* x, int dtype, int64_t rows, int64_t cols, int64_t s
     if (!(temperature >= 0x1p-60f && temperature <= 0x1p60f)) return ARGREDUCE_ERR_INVALID_ARG;
     if (rows > 0 && (x == nullptr || reinterpret_cast<uintptr_t>(x) % logits_elem_size(dtype) != 0))
         return ARGREDUCE_ERR_INVALID_ARG;
+    if (rows > 1 && stride >= kMaxBytes / logits_elem_size(dtype) / rows) return ARGREDUCE_ERR_TOO_WIDE;
     *a = LogitsArgs{x, dtype, rows, cols, rows > 1 ? stride : cols,
                     static_cast<float>(1.4426950408889634 / static_cast<double>(temperature)),
                     rows <= kKeepBytes / logits_elem_size(dtype) / cols};
@@ -82,6 +84,8 @@ int64_t step_blocks(int64_t cap, int team, int held, int k) {
     const int64_t cus = cap / kThreadsPerCu > 0 ? cap / kThreadsPerCu : 1;
     return per_cu * cus < 65535 ? per_cu * cus : 65535;
 }
+
+bool grid_too_large(int64_t blocks, int64_t threads) { return blocks >= kMaxGridThreads / threads; }
 
 // Teacher entries, at most, of a row left to one wavefront: four rows' entries and tables then take
 // 24 KiB of LDS. (A workgroup per row has a lane for each entry, and is slower: [21454,251] f16 with
@@ -125,8 +129,7 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
         p->path = ARGREDUCE_PATH_SUBWAVE;
         p->team = static_cast<int>(lanes);
         p->grid_blocks = ceil_div(rows1, kBlock / lanes);
-        if (rows1 * lanes >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
-        return ARGREDUCE_OK;
+        return grid_too_large(p->grid_blocks, kBlock) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
     }
     // a wavefront per row: up to four vectors per lane; in a distillation step up to the eight that
     // it holds ([19940,2312] f16, 291 vectors: 256 lanes 152 us, see the step's figures below)
@@ -134,13 +137,12 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
         p->path = ARGREDUCE_PATH_SUBWAVE;
         p->team = 64;
         p->grid_blocks = ceil_div(rows1, kBlock / 64);
-        if (rows1 * 64 >= kMaxGridThreads - kBlock) return ARGREDUCE_ERR_TOO_WIDE;
         if (use == kDistillStep) {
             p->held = vecs <= 128 ? 2 : 8;
             const int64_t most = step_blocks(cap, p->team, p->held, k);
             p->grid_blocks = p->grid_blocks < most ? p->grid_blocks : most;
         }
-        return ARGREDUCE_OK;
+        return grid_too_large(p->grid_blocks, kBlock) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
     }
     // Long rows too few to give every second CU one: split, in one device wave.
     const int64_t one_block = use == kDistillStep ? kOneBlockStepVecs : kOneBlockVecs;
@@ -171,13 +173,12 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
     else
         p->team = vecs > (use == kLogprobsTop ? 4096 : 3000) ? 512 : 256;
     p->grid_blocks = rows1;
-    if (rows1 * p->team >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
     if (use == kDistillStep) {
         p->held = vecs > 8 * p->team ? 16 : 8;
         const int64_t most = step_blocks(cap, p->team, p->held, k);
         p->grid_blocks = rows1 < most ? rows1 : most;
     }
-    return ARGREDUCE_OK;
+    return grid_too_large(p->grid_blocks, p->team) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
 }
 
 // `k`: teacher entries (0: none).
@@ -199,8 +200,7 @@ int make_grad_plan(int dtype, int64_t rows, int64_t cols, int k, GradPlan* p) {
         p->slices = static_cast<int>(std::min<int64_t>(ceil_div(vecs, kBlock * each), 4095));
     }
     p->grid_blocks = ceil_div(rows1 * p->slices, kBlock / p->team);
-    if (p->grid_blocks * kBlock >= kMaxGridThreads) return ARGREDUCE_ERR_TOO_WIDE;
-    return ARGREDUCE_OK;
+    return grid_too_large(p->grid_blocks, kBlock) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
 }
 
 // The caller's scratch aligned up to 16 bytes in *out; an ARGREDUCE_* status.
@@ -252,12 +252,14 @@ int check_teacher(const LogitsArgs& a, int32_t k, const int64_t* ids, const floa
 int distill(const LogitsArgs& a, int32_t k, const int64_t* ids, const float* values, float* stats,
             const float* weights, void* grad, void* scratch, size_t scratch_bytes, void* stream) {
     LogitsPlan p;
-    GradPlan g;
+    GradPlan g{};
     int rc = make_logits_plan(a.dtype, a.rows, a.cols, grad != nullptr ? kDistillStep : kDistill, k,
                               vec_rows(a), &p);
     if (rc != ARGREDUCE_OK) return rc;
-    rc = make_grad_plan(a.dtype, a.rows, a.cols, k, &g);
-    if (rc != ARGREDUCE_OK) return rc;
+    if (grad != nullptr && p.path == ARGREDUCE_PATH_SPLIT) {  // a launch of its own for the gradient
+        rc = make_grad_plan(a.dtype, a.rows, a.cols, k, &g);
+        if (rc != ARGREDUCE_OK) return rc;
+    }
     uint8_t* scratch16 = nullptr;
     rc = scratch_of(p, scratch, scratch_bytes, &scratch16);
     if (rc != ARGREDUCE_OK) return rc;
@@ -340,10 +342,11 @@ ARGREDUCE_EXPORT int argreduce_logprobs_grad(const void* x, argreduce_dtype_t dt
 ARGREDUCE_EXPORT size_t argreduce_distill_scratch_bytes(int64_t rows, int64_t cols,
                                                         argreduce_dtype_t dtype) {
     LogitsPlan p;
-    if (argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1,
-                                    argreduce::vec_rows(dtype, cols), &p) != ARGREDUCE_OK)
-        return std::numeric_limits<size_t>::max();
-    return p.scratch_bytes;
+    const bool vec = argreduce::vec_rows(dtype, cols);
+    int rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistill, 1, vec, &p);
+    if (rc == ARGREDUCE_ERR_TOO_WIDE)  // rows that only a step's grid holds
+        rc = argreduce::make_logits_plan(dtype, rows, cols, argreduce::kDistillStep, 1, vec, &p);
+    return rc == ARGREDUCE_OK ? p.scratch_bytes : std::numeric_limits<size_t>::max();
 }
 
 ARGREDUCE_EXPORT int argreduce_distill_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,

@@ -317,8 +317,8 @@ int argreduce_scan_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
  *   - Rows are independent: a row's contents change no other row's results.
  *
  * rows >= 0 (0 is a no-op); 1 <= cols <= INT32_MAX, rows <= INT32_MAX, row_stride <= UINT32_MAX
- * (else ARGREDUCE_ERR_TOO_WIDE, also where a launch would hold 2^32 threads or more, which takes at
- * least 2^23 rows); 2^-60 <= T <= 2^60. x is aligned to its elements, int64 arrays to 8 and float
+ * (else ARGREDUCE_ERR_TOO_WIDE, also where the logits would span 2^48 bytes or more, or one of the
+ * call's own launches would hold 2^32 threads or more); 2^-60 <= T <= 2^60. x is aligned to its elements, int64 arrays to 8 and float
  * arrays to 4 bytes. Inputs, outputs and scratch must not overlap. Scratch
  * (argreduce_*_scratch_bytes, which depends on the shape only) is as for argreduce_lastaxis: any
  * contents, any byte alignment, not shared by calls that can run at the same time. Token ids are

@@ -864,3 +864,34 @@ def test_an_id_beyond_an_empty_row(dtype, rows, cols):
     check_distill(x, ids, v, dtype, 1.0, rng)
     loss = ar.distill_loss(x, ids, v).loss
     assert loss.isnan().tolist() == [True, True, False, False, True] and loss[2] == INF
+
+
+@pytest.mark.parametrize("rows,cols,step", [((1 << 26) + 5, 264, True), (1 << 28, 64, False)])
+def test_more_rows_than_other_calls_hold(rows, cols, step):
+    """A step of more rows than a launch holds wavefronts; a loss whose separate gradient call would
+    not fit a launch."""
+    announce(f"distill [{rows},{cols}] step={step}")
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.empty(rows, cols, dtype=torch.float16, device="cuda").normal_(generator=g)
+    ids = torch.randint(0, cols, (rows, 1), device="cuda", generator=g)
+    v, w = torch.zeros(rows, 1, device="cuda"), torch.ones(rows, device="cuda")
+    if step:
+        loss, grad = ar.distill_step(x, ids, v, w)
+        with pytest.raises(ar.ArgreduceError):
+            ar.distill_loss(x, ids, v)
+    else:
+        d = ar.distill_loss(x, ids, v)
+        loss, grad = d.loss, None
+        with pytest.raises(ar.ArgreduceError):
+            ar.distill_loss_grad(x, ids, v, d.stats, w)
+    torch.cuda.synchronize()
+    at = torch.tensor([0, 1, rows // 2 - 1, rows // 3, (1 << 26) - 1, rows - 5, rows - 1], device="cuda")
+    xs, i_s = host(x[at]), ids[at].cpu().numpy()
+    for n in range(len(xs)):
+        want = R.distill_row(xs[n], i_s[n], np.zeros(1), 1.0)
+        R.agree(host(loss[at])[n], want["loss"], want["tol"], f"sample {n}")
+        if step:
+            d, tol = R.distill_grad_row(want, xs[n], 1.0, 1.0, "f16")
+            R.agree(host(grad[at])[n], d, tol, f"sample {n} gradient")
+    del x, ids, v, w, loss, grad
+    torch.cuda.empty_cache()

@@ -179,3 +179,37 @@ def test_the_stride_of_a_single_row_does_not_matter(lib):
 def test_rows_times_columns_past_64_bits(lib):
     args = (FAKE, B.F32, INT32_MAX, INT32_MAX, INT32_MAX) + CALLS["argreduce_logprobs"]
     assert lib.argreduce_logprobs(*args) == -3
+
+
+# (call, rows, cols, dtype, k) whose own launches hold fewer than 2^32 threads, though those of the
+# gradient as a call of its own (the first two), or a workgroup or wavefront per row, would not
+WIDE_BUT_FINE = [("argreduce_distill", 1 << 23, 4104, B.F32, 3), ("argreduce_distill", 1 << 28, 64, B.F16, 3),
+                 ("argreduce_distill_step", 1 << 23, 4104, B.F32, 3),
+                 ("argreduce_distill_step", 1 << 28, 64, B.F16, 3),
+                 ("argreduce_distill_step", 1 << 26, 264, B.F16, 1),
+                 ("argreduce_distill_step", 1 << 24, 5000, B.F16, 64),
+                 ("argreduce_distill_step", 1 << 24, 264, B.BF16, 1024)]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="accepted calls would run on these addresses")
+@pytest.mark.parametrize("name,rows,cols,dtype,k", WIDE_BUT_FINE)
+def test_a_call_is_refused_for_its_own_launches_only(lib, name, rows, cols, dtype, k):
+    """Without a GPU such a call gets as far as its launch, which fails."""
+    rest = (k,) + CALLS[name][1:]
+    assert getattr(lib, name)(FAKE, dtype, rows, cols, cols, *rest) == -5
+    assert B.argreduce_distill_scratch_bytes(rows, cols, dtype) == 0
+    if name == "argreduce_distill":
+        assert B.argreduce_distill_plan(rows, cols, dtype)["grid_blocks"] > 0
+
+
+@pytest.mark.parametrize("rows,cols,stride,dtype", [(INT32_MAX, 1 << 20, 1 << 20, B.F32),
+                                                    (1 << 15, 8, 1 << 31, B.F32), (1 << 16, 8, 1 << 31, B.BF16),
+                                                    (INT32_MAX, 8, (1 << 32) - 1, B.F16)])
+def test_logits_beyond_the_address_space(lib, rows, cols, stride, dtype):
+    for name, rest in CALLS.items():
+        assert getattr(lib, name)(FAKE, dtype, rows, cols, stride, *rest) == -3
+
+
+def test_a_gradient_with_too_large_a_grid_is_refused(lib):
+    for name in ("argreduce_logprobs_grad", "argreduce_distill_grad"):
+        assert getattr(lib, name)(FAKE, B.F32, 1 << 23, 4104, 4104, *CALLS[name]) == -3
