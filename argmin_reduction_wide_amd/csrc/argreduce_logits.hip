@@ -678,12 +678,18 @@ __device__ inline void top_none(uint32_t k, int lane, int step, float v, float* 
 struct RowOut {
     float logprob, entropy, m, l2;
 };
-// stats is [4, rows]: log probability, entropy, maximum, log2 of the sum.
-__device__ inline void store_stats(float* stats, uint32_t rows, uint32_t r, const RowOut& o) {
+// A row's alternatives, and whether the entropy goes to a row of its own too, in 16 bits.
+constexpr uint32_t kApart = 0x8000u;
+__device__ inline uint32_t alternatives(uint32_t outputs) { return outputs & ~kApart; }
+// stats is [4, rows]: log probability, entropy, maximum, log2 of the sum; [5, rows]: the entropy again.
+template <bool ENT>
+__device__ inline void store_stats(float* stats, uint32_t rows, uint32_t r, const RowOut& o,
+                                   uint32_t outputs) {
     stats[r] = o.logprob;
     stats[static_cast<size_t>(rows) + r] = o.entropy;
     stats[2 * static_cast<size_t>(rows) + r] = o.m;
     stats[3 * static_cast<size_t>(rows) + r] = o.l2;
+    if (ENT && (outputs & kApart)) stats[4 * static_cast<size_t>(rows) + r] = o.entropy;
 }
 template <bool ENT>
 __device__ inline RowOut row_out(const Stat& a, float xt, float scale) {
@@ -723,7 +729,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint3
                                                             float* stats, uint64_t top_lp,
                                                             int64_t* top_tok) {
     constexpr int VW = Fmt::VW;
-    const uint32_t k = tag(top_lp);
+    const uint32_t outputs = tag(top_lp), k = alternatives(outputs);
     const uint32_t want = blockIdx.x * (kBlockThreads / G) + threadIdx.x / G;
     const uint32_t r = want < rows ? want : rows - 1;  // lanes past the end repeat the last row
     const int lane = threadIdx.x % G;
@@ -751,7 +757,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint3
     a.s = lanes_sum<G>(a.s);
     if constexpr (ENT) a.h = lanes_sum<G>(a.h);
     const RowOut o = live ? row_out<ENT>(a, xt, scale) : row_left_out<ENT>();
-    if (lane == 0 && want < rows) store_stats(stats, rows, r, o);
+    if (lane == 0 && want < rows) store_stats<ENT>(stats, rows, r, o, outputs);
     if (k == 0) return;
     float* lp = addr<float>(top_lp) + static_cast<size_t>(r) * k;
     int64_t* tok = top_tok + static_cast<size_t>(r) * k;
@@ -809,11 +815,11 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32
     const int lane = lane_of<T>();
     if (r >= rows) return;  // whole teams, and never one of several wavefronts
     const int64_t t = tokens[r];
-    const uint32_t k = tag(top_lp);
+    const uint32_t outputs = tag(top_lp), k = alternatives(outputs);
     float* lp = addr<float>(top_lp) + static_cast<size_t>(r) * k;
     int64_t* tok = top_tok + static_cast<size_t>(r) * k;
     if (t < 0) {
-        if (lane == 0) store_stats(stats, rows, r, row_left_out<ENT>());
+        if (lane == 0) store_stats<ENT>(stats, rows, r, row_left_out<ENT>(), outputs);
         if constexpr (TOP) top_none(k, lane, T, -__builtin_huge_valf(), lp, tok);
         return;
     }
@@ -826,7 +832,7 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32
     scan_span<Fmt, ENT, T, U, TOP>(sp, true, sp.va, sp.vb, lane, scale, a, g, L.seg);
     team_merge<ENT, T>(a, scale, lane, sh);
     const RowOut o = row_out<ENT>(a, xt, scale);
-    if (lane == 0) store_stats(stats, rows, r, o);
+    if (lane == 0) store_stats<ENT>(stats, rows, r, o, outputs);
     if constexpr (TOP) {
         if (!(a.s > 0.0f)) {
             top_none(k, lane, T, a.s == 0.0f ? -__builtin_huge_valf() : __builtin_nanf(""), lp, tok);
@@ -905,7 +911,7 @@ __device__ inline Stat merge_parts(const Part* p, uint32_t parts, float scale, i
 // ([32,202048] bf16): chained latencies, of the slices' statistics, the bisection, and the segments'
 // second read. A kernel of its own, since the last workgroup of k_part to arrive could do it only
 // with a counter that something has to clear for every call. Tags: columns in (x, tokens), slices,
-// alternatives, scale.
+// outputs, scale.
 template <typename Fmt, bool ENT, bool TOP, int T = TOP ? kMergeTopThreads : kMergeThreads>
 __global__ __launch_bounds__(T) void k_lp_merge(uint64_t x, uint64_t tokens,
                                                             uint64_t part, uint64_t stats_,
@@ -914,7 +920,7 @@ __global__ __launch_bounds__(T) void k_lp_merge(uint64_t x, uint64_t tokens,
     __shared__ float sh[T / kWave][kShared];
     __shared__ TopLds<TOP ? T : 64, TOP ? kMergeSegs : 1> L;
     const uint32_t cols = tags(x, tokens);
-    const uint32_t parts = tag(part), k = tag(stats_);
+    const uint32_t parts = tag(part), outputs = tag(stats_), k = alternatives(outputs);
     const float scale = __uint_as_float(tags(top_lp, top_tok));
     float* stats = addr<float>(stats_);
     const uint32_t r = blockIdx.x;
@@ -923,7 +929,7 @@ __global__ __launch_bounds__(T) void k_lp_merge(uint64_t x, uint64_t tokens,
     float* lp = addr<float>(top_lp) + static_cast<size_t>(r) * k;
     int64_t* tok = addr<int64_t>(top_tok) + static_cast<size_t>(r) * k;
     if (t < 0) {
-        if (lane == 0) store_stats(stats, rows, r, row_left_out<ENT>());
+        if (lane == 0) store_stats<ENT>(stats, rows, r, row_left_out<ENT>(), outputs);
         if constexpr (TOP) top_none(k, lane, T, -__builtin_huge_valf(), lp, tok);
         return;
     }
@@ -932,7 +938,7 @@ __global__ __launch_bounds__(T) void k_lp_merge(uint64_t x, uint64_t tokens,
     const Part* p = addr<const Part>(part) + static_cast<size_t>(r) * parts;
     const Stat a = merge_parts<ENT, T>(p, parts, scale, lane, sh);
     const RowOut o = row_out<ENT>(a, xt, scale);
-    if (lane == 0) store_stats(stats, rows, r, o);
+    if (lane == 0) store_stats<ENT>(stats, rows, r, o, outputs);
     if constexpr (TOP) {
         if (!(a.s > 0.0f)) {
             top_none(k, lane, T, a.s == 0.0f ? -__builtin_huge_valf() : __builtin_nanf(""), lp, tok);
@@ -1831,8 +1837,9 @@ void launch_entries(void (*kernel)(KArgs...), uint32_t grid, int block, size_t l
 size_t part_bytes() { return sizeof(Part); }
 
 hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const int64_t* tokens,
-                           bool entropy, int top, float* stats, float* top_logprobs,
+                           bool entropy, bool apart, int top, float* stats, float* top_logprobs,
                            int64_t* top_tokens, uint8_t* scratch16, hipStream_t s) {
+    const uint32_t outputs = static_cast<uint32_t>(top) | (apart ? kApart : 0);
     const uint32_t cols = static_cast<uint32_t>(a.cols), stride = static_cast<uint32_t>(a.row_stride);
     const uint32_t rows = static_cast<uint32_t>(a.rows);
     const uint32_t grid = static_cast<uint32_t>(plan.grid_blocks);
@@ -1844,7 +1851,7 @@ hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const in
             if (plan.path == ARGREDUCE_PATH_SUBWAVE && plan.team < kWave) {
                 const auto go = [&](auto g) {
                     launch(k_lp_group<Fmt, KEEP, ENT, decltype(g)::value>, grid, kBlockThreads, s, a.x, cols,
-                           stride, a.scale, rows, tokens, stats, tagged(top_logprobs, top), top_tokens);
+                           stride, a.scale, rows, tokens, stats, tagged(top_logprobs, outputs), top_tokens);
                 };
                 with_group(plan.team, go);
                 return;
@@ -1858,13 +1865,13 @@ hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const in
                     const uint32_t sc = bits_of(a.scale);
                     launch(k_lp_merge<Fmt, ENT, TOP>, rows, TOP ? kMergeTopThreads : kMergeThreads, s,
                            tagged(a.x, cols), tagged(tokens, cols >> 16), tagged(part, plan.parts),
-                           tagged(stats, top), tagged(top_logprobs, sc), tagged(top_tokens, sc >> 16), stride, rows);
+                           tagged(stats, outputs), tagged(top_logprobs, sc), tagged(top_tokens, sc >> 16), stride, rows);
                     return;
                 }
                 with_team(plan.team, [&](auto team) {
                     constexpr int T = decltype(team)::value;
                     launch(k_lp_team<Fmt, KEEP, ENT, TOP, T>, grid, kTeamBlock<T>, s, a.x, cols, stride,
-                           a.scale, rows, tokens, stats, tagged(top_logprobs, top), top_tokens);
+                           a.scale, rows, tokens, stats, tagged(top_logprobs, outputs), top_tokens);
                 });
             });
         });

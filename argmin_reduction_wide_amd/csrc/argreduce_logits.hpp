@@ -62,8 +62,9 @@ struct LogitsArgs {
 
 size_t part_bytes();  // scratch of one slice of a split row
 
+// `apart`: the entropy also goes to a fifth row of stats.
 hipError_t launch_logprobs(const LogitsPlan& plan, const LogitsArgs& a, const int64_t* tokens,
-                           bool entropy, int top, float* stats, float* top_logprobs,
+                           bool entropy, bool apart, int top, float* stats, float* top_logprobs,
                            int64_t* top_tokens, uint8_t* scratch16, hipStream_t stream);
 hipError_t launch_logprobs_grad(const GradPlan& plan, const LogitsArgs& a, const int64_t* tokens,
                                 const float* stats, const float* g_logprob, const float* g_entropy,

@@ -313,9 +313,9 @@ ARGREDUCE_EXPORT int argreduce_logprobs(const void* x, argreduce_dtype_t dtype, 
     uint8_t* scratch16 = nullptr;
     rc = scratch_of(p, scratch, scratch_bytes, &scratch16);
     if (rc != ARGREDUCE_OK) return rc;
-    return status_of(launch_logprobs(p, a, tokens, entropy != 0, top, stats, top > 0 ? top_logprobs : nullptr,
-                                     top > 0 ? top_tokens : nullptr, scratch16,
-                                     static_cast<hipStream_t>(stream)));
+    return status_of(launch_logprobs(p, a, tokens, entropy != 0, entropy == ARGREDUCE_ENTROPY_APART, top,
+                                     stats, top > 0 ? top_logprobs : nullptr, top > 0 ? top_tokens : nullptr,
+                                     scratch16, static_cast<hipStream_t>(stream)));
 }
 
 ARGREDUCE_EXPORT int argreduce_logprobs_grad(const void* x, argreduce_dtype_t dtype, int64_t rows,

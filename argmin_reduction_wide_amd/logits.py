@@ -21,13 +21,16 @@ from . import binding as B
 
 TOP_MAX = 64         # alternatives per row (ARGREDUCE_TOP_MAX)
 TEACHER_MAX = 1024   # teacher entries per row (ARGREDUCE_TEACHER_MAX)
+_ENTROPY_APART = -2  # ARGREDUCE_ENTROPY_APART
 
+_F32, _I64 = torch.float32, torch.int64
 _CODES = {torch.float32: B.F32, torch.float16: B.F16, torch.bfloat16: B.BF16}
 
 
 class TokenLogprobs(NamedTuple):
     """What token_logprobs returns. ``stats`` (float32 [4, rows]) is what token_logprobs_grad
-    takes; logprob and entropy are its first two rows in the logits' leading shape."""
+    takes: the log probabilities and entropies once more, and two rows of its own. It reads none of
+    the memory of logprob and entropy, which may be written over."""
 
     logprob: torch.Tensor
     entropy: Optional[torch.Tensor]
@@ -75,7 +78,7 @@ def _rows(logits):
 
 def _same(t, name: str, like, dtype, shape) -> None:
     """An input array: contiguous, of this type and shape, on the logits' device."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == like.device:
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == like.get_device():
         return
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}; got {t.dtype}")
@@ -146,39 +149,45 @@ def _refuse_captured_autograd() -> None:
 # token_logprobs
 
 
-def _logprobs(logits, tokens, temperature, entropy, top, scratch):
+def _logprobs(logits, tokens, temperature, entropy, top, scratch, apart=False):
+    """(stats, top_logprobs, top_tokens, entropy): with `apart` the entropy in memory that the
+    gradient does not read, else None."""
     code, rows, cols, stride = _rows(logits)
-    shape = logits.shape
-    lead = shape[:-1]
-    _same(tokens, "tokens", logits, torch.int64, lead)
+    lead = (rows,) if logits.dim() == 2 else logits.shape[:-1]
+    _same(tokens, "tokens", logits, _I64, lead)
     temperature = _temperature(temperature)
     if not 0 <= top <= TOP_MAX:
         raise ValueError(f"top must lie in 0..{TOP_MAX}; got {top}")
-    if _elsewhere(logits):
-        with torch.cuda.device(logits.device):
-            return _logprobs(logits, tokens, temperature, entropy, top, scratch)
     device = logits.device
-    stats = torch.empty(4, rows, dtype=torch.float32, device=device)
-    lp = tok = None
-    lp_ptr = tok_ptr = 0
+    if device.index != _device():
+        with torch.cuda.device(device):
+            return _logprobs(logits, tokens, temperature, entropy, top, scratch, apart)
+    ent = lp = tok = None
+    lp_ptr = tok_ptr = sptr = sbytes = 0
+    if entropy and apart:
+        buf = torch.empty(5, rows, dtype=_F32, device=device)
+        stats, ent, entropy = buf.as_strided((4, rows), (rows, 1)), buf[4], _ENTROPY_APART
+    else:
+        stats = torch.empty(4, rows, dtype=_F32, device=device)
     if top:
-        lp = torch.empty(*lead, top, dtype=torch.float32, device=device)
-        tok = torch.empty(*lead, top, dtype=torch.int64, device=device)
+        lp = torch.empty(*lead, top, dtype=_F32, device=device)
+        tok = torch.empty(*lead, top, dtype=_I64, device=device)
         lp_ptr, tok_ptr = lp.data_ptr(), tok.data_ptr()
     need = _call.logprobs_scratch_bytes(rows, cols, code)
-    sptr, sbytes, scratch = _scratch(need, "argreduce_logprobs", scratch, device)
+    if need or scratch is not None:
+        sptr, sbytes, scratch = _scratch(need, "argreduce_logprobs", scratch, device)
     rc = _call.logprobs(logits.data_ptr(), code, rows, cols, stride, tokens.data_ptr(), temperature,
-                        1 if entropy else 0, top, stats.data_ptr(), lp_ptr, tok_ptr, sptr, sbytes,
+                        int(entropy), top, stats.data_ptr(), lp_ptr, tok_ptr, sptr, sbytes,
                         _stream(device.index))
     if rc:
         raise _failed(rc, "logprobs", rows, cols, stride)
-    return stats, lp, tok
+    return stats, lp, tok, ent
 
 
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, temperature, entropy, top, scratch):
-        stats, lp, tok = _logprobs(logits, tokens, temperature, entropy, top, scratch)
+        stats, lp, tok, _ = _logprobs(logits, tokens, temperature, entropy, top, scratch)
         ctx.save_for_backward(logits, tokens, stats)
         ctx.temperature, ctx.entropy = temperature, entropy
         # outputs of their own: a view of stats would carry its gradient to the other rows
@@ -219,11 +228,11 @@ def token_logprobs(logits, tokens, *, temperature: float = 1.0, entropy: bool = 
         _refuse_captured_autograd()
         return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, bool(entropy), top,
                                                    scratch))
-    stats, lp, tok = _logprobs(logits, tokens, temperature, entropy, top, scratch)
+    stats, lp, tok, ent = _logprobs(logits, tokens, temperature, bool(entropy), top, scratch, True)
     if logits.dim() == 2:
-        return TokenLogprobs(stats[0], stats[1] if entropy else None, lp, tok, stats)
+        return TokenLogprobs(stats[0], ent, lp, tok, stats)
     lead = logits.shape[:-1]
-    return TokenLogprobs(stats[0].view(lead), stats[1].view(lead) if entropy else None, lp, tok, stats)
+    return TokenLogprobs(stats[0].view(lead), None if ent is None else ent.view(lead), lp, tok, stats)
 
 
 def _grad_out(logits, rows, cols, stride, out):

@@ -328,6 +328,7 @@ int argreduce_scan_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
  */
 #define ARGREDUCE_TOP_MAX 64        /* alternatives per row */
 #define ARGREDUCE_TEACHER_MAX 1024  /* teacher entries per row */
+#define ARGREDUCE_ENTROPY_APART (-2) /* argreduce_logprobs: the entropy in a row of its own too */
 
 /*
  * Log probabilities of given tokens, with entropy and the top alternatives.
@@ -336,7 +337,10 @@ int argreduce_scan_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
  *                 do not matter, log probability and entropy are 0, and it has no alternatives.
  *                 One >= cols gives a NaN log probability (and a NaN gradient, unless every
  *                 logit of the row is -inf).
- *   entropy       non-zero: compute the entropy; 0: row 1 of stats is NaN.
+ *   entropy       non-zero: compute the entropy; 0: row 1 of stats is NaN. ARGREDUCE_ENTROPY_APART:
+ *                 the entropy also goes to a fifth row of stats, which is [5, rows] then, for a
+ *                 caller who hands that row out to be written over (argreduce_logprobs_grad reads
+ *                 rows 1 to 3).
  *   top           alternatives per row, 0 .. ARGREDUCE_TOP_MAX.
  *   stats         [4, rows] out: ln p of the token; entropy -sum p ln p; and two rows for
  *                 argreduce_logprobs_grad (the row's maximum, and log2 sum exp((x - max) / T)).

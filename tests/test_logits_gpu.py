@@ -895,3 +895,52 @@ def test_more_rows_than_other_calls_hold(rows, cols, step):
             R.agree(host(grad[at])[n], d, tol, f"sample {n} gradient")
     del x, ids, v, w, loss, grad
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("rows,cols", [(13, 50), (13, 700), (13, 9000), (13, 140001), (3, 202048)])
+def test_outputs_may_be_written_over(dtype, rows, cols):
+    """The gradient does not depend on what a caller does with the log probabilities and entropies."""
+    announce(f"outputs written over {dtype} [{rows},{cols}]")
+    rng = np.random.default_rng(cols)
+    x = make_rows(rng, rows, cols, dtype)
+    tokens = make_tokens(rng, rows, cols)
+    w, e = torch.ones(rows, device="cuda"), torch.ones(rows, device="cuda")
+    for top in (0, 3):
+        r = ar.token_logprobs(x, tokens, entropy=True, top=top)
+        assert r.stats.shape == (4, rows)
+        assert torch.equal(r.logprob.nan_to_num(9.0), r.stats[0].nan_to_num(9.0))
+        assert torch.equal(r.entropy.nan_to_num(9.0), r.stats[1].nan_to_num(9.0))
+        want = ar.token_logprobs_grad(x, tokens, r.stats, w, e)
+        r.logprob.fill_(7.0)
+        r.entropy.mul_(0.0)
+        got = ar.token_logprobs_grad(x, tokens, r.stats, w, e)
+        assert torch.equal(got.nan_to_num(9.0), want.nan_to_num(9.0))
+    ids, v = make_teacher(np.random.default_rng(1), rows, cols, 4)
+    d = ar.distill_loss(x, ids, v)
+    want = ar.distill_loss_grad(x, ids, v, d.stats, w)
+    d.loss.fill_(7.0)
+    got = ar.distill_loss_grad(x, ids, v, d.stats, w)
+    assert torch.equal(got.nan_to_num(9.0), want.nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("entropy", [0, 1, 2, -1, -2])
+@pytest.mark.parametrize("rows,cols", [(3, 50), (3, 700), (3, 9000), (3, 202048)])
+def test_rows_of_the_statistics(rows, cols, entropy):
+    """[4, rows], and the entropy again in a fifth row for ARGREDUCE_ENTROPY_APART alone."""
+    announce(f"statistics [{rows},{cols}] entropy={entropy}")
+    x = torch.randn(rows, cols, device="cuda")
+    tokens = torch.tensor([0, -1, cols - 1], device="cuda")
+    need = B.argreduce_logprobs_scratch_bytes(rows, cols, B.F32)
+    scratch = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    want = ar.token_logprobs(x, tokens, entropy=True).stats
+    stats = torch.full((6, rows), 5.0, device="cuda")
+    for call in (B.fast().argreduce_logprobs, B.lib().argreduce_logprobs):
+        stats.fill_(5.0)
+        assert call(x.data_ptr(), B.F32, rows, cols, cols, tokens.data_ptr(), 1.0, entropy, 0, stats.data_ptr(),
+                    0, 0, scratch.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(stats[0], want[0]) and torch.equal(stats[2:4], want[2:4])
+        assert torch.equal(stats[1], want[1]) if entropy else stats[1].isnan().all()
+        assert torch.equal(stats[4], want[1]) if entropy == -2 else (stats[4] == 5).all()
+        assert (stats[5] == 5).all()

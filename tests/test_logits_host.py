@@ -213,3 +213,8 @@ def test_logits_beyond_the_address_space(lib, rows, cols, stride, dtype):
 def test_a_gradient_with_too_large_a_grid_is_refused(lib):
     for name in ("argreduce_logprobs_grad", "argreduce_distill_grad"):
         assert getattr(lib, name)(FAKE, B.F32, 1 << 23, 4104, 4104, *CALLS[name]) == -3
+
+
+def test_the_fifth_row_of_statistics_is_named_alike():
+    text = open(B.LIB_PATH.replace("libargreduce.so", "../include/argreduce.h")).read()
+    assert f"#define ARGREDUCE_ENTROPY_APART ({ar.logits._ENTROPY_APART}) " in text
