@@ -8,14 +8,16 @@ and rows may be further apart than cols (a slice of a padded vocabulary, or of o
 sequence, needs no copy).
 
 ``token_logprobs`` and ``distill_loss`` take part in autograd when the logits require a
-gradient. ``token_logprobs_grad``, ``distill_loss_grad`` and ``distill_step`` are the same
-gradients as plain calls, which can also be captured into a graph.
+gradient; they have no forward-mode derivative and refuse logits that carry a tangent.
+``token_logprobs_grad``, ``distill_loss_grad`` and ``distill_step`` are the same gradients as plain
+calls, which take no part in autograd and can also be captured into a graph.
 """
 from __future__ import annotations
 
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import binding as B
 
@@ -145,6 +147,12 @@ def _refuse_captured_autograd() -> None:
                            "token_logprobs_grad, distill_loss_grad or distill_step in the capture")
 
 
+def _refuse_forward_mode(logits) -> None:
+    """A dual tensor need not require a gradient: its tangent would be lost without a word."""
+    if _forward_ad._current_level >= 0 and _forward_ad.unpack_dual(logits).tangent is not None:
+        raise NotImplementedError("the logits operators have no forward-mode derivative")
+
+
 # ---------------------------------------------------------------------------------------
 # token_logprobs
 
@@ -224,6 +232,7 @@ def token_logprobs(logits, tokens, *, temperature: float = 1.0, entropy: bool = 
     likely first, ties to the lower token; rows with fewer unmasked logits end in token -1.
 
     Differentiable in logprob and entropy (float32) when the logits require a gradient."""
+    _refuse_forward_mode(logits)
     if logits.requires_grad and torch.is_grad_enabled():
         _refuse_captured_autograd()
         return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, bool(entropy), top,
@@ -342,6 +351,7 @@ def distill_loss(logits, teacher_tokens, teacher_logits, *, temperature: float =
     without an entry of weight has loss 0. The loss is not multiplied by temperature ** 2.
 
     Differentiable in the loss when the logits require a gradient; the teacher is a constant."""
+    _refuse_forward_mode(logits)
     if logits.requires_grad and torch.is_grad_enabled():
         _refuse_captured_autograd()
         return DistillLoss(*_DistillLoss.apply(logits, teacher_tokens, teacher_logits, temperature,

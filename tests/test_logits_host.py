@@ -218,3 +218,34 @@ def test_a_gradient_with_too_large_a_grid_is_refused(lib):
 def test_the_fifth_row_of_statistics_is_named_alike():
     text = open(B.LIB_PATH.replace("libargreduce.so", "../include/argreduce.h")).read()
     assert f"#define ARGREDUCE_ENTROPY_APART ({ar.logits._ENTROPY_APART}) " in text
+
+
+@pytest.mark.parametrize("requires_grad", [False, True])
+def test_forward_mode_is_refused(requires_grad):
+    """Logits with a tangent, also where autograd is off; without one, and after the level, the calls
+    get as far as their other checks."""
+    from torch.autograd import forward_ad
+
+    x, t = torch.zeros(2, 8, requires_grad=requires_grad), torch.zeros(2, dtype=torch.int64)
+    ids, v = torch.zeros(2, 3, dtype=torch.int64), torch.zeros(2, 3)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones(2, 8))
+        for f in (lambda y: ar.token_logprobs(y, t), lambda y: ar.distill_loss(y, ids, v)):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                f(dual)
+            with torch.no_grad(), pytest.raises(NotImplementedError, match="forward-mode"):
+                f(dual)
+            with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+                f(x)
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+        ar.token_logprobs(x, t)
+
+
+def test_function_transforms_are_refused():
+    t = torch.zeros(2, dtype=torch.int64)
+    f = lambda y: ar.token_logprobs(y, t).logprob.sum()
+    with pytest.raises(NotImplementedError, match="forward-mode"):
+        torch.func.jvp(f, (torch.zeros(2, 8),), (torch.ones(2, 8),))
+    for transform in (torch.func.grad(f), torch.func.jacfwd(f)):
+        with pytest.raises((RuntimeError, ValueError)):
+            transform(torch.zeros(2, 8))
