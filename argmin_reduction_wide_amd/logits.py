@@ -139,10 +139,10 @@ def _failed(rc: int, what: str, rows, cols, stride):
     return B.ArgreduceError(rc, f"argreduce_{what}(rows={rows}, cols={cols}, row_stride={stride})")
 
 
-def _refuse_captured_autograd() -> None:
+def _refuse_captured_autograd(logits) -> None:
     """An autograd graph recorded while a HIP graph is captured can share gradient accumulators
     with an eager one, which ends the process when the engine joins their streams."""
-    if torch.cuda.is_current_stream_capturing():
+    if logits.is_cuda and torch.cuda.is_current_stream_capturing():
         raise RuntimeError("autograd through the logits operators cannot be captured: call "
                            "token_logprobs_grad, distill_loss_grad or distill_step in the capture")
 
@@ -210,7 +210,7 @@ class _TokenLogprobs(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, g_logprob, g_entropy, *_):
         logits, tokens, stats = ctx.saved_tensors
-        _refuse_captured_autograd()
+        _refuse_captured_autograd(logits)
         if g_logprob is None and g_entropy is None:
             return (None,) * 6
         lead = logits.shape[:-1]
@@ -234,7 +234,7 @@ def token_logprobs(logits, tokens, *, temperature: float = 1.0, entropy: bool = 
     Differentiable in logprob and entropy (float32) when the logits require a gradient."""
     _refuse_forward_mode(logits)
     if logits.requires_grad and torch.is_grad_enabled():
-        _refuse_captured_autograd()
+        _refuse_captured_autograd(logits)
         return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, bool(entropy), top,
                                                    scratch))
     stats, lp, tok, ent = _logprobs(logits, tokens, temperature, bool(entropy), top, scratch, True)
@@ -335,7 +335,7 @@ class _DistillLoss(torch.autograd.Function):
         if g_loss is None:
             return (None,) * 5
         logits, teacher_tokens, teacher_logits, stats = ctx.saved_tensors
-        _refuse_captured_autograd()
+        _refuse_captured_autograd(logits)
         grad = distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, g_loss.contiguous(),
                                  temperature=ctx.temperature)
         return grad, None, None, None, None
@@ -353,7 +353,7 @@ def distill_loss(logits, teacher_tokens, teacher_logits, *, temperature: float =
     Differentiable in the loss when the logits require a gradient; the teacher is a constant."""
     _refuse_forward_mode(logits)
     if logits.requires_grad and torch.is_grad_enabled():
-        _refuse_captured_autograd()
+        _refuse_captured_autograd(logits)
         return DistillLoss(*_DistillLoss.apply(logits, teacher_tokens, teacher_logits, temperature,
                                                scratch))
     stats = _distill(logits, teacher_tokens, teacher_logits, temperature, scratch)

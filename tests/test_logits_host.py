@@ -249,3 +249,12 @@ def test_function_transforms_are_refused():
     for transform in (torch.func.grad(f), torch.func.jacfwd(f)):
         with pytest.raises((RuntimeError, ValueError)):
             transform(torch.zeros(2, 8))
+
+
+def test_cpu_logits_that_require_a_gradient_are_refused_alike():
+    """With or without a GPU in the machine: no HIP call comes before the refusal."""
+    x, t = torch.zeros(2, 8, requires_grad=True), torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="GPU"):
+        ar.token_logprobs(x, t)
+    with pytest.raises(ValueError, match="GPU"):
+        ar.distill_loss(x, t.view(2, 1), torch.zeros(2, 1))
