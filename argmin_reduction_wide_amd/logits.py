@@ -244,23 +244,31 @@ def token_logprobs(logits, tokens, *, temperature: float = 1.0, entropy: bool = 
     return TokenLogprobs(stats[0].view(lead), None if ent is None else ent.view(lead), lp, tok, stats)
 
 
-def _grad_out(logits, rows, cols, stride, out):
-    if out is None:
-        return torch.empty(*logits.shape, dtype=logits.dtype, device=logits.device)
+def _new_grad(logits):
+    return torch.empty(*logits.shape, dtype=logits.dtype, device=logits.device)
+
+
+def _check_grad(logits, rows, cols, stride, out, **others):
+    """The caller's gradient tensor, which shares no memory with the logits or the other arguments,
+    all contiguous (the kernels read them while they write it)."""
     B._check_buffer(out, "out", logits.device, logits.dtype, logits.numel())
     if out.shape != logits.shape:
         raise ValueError(f"out must have shape {tuple(logits.shape)}; got {tuple(out.shape)}")
     size, x, g = logits.element_size(), logits.data_ptr(), out.data_ptr()
     if rows > 0 and g < x + ((rows - 1) * stride + cols) * size and x < g + rows * cols * size:
         raise ValueError("out must not overlap the logits")
+    for name, t in others.items():
+        if t is not None and g < t.data_ptr() + t.numel() * t.element_size() and \
+                t.data_ptr() < g + rows * cols * size:
+            raise ValueError(f"out must not overlap {name}")
     return out
 
 
 def token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy=None, *,
                         temperature: float = 1.0, out=None):
     """Gradient of ``(grad_logprob * logprob + grad_entropy * entropy).sum()`` with respect to the
-    logits, in their type and shape (contiguous; ``out``, if given, is such a tensor). stats is
-    that of the forward call on the same logits, tokens and temperature, made with
+    logits, in their type and shape (contiguous; ``out``, if given, is such a tensor, apart from
+    every argument's memory). stats is that of the forward call on the same logits, tokens and temperature, made with
     ``entropy=True`` if grad_entropy is given; grad_logprob and grad_entropy are float32 in the
     logits' leading shape."""
     code, rows, cols, stride = _rows(logits)
@@ -271,7 +279,9 @@ def token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy=None, 
     if grad_entropy is not None:
         _same(grad_entropy, "grad_entropy", logits, torch.float32, lead)
     temperature = _temperature(temperature)
-    out = _grad_out(logits, rows, cols, stride, out)
+    out = _new_grad(logits) if out is None else _check_grad(
+        logits, rows, cols, stride, out, tokens=tokens, stats=stats, grad_logprob=grad_logprob,
+        grad_entropy=grad_entropy)
     if _elsewhere(logits):
         with torch.cuda.device(logits.device):
             return token_logprobs_grad(logits, tokens, stats, grad_logprob, grad_entropy,
@@ -363,14 +373,16 @@ def distill_loss(logits, teacher_tokens, teacher_logits, *, temperature: float =
 def distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss, *,
                       temperature: float = 1.0, out=None):
     """Gradient of ``(grad_loss * loss).sum()`` with respect to the logits, in their type and shape
-    (contiguous; ``out``, if given, is such a tensor). stats is that of the forward call on the
-    same inputs; grad_loss is float32 in the logits' leading shape."""
+    (contiguous; ``out``, if given, is such a tensor, apart from every argument's memory). stats is
+    that of the forward call on the same inputs; grad_loss is float32 in the logits' leading shape."""
     code, rows, cols, stride = _rows(logits)
     k = _teacher(logits, teacher_tokens, teacher_logits)
     _same(stats, "stats", logits, torch.float32, (5, rows))
     _same(grad_loss, "grad_loss", logits, torch.float32, logits.shape[:-1])
     temperature = _temperature(temperature)
-    out = _grad_out(logits, rows, cols, stride, out)
+    out = _new_grad(logits) if out is None else _check_grad(
+        logits, rows, cols, stride, out, teacher_tokens=teacher_tokens, teacher_logits=teacher_logits,
+        stats=stats, grad_loss=grad_loss)
     if _elsewhere(logits):
         with torch.cuda.device(logits.device):
             return distill_loss_grad(logits, teacher_tokens, teacher_logits, stats, grad_loss,
@@ -388,12 +400,15 @@ def distill_step(logits, teacher_tokens, teacher_logits, weights, *, temperature
                  out=None, scratch=None):
     """(loss, grad): the loss of every row, and the gradient of ``(weights * loss).sum()`` with
     respect to the logits, in one call that reads the logits from memory once. For a training step
-    whose row weights (float32, the logits' leading shape) do not depend on the loss."""
+    whose row weights (float32, the logits' leading shape) do not depend on the loss. out: as for
+    distill_loss_grad."""
     code, rows, cols, stride = _rows(logits)
     k = _teacher(logits, teacher_tokens, teacher_logits)
     _same(weights, "weights", logits, torch.float32, logits.shape[:-1])
     temperature = _temperature(temperature)
-    out = _grad_out(logits, rows, cols, stride, out)
+    out = _new_grad(logits) if out is None else _check_grad(
+        logits, rows, cols, stride, out, teacher_tokens=teacher_tokens, teacher_logits=teacher_logits,
+        weights=weights, scratch=scratch)
     if _elsewhere(logits):
         with torch.cuda.device(logits.device):
             return distill_step(logits, teacher_tokens, teacher_logits, weights,

@@ -944,3 +944,35 @@ def test_rows_of_the_statistics(rows, cols, entropy):
         assert torch.equal(stats[1], want[1]) if entropy else stats[1].isnan().all()
         assert torch.equal(stats[4], want[1]) if entropy == -2 else (stats[4] == 5).all()
         assert (stats[5] == 5).all()
+
+
+def test_gradient_over_another_argument_is_refused():
+    announce("overlap with other arguments")
+    rows, cols, k = 4, 8, 3
+    buf = torch.zeros(256, device="cuda")
+    out = buf[16:16 + rows * cols].view(rows, cols)
+    x = torch.randn(rows, cols, device="cuda")
+    t = torch.zeros(rows, dtype=torch.int64, device="cuda")
+    ids, v, w = torch.zeros(rows, k, dtype=torch.int64, device="cuda"), torch.zeros(rows, k, device="cuda"), \
+        torch.ones(rows, device="cuda")
+    stats, dstats = ar.token_logprobs(x, t, entropy=True).stats, ar.distill_loss(x, ids, v).stats
+
+    def inside(like, at):  # like's values in buf, from element `at`
+        r = buf[at:at + like.numel() * like.element_size() // 4].view(like.dtype).view(like.shape)
+        return r.copy_(like)
+
+    calls = [(ar.token_logprobs_grad, dict(tokens=t, stats=stats, grad_logprob=w, grad_entropy=w)),
+             (ar.distill_loss_grad, dict(teacher_tokens=ids, teacher_logits=v, stats=dstats, grad_loss=w)),
+             (ar.distill_step, dict(teacher_tokens=ids, teacher_logits=v, weights=w))]
+    for f, args in calls:
+        for name, value in args.items():
+            n = value.numel() * value.element_size() // 4
+            for at in (16 - n + 2, 16 + rows * cols - 2):  # the last or first 8 bytes shared
+                if at >= 0:
+                    with pytest.raises(ValueError, match=f"overlap {name}"):
+                        f(x, **{**args, name: inside(value, at)}, out=out)
+            buf.fill_(5.0)
+            f(x, **{**args, name: inside(value, 16 + rows * cols)}, out=out)  # right behind it
+            assert not (out == 5).any()
+    with pytest.raises(ValueError, match="overlap scratch"):
+        ar.distill_step(x, ids, v, w, out=out, scratch=buf)
