@@ -976,3 +976,34 @@ def test_gradient_over_another_argument_is_refused():
             assert not (out == 5).any()
     with pytest.raises(ValueError, match="overlap scratch"):
         ar.distill_step(x, ids, v, w, out=out, scratch=buf)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("cap,path", [(256 * 2048, B.PATH_SPLIT), (2048, B.PATH_BLOCK)])
+@pytest.mark.parametrize("cols", [100001, 140001])
+def test_special_rows_split_and_whole(capacity, dtype, cap, path, cols):
+    """Rows of every kind, tokens and teacher entries beyond the row or absent, where the rows are
+    split over workgroups and where a workgroup has one each. (The step of a 16-bit row of 100001 is
+    one kernel, its loss alone is split.)"""
+    rows = 13
+    capacity(cap)
+    for plan in (B.argreduce_logprobs_plan, B.argreduce_distill_plan):
+        assert plan(rows, cols, dtype)["path"] == path
+    announce(f"special rows {dtype} [{rows},{cols}] path {path}")
+    rng = np.random.default_rng(cols)
+    x = make_rows(rng, rows, cols, dtype)
+    tokens = make_tokens(rng, rows, cols)
+    kinds = set()
+    for top in (0, 7, 64):
+        got = check_logprobs(x, tokens, dtype, 1.3, top != 0, top)
+        kinds |= {(row["kind"], row.get("beyond")) for row in got[3]}
+    assert kinds == {("ok", False), ("ok", True), ("nan", None), ("empty", None), ("left out", None)}
+    check_logprobs_grad(x, tokens, dtype, 1.3, True, *got, rng)
+    for k in (1, 40, 300, 1024):
+        ids, v = make_teacher(rng, rows, cols, k)
+        v[8, 0] = 50.0                     # the id beyond the row has weight
+        ids[0, 0], v[0, 0] = cols - 1, 9.0
+        ids[7, 0], v[7, 0] = 5, INF        # a teacher of +inf
+        ids[2, 0], v[2, 0] = 5, 1.0        # an empty row with a teacher
+        ids[12] = ids[12, 0].clamp(min=0)  # one id, k times
+        check_distill(x, ids, v, dtype, 1.3, rng)
