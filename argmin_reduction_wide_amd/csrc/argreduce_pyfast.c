@@ -153,8 +153,9 @@ static PyObject *fast_scan(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return PyLong_FromLong(rc);
 }
 
-/* The logits operators. int32_t and float arguments are range-checked here: a value that the
- * narrower type cannot hold raises OverflowError. */
+/* The logits operators. int32_t arguments are range-checked here: a value that the type cannot
+ * hold raises OverflowError. A temperature beyond float's range becomes an infinity, which the call
+ * refuses by its status, as it does through ctypes. */
 static int32_t arg_i32(PyObject *o) {
     const long v = PyLong_AsLong(o);
     if (v == -1 && PyErr_Occurred()) return -1;

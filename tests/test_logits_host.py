@@ -258,3 +258,12 @@ def test_cpu_logits_that_require_a_gradient_are_refused_alike():
         ar.token_logprobs(x, t)
     with pytest.raises(ValueError, match="GPU"):
         ar.distill_loss(x, t.view(2, 1), torch.zeros(2, 1))
+
+
+@pytest.mark.parametrize("temperature", [1e39, -1e39, 1e300, float("inf"), float("nan"), 1e-300])
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_temperatures_beyond_a_float_are_refused_by_status(lib, name, temperature):
+    rest = list(CALLS[name])
+    rest[1 if "logprobs" in name else 3] = temperature
+    assert getattr(lib, name)(*GOOD, *rest) == -1
+    assert getattr(B.fast(), name)(*GOOD, *rest) == -1
