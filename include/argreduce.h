@@ -308,8 +308,9 @@ int argreduce_scan_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
  * format. Results do not depend on the order in which workgroups run: the same call gives the
  * same bits.
  *
- *   - A logit of -inf is masked: probability 0, no gradient, never an alternative. The lowest
- *     finite value is an ordinary value.
+ *   - A logit of -inf is masked: probability 0, never an alternative, and no gradient but by its
+ *     own log probability, where it is the row's token (grad_logprob / T) or has a teacher's weight
+ *     q (-grad_loss q / T). The lowest finite value is an ordinary value.
  *   - A row whose every logit is -inf has log probabilities -inf, entropy 0, no alternatives
  *     and gradient 0.
  *   - A row with a NaN or +inf has NaN log probabilities, entropy and gradient and no
@@ -362,8 +363,12 @@ int argreduce_logprobs_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
 
 /*
  * Gradient of sum_r (grad_logprob[r] * ln p of the token + grad_entropy[r] * entropy) with
- * respect to the logits: grad is [rows, cols], contiguous, in the logits' format, every element
- * written; 0 in rows left out and in rows of -inf. x, tokens and temperature are those of the
+ * respect to the logits, with t the row's token and H its entropy
+ *
+ *     grad_j = (grad_logprob (delta_jt - p_j) - grad_entropy p_j (ln p_j + H)) / T:
+ *
+ * [rows, cols], contiguous, in the logits' format, every element written; 0 in rows left out and in
+ * rows of -inf. x, tokens and temperature are those of the
  * forward call, stats what it wrote (with entropy if grad_entropy is not NULL).
  */
 int argreduce_logprobs_grad(const void *x, argreduce_dtype_t dtype, int64_t rows, int64_t cols,

@@ -1007,3 +1007,23 @@ def test_special_rows_split_and_whole(capacity, dtype, cap, path, cols):
         ids[2, 0], v[2, 0] = 5, 1.0        # an empty row with a teacher
         ids[12] = ids[12, 0].clamp(min=0)  # one id, k times
         check_distill(x, ids, v, dtype, 1.3, rng)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("cols", [24, 700, 9000, 202048])
+def test_gradient_at_masked_logits(dtype, cols):
+    """A masked logit has the gradient of its own log probability and no other."""
+    announce(f"masked logits {dtype} cols={cols}")
+    x = torch.randn(2, cols, device="cuda").to(DT[dtype])
+    x[:, 3:9] = -INF
+    tokens = torch.tensor([5, 0], device="cuda")
+    w, half = torch.full((2,), 3.0, device="cuda"), torch.full((2,), 0.5, device="cuda")
+    r = ar.token_logprobs(x, tokens, temperature=2.0, entropy=True)
+    assert r.logprob[0] == -INF and r.logprob[1].isfinite()
+    g = ar.token_logprobs_grad(x, tokens, r.stats, w, half, temperature=2.0)
+    near = 8 * R.U + R.HALF_STEP[dtype]  # the scale, the weight and the product, and the type's rounding
+    assert abs(float(g[0, 5]) - 1.5) <= 1.5 * near and (g[0, 3:5] == 0).all() and (g[0, 6:9] == 0).all() and (g[1, 3:9] == 0).all()
+    ids = torch.tensor([[5, 0], [0, 1]], device="cuda")
+    loss, g = ar.distill_step(x, ids, torch.zeros(2, 2, device="cuda"), w, temperature=2.0)
+    assert loss[0] == INF and loss[1].isfinite()
+    assert abs(float(g[0, 5]) + 0.75) <= 0.75 * near and (g[0, 3:5] == 0).all() and (g[0, 6:9] == 0).all() and (g[1, 3:9] == 0).all()
