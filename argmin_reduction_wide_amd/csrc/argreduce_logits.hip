@@ -205,8 +205,7 @@ __device__ inline float team_reduce(float v, int lane, float (*sh)[kShared], Slo
 // it lies in a mapped page.
 
 // KEEP: ordinary loads, which leave the logits in the Infinity Cache for a gradient call to read;
-// else nontemporal ones, for logits too large for it. [257,32003] f32, forward and gradient: 7.2 +
-// 10.7 us kept, 7.2 + 14.1 not; [2048,128256] bf16: 136 + 178 kept, 97 + 193 not.
+// else nontemporal ones, for logits too large for it (kKeepBytes has the figures of both).
 template <typename Fmt, bool KEEP = false>
 struct Span {
     const uint8_t* base;
@@ -720,8 +719,9 @@ __device__ inline const uint8_t* row_ptr(const void* x, uint32_t r, uint32_t str
 
 // Rows of at most G vectors, G lanes each, the row held in registers: maximum first, then the
 // exponentials. Alternatives are taken one by one, as the largest key left. [65536,64] f16 with
-// entropy and 2 alternatives: 7.8 us (8 lanes; 11 MB, 1.4 TB/s), bound by the latency of one load and
-// the chain of reductions after it: a wavefront has eight rows and no work beside them.
+// entropy and 2 alternatives: 8.3 us (8 lanes; 12 MB, 1.4 TB/s), bound by the latency of one load and
+// the chain of reductions after it: a wavefront has eight rows and no work beside them. With 30
+// alternatives and no entropy 38 us, bound by their rounds.
 template <typename Fmt, bool KEEP, bool ENT, int G>
 __global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint32_t cols,
                                                             uint32_t stride, float scale,
@@ -795,11 +795,12 @@ __global__ __launch_bounds__(kBlockThreads) void k_lp_group(const void* x, uint3
 template <int T>
 constexpr int kSegs = T == kWave ? 256 : 1024;
 
-// A team of T lanes per row, in one pass. [4001,32001] f16: 38.0 us, 6.7 TB/s, bound by the read;
-// [2048,128256] bf16 with entropy 89 us, 5.9 TB/s, with 64 alternatives and no entropy 96 us, 5.4 TB/s:
-// the read, and the alternatives' selection (about 10 us a row) as far as the CU's other rows do not
-// hide it. [1,32000] f32 with entropy and 5 alternatives: 8.2 us, the latency of the read and of the
-// selection's barriers (split over 8 workgroups: 10, and a second launch).
+// A team of T lanes per row, in one pass. [4001,32001] f16 with a tenth of the rows left out: 37.6 us,
+// 6.1 TB/s, bound by the read; [2048,128256] bf16 with entropy 95 us, 5.5 TB/s, with 64 alternatives and
+// no entropy 96 us, 5.5 TB/s: the read, and the alternatives' selection (about 10 us a row) as far as
+// the CU's other rows do not hide it. [49539,2032] bf16 by wavefronts 36 us, 5.6 TB/s. [1,32000] f32
+// with entropy and 5 alternatives: 8.1 us, the latency of the read and of the selection's barriers
+// (split over 8 workgroups: 10, and a second launch).
 template <typename Fmt, bool KEEP, bool ENT, bool TOP, int T>
 __global__ __launch_bounds__(kTeamBlock<T>) void k_lp_team(const void* x, uint32_t cols,
                                                            uint32_t stride, float scale,
@@ -907,10 +908,10 @@ __device__ inline Stat merge_parts(const Part* p, uint32_t parts, float scale, i
     return a;
 }
 
-// One workgroup per split row; with 20 alternatives 6.6 us ([1,202048] f32), with 8 7.6 us
+// One workgroup per split row; with 20 alternatives 6.8 us ([1,202048] f32), with 8 7.5 us
 // ([32,202048] bf16): chained latencies, of the slices' statistics, the bisection, and the segments'
-// second read. A kernel of its own, since the last workgroup of k_part to arrive could do it only
-// with a counter that something has to clear for every call. Tags: columns in (x, tokens), slices,
+// second read, all of them after k_part has ended. (One launch for both, through words tagged with a
+// nonce as k_split joins its slices by, has not been built.) Tags: columns in (x, tokens), slices,
 // outputs, scale.
 template <typename Fmt, bool ENT, bool TOP, int T = TOP ? kMergeTopThreads : kMergeThreads>
 __global__ __launch_bounds__(T) void k_lp_merge(uint64_t x, uint64_t tokens,
@@ -1061,9 +1062,10 @@ struct GradSlice {
 
 // d logprob and d entropy: dx_j = [ g (delta_jt - p_j) - e p_j (ln p_j + H) ] / T.
 // One exponential per element: bound by the read and the store. [2048,128256] bf16 with the entropy's
-// gradient 194 us, 5.4 TB/s read and written; [257,32003] f32 10.6 us, 6.2 TB/s, the logits from the
-// Infinity Cache. Slices of 1024 vectors, so that few rows occupy every CU and a workgroup's loads
-// are all under way at once. Tags: columns in (x, tokens), scale in (stats, g_lp), slices in g_ent,
+// gradient 195 us, 5.4 TB/s read and written; [257,32003] f32 with a quarter of the rows left out 10.6
+// us, 5.4 TB/s, the logits from the Infinity Cache. Slices of 1024 vectors (make_grad_plan has other
+// lengths' figures), so that few rows occupy every CU and a workgroup's loads are all under way at
+// once. Tags: columns in (x, tokens), scale in (stats, g_lp), slices in g_ent,
 // log2 of the team's lanes in grad.
 template <typename Fmt, bool ENT, bool WIDE>
 __global__ __launch_bounds__(kBlockThreads) void k_lp_grad(uint64_t x, uint64_t tokens,
@@ -1156,10 +1158,9 @@ __device__ inline void own_student(Entry& mine, const uint8_t* row, uint32_t k, 
 }
 
 // Which ids of a row of more than kTeacherCompared entries occur more than once: an open hash table
-// in LDS of at least twice as many places. Comparing every entry with every other took most of the
-// time instead: [11266,617] f16 with 256 entries 229 us, with the table 36 (71 before the table's
-// places were 4 bytes and such rows held two vectors per lane). A place holds an id, its
-// top bit set once the id has come again. (No id has all 31 bits set: ids are below cols <=
+// in LDS of at least twice as many places. [21454,251] f16 with 251 different ids, loss and gradient:
+// 229 us with every entry compared with every other, 129 with the table instead. A place holds an id,
+// its top bit set once the id has come again. (No id has all 31 bits set: ids are below cols <=
 // INT32_MAX, and cols itself, for ids beyond the row, is not entered.)
 struct IdTable {
     uint32_t* place;
@@ -1195,10 +1196,12 @@ struct IdTable {
     }
 };
 
-// The totals of a row's entries in LDS, each the sum in the entries' order. Few ids are there twice:
-// a wavefront takes those of its entries one after the other and looks the row through for them,
-// 64 entries at a time. ([4096,32000] bf16 with 1024 random ids, about 16 of them there already, loss
-// and gradient: 1036 us with a lane per entry adding its row up, 301 so.)
+// The totals of a row's entries in LDS, each the sum in the entries' order. A top-k list has no id
+// twice: where one is, a wavefront takes such ids of its entries one after the other and looks the row
+// through for them, 64 entries at a time. ([4096,32000] bf16 with 1024 random ids, about 16 of them
+// there already, loss and gradient: 307 us so, 1036 with a lane per entry adding its row up; 164 with
+// different ids. Where most ids are there several times this bounds the kernel: [21454,251] f16 with
+// 251 random ids 397 us, 57 with different ones.)
 template <int T>
 __device__ inline void entry_totals(Entry* ent, const IdTable& table, uint32_t k, int lane) {
     const uint32_t l = lane % kWave;
@@ -1371,8 +1374,8 @@ __device__ inline float distill_loss(const Entry* ent, uint32_t k, float scale, 
     return loss_of(q, sum);
 }
 
-// The loss alone, a team of T lanes per row. [512,128256] f16 with 32 entries: 22.9-24.5 us, 5.4-5.7
-// TB/s, bound by the read of two rows per CU one after the other, with the tail of each exposed.
+// The loss alone, a team of T lanes per row. [512,128256] f16 with 32 entries: 23.7 us, 5.5 TB/s, bound
+// by the read of two rows per CU one after the other, with the tail of each exposed.
 template <typename Fmt, bool KEEP, int T>
 __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32_t cols,
                                                            uint32_t stride, float scale,
@@ -1406,8 +1409,9 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_ds_team(const void* x, uint32
 }
 
 // Rows of at most G vectors, G lanes each, the row held in registers; with GRAD the gradient too.
-// [52618,63] bf16 with 16 entries: 7.8 us for the loss, 13.2 for both (23 MB, 1.8 TB/s, bound by a
-// row's chain of loads and reductions); 29.8 and 95.8 with a wavefront per row. Tags as for k_ds_grad (none in grad).
+// [52618,63] bf16 with 16 entries: 8.0 us for the loss, 13.8 for both (24 MB, 1.8 TB/s, bound by a
+// row's chain of loads and reductions); 29.8 and 95.8 with a wavefront per row. Tags as for k_ds_grad
+// (none in grad).
 template <typename Fmt, bool GRAD, int G>
 __global__ __launch_bounds__(kBlockThreads) void k_ds_group(uint64_t x, uint64_t ids_, uint64_t values_,
                                                             uint64_t stats_, uint64_t w, uint64_t grad,
@@ -1517,7 +1521,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_group(uint64_t x, uint64_t
     }
 }
 
-// One workgroup per split row: 2.8 us for one row, 4.0 for 100, a launch and the latencies of the
+// One workgroup per split row: 2.5 us for one row, 3.9 for 100, a launch and the latencies of the
 // entries and the slices' statistics. Tags: teacher entries in ids, slices of the row in values.
 template <typename Fmt>
 __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint32_t cols,
@@ -1551,10 +1555,12 @@ __global__ __launch_bounds__(kMergeThreads) void k_ds_merge(const void* x, uint3
 // The gradient of a row: g (p_j - q_j) / T. The dense part g p_j / T is stored first; after it each
 // teacher entry's element is stored again with its weight taken off: the sum of the weights of equal
 // ids, which every one of them stores. A team of T lanes (32: of 2^lg, up to 32) for a slice of a
-// row has the slice's entries in LDS. [4096,128256] bf16 with 64 entries: 421 us, 5.0 TB/s read and
-// written, bound by that; [4096,32000] with 1024 268 us, bound by the entries (553 and 7958 us with
-// each entry compared with all others from global memory). Tags: columns in (x, ids), teacher entries
-// in values, scale in (stats, g), lg and the slices (12 bits above 4) in grad.
+// row has the slice's entries in LDS. [4096,128256] bf16 with 64 entries: 416 us, 5.1 TB/s read and
+// written, bound by that; [4096,32000] with 1024 random ones 265 us, bound by the entries (553 and 7958
+// us with each entry compared with all others from global memory). A row by a wavefront: [21454,251]
+// f16 with 251 different ids 42 us; by a group of lanes: [52618,63] bf16 with 16 12.2 us. Tags: columns
+// in (x, ids), teacher entries in values, scale in (stats, g), lg and the slices (12 bits above 4) in
+// grad.
 template <typename Fmt, int T>
 __global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t ids_, uint64_t values_,
                                                            uint64_t stats_, uint64_t g, uint64_t grad,
@@ -1631,11 +1637,12 @@ __global__ __launch_bounds__(kBlockThreads) void k_ds_grad(uint64_t x, uint64_t 
 // The registers of a CU hold few rows, so a team goes through several, and as soon as a vector's
 // gradient is stored, the vector of the team's next row is loaded in its place: the loads run
 // beside the second pass's arithmetic and stores. [4096,128256] bf16 with 64 entries: 439 us, 4.8 TB/s
-// read and written, the rate of a device copy (535 when all vectors were read again, 597 held without
-// that overlap); [1003,50001] f16 43 us, 4.6 TB/s; [16,32000] f32 8.7 us, a row's latency from end to
-// end. Rows of up to 128 vectors hold two per lane, in half the registers, so that twice the wavefronts
-// hide their latency: [21454,251] f16 with 251 entries 57 us, 100 with eight. Tags as for k_ds_grad,
-// but the workgroups of the grid in grad.
+// read and written (535 with all vectors read again, 597 held without that overlap); [1003,50001] f16
+// 43 us, 4.6 TB/s; [16,32000] f32 8.5 us, a row's latency from end to end. Rows of up to 128 vectors
+// hold two per lane, in half the registers, so that twice the wavefronts hide their latency:
+// [21454,251] f16 with 251 different entries 57 us, 100 with eight. A row without a teacher is read
+// like any other, since its loads are under way before its entries are known: with three rows in four
+// of [4096,128256] so, 430 us. Tags as for k_ds_grad, but the workgroups of the grid in grad.
 template <int T>
 constexpr int kStepRows = step_rows(T);
 template <typename Fmt, int T, int NV>

@@ -16,8 +16,11 @@ namespace {
 constexpr int64_t kBlock = 256;
 constexpr int64_t kThreadsPerCu = 2048;
 constexpr int64_t kLdsPerCu = 160 * 1024;
-// Logits of up to this size are left in the 256 MiB Infinity Cache (struct Span; at 125 MiB,
-// [512,128256] f16, the forward pass takes 25.7 us with them left there, 23.0 without).
+// Logits of up to this size are left in the 256 MiB Infinity Cache (struct Span). Log probabilities
+// and their gradient of f32 rows of 32003, in us, logits left there and not: 4 MiB 9.5 and 11.6, 16
+// MiB 15.0 and 17.7, 48 MiB 30.9 and 34.9, 64 MiB 46.4 and 46.0, 96 MiB 63.4 and 63.2, 128 MiB 85.6
+// and 80.8, 256 MiB 164 and 151; the forward pass alone 4.6 and 5.5, 6.1 and 6.3, 11.9 and 11.7, 16.9
+// and 15.9, 21.9 and 20.8, 27.7 and 26.2, 50.5 and 47.1. (bf16 within 3 us of these.)
 constexpr int64_t kKeepBytes = int64_t{64} << 20;
 constexpr int64_t kMaxGridThreads = int64_t{1} << 32;  // a launch's grid holds fewer threads
 constexpr int64_t kMaxBytes = int64_t{1} << 48;        // a device address is below it
@@ -132,7 +135,9 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
         return grid_too_large(p->grid_blocks, kBlock) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
     }
     // a wavefront per row: up to four vectors per lane; in a distillation step up to the eight that
-    // it holds ([19940,2312] f16, 291 vectors: 256 lanes 152 us, see the step's figures below)
+    // it holds ([19940,2312] f16, 291 vectors: 256 lanes 152 us, see the step's figures below).
+    // Log probabilities of [49539,2032] bf16, 254 vectors: 37 us, 256 lanes 60; with 16 alternatives
+    // 70 and 157. (Longer rows would gain too: of [31457,3200] 35 and 49, of [15728,6400] 35 and 39.)
     if (vecs <= (use == kDistillStep ? 512 : 256) && k <= kWaveEntries) {
         p->path = ARGREDUCE_PATH_SUBWAVE;
         p->team = 64;
@@ -168,9 +173,16 @@ int make_logits_plan(int dtype, int64_t rows, int64_t cols, Use use, int k, bool
                   : vecs <= 8 * 256                             ? 256
                   : vecs <= 16 * 512                            ? 512
                                                                 : 1024;
+    // The figures below: bf16 rows, us by 256, 512 and 1024 lanes; after the semicolon with 16
+    // alternatives.
     else if (vecs > 2048 && rows1 * 1024 <= cap)
-        p->team = 1024;  // the whole device in one wave of workgroups
+        // The whole device in one wave of workgroups. [256,16320], 2040 vectors: 4.7, 4.9, 4.8; 9.2,
+        // 8.2, 8.5. [256,32720]: 7.2, 6.6, 7.0; 14.1, 10.9, 10.2. [64,72000]: 9.0, 7.0, 6.8; 17.7, 11.9,
+        // 11.1.
+        p->team = 1024;
     else
+        // [6168,16320], 2040 vectors: 33.9, 35.1, 42.2; 45.4, 55.7, 88.3. [3700,27200], 3400: 34.7, 32.5,
+        // 39.5; 44.0, 47.0, 65.9. [2097,48000], 6000: 36.8, 34.2, 34.5; 48.2, 44.6, 50.0.
         p->team = vecs > (use == kLogprobsTop ? 4096 : 3000) ? 512 : 256;
     p->grid_blocks = rows1;
     if (use == kDistillStep) {
@@ -195,7 +207,11 @@ int make_grad_plan(int dtype, int64_t rows, int64_t cols, int k, GradPlan* p) {
     p->team = static_cast<int>(team < kBlock ? team : kBlock);
     p->slices = 1;
     if (p->team == kBlock) {
-        // four vectors to a thread, with many teacher entries more: every slice goes through them
+        // Four vectors to a thread, with many teacher entries more: every slice goes through them.
+        // us by 2, 4, 8 and 16 vectors to a thread: [4096,32000] bf16 with 1024 random entries 323, 258,
+        // 239, 265, with 64 of them 106, 114, 127, 130; [16,202048] f32 without any 7.2, 8.6, 12.6, 18.7.
+        // (Two or three would gain where the entries are few: [4096,128256] bf16 with 64 371 and 366 us,
+        // 421 with four.)
         const int64_t each = std::max(4, k / 64);
         p->slices = static_cast<int>(std::min<int64_t>(ceil_div(vecs, kBlock * each), 4095));
     }
