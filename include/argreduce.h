@@ -386,7 +386,8 @@ int argreduce_logprobs_grad(const void *x, argreduce_dtype_t dtype, int64_t rows
  *   teacher_tokens  [rows, k]: ids. A negative one marks an absent entry (its value does not
  *                   matter). The same id twice: both entries count. An id >= cols with weight
  *                   makes the row's loss and gradient NaN, whatever its logits are.
- *   teacher_logits  [rows, k] f32: logits or log probabilities; -inf has no weight. The outputs
+ *   teacher_logits  [rows, k] f32: logits or log probabilities; -inf has no weight, and neither has
+ *                   an entry whose q_i underflows in binary32 (below 2^-126). The outputs
  *                   of argreduce_logprobs (top_tokens, top_logprobs) can be passed as they are.
  *                   A NaN (or +inf) of a present entry makes loss and gradient NaN.
  *   k               1 .. ARGREDUCE_TEACHER_MAX.
