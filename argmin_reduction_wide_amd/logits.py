@@ -98,6 +98,7 @@ def _temperature(t) -> float:
     return t
 
 
+_tuple = tuple.__new__
 # The current device and its current stream's handle, as cheaply as torch gives them
 # (torch.cuda.current_stream(...).cuda_stream takes 2 us, a tenth of a small call).
 _device = torch._C._cuda_getDevice
@@ -147,9 +148,10 @@ def _refuse_captured_autograd(logits) -> None:
                            "token_logprobs_grad, distill_loss_grad or distill_step in the capture")
 
 
-def _refuse_forward_mode(logits) -> None:
-    """A dual tensor need not require a gradient: its tangent would be lost without a word."""
-    if _forward_ad._current_level >= 0 and _forward_ad.unpack_dual(logits).tangent is not None:
+def _refuse_tangent(logits) -> None:
+    """In forward mode: a dual tensor need not require a gradient, and its tangent would be lost
+    without a word."""
+    if _forward_ad.unpack_dual(logits).tangent is not None:
         raise NotImplementedError("the logits operators have no forward-mode derivative")
 
 
@@ -185,7 +187,7 @@ def _logprobs(logits, tokens, temperature, entropy, top, scratch, apart=False):
     if need or scratch is not None:
         sptr, sbytes, scratch = _scratch(need, "argreduce_logprobs", scratch, device)
     rc = _call.logprobs(logits.data_ptr(), code, rows, cols, stride, tokens.data_ptr(), temperature,
-                        int(entropy), top, stats.data_ptr(), lp_ptr, tok_ptr, sptr, sbytes,
+                        entropy, top, stats.data_ptr(), lp_ptr, tok_ptr, sptr, sbytes,
                         _stream(device.index))
     if rc:
         raise _failed(rc, "logprobs", rows, cols, stride)
@@ -232,14 +234,15 @@ def token_logprobs(logits, tokens, *, temperature: float = 1.0, entropy: bool = 
     likely first, ties to the lower token; rows with fewer unmasked logits end in token -1.
 
     Differentiable in logprob and entropy (float32) when the logits require a gradient."""
-    _refuse_forward_mode(logits)
+    if _forward_ad._current_level >= 0:
+        _refuse_tangent(logits)
     if logits.requires_grad and torch.is_grad_enabled():
         _refuse_captured_autograd(logits)
         return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, bool(entropy), top,
                                                    scratch))
     stats, lp, tok, ent = _logprobs(logits, tokens, temperature, bool(entropy), top, scratch, True)
-    if logits.dim() == 2:
-        return TokenLogprobs(stats[0], ent, lp, tok, stats)
+    if logits.dim() == 2:  # (a named tuple's own constructor takes twice the time)
+        return _tuple(TokenLogprobs, (stats[0], ent, lp, tok, stats))
     lead = logits.shape[:-1]
     return TokenLogprobs(stats[0].view(lead), None if ent is None else ent.view(lead), lp, tok, stats)
 
@@ -361,7 +364,8 @@ def distill_loss(logits, teacher_tokens, teacher_logits, *, temperature: float =
     without an entry of weight has loss 0. The loss is not multiplied by temperature ** 2.
 
     Differentiable in the loss when the logits require a gradient; the teacher is a constant."""
-    _refuse_forward_mode(logits)
+    if _forward_ad._current_level >= 0:
+        _refuse_tangent(logits)
     if logits.requires_grad and torch.is_grad_enabled():
         _refuse_captured_autograd(logits)
         return DistillLoss(*_DistillLoss.apply(logits, teacher_tokens, teacher_logits, temperature,
