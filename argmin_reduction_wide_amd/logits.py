@@ -23,7 +23,7 @@ from . import binding as B
 
 TOP_MAX = 64         # alternatives per row (ARGREDUCE_TOP_MAX)
 TEACHER_MAX = 1024   # teacher entries per row (ARGREDUCE_TEACHER_MAX)
-_ENTROPY_APART = -2  # ARGREDUCE_ENTROPY_APART
+_ENTROPY_APART = 0x61706172  # ARGREDUCE_ENTROPY_APART
 
 _F32, _I64 = torch.float32, torch.int64
 _CODES = {torch.float32: B.F32, torch.float16: B.F16, torch.bfloat16: B.BF16}

@@ -329,7 +329,8 @@ int argreduce_scan_plan(int64_t rows, int64_t cols, argreduce_dtype_t dtype,
  */
 #define ARGREDUCE_TOP_MAX 64        /* alternatives per row */
 #define ARGREDUCE_TEACHER_MAX 1024  /* teacher entries per row */
-#define ARGREDUCE_ENTROPY_APART (-2) /* argreduce_logprobs: the entropy in a row of its own too */
+/* argreduce_logprobs: the entropy in a row of its own too (a value that no caller's "true" has) */
+#define ARGREDUCE_ENTROPY_APART 0x61706172
 
 /*
  * Log probabilities of given tokens, with entropy and the top alternatives.

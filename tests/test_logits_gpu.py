@@ -924,7 +924,10 @@ def test_outputs_may_be_written_over(dtype, rows, cols):
     assert torch.equal(got.nan_to_num(9.0), want.nan_to_num(9.0))
 
 
-@pytest.mark.parametrize("entropy", [0, 1, 2, -1, -2])
+ENTROPY_APART = 0x61706172  # as the header has it
+
+
+@pytest.mark.parametrize("entropy", [0, 1, 2, -1, -2, 2 ** 31 - 1, ENTROPY_APART])
 @pytest.mark.parametrize("rows,cols", [(3, 50), (3, 700), (3, 9000), (3, 202048)])
 def test_rows_of_the_statistics(rows, cols, entropy):
     """[4, rows], and the entropy again in a fifth row for ARGREDUCE_ENTROPY_APART alone."""
@@ -942,7 +945,7 @@ def test_rows_of_the_statistics(rows, cols, entropy):
         torch.cuda.synchronize()
         assert torch.equal(stats[0], want[0]) and torch.equal(stats[2:4], want[2:4])
         assert torch.equal(stats[1], want[1]) if entropy else stats[1].isnan().all()
-        assert torch.equal(stats[4], want[1]) if entropy == -2 else (stats[4] == 5).all()
+        assert torch.equal(stats[4], want[1]) if entropy == ENTROPY_APART else (stats[4] == 5).all()
         assert (stats[5] == 5).all()
 
 
