@@ -50,7 +50,11 @@ EXPORTS = ("argreduce_scratch_bytes", "argreduce_lastaxis", "argreduce_plan",
            "argreduce_wait_timeouts", "argreduce_lastaxis_noalloc",
            "argreduce_logprobs_scratch_bytes", "argreduce_logprobs", "argreduce_logprobs_plan",
            "argreduce_logprobs_grad", "argreduce_distill_scratch_bytes", "argreduce_distill",
-           "argreduce_distill_plan", "argreduce_distill_grad", "argreduce_distill_step")
+           "argreduce_distill_plan", "argreduce_distill_grad", "argreduce_distill_step",
+           "argreduce_beam_scratch_bytes", "argreduce_beam_out_bytes", "argreduce_beam_step",
+           "argreduce_beam_plan", "argreduce_reorder_plan", "argreduce_reorder",
+           "argreduce_route_scratch_bytes", "argreduce_route_totals_bytes", "argreduce_route",
+           "argreduce_route_plan", "argreduce_route_grad")
 
 
 class ArgreduceError(RuntimeError):
@@ -70,6 +74,18 @@ class argreduce_plan_t(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class argreduce_state_t(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("group_stride", ctypes.c_int64),
+                ("beam_stride", ctypes.c_int64), ("outer", ctypes.c_int64),
+                ("outer_stride", ctypes.c_int64), ("positions", ctypes.c_int64),
+                ("position_stride", ctypes.c_int64), ("inner", ctypes.c_int64)]
+
+
+class argreduce_reorder_t(ctypes.Structure):
+    _fields_ = [("tensors", ctypes.c_int32), ("beams", ctypes.c_int32), ("groups", ctypes.c_int64),
+                ("positions", ctypes.c_int64), ("position_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -154,6 +170,34 @@ def lib() -> ctypes.CDLL:
                 h.argreduce_distill_grad.restype = c_int
                 h.argreduce_distill_step.argtypes = logits + teacher + [vp, vp, vp, vp, sz, vp]
                 h.argreduce_distill_step.restype = c_int
+                f64 = ctypes.c_double
+                h.argreduce_beam_scratch_bytes.argtypes = [i64, i64, i64, c_int, i32]
+                h.argreduce_beam_scratch_bytes.restype = sz
+                h.argreduce_beam_out_bytes.argtypes = [i64, i32]
+                h.argreduce_beam_out_bytes.restype = sz
+                h.argreduce_beam_step.argtypes = [vp, c_int, i64, i64, i64, i64, vp, vp, i64, f64, i32, vp,
+                                                  vp, sz, vp]
+                h.argreduce_beam_step.restype = c_int
+                h.argreduce_beam_plan.argtypes = [i64, i64, i64, c_int, i32,
+                                                  ctypes.POINTER(argreduce_plan_t)]
+                h.argreduce_beam_plan.restype = c_int
+                h.argreduce_reorder_plan.argtypes = [ctypes.POINTER(argreduce_state_t), i32, i64, i64,
+                                                     ctypes.POINTER(argreduce_reorder_t)]
+                h.argreduce_reorder_plan.restype = c_int
+                h.argreduce_reorder.argtypes = [vp, vp, vp, vp, vp, i64, i64, vp]
+                h.argreduce_reorder.restype = c_int
+                h.argreduce_route_scratch_bytes.argtypes = [i64, i64, i64, c_int]
+                h.argreduce_route_scratch_bytes.restype = sz
+                h.argreduce_route_totals_bytes.argtypes = [i64, i64]
+                h.argreduce_route_totals_bytes.restype = sz
+                h.argreduce_route.argtypes = [vp, c_int, i64, i64, i64, i64, vp, i32, i32, vp, vp, vp, vp, sz,
+                                              vp]
+                h.argreduce_route.restype = c_int
+                h.argreduce_route_plan.argtypes = [i64, i64, i64, c_int, ctypes.POINTER(argreduce_plan_t)]
+                h.argreduce_route_plan.restype = c_int
+                h.argreduce_route_grad.argtypes = [vp, c_int, i64, i64, i64, i64, i32, i32, vp, vp, vp, vp,
+                                                   vp, vp, vp]
+                h.argreduce_route_grad.restype = c_int
                 _bind_fast(h)
                 _lib = h
     return _lib
@@ -179,6 +223,9 @@ def _bind_fast(h: ctypes.CDLL) -> None:
                   addr(h.argreduce_logprobs), addr(h.argreduce_logprobs_grad),
                   addr(h.argreduce_distill), addr(h.argreduce_distill_grad),
                   addr(h.argreduce_distill_step))
+    m.bind_choices(addr(h.argreduce_beam_scratch_bytes), addr(h.argreduce_beam_step),
+                   addr(h.argreduce_reorder), addr(h.argreduce_route_scratch_bytes),
+                   addr(h.argreduce_route), addr(h.argreduce_route_grad))
     _fast = m
 
 
@@ -342,6 +389,77 @@ def argreduce_distill_step(x_ptr: int, dtype, rows: int, cols: int, row_stride: 
         x_ptr, _dtype_code(dtype), rows, cols, row_stride, k, teacher_tokens_ptr,
         teacher_logits_ptr, temperature, weights_ptr, stats_ptr, grad_ptr, scratch_ptr,
         scratch_bytes, stream)
+
+
+def argreduce_beam_scratch_bytes(groups: int, beams: int, cols: int, dtype, width: int) -> int:
+    return entry_point("argreduce_beam_scratch_bytes")(groups, beams, cols, _dtype_code(dtype), width)
+
+
+def argreduce_beam_out_bytes(groups: int, width: int) -> int:
+    return lib().argreduce_beam_out_bytes(groups, width)
+
+
+def argreduce_beam_step(x_ptr: int, dtype, groups: int, beams: int, cols: int, row_stride: int,
+                        scores_ptr: int, ended_ptr: int, end_token: int, temperature: float, width: int,
+                        out_ptr: int, scratch_ptr: int, scratch_bytes: int, stream: int) -> int:
+    return entry_point("argreduce_beam_step")(
+        x_ptr, _dtype_code(dtype), groups, beams, cols, row_stride, scores_ptr, ended_ptr, end_token,
+        temperature, width, out_ptr, scratch_ptr, scratch_bytes, stream)
+
+
+def argreduce_beam_plan(groups: int, beams: int, cols: int, dtype, width: int) -> dict:
+    p = argreduce_plan_t()
+    rc = lib().argreduce_beam_plan(groups, beams, cols, _dtype_code(dtype), width, ctypes.byref(p))
+    if rc != OK:
+        raise ArgreduceError(rc, "argreduce_beam_plan")
+    return p.as_dict()
+
+
+def argreduce_reorder_plan(states, groups: int, beams: int) -> argreduce_reorder_t:
+    """The plan of a ctypes array of argreduce_state_t."""
+    plan = argreduce_reorder_t()
+    rc = lib().argreduce_reorder_plan(states, len(states), groups, beams, ctypes.byref(plan))
+    if rc != OK:
+        raise ArgreduceError(rc, "argreduce_reorder_plan")
+    return plan
+
+
+def argreduce_reorder(plan: argreduce_reorder_t, table_ptr: int, parents_ptr: int, first_ptr: int,
+                      last_ptr: int, first_value: int, last_value: int, stream: int) -> int:
+    return entry_point("argreduce_reorder")(ctypes.addressof(plan), table_ptr, parents_ptr, first_ptr,
+                                            last_ptr, first_value, last_value, stream)
+
+
+def argreduce_route_scratch_bytes(groups: int, tokens: int, experts: int, dtype) -> int:
+    return entry_point("argreduce_route_scratch_bytes")(groups, tokens, experts, _dtype_code(dtype))
+
+
+def argreduce_route_totals_bytes(groups: int, experts: int) -> int:
+    return lib().argreduce_route_totals_bytes(groups, experts)
+
+
+def argreduce_route(x_ptr: int, dtype, groups: int, tokens: int, experts: int, row_stride: int,
+                    live_ptr: int, top: int, renormalize: int, weights_ptr: int, chosen_ptr: int,
+                    totals_ptr: int, scratch_ptr: int, scratch_bytes: int, stream: int) -> int:
+    return entry_point("argreduce_route")(
+        x_ptr, _dtype_code(dtype), groups, tokens, experts, row_stride, live_ptr, top, renormalize,
+        weights_ptr, chosen_ptr, totals_ptr, scratch_ptr, scratch_bytes, stream)
+
+
+def argreduce_route_plan(groups: int, tokens: int, experts: int, dtype) -> dict:
+    p = argreduce_plan_t()
+    rc = lib().argreduce_route_plan(groups, tokens, experts, _dtype_code(dtype), ctypes.byref(p))
+    if rc != OK:
+        raise ArgreduceError(rc, "argreduce_route_plan")
+    return p.as_dict()
+
+
+def argreduce_route_grad(x_ptr: int, dtype, groups: int, tokens: int, experts: int, row_stride: int,
+                         top: int, renormalize: int, chosen_ptr: int, totals_ptr: int, g_weights_ptr: int,
+                         g_balance_ptr: int, g_z_ptr: int, grad_ptr: int, stream: int) -> int:
+    return entry_point("argreduce_route_grad")(
+        x_ptr, _dtype_code(dtype), groups, tokens, experts, row_stride, top, renormalize, chosen_ptr,
+        totals_ptr, g_weights_ptr, g_balance_ptr, g_z_ptr, grad_ptr, stream)
 
 
 def argreduce_debug_set_capacity(threads: int) -> int:

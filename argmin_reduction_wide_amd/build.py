@@ -18,7 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libargreduce.so")
 SOURCES = [os.path.join(CSRC, "argreduce_kernels.hip"), os.path.join(CSRC, "argreduce_scan.hip"),
            os.path.join(CSRC, "argreduce_logits.hip"), os.path.join(CSRC, "argreduce_api.cpp"),
-           os.path.join(CSRC, "argreduce_logits_api.cpp")]
+           os.path.join(CSRC, "argreduce_logits_api.cpp"), os.path.join(CSRC, "argreduce_beam.hip"),
+           os.path.join(CSRC, "argreduce_beam_api.cpp"), os.path.join(CSRC, "argreduce_route.hip"),
+           os.path.join(CSRC, "argreduce_route_api.cpp")]
 ARCH = "gfx950"
 
 

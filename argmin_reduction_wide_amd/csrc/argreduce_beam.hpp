@@ -1,0 +1,58 @@
+// Plans and launchers of beam search's step and reordering (argreduce_beam.hip), shared with their
+// C ABI (argreduce_beam_api.cpp).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "argreduce.h"
+
+namespace argreduce {
+
+constexpr int kBeamMax = 64;     // beams of a group, and candidates kept (ARGREDUCE_BEAM_MAX)
+constexpr int kBeamLists = 256;  // lists of candidates that one group's join takes
+
+// How the rows (one per beam) of one step are scanned.
+struct BeamPlan {
+    int path;             // argreduce_path_t: SUBWAVE (a wavefront per row), BLOCK or SPLIT
+    int team;             // lanes that scan one slice: 64, 256, 512 or 1024
+    int parts;            // slices per row, each with a list of candidates of its own
+    int64_t grid_blocks;  // workgroups of the scanning kernel
+    int64_t device_threads;
+    size_t scratch_bytes; // including 15 bytes of alignment slack
+};
+
+struct BeamArgs {
+    const void* x;
+    int dtype;
+    int64_t groups, cols, row_stride;
+    int beams, width;
+    const float* scores;
+    const uint8_t* ended;  // or null
+    int64_t end_token;
+    double temperature;
+    uint8_t* out;          // parents, tokens, scores, ended
+};
+
+size_t beam_list_bytes(int width);  // scratch of one list and its slice's statistics
+hipError_t launch_beam_step(const BeamPlan& plan, const BeamArgs& a, uint8_t* scratch16, hipStream_t stream);
+
+// Positions [first, last) of every group's beams: values, or arrays of one per group.
+struct ReorderArgs {
+    const argreduce_state_t* table;  // on the device
+    int tensors;
+    int64_t groups;
+    int beams;
+    const int64_t* parents;
+    const int64_t* first;  // or null: first_value
+    const int64_t* last;
+    int64_t first_value, last_value;
+    int blocks;            // workgroups per tensor and group
+};
+hipError_t launch_reorder(const ReorderArgs& a, hipStream_t stream);
+
+// Thread capacity plans are made for (the simulated one if set); an ARGREDUCE_* status.
+int plan_device_threads(int64_t* threads);
+
+}  // namespace argreduce

@@ -1109,18 +1109,6 @@ __global__ __launch_bounds__(kTeamBlock<T>, NV > 2 ? 4 : 8) void k_ds_step(uint6
 // Launch
 
 template <typename F>
-void with_format(int dtype, F f) {
-    switch (dtype) {
-        case ARGREDUCE_F32: f(F32{}); break;
-        case ARGREDUCE_F16: f(F16{}); break;
-        default: f(BF16{}); break;
-    }
-}
-template <int N>
-struct Int {
-    static constexpr int value = N;
-};
-template <typename F>
 void with_team(int team, F f) {
     switch (team) {
         case 64: f(Int<64>{}); break;
@@ -1139,24 +1127,10 @@ void with_group(int lanes, F f) {
     }
 }
 template <typename F>
-void with_bool(bool b, F f) {
-    if (b)
-        f(Int<1>{});
-    else
-        f(Int<0>{});
-}
-
-template <typename F>
 void with_format_and_keep(const LogitsArgs& a, F f) {
     with_format(a.dtype, [&](auto fmt) { with_bool(a.keep, [&](auto keep) { f(fmt, keep); }); });
 }
 
-uint32_t log2_of(int v) { return static_cast<uint32_t>(__builtin_ctz(static_cast<unsigned>(v))); }
-
-template <typename... KArgs, typename... Args>
-void launch(void (*kernel)(KArgs...), uint32_t grid, int block, hipStream_t s, Args... args) {
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, s, args...);
-}
 // With LDS for the teacher's entries of the workgroup's rows, and a hash table for each.
 static_assert(sizeof(Entry) == kEntryBytes, "the plans count with it");
 template <typename... KArgs, typename... Args>

@@ -2,79 +2,30 @@
 // and the contract are in include/argreduce.h, the kernels in argreduce_logits.hip.
 #include <hip/hip_runtime_api.h>
 
-#include <algorithm>
-#include <limits>
-
-#include "argreduce.h"
-#include "argreduce_logits.hpp"
-
-#define ARGREDUCE_EXPORT extern "C" __attribute__((visibility("default")))
+#include "argreduce_checks.hpp"
 
 namespace argreduce {
 namespace {
 
-constexpr int64_t kBlock = 256;
-constexpr int64_t kThreadsPerCu = 2048;
-constexpr int64_t kLdsPerCu = 160 * 1024;
 // Logits of up to this size are left in the 256 MiB Infinity Cache (struct Span). Log probabilities
 // and their gradient of f32 rows of 32003, in us, logits left there and not: 4 MiB 9.5 and 11.6, 16
 // MiB 15.0 and 17.7, 48 MiB 30.9 and 34.9, 64 MiB 46.4 and 46.0, 96 MiB 63.4 and 63.2, 128 MiB 85.6
 // and 80.8, 256 MiB 164 and 151; the forward pass alone 4.6 and 5.5, 6.1 and 6.3, 11.9 and 11.7, 16.9
 // and 15.9, 21.9 and 20.8, 27.7 and 26.2, 50.5 and 47.1. (bf16 within 3 us of these.)
 constexpr int64_t kKeepBytes = int64_t{64} << 20;
-constexpr int64_t kMaxGridThreads = int64_t{1} << 32;  // a launch's grid holds fewer threads
-constexpr int64_t kMaxBytes = int64_t{1} << 48;        // a device address is below it
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t next_pow2(int64_t v) {
-    int64_t p = 1;
-    while (p < v) p <<= 1;
-    return p;
-}
-
-int64_t logits_elem_size(int dtype) {
-    switch (dtype) {
-        case ARGREDUCE_F32: return 4;
-        case ARGREDUCE_F16: return 2;
-        case ARGREDUCE_BF16: return 2;
-        default: return 0;
-    }
-}
-
-// 16-byte vectors that a row's bytes lie in, for the worst aligned row.
-int64_t span_vecs(int64_t cols, int64_t es) { return cols * es / 16 + 2; }
-
-int check_logits_shape(int dtype, int64_t rows, int64_t cols) {
-    if (logits_elem_size(dtype) == 0) return ARGREDUCE_ERR_UNSUPPORTED_DTYPE;
-    if (rows < 0 || cols < 1) return ARGREDUCE_ERR_INVALID_ARG;
-    if (cols > std::numeric_limits<int32_t>::max() || rows > std::numeric_limits<int32_t>::max())
-        return ARGREDUCE_ERR_TOO_WIDE;
-    return ARGREDUCE_OK;
-}
 
 // Checks of the arguments that every call takes; fills *a. Row stride: see the header.
 int check_logits(const void* x, int dtype, int64_t rows, int64_t cols, int64_t stride,
                  float temperature, LogitsArgs* a) {
-    const int rc = check_logits_shape(dtype, rows, cols);
+    const int rc = check_rows(x, dtype, rows, cols, stride);
     if (rc != ARGREDUCE_OK) return rc;
-    if (rows > 1 && stride > std::numeric_limits<uint32_t>::max()) return ARGREDUCE_ERR_TOO_WIDE;
-    if (rows > 1 && stride < cols) return ARGREDUCE_ERR_INVALID_ARG;
     // powers of two far inside the range of a float: log2(e) / T and its products stay normal
     if (!(temperature >= 0x1p-60f && temperature <= 0x1p60f)) return ARGREDUCE_ERR_INVALID_ARG;
-    if (rows > 0 && (x == nullptr || reinterpret_cast<uintptr_t>(x) % logits_elem_size(dtype) != 0))
-        return ARGREDUCE_ERR_INVALID_ARG;
-    if (rows > 1 && stride >= kMaxBytes / logits_elem_size(dtype) / rows) return ARGREDUCE_ERR_TOO_WIDE;
     *a = LogitsArgs{x, dtype, rows, cols, rows > 1 ? stride : cols,
                     static_cast<float>(1.4426950408889634 / static_cast<double>(temperature)),
                     rows <= kKeepBytes / logits_elem_size(dtype) / cols};
     return ARGREDUCE_OK;
 }
-
-// Device addresses carry 16 bits of other arguments in their upper bits (argreduce_logits.hip).
-bool fits48(const void* p) { return (reinterpret_cast<uintptr_t>(p) >> 48) == 0; }
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-// A device array of `n`-byte elements that a call with rows > 0 needs.
-bool usable(const void* p, uintptr_t n) { return p != nullptr && aligned(p, n) && fits48(p); }
 
 // Workgroups of the distillation step: as many as its registers (at most 128 per lane, 64 if it
 // holds two vectors) and LDS let the CUs hold at once; each goes through several rows. The kernel
@@ -87,8 +38,6 @@ int64_t step_blocks(int64_t cap, int team, int held, int k) {
     const int64_t cus = cap / kThreadsPerCu > 0 ? cap / kThreadsPerCu : 1;
     return per_cu * cus < 65535 ? per_cu * cus : 65535;
 }
-
-bool grid_too_large(int64_t blocks, int64_t threads) { return blocks >= kMaxGridThreads / threads; }
 
 // Teacher entries, at most, of a row left to one wavefront: four rows' entries and tables then take
 // 24 KiB of LDS. (A workgroup per row has a lane for each entry, and is slower: [21454,251] f16 with
@@ -219,24 +168,11 @@ int make_grad_plan(int dtype, int64_t rows, int64_t cols, int k, GradPlan* p) {
     return grid_too_large(p->grid_blocks, kBlock) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
 }
 
-// The caller's scratch aligned up to 16 bytes in *out; an ARGREDUCE_* status.
-int scratch_of(const LogitsPlan& p, void* scratch, size_t bytes, uint8_t** out) {
-    *out = nullptr;
-    if (p.scratch_bytes == 0) return ARGREDUCE_OK;
-    if (scratch == nullptr || bytes < p.scratch_bytes) return ARGREDUCE_ERR_SCRATCH_TOO_SMALL;
-    if (!fits48(scratch)) return ARGREDUCE_ERR_INVALID_ARG;
-    *out = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(scratch) + 15u) &
-                                      ~static_cast<uintptr_t>(15u));
-    return ARGREDUCE_OK;
-}
-
 // Whether every row starts on a 16-byte boundary; of contiguous rows in an aligned tensor.
 bool vec_rows(const LogitsArgs& a) {
     return aligned(a.x, 16) && a.row_stride * logits_elem_size(a.dtype) % 16 == 0;
 }
 bool vec_rows(int dtype, int64_t cols) { return cols * logits_elem_size(dtype) % 16 == 0; }
-
-int status_of(hipError_t e) { return e == hipSuccess ? ARGREDUCE_OK : ARGREDUCE_ERR_HIP; }
 
 void fill_logits_plan(const LogitsPlan& p, int dispatches, argreduce_plan_t* out) {
     *out = argreduce_plan_t{};
@@ -277,7 +213,7 @@ int distill(const LogitsArgs& a, int32_t k, const int64_t* ids, const float* val
         if (rc != ARGREDUCE_OK) return rc;
     }
     uint8_t* scratch16 = nullptr;
-    rc = scratch_of(p, scratch, scratch_bytes, &scratch16);
+    rc = scratch_of(p.scratch_bytes, scratch, scratch_bytes, &scratch16);
     if (rc != ARGREDUCE_OK) return rc;
     return status_of(launch_distill(p, g, a, k, ids, values, stats, weights, grad, scratch16,
                                     static_cast<hipStream_t>(stream)));
@@ -327,7 +263,7 @@ ARGREDUCE_EXPORT int argreduce_logprobs(const void* x, argreduce_dtype_t dtype, 
     rc = make_logits_plan(dtype, rows, cols, top > 0 ? kLogprobsTop : kLogprobs, 0, vec_rows(a), &p);
     if (rc != ARGREDUCE_OK) return rc;
     uint8_t* scratch16 = nullptr;
-    rc = scratch_of(p, scratch, scratch_bytes, &scratch16);
+    rc = scratch_of(p.scratch_bytes, scratch, scratch_bytes, &scratch16);
     if (rc != ARGREDUCE_OK) return rc;
     return status_of(launch_logprobs(p, a, tokens, entropy != 0, entropy == ARGREDUCE_ENTROPY_APART, top,
                                      stats, top > 0 ? top_logprobs : nullptr, top > 0 ? top_tokens : nullptr,

@@ -221,8 +221,35 @@ struct Span {
         else
             return __builtin_nontemporal_load(p);
     }
+    // A vector that lies wholly in the row.
+    __device__ typename Fmt::Vec load_whole(uint32_t v) const { return load(v); }
     // Position of element 0 of vector v (wraps for elements before the row).
     __device__ uint32_t pos(uint32_t v) const { return v * Fmt::VW - off; }
+};
+
+// The same of a row counted from its first element, wherever that lies (the hardware reads a vector at
+// any element's address): lanes and sums do not depend on the row's address, so equal rows have equal
+// statistics. Vectors [0, vb) lie wholly in the row; what is left past them is the one edge, read element
+// by element.
+template <typename Fmt>
+struct RowSpan {
+    const uint8_t* base;
+    uint32_t cols, va, vb;
+    __device__ RowSpan(const uint8_t* row, uint32_t n) : base(row), cols(n), va(0), vb(n / Fmt::VW) {}
+    __device__ uint32_t edge(int lane) const { return lane == 0 && cols % Fmt::VW ? vb : kNoVec; }
+    __device__ typename Fmt::Vec load_whole(uint32_t v) const {
+        typedef typename Fmt::Vec __attribute__((aligned(2))) Anywhere;
+        return __builtin_nontemporal_load(reinterpret_cast<const Anywhere*>(base + static_cast<size_t>(v) * 16));
+    }
+    __device__ typename Fmt::Vec load(uint32_t v) const {
+        if (v < vb) return load_whole(v);
+        typename Fmt::Bits b[Fmt::VW];
+        const auto* p = reinterpret_cast<const typename Fmt::Bits*>(base + static_cast<size_t>(v) * 16);
+#pragma unroll
+        for (uint32_t i = 0; i < Fmt::VW; ++i) b[i] = i < cols % Fmt::VW ? p[i] : 0;
+        return __builtin_bit_cast(typename Fmt::Vec, b);
+    }
+    __device__ uint32_t pos(uint32_t v) const { return v * Fmt::VW; }
 };
 
 // A vector of -inf.
@@ -357,7 +384,7 @@ __device__ inline void scan_on(const Sp& sp, uint32_t first, uint32_t last, int 
         Vec q[U];
         float e[U * VW];
 #pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = sp.load(base + lane + u * T);
+        for (int u = 0; u < U; ++u) q[u] = sp.load_whole(base + lane + u * T);
         unpack_all<Fmt, U>(q, e);
         if constexpr (SEG) {
             if (g.group == 0) {
@@ -382,7 +409,7 @@ __device__ inline void scan_on(const Sp& sp, uint32_t first, uint32_t last, int 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t v = base + lane + u * T;
-            if (base + u * T < last) q[u] = sp.load(v < last ? v : last - 1);
+            if (base + u * T < last) q[u] = sp.load_whole(v < last ? v : last - 1);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -558,11 +585,13 @@ __device__ inline float kth_bound(const float* seg, uint32_t segs, uint32_t k, i
     return bound > order_of(kLowest) ? value_of(bound) : kLowest;
 }
 
-// `segs` maxima are in L.seg. `vec(seg, i)` names vector i (of 2^lg_seg) of a segment, or kNoVec.
-// Leaves the k best (fewer if the row has fewer) in L.buf, their number in L.count.
+// `segs` maxima are in L.seg. `vec(seg, i)` names vector i (of 2^lg_seg) of a segment, or kNoVec;
+// `edges`: the row's edge vectors are looked at too. Leaves the k best (fewer if there are fewer) in
+// L.buf, their number in L.count.
 template <typename Fmt, int T, int S, typename Sp, typename VecOf>
 __device__ inline void top_select(TopLds<T, S>& L, const Sp& sp, uint32_t segs,
-                                  uint32_t lg_seg, uint32_t k, int lane, VecOf vec) {
+                                  uint32_t lg_seg, uint32_t k, int lane, VecOf vec,
+                                  bool edges = true) {
     constexpr int VW = Fmt::VW;
     constexpr int U = 4;  // vectors a thread reads at once
     if (lane == 0) {
@@ -581,7 +610,7 @@ __device__ inline void top_select(TopLds<T, S>& L, const Sp& sp, uint32_t segs,
         if (L.seg[s] >= tau) L.list[atomicAdd(&L.listed, 1u)] = static_cast<uint16_t>(s);
     team_sync<T>();
     const uint32_t main_items = L.listed << lg_seg;
-    const uint32_t items = main_items + 2;  // and the edges
+    const uint32_t items = main_items + (edges ? 2 : 0);
     const auto item_vec = [&](uint32_t it) {
         if (it < main_items) return vec(L.list[it >> lg_seg], it & ((1u << lg_seg) - 1));
         return it < items ? sp.edge(static_cast<int>(it - main_items)) : kNoVec;
@@ -694,6 +723,36 @@ __device__ inline typename Fmt::Vec pack(const float (&g)[Fmt::VW]) {
 #pragma unroll
     for (int i = 0; i < Fmt::VW; ++i) b[i] = round_to<Fmt>(g[i]);
     return __builtin_bit_cast(typename Fmt::Vec, b);
+}
+
+// ---------------------------------------------------------------------------------------
+// Launches.
+
+template <typename F>
+inline void with_format(int dtype, F f) {
+    switch (dtype) {
+        case ARGREDUCE_F32: f(F32{}); break;
+        case ARGREDUCE_F16: f(F16{}); break;
+        default: f(BF16{}); break;
+    }
+}
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+template <typename F>
+inline void with_bool(bool b, F f) {
+    if (b)
+        f(Int<1>{});
+    else
+        f(Int<0>{});
+}
+
+inline uint32_t log2_of(int v) { return static_cast<uint32_t>(__builtin_ctz(static_cast<unsigned>(v))); }
+
+template <typename... KArgs, typename... Args>
+inline void launch(void (*kernel)(KArgs...), uint32_t grid, int block, hipStream_t s, Args... args) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), 0, s, args...);
 }
 
 }  // namespace

@@ -49,6 +49,20 @@ typedef int (*distill_step_fn)(const void *, argreduce_dtype_t, int64_t, int64_t
                                const int64_t *, const float *, float, const float *, float *, void *,
                                void *, size_t, void *);
 
+typedef size_t (*beam_bytes_fn)(int64_t, int64_t, int64_t, argreduce_dtype_t, int32_t);
+typedef int (*beam_step_fn)(const void *, argreduce_dtype_t, int64_t, int64_t, int64_t, int64_t,
+                            const float *, const uint8_t *, int64_t, double, int32_t, void *, void *,
+                            size_t, void *);
+typedef int (*reorder_fn)(const argreduce_reorder_t *, const argreduce_state_t *, const int64_t *,
+                          const int64_t *, const int64_t *, int64_t, int64_t, void *);
+typedef size_t (*route_bytes_fn)(int64_t, int64_t, int64_t, argreduce_dtype_t);
+typedef int (*route_fn)(const void *, argreduce_dtype_t, int64_t, int64_t, int64_t, int64_t,
+                        const uint8_t *, int32_t, int32_t, float *, int64_t *, void *, void *, size_t,
+                        void *);
+typedef int (*route_grad_fn)(const void *, argreduce_dtype_t, int64_t, int64_t, int64_t, int64_t, int32_t,
+                             int32_t, const int64_t *, const void *, const float *, const float *,
+                             const float *, void *, void *);
+
 static lastaxis_fn g_lastaxis = NULL;
 static axis_fn g_axis = NULL;
 static scan_fn g_scan = NULL;
@@ -62,6 +76,12 @@ static logprobs_grad_fn g_logprobs_grad = NULL;
 static distill_fn g_distill = NULL;
 static distill_grad_fn g_distill_grad = NULL;
 static distill_step_fn g_distill_step = NULL;
+static beam_bytes_fn g_beam_bytes = NULL;
+static beam_step_fn g_beam_step = NULL;
+static reorder_fn g_reorder = NULL;
+static route_bytes_fn g_route_bytes = NULL;
+static route_fn g_route = NULL;
+static route_grad_fn g_route_grad = NULL;
 
 /* An address from a Python int (0 for NULL). */
 static void *arg_ptr(PyObject *o) { return PyLong_AsVoidPtr(o); }
@@ -322,6 +342,151 @@ static PyObject *fast_distill_step(PyObject *self, PyObject *const *a, Py_ssize_
     return PyLong_FromLong(rc);
 }
 
+/* argreduce_beam_scratch_bytes(groups, beams, cols, dtype, width) */
+static PyObject *fast_beam_bytes(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (check_nargs(n, 5, "argreduce_beam_scratch_bytes") || check_bound((const void *)g_beam_bytes))
+        return NULL;
+    const long long groups = PyLong_AsLongLong(a[0]);
+    const long long beams = PyLong_AsLongLong(a[1]);
+    const long long cols = PyLong_AsLongLong(a[2]);
+    const int32_t dtype = arg_i32(a[3]);
+    const int32_t width = arg_i32(a[4]);
+    if (PyErr_Occurred()) return NULL;
+    return PyLong_FromSize_t(g_beam_bytes((int64_t)groups, (int64_t)beams, (int64_t)cols,
+                                          (argreduce_dtype_t)dtype, width));
+}
+
+/* argreduce_beam_step(x, dtype, groups, beams, cols, row_stride, scores, ended, end_token, temperature,
+ *                     width, out, scratch, scratch_bytes, stream) */
+static PyObject *fast_beam_step(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (check_nargs(n, 15, "argreduce_beam_step") || check_bound((const void *)g_beam_step)) return NULL;
+    const void *x = arg_ptr(a[0]);
+    const int32_t dtype = arg_i32(a[1]);
+    const long long groups = PyLong_AsLongLong(a[2]);
+    const long long beams = PyLong_AsLongLong(a[3]);
+    const long long cols = PyLong_AsLongLong(a[4]);
+    const long long stride = PyLong_AsLongLong(a[5]);
+    const float *scores = (const float *)arg_ptr(a[6]);
+    const uint8_t *ended = (const uint8_t *)arg_ptr(a[7]);
+    const long long end_token = PyLong_AsLongLong(a[8]);
+    const double temperature = PyFloat_AsDouble(a[9]);
+    const int32_t width = arg_i32(a[10]);
+    void *out = arg_ptr(a[11]);
+    void *scratch = arg_ptr(a[12]);
+    const size_t sbytes = PyLong_AsSize_t(a[13]);
+    void *stream = arg_ptr(a[14]);
+    if (PyErr_Occurred()) return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_beam_step(x, (argreduce_dtype_t)dtype, (int64_t)groups, (int64_t)beams, (int64_t)cols,
+                     (int64_t)stride, scores, ended, (int64_t)end_token, temperature, width, out, scratch,
+                     sbytes, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* argreduce_reorder(plan, table, parents, first, last, first_value, last_value, stream); plan: the
+ * address of an argreduce_reorder_t in host memory */
+static PyObject *fast_reorder(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (check_nargs(n, 8, "argreduce_reorder") || check_bound((const void *)g_reorder)) return NULL;
+    const argreduce_reorder_t *plan = (const argreduce_reorder_t *)arg_ptr(a[0]);
+    const argreduce_state_t *table = (const argreduce_state_t *)arg_ptr(a[1]);
+    const int64_t *parents = (const int64_t *)arg_ptr(a[2]);
+    const int64_t *first = (const int64_t *)arg_ptr(a[3]);
+    const int64_t *last = (const int64_t *)arg_ptr(a[4]);
+    const long long first_value = PyLong_AsLongLong(a[5]);
+    const long long last_value = PyLong_AsLongLong(a[6]);
+    void *stream = arg_ptr(a[7]);
+    if (PyErr_Occurred()) return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_reorder(plan, table, parents, first, last, (int64_t)first_value, (int64_t)last_value, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* argreduce_route_scratch_bytes(groups, tokens, experts, dtype) */
+static PyObject *fast_route_bytes(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (check_nargs(n, 4, "argreduce_route_scratch_bytes") || check_bound((const void *)g_route_bytes))
+        return NULL;
+    const long long groups = PyLong_AsLongLong(a[0]);
+    const long long tokens = PyLong_AsLongLong(a[1]);
+    const long long experts = PyLong_AsLongLong(a[2]);
+    const int32_t dtype = arg_i32(a[3]);
+    if (PyErr_Occurred()) return NULL;
+    return PyLong_FromSize_t(g_route_bytes((int64_t)groups, (int64_t)tokens, (int64_t)experts,
+                                           (argreduce_dtype_t)dtype));
+}
+
+/* The arguments both routing calls start with: x, dtype, groups, tokens, experts, row_stride. */
+typedef struct {
+    const void *x;
+    argreduce_dtype_t dtype;
+    int64_t groups, tokens, experts, stride;
+} router_t;
+static router_t arg_router(PyObject *const *a) {
+    router_t l;
+    l.x = arg_ptr(a[0]);
+    l.dtype = (argreduce_dtype_t)arg_i32(a[1]);
+    l.groups = (int64_t)PyLong_AsLongLong(a[2]);
+    l.tokens = (int64_t)PyLong_AsLongLong(a[3]);
+    l.experts = (int64_t)PyLong_AsLongLong(a[4]);
+    l.stride = (int64_t)PyLong_AsLongLong(a[5]);
+    return l;
+}
+
+/* argreduce_route(x, dtype, groups, tokens, experts, row_stride, live, top, renormalize, weights, chosen,
+ *                 totals, scratch, scratch_bytes, stream) */
+static PyObject *fast_route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (check_nargs(n, 15, "argreduce_route") || check_bound((const void *)g_route)) return NULL;
+    const router_t l = arg_router(a);
+    const uint8_t *live = (const uint8_t *)arg_ptr(a[6]);
+    const int32_t top = arg_i32(a[7]);
+    const int32_t renormalize = arg_i32(a[8]);
+    float *weights = (float *)arg_ptr(a[9]);
+    int64_t *chosen = (int64_t *)arg_ptr(a[10]);
+    void *totals = arg_ptr(a[11]);
+    void *scratch = arg_ptr(a[12]);
+    const size_t sbytes = PyLong_AsSize_t(a[13]);
+    void *stream = arg_ptr(a[14]);
+    if (PyErr_Occurred()) return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_route(l.x, l.dtype, l.groups, l.tokens, l.experts, l.stride, live, top, renormalize, weights,
+                 chosen, totals, scratch, sbytes, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* argreduce_route_grad(x, dtype, groups, tokens, experts, row_stride, top, renormalize, chosen, totals,
+ *                      g_weights, g_balance, g_z, grad, stream) */
+static PyObject *fast_route_grad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (check_nargs(n, 15, "argreduce_route_grad") || check_bound((const void *)g_route_grad)) return NULL;
+    const router_t l = arg_router(a);
+    const int32_t top = arg_i32(a[6]);
+    const int32_t renormalize = arg_i32(a[7]);
+    const int64_t *chosen = (const int64_t *)arg_ptr(a[8]);
+    const void *totals = arg_ptr(a[9]);
+    const float *g_weights = (const float *)arg_ptr(a[10]);
+    const float *g_balance = (const float *)arg_ptr(a[11]);
+    const float *g_z = (const float *)arg_ptr(a[12]);
+    void *grad = arg_ptr(a[13]);
+    void *stream = arg_ptr(a[14]);
+    if (PyErr_Occurred()) return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = g_route_grad(l.x, l.dtype, l.groups, l.tokens, l.experts, l.stride, top, renormalize, chosen,
+                      totals, g_weights, g_balance, g_z, grad, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
 /* The measurement hooks, marshalled the same way so that their floors carry the same
  * host cost per call as the reductions they are compared with. */
 
@@ -407,7 +572,48 @@ static PyObject *fast_bind_logits(PyObject *self, PyObject *const *a, Py_ssize_t
     Py_RETURN_NONE;
 }
 
+/* bind_choices(beam_scratch_bytes, beam_step, reorder, route_scratch_bytes, route, route_grad): the
+ * library's entry points of beam search and routing, as addresses. */
+static PyObject *fast_bind_choices(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (check_nargs(n, 6, "bind_choices")) return NULL;
+    void *p[6];
+    for (int k = 0; k < 6; ++k) p[k] = arg_ptr(a[k]);
+    if (PyErr_Occurred()) return NULL;
+    for (int k = 0; k < 6; ++k) {
+        if (p[k] == NULL) {
+            PyErr_SetString(PyExc_ValueError, "bind_choices() needs six non-null addresses");
+            return NULL;
+        }
+    }
+    g_beam_bytes = (beam_bytes_fn)p[0];
+    g_beam_step = (beam_step_fn)p[1];
+    g_reorder = (reorder_fn)p[2];
+    g_route_bytes = (route_bytes_fn)p[3];
+    g_route = (route_fn)p[4];
+    g_route_grad = (route_grad_fn)p[5];
+    Py_RETURN_NONE;
+}
+
 static PyMethodDef k_methods[] = {
+    {"bind_choices", (PyCFunction)(void (*)(void))fast_bind_choices, METH_FASTCALL,
+     "bind_choices(beam_scratch_bytes, beam_step, reorder, route_scratch_bytes, route, route_grad): the "
+     "entry points of beam search and routing to call, as addresses."},
+    {"argreduce_beam_scratch_bytes", (PyCFunction)(void (*)(void))fast_beam_bytes, METH_FASTCALL,
+     "argreduce_beam_scratch_bytes(groups, beams, cols, dtype, width)"},
+    {"argreduce_beam_step", (PyCFunction)(void (*)(void))fast_beam_step, METH_FASTCALL,
+     "argreduce_beam_step(x, dtype, groups, beams, cols, row_stride, scores, ended, end_token, "
+     "temperature, width, out, scratch, scratch_bytes, stream)"},
+    {"argreduce_reorder", (PyCFunction)(void (*)(void))fast_reorder, METH_FASTCALL,
+     "argreduce_reorder(plan, table, parents, first, last, first_value, last_value, stream)"},
+    {"argreduce_route_scratch_bytes", (PyCFunction)(void (*)(void))fast_route_bytes, METH_FASTCALL,
+     "argreduce_route_scratch_bytes(groups, tokens, experts, dtype)"},
+    {"argreduce_route", (PyCFunction)(void (*)(void))fast_route, METH_FASTCALL,
+     "argreduce_route(x, dtype, groups, tokens, experts, row_stride, live, top, renormalize, weights, "
+     "chosen, totals, scratch, scratch_bytes, stream)"},
+    {"argreduce_route_grad", (PyCFunction)(void (*)(void))fast_route_grad, METH_FASTCALL,
+     "argreduce_route_grad(x, dtype, groups, tokens, experts, row_stride, top, renormalize, chosen, "
+     "totals, g_weights, g_balance, g_z, grad, stream)"},
     {"bind_logits", (PyCFunction)(void (*)(void))fast_bind_logits, METH_FASTCALL,
      "bind_logits(logprobs_scratch_bytes, distill_scratch_bytes, logprobs, logprobs_grad, distill, "
      "distill_grad, distill_step): the logits entry points to call, as addresses."},

@@ -68,6 +68,14 @@ KERNEL_SOURCES = ("argmin_reduction_wide_amd/csrc/argreduce_kernels.hip",
                   "argmin_reduction_wide_amd/csrc/argreduce_logits.hip",
                   "argmin_reduction_wide_amd/csrc/argreduce_logits.hpp",
                   "argmin_reduction_wide_amd/csrc/argreduce_logits_api.cpp",
+                  "argmin_reduction_wide_amd/csrc/argreduce_logits_device.hpp",
+                  "argmin_reduction_wide_amd/csrc/argreduce_checks.hpp",
+                  "argmin_reduction_wide_amd/csrc/argreduce_beam.hip",
+                  "argmin_reduction_wide_amd/csrc/argreduce_beam.hpp",
+                  "argmin_reduction_wide_amd/csrc/argreduce_beam_api.cpp",
+                  "argmin_reduction_wide_amd/csrc/argreduce_route.hip",
+                  "argmin_reduction_wide_amd/csrc/argreduce_route.hpp",
+                  "argmin_reduction_wide_amd/csrc/argreduce_route_api.cpp",
                   "include/argreduce.h")
 ROTATE_BYTES = 1 << 29  # 512 MiB of rotated inputs, twice the Infinity Cache
 PAGES_US_1x202048 = 6.4  # ArgMax fp32 [1,202048] per call on the pages' H200

@@ -423,6 +423,136 @@ int argreduce_distill_step(const void *x, argreduce_dtype_t dtype, int64_t rows,
                            float *stats, void *grad, void *scratch, size_t scratch_bytes,
                            void *stream);
 
+/* ----------------------------------------------------------------------------------------
+ * Beam search: the step that chooses how a search goes on, and the reordering of what the model
+ * keeps for every beam.
+ *
+ * Step. Row g * beams + b of the logits (format, stride, -inf, NaN and +inf as for the logits
+ * operators) belongs to beam b of group g, whose score is a sum of log probabilities. A beam offers
+ * for every unmasked token v the value
+ *
+ *     scores[g][b] + ln softmax(x / T)[v],
+ *
+ * and the step returns the `width` largest values of each group, largest first, equal ones by beam,
+ * then by logit and by token, with their beams ("parents") and tokens. Logits of one row keep their order
+ * (equal logits by token); values of different rows are compared in binary64, from sums whose relative error
+ * is about 1e-8, and rounded once, to binary32.
+ *
+ *   scores       [groups, beams]. A beam whose score is -inf, +inf or NaN offers nothing, nor does a
+ *                row with a NaN or +inf, or of -inf only. Rows that offer nothing by their score
+ *                or because they have ended are not read.
+ *   ended        [groups, beams] bytes or NULL: a non-zero one marks a beam that is finished: it offers
+ *                one value, its score, with the token `end_token`.
+ *   end_token    0 .. cols - 1, or negative: none (only without `ended`).
+ *   temperature  2^-60 <= T <= 2^60.
+ *   beams, width 1 .. ARGREDUCE_BEAM_MAX; groups * 256 <= INT32_MAX.
+ *   out          argreduce_beam_out_bytes bytes, 8-byte aligned: parents int64 [groups, width], tokens
+ *                int64 [groups, width], scores float [groups, width], ended bytes [groups, width] (1
+ *                where the token is end_token), one after another. Where a group offers fewer values the
+ *                rest is -1, -1, -inf and 0.
+ *
+ * Scratch, streams, captures and status codes as for the logits operators.
+ */
+#define ARGREDUCE_BEAM_MAX 64
+size_t argreduce_beam_scratch_bytes(int64_t groups, int64_t beams, int64_t cols, argreduce_dtype_t dtype,
+                                    int32_t width);
+size_t argreduce_beam_out_bytes(int64_t groups, int32_t width);
+int argreduce_beam_step(const void *x, argreduce_dtype_t dtype, int64_t groups, int64_t beams,
+                        int64_t cols, int64_t row_stride, const float *scores, const uint8_t *ended,
+                        int64_t end_token, double temperature, int32_t width, void *out, void *scratch,
+                        size_t scratch_bytes, void *stream);
+/* The plan of argreduce_beam_step: SUBWAVE (a wavefront per row), BLOCK or SPLIT; blocks_per_row is the
+ * number of slices of a row. */
+int argreduce_beam_plan(int64_t groups, int64_t beams, int64_t cols, argreduce_dtype_t dtype, int32_t width,
+                        argreduce_plan_t *plan);
+
+/*
+ * Reordering, in place: for every state, group g, beam b and position t in [first, last) of the group,
+ *
+ *     state[g][b][..., t, ...] = (state before the call)[g][parents[g][b]][..., t, ...],
+ *
+ * the other positions stay as they are. A state is a tensor of any element type, addressed in bytes:
+ * element run (g, b, o, t) of `inner` contiguous bytes lies at base + g * group_stride + b * beam_stride
+ * + o * outer_stride + t * position_stride. No two runs of a state may share a byte (else
+ * ARGREDUCE_ERR_INVALID_ARG), nor may two states (not checked).
+ *
+ *   parents   [groups, beams]; one that is negative or >= beams leaves its beam as it is.
+ *   first     [groups] int64, or NULL: first_value for all groups. Positions below 0 count as 0,
+ *   last      likewise;               those past the state's as its last.
+ *
+ * argreduce_reorder_plan checks the states (in host memory) once; argreduce_reorder takes the plan, and
+ * `table`, the same states in device memory. Beams that stay are neither read nor written; no scratch.
+ */
+#define ARGREDUCE_STATES_MAX 4096
+typedef struct {
+    void *base; /* device memory */
+    int64_t group_stride, beam_stride;
+    int64_t outer, outer_stride;
+    int64_t positions, position_stride;
+    int64_t inner;
+} argreduce_state_t;
+typedef struct {
+    int32_t tensors, beams;
+    int64_t groups;
+    int64_t positions;      /* the most that a state has */
+    int64_t position_bytes; /* of one beam and position: the most that a state has */
+} argreduce_reorder_t;
+int argreduce_reorder_plan(const argreduce_state_t *states, int32_t tensors, int64_t groups, int64_t beams,
+                           argreduce_reorder_t *plan);
+int argreduce_reorder(const argreduce_reorder_t *plan, const argreduce_state_t *table, const int64_t *parents,
+                      const int64_t *first, const int64_t *last, int64_t first_value, int64_t last_value,
+                      void *stream);
+
+/* ----------------------------------------------------------------------------------------
+ * Expert routing: the choice of `top` of the experts for every token from a router's logits, with
+ * weights, per-expert counts and two losses, and the gradient.
+ *
+ * Row g * tokens + t of the logits [.., experts] (format, stride and -inf as for the logits operators)
+ * belongs to token t of group g (a sequence, or all tokens of a batch). With p = softmax(x) of a token, c_e
+ * the number of tokens of the group that chose expert e and n the number of its tokens:
+ *
+ *     chosen   the `top` largest logits, largest first, equal ones by expert
+ *     weights  p of the chosen; with renormalize divided by their sum
+ *     balance  experts / (top n^2) sum_e c_e sum_t p_te
+ *     z        1 / n sum_t (ln sum_e exp x_te)^2
+ *
+ *   - A token that `live` marks with 0 is left out, and so is one whose every logit is -inf: chosen -1,
+ *     weights 0, no part in counts, n and losses, and gradient 0. The logits of the former are not read.
+ *   - Past the experts that are not masked: chosen -1, weights 0.
+ *   - A live token with a NaN or +inf: chosen -2, weights NaN, no counts; the group's losses are NaN, and
+ *     the token's own gradient.
+ *   - A group without tokens has losses 0.
+ *
+ *   live      [groups, tokens] bytes or NULL.
+ *   top       1 .. min(experts, ARGREDUCE_ROUTE_TOP_MAX); experts 1 .. ARGREDUCE_EXPERTS_MAX.
+ *   weights   [groups, tokens, top] out; chosen [groups, tokens, top] out.
+ *   totals    argreduce_route_totals_bytes bytes out, 8-byte aligned: counts int64 [groups, experts],
+ *             tokens (n) int64 [groups], balance float [groups], z float [groups], one after another.
+ *
+ * Sums are in binary32 in a workgroup and in binary64 between them, in one order; z is +inf where a sum
+ * leaves binary32.
+ */
+#define ARGREDUCE_EXPERTS_MAX 1024
+#define ARGREDUCE_ROUTE_TOP_MAX 64
+size_t argreduce_route_scratch_bytes(int64_t groups, int64_t tokens, int64_t experts, argreduce_dtype_t dtype);
+size_t argreduce_route_totals_bytes(int64_t groups, int64_t experts);
+int argreduce_route(const void *x, argreduce_dtype_t dtype, int64_t groups, int64_t tokens, int64_t experts,
+                    int64_t row_stride, const uint8_t *live, int32_t top, int32_t renormalize, float *weights,
+                    int64_t *chosen, void *totals, void *scratch, size_t scratch_bytes, void *stream);
+/* The plan of argreduce_route (path SUBWAVE: lanes_per_row lanes of a wavefront per token). */
+int argreduce_route_plan(int64_t groups, int64_t tokens, int64_t experts, argreduce_dtype_t dtype,
+                         argreduce_plan_t *plan);
+
+/* Gradient of sum (g_weights * weights) + sum_g (g_balance * balance + g_z * z) with respect to the
+ * logits: [groups, tokens, experts], contiguous, in the logits' format, every element written. Choice and
+ * counts are constants. x, top and renormalize are those of the forward call, chosen and totals what it
+ * wrote (of totals the counts and n are read). g_weights [groups, tokens, top], g_balance [groups] and g_z
+ * [groups] may be NULL: 0. An expert number beyond the row has no gradient. */
+int argreduce_route_grad(const void *x, argreduce_dtype_t dtype, int64_t groups, int64_t tokens, int64_t experts,
+                         int64_t row_stride, int32_t top, int32_t renormalize, const int64_t *chosen,
+                         const void *totals, const float *g_weights, const float *g_balance, const float *g_z,
+                         void *grad, void *stream);
+
 /* Measurement hook: the launch floor. Enqueues one empty kernel (one workgroup of 64
  * threads) on `stream`, the same way argreduce_lastaxis enqueues its kernels, so that a
  * benchmark can time bare launch latency in the same harness ("[CUDA] Parallelize
