@@ -79,6 +79,191 @@ __global__ __launch_bounds__(kTeamBlock<T>) void k_beam_scan(uint64_t x, uint64_
 }
 
 // ---------------------------------------------------------------------------------------
+// A slice that its workgroup holds in registers: the best of each wavefront by itself, then of the four.
+
+constexpr int kSliceWaves = kSliceThreads / kWave;
+constexpr int kWaveCap = 256;  // keys that a wavefront collects
+static_assert(kWaveCap >= kBeamMax, "the k best fit");
+
+// Lanes before this one in a mask.
+__device__ inline uint32_t below(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                     __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
+}
+
+// Keys of a wavefront's elements, the k best among them, in buf; returns their number. q: vectors of
+// one lane, element 0 of vector u at position pos + u * step; lane_max: the lane's maximum.
+//
+// A bound that k to 2 k of the 64 lanes' maxima reach (bisection by lane masks) bounds the k-th best
+// element from below; what reaches it is collected, each lane's at an offset of its own (a ballot and a
+// branch per element took 3600 cycles for 32 of them, this 1100). Where ties or a mask put more there than
+// buf holds, the k best are taken one by one.
+template <typename Fmt, int NV>
+__device__ inline uint32_t wave_best(const typename Fmt::Vec (&q)[NV], uint32_t pos, uint32_t step,
+                                     float lane_max, uint32_t k, uint64_t* buf, int lane) {
+    constexpr int VW = Fmt::VW;
+    const uint32_t o[1] = {lane_max >= kLowest ? order_of(lane_max) >> kLowBits<Fmt> : 0};
+    float tau = kLowest;
+    if (static_cast<uint32_t>(__popcll(__ballot(o[0] != 0))) >= k) {
+        const uint32_t bound = bisect(o, k, 2 * k) << kLowBits<Fmt>;
+        tau = bound > order_of(kLowest) ? value_of(bound) : kLowest;
+    }
+    uint32_t hits = 0;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float e[VW];
+        Fmt::unpack(q[u], e);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) hits += e[i] >= tau ? 1 : 0;
+    }
+    uint32_t at = hits;  // those of this lane and the lanes before it
+#pragma unroll
+    for (int off = 1; off < kWave; off *= 2) {
+        const uint32_t other = __shfl_up(at, off);
+        at += lane >= off ? other : 0;
+    }
+    const uint32_t n = __builtin_amdgcn_readlane(at, kWave - 1);
+    if (n <= kWaveCap) {
+        at -= hits;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            float e[VW];
+            Fmt::unpack(q[u], e);
+#pragma unroll
+            for (int i = 0; i < VW; ++i)
+                if (e[i] >= tau) buf[at++] = key_of(e[i], pos + u * step + i);
+        }
+        return n;
+    }
+    uint64_t last = ~uint64_t{0};
+    uint32_t taken = 0;
+    for (; taken < k; ++taken) {
+        uint64_t best = 0;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            float e[VW];
+            Fmt::unpack(q[u], e);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                const uint64_t key = e[i] >= kLowest ? key_of(e[i], pos + u * step + i) : 0;
+                best = key < last && key > best ? key : best;
+            }
+        }
+#pragma unroll
+        for (int off = 1; off < kWave; off *= 2) {
+            const uint64_t other = __shfl_xor(static_cast<unsigned long long>(best), off);
+            best = other > best ? other : best;
+        }
+        if (best == 0) break;
+        if (lane == 0) buf[taken] = best;
+        last = best;
+    }
+    return taken;
+}
+
+// One slice of up to NV vectors per lane. Tags as k_beam_scan's.
+template <typename Fmt, int NV>
+__global__ __launch_bounds__(kSliceThreads) void k_beam_slice(uint64_t x, uint64_t scores_, uint64_t ended_,
+                                                              uint64_t scratch, uint32_t stride,
+                                                              uint32_t slices, float scale) {
+    constexpr int VW = Fmt::VW;
+    __shared__ uint64_t s_buf[kSliceWaves][kWaveCap];
+    __shared__ Stat s_stat[kSliceWaves];
+    __shared__ uint32_t s_count[kSliceWaves];
+    const uint32_t cols = tags(x, scores_), parts = tag(ended_), k = tag(scratch);
+    const uint32_t at = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const uint32_t r = at / parts, b = at - r * parts;
+    const uint8_t* ended = addr<const uint8_t>(ended_);
+    if (!alive(addr<const float>(scores_)[r]) || (ended != nullptr && ended[r] != 0)) return;
+    const RowSpan<Fmt> sp(row_ptr<Fmt>(addr<const void>(x), r, stride), cols);
+    const uint32_t n = part_vecs(span_max<Fmt>(cols), parts);  // the row's last vector is in the last slices
+    const uint32_t first = b * n, vecs = sp.vb + (cols % VW ? 1 : 0);
+    const uint32_t last = first < vecs ? (vecs - first < n ? vecs : first + n) : first;
+    typename Fmt::Vec q[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const uint32_t v = first + tid + u * kSliceThreads;
+        q[u] = masked16<Fmt>();
+        if (v < last) {
+            if (v < sp.vb) {
+                q[u] = sp.load_whole(v);
+            } else {
+                q[u] = sp.load_tail();
+            }
+        }
+    }
+    Stat a;
+    a.init();
+    float most = -__builtin_huge_valf();  // the lane's maximum
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float e[VW];
+        Fmt::unpack(q[u], e);
+        most = max_f(most, max_of(e));
+    }
+    a.m = lanes_max<kWave>(max_f(most, kLowest));
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float e[VW];
+        Fmt::unpack(q[u], e);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            const float z = (e[i] - a.m) * scale;
+            const float p = exp2_f(z);
+            a.s += p;
+            a.h = fmaf(p, max_f(z, kZFloor), a.h);
+        }
+    }
+    a.s = lanes_sum<kWave>(a.s);
+    a.h = lanes_sum<kWave>(a.h);
+    uint32_t count = 0;
+    if (a.s > 0.0f)
+        count = wave_best<Fmt, NV>(q, (first + tid) * VW, kSliceThreads * VW, most, k, s_buf[wave], lane);
+    if (lane == 0) {
+        s_stat[wave] = a;
+        s_count[wave] = count;
+    }
+    __syncthreads();
+    // every thread merges the four statistics; the keys' ranks among all of them
+    Stat all = s_stat[0];
+    uint32_t total = s_count[0];
+#pragma unroll
+    for (int w = 1; w < kSliceWaves; ++w) {
+        Stat o = s_stat[w];
+        const float to = max_f(all.m, o.m);
+        all.move<true>(to, scale);
+        o.move<true>(to, scale);
+        all.s += o.s;
+        all.h += o.h;
+        total += s_count[w];
+    }
+    Slice* slice = addr<Slice>(scratch) + at;
+    uint64_t* list = reinterpret_cast<uint64_t*>(addr<Slice>(scratch) + slices) + static_cast<size_t>(at) * k;
+    const bool ok = all.s > 0.0f;
+    for (uint32_t i = tid; ok && i < total; i += kSliceThreads) {
+        uint32_t in = i, w = 0;
+#pragma unroll
+        for (int x = 0; x < kSliceWaves - 1; ++x)
+            if (w == static_cast<uint32_t>(x) && in >= s_count[x]) {
+                in -= s_count[x];
+                ++w;
+            }
+        const uint64_t key = s_buf[w][in];
+        uint32_t rank = 0;
+#pragma unroll
+        for (int x = 0; x < kSliceWaves; ++x) {
+            const uint32_t many = s_count[x];
+#pragma unroll 8
+            for (uint32_t j = 0; j < many; ++j) rank += s_buf[x][j] > key ? 1 : 0;
+        }
+        if (rank < k) list[rank] = key;
+    }
+    if (tid == 0) *slice = Slice{all.m, all.s, all.h, ok ? (total < k ? total : k) : 0};
+}
+
+// ---------------------------------------------------------------------------------------
 // The join of one group's lists, at most kBeamLists of them, one per thread.
 
 constexpr int kJoinThreads = 256;
@@ -99,8 +284,9 @@ __device__ inline double value64(uint64_t o) {
 struct Cand {
     uint64_t value, key;  // value 0: none
     uint32_t beam;
-    __device__ bool above(const Cand& o) const {
-        return value > o.value || (value == o.value && (beam < o.beam || (beam == o.beam && key > o.key)));
+    __device__ bool above(const Cand& o) const {  // without branches
+        const bool before = (beam < o.beam) | ((beam == o.beam) & (key > o.key));
+        return (value > o.value) | ((value == o.value) & before);
     }
 };
 
@@ -117,12 +303,18 @@ struct CandLds {
     }
 };
 
+constexpr uint16_t kNoList = 0xffff;
+constexpr int kCands = kBeamMax * (kBeamMax + 1) / 2;
 struct JoinLds {
     double base[kBeamMax];  // S_b - ln s_b, of a row that can be continued
     float m[kBeamMax];
     CandLds<kBeamLists> head;
+    uint16_t near[kBeamLists];  // lists whose heads can be among the width best
+    uint16_t entries[kBeamLists];
+    uint16_t list[kBeamMax];    // of the r-th best head
+    uint32_t close;
     // What can be among the width best: entry j of the list whose head is the r-th best where r + j < width.
-    CandLds<kBeamMax * (kBeamMax + 1) / 2> cand;
+    CandLds<kCands> cand;
     uint32_t count;
 };
 
@@ -141,25 +333,46 @@ struct JoinArgs {
     double k, lo;          // log2(e) / T, and ln 2 k_lo / k_hi
 };
 
-// Statistics of the rows, a wavefront each; then heads, candidates and ranks. After it the thread
-// of rank r < width (r < count) holds candidate r in *out.
+// Statistics of the rows, a wavefront each; the heads of the lists, one per thread, and their ranks; the
+// entries that can be among the best, all at once. Leaves them in L.cand, their number in L.count.
 __device__ inline void join(JoinLds& L, const JoinArgs& a) {
     const int tid = threadIdx.x, lane = tid % kWave;
     const double invt = a.k * kLn2d;
+    const uint32_t lists = a.beams * a.parts, width = a.width;
+    // this thread's list: loaded ahead of the statistics it is judged by
+    const bool mine = static_cast<uint32_t>(tid) < lists;
+    const uint32_t b_mine = mine ? tid / a.parts : 0;
+    const float score_mine = a.scores[b_mine];
+    const bool done_mine = a.ended != nullptr && a.ended[b_mine] != 0;
+    const bool on = mine && alive(score_mine) && !done_mine;
+    uint64_t key = 0;
+    uint32_t entries = 0;
+    if (on) {
+        entries = a.slices[tid].count;
+        key = a.lists[static_cast<size_t>(tid) * width];
+    }
     for (uint32_t b = tid / kWave; b < a.beams; b += kJoinThreads / kWave) {
         const float score = a.scores[b];
         double base = -__builtin_huge_val();
         float m = kLowest;
         if (alive(score) && !(a.ended != nullptr && a.ended[b] != 0)) {
             const Slice* p = a.slices + b * a.parts;
-            for (uint32_t i = lane; i < a.parts; i += kWave) m = max_f(m, p[i].m);
+            Slice s[kBeamLists / kWave];
+#pragma unroll
+            for (int i = 0; i < kBeamLists / kWave; ++i) {
+                s[i] = Slice{kLowest, 0.0f, 0.0f, 0};
+                if (lane + i * kWave < a.parts) s[i] = p[lane + i * kWave];
+                m = max_f(m, s[i].m);
+            }
             m = lanes_max<kWave>(m);
-            double s = 0.0;
-            for (uint32_t i = lane; i < a.parts; i += kWave)
-                s += (static_cast<double>(p[i].s) + a.lo * static_cast<double>(p[i].h)) *
-                     exp2((static_cast<double>(p[i].m) - static_cast<double>(m)) * a.k);
-            s = lanes_sum64(s);
-            if (s > 0.0) base = static_cast<double>(score) - log(s);
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < kBeamLists / kWave; ++i)
+                if (static_cast<uint32_t>(i) * kWave < a.parts)
+                    sum += (static_cast<double>(s[i].s) + a.lo * static_cast<double>(s[i].h)) *
+                           exp2((static_cast<double>(s[i].m) - static_cast<double>(m)) * a.k);
+            sum = lanes_sum64(sum);
+            if (sum > 0.0) base = static_cast<double>(score) - log(sum);
         }
         if (lane == 0) {
             L.base[b] = base;
@@ -167,43 +380,65 @@ __device__ inline void join(JoinLds& L, const JoinArgs& a) {
         }
     }
     if (tid == 0) L.count = 0;
+    if (tid < kBeamMax) L.list[tid] = kNoList;
     __syncthreads();
-    const auto candidate = [&](uint32_t b, uint64_t key) {
+    const auto candidate = [&](uint32_t b, uint64_t k) {
         float v;
         uint32_t i;
-        Key32<kMax>::split(key, v, i);
+        Key32<kMax>::split(k, v, i);
         const double value = L.base[b] + (static_cast<double>(v) - static_cast<double>(L.m[b])) * invt;
-        return Cand{order64(value), key, b};
+        return Cand{order64(value), k, b};
     };
-    const uint32_t lists = a.beams * a.parts;
     Cand head{0, 0, 0};
-    uint32_t mine = 0;  // entries of this thread's list
-    if (static_cast<uint32_t>(tid) < lists) {
-        const uint32_t b = tid / a.parts;
-        if (a.ended != nullptr && a.ended[b] != 0) {
-            if (tid % a.parts == 0 && alive(a.scores[b])) {  // goes on as it is
-                head = Cand{order64(static_cast<double>(a.scores[b])), key_of(0.0f, a.end_token), b};
-                mine = 1;
-            }
-        } else if (L.base[b] > -__builtin_huge_val()) {
-            mine = a.slices[tid].count;
-            if (mine > 0) head = candidate(b, a.lists[static_cast<size_t>(tid) * a.width]);
-        }
+    if (on) {
+        if (L.base[b_mine] > -__builtin_huge_val() && entries > 0) head = candidate(b_mine, key);
+    } else if (mine && done_mine && alive(score_mine) && tid % a.parts == 0) {  // goes on as it is
+        head = Cand{order64(static_cast<double>(score_mine)), key_of(0.0f, a.end_token), b_mine};
+        entries = 1;
+    }
+    if (tid < kBeamLists) {
         L.head.put(tid, head);
+        L.entries[tid] = static_cast<uint16_t>(entries);
     }
     __syncthreads();
-    if (mine > 0) {
-        uint32_t rank = 0;
-        for (uint32_t i = 0; i < lists; ++i) rank += L.head.get(i).above(head) ? 1 : 0;
-        if (rank < a.width) {
-            const uint32_t room = a.width - rank;
-            mine = mine < room ? mine : room;
-            const uint32_t to = atomicAdd(&L.count, mine);
-            L.cand.put(to, head);
-            const uint32_t b = tid / a.parts;
-            for (uint32_t j = 1; j < mine; ++j)
-                L.cand.put(to + j, candidate(b, a.lists[static_cast<size_t>(tid) * a.width + j]));
+    // One wavefront finds a bound that the width best heads reach, and few more (by the upper words of the
+    // values); the others wait. Ranks among all heads took 25 us with 256 of them.
+    if (tid < kWave) {
+        constexpr int kPer = kBeamLists / kWave;
+        uint32_t o[kPer], some = 0, bound = 0, n = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            o[i] = static_cast<uint32_t>(L.head.value[tid + i * kWave] >> 32);
+            some += __popcll(__ballot(o[i] != 0));
         }
+        if (some > width) bound = bisect(o, width);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const bool in = o[i] != 0 && o[i] >= bound;
+            const uint64_t mask = __ballot(in);
+            if (in) L.near[n + below(mask)] = static_cast<uint16_t>(tid + i * kWave);
+            n += __popcll(mask);
+        }
+        if (tid == 0) L.close = n;
+    }
+    __syncthreads();
+    const uint32_t close = L.close;
+    if (static_cast<uint32_t>(tid) < close) {
+        const uint32_t list = L.near[tid];
+        const Cand c = L.head.get(list);
+        uint32_t rank = 0;
+#pragma unroll 4
+        for (uint32_t i = 0; i < close; ++i) rank += L.head.get(L.near[i]).above(c) ? 1 : 0;
+        if (rank < width) L.list[rank] = static_cast<uint16_t>(list);
+    }
+    __syncthreads();
+    const uint64_t least = L.list[width - 1] != kNoList ? L.head.value[L.list[width - 1]] : 0;
+    for (uint32_t i = tid; i < width * width; i += kJoinThreads) {
+        const uint32_t r = i / width, j = i - r * width, list = L.list[r];
+        if (r + j >= width || list == kNoList || j >= L.entries[list]) continue;
+        Cand c = L.head.get(list);
+        if (j > 0) c = candidate(c.beam, a.lists[static_cast<size_t>(list) * width + j]);
+        if (c.value >= least) L.cand.put(atomicAdd(&L.count, 1u), c);
     }
     __syncthreads();
 }
@@ -257,6 +492,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_beam_join(uint64_t scores, uin
     for (uint32_t i = tid; i < n; i += kJoinThreads) {
         const Cand c = L.cand.get(i);
         uint32_t rank = 0;
+#pragma unroll 4
         for (uint32_t j = 0; j < n; ++j) rank += L.cand.get(j).above(c) ? 1 : 0;
         if (rank < width) {
             const uint32_t token = ~static_cast<uint32_t>(c.key);
@@ -388,7 +624,18 @@ hipError_t launch_beam_step(const BeamPlan& plan, const BeamArgs& a, uint8_t* sc
                tagged(a.x, cols), tagged(a.scores, cols >> 16), tagged(a.ended, plan.parts),
                tagged(scratch16, a.width), static_cast<uint32_t>(a.row_stride), slices, hi);
     };
+    const auto slice = [&](auto fmt, auto held) {
+        launch(k_beam_slice<decltype(fmt), decltype(held)::value>, slices, kSliceThreads, s, tagged(a.x, cols),
+               tagged(a.scores, cols >> 16), tagged(a.ended, plan.parts), tagged(scratch16, a.width),
+               static_cast<uint32_t>(a.row_stride), slices, hi);
+    };
     with_format(a.dtype, [&](auto fmt) {
+        switch (plan.held) {
+            case 1: return slice(fmt, Int<1>{});
+            case 2: return slice(fmt, Int<2>{});
+            case 4: return slice(fmt, Int<4>{});
+            case 8: return slice(fmt, Int<8>{});
+        }
         switch (plan.team) {
             case 64: scan(fmt, Int<64>{}); break;
             case 256: scan(fmt, Int<256>{}); break;

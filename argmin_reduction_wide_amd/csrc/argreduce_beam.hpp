@@ -11,6 +11,8 @@
 namespace argreduce {
 
 constexpr int kBeamMax = 64;     // beams of a group, and candidates kept (ARGREDUCE_BEAM_MAX)
+constexpr int kSliceThreads = 256;  // of a workgroup that holds a slice in registers
+constexpr int kSliceVecs = 8;    // 16-byte vectors each of its lanes holds, at most
 constexpr int kBeamLists = 256;  // lists of candidates that one group's join takes
 
 // How the rows (one per beam) of one step are scanned.
@@ -18,6 +20,7 @@ struct BeamPlan {
     int path;             // argreduce_path_t: SUBWAVE (a wavefront per row), BLOCK or SPLIT
     int team;             // lanes that scan one slice: 64, 256, 512 or 1024
     int parts;            // slices per row, each with a list of candidates of its own
+    int held;             // vectors per lane of a slice held in registers: 1, 2, 4, 8, or 0 (one pass)
     int64_t grid_blocks;  // workgroups of the scanning kernel
     int64_t device_threads;
     size_t scratch_bytes; // including 15 bytes of alignment slack

@@ -9,7 +9,7 @@ namespace argreduce {
 namespace {
 
 // Slices of at least this many vectors: two for each of 256 lanes.
-constexpr int64_t kSliceVecs = 512;
+constexpr int64_t kLeastSlice = 512;
 
 int check_beams(int64_t groups, int64_t beams, int64_t cols, int dtype) {
     if (logits_elem_size(dtype) == 0) return ARGREDUCE_ERR_UNSUPPORTED_DTYPE;
@@ -36,10 +36,14 @@ int make_beam_plan(int dtype, int64_t groups, int64_t beams, int64_t cols, int w
         p->team = 64;
     } else {
         // slices of rows too few to give every CU one
-        parts = std::min({ceil_div(vecs, kSliceVecs), std::max<int64_t>(1, cus / rows), kBeamLists / beams});
+        parts = std::min({ceil_div(vecs, kLeastSlice), std::max<int64_t>(1, cus / rows), kBeamLists / beams});
         p->path = parts > 1 ? ARGREDUCE_PATH_SPLIT : ARGREDUCE_PATH_BLOCK;
         const int64_t slice = ceil_div(vecs, parts);
         p->team = slice > 2048 && rows * 1024 <= cap ? 1024 : slice > 4096 ? 512 : 256;
+        if (parts > 1 && slice <= kSliceVecs * kSliceThreads) {
+            p->team = kSliceThreads;
+            p->held = static_cast<int>(next_pow2(ceil_div(slice, kSliceThreads)));
+        }
     }
     p->parts = static_cast<int>(parts);
     p->grid_blocks = p->team == 64 ? ceil_div(rows * parts, kBlock / 64) : rows * parts;

@@ -227,31 +227,6 @@ struct Span {
     __device__ uint32_t pos(uint32_t v) const { return v * Fmt::VW - off; }
 };
 
-// The same of a row counted from its first element, wherever that lies (the hardware reads a vector at
-// any element's address): lanes and sums do not depend on the row's address, so equal rows have equal
-// statistics. Vectors [0, vb) lie wholly in the row; what is left past them is the one edge, read element
-// by element.
-template <typename Fmt>
-struct RowSpan {
-    const uint8_t* base;
-    uint32_t cols, va, vb;
-    __device__ RowSpan(const uint8_t* row, uint32_t n) : base(row), cols(n), va(0), vb(n / Fmt::VW) {}
-    __device__ uint32_t edge(int lane) const { return lane == 0 && cols % Fmt::VW ? vb : kNoVec; }
-    __device__ typename Fmt::Vec load_whole(uint32_t v) const {
-        typedef typename Fmt::Vec __attribute__((aligned(2))) Anywhere;
-        return __builtin_nontemporal_load(reinterpret_cast<const Anywhere*>(base + static_cast<size_t>(v) * 16));
-    }
-    __device__ typename Fmt::Vec load(uint32_t v) const {
-        if (v < vb) return load_whole(v);
-        typename Fmt::Bits b[Fmt::VW];
-        const auto* p = reinterpret_cast<const typename Fmt::Bits*>(base + static_cast<size_t>(v) * 16);
-#pragma unroll
-        for (uint32_t i = 0; i < Fmt::VW; ++i) b[i] = i < cols % Fmt::VW ? p[i] : 0;
-        return __builtin_bit_cast(typename Fmt::Vec, b);
-    }
-    __device__ uint32_t pos(uint32_t v) const { return v * Fmt::VW; }
-};
-
 // A vector of -inf.
 template <typename Fmt>
 __device__ inline typename Fmt::Vec masked16() {
@@ -266,6 +241,36 @@ __device__ inline typename Fmt::Vec masked_unless(bool in, const typename Fmt::V
     return __builtin_bit_cast(typename Fmt::Vec,
                               u32x4{in ? a.x : b.x, in ? a.y : b.y, in ? a.z : b.z, in ? a.w : b.w});
 }
+
+// The same of a row counted from its first element, wherever that lies (the hardware reads a vector at
+// any element's address): lanes and sums do not depend on the row's address, so equal rows have equal
+// statistics. Vectors [0, vb) lie wholly in the row; what is left past them is the one edge, read element
+// by element.
+template <typename Fmt>
+struct RowSpan {
+    const uint8_t* base;
+    uint32_t cols, va, vb;
+    __device__ RowSpan(const uint8_t* row, uint32_t n) : base(row), cols(n), va(0), vb(n / Fmt::VW) {}
+    __device__ uint32_t edge(int lane) const { return lane == 0 && cols % Fmt::VW ? vb : kNoVec; }
+    __device__ typename Fmt::Vec load_whole(uint32_t v) const {
+        typedef typename Fmt::Vec __attribute__((aligned(2))) Anywhere;
+        return __builtin_nontemporal_load(reinterpret_cast<const Anywhere*>(base + static_cast<size_t>(v) * 16));
+    }
+    // The edge, -inf past the row's end.
+    __device__ typename Fmt::Vec load_tail() const {
+        struct Bits {
+            typename Fmt::Bits b[Fmt::VW];
+        };
+        const auto* p = reinterpret_cast<const typename Fmt::Bits*>(base + static_cast<size_t>(vb) * 16);
+        Bits t = __builtin_bit_cast(Bits, masked16<Fmt>());
+#pragma unroll
+        for (uint32_t i = 0; i < Fmt::VW; ++i)
+            if (i < cols % Fmt::VW) t.b[i] = p[i];
+        return __builtin_bit_cast(typename Fmt::Vec, t);
+    }
+    __device__ typename Fmt::Vec load(uint32_t v) const { return v < vb ? load_whole(v) : load_tail(); }
+    __device__ uint32_t pos(uint32_t v) const { return v * Fmt::VW; }
+};
 
 // Vectors a lane reads per step of a scan: four, or 16 elements where the alternatives' segments
 // take registers too ([2048,128256] bf16, T = 512, four and two vectors: 87 and 93 us without
@@ -525,9 +530,10 @@ __device__ inline void top_cut(TopLds<T, S>& L, int lane, uint32_t k) {
 template <typename Fmt>
 constexpr int kLowBits = std::is_same<Fmt, F32>::value ? 0 : std::is_same<Fmt, F16>::value ? 13 : 16;
 
-// Bisection for kth_bound over N maxima per lane: N comparisons a step, the counts from lane masks.
+// Bisection for kth_bound over N maxima per lane: N comparisons a step, the counts from lane masks. Stops
+// when at most `enough` maxima reach the bound.
 template <int N>
-__device__ inline uint32_t bisect(const uint32_t (&o)[N], uint32_t k) {
+__device__ inline uint32_t bisect(const uint32_t (&o)[N], uint32_t k, uint32_t enough) {
     uint32_t hi = 0, lo = 0;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -536,7 +542,6 @@ __device__ inline uint32_t bisect(const uint32_t (&o)[N], uint32_t k) {
     }
     hi = wave_max_u32(hi) + 1;
     lo = ~wave_max_u32(lo);
-    const uint32_t enough = k + k / 8 + 2;
     while (hi - lo > 1) {
         const uint32_t mid = lo + (hi - lo) / 2;
         uint32_t n = 0;
@@ -550,6 +555,11 @@ __device__ inline uint32_t bisect(const uint32_t (&o)[N], uint32_t k) {
         }
     }
     return lo;
+}
+
+template <int N>
+__device__ inline uint32_t bisect(const uint32_t (&o)[N], uint32_t k) {
+    return bisect(o, k, k + k / 8 + 2);
 }
 
 // A value that at least k, and if the values allow few more, of the `segs` maxima reach (the
