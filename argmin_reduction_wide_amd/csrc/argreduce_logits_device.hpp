@@ -736,6 +736,57 @@ __device__ inline typename Fmt::Vec pack(const float (&g)[Fmt::VW]) {
 }
 
 // ---------------------------------------------------------------------------------------
+// Which workgroup of a launch is the last of several to be done with its part, so that it can join the
+// parts: nothing waits, and the words in scratch may hold anything before. Every workgroup stores its part
+// with store_part, then the launch's tag into its own slot, and then reads all slots: who finds the tag in
+// all of them comes after all parts. Several can find it, and the first of them to put the tag into the
+// owner's word is the one. The parts are read with load_part.
+//
+// The tag is one of 2^64 made from the call's nonce and a generation word in scratch, which the last
+// workgroup moves on and all others have read before: a graph's replay, whose nonce is that of its
+// capture, has another tag than the replay before it.
+//
+// Parts and slots are agent-scope accesses, which pass the L2 caches of the XCDs; a store is done when its
+// wavefront's count of memory operations says so (vmcnt), so that no cache has to be written back.
+
+template <typename T>
+__device__ inline void store_part(T* p, T v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ inline T load_part(const T* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ inline uint64_t arrival_tag(uint32_t nonce, uint64_t generation) {
+    uint64_t v = generation + 0x9e3779b97f4a7c15ull * (nonce | uint64_t{1} << 32);
+    v = (v ^ (v >> 30)) * 0xbf58476d1ce4e5b9ull;
+    v = (v ^ (v >> 27)) * 0x94d049bb133111ebull;
+    return v ^ (v >> 31);
+}
+
+// Called by the whole workgroup after its last store_part; `found` is in LDS. Whether it is the last of n.
+__device__ inline bool arrive(uint64_t* slots, uint64_t* owner, uint32_t mine, uint32_t n, uint64_t tag,
+                              uint32_t* found) {
+    stores_done();
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        if (threadIdx.x == 0) store_part(slots + mine, tag);
+        stores_done();
+        bool there = true;
+        for (uint32_t i = threadIdx.x; i < n; i += kWave) there &= load_part(slots + i) == tag;
+        bool one = __ballot(!there) == 0;
+        if (threadIdx.x == 0) {
+            if (one) one = __hip_atomic_exchange(owner, tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != tag;
+            *found = one ? 1 : 0;
+        }
+    }
+    __syncthreads();
+    return *found != 0;
+}
+
+// ---------------------------------------------------------------------------------------
 // Launches.
 
 template <typename F>

@@ -17,6 +17,7 @@
 // workgroups run.
 #include <hip/hip_runtime.h>
 
+#include "argreduce_launch.hpp"
 #include "argreduce_logits_device.hpp"
 #include "argreduce_route.hpp"
 
@@ -26,75 +27,230 @@ namespace argreduce {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kRouteThreads = 256;
 constexpr uint32_t kColBits = 10;  // of an expert's number in a key
 static_assert(kExpertsMax == 1 << kColBits, "numbers of experts in a key");
 
-// Keys of logits, larger for a larger logit and among equals for the lower expert; 0: none. 16-bit
-// formats have at most 19 bits that differ between values (kLowBits), so 32 bits hold both.
+// ---------------------------------------------------------------------------------------
+// Keys of logits: larger for a larger logit and among equals for the lower expert, so that two keys are
+// never equal and a maximum takes one instruction. A logit's bits count as sign and magnitude, which
+// makes -0 and +0 alike. Keys below kSome are those of -inf and of nothing.
+
 template <typename Fmt>
-struct Key {
-    using T = uint32_t;
-    __device__ static T make(float v, uint32_t col) {
-        return (order_of(v + 0.0f) >> kLowBits<Fmt>) << kColBits | ((1u << kColBits) - 1 - col);
+struct Key;
+
+// 16-bit formats: the signed value of the bits above 16 bits for the expert.
+struct Key16 {
+    using T = int32_t;
+    static constexpr T kNone = INT32_MIN;
+    __device__ static T max(T a, T b) { return a > b ? a : b; }
+    __device__ static T min(T a, T b) { return a < b ? a : b; }
+    template <int CTRL>
+    __device__ static T dpp(T v) {
+        return static_cast<T>(dpp_u32<CTRL, 0xf>(static_cast<uint32_t>(v)));
     }
-    __device__ static float value(T k) {
-        const uint32_t o = k >> kColBits << kLowBits<Fmt>;  // the low bits are ones in a negative value's order
-        return value_of((o >> 31) ? o : o | ((1u << kLowBits<Fmt>) - 1));
+    // v of each lane's own half (of 16 or 32 lanes) and of the other one: the same two in both.
+    template <int HALF>
+    __device__ static void halves(T v, T& a, T& b) {
+        const auto r = HALF == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                                  : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        a = static_cast<T>(r[0]);
+        b = static_cast<T>(r[1]);
     }
-    __device__ static uint32_t col(T k) { return (1u << kColBits) - 1 - (k & ((1u << kColBits) - 1)); }
+    // The keys of a vector's eight elements; the first is expert `col`.
+    __device__ static void make(const u32x4 q, uint32_t col, T (&k)[8]) {
+        const uint32_t c = kExpertsMax - 1 - col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            typedef short s16x2 __attribute__((ext_vector_type(2)));
+            const uint32_t two = q[i];  // (a bit cast of q[i] itself would read q[0])
+            const s16x2 sign = __builtin_bit_cast(s16x2, two) >> 15;
+            const s16x2 magnitude = __builtin_bit_cast(s16x2, two & 0x7fff7fffu);
+            const uint32_t v = __builtin_bit_cast(uint32_t, (magnitude ^ sign) - sign);
+            k[2 * i] = static_cast<T>(v << 16 | (c - 2 * i));
+            k[2 * i + 1] = static_cast<T>((v & 0xffff0000u) | (c - 2 * i - 1));
+        }
+    }
+    __device__ static uint32_t bits(T k) {
+        const int32_t v = k >> 16;
+        return v < 0 ? 0x8000u | static_cast<uint32_t>(-v) : static_cast<uint32_t>(v);
+    }
+    __device__ static uint32_t col(T k) { return kExpertsMax - 1 - (static_cast<uint32_t>(k) & (kExpertsMax - 1)); }
 };
 template <>
+struct Key<F16> : Key16 {
+    static constexpr T kSome = -0x7bff * 0x10000;  // the lowest finite value's, of the last expert
+    __device__ static float value(T k) { return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits(k)))); }
+};
+template <>
+struct Key<BF16> : Key16 {
+    static constexpr T kSome = -0x7f7f * 0x10000;
+    __device__ static float value(T k) { return __uint_as_float(bits(k) << 16); }
+};
+// binary32: 32 bits for the value and 10 for the expert, as the mantissa of a binary64 in [1, 2), which has a
+// maximum and a minimum in one instruction.
+template <>
 struct Key<F32> {
-    using T = uint64_t;
-    __device__ static T make(float v, uint32_t col) { return key_of(v, col); }
-    __device__ static float value(T k) { return value_of(static_cast<uint32_t>(k >> 32)); }
-    __device__ static uint32_t col(T k) { return ~static_cast<uint32_t>(k); }
+    using T = double;
+    static constexpr T kNone = 1.0;
+    __device__ static T from(uint32_t o, uint32_t low) {
+        return __builtin_bit_cast(double, static_cast<uint64_t>(0x3ff00000u | o >> 12) << 32 | (o << 20 | low));
+    }
+    static constexpr T kSome = 1.0 + 0x00800001 * 0x1p-32;
+    __device__ static T max(T a, T b) {
+        T r;
+        asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+        return r;
+    }
+    __device__ static T min(T a, T b) {
+        T r;
+        asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+        return r;
+    }
+    template <int CTRL>
+    __device__ static T dpp(T v) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = dpp_u32<CTRL, 0xf>(static_cast<uint32_t>(u));
+        const uint32_t hi = dpp_u32<CTRL, 0xf>(static_cast<uint32_t>(u >> 32));
+        return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+    }
+    template <int HALF>
+    __device__ static void halves(T v, T& a, T& b) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        int32_t l[2], h[2];
+        Key16::halves<HALF>(static_cast<int32_t>(u), l[0], l[1]);
+        Key16::halves<HALF>(static_cast<int32_t>(u >> 32), h[0], h[1]);
+        a = __builtin_bit_cast(double, static_cast<uint64_t>(static_cast<uint32_t>(h[0])) << 32 | static_cast<uint32_t>(l[0]));
+        b = __builtin_bit_cast(double, static_cast<uint64_t>(static_cast<uint32_t>(h[1])) << 32 | static_cast<uint32_t>(l[1]));
+    }
+    __device__ static void make(const u32x4 q, uint32_t col, T (&k)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int32_t sign = static_cast<int32_t>(q[i]) >> 31;
+            const int32_t v = (static_cast<int32_t>(q[i] & 0x7fffffffu) ^ sign) - sign;
+            k[i] = from(static_cast<uint32_t>(v) ^ 0x80000000u, kExpertsMax - 1 - col - i);
+        }
+    }
+    __device__ static float value(T k) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, k);
+        const int32_t v = static_cast<int32_t>(static_cast<uint32_t>(u >> 20) ^ 0x80000000u);
+        return __uint_as_float(v < 0 ? 0x80000000u | static_cast<uint32_t>(-v) : static_cast<uint32_t>(v));
+    }
+    __device__ static uint32_t col(T k) {
+        return kExpertsMax - 1 - (static_cast<uint32_t>(__builtin_bit_cast(uint64_t, k)) & (kExpertsMax - 1));
+    }
 };
 
-template <int G>
-__device__ inline uint32_t lanes_best(uint32_t v) {
-    const auto up = [&](uint32_t o) { v = o > v ? o : v; };
-    if constexpr (G >= 2) up(dpp_u32<0xB1, 0xf>(v));
-    if constexpr (G >= 4) up(dpp_u32<0x4E, 0xf>(v));
-    if constexpr (G >= 8) up(dpp_u32<0x141, 0xf>(v));
-    if constexpr (G >= 16) up(dpp_u32<0x140, 0xf>(v));
-    if constexpr (G >= 32) up(__shfl_xor(v, 16));
-    if constexpr (G >= 64) up(__shfl_xor(v, 32));
-    return v;
+// Sorting networks, descending. A list of L keys in registers is merged with another one by taking the
+// larger of each two that stand opposite, which leaves the L largest of both, and sorting those.
+template <typename K>
+__device__ inline void exchange(typename K::T& a, typename K::T& b) {
+    const typename K::T hi = K::max(a, b);
+    b = K::min(a, b);
+    a = hi;
 }
-template <int G>
-__device__ inline uint64_t lanes_best(uint64_t v) {
-    const auto up = [&](uint64_t o) { v = o > v ? o : v; };
-    if constexpr (G >= 2) v = dpp_max_key<0xB1, 0xf>(v);
-    if constexpr (G >= 4) v = dpp_max_key<0x4E, 0xf>(v);
-    if constexpr (G >= 8) v = dpp_max_key<0x141, 0xf>(v);
-    if constexpr (G >= 16) v = dpp_max_key<0x140, 0xf>(v);
-    if constexpr (G >= 32) up(__shfl_xor(static_cast<unsigned long long>(v), 16));
-    if constexpr (G >= 64) up(__shfl_xor(static_cast<unsigned long long>(v), 32));
+template <typename K, int L>
+__device__ inline void sort_merged(typename K::T (&a)[L]) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            if ((i & d) == 0) exchange<K>(a[i], a[i + d]);
+}
+template <typename K, int L>
+__device__ inline void merge(typename K::T (&a)[L], const typename K::T (&b)[L]) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) a[i] = K::max(a[i], b[L - 1 - i]);
+    sort_merged<K, L>(a);
+}
+template <typename K>
+__device__ inline void sort8(typename K::T* a) {
+    constexpr int8_t kPairs[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                                      {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+    for (int i = 0; i < 19; ++i) exchange<K>(a[kPairs[i][0]], a[kPairs[i][1]]);
+}
+
+// The L largest of a lane's N keys, sorted.
+template <typename K, int L, int N>
+__device__ inline void best_of_lane(const typename K::T (&key)[N], typename K::T (&best)[L]) {
+    if constexpr (L == 2) {
+        best[0] = key[0];
+        best[1] = K::kNone;
+#pragma unroll
+        for (int i = 1; i < N; ++i) {
+            best[1] = K::max(best[1], K::min(best[0], key[i]));
+            best[0] = K::max(best[0], key[i]);
+        }
+    } else {
+        static_assert(L == 8, "lists of two or eight");
+#pragma unroll
+        for (int j = 0; j < N; j += L) {
+            typename K::T part[L];
+#pragma unroll
+            for (int i = 0; i < L; ++i) part[i] = j + i < N ? key[j + i] : K::kNone;
+            sort8<K>(part);
+            if (j == 0) {
+#pragma unroll
+                for (int i = 0; i < L; ++i) best[i] = part[i];
+            } else {
+                merge<K, L>(best, part);
+            }
+        }
+    }
+}
+// The L largest of G lanes' lists, in every lane.
+template <typename K, int G, int L>
+__device__ inline void best_of_lanes(typename K::T (&a)[L]) {
+    const auto with = [&](auto ctrl) {
+        typename K::T b[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) b[i] = K::template dpp<decltype(ctrl)::value>(a[i]);
+        merge<K, L>(a, b);
+    };
+    const auto across = [&](auto half) {
+        typename K::T b[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) K::template halves<decltype(half)::value>(a[i], a[i], b[i]);
+        merge<K, L>(a, b);
+    };
+    if constexpr (G >= 2) with(Int<0xB1>{});
+    if constexpr (G >= 4) with(Int<0x4E>{});
+    if constexpr (G >= 8) with(Int<0x141>{});
+    if constexpr (G >= 16) with(Int<0x140>{});
+    if constexpr (G >= 32) across(Int<16>{});
+    if constexpr (G >= 64) across(Int<32>{});
+}
+template <typename K, int G>
+__device__ inline typename K::T lanes_best(typename K::T v) {
+    if constexpr (G >= 2) v = K::max(v, K::template dpp<0xB1>(v));
+    if constexpr (G >= 4) v = K::max(v, K::template dpp<0x4E>(v));
+    if constexpr (G >= 8) v = K::max(v, K::template dpp<0x141>(v));
+    if constexpr (G >= 16) v = K::max(v, K::template dpp<0x140>(v));
+    typename K::T a = v, b = v;
+    if constexpr (G >= 32) {
+        K::template halves<16>(v, a, b);
+        v = K::max(a, b);
+    }
+    if constexpr (G >= 64) {
+        K::template halves<32>(v, a, b);
+        v = K::max(a, b);
+    }
     return v;
 }
 
-// A lane's columns of one token: NV vectors from column `col` on; -inf past the last expert.
-template <typename Fmt, int NV>
-__device__ inline void load_cols(const uint8_t* row, uint32_t col, uint32_t experts, float (&e)[NV * Fmt::VW]) {
-    constexpr int VW = Fmt::VW;
+// A vector of one token's logits from column c on; -inf past the last expert.
+template <typename Fmt>
+__device__ inline typename Fmt::Vec load_cols(const uint8_t* row, uint32_t c, uint32_t experts) {
+    if (c + Fmt::VW <= experts) return load16_any<Fmt>(row + static_cast<size_t>(c) * Fmt::kSize);
+    struct Bits {
+        typename Fmt::Bits b[Fmt::VW];
+    };
+    Bits t = __builtin_bit_cast(Bits, masked16<Fmt>());
+    const auto* p = reinterpret_cast<const typename Fmt::Bits*>(row) + c;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const uint32_t c = col + n * VW;
-        float f[VW];
-#pragma unroll
-        for (int i = 0; i < VW; ++i) f[i] = -__builtin_huge_valf();
-        if (c + VW <= experts) {
-            Fmt::unpack(load16_any<Fmt>(row + static_cast<size_t>(c) * Fmt::kSize), f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VW; ++i)
-                if (c + i < experts) f[i] = Fmt::load1(row + static_cast<size_t>(c + i) * Fmt::kSize);
-        }
-#pragma unroll
-        for (int i = 0; i < VW; ++i) e[n * VW + i] = f[i];
-    }
+    for (uint32_t i = 0; i < Fmt::VW; ++i)
+        if (c + i < experts) t.b[i] = p[i];
+    return __builtin_bit_cast(typename Fmt::Vec, t);
 }
 
 // A token's maximum and sum of exponentials; e becomes exp(x - m).
@@ -113,137 +269,100 @@ __device__ inline void softmax(float (&e)[N], float& m, float& s) {
     s = lanes_sum<G>(s);
 }
 
-// Partial sums of a workgroup in scratch: [experts] float, [experts] uint32, and these.
-struct Tail {
-    float z;
-    uint32_t tokens;
-};
-__host__ __device__ inline size_t partial_bytes(uint32_t experts) { return 8 * static_cast<size_t>(experts) + sizeof(Tail); }
+// ---------------------------------------------------------------------------------------
+// Sums over the tokens of a group: one partial per workgroup, joined by the last of up to kRouteSet
+// workgroups; of more than that, the sets' partials by the last set's.
 
-// Tags: experts in x, top in live, blocks per group in weights, whether to renormalize in chosen.
-template <typename Fmt, int G, int NV>
-__global__ __launch_bounds__(kRouteThreads) void k_route(uint64_t x, uint64_t live_, uint64_t weights,
-                                                         uint64_t chosen, uint64_t scratch, uint32_t stride,
-                                                         uint32_t tokens) {
-    constexpr int N = NV * Fmt::VW, kTeams = kRouteThreads / G;
-    using K = Key<Fmt>;
-    __shared__ float s_sum[kTeams * G * N];
-    __shared__ uint32_t s_cnt[kTeams * G * N];
-    __shared__ float s_z[kRouteThreads / kWave];
-    __shared__ uint32_t s_n[kRouteThreads / kWave];
-    const uint32_t experts = tag(x), top = tag(live_), blocks = tag(weights);
-    const bool renormalize = tag(chosen) != 0;
-    const uint32_t g = blockIdx.x / blocks, b = blockIdx.x - g * blocks;
-    const uint32_t per = (tokens + blocks - 1) / blocks;
-    const uint32_t t0 = b * per < tokens ? b * per : tokens;
-    const uint32_t t1 = tokens - t0 < per ? tokens : t0 + per;
-    const uint32_t team = threadIdx.x / G;
-    const int lane = threadIdx.x % G;
-    const uint32_t col = lane * N;
-    const uint8_t* live = addr<const uint8_t>(live_);
-    float sum[N], z = 0.0f;
-    uint32_t cnt[N], n = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        sum[i] = 0.0f;
-        cnt[i] = 0;
+// A partial: a word per expert (the sum of its probabilities, and how often it was chosen above it), one for
+// the sum of z and the number of tokens above it.
+__device__ inline uint64_t word(float sum, uint32_t count) { return static_cast<uint64_t>(count) << 32 | __float_as_uint(sum); }
+__device__ inline float sum_of(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
+__device__ inline uint32_t count_of(uint64_t w) { return static_cast<uint32_t>(w >> 32); }
+
+// A group's words in scratch: its generation; owners and slots of its sets, and an owner and slots of the
+// group where there are several sets (arrive); partials of workgroups and of sets.
+struct Group {
+    uint64_t* generation;
+    uint64_t *owners, *slots, *last, *set_slots, *partials, *set_partials;
+    __host__ __device__ static uint32_t sets(uint32_t blocks) { return (blocks + kRouteSet - 1) / kRouteSet; }
+    __host__ __device__ static size_t words(uint32_t experts, uint32_t blocks) {
+        const uint32_t n = sets(blocks);
+        return 2 + n + (blocks + n) * (1 + static_cast<size_t>(experts) + 1);
     }
-    for (uint32_t base = t0; base < t1; base += kTeams) {
-        const uint32_t t = base + team;
-        const size_t r = static_cast<size_t>(g) * tokens + t;
-        const bool there = t < t1;
-        const bool on = there && (live == nullptr || live[r] != 0);
-        float e[N];
+    __device__ Group(uint8_t* scratch, uint32_t g, uint32_t experts, uint32_t blocks) {
+        const uint32_t n = sets(blocks);
+        generation = reinterpret_cast<uint64_t*>(scratch) + g * words(experts, blocks);
+        owners = generation + 1;
+        slots = owners + n;
+        last = slots + blocks;
+        set_slots = last + 1;
+        partials = set_slots + n;
+        set_partials = partials + static_cast<size_t>(blocks) * (experts + 1);
+    }
+};
+
+__device__ inline double lanes_sum64(double v) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) e[i] = -__builtin_huge_valf();
-        if (on) load_cols<Fmt, NV>(addr<const uint8_t>(x) + r * stride * Fmt::kSize, col, experts, e);
-        typename K::T key[N];
+    for (int o = 1; o < kWave; o *= 2) v += __shfl_xor(v, o);
+    return v;
+}
+
+struct JoinLds {
+    double share[kRouteThreads];
+    uint32_t times[kRouteThreads];
+    double red[kRouteThreads / kWave];
+};
+
+// Adds up n <= kRouteSet partials: each(expert, sum, count) by the threads of the workgroup in turn, in teams that
+// take a share of the partials each where there are fewer experts than threads; kBatch loads of a thread at
+// once (32 would take registers from the tokens' part: 157 instead of 72). Returns the sums of z and of the tokens, in the first wavefront.
+constexpr uint32_t kBatch = 16;
+struct Tail {
+    double z, tokens;
+};
+template <typename Each>
+__device__ inline Tail add_up(JoinLds& L, const uint64_t* partials, uint32_t n, uint32_t experts, Each each) {
+    const uint32_t columns = experts + 1;
+    static_assert(kRouteSet <= kWave, "a lane for each partial's last word");
+    uint64_t tail = 0;
+    if (threadIdx.x < n) tail = load_part(partials + static_cast<size_t>(threadIdx.x) * columns + experts);
+    uint32_t wide = kRouteThreads / 8;
+    while (wide < kRouteThreads && wide < experts) wide *= 2;
+    const uint32_t teams = kRouteThreads / wide, team = threadIdx.x / wide;
+    for (uint32_t c0 = 0; c0 < experts; c0 += wide) {
+        const uint32_t c = c0 + threadIdx.x % wide;
+        double share = 0.0;
+        uint32_t times = 0;
+        if (c < experts) {
+#pragma unroll 1
+            for (uint32_t b0 = team; b0 < n; b0 += kBatch * teams) {
+                uint64_t w[kBatch];
 #pragma unroll
-        for (int i = 0; i < N; ++i) key[i] = e[i] >= kLowest ? K::make(e[i], col + i) : 0;
-        float m, s;
-        softmax<G, N>(e, m, s);
-        const bool counts = on && s != 0.0f;  // a token whose every logit is -inf is left out
-        const bool ok = s > 0.0f && s < __builtin_huge_valf();
-        const float inv = 1.0f / s;
-        if (counts) {
-            const float lse = fmaf(log2_f(s), kLn2, m);
-            if (lane == 0) {
-                z = fmaf(lse, lse, z);
-                ++n;
-            }
+                for (uint32_t i = 0; i < kBatch; ++i) {
+                    const uint32_t b = b0 + i * teams;
+                    w[i] = b < n ? load_part(partials + static_cast<size_t>(b) * columns + c) : 0;
+                }
 #pragma unroll
-            for (int i = 0; i < N; ++i) sum[i] = fmaf(e[i], inv, sum[i]);
-        }
-        // the best key left, `top` times: lane j % G keeps the j-th
-        float kept_sum = 0.0f;
-        float* wt = addr<float>(weights) + r * top;
-        int64_t* ch = addr<int64_t>(chosen) + r * top;
-        for (uint32_t j0 = 0; j0 < top; j0 += G) {
-            typename K::T mine = 0;
-            const uint32_t j1 = top - j0 < G ? top - j0 : G;
-            for (uint32_t j = 0; j < j1; ++j) {
-                typename K::T best = 0;
-#pragma unroll
-                for (int i = 0; i < N; ++i) best = key[i] > best ? key[i] : best;
-                best = lanes_best<G>(best);
-                if (static_cast<uint32_t>(lane) == j) mine = best;
-                if (!ok) best = 0;
-                const typename K::T gone = best == 0 ? ~typename K::T{0} : best;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const bool taken = key[i] == gone;
-                    key[i] = taken ? 0 : key[i];
-                    cnt[i] += taken ? 1u : 0u;
+                for (uint32_t i = 0; i < kBatch; ++i) {
+                    share += static_cast<double>(sum_of(w[i]));
+                    times += count_of(w[i]);
                 }
             }
-            const bool some = ok && mine != 0;
-            const float w = some ? exp2_f((K::value(mine) - m) * kLog2e) : 0.0f;
-            kept_sum += lanes_sum<G>(w);
-            if (there && static_cast<uint32_t>(lane) < j1) {
-                const bool bad = on && !(s < __builtin_huge_valf());  // NaN or +inf
-                ch[j0 + lane] = some ? static_cast<int64_t>(K::col(mine)) : bad ? -2 : -1;
-                wt[j0 + lane] = bad ? __builtin_nanf("") : renormalize ? w : w * inv;
-                if (!bad && !some) wt[j0 + lane] = 0.0f;
-            }
         }
-        if (renormalize && there && ok) {
-            for (uint32_t j = lane; j < top; j += G) wt[j] = wt[j] / kept_sum;
+        if (teams > 1) {
+            __syncthreads();
+            L.share[threadIdx.x] = share;
+            L.times[threadIdx.x] = times;
+            __syncthreads();
+            if (team == 0)
+                for (uint32_t t = 1; t < teams; ++t) {
+                    share += L.share[t * wide + threadIdx.x];
+                    times += L.times[t * wide + threadIdx.x];
+                }
         }
+        if (team == 0 && c < experts) each(c, share, times);
     }
-    // the workgroup's sums
-    z = lanes_sum<kWave>(z);
-#pragma unroll
-    for (int o = 1; o < kWave; o *= 2) n += __shfl_xor(n, o);
-    if (threadIdx.x % kWave == 0) {
-        s_z[threadIdx.x / kWave] = z;
-        s_n[threadIdx.x / kWave] = n;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        s_sum[team * G * N + col + i] = sum[i];
-        s_cnt[team * G * N + col + i] = cnt[i];
-    }
-    __syncthreads();
-    uint8_t* out = addr<uint8_t>(scratch) + blockIdx.x * partial_bytes(experts);
-    for (uint32_t c = threadIdx.x; c < experts; c += kRouteThreads) {
-        float total = 0.0f;
-        uint32_t times = 0;
-        for (int i = 0; i < kTeams; ++i) {
-            total += s_sum[i * G * N + c];
-            times += s_cnt[i * G * N + c];
-        }
-        reinterpret_cast<float*>(out)[c] = total;
-        reinterpret_cast<uint32_t*>(out)[experts + c] = times;
-    }
-    if (threadIdx.x == 0) {
-        float zs = 0.0f;
-        uint32_t ns = 0;
-        for (int i = 0; i < kRouteThreads / kWave; ++i) {
-            zs += s_z[i];
-            ns += s_n[i];
-        }
-        *reinterpret_cast<Tail*>(out + 8 * static_cast<size_t>(experts)) = Tail{zs, ns};
-    }
+    return {lanes_sum64(static_cast<double>(sum_of(tail))), lanes_sum64(static_cast<double>(count_of(tail)))};
 }
 
 // Totals of all groups, one after another: counts (int64 [groups, experts]), tokens (int64 [groups]),
@@ -259,62 +378,233 @@ struct Totals {
     }
 };
 
-__device__ inline double lanes_sum64(double v) {
-#pragma unroll
-    for (int o = 1; o < kWave; o *= 2) v += __shfl_xor(v, o);
-    return v;
-}
-
-// One workgroup per group adds its partial sums up, in binary64. Tags: experts in scratch, top in totals.
-__global__ __launch_bounds__(kRouteThreads) void k_route_join(uint64_t scratch, uint64_t totals, uint32_t blocks,
-                                                              uint32_t groups) {
-    __shared__ double s_red[3][kRouteThreads / kWave];
-    const uint32_t experts = tag(scratch), top = tag(totals), g = blockIdx.x;
-    const Totals out(addr<uint8_t>(totals), groups, experts);
-    const size_t step = partial_bytes(experts);
-    const uint8_t* part = addr<const uint8_t>(scratch) + static_cast<size_t>(g) * blocks * step;
-    double both = 0.0, z = 0.0, n = 0.0;
-    for (uint32_t c = threadIdx.x; c < experts; c += kRouteThreads) {
-        double share = 0.0;
-        int64_t times = 0;
-        for (uint32_t b = 0; b < blocks; ++b) {
-            share += static_cast<double>(reinterpret_cast<const float*>(part + b * step)[c]);
-            times += reinterpret_cast<const uint32_t*>(part + b * step)[experts + c];
-        }
-        out.counts[static_cast<size_t>(g) * experts + c] = times;
-        both += static_cast<double>(times) * share;
-    }
-    for (uint32_t b = threadIdx.x; b < blocks; b += kRouteThreads) {
-        const Tail t = *reinterpret_cast<const Tail*>(part + b * step + 8 * static_cast<size_t>(experts));
-        z += static_cast<double>(t.z);
-        n += static_cast<double>(t.tokens);
-    }
+// A group's balance, z and tokens: `both` is the thread's share of sum_e c_e sum_t p_te, tail that of thread 0.
+__device__ inline void finish(JoinLds& L, const Totals& out, double both, Tail tail, uint32_t g, uint32_t experts,
+                              uint32_t top) {
     both = lanes_sum64(both);
-    z = lanes_sum64(z);
-    n = lanes_sum64(n);
-    if (threadIdx.x % kWave == 0) {
-        s_red[0][threadIdx.x / kWave] = both;
-        s_red[1][threadIdx.x / kWave] = z;
-        s_red[2][threadIdx.x / kWave] = n;
-    }
+    if (threadIdx.x % kWave == 0) L.red[threadIdx.x / kWave] = both;
     __syncthreads();
     if (threadIdx.x == 0) {
-        both = z = n = 0.0;
-        for (int i = 0; i < kRouteThreads / kWave; ++i) {
-            both += s_red[0][i];
-            z += s_red[1][i];
-            n += s_red[2][i];
-        }
+        both = 0.0;
+        for (int i = 0; i < kRouteThreads / kWave; ++i) both += L.red[i];
+        const double n = tail.tokens;
         out.tokens[g] = static_cast<int64_t>(n);
         out.balance[g] = n > 0.0 ? static_cast<float>(both * experts / (top * n * n)) : 0.0f;
-        out.z[g] = n > 0.0 ? static_cast<float>(z / n) : 0.0f;
+        out.z[g] = n > 0.0 ? static_cast<float>(tail.z / n) : 0.0f;
     }
 }
 
-// Marks an expert that the token has not chosen, among the gradients of weights (a NaN that no
-// arithmetic gives; a gradient of these very bits is read as the ordinary NaN).
-constexpr uint32_t kNotChosen = 0xffffffffu;
+// G lanes per token, NV vectors each: vector v of the token in lane v % G. L: the length of the lists that
+// are merged (2 or 8), or 0 for more choices than that, which are taken one by one.
+// Tags: experts in x, top (and 0x8000: renormalize) in live, workgroups per group in weights, nonce in
+// (chosen, scratch).
+template <typename Fmt, int G, int NV, int L>
+__global__ __launch_bounds__(kRouteThreads) void k_route(uint64_t x, uint64_t live_, uint64_t weights,
+                                                         uint64_t chosen, uint64_t scratch, uint64_t totals,
+                                                         uint32_t stride, uint32_t tokens) {
+    constexpr int VW = Fmt::VW, N = NV * VW, kTeams = kRouteThreads / G, kWaves = kRouteThreads / kWave;
+    using K = Key<Fmt>;
+    using T = typename K::T;
+    __shared__ float s_sum[kWaves][G * N];
+    __shared__ uint32_t s_cnt[G * N];
+    __shared__ float s_z[kWaves];
+    __shared__ uint32_t s_n[kWaves];
+    __shared__ uint32_t s_found;
+    __shared__ JoinLds s_join;
+    const uint32_t experts = tag(x), top = tag(live_) & 0x7fffu, blocks = tag(weights);
+    const bool renormalize = (tag(live_) & 0x8000u) != 0;
+    const uint32_t g = blockIdx.x / blocks, b = blockIdx.x - g * blocks;
+    const uint32_t per = (tokens + blocks - 1) / blocks;
+    const uint32_t t0 = b * per < tokens ? b * per : tokens;
+    const uint32_t t1 = tokens - t0 < per ? tokens : t0 + per;
+    const uint32_t team = threadIdx.x / G;
+    const int lane = threadIdx.x % G;
+    const uint8_t* live = addr<const uint8_t>(live_);
+    const Group group(addr<uint8_t>(scratch), g, experts, blocks);
+    const uint64_t generation = blocks > 1 ? load_part(group.generation) : 0;
+    for (int i = threadIdx.x; i < G * N; i += kRouteThreads) s_cnt[i] = 0;
+    __syncthreads();
+    float sum[N], z = 0.0f;
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = 0.0f;
+    // the next token's logits and the one after's `live` are on their way while a token is worked on
+    const auto is_live = [&](uint32_t t) {
+        return t < t1 && (live == nullptr || live[static_cast<size_t>(g) * tokens + t] != 0);
+    };
+    const auto load = [&](uint32_t t, bool on, typename Fmt::Vec(&to)[NV]) {
+        const uint8_t* row = addr<const uint8_t>(x) + (static_cast<size_t>(g) * tokens + t) * stride * Fmt::kSize;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) to[v] = masked16<Fmt>();
+        if (on) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) to[v] = load_cols<Fmt>(row, (v * G + lane) * VW, experts);
+        }
+    };
+    typename Fmt::Vec next[NV];
+    load(t0 + team, is_live(t0 + team), next);
+    bool next_on = is_live(t0 + team + kTeams);
+    for (uint32_t base = t0; base < t1; base += kTeams) {
+        const uint32_t t = base + team;
+        const size_t r = static_cast<size_t>(g) * tokens + t;
+        const bool there = t < t1;
+        typename Fmt::Vec q[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) q[v] = next[v];
+        load(t + kTeams, next_on, next);
+        next_on = is_live(t + 2 * kTeams);
+        float e[N];
+        T key[N];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float f[VW];
+            T k[VW];
+            Fmt::unpack(q[v], f);
+            K::make(__builtin_bit_cast(u32x4, q[v]), (v * G + lane) * VW, k);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                e[v * VW + i] = f[i];
+                key[v * VW + i] = k[i];
+            }
+        }
+        float m, s;
+        softmax<G, N>(e, m, s);
+        const bool ok = s > 0.0f && s < __builtin_huge_valf();
+        const bool bad = !(s < __builtin_huge_valf());  // NaN or +inf
+        const float inv = 1.0f / s;
+        if (s != 0.0f) {  // else left out, or every logit is -inf
+            const float lse = fmaf(log2_f(s), kLn2, m);
+            if (lane == 0) {
+                z = fmaf(lse, lse, z);
+                ++n;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) sum[i] = fmaf(e[i], inv, sum[i]);
+        }
+        float* wt = addr<float>(weights) + r * top;
+        int64_t* ch = addr<int64_t>(chosen) + r * top;
+        // lane j % G stores choice j
+        const auto store = [&](uint32_t j, T k, float w, bool some) {
+            ch[j] = some ? static_cast<int64_t>(K::col(k)) : bad ? -2 : -1;
+            wt[j] = bad ? __builtin_nanf("") : w;
+            if (some) atomicAdd(&s_cnt[K::col(k)], 1u);
+        };
+        if constexpr (L > 0) {
+            constexpr int kRounds = (L + G - 1) / G;
+            T best[L];
+            best_of_lane<K, L, N>(key, best);
+            best_of_lanes<K, G, L>(best);
+            T mine[kRounds];
+            float w[kRounds], kept = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kRounds; ++c) {
+                mine[c] = K::kNone;
+#pragma unroll
+                for (int i = c * G; i < L && i < (c + 1) * G; ++i) mine[c] = lane == i - c * G ? best[i] : mine[c];
+                const bool some = ok && mine[c] >= K::kSome && static_cast<uint32_t>(c * G + lane) < top;
+                w[c] = some ? exp2_f((K::value(mine[c]) - m) * kLog2e) : 0.0f;
+                kept += w[c];
+            }
+            const float scale = renormalize ? 1.0f / lanes_sum<G>(kept) : inv;
+#pragma unroll
+            for (int c = 0; c < kRounds; ++c) {
+                const uint32_t j = c * G + lane;
+                if (there && j < top) store(j, mine[c], ok ? w[c] * scale : 0.0f, ok && mine[c] >= K::kSome);
+            }
+        } else {
+            float kept = 0.0f;
+            for (uint32_t j0 = 0; j0 < top; j0 += G) {
+                T mine = K::kNone;
+                const uint32_t j1 = top - j0 < G ? top - j0 : G;
+                for (uint32_t j = 0; j < j1; ++j) {
+                    T best = key[0];
+#pragma unroll
+                    for (int i = 1; i < N; ++i) best = K::max(best, key[i]);
+                    best = lanes_best<K, G>(best);
+                    if (static_cast<uint32_t>(lane) == j) mine = best;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) key[i] = key[i] == best ? K::kNone : key[i];
+                }
+                const bool some = ok && mine >= K::kSome;
+                const float w = some ? exp2_f((K::value(mine) - m) * kLog2e) : 0.0f;
+                kept += w;
+                if (there && static_cast<uint32_t>(lane) < j1) store(j0 + lane, mine, some ? w * (renormalize ? 1.0f : inv) : 0.0f, some);
+            }
+            kept = lanes_sum<G>(kept);
+            if (renormalize && there && ok)
+                for (uint32_t j = lane; j < top; j += G) wt[j] = wt[j] / kept;
+        }
+    }
+    // the workgroup's sums: of a wavefront's teams by lanes, then of the wavefronts
+    const int wave = threadIdx.x / kWave;
+    z = lanes_sum<kWave>(z);
+#pragma unroll
+    for (int o = 1; o < kWave; o *= 2) n += __shfl_xor(n, o);
+    if (threadIdx.x % kWave == 0) {
+        s_z[wave] = z;
+        s_n[wave] = n;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            float t = sum[v * VW + i];
+#pragma unroll
+            for (int o = G; o < kWave; o *= 2) t += __shfl_xor(t, o);
+            if (threadIdx.x % kWave < G) s_sum[wave][(v * G + lane) * VW + i] = t;
+        }
+    __syncthreads();
+    const Totals out(addr<uint8_t>(totals), gridDim.x / blocks, experts);
+    uint64_t* part = group.partials + static_cast<size_t>(b) * (experts + 1);
+    int64_t* counts = out.counts + static_cast<size_t>(g) * experts;
+    double both = 0.0;
+    for (uint32_t c = threadIdx.x; c < experts; c += kRouteThreads) {
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) total += s_sum[i][c];
+        const uint32_t times = s_cnt[c];
+        if (blocks == 1) {  // nothing to join
+            counts[c] = times;
+            both += static_cast<double>(times) * static_cast<double>(total);
+        } else {
+            store_part(part + c, word(total, times));
+        }
+    }
+    float zs = 0.0f;
+    uint32_t ns = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        zs += s_z[i];
+        ns += s_n[i];
+    }
+    if (blocks == 1) return finish(s_join, out, both, {zs, static_cast<double>(ns)}, g, experts, top);
+    if (threadIdx.x == 0) store_part(part + experts, word(zs, ns));
+    const uint64_t launch_tag = arrival_tag(tags(chosen, scratch), generation);
+    const uint32_t set = b / kRouteSet, sets = Group::sets(blocks), from = set * kRouteSet;
+    const uint32_t many = blocks - from < kRouteSet ? blocks - from : kRouteSet;
+    if (!arrive(group.slots + from, group.owners + set, b - from, many, launch_tag, &s_found)) return;
+    const uint64_t* ours = group.partials + static_cast<size_t>(from) * (experts + 1);
+    uint32_t last = many;
+    if (sets > 1) {
+        uint64_t* to = group.set_partials + static_cast<size_t>(set) * (experts + 1);
+        const Tail tail = add_up(s_join, ours, many, experts, [&](uint32_t c, double share, uint32_t times) {
+            store_part(to + c, word(static_cast<float>(share), times));
+        });
+        if (threadIdx.x == 0) store_part(to + experts, word(static_cast<float>(tail.z), static_cast<uint32_t>(tail.tokens)));
+        if (!arrive(group.set_slots, group.last, set, sets, launch_tag, &s_found)) return;
+        ours = group.set_partials;
+        last = sets;
+    }
+    const Tail tail = add_up(s_join, ours, last, experts, [&](uint32_t c, double share, uint32_t times) {
+        counts[c] = times;
+        both += static_cast<double>(times) * share;
+    });
+    finish(s_join, out, both, tail, g, experts, top);
+    if (threadIdx.x == 0) store_part(group.generation, generation + 1);
+}
 
+// A row is read once and kept; what the chosen experts' weights add lies in LDS, one value per expert, 0 for
+// the others: dx_j = p_j (per_balance c_j + each + add_j).
 // Tags: experts in x, top (and 0x8000: renormalize) in chosen, blocks per group in totals, tokens in
 // (g_weights, g_balance), row stride in (g_z, grad). g_weights, g_balance and g_z may be null.
 template <typename Fmt, int G, int NV>
@@ -322,7 +612,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(uint64_t x, uint64
                                                               uint64_t g_weights, uint64_t g_balance,
                                                               uint64_t g_z, uint64_t grad) {
     constexpr int VW = Fmt::VW, N = NV * VW, kTeams = kRouteThreads / G;
-    __shared__ uint32_t s_gw[kTeams * G * N];
+    __shared__ float s_add[kTeams][G * N];
     const uint32_t experts = tag(x), top = tag(chosen) & 0x7fffu, blocks = tag(totals);
     const bool renormalize = (tag(chosen) & 0x8000u) != 0;
     const uint32_t tokens = tags(g_weights, g_balance), stride = tags(g_z, grad);
@@ -333,7 +623,6 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(uint64_t x, uint64
     const uint32_t t1 = tokens - t0 < per ? tokens : t0 + per;
     const uint32_t team = threadIdx.x / G;
     const int lane = threadIdx.x % G;
-    const uint32_t col = lane * N;
     const Totals tot(addr<uint8_t>(totals), groups, experts);
     const double n = static_cast<double>(tot.tokens[g]);
     const float* gb = addr<const float>(g_balance);
@@ -343,121 +632,139 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_grad(uint64_t x, uint64
         gb != nullptr && n > 0.0 ? static_cast<float>(gb[g] * static_cast<double>(experts) / (top * n * n)) : 0.0f;
     const float per_z = gz != nullptr && n > 0.0 ? static_cast<float>(2.0 * gz[g] / n) : 0.0f;
     float c[N];
+    float* mine = s_add[team];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        c[i] = col + i < experts ? static_cast<float>(tot.counts[static_cast<size_t>(g) * experts + col + i]) : 0.0f;
-        s_gw[team * G * N + col + i] = kNotChosen;
+        const uint32_t col = (i / VW * G + lane) * VW + i % VW;
+        c[i] = col < experts ? static_cast<float>(tot.counts[static_cast<size_t>(g) * experts + col]) : 0.0f;
+        mine[col] = 0.0f;
     }
-    uint32_t* mine = s_gw + team * G * N;
+    team_sync<kWave>();
     for (uint32_t base = t0; base < t1; base += kTeams) {
         const uint32_t t = base + team;
         const size_t r = static_cast<size_t>(g) * tokens + t;
         const bool there = t < t1;
         const int64_t* ch = addr<const int64_t>(chosen) + r * top;
-        const bool on = there && ch[0] != -1;  // left out, or every logit -inf
+        const bool on = there && ch[0] != -1;  // else left out, or every logit is -inf
+        const uint8_t* row = addr<const uint8_t>(x) + r * stride * Fmt::kSize;
         float e[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) e[i] = -__builtin_huge_valf();
-        if (on) load_cols<Fmt, NV>(addr<const uint8_t>(x) + r * stride * Fmt::kSize, col, experts, e);
-        if (on && gw != nullptr) {
-            for (uint32_t j = lane; j < top; j += G) {
-                const uint64_t at = static_cast<uint64_t>(ch[j]);
-                const uint32_t v = __float_as_uint(gw[r * top + j]);
-                if (at < experts) mine[at] = v == kNotChosen ? 0x7fc00000u : v;
+        if (on) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                float f[VW];
+                Fmt::unpack(load_cols<Fmt>(row, (v * G + lane) * VW, experts), f);
+#pragma unroll
+                for (int i = 0; i < VW; ++i) e[v * VW + i] = f[i];
             }
         }
         float m, s;
         softmax<G, N>(e, m, s);
         const float inv = 1.0f / s, lse = fmaf(log2_f(s), kLn2, m);
-        team_sync<kWave>();
-        float even = 0.0f, inside = 0.0f, kept = 0.0f, w[N];
-        bool of[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            e[i] *= inv;
-            even = fmaf(c[i], e[i], even);
-            const uint32_t v = mine[col + i];
-            of[i] = v != kNotChosen;
-            w[i] = of[i] ? __uint_as_float(v) : 0.0f;
-            if (of[i]) {
-                inside = fmaf(w[i], e[i], inside);
-                kept += e[i];
-            }
-        }
-        even = lanes_sum<G>(even);
-        inside = lanes_sum<G>(inside);
-        kept = lanes_sum<G>(kept);
-        team_sync<kWave>();
-        if (on && gw != nullptr) {
-            for (uint32_t j = lane; j < top; j += G) {
+        // the chosen: lane j % G has choice j
+        float inside = 0.0f, by = 1.0f, less = 0.0f;
+        if (gw != nullptr) {
+            float kept = 0.0f;
+            for (uint32_t j = lane; on && j < top; j += G) {
                 const uint64_t at = static_cast<uint64_t>(ch[j]);
-                if (at < experts) mine[at] = kNotChosen;
+                const float p = at < experts ? exp2_f((Fmt::load1(row + at * Fmt::kSize) - m) * kLog2e) * inv : 0.0f;
+                kept += p;
+                inside = at < experts ? fmaf(gw[r * top + j], p, inside) : inside;
+            }
+            inside = lanes_sum<G>(inside);
+            if (renormalize) {
+                by = 1.0f / lanes_sum<G>(kept);
+                less = inside * by;
+                inside = 0.0f;
+            }
+            for (uint32_t j = lane; on && j < top; j += G) {
+                const uint64_t at = static_cast<uint64_t>(ch[j]);
+                if (at < experts) mine[at] = (gw[r * top + j] - less) * by;
+            }
+            team_sync<kWave>();
+        }
+        float even = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) even = fmaf(c[i], e[i], even);
+        even = lanes_sum<G>(even) * inv;
+        const float each = fmaf(per_z, lse, -per_balance * even) - inside;
+        uint8_t* out = addr<uint8_t>(grad) + r * experts * Fmt::kSize;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const uint32_t col = (v * G + lane) * VW;
+            float f[VW];
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                const int k = v * VW + i;
+                const float d = e[k] * inv * (fmaf(per_balance, c[k], each) + mine[col + i]);
+                f[i] = on ? d : 0.0f;
+            }
+            if (!there) continue;
+            if (col + VW <= experts) {
+                store16_any<Fmt>(out + static_cast<size_t>(col) * Fmt::kSize, pack<Fmt>(f));
+            } else {
+#pragma unroll
+                for (int i = 0; i < VW; ++i)
+                    if (col + i < experts) reinterpret_cast<typename Fmt::Bits*>(out)[col + i] = round_to<Fmt>(f[i]);
             }
         }
-        const float each = fmaf(per_z, lse, -per_balance * even) - (renormalize ? 0.0f : inside);
-        const float by = renormalize ? 1.0f / kept : 1.0f, less = renormalize ? inside * by : 0.0f;
-        float d[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            d[i] = e[i] * fmaf(per_balance, c[i], each);
-            if (of[i]) d[i] = fmaf(e[i] * by, w[i] - less, d[i]);
-            if (!on) d[i] = 0.0f;
-        }
-        if (there) {
-            uint8_t* out = addr<uint8_t>(grad) + r * experts * Fmt::kSize;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const uint32_t at = col + v * VW;
-                float f[VW];
-#pragma unroll
-                for (int i = 0; i < VW; ++i) f[i] = d[v * VW + i];
-                if (at + VW <= experts) {
-                    store16_any<Fmt>(out + static_cast<size_t>(at) * Fmt::kSize, pack<Fmt>(f));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VW; ++i)
-                        if (at + i < experts)
-                            reinterpret_cast<typename Fmt::Bits*>(out)[at + i] = round_to<Fmt>(f[i]);
-                }
+        if (gw != nullptr) {
+            team_sync<kWave>();
+            for (uint32_t j = lane; on && j < top; j += G) {
+                const uint64_t at = static_cast<uint64_t>(ch[j]);
+                if (at < experts) mine[at] = 0.0f;
             }
+            team_sync<kWave>();
         }
     }
 }
 
-// f(lanes, vectors per lane) of a plan: 16-bit formats have at most two vectors per lane.
+// f(lanes, vectors per lane) of a plan.
 template <typename Fmt, typename F>
 void with_lanes(const RoutePlan& p, F f) {
-    if constexpr (Fmt::VW == 4)
-        if (p.vecs == 4) return f(Int<64>{}, Int<4>{});
-    if (p.vecs == 2) return f(Int<64>{}, Int<2>{});
-    switch (p.lanes) {
-        case 1: return f(Int<1>{}, Int<1>{});
-        case 2: return f(Int<2>{}, Int<1>{});
-        case 4: return f(Int<4>{}, Int<1>{});
-        case 8: return f(Int<8>{}, Int<1>{});
-        case 16: return f(Int<16>{}, Int<1>{});
-        case 32: return f(Int<32>{}, Int<1>{});
-        default: return f(Int<64>{}, Int<1>{});
+    switch (p.lanes * 8 + p.vecs) {
+        case 1 * 8 + 1: return f(Int<1>{}, Int<1>{});
+        case 2 * 8 + 1: return f(Int<2>{}, Int<1>{});
+        case 4 * 8 + 1: return f(Int<4>{}, Int<1>{});
+        case 8 * 8 + 1: return f(Int<8>{}, Int<1>{});
+        case 16 * 8 + 1: return f(Int<16>{}, Int<1>{});
+        case 8 * 8 + 2: return f(Int<8>{}, Int<2>{});
+        case 16 * 8 + 2: return f(Int<16>{}, Int<2>{});
+        case 8 * 8 + 4: return f(Int<8>{}, Int<4>{});
+        case 16 * 8 + 4: return f(Int<16>{}, Int<4>{});
+        case 32 * 8 + 4: return f(Int<32>{}, Int<4>{});
+        case 64 * 8 + 4:
+            if constexpr (Fmt::VW == 4) return f(Int<64>{}, Int<4>{});
     }
 }
 
 }  // namespace
 
-size_t route_partial_bytes(int64_t experts) { return partial_bytes(static_cast<uint32_t>(experts)); }
+size_t route_group_bytes(int64_t experts, int blocks) {
+    return 8 * Group::words(static_cast<uint32_t>(experts), static_cast<uint32_t>(blocks));
+}
 
 hipError_t launch_route(const RoutePlan& plan, const RouteArgs& a, const uint8_t* live, float* weights,
                         int64_t* chosen, uint8_t* totals, uint8_t* scratch16, hipStream_t s) {
-    const uint32_t groups = static_cast<uint32_t>(a.groups);
+    const uint32_t nonce = next_nonce();
     with_format(a.dtype, [&](auto fmt) {
         with_lanes<decltype(fmt)>(plan, [&](auto lanes, auto vecs) {
-            launch(k_route<decltype(fmt), decltype(lanes)::value, decltype(vecs)::value>,
-                   static_cast<uint32_t>(plan.grid_blocks), kRouteThreads, s, tagged(a.x, a.experts),
-                   tagged(live, a.top), tagged(weights, plan.blocks), tagged(chosen, a.renormalize),
-                   tagged(scratch16, 0), static_cast<uint32_t>(a.row_stride), static_cast<uint32_t>(a.tokens));
+            const auto go = [&](auto list) {
+                launch(k_route<decltype(fmt), decltype(lanes)::value, decltype(vecs)::value, decltype(list)::value>,
+                       static_cast<uint32_t>(plan.grid_blocks), kRouteThreads, s, tagged(a.x, a.experts),
+                       tagged(live, a.top | (a.renormalize ? 0x8000 : 0)), tagged(weights, plan.blocks),
+                       tagged(chosen, nonce), tagged(scratch16, nonce >> 16), tagged(totals, 0),
+                       static_cast<uint32_t>(a.row_stride), static_cast<uint32_t>(a.tokens));
+            };
+            if (a.top <= 2)
+                go(Int<2>{});
+            else if (a.top <= 8)
+                go(Int<8>{});
+            else
+                go(Int<0>{});
         });
     });
-    launch(k_route_join, groups, kRouteThreads, s, tagged(scratch16, a.experts), tagged(totals, a.top),
-           static_cast<uint32_t>(plan.blocks), groups);
     return hipGetLastError();
 }
 

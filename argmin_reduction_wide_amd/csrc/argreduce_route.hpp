@@ -13,6 +13,9 @@ namespace argreduce {
 constexpr int kExpertsMax = 1024;  // experts of a router (ARGREDUCE_EXPERTS_MAX)
 constexpr int kRouteTopMax = 64;   // experts chosen per token (ARGREDUCE_ROUTE_TOP_MAX)
 
+constexpr int kRouteThreads = 256;  // of a workgroup
+constexpr uint32_t kRouteSet = 64;  // workgroups whose sums one of them adds up
+
 // A token's logits lie in `lanes` lanes of a wavefront, `vecs` vectors of 16 bytes each.
 struct RoutePlan {
     int lanes, vecs;
@@ -29,6 +32,8 @@ struct RouteArgs {
     int top;
     bool renormalize;
 };
+
+size_t route_group_bytes(int64_t experts, int blocks);  // scratch of one group
 
 hipError_t launch_route(const RoutePlan& plan, const RouteArgs& a, const uint8_t* live, float* weights,
                         int64_t* chosen, uint8_t* totals, uint8_t* scratch16, hipStream_t stream);

@@ -7,8 +7,6 @@
 
 namespace argreduce {
 
-size_t route_partial_bytes(int64_t experts);  // scratch of one workgroup
-
 namespace {
 
 int check_route(int dtype, int64_t groups, int64_t tokens, int64_t experts) {
@@ -21,7 +19,19 @@ int check_route(int dtype, int64_t groups, int64_t tokens, int64_t experts) {
     return ARGREDUCE_OK;
 }
 
-int make_route_plan(int dtype, int64_t groups, int64_t tokens, int64_t experts, RoutePlan* p) {
+// Tokens up to this many (of all groups) take up to 16 lanes each, more of them up to 8, as long as a lane has no
+// more than four vectors. Forward and gradient of [16,4096,256] bf16 with 8 experts per token, us: 8 lanes 27.3 and
+// 23.6, 16 lanes 29.0 and 23.2, 32 lanes 42.6 and 30.5; [16,4096,128] 18.6 and 15.3, 22.2 and 17.7; [16,4096,64]
+// f16 with 2 (8 vectors) 12.0 by 8 lanes, 13.0 by 4, 15.9 by 2; but [1,300,256] 11.2 and 8.1 by 8, 9.6 and 5.6 by 16.
+constexpr int64_t kFewTokens = 4096;
+// Workgroups per CU, of all groups together: forward 2 ([16,4096,256] 27.3 us, with 3 of them 30.4, with 4
+// 33.8: more sums to join), gradient 4 ([16,4096,64] f16 11.4, with 2 14.5).
+constexpr int64_t kForwardPerCu = 2, kGradPerCu = 4;
+// Tokens of a group that one workgroup goes through by itself, in rounds: nothing to join then ([1,32,256] bf16
+// 6.1 us, with four workgroups 7.8).
+constexpr int64_t kAloneRounds = 4;
+
+int make_route_plan(int dtype, int64_t groups, int64_t tokens, int64_t experts, bool grad, RoutePlan* p) {
     int rc = check_route(dtype, groups, tokens, experts);
     if (rc != ARGREDUCE_OK) return rc;
     int64_t cap = 0;
@@ -29,16 +39,19 @@ int make_route_plan(int dtype, int64_t groups, int64_t tokens, int64_t experts, 
     if (rc != ARGREDUCE_OK) return rc;
     *p = RoutePlan{};
     p->device_threads = cap;
-    const int64_t vw = 16 / logits_elem_size(dtype);
-    const int64_t vecs = ceil_div(experts, vw);
-    p->lanes = static_cast<int>(std::min<int64_t>(64, next_pow2(vecs)));
-    p->vecs = static_cast<int>(next_pow2(ceil_div(vecs, 64)));
-    // Two workgroups per CU, or as many as the tokens fill; several of one group's.
-    const int64_t groups1 = std::max<int64_t>(1, groups), at_once = kBlock / p->lanes;
-    const int64_t most = std::max<int64_t>(1, 2 * (cap / kThreadsPerCu) / groups1);
-    p->blocks = static_cast<int>(std::max<int64_t>(1, std::min({ceil_div(tokens, at_once), most, int64_t{65535}})));
+    const int64_t vecs = ceil_div(experts, 16 / logits_elem_size(dtype));
+    const int64_t lanes = groups * tokens <= kFewTokens ? 16 : 8;
+    p->vecs = static_cast<int>(std::min<int64_t>(4, next_pow2(ceil_div(vecs, lanes))));
+    p->lanes = static_cast<int>(next_pow2(ceil_div(vecs, p->vecs)));
+    const int64_t groups1 = std::max<int64_t>(1, groups), at_once = kRouteThreads / p->lanes;
+    const int64_t per_cu = grad ? kGradPerCu : kForwardPerCu;
+    const int64_t most = std::max<int64_t>(1, per_cu * (cap / kThreadsPerCu) / groups1);
+    int64_t blocks = std::min({ceil_div(tokens, at_once), most, int64_t{kRouteSet * kRouteSet}});
+    if (blocks < 1 || (!grad && tokens <= at_once * kAloneRounds)) blocks = 1;
+    p->blocks = static_cast<int>(blocks);
     p->grid_blocks = groups1 * p->blocks;
-    p->scratch_bytes = 15 + static_cast<size_t>(p->grid_blocks) * route_partial_bytes(experts);
+    if (!grad)
+        p->scratch_bytes = blocks == 1 ? 0 : 15 + static_cast<size_t>(groups1) * route_group_bytes(experts, p->blocks);
     return grid_too_large(p->grid_blocks, kBlock) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
 }
 
@@ -63,7 +76,7 @@ using namespace argreduce;
 ARGREDUCE_EXPORT size_t argreduce_route_scratch_bytes(int64_t groups, int64_t tokens, int64_t experts,
                                                       argreduce_dtype_t dtype) {
     RoutePlan p;
-    return make_route_plan(dtype, groups, tokens, experts, &p) == ARGREDUCE_OK
+    return make_route_plan(dtype, groups, tokens, experts, false, &p) == ARGREDUCE_OK
                ? p.scratch_bytes
                : std::numeric_limits<size_t>::max();
 }
@@ -72,7 +85,7 @@ ARGREDUCE_EXPORT int argreduce_route_plan(int64_t groups, int64_t tokens, int64_
                                           argreduce_plan_t* out) {
     if (out == nullptr) return ARGREDUCE_ERR_INVALID_ARG;
     RoutePlan p;
-    const int rc = make_route_plan(dtype, groups, tokens, experts, &p);
+    const int rc = make_route_plan(dtype, groups, tokens, experts, false, &p);
     if (rc != ARGREDUCE_OK) return rc;
     *out = argreduce_plan_t{};
     out->path = ARGREDUCE_PATH_SUBWAVE;
@@ -86,7 +99,7 @@ ARGREDUCE_EXPORT int argreduce_route_plan(int64_t groups, int64_t tokens, int64_
     out->device_threads = p.device_threads;
     out->scratch_bytes = p.scratch_bytes;
     out->load_bytes = 16;
-    out->dispatches = 2;
+    out->dispatches = 1;
     return ARGREDUCE_OK;
 }
 
@@ -108,7 +121,7 @@ ARGREDUCE_EXPORT int argreduce_route(const void* x, argreduce_dtype_t dtype, int
     if (!usable(totals, 8) || !fits48(live)) return ARGREDUCE_ERR_INVALID_ARG;
     if (tokens > 0 && (!usable(weights, 4) || !usable(chosen, 8))) return ARGREDUCE_ERR_INVALID_ARG;
     RoutePlan p;
-    rc = make_route_plan(dtype, groups, tokens, experts, &p);
+    rc = make_route_plan(dtype, groups, tokens, experts, false, &p);
     if (rc != ARGREDUCE_OK) return rc;
     uint8_t* scratch16 = nullptr;
     rc = scratch_of(p.scratch_bytes, scratch, scratch_bytes, &scratch16);
@@ -131,7 +144,7 @@ ARGREDUCE_EXPORT int argreduce_route_grad(const void* x, argreduce_dtype_t dtype
         !optional(g_z) || !usable(grad, static_cast<uintptr_t>(logits_elem_size(dtype))))
         return ARGREDUCE_ERR_INVALID_ARG;
     RoutePlan p;
-    rc = make_route_plan(dtype, groups, tokens, experts, &p);
+    rc = make_route_plan(dtype, groups, tokens, experts, true, &p);
     if (rc != ARGREDUCE_OK) return rc;
     return status_of(launch_route_grad(p, a, chosen, static_cast<const uint8_t*>(totals), g_weights, g_balance,
                                        g_z, grad, static_cast<hipStream_t>(stream)));

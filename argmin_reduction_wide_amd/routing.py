@@ -70,12 +70,15 @@ def _route(logits, top, live, renormalize, scratch) -> RouteExperts:
     if device.index != _device():
         with torch.cuda.device(device):
             return _route(logits, top, live, renormalize, scratch)
-    weights = torch.empty(*lead, tokens, top, dtype=_F32, device=device)
-    chosen = torch.empty(*lead, tokens, top, dtype=_I64, device=device)
+    shape = lead + (tokens, top)
+    weights = torch.empty(shape, dtype=_F32, device=device)
+    chosen = torch.empty(shape, dtype=_I64, device=device)
     # counts, tokens (8 bytes each), balance and z (4 each), one after another
     totals = torch.empty(groups * (experts + 2), dtype=_I64, device=device)
     need = _call.route_scratch_bytes(groups, tokens, experts, code)
-    sptr, sbytes, scratch = _scratch(need, "argreduce_route", scratch, device)
+    sptr = sbytes = 0
+    if need or scratch is not None:
+        sptr, sbytes, scratch = _scratch(need, "argreduce_route", scratch, device)
     rc = _call.route(logits.data_ptr(), code, groups, tokens, experts, stride,
                      0 if live is None else live.data_ptr(), top, bool(renormalize), weights.data_ptr(),
                      chosen.data_ptr(), totals.data_ptr(), sptr, sbytes, _stream(device.index))
@@ -89,10 +92,13 @@ def _route(logits, top, live, renormalize, scratch) -> RouteExperts:
 def _totals(totals, groups, experts, lead):
     """The four parts of totals, in the logits' leading shape."""
     n = groups * experts
-    counts = totals[:n].view(*lead, experts)
-    number = totals[n:n + groups].view(lead)
-    losses = totals[n + groups:].view(_F32)
-    return counts, number, losses[:groups].view(lead), losses[groups:].view(lead)
+    losses = totals.view(_F32)
+    if len(lead) == 1:  # (views by strides are the cheapest ones)
+        one = (1,)
+        return (totals.as_strided((groups, experts), (experts, 1)), totals.as_strided(lead, one, n),
+                losses.as_strided(lead, one, 2 * (n + groups)), losses.as_strided(lead, one, 2 * n + 3 * groups))
+    return (totals[:n].view(*lead, experts), totals[n:n + groups].view(lead),
+            losses[2 * (n + groups):][:groups].view(lead), losses[2 * n + 3 * groups:].view(lead))
 
 
 class _RouteExperts(torch.autograd.Function):
