@@ -83,7 +83,9 @@ def beam_step(logits, scores, width: Optional[int] = None, *, temperature: float
     # parents, tokens (8 bytes each), scores (4) and ended (1), one after another
     out = torch.empty(2 * n + (5 * n + 7) // 8, dtype=_I64, device=device)
     need = _call.beam_scratch_bytes(groups, beams, cols, code, width)
-    sptr, sbytes, scratch = _scratch(need, "argreduce_beam_step", scratch, device)
+    sptr = sbytes = 0
+    if need or scratch is not None:
+        sptr, sbytes, scratch = _scratch(need, "argreduce_beam_step", scratch, device)
     rc = _call.beam_step(logits.data_ptr(), code, groups, beams, cols, stride, scores.data_ptr(), ended_ptr,
                          end, temperature, width, out.data_ptr(), sptr, sbytes, _stream(device.index))
     if rc:

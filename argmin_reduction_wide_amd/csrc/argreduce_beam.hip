@@ -20,6 +20,7 @@
 #include <hip/hip_runtime.h>
 
 #include "argreduce_beam.hpp"
+#include "argreduce_launch.hpp"
 #include "argreduce_logits_device.hpp"
 
 #pragma clang fp contract(off)
@@ -29,61 +30,16 @@ namespace {
 
 constexpr double kLn2d = 0.693147180559945309417;
 
-// What a slice leaves in scratch, before its list of candidates (keys of key_of, best first).
-struct Slice {
-    float m, s, h;
-    uint32_t count;
-};
-
 __device__ inline bool alive(float score) { return score > -__builtin_huge_valf() && score < __builtin_huge_valf(); }
 
-// One slice of a row per team. [2048,128256] bf16: bound by the read, like the log probabilities
-// with alternatives.
-// Tags: columns in (x, scores), slices per row in ended, width in scratch.
-template <typename Fmt, int T>
-__global__ __launch_bounds__(kTeamBlock<T>) void k_beam_scan(uint64_t x, uint64_t scores_, uint64_t ended_,
-                                                             uint64_t scratch, uint32_t stride,
-                                                             uint32_t slices, float scale) {
-    constexpr int kTeams = kTeamsPerBlock<T>;
-    constexpr int U = kUnroll<Fmt, true>;
-    __shared__ float sh[T / kWave][kShared];
-    __shared__ TopLds<T, kSegs<T>> lds[kTeams];
-    const uint32_t cols = tags(x, scores_), parts = tag(ended_), k = tag(scratch);
-    const uint32_t team = team_of<T>();
-    const uint32_t at = blockIdx.x * kTeams + team;
-    const int lane = lane_of<T>();
-    if (at >= slices) return;  // whole teams, and never one of several wavefronts
-    const uint32_t r = at / parts, b = at - r * parts;
-    const uint8_t* ended = addr<const uint8_t>(ended_);
-    if (!alive(addr<const float>(scores_)[r]) || (ended != nullptr && ended[r] != 0)) return;
-    const RowSpan<Fmt> sp(row_ptr<Fmt>(addr<const void>(x), r, stride), cols);
-    const uint32_t n = part_vecs(span_max<Fmt>(cols), parts);
-    uint32_t first = sp.va + b * n;
-    first = first < sp.vb ? first : sp.vb;
-    const uint32_t last = sp.vb - first < n ? sp.vb : first + n;
-    auto& L = lds[team];
-    const Segments g = Segments::cut<T, U>(first, last, kSegs<T>);
-    Stat a;
-    scan_span<Fmt, true, T, U, true>(sp, b == 0, first, last, lane, scale, a, g, L.seg);
-    team_merge<true, T>(a, scale, lane, sh);
-    Slice* slice = addr<Slice>(scratch) + at;
-    uint64_t* list = reinterpret_cast<uint64_t*>(addr<Slice>(scratch) + slices) + static_cast<size_t>(at) * k;
-    uint32_t count = 0;
-    if (a.s > 0.0f) {  // not only masked logits, and neither NaN nor +inf
-        top_select<Fmt, T, kSegs<T>>(L, sp, g.count(), g.lg_vecs, k, lane,
-                                     [&](uint32_t s, uint32_t i) { return g.vec(s, i); }, b == 0);
-        count = L.count;
-        if (static_cast<uint32_t>(lane) < count) list[lane] = L.buf[lane];
-    }
-    if (lane == 0) *slice = Slice{a.m, a.s, a.h, count};
+// The sum over groups of 2^lg lanes, lg <= 4 and the same in all lanes.
+__device__ inline uint32_t lanes_sum_u32(uint32_t v, uint32_t lg) {
+    if (lg >= 1) v += dpp_u32<0xB1, 0xf>(v);
+    if (lg >= 2) v += dpp_u32<0x4E, 0xf>(v);
+    if (lg >= 3) v += dpp_u32<0x141, 0xf>(v);
+    if (lg >= 4) v += dpp_u32<0x140, 0xf>(v);
+    return v;
 }
-
-// ---------------------------------------------------------------------------------------
-// A slice that its workgroup holds in registers: the best of each wavefront by itself, then of the four.
-
-constexpr int kSliceWaves = kSliceThreads / kWave;
-constexpr int kWaveCap = 256;  // keys that a wavefront collects
-static_assert(kWaveCap >= kBeamMax, "the k best fit");
 
 // Lanes before this one in a mask.
 __device__ inline uint32_t below(uint64_t mask) {
@@ -91,183 +47,8 @@ __device__ inline uint32_t below(uint64_t mask) {
                                      __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
 }
 
-// Keys of a wavefront's elements, the k best among them, in buf; returns their number. q: vectors of
-// one lane, element 0 of vector u at position pos + u * step; lane_max: the lane's maximum.
-//
-// A bound that k to 2 k of the 64 lanes' maxima reach (bisection by lane masks) bounds the k-th best
-// element from below; what reaches it is collected, each lane's at an offset of its own (a ballot and a
-// branch per element took 3600 cycles for 32 of them, this 1100). Where ties or a mask put more there than
-// buf holds, the k best are taken one by one.
-template <typename Fmt, int NV>
-__device__ inline uint32_t wave_best(const typename Fmt::Vec (&q)[NV], uint32_t pos, uint32_t step,
-                                     float lane_max, uint32_t k, uint64_t* buf, int lane) {
-    constexpr int VW = Fmt::VW;
-    const uint32_t o[1] = {lane_max >= kLowest ? order_of(lane_max) >> kLowBits<Fmt> : 0};
-    float tau = kLowest;
-    if (static_cast<uint32_t>(__popcll(__ballot(o[0] != 0))) >= k) {
-        const uint32_t bound = bisect(o, k, 2 * k) << kLowBits<Fmt>;
-        tau = bound > order_of(kLowest) ? value_of(bound) : kLowest;
-    }
-    uint32_t hits = 0;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        float e[VW];
-        Fmt::unpack(q[u], e);
-#pragma unroll
-        for (int i = 0; i < VW; ++i) hits += e[i] >= tau ? 1 : 0;
-    }
-    uint32_t at = hits;  // those of this lane and the lanes before it
-#pragma unroll
-    for (int off = 1; off < kWave; off *= 2) {
-        const uint32_t other = __shfl_up(at, off);
-        at += lane >= off ? other : 0;
-    }
-    const uint32_t n = __builtin_amdgcn_readlane(at, kWave - 1);
-    if (n <= kWaveCap) {
-        at -= hits;
-#pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            float e[VW];
-            Fmt::unpack(q[u], e);
-#pragma unroll
-            for (int i = 0; i < VW; ++i)
-                if (e[i] >= tau) buf[at++] = key_of(e[i], pos + u * step + i);
-        }
-        return n;
-    }
-    uint64_t last = ~uint64_t{0};
-    uint32_t taken = 0;
-    for (; taken < k; ++taken) {
-        uint64_t best = 0;
-#pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            float e[VW];
-            Fmt::unpack(q[u], e);
-#pragma unroll
-            for (int i = 0; i < VW; ++i) {
-                const uint64_t key = e[i] >= kLowest ? key_of(e[i], pos + u * step + i) : 0;
-                best = key < last && key > best ? key : best;
-            }
-        }
-#pragma unroll
-        for (int off = 1; off < kWave; off *= 2) {
-            const uint64_t other = __shfl_xor(static_cast<unsigned long long>(best), off);
-            best = other > best ? other : best;
-        }
-        if (best == 0) break;
-        if (lane == 0) buf[taken] = best;
-        last = best;
-    }
-    return taken;
-}
-
-// One slice of up to NV vectors per lane. Tags as k_beam_scan's.
-template <typename Fmt, int NV>
-__global__ __launch_bounds__(kSliceThreads) void k_beam_slice(uint64_t x, uint64_t scores_, uint64_t ended_,
-                                                              uint64_t scratch, uint32_t stride,
-                                                              uint32_t slices, float scale) {
-    constexpr int VW = Fmt::VW;
-    __shared__ uint64_t s_buf[kSliceWaves][kWaveCap];
-    __shared__ Stat s_stat[kSliceWaves];
-    __shared__ uint32_t s_count[kSliceWaves];
-    const uint32_t cols = tags(x, scores_), parts = tag(ended_), k = tag(scratch);
-    const uint32_t at = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid % kWave;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const uint32_t r = at / parts, b = at - r * parts;
-    const uint8_t* ended = addr<const uint8_t>(ended_);
-    if (!alive(addr<const float>(scores_)[r]) || (ended != nullptr && ended[r] != 0)) return;
-    const RowSpan<Fmt> sp(row_ptr<Fmt>(addr<const void>(x), r, stride), cols);
-    const uint32_t n = part_vecs(span_max<Fmt>(cols), parts);  // the row's last vector is in the last slices
-    const uint32_t first = b * n, vecs = sp.vb + (cols % VW ? 1 : 0);
-    const uint32_t last = first < vecs ? (vecs - first < n ? vecs : first + n) : first;
-    typename Fmt::Vec q[NV];
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        const uint32_t v = first + tid + u * kSliceThreads;
-        q[u] = masked16<Fmt>();
-        if (v < last) {
-            if (v < sp.vb) {
-                q[u] = sp.load_whole(v);
-            } else {
-                q[u] = sp.load_tail();
-            }
-        }
-    }
-    Stat a;
-    a.init();
-    float most = -__builtin_huge_valf();  // the lane's maximum
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        float e[VW];
-        Fmt::unpack(q[u], e);
-        most = max_f(most, max_of(e));
-    }
-    a.m = lanes_max<kWave>(max_f(most, kLowest));
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        float e[VW];
-        Fmt::unpack(q[u], e);
-#pragma unroll
-        for (int i = 0; i < VW; ++i) {
-            const float z = (e[i] - a.m) * scale;
-            const float p = exp2_f(z);
-            a.s += p;
-            a.h = fmaf(p, max_f(z, kZFloor), a.h);
-        }
-    }
-    a.s = lanes_sum<kWave>(a.s);
-    a.h = lanes_sum<kWave>(a.h);
-    uint32_t count = 0;
-    if (a.s > 0.0f)
-        count = wave_best<Fmt, NV>(q, (first + tid) * VW, kSliceThreads * VW, most, k, s_buf[wave], lane);
-    if (lane == 0) {
-        s_stat[wave] = a;
-        s_count[wave] = count;
-    }
-    __syncthreads();
-    // every thread merges the four statistics; the keys' ranks among all of them
-    Stat all = s_stat[0];
-    uint32_t total = s_count[0];
-#pragma unroll
-    for (int w = 1; w < kSliceWaves; ++w) {
-        Stat o = s_stat[w];
-        const float to = max_f(all.m, o.m);
-        all.move<true>(to, scale);
-        o.move<true>(to, scale);
-        all.s += o.s;
-        all.h += o.h;
-        total += s_count[w];
-    }
-    Slice* slice = addr<Slice>(scratch) + at;
-    uint64_t* list = reinterpret_cast<uint64_t*>(addr<Slice>(scratch) + slices) + static_cast<size_t>(at) * k;
-    const bool ok = all.s > 0.0f;
-    for (uint32_t i = tid; ok && i < total; i += kSliceThreads) {
-        uint32_t in = i, w = 0;
-#pragma unroll
-        for (int x = 0; x < kSliceWaves - 1; ++x)
-            if (w == static_cast<uint32_t>(x) && in >= s_count[x]) {
-                in -= s_count[x];
-                ++w;
-            }
-        const uint64_t key = s_buf[w][in];
-        uint32_t rank = 0;
-#pragma unroll
-        for (int x = 0; x < kSliceWaves; ++x) {
-            const uint32_t many = s_count[x];
-#pragma unroll 8
-            for (uint32_t j = 0; j < many; ++j) rank += s_buf[x][j] > key ? 1 : 0;
-        }
-        if (rank < k) list[rank] = key;
-    }
-    if (tid == 0) *slice = Slice{all.m, all.s, all.h, ok ? (total < k ? total : k) : 0};
-}
-
 // ---------------------------------------------------------------------------------------
-// The join of one group's lists, at most kBeamLists of them, one per thread.
-
-constexpr int kJoinThreads = 256;
-static_assert(kJoinThreads >= kBeamLists, "a thread for each list");
+// The join of one group's lists, at most kBeamLists of them.
 
 // Values in the order of unsigned integers, and back.
 __device__ inline uint64_t order64(double v) {
@@ -304,7 +85,6 @@ struct CandLds {
 };
 
 constexpr uint16_t kNoList = 0xffff;
-constexpr int kCands = kBeamMax * (kBeamMax + 1) / 2;
 struct JoinLds {
     double base[kBeamMax];  // S_b - ln s_b, of a row that can be continued
     float m[kBeamMax];
@@ -312,136 +92,31 @@ struct JoinLds {
     uint16_t near[kBeamLists];  // lists whose heads can be among the width best
     uint16_t entries[kBeamLists];
     uint16_t list[kBeamMax];    // of the r-th best head
-    uint32_t close;
-    // What can be among the width best: entry j of the list whose head is the r-th best where r + j < width.
-    CandLds<kCands> cand;
-    uint32_t count;
+    uint32_t close, bound, count;
 };
-
-__device__ inline double lanes_sum64(double v) {
-#pragma unroll
-    for (int o = 1; o < kWave; o *= 2) v += __shfl_xor(v, o);
-    return v;
+// What can be among the width best, at most entry j of the list whose head is the r-th best where r + j < width: in LDS
+// that the launch sizes (beam_cands).
+__host__ __device__ inline uint32_t beam_room(uint32_t width) {
+    const uint32_t most = width * (width + 1) / 2;
+    return most < 64 ? 64 : most;
 }
-
-struct JoinArgs {
-    const float* scores;   // of the group
-    const uint8_t* ended;  // or null
-    const Slice* slices;
-    const uint64_t* lists;
-    uint32_t beams, parts, width, end_token;
-    double k, lo;          // log2(e) / T, and ln 2 k_lo / k_hi
+struct Cands {
+    uint64_t *value, *key;
+    uint8_t* beam;
+    __device__ Cands(uint64_t* lds, uint32_t width) {
+        const uint32_t n = beam_room(width);
+        value = lds;
+        key = lds + n;
+        beam = reinterpret_cast<uint8_t*>(lds + 2 * n);
+    }
+    __device__ Cand get(uint32_t i) const { return {value[i], key[i], beam[i]}; }
+    __device__ void put(uint32_t i, const Cand& c) const {
+        value[i] = c.value;
+        key[i] = c.key;
+        beam[i] = static_cast<uint8_t>(c.beam);
+    }
 };
-
-// Statistics of the rows, a wavefront each; the heads of the lists, one per thread, and their ranks; the
-// entries that can be among the best, all at once. Leaves them in L.cand, their number in L.count.
-__device__ inline void join(JoinLds& L, const JoinArgs& a) {
-    const int tid = threadIdx.x, lane = tid % kWave;
-    const double invt = a.k * kLn2d;
-    const uint32_t lists = a.beams * a.parts, width = a.width;
-    // this thread's list: loaded ahead of the statistics it is judged by
-    const bool mine = static_cast<uint32_t>(tid) < lists;
-    const uint32_t b_mine = mine ? tid / a.parts : 0;
-    const float score_mine = a.scores[b_mine];
-    const bool done_mine = a.ended != nullptr && a.ended[b_mine] != 0;
-    const bool on = mine && alive(score_mine) && !done_mine;
-    uint64_t key = 0;
-    uint32_t entries = 0;
-    if (on) {
-        entries = a.slices[tid].count;
-        key = a.lists[static_cast<size_t>(tid) * width];
-    }
-    for (uint32_t b = tid / kWave; b < a.beams; b += kJoinThreads / kWave) {
-        const float score = a.scores[b];
-        double base = -__builtin_huge_val();
-        float m = kLowest;
-        if (alive(score) && !(a.ended != nullptr && a.ended[b] != 0)) {
-            const Slice* p = a.slices + b * a.parts;
-            Slice s[kBeamLists / kWave];
-#pragma unroll
-            for (int i = 0; i < kBeamLists / kWave; ++i) {
-                s[i] = Slice{kLowest, 0.0f, 0.0f, 0};
-                if (lane + i * kWave < a.parts) s[i] = p[lane + i * kWave];
-                m = max_f(m, s[i].m);
-            }
-            m = lanes_max<kWave>(m);
-            double sum = 0.0;
-#pragma unroll
-            for (int i = 0; i < kBeamLists / kWave; ++i)
-                if (static_cast<uint32_t>(i) * kWave < a.parts)
-                    sum += (static_cast<double>(s[i].s) + a.lo * static_cast<double>(s[i].h)) *
-                           exp2((static_cast<double>(s[i].m) - static_cast<double>(m)) * a.k);
-            sum = lanes_sum64(sum);
-            if (sum > 0.0) base = static_cast<double>(score) - log(sum);
-        }
-        if (lane == 0) {
-            L.base[b] = base;
-            L.m[b] = m;
-        }
-    }
-    if (tid == 0) L.count = 0;
-    if (tid < kBeamMax) L.list[tid] = kNoList;
-    __syncthreads();
-    const auto candidate = [&](uint32_t b, uint64_t k) {
-        float v;
-        uint32_t i;
-        Key32<kMax>::split(k, v, i);
-        const double value = L.base[b] + (static_cast<double>(v) - static_cast<double>(L.m[b])) * invt;
-        return Cand{order64(value), k, b};
-    };
-    Cand head{0, 0, 0};
-    if (on) {
-        if (L.base[b_mine] > -__builtin_huge_val() && entries > 0) head = candidate(b_mine, key);
-    } else if (mine && done_mine && alive(score_mine) && tid % a.parts == 0) {  // goes on as it is
-        head = Cand{order64(static_cast<double>(score_mine)), key_of(0.0f, a.end_token), b_mine};
-        entries = 1;
-    }
-    if (tid < kBeamLists) {
-        L.head.put(tid, head);
-        L.entries[tid] = static_cast<uint16_t>(entries);
-    }
-    __syncthreads();
-    // One wavefront finds a bound that the width best heads reach, and few more (by the upper words of the
-    // values); the others wait. Ranks among all heads took 25 us with 256 of them.
-    if (tid < kWave) {
-        constexpr int kPer = kBeamLists / kWave;
-        uint32_t o[kPer], some = 0, bound = 0, n = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            o[i] = static_cast<uint32_t>(L.head.value[tid + i * kWave] >> 32);
-            some += __popcll(__ballot(o[i] != 0));
-        }
-        if (some > width) bound = bisect(o, width);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const bool in = o[i] != 0 && o[i] >= bound;
-            const uint64_t mask = __ballot(in);
-            if (in) L.near[n + below(mask)] = static_cast<uint16_t>(tid + i * kWave);
-            n += __popcll(mask);
-        }
-        if (tid == 0) L.close = n;
-    }
-    __syncthreads();
-    const uint32_t close = L.close;
-    if (static_cast<uint32_t>(tid) < close) {
-        const uint32_t list = L.near[tid];
-        const Cand c = L.head.get(list);
-        uint32_t rank = 0;
-#pragma unroll 4
-        for (uint32_t i = 0; i < close; ++i) rank += L.head.get(L.near[i]).above(c) ? 1 : 0;
-        if (rank < width) L.list[rank] = static_cast<uint16_t>(list);
-    }
-    __syncthreads();
-    const uint64_t least = L.list[width - 1] != kNoList ? L.head.value[L.list[width - 1]] : 0;
-    for (uint32_t i = tid; i < width * width; i += kJoinThreads) {
-        const uint32_t r = i / width, j = i - r * width, list = L.list[r];
-        if (r + j >= width || list == kNoList || j >= L.entries[list]) continue;
-        Cand c = L.head.get(list);
-        if (j > 0) c = candidate(c.beam, a.lists[static_cast<size_t>(list) * width + j]);
-        if (c.value >= least) L.cand.put(atomicAdd(&L.count, 1u), c);
-    }
-    __syncthreads();
-}
+inline size_t beam_cands(uint32_t width) { return static_cast<size_t>(beam_room(width)) * 17; }
 
 // Outputs of all groups, one after another: parents, tokens (int64), scores (float), ended (bytes).
 struct BeamOut {
@@ -461,47 +136,728 @@ struct BeamOut {
         scores[at] = score;
         ended[at] = end ? 1 : 0;
     }
+    __device__ void put(size_t at, const Cand& c, uint32_t end_token) const {
+        const uint32_t token = ~static_cast<uint32_t>(c.key);
+        put(at, c.beam, token, static_cast<float>(value64(c.value)), token == end_token);
+    }
+    __device__ void none(size_t at) const { put(at, -1, -1, -__builtin_huge_valf(), false); }
+};
+constexpr uint32_t kNoEnd = 0xffffffffu;  // no token's number
+
+// What is alike for all rows: k = log2(e) / T in two parts, and what follows from it.
+struct Scale {
+    double k, lo, invt;  // k, ln 2 k_lo / k_hi, 1 / T
+    __device__ Scale(float hi, uint32_t low) {  // low: the upper half of the low part's bits
+        const double l = __uint_as_float(low << 16);
+        k = static_cast<double>(hi) + l;
+        lo = kLn2d * l / static_cast<double>(hi);
+        invt = k * kLn2d;
+    }
+    // S_b - ln s_b of a row whose sums are s and h; -inf if the row has nothing to offer (s 0 or NaN).
+    __device__ double base(float score, double s) const {
+        return s > 0.0 ? static_cast<double>(score) - log(s) : -__builtin_huge_val();
+    }
+    __device__ Cand candidate(double base, float m, uint32_t b, uint64_t key) const {
+        float v;
+        uint32_t i;
+        Key32<kMax>::split(key, v, i);
+        return {order64(base + (static_cast<double>(v) - static_cast<double>(m)) * invt), key, b};
+    }
+};
+__device__ inline Cand finished(float score, uint32_t b, uint32_t end_token) {
+    return {order64(static_cast<double>(score)), key_of(0.0f, end_token), b};
+}
+
+// Scratch: generation and owner of every group, a slot for every slice (arrive), slices, lists.
+struct Scratch {
+    uint64_t *generation, *owner, *slots;  // of the group
+    uint64_t *slices, *lists;              // of the group: two words, and width words each
+    static size_t bytes(int64_t groups, int64_t lists, int width) {
+        return 8 * static_cast<size_t>(groups) * (2 + static_cast<size_t>(lists) * (3 + width));
+    }
+    __device__ Scratch(uint8_t* p, uint32_t groups, uint32_t g, uint32_t lists_, uint32_t width) {
+        uint64_t* w = reinterpret_cast<uint64_t*>(p);
+        const size_t all = static_cast<size_t>(groups) * lists_, mine = static_cast<size_t>(g) * lists_;
+        generation = w + g;
+        owner = w + groups + g;
+        slots = w + 2 * static_cast<size_t>(groups) + mine;
+        slices = w + 2 * static_cast<size_t>(groups) + all + 2 * mine;
+        lists = w + 2 * static_cast<size_t>(groups) + 3 * all + mine * width;
+    }
+};
+__device__ inline uint64_t two(float a, uint32_t b) { return static_cast<uint64_t>(b) << 32 | __float_as_uint(a); }
+__device__ inline float low_of(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
+__device__ inline uint32_t high_of(uint64_t w) { return static_cast<uint32_t>(w >> 32); }
+
+struct Step {
+    const float* scores;   // of the group
+    const uint8_t* ended;  // or null
+    uint32_t g, beams, parts, width, end_token;
+    __device__ bool done(uint32_t b) const { return ended != nullptr && ended[b] != 0; }
 };
 
-constexpr uint32_t kNoEnd = 0xffffffffu;
-
-// Tags: beams in scores, slices per row in ended, width in scratch, the low part of k (bf16) in out.
-__global__ __launch_bounds__(kJoinThreads) void k_beam_join(uint64_t scores, uint64_t ended, uint64_t scratch,
-                                                            uint64_t out, uint32_t end_token, float k_hi,
-                                                            uint32_t groups) {
-    __shared__ JoinLds L;
-    const uint32_t g = blockIdx.x, width = tag(scratch);
+// The best of the group's lists, by a workgroup of T threads: statistics of the rows, a wavefront each; the heads
+// of the lists, one per thread, and those that can be among the best; their entries, all at once; ranks.
+template <int T>
+__device__ inline void join(JoinLds& L, const Cands& cands, const Step& a, const Scratch& w, const Scale& k,
+                            const BeamOut& out) {
     const int tid = threadIdx.x;
-    JoinArgs a;
-    a.beams = tag(scores);
-    a.parts = tag(ended);
-    a.width = width;
-    a.end_token = end_token;
-    const size_t lists = static_cast<size_t>(a.beams) * a.parts;
-    a.scores = addr<const float>(scores) + static_cast<size_t>(g) * a.beams;
-    a.ended = addr<const uint8_t>(ended);
-    if (a.ended != nullptr) a.ended += static_cast<size_t>(g) * a.beams;
-    a.slices = addr<const Slice>(scratch) + g * lists;
-    a.lists = reinterpret_cast<const uint64_t*>(addr<const Slice>(scratch) + groups * lists) + g * lists * width;
-    const double hi = k_hi, lo = __uint_as_float(tag(out) << 16);
-    a.k = hi + lo;
-    a.lo = kLn2d * lo / hi;
-    join(L, a);
-    const BeamOut o(addr<uint8_t>(out), groups, width);
-    const uint32_t n = L.count;
-    for (uint32_t i = tid; i < n; i += kJoinThreads) {
-        const Cand c = L.cand.get(i);
-        uint32_t rank = 0;
-#pragma unroll 4
-        for (uint32_t j = 0; j < n; ++j) rank += L.cand.get(j).above(c) ? 1 : 0;
-        if (rank < width) {
-            const uint32_t token = ~static_cast<uint32_t>(c.key);
-            o.put(static_cast<size_t>(g) * width + rank, c.beam, token, static_cast<float>(value64(c.value)),
-                  end_token != kNoEnd && token == end_token);
+    const uint32_t lists = a.beams * a.parts, width = a.width;
+    // this thread's list: loaded ahead of the statistics it is judged by
+    const bool mine = static_cast<uint32_t>(tid) < lists;
+    const uint32_t b_mine = mine ? tid / a.parts : 0;
+    const float score_mine = a.scores[b_mine];
+    const bool done_mine = a.done(b_mine);
+    const bool on = mine && alive(score_mine) && !done_mine;
+    uint64_t key = 0;
+    uint32_t entries = 0;
+    if (on) {
+        entries = high_of(load_part(w.slices + 2 * tid + 1));
+        key = load_part(w.lists + static_cast<size_t>(tid) * width);
+    }
+    // a row's slices by 16, 32 or 64 lanes, so that few rounds do
+    const auto rows = [&](auto lanes) {
+        constexpr int G = decltype(lanes)::value, kPer = G == kWave ? kBeamLists / kWave : 1;
+        const int at = tid % G;
+        for (uint32_t b = tid / G; b < a.beams; b += T / G) {
+            const float score = a.scores[b];
+            const bool live = alive(score) && !a.done(b);
+            const uint64_t* p = w.slices + 2 * static_cast<size_t>(b) * a.parts;
+            uint64_t one[kPer];
+            float h[kPer], m = kLowest;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                one[i] = two(kLowest, 0);
+                h[i] = 0.0f;
+                if (live && at + i * G < static_cast<int>(a.parts)) {
+                    one[i] = load_part(p + 2 * (at + i * G));
+                    h[i] = low_of(load_part(p + 2 * (at + i * G) + 1));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) m = max_f(m, low_of(one[i]));
+            m = lanes_max<G>(m);
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (i == 0 || static_cast<uint32_t>(i) * G < a.parts)
+                    sum += (static_cast<double>(__uint_as_float(high_of(one[i]))) + k.lo * static_cast<double>(h[i])) *
+                           exp2((static_cast<double>(low_of(one[i])) - static_cast<double>(m)) * k.k);
+            const double base = k.base(score, lanes_sum64<G>(sum));
+            if (at == 0) {
+                L.base[b] = live ? base : -__builtin_huge_val();
+                L.m[b] = m;
+            }
+        }
+    };
+    if (a.parts <= 16)
+        rows(Int<16>{});
+    else if (a.parts <= 32)
+        rows(Int<32>{});
+    else
+        rows(Int<64>{});
+    if (tid == 0) L.count = 0;
+    if (tid < kBeamMax) L.list[tid] = kNoList;
+    __syncthreads();
+    Cand head{0, 0, 0};
+    if (on) {
+        if (L.base[b_mine] > -__builtin_huge_val() && entries > 0)
+            head = k.candidate(L.base[b_mine], L.m[b_mine], b_mine, key);
+    } else if (mine && done_mine && alive(score_mine) && tid % a.parts == 0) {  // goes on as it is
+        head = finished(score_mine, b_mine, a.end_token);
+        entries = 1;
+    }
+    if (tid < kBeamLists) {
+        L.head.put(tid, head);
+        L.entries[tid] = static_cast<uint16_t>(entries);
+    }
+    __syncthreads();
+    // One wavefront finds a bound that the width best heads reach, and few more (by the upper words of the
+    // values); the others wait. Ranks among all heads took 25 us with 256 of them.
+    if (tid < kWave) {
+        constexpr int kPer = kBeamLists / kWave;
+        uint32_t o[kPer], some = 0, bound = 0, n = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            o[i] = high_of(L.head.value[tid + i * kWave]);
+            some += __popcll(__ballot(o[i] != 0));
+        }
+        if (some > width) bound = bisect(o, width, width + width / 4 + 1);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const bool in = o[i] != 0 && o[i] >= bound;
+            const uint64_t mask = __ballot(in);
+            if (in) L.near[n + below(mask)] = static_cast<uint16_t>(tid + i * kWave);
+            n += __popcll(mask);
+        }
+        if (tid == 0) {
+            L.close = n;
+            L.bound = bound;
         }
     }
-    if (static_cast<uint32_t>(tid) < width && static_cast<uint32_t>(tid) >= n)
-        o.put(static_cast<size_t>(g) * width + tid, -1, -1, -__builtin_huge_valf(), false);
+    __syncthreads();
+    // All entries of those lists that reach the bound; where ties make them too many, those alone that can be among
+    // the best by the ranks of the heads: entry j of the list of the r-th best head where r + j < width.
+    const uint32_t close = L.close, room = beam_room(width);
+    const uint64_t bound = static_cast<uint64_t>(L.bound) << 32;
+    const auto entry = [&](uint32_t list, uint32_t j) {
+        const Cand c = L.head.get(list);
+        return j == 0 ? c : k.candidate(L.base[c.beam], L.m[c.beam], c.beam,
+                                        load_part(w.lists + static_cast<size_t>(list) * width + j));
+    };
+    for (uint32_t i = tid; i < close * width; i += T) {
+        const uint32_t r = i / width, j = i - r * width, list = L.near[r];
+        if (j >= L.entries[list]) continue;
+        const Cand c = entry(list, j);
+        if (c.value < bound) continue;
+        const uint32_t at = atomicAdd(&L.count, 1u);
+        if (at < room) cands.put(at, c);
+    }
+    __syncthreads();
+    if (L.count > room) {
+        __syncthreads();
+        if (tid == 0) L.count = 0;
+        for (uint32_t i = tid; i < close; i += T) {
+            const uint32_t list = L.near[i];
+            const Cand c = L.head.get(list);
+            uint32_t rank = 0;
+            for (uint32_t x = 0; x < close; ++x) rank += L.head.get(L.near[x]).above(c) ? 1 : 0;
+            if (rank < width) L.list[rank] = static_cast<uint16_t>(list);
+        }
+        __syncthreads();
+        for (uint32_t i = tid; i < width * width; i += T) {
+            const uint32_t r = i / width, j = i - r * width, list = L.list[r];
+            if (r + j < width && list != kNoList && j < L.entries[list]) cands.put(atomicAdd(&L.count, 1u), entry(list, j));
+        }
+        __syncthreads();
+    }
+    // ranks: several lanes count for a candidate, each over its share of the others
+    const uint32_t n = L.count;
+    const size_t first = static_cast<size_t>(a.g) * width;
+    const uint32_t lg = n <= T / 16 ? 4 : n <= T / 8 ? 3 : n <= T / 4 ? 2 : n <= T / 2 ? 1 : 0;
+    for (uint32_t i = tid >> lg; i < n; i += T >> lg) {
+        const Cand c = cands.get(i);
+        uint32_t rank = 0;
+#pragma unroll 2
+        for (uint32_t j = tid & ((1u << lg) - 1); j < n; j += 1u << lg) rank += cands.get(j).above(c) ? 1 : 0;
+        rank = lanes_sum_u32(rank, lg);
+        if ((tid & ((1u << lg) - 1)) == 0 && rank < width) out.put(first + rank, c, a.end_token);
+    }
+    if (static_cast<uint32_t>(tid) < width && static_cast<uint32_t>(tid) >= n) out.none(first + tid);
+}
+
+// What the kernels over slices have in common. Tags: columns in (x, scores), beams - 1 and slices per row - 1 (8 bits
+// each) in ended, width in scratch, the low part of k in out.
+struct SliceJob {
+    uint32_t cols, parts, width, row, part, at, beams, groups;
+    Step step;
+    __device__ SliceJob(uint64_t x, uint64_t scores, uint64_t ended, uint64_t scratch, uint32_t end_token) {
+        cols = tags(x, scores);
+        beams = (tag(ended) >> 8) + 1;
+        parts = (tag(ended) & 0xffu) + 1;
+        width = tag(scratch);
+        at = blockIdx.x;
+        row = at / parts;
+        part = at - row * parts;
+        groups = gridDim.x / (beams * parts);
+        const uint32_t g = row / beams;
+        const uint8_t* e = addr<const uint8_t>(ended);
+        step = {addr<const float>(scores) + static_cast<size_t>(g) * beams,
+                e == nullptr ? e : e + static_cast<size_t>(g) * beams, g, beams, parts, width, end_token};
+    }
+    __device__ uint32_t beam() const { return row - step.g * beams; }
+    __device__ bool on() const { return alive(step.scores[beam()]) && !step.done(beam()); }
+    // This slice's number in its group.
+    __device__ uint32_t list() const { return at - step.g * beams * parts; }
+};
+
+// After a slice's words are stored: the group's last workgroup joins its lists.
+template <int T>
+__device__ inline void join_if_last(JoinLds& L, uint64_t* cands, uint32_t* found, const SliceJob& j, const Scratch& w,
+                                    uint64_t generation, uint32_t nonce, float k_hi, uint64_t out) {
+    if (!arrive(w.slots, w.owner, j.list(), j.beams * j.parts, arrival_tag(nonce, generation), found)) return;
+    join<T>(L, Cands(cands, j.width), j.step, w, Scale(k_hi, tag(out)), BeamOut(addr<uint8_t>(out), j.groups, j.width));
+    if (threadIdx.x == 0) store_part(w.generation, generation + 1);
+}
+
+// One slice of a row per workgroup, in one pass; the join is a launch of its own (its registers would halve the
+// wavefronts of a CU: [2048,128256] bf16 131 us with it, 91 and 6 apart).
+template <typename Fmt, int T>
+__global__ __launch_bounds__(T) void k_beam_scan(uint64_t x, uint64_t scores, uint64_t ended, uint64_t scratch,
+                                                 uint32_t stride, float k_hi) {
+    constexpr int U = kUnroll<Fmt, true>;
+    __shared__ float sh[T / kWave][kShared];
+    __shared__ TopLds<T, kSegs<T>> L;
+    const SliceJob j(x, scores, ended, scratch, kNoEnd);
+    const Scratch w(addr<uint8_t>(scratch), j.groups, j.step.g, j.beams * j.parts, j.width);
+    const int lane = threadIdx.x;
+    if (!j.on()) return;
+    const RowSpan<Fmt> sp(row_ptr<Fmt>(addr<const void>(x), j.row, stride), j.cols);
+    const uint32_t n = part_vecs(span_max<Fmt>(j.cols), j.parts);
+    uint32_t first = sp.va + j.part * n;
+    first = first < sp.vb ? first : sp.vb;
+    const uint32_t last = sp.vb - first < n ? sp.vb : first + n;
+    const Segments g = Segments::cut<T, U>(first, last, kSegs<T>);
+    Stat a;
+    scan_span<Fmt, true, T, U, true>(sp, j.part == 0, first, last, lane, k_hi, a, g, L.seg);
+    team_merge<true, T>(a, k_hi, lane, sh);
+    uint32_t count = 0;
+    if (a.s > 0.0f) {  // not only masked logits, and neither NaN nor +inf
+        top_select<Fmt, T, kSegs<T>>(L, sp, g.count(), g.lg_vecs, j.width, lane,
+                                     [&](uint32_t s, uint32_t i) { return g.vec(s, i); }, j.part == 0);
+        count = L.count;
+        if (static_cast<uint32_t>(lane) < count)
+            store_part(w.lists + static_cast<size_t>(j.list()) * j.width + lane, L.buf[lane]);
+    }
+    if (lane == 0) {
+        store_part(w.slices + 2 * j.list(), two(a.m, __float_as_uint(a.s)));
+        store_part(w.slices + 2 * j.list() + 1, two(a.h, count));
+    }
+}
+
+// One workgroup per group. Tags as SliceJob's, without the columns.
+__global__ __launch_bounds__(kSliceThreads) void k_beam_join(uint64_t scores, uint64_t ended, uint64_t scratch,
+                                                             uint64_t out, uint32_t end_token, float k_hi) {
+    __shared__ JoinLds L;
+    extern __shared__ uint64_t s_cands[];
+    const uint32_t g = blockIdx.x, beams = (tag(ended) >> 8) + 1, parts = (tag(ended) & 0xffu) + 1, width = tag(scratch);
+    const uint8_t* e = addr<const uint8_t>(ended);
+    const Step step{addr<const float>(scores) + static_cast<size_t>(g) * beams,
+                    e == nullptr ? e : e + static_cast<size_t>(g) * beams, g, beams, parts, width, end_token};
+    join<kSliceThreads>(L, Cands(s_cands, width), step, Scratch(addr<uint8_t>(scratch), gridDim.x, g, beams * parts, width),
+                        Scale(k_hi, tag(out)), BeamOut(addr<uint8_t>(out), gridDim.x, width));
+}
+
+// ---------------------------------------------------------------------------------------
+// A slice that its workgroup holds in registers. Its k best elements are at least the smallest of four bounds
+// that k / 4 lanes of each wavefront reach; what reaches that, less than 2 k as a rule, is collected and ranked by
+// counting. (By a bound for k of each wavefront alone, 16 best of 6300 elements took 9000 cycles more.)
+
+constexpr int kSliceWaves = kSliceThreads / kWave;
+constexpr int kSliceCap = 1024;  // keys that a workgroup collects, an even share by each wavefront
+static_assert(kSliceCap >= kSliceWaves * kBeamMax, "the k best of each wavefront fit");
+
+// A vector as the compiler does not know it: what was made of it before is not kept in registers.
+template <typename Vec>
+__device__ inline Vec anew(Vec v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// A bound that at least k (and few more) of the wavefront's 64 lane maxima reach, by bisection; -inf if there
+// are fewer than k. As an ordered integer: 0 for -inf.
+template <typename Fmt>
+__device__ inline uint32_t wave_bound(float lane_max, uint32_t k) {
+    const uint32_t o[1] = {lane_max >= kLowest ? order_of(lane_max) >> kLowBits<Fmt> : 0};
+    if (static_cast<uint32_t>(__popcll(__ballot(o[0] != 0))) < k) return 0;
+    return bisect(o, k, k + k / 4 + 1);
+}
+
+// Word i of N (a power of two) in registers.
+template <int N>
+__device__ __forceinline__ uint32_t pick(const uint32_t (&w)[N], uint32_t i) {
+    if constexpr (N == 1) {
+        return w[0];
+    } else {
+        uint32_t half[N / 2];
+        const uint32_t upper = 0u - (i / (N / 2) & 1u);  // (a choice by ?: would put w into memory)
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) half[j] = (w[j + N / 2] & upper) | (w[j] & ~upper);
+        return pick(half, i);
+    }
+}
+
+// Which of a lane's elements are at least tau, as masks of 32; and their keys, one per lane and round (a ballot and
+// a branch per element took 3600 cycles for 32 of them).
+template <typename Fmt, int NV>
+struct Hits {
+    static constexpr int kElems = NV * Fmt::VW, kMasks = (kElems + 31) / 32;
+    uint32_t mask[kMasks];
+    uint32_t count;
+    __device__ Hits(const typename Fmt::Vec (&q)[NV], float tau) {
+        count = 0;
+#pragma unroll
+        for (int m = 0; m < kMasks; ++m) mask[m] = 0;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            float e[Fmt::VW];
+            Fmt::unpack(anew(q[u]), e);
+#pragma unroll
+            for (int i = 0; i < Fmt::VW; ++i) {
+                const int at = u * Fmt::VW + i;
+                mask[at / 32] |= e[i] >= tau ? 1u << (at % 32) : 0;
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < kMasks; ++m) count += __popc(mask[m]);
+    }
+    // put(key); element 0 of vector u is at position pos + u * step.
+    template <typename Put>
+    __device__ void each(const typename Fmt::Vec (&q)[NV], uint32_t pos, uint32_t step, Put put) {
+        constexpr int kVecs = kElems < 32 ? NV : 32 / Fmt::VW, kWords = 4 * kVecs;  // of a mask's elements
+#pragma unroll
+        for (int m = 0; m < kMasks; ++m) {
+            uint32_t w[kWords];
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const u32x4 v = __builtin_bit_cast(u32x4, q[m * kVecs + i]);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+            while (__ballot(mask[m] != 0) != 0) {
+                const bool some = mask[m] != 0;
+                const uint32_t i = some ? __builtin_ctz(mask[m]) : 0;
+                mask[m] &= mask[m] - 1;
+                constexpr uint32_t kPerWord = 4 / Fmt::kSize;
+                const uint32_t word = pick(w, i / kPerWord);
+                const float e = Fmt::from_bits(static_cast<typename Fmt::Bits>(word >> (i % kPerWord * 16)));
+                const uint32_t at = m * 32 + i;
+                if (some) put(key_of(e, pos + at / Fmt::VW * step + at % Fmt::VW));
+            }
+        }
+    }
+};
+
+// The k best keys of a wavefront's elements, one by one, best first; returns their number.
+template <typename Fmt, int NV>
+__device__ inline uint32_t wave_best(const typename Fmt::Vec (&q)[NV], uint32_t pos, uint32_t step, uint32_t k,
+                                     uint64_t* buf, int lane) {
+    constexpr int VW = Fmt::VW;
+    uint64_t last = ~uint64_t{0};
+    uint32_t taken = 0;
+    for (; taken < k; ++taken) {
+        uint64_t best = 0;
+        uint32_t from = pos;  // (the keys, too, are made anew in every round)
+        asm volatile("" : "+v"(from));
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            float e[VW];
+            Fmt::unpack(q[u], e);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                const uint64_t key = e[i] >= kLowest ? key_of(e[i], from + u * step + i) : 0;
+                best = key < last && key > best ? key : best;
+            }
+        }
+#pragma unroll
+        for (int off = 1; off < kWave; off *= 2) {
+            const uint64_t other = __shfl_xor(static_cast<unsigned long long>(best), off);
+            best = other > best ? other : best;
+        }
+        if (best == 0) break;
+        if (lane == 0) buf[taken] = best;
+        last = best;
+    }
+    return taken;
+}
+
+// One slice of up to NV vectors per lane.
+template <typename Fmt, int NV>
+__global__ __launch_bounds__(kSliceThreads) void k_beam_slice(uint64_t x, uint64_t scores, uint64_t ended,
+                                                              uint64_t scratch, uint64_t out, uint32_t stride,
+                                                              uint32_t end_token, float k_hi, uint32_t nonce) {
+    constexpr int VW = Fmt::VW;
+    __shared__ Stat s_stat[kSliceWaves];
+    __shared__ uint32_t s_bound[kSliceWaves], s_total, s_found;
+    __shared__ uint64_t s_best[kSliceWaves][kBeamMax];
+    __shared__ union Lds {
+        uint64_t buf[kSliceCap];
+        JoinLds join;
+        __device__ Lds() {}
+    } lds;
+    extern __shared__ uint64_t s_cands[];
+    const SliceJob j(x, scores, ended, scratch, end_token);
+    const Scratch w(addr<uint8_t>(scratch), j.groups, j.step.g, j.beams * j.parts, j.width);
+    const uint64_t generation = load_part(w.generation);
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    auto& buf = lds.buf;
+    if (j.on()) {
+        const RowSpan<Fmt> sp(row_ptr<Fmt>(addr<const void>(x), j.row, stride), j.cols);
+        const uint32_t n = part_vecs(span_max<Fmt>(j.cols), j.parts);  // the row's last vector is in the last slices
+        const uint32_t first = j.part * n, vecs = sp.vb + (j.cols % VW ? 1 : 0);
+        const uint32_t last = first < vecs ? (vecs - first < n ? vecs : first + n) : first;
+        typename Fmt::Vec q[NV];
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const uint32_t v = first + tid + u * kSliceThreads;
+            q[u] = masked16<Fmt>();
+            if (v < last) {
+                if (v < sp.vb) {
+                    q[u] = sp.load_whole(v);
+                } else {
+                    q[u] = sp.load_tail();
+                }
+            }
+        }
+        Stat a;
+        a.init();
+        float most = -__builtin_huge_valf();  // the lane's maximum
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            float e[VW];
+            Fmt::unpack(q[u], e);
+            most = max_f(most, max_of(e));
+        }
+        a.m = lanes_max<kWave>(max_f(most, kLowest));
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            float e[VW];
+            Fmt::unpack(anew(q[u]), e);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                const float z = (e[i] - a.m) * k_hi;
+                const float p = exp2_f(z);
+                a.s += p;
+                a.h = fmaf(p, max_f(z, kZFloor), a.h);
+            }
+        }
+        a.s = lanes_sum<kWave>(a.s);
+        a.h = lanes_sum<kWave>(a.h);
+        const uint32_t enough = a.s > 0.0f ? wave_bound<Fmt>(most, (j.width + kSliceWaves - 1) / kSliceWaves) : 0;
+        if (lane == 0) {
+            s_stat[wave] = a;
+            s_bound[wave] = enough;
+        }
+        if (tid == 0) s_total = 0;
+        __syncthreads();
+        uint32_t bound = s_bound[0];
+#pragma unroll
+        for (int w = 1; w < kSliceWaves; ++w) bound = s_bound[w] < bound ? s_bound[w] : bound;
+        if (bound == 0) bound = wave_bound<Fmt>(most, j.width);  // a wavefront with next to nothing
+        bound <<= kLowBits<Fmt>;
+        const float tau = bound > order_of(kLowest) ? value_of(bound) : kLowest;
+        const uint32_t pos = (first + tid) * VW;
+        // the lanes' hits, and those of the lanes before each
+        Hits<Fmt, NV> hits(q, a.s > 0.0f ? tau : __builtin_nanf(""));
+        uint32_t at = hits.count;
+#pragma unroll
+        for (int off = 1; off < kWave; off *= 2) {
+            const uint32_t other = __shfl_up(at, off);
+            at += lane >= off ? other : 0;
+        }
+        const uint32_t many = __builtin_amdgcn_readlane(at, kWave - 1);
+        at -= hits.count;
+        uint32_t place = 0;
+        if (many <= kSliceCap / kSliceWaves) {
+            if (lane == 0) place = atomicAdd(&s_total, many);
+            at += __builtin_amdgcn_readfirstlane(place);
+            hits.each(q, pos, kSliceThreads * VW, [&](uint64_t key) { buf[at++] = key; });
+        } else {  // ties
+            const uint32_t n = wave_best<Fmt, NV>(q, pos, kSliceThreads * VW, j.width, s_best[wave], lane);
+            team_sync<kWave>();
+            if (lane == 0) place = atomicAdd(&s_total, n);
+            place = __builtin_amdgcn_readfirstlane(place);
+            if (static_cast<uint32_t>(lane) < n) buf[place + lane] = s_best[wave][lane];
+        }
+        __syncthreads();
+        // every thread merges the four statistics
+        Stat all = s_stat[0];
+#pragma unroll
+        for (int x = 1; x < kSliceWaves; ++x) {
+            Stat o = s_stat[x];
+            const float to = max_f(all.m, o.m);
+            all.move<true>(to, k_hi);
+            o.move<true>(to, k_hi);
+            all.s += o.s;
+            all.h += o.h;
+        }
+        // ranks: several lanes count for a key, each over its share of the others
+        const uint32_t total = s_total;
+        const bool ok = all.s > 0.0f;
+        const uint32_t lg = total <= 16 ? 4 : total <= 32 ? 3 : total <= 64 ? 2 : total <= 128 ? 1 : 0;
+        for (uint32_t i = tid >> lg; ok && i < total; i += kSliceThreads >> lg) {
+            const uint64_t key = buf[i];
+            uint32_t rank = 0;
+#pragma unroll 4
+            for (uint32_t y = tid & ((1u << lg) - 1); y < total; y += 1u << lg) rank += buf[y] > key ? 1 : 0;
+            rank = lanes_sum_u32(rank, lg);
+            if ((tid & ((1u << lg) - 1)) == 0 && rank < j.width)
+                store_part(w.lists + static_cast<size_t>(j.list()) * j.width + rank, key);
+        }
+        if (tid == 0) {
+            store_part(w.slices + 2 * j.list(), two(all.m, __float_as_uint(all.s)));
+            store_part(w.slices + 2 * j.list() + 1, two(all.h, ok ? (total < j.width ? total : j.width) : 0));
+        }
+    }
+    join_if_last<kSliceThreads>(lds.join, s_cands, &s_found, j, w, generation, nonce, k_hi, out);
+}
+
+// ---------------------------------------------------------------------------------------
+// Groups of short rows: one wavefront per group holds all of its beams' logits and needs no scratch.
+
+constexpr int kGroupCap = 256;  // candidates that a wavefront collects
+
+// G lanes per row, 64 / G rows to a unit (C == 1), or a row of C units of 64 vectors; I units of a vector per lane.
+// Every lane judges its elements by the row's base in binary64; a bound that `width` lanes' best reach leaves few
+// more to collect and rank. [2048,4,64] f16: see argreduce_beam_api.cpp.
+// Tags: columns in (x, scores), beams - 1 and width (8 bits each) in ended, the low part of k in out.
+template <typename Fmt, int G, int C, int I>
+__global__ __launch_bounds__(kBlockThreads) void k_beam_group(uint64_t x, uint64_t scores_, uint64_t ended_, uint64_t out_,
+                                                              uint32_t stride, uint32_t end_token, float k_hi,
+                                                              uint32_t groups) {
+    constexpr int VW = Fmt::VW, kRows = kWave / G;  // rows of a unit
+    static_assert(C == 1 || G == kWave, "long rows take whole units");
+    __shared__ CandLds<kGroupCap> s_cand[kBlockThreads / kWave];
+    const uint32_t cols = tags(x, scores_), beams = (tag(ended_) >> 8) + 1, width = tag(ended_) & 0xffu;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t g = blockIdx.x * (kBlockThreads / kWave) + wave;
+    if (g >= groups) return;  // whole wavefronts, and no barriers
+    const int lane = threadIdx.x % kWave;
+    auto& cand = s_cand[wave];
+    const Scale k(k_hi, tag(out_));
+    const float* scores = addr<const float>(scores_) + static_cast<size_t>(g) * beams;
+    const uint8_t* ended = addr<const uint8_t>(ended_);
+    const auto beam = [&](int u) { return C > 1 ? static_cast<uint32_t>(u / C) : static_cast<uint32_t>(u * kRows + lane / G); };
+    const auto vec = [&](int u) { return C > 1 ? static_cast<uint32_t>(u % C * kWave + lane) : static_cast<uint32_t>(lane % G); };
+    typename Fmt::Vec q[I];
+    float score[I];
+    bool on[I], done[I];
+#pragma unroll
+    for (int u = 0; u < I; ++u) {
+        const uint32_t b = beam(u), v = vec(u);
+        score[u] = b < beams ? scores[b] : -__builtin_huge_valf();
+        done[u] = b < beams && ended != nullptr && ended[static_cast<size_t>(g) * beams + b] != 0;
+        on[u] = alive(score[u]) && !done[u];
+        done[u] = done[u] && alive(score[u]) && v == 0;  // offers its score, from the row's first lane
+        q[u] = masked16<Fmt>();
+        if (on[u]) {
+            const RowSpan<Fmt> sp(row_ptr<Fmt>(addr<const void>(x), g * beams + b, stride), cols);
+            if (v < sp.vb)
+                q[u] = sp.load_whole(v);
+            else if (v == sp.vb && cols % VW != 0)
+                q[u] = sp.load_tail();
+        }
+    }
+    // statistics of the rows
+    float most[I], m[I];
+    double base[I];
+#pragma unroll
+    for (int u = 0; u < I; ++u) {
+        float e[VW];
+        Fmt::unpack(q[u], e);
+        most[u] = max_of(e);
+    }
+#pragma unroll
+    for (int r = 0; r < I; r += C) {
+        float top = kLowest, s = 0.0f, h = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) top = max_f(top, most[r + c]);
+        top = lanes_max<G>(top);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float e[VW];
+            Fmt::unpack(anew(q[r + c]), e);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+                const float z = (e[i] - top) * k_hi, p = exp2_f(z);
+                s += p;
+                h = fmaf(p, max_f(z, kZFloor), h);
+            }
+        }
+        s = lanes_sum<G>(s);
+        h = lanes_sum<G>(h);
+        const double b = k.base(score[r], static_cast<double>(s) + k.lo * static_cast<double>(h));
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            m[r + c] = top;
+            base[r + c] = on[r + c] ? b : -__builtin_huge_val();
+        }
+    }
+    const auto valid = [&](int u) { return base[u] > -__builtin_huge_val(); };
+    // the lane's best value, and a bound that `width` of them reach
+    uint64_t best = 0;
+#pragma unroll
+    for (int u = 0; u < I; ++u) {
+        uint64_t o = 0;
+        if (valid(u) && most[u] >= kLowest)
+            o = order64(base[u] + (static_cast<double>(most[u]) - static_cast<double>(m[u])) * k.invt);
+        if (done[u]) o = order64(static_cast<double>(score[u]));
+        best = o > best ? o : best;
+    }
+    const uint32_t o[1] = {high_of(best)};
+    uint32_t bound = 0;
+    if (static_cast<uint32_t>(__popcll(__ballot(o[0] != 0))) > width) bound = bisect(o, width, width + width / 4 + 1);
+    // what a logit must be at least, row by row: the bound's, less what the rounding of this can be off by
+    const double least = value64(static_cast<uint64_t>(bound) << 32), t = 1.0 / k.invt;
+    uint32_t count = 0;
+    float tau[I];
+#pragma unroll
+    for (int u = 0; u < I; ++u) {
+        tau[u] = __builtin_nanf("");  // nothing reaches it, not +inf either
+        if (valid(u)) {
+            const double v = static_cast<double>(m[u]) + (least - base[u]) * t;
+            const double off = (fabs(least) + fabs(base[u])) * 0x1p-48 * t + fabs(v) * 0x1p-20 + 0x1p-120;
+            const float f = static_cast<float>(v - off);
+            tau[u] = bound != 0 && f > kLowest ? f : kLowest;
+        }
+        const typename Fmt::Vec one[1] = {q[u]};
+        count += Hits<Fmt, 1>(one, tau[u]).count + (done[u] ? 1 : 0);
+    }
+    uint32_t at = count;
+#pragma unroll
+    for (int off = 1; off < kWave; off *= 2) {
+        const uint32_t other = __shfl_up(at, off);
+        at += lane >= off ? other : 0;
+    }
+    const uint32_t n = __builtin_amdgcn_readlane(at, kWave - 1);
+    at -= count;
+    const BeamOut out(addr<uint8_t>(out_), groups, width);
+    const size_t first = static_cast<size_t>(g) * width;
+    if (n <= kGroupCap) {
+#pragma unroll
+        for (int u = 0; u < I; ++u) {
+            const typename Fmt::Vec one[1] = {q[u]};
+            Hits<Fmt, 1> hits(one, tau[u]);
+            hits.each(one, vec(u) * VW, 0, [&](uint64_t key) { cand.put(at++, k.candidate(base[u], m[u], beam(u), key)); });
+            if (done[u]) cand.put(at++, finished(score[u], beam(u), end_token));
+        }
+        team_sync<kWave>();
+        // ranks: several lanes count for a candidate, each over its share of the others
+        const uint32_t lg = n <= 4 ? 4 : n <= 8 ? 3 : n <= 16 ? 2 : n <= 32 ? 1 : 0;
+        for (uint32_t i = lane >> lg; i < n; i += kWave >> lg) {
+            const Cand c = cand.get(i);
+            uint32_t rank = 0;
+#pragma unroll 2
+            for (uint32_t j = lane & ((1u << lg) - 1); j < n; j += 1u << lg) rank += cand.get(j).above(c) ? 1 : 0;
+            rank = lanes_sum_u32(rank, lg);
+            if ((lane & ((1u << lg) - 1)) == 0 && rank < width) out.put(first + rank, c, end_token);
+        }
+        if (static_cast<uint32_t>(lane) < width && static_cast<uint32_t>(lane) >= n) out.none(first + lane);
+        return;
+    }
+    // ties: the best are taken one by one
+    Cand last{~uint64_t{0}, ~uint64_t{0}, 0};
+    for (uint32_t r = 0; r < width; ++r) {
+        Cand top{0, 0, 0};
+        const auto offer = [&](const Cand& c) {
+            if (last.above(c) && c.above(top)) top = c;
+        };
+#pragma unroll
+        for (int u = 0; u < I; ++u) {
+            float e[VW];
+            Fmt::unpack(anew(q[u]), e);
+#pragma unroll
+            for (int i = 0; i < VW; ++i)
+                if (valid(u) && e[i] >= kLowest) offer(k.candidate(base[u], m[u], beam(u), key_of(e[i], vec(u) * VW + i)));
+            if (done[u]) offer(finished(score[u], beam(u), end_token));
+        }
+#pragma unroll
+        for (int off = 1; off < kWave; off *= 2) {
+            const Cand c{__shfl_xor(static_cast<unsigned long long>(top.value), off),
+                         __shfl_xor(static_cast<unsigned long long>(top.key), off), __shfl_xor(top.beam, off)};
+            if (c.above(top)) top = c;
+        }
+        if (lane == 0) {
+            if (top.value != 0)
+                out.put(first + r, top, end_token);
+            else
+                out.none(first + r);
+        }
+        last = top;
+    }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -608,44 +964,68 @@ __global__ __launch_bounds__(kBlockThreads) void k_reorder(uint64_t table, uint6
 
 }  // namespace
 
-size_t beam_list_bytes(int width) { return sizeof(Slice) + static_cast<size_t>(width) * sizeof(uint64_t); }
+size_t beam_scratch(int64_t groups, int64_t lists, int width) { return Scratch::bytes(groups, lists, width); }
 
 hipError_t launch_beam_step(const BeamPlan& plan, const BeamArgs& a, uint8_t* scratch16, hipStream_t s) {
-    const uint32_t cols = static_cast<uint32_t>(a.cols), groups = static_cast<uint32_t>(a.groups);
-    const uint32_t slices = groups * static_cast<uint32_t>(a.beams * plan.parts);
+    const uint32_t cols = static_cast<uint32_t>(a.cols), stride = static_cast<uint32_t>(a.row_stride);
     const double k = 1.4426950408889634074 / a.temperature;
     const float hi = static_cast<float>(k);
     // the rest of k to 8 bits: k is then good to 2^-33 of itself
     const float rest = static_cast<float>(k - static_cast<double>(hi));
     const uint32_t low = (bits_of(rest) + 0x8000u) >> 16;
-    const auto scan = [&](auto fmt, auto team) {
-        constexpr int T = decltype(team)::value;
-        launch(k_beam_scan<decltype(fmt), T>, static_cast<uint32_t>(plan.grid_blocks), kTeamBlock<T>, s,
-               tagged(a.x, cols), tagged(a.scores, cols >> 16), tagged(a.ended, plan.parts),
-               tagged(scratch16, a.width), static_cast<uint32_t>(a.row_stride), slices, hi);
+    const uint32_t end = a.end_token < 0 ? kNoEnd : static_cast<uint32_t>(a.end_token);
+    const uint32_t shape = static_cast<uint32_t>(a.beams - 1) << 8 | static_cast<uint32_t>(plan.parts - 1);
+    const uint32_t grid = static_cast<uint32_t>(plan.grid_blocks);
+    const auto x = tagged(a.x, cols), scores = tagged(a.scores, cols >> 16), ended = tagged(a.ended, shape),
+               scratch = tagged(scratch16, a.width), out = tagged(a.out, low);
+    const auto slice = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(kSliceThreads), beam_cands(a.width), s, x, scores, ended, scratch, out,
+                           stride, end, hi, next_nonce());
     };
-    const auto slice = [&](auto fmt, auto held) {
-        launch(k_beam_slice<decltype(fmt), decltype(held)::value>, slices, kSliceThreads, s, tagged(a.x, cols),
-               tagged(a.scores, cols >> 16), tagged(a.ended, plan.parts), tagged(scratch16, a.width),
-               static_cast<uint32_t>(a.row_stride), slices, hi);
+    const auto scan = [&](auto kernel) {
+        launch(kernel, grid, plan.team, s, x, scores, ended, scratch, stride, hi);
+        hipLaunchKernelGGL(k_beam_join, dim3(static_cast<uint32_t>(a.groups)), dim3(kSliceThreads), beam_cands(a.width), s,
+                           scores, ended, scratch, out, end, hi);
+    };
+    const auto group = [&](auto kernel) {
+        const uint32_t sizes = static_cast<uint32_t>(a.beams - 1) << 8 | static_cast<uint32_t>(a.width);
+        launch(kernel, grid, kBlockThreads, s, x, scores, tagged(a.ended, sizes), out, stride, end, hi,
+               static_cast<uint32_t>(a.groups));
     };
     with_format(a.dtype, [&](auto fmt) {
+        using Fmt = decltype(fmt);
+        if (plan.path == ARGREDUCE_PATH_SUBWAVE) {
+            const auto units = [&](auto lanes, auto chunks) {
+                constexpr int G = decltype(lanes)::value, C = decltype(chunks)::value;
+                switch (plan.held) {
+                    case 1:
+                        if constexpr (C == 1) return group(k_beam_group<Fmt, G, C, 1>);
+                    case 2: return group(k_beam_group<Fmt, G, C, 2>);
+                    case 4: return group(k_beam_group<Fmt, G, C, 4>);
+                    default: return group(k_beam_group<Fmt, G, C, 8>);
+                }
+            };
+            switch (plan.team) {
+                case 4: return units(Int<4>{}, Int<1>{});
+                case 8: return units(Int<8>{}, Int<1>{});
+                case 16: return units(Int<16>{}, Int<1>{});
+                case 32: return units(Int<32>{}, Int<1>{});
+                case 64: return units(Int<64>{}, Int<1>{});
+                default: return units(Int<64>{}, Int<2>{});
+            }
+        }
         switch (plan.held) {
-            case 1: return slice(fmt, Int<1>{});
-            case 2: return slice(fmt, Int<2>{});
-            case 4: return slice(fmt, Int<4>{});
-            case 8: return slice(fmt, Int<8>{});
+            case 1: return slice(k_beam_slice<Fmt, 1>);
+            case 2: return slice(k_beam_slice<Fmt, 2>);
+            case 4: return slice(k_beam_slice<Fmt, 4>);
+            case 8: return slice(k_beam_slice<Fmt, 8>);
         }
         switch (plan.team) {
-            case 64: scan(fmt, Int<64>{}); break;
-            case 256: scan(fmt, Int<256>{}); break;
-            case 512: scan(fmt, Int<512>{}); break;
-            default: scan(fmt, Int<1024>{}); break;
+            case 256: return scan(k_beam_scan<Fmt, 256>);
+            case 512: return scan(k_beam_scan<Fmt, 512>);
+            default: return scan(k_beam_scan<Fmt, 1024>);
         }
     });
-    const uint32_t end = a.end_token < 0 ? kNoEnd : static_cast<uint32_t>(a.end_token);
-    launch(k_beam_join, groups, kJoinThreads, s, tagged(a.scores, a.beams), tagged(a.ended, plan.parts),
-           tagged(scratch16, a.width), tagged(a.out, low), end, hi, groups);
     return hipGetLastError();
 }
 

@@ -15,15 +15,15 @@ constexpr int kSliceThreads = 256;  // of a workgroup that holds a slice in regi
 constexpr int kSliceVecs = 8;    // 16-byte vectors each of its lanes holds, at most
 constexpr int kBeamLists = 256;  // lists of candidates that one group's join takes
 
-// How the rows (one per beam) of one step are scanned.
+// How one step is done.
 struct BeamPlan {
-    int path;             // argreduce_path_t: SUBWAVE (a wavefront per row), BLOCK or SPLIT
-    int team;             // lanes that scan one slice: 64, 256, 512 or 1024
-    int parts;            // slices per row, each with a list of candidates of its own
-    int held;             // vectors per lane of a slice held in registers: 1, 2, 4, 8, or 0 (one pass)
-    int64_t grid_blocks;  // workgroups of the scanning kernel
+    int path;             // argreduce_path_t: SUBWAVE (a wavefront per group), BLOCK or SPLIT
+    int team;             // SUBWAVE: lanes per row, 4 to 128; else threads that scan one slice
+    int parts;            // BLOCK, SPLIT: slices per row, each with a list of candidates of its own
+    int held;             // 16-byte vectors per lane held in registers: 1, 2, 4, 8, or 0 (a slice in one pass)
+    int64_t grid_blocks;  // workgroups of the (scanning) kernel
     int64_t device_threads;
-    size_t scratch_bytes; // including 15 bytes of alignment slack
+    size_t scratch_bytes; // including 15 bytes of alignment slack; 0 if none needed
 };
 
 struct BeamArgs {
@@ -38,7 +38,7 @@ struct BeamArgs {
     uint8_t* out;          // parents, tokens, scores, ended
 };
 
-size_t beam_list_bytes(int width);  // scratch of one list and its slice's statistics
+size_t beam_scratch(int64_t groups, int64_t lists, int width);  // scratch of a step with so many lists per group
 hipError_t launch_beam_step(const BeamPlan& plan, const BeamArgs& a, uint8_t* scratch16, hipStream_t stream);
 
 // Positions [first, last) of every group's beams: values, or arrays of one per group.

@@ -30,28 +30,33 @@ int make_beam_plan(int dtype, int64_t groups, int64_t beams, int64_t cols, int w
     const int64_t rows = std::max<int64_t>(1, groups * beams);
     const int64_t cus = std::max<int64_t>(1, cap / kThreadsPerCu);
     const int64_t vecs = span_vecs(cols, logits_elem_size(dtype));
-    int64_t parts = 1;
-    if (vecs <= 256) {
+    // A wavefront per group, if its beams' rows are units of at most eight vectors per lane.
+    const int64_t whole = ceil_div(cols * logits_elem_size(dtype), 16);  // vectors of a row from its first element
+    const int64_t lanes = std::max<int64_t>(4, next_pow2(whole));
+    const int64_t units = next_pow2(lanes <= 64 ? ceil_div(beams, 64 / lanes) : beams * 2);
+    if (lanes <= 128 && units <= 8) {
         p->path = ARGREDUCE_PATH_SUBWAVE;
-        p->team = 64;
+        p->team = static_cast<int>(lanes);
+        p->held = static_cast<int>(units);
+        p->parts = 1;
+        p->grid_blocks = ceil_div(std::max<int64_t>(1, groups), kBlock / 64);
+        return grid_too_large(p->grid_blocks, kBlock) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
+    }
+    // slices of rows too few to give every CU one, held in registers if they are short
+    const int64_t parts = std::min({ceil_div(vecs, kLeastSlice), std::max<int64_t>(1, cus / rows), kBeamLists / beams});
+    const int64_t slice = ceil_div(vecs, parts);
+    p->path = parts > 1 ? ARGREDUCE_PATH_SPLIT : ARGREDUCE_PATH_BLOCK;
+    if (rows <= cus && slice <= kSliceVecs * kSliceThreads) {
+        p->team = kSliceThreads;
+        p->held = static_cast<int>(next_pow2(ceil_div(slice, kSliceThreads)));
     } else {
-        // slices of rows too few to give every CU one
-        parts = std::min({ceil_div(vecs, kLeastSlice), std::max<int64_t>(1, cus / rows), kBeamLists / beams});
-        p->path = parts > 1 ? ARGREDUCE_PATH_SPLIT : ARGREDUCE_PATH_BLOCK;
-        const int64_t slice = ceil_div(vecs, parts);
         p->team = slice > 2048 && rows * 1024 <= cap ? 1024 : slice > 4096 ? 512 : 256;
-        if (parts > 1 && slice <= kSliceVecs * kSliceThreads) {
-            p->team = kSliceThreads;
-            p->held = static_cast<int>(next_pow2(ceil_div(slice, kSliceThreads)));
-        }
     }
     p->parts = static_cast<int>(parts);
-    p->grid_blocks = p->team == 64 ? ceil_div(rows * parts, kBlock / 64) : rows * parts;
-    p->scratch_bytes = 15 + static_cast<size_t>(rows * parts) * beam_list_bytes(width);
-    return grid_too_large(p->grid_blocks, std::max<int64_t>(p->team, kBlock)) ||
-                   grid_too_large(groups, kBlock)
-               ? ARGREDUCE_ERR_TOO_WIDE
-               : ARGREDUCE_OK;
+    p->grid_blocks = rows * parts;
+    p->scratch_bytes = 15 + beam_scratch(std::max<int64_t>(1, groups), beams * parts, width);
+    return grid_too_large(p->grid_blocks, p->team) || grid_too_large(groups, kBlock) ? ARGREDUCE_ERR_TOO_WIDE
+                                                                                     : ARGREDUCE_OK;
 }
 
 // One dimension of a state, in bytes.
@@ -95,17 +100,18 @@ ARGREDUCE_EXPORT int argreduce_beam_plan(int64_t groups, int64_t beams, int64_t 
     if (rc != ARGREDUCE_OK) return rc;
     *out = argreduce_plan_t{};
     out->path = p.path;
+    const bool wave = p.path == ARGREDUCE_PATH_SUBWAVE;
     out->lanes_per_row = p.team * p.parts;
     out->blocks_per_row = p.parts;
-    out->block_threads = p.team == 64 ? static_cast<int32_t>(kBlock) : p.team;
+    out->block_threads = wave ? static_cast<int32_t>(kBlock) : p.team;
     out->grid_blocks = p.grid_blocks;
-    out->outputs_per_block = p.team == 64 ? static_cast<int32_t>(kBlock / 64) : 1;
+    out->outputs_per_block = wave ? static_cast<int32_t>(kBlock / 64 * beams) : 1;
     out->grid_rows = p.grid_blocks * out->outputs_per_block / p.parts;
-    out->unroll = logits_elem_size(dtype);  // 16 elements per lane and step
+    out->unroll = p.held > 0 ? p.held : logits_elem_size(dtype);  // 16 elements per lane and step
     out->device_threads = p.device_threads;
     out->scratch_bytes = p.scratch_bytes;
     out->load_bytes = 16;
-    out->dispatches = 2;
+    out->dispatches = p.held > 0 ? 1 : 2;
     return ARGREDUCE_OK;
 }
 

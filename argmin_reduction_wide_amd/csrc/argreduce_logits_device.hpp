@@ -81,6 +81,51 @@ __device__ inline float lanes_sum(float v) {
     return lanes_all<G>(v, [](float a, float b) { return a + b; });
 }
 
+// The sum of G lanes' values in binary64, in every lane (by DPP and lane swaps: six shuffles through LDS
+// took 900 cycles).
+template <int CTRL>
+__device__ inline double dpp64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = dpp_u32<CTRL, 0xf>(static_cast<uint32_t>(u));
+    const uint32_t hi = dpp_u32<CTRL, 0xf>(static_cast<uint32_t>(u >> 32));
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// v of each lane's own half of 32 (HALF 16) or 64 (HALF 32) lanes and of the other one: the same two in both.
+template <int HALF>
+__device__ inline void halves(uint32_t v, uint32_t& a, uint32_t& b) {
+    const auto r = HALF == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                              : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
+}
+template <int HALF>
+__device__ inline void halves64(double v, double& a, double& b) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    uint32_t l[2], h[2];
+    halves<HALF>(static_cast<uint32_t>(u), l[0], l[1]);
+    halves<HALF>(static_cast<uint32_t>(u >> 32), h[0], h[1]);
+    a = __builtin_bit_cast(double, static_cast<uint64_t>(h[0]) << 32 | l[0]);
+    b = __builtin_bit_cast(double, static_cast<uint64_t>(h[1]) << 32 | l[1]);
+}
+template <int G = kWave>
+__device__ inline double lanes_sum64(double v) {
+    static_assert(G >= 16, "whole rows of lanes");
+    v += dpp64<0xB1>(v);
+    v += dpp64<0x4E>(v);
+    v += dpp64<0x141>(v);
+    v += dpp64<0x140>(v);
+    double a, b;
+    if constexpr (G >= 32) {
+        halves64<16>(v, a, b);
+        v = a + b;
+    }
+    if constexpr (G >= 64) {
+        halves64<32>(v, a, b);
+        v = a + b;
+    }
+    return v;
+}
+
 // A team is one wavefront (T == 64, four teams to a workgroup) or one workgroup of T threads.
 // The barrier orders LDS accesses only: __syncthreads() would also wait for every load and store
 // to global memory under way, which no team exchanges anything through.

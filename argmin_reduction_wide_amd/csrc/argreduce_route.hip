@@ -48,13 +48,12 @@ struct Key16 {
     __device__ static T dpp(T v) {
         return static_cast<T>(dpp_u32<CTRL, 0xf>(static_cast<uint32_t>(v)));
     }
-    // v of each lane's own half (of 16 or 32 lanes) and of the other one: the same two in both.
     template <int HALF>
-    __device__ static void halves(T v, T& a, T& b) {
-        const auto r = HALF == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
-                                  : __builtin_amdgcn_permlane32_swap(v, v, false, false);
-        a = static_cast<T>(r[0]);
-        b = static_cast<T>(r[1]);
+    __device__ static void both(T v, T& a, T& b) {
+        uint32_t x, y;
+        halves<HALF>(static_cast<uint32_t>(v), x, y);
+        a = static_cast<T>(x);
+        b = static_cast<T>(y);
     }
     // The keys of a vector's eight elements; the first is expert `col`.
     __device__ static void make(const u32x4 q, uint32_t col, T (&k)[8]) {
@@ -108,19 +107,11 @@ struct Key<F32> {
     }
     template <int CTRL>
     __device__ static T dpp(T v) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        const uint32_t lo = dpp_u32<CTRL, 0xf>(static_cast<uint32_t>(u));
-        const uint32_t hi = dpp_u32<CTRL, 0xf>(static_cast<uint32_t>(u >> 32));
-        return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+        return dpp64<CTRL>(v);
     }
     template <int HALF>
-    __device__ static void halves(T v, T& a, T& b) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        int32_t l[2], h[2];
-        Key16::halves<HALF>(static_cast<int32_t>(u), l[0], l[1]);
-        Key16::halves<HALF>(static_cast<int32_t>(u >> 32), h[0], h[1]);
-        a = __builtin_bit_cast(double, static_cast<uint64_t>(static_cast<uint32_t>(h[0])) << 32 | static_cast<uint32_t>(l[0]));
-        b = __builtin_bit_cast(double, static_cast<uint64_t>(static_cast<uint32_t>(h[1])) << 32 | static_cast<uint32_t>(l[1]));
+    __device__ static void both(T v, T& a, T& b) {
+        halves64<HALF>(v, a, b);
     }
     __device__ static void make(const u32x4 q, uint32_t col, T (&k)[4]) {
 #pragma unroll
@@ -210,7 +201,7 @@ __device__ inline void best_of_lanes(typename K::T (&a)[L]) {
     const auto across = [&](auto half) {
         typename K::T b[L];
 #pragma unroll
-        for (int i = 0; i < L; ++i) K::template halves<decltype(half)::value>(a[i], a[i], b[i]);
+        for (int i = 0; i < L; ++i) K::template both<decltype(half)::value>(a[i], a[i], b[i]);
         merge<K, L>(a, b);
     };
     if constexpr (G >= 2) with(Int<0xB1>{});
@@ -228,11 +219,11 @@ __device__ inline typename K::T lanes_best(typename K::T v) {
     if constexpr (G >= 16) v = K::max(v, K::template dpp<0x140>(v));
     typename K::T a = v, b = v;
     if constexpr (G >= 32) {
-        K::template halves<16>(v, a, b);
+        K::template both<16>(v, a, b);
         v = K::max(a, b);
     }
     if constexpr (G >= 64) {
-        K::template halves<32>(v, a, b);
+        K::template both<32>(v, a, b);
         v = K::max(a, b);
     }
     return v;
@@ -300,12 +291,6 @@ struct Group {
         set_partials = partials + static_cast<size_t>(blocks) * (experts + 1);
     }
 };
-
-__device__ inline double lanes_sum64(double v) {
-#pragma unroll
-    for (int o = 1; o < kWave; o *= 2) v += __shfl_xor(v, o);
-    return v;
-}
 
 struct JoinLds {
     double share[kRouteThreads];

@@ -89,7 +89,8 @@ def check(x, scores, width, temperature=1.0, ended=None, end=None, **kw):
 
 SHAPES = [(1, 1, 1, 1), (5, 3, 2, 3), (21, 4, 7, 4), (11, 1, 64, 5), (21, 5, 65, 10), (11, 3, 129, 64), (11, 4, 500, 4),
           (11, 2, 1025, 17), (11, 6, 2049, 6), (10, 3, 4100, 33), (3, 7, 8200, 14), (2, 4, 16411, 4), (1, 64, 300, 64),
-          (2, 33, 2100, 40)]
+          (2, 33, 2100, 40), (10, 4, 1000, 9), (10, 8, 500, 8), (10, 16, 60, 20), (10, 30, 60, 64), (10, 64, 16, 64),
+          (300, 3, 700, 3), (40, 7, 3001, 7)]
 
 
 @pytest.mark.parametrize("dtype", sorted(DT))

@@ -46,10 +46,14 @@ def test_step_arguments(lib, at, value, status):
 
 
 def test_step_scratch(lib):
-    need = B.argreduce_beam_scratch_bytes(2, 4, 100, "f32", 4)
-    assert need == 15 + 8 * (16 + 4 * 8)
+    assert B.argreduce_beam_scratch_bytes(2, 4, 100, "f32", 4) == 0  # a wavefront per group
+    args = list(STEP)
+    args[4:6] = [9000, 9000]
+    need = B.argreduce_beam_scratch_bytes(2, 4, 9000, "f32", 4)
+    lists = 4 * B.argreduce_beam_plan(2, 4, 9000, "f32", 4)["blocks_per_row"]
+    assert need == 15 + 2 * 8 * (2 + lists * (3 + 4))
     for ptr, size in [(0, need), (FAKE, need - 1), (0, 0)]:
-        assert both(lib, "argreduce_beam_step", *STEP[:12], ptr, size, 0) == -4
+        assert both(lib, "argreduce_beam_step", *args[:12], ptr, size, 0) == -4
     assert B.argreduce_beam_out_bytes(3, 5) == 15 * 21
     for bad in [(-1, 4), (2, 0), (2, 65), (1 << 31, 1)]:
         assert B.argreduce_beam_out_bytes(*bad) == B.SIZE_MAX
