@@ -8,6 +8,7 @@ torch supplies device memory and the current stream; the arithmetic runs in the 
 from __future__ import annotations
 
 import ctypes
+from bisect import bisect_left
 from typing import NamedTuple, Optional
 
 import torch
@@ -103,12 +104,16 @@ def beam_step(logits, scores, width: Optional[int] = None, *, temperature: float
 
 
 def _contiguous(shape):
-    if len(shape) == 2:
+    """Strides of a contiguous tensor."""
+    d = len(shape)
+    if d == 3:
+        return (shape[1] * shape[2], shape[2], 1)
+    if d == 2:
         return (shape[1], 1)
     strides, n = [], 1
     for s in reversed(shape):
         strides.append(n)
-        n *= max(1, s)
+        n *= s
     return tuple(reversed(strides))
 
 
@@ -158,7 +163,8 @@ class BeamStates:
     positions, heads, size] are both fine, and so are slices of longer caches.
 
     The tensors are held, not copied: they must keep their memory (no ``resize_`` or ``set_``), and may
-    share no memory with each other. Made once, outside of a graph capture."""
+    share no memory with each other. Made once, outside of a graph capture; a graph that captured a
+    reordering reads this object's memory, which must live as long as the graph."""
 
     def __init__(self, states, *, dim: Optional[int] = None):
         states = [states] if isinstance(states, torch.Tensor) else list(states)
@@ -175,11 +181,14 @@ class BeamStates:
         self.groups, self.beams = first.shape[:2]
         if not 1 <= self.beams <= BEAM_MAX:
             raise ValueError(f"a group must have 1..{BEAM_MAX} beams; got {self.beams}")
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("BeamStates cannot be made in a capture: make it before")
         self.states, self.device = states, first.device
         used = [t for t in states if t.numel()]
         spans = sorted(_span(t) for t in used)
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise ValueError("states must not overlap (pass interleaved ones as one tensor)")
+        self._starts, self._ends = [a[0] for a in spans], [a[1] for a in spans]
         table = (B.argreduce_state_t * max(1, len(used)))()
         for i, t in enumerate(used):
             d = dim
@@ -192,6 +201,7 @@ class BeamStates:
         if used:
             host = torch.frombuffer(bytearray(bytes(table)), dtype=torch.int64)
             self._table = host.to(self.device)
+            self._streams = {_stream(self.device.index)}  # those the table's memory is known to be used on
 
     def reorder(self, parents, *, first=None, last=None) -> None:
         """Every beam becomes a copy of its parent as that was before the call: ``state[g, b] =
@@ -210,15 +220,27 @@ class BeamStates:
             raise ValueError(f"parents must be contiguous and on {self.device}")
         if self._plan is None:
             return
+        self._apart(parents, "parents")
         first_ptr, first_value = self._positions(first, "first", 0)
         last_ptr, last_value = self._positions(last, "last", 1 << 62)
         if self.device.index != _device():
             with torch.cuda.device(self.device):
                 return self.reorder(parents, first=first, last=last)
+        stream = _stream(self.device.index)
+        if stream not in self._streams:
+            self._table.record_stream(torch.cuda.current_stream())
+            self._streams.add(stream)
         rc = _call.reorder(ctypes.addressof(self._plan), self._table.data_ptr(), parents.data_ptr(), first_ptr,
-                           last_ptr, first_value, last_value, _stream(self.device.index))
+                           last_ptr, first_value, last_value, stream)
         if rc:
             raise B.ArgreduceError(rc, f"argreduce_reorder(tensors={len(self.states)}, groups={groups}, beams={beams})")
+
+    def _apart(self, t, name: str) -> None:
+        """What the kernel reads while it moves the states lies in none of them."""
+        start = t.data_ptr()
+        i = bisect_left(self._starts, start + 8 * t.numel())  # states that begin before t's end
+        if i and self._ends[i - 1] > start:
+            raise ValueError(f"{name} must lie apart from the states")
 
     def _positions(self, given, name: str, default: int):
         """(address, value) of a bound."""
@@ -228,5 +250,6 @@ class BeamStates:
             if given.dtype is not _I64 or given.numel() != self.groups or given.device != self.device or \
                     not given.is_contiguous():
                 raise ValueError(f"{name} must be a number or contiguous int64 [{self.groups}] on {self.device}")
+            self._apart(given, name)
             return given.data_ptr(), 0
         return 0, min(max(int(given), 0), 1 << 62)

@@ -489,6 +489,88 @@ def test_reorder_refusals():
     torch.cuda.synchronize()
 
 
+def test_parents_inside_of_the_states_are_refused():
+    """A call would change what its other workgroups still read."""
+    announce("reorder by its own states")
+    tokens = torch.zeros(3, 4, dtype=torch.int64, device="cuda")
+    both = torch.zeros(2, 4, 8, 3, dtype=torch.int64, device="cuda")
+    handle = ar.BeamStates([both[0, :3, :4], tokens, both[1, :3, :4]])
+    p = torch.zeros(3, 4, dtype=torch.int64, device="cuda")
+    handle.reorder(p)
+    for bad in (tokens, both.view(-1)[:12].view(3, 4), both.view(-1)[90:102].view(3, 4)):
+        with pytest.raises(ValueError, match="parents must lie apart"):
+            handle.reorder(bad)
+    caches = ar.BeamStates(both.view(3, 4, 16), dim=2)
+    for name in ("first", "last"):
+        with pytest.raises(ValueError, match=f"{name} must lie apart"):
+            caches.reorder(p, **{name: both.view(-1)[189:]})
+    caches.reorder(tokens, last=p[:, 0].contiguous())
+    torch.cuda.synchronize()
+
+
+def test_states_made_in_a_capture_are_refused():
+    announce("states in a capture")
+    t = torch.zeros(3, 4, 5, device="cuda")
+    refused = False
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t.add_(1)
+        try:
+            ar.BeamStates(t)
+        except RuntimeError as e:
+            refused = "capture" in str(e)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert refused and (t == 1).all()
+
+
+def test_states_dropped_while_another_stream_moves_them():
+    """The table that the kernel reads is not given to another tensor before the kernel has run."""
+    announce("states dropped early")
+    t = torch.arange(4.0, device="cuda").expand(2, 4).contiguous()
+    p = torch.full((2, 4), 3, device="cuda")
+    handle = ar.BeamStates(t)
+    address, size = handle._table.data_ptr(), handle._table.numel() * 8
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        handle.reorder(p)
+    del handle
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    waiting = not side.query()
+    assert all(o.data_ptr() != address for o in others) or not waiting
+    torch.cuda.synchronize()
+    assert (t == 3).all()
+
+
+def test_calls_without_the_fast_module(monkeypatch):
+    """The same bits through ctypes alone."""
+    announce("ctypes")
+    import argmin_reduction_wide_amd.beams as module
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(3, 4, 9001, device="cuda", generator=g)
+    scores = torch.randn(3, 4, device="cuda", generator=g)
+    ended = torch.tensor([[True, False, False, True]] * 3, device="cuda")
+    states = torch.randn(3, 4, 2, 20, 8, device="cuda", generator=g)
+
+    def work():
+        t = states.clone()
+        r = ar.beam_step(x, scores, temperature=0.7, ended=ended, end_token=11)
+        ar.BeamStates(t, dim=3).reorder(r.parents, first=2, last=15)
+        return [*r, t]
+
+    fast = work()
+
+    class Ctypes:
+        def __getattr__(self, name):
+            return getattr(B.lib(), "argreduce_" + name)
+
+    monkeypatch.setattr(module, "_call", Ctypes())
+    for a, b in zip(fast, work()):
+        assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------------------------------
 # A search
 
