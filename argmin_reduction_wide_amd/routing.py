@@ -14,6 +14,7 @@ import torch
 from torch.autograd import forward_ad as _forward_ad
 
 from . import binding as B
+from .beams import _contiguous
 from .logits import (_F32, _I64, _Calls, _check_grad, _device, _elsewhere, _new_grad, _refuse_tangent, _rows, _same,
                      _scratch, _stream, _tuple)
 
@@ -27,7 +28,7 @@ class RouteExperts(NamedTuple):
     """What route_experts returns, for logits [..., tokens, experts]: weights (float32) and experts
     (int64), [..., tokens, top]; counts (int64 [..., experts]), how many tokens chose each expert; tokens
     (int64 [...]), how many there are; the losses balance and z (float32 [...]). ``totals`` is what
-    route_experts_grad takes; counts and tokens lie in its memory."""
+    route_experts_grad takes; without autograd counts, tokens, balance and z lie in its memory."""
 
     weights: torch.Tensor
     experts: torch.Tensor
@@ -62,19 +63,24 @@ def _refuse_captured_autograd(logits) -> None:
                            "capture")
 
 
-def _route(logits, top, live, renormalize, scratch) -> RouteExperts:
+def _route(logits, top, live, renormalize, scratch, apart=False) -> RouteExperts:
+    """apart: the weights in memory of their own (a write to them by the caller would count as one to what
+    the backward pass saves)."""
     code, groups, tokens, experts, stride, lead = _router(logits, top)
     if live is not None:
         _same(live, "live", logits, torch.bool, lead + (tokens,))
     device = logits.device
     if device.index != _device():
         with torch.cuda.device(device):
-            return _route(logits, top, live, renormalize, scratch)
+            return _route(logits, top, live, renormalize, scratch, apart)
     shape = lead + (tokens, top)
-    weights = torch.empty(shape, dtype=_F32, device=device)
-    chosen = torch.empty(shape, dtype=_I64, device=device)
-    # counts, tokens (8 bytes each), balance and z (4 each), one after another
-    totals = torch.empty(groups * (experts + 2), dtype=_I64, device=device)
+    # totals (counts, tokens: 8 bytes each, balance and z: 4 each, one after another), experts (8) and weights (4)
+    per, n = groups * (experts + 2), groups * tokens * top
+    out = torch.empty(per + n + (0 if apart else (n + 1) // 2), dtype=_I64, device=device)
+    strides, floats = _contiguous(shape), out.view(_F32)
+    totals = out.as_strided((per,), (1,))
+    chosen = out.as_strided(shape, strides, per)
+    weights = torch.empty(shape, dtype=_F32, device=device) if apart else floats.as_strided(shape, strides, 2 * (per + n))
     need = _call.route_scratch_bytes(groups, tokens, experts, code)
     sptr = sbytes = 0
     if need or scratch is not None:
@@ -85,26 +91,18 @@ def _route(logits, top, live, renormalize, scratch) -> RouteExperts:
     if rc:
         raise B.ArgreduceError(rc, f"argreduce_route(groups={groups}, tokens={tokens}, experts={experts}, "
                                    f"row_stride={stride}, top={top})")
-    counts, number, balance, z = _totals(totals, groups, experts, lead)
-    return _tuple(RouteExperts, (weights, chosen, counts, number, balance, z, totals))
-
-
-def _totals(totals, groups, experts, lead):
-    """The four parts of totals, in the logits' leading shape."""
     n = groups * experts
-    losses = totals.view(_F32)
-    if len(lead) == 1:  # (views by strides are the cheapest ones)
-        one = (1,)
-        return (totals.as_strided((groups, experts), (experts, 1)), totals.as_strided(lead, one, n),
-                losses.as_strided(lead, one, 2 * (n + groups)), losses.as_strided(lead, one, 2 * n + 3 * groups))
-    return (totals[:n].view(*lead, experts), totals[n:n + groups].view(lead),
-            losses[2 * (n + groups):][:groups].view(lead), losses[2 * n + 3 * groups:].view(lead))
+    each = _contiguous(lead)
+    return _tuple(RouteExperts, (
+        weights, chosen, out.as_strided(lead + (experts,), _contiguous(lead + (experts,))),
+        out.as_strided(lead, each, n), floats.as_strided(lead, each, 2 * (n + groups)),
+        floats.as_strided(lead, each, 2 * n + 3 * groups), totals))
 
 
 class _RouteExperts(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top, live, renormalize, scratch):
-        r = _route(logits, top, live, renormalize, scratch)
+        r = _route(logits, top, live, renormalize, scratch, True)
         ctx.save_for_backward(logits, r.experts, r.totals)
         ctx.renormalize = renormalize
         # outputs of their own, which may be written over, and no views of what the backward pass reads
@@ -162,7 +160,7 @@ def _grad(logits, experts, totals, grad_weights, grad_balance, grad_z, live, ren
         _same(grad_z, "grad_z", logits, _F32, lead)
     out = _new_grad(logits) if out is None else _check_grad(
         logits, groups * tokens, cols, stride, out, experts=experts, totals=totals, grad_weights=grad_weights,
-        grad_balance=grad_balance, grad_z=grad_z)
+        grad_balance=grad_balance, grad_z=grad_z, live=live)
     if _elsewhere(logits):
         with torch.cuda.device(logits.device):
             return _grad(logits, experts, totals, grad_weights, grad_balance, grad_z, live, renormalize, out)

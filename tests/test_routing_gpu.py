@@ -388,6 +388,68 @@ def test_refusals():
     torch.cuda.synchronize()
 
 
+def test_gradient_over_the_mask_is_refused():
+    announce("route gradient over the mask")
+    room = torch.zeros(4 * 192 + 12, dtype=torch.uint8, device="cuda")
+    live, out = room[760:772].view(torch.bool).view(2, 6), room[:768].view(torch.float32).view(2, 6, 16)
+    x = torch.randn(2, 6, 16, device="cuda")
+    live.fill_(True)
+    r = ar.route_experts(x, 2, live=live)
+    with pytest.raises(ValueError, match="out must not overlap live"):
+        ar.route_experts_grad(x, r, r.weights, live=live, out=out)
+    torch.cuda.synchronize()
+
+
+def test_weights_may_be_written_over():
+    """What a caller writes into a result changes nothing that the gradient reads."""
+    announce("route results written over")
+    x = torch.randn(3, 7, 16, device="cuda")
+    g = torch.randn(3, 7, 4, device="cuda")
+
+    def work(write):
+        y = x.clone().requires_grad_()
+        r = ar.route_experts(y, 4)
+        loss = (r.weights * g).sum() + r.balance.sum() + r.z.sum()
+        if write:
+            for t in (r.experts, r.counts, r.tokens):
+                t.fill_(-7)
+            with torch.no_grad():
+                r.weights.fill_(9.0)
+        loss.backward()
+        return y.grad
+
+    want = work(False)
+    assert torch.equal(work(True), want)
+    r = ar.route_experts(x, 4)
+    r.weights.fill_(9.0)
+    one = torch.ones(3, device="cuda")
+    assert torch.equal(ar.route_experts_grad(x, r, g, one, one), want)
+
+
+def test_calls_without_the_fast_module(monkeypatch):
+    """The same bits through ctypes alone."""
+    announce("ctypes")
+    import argmin_reduction_wide_amd.routing as module
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(3, 501, 60, device="cuda", generator=g)
+    w, v = torch.rand(3, 501, 6, device="cuda", generator=g), torch.rand(3, device="cuda", generator=g)
+    live = torch.rand(3, 501, device="cuda", generator=g) < 0.9
+
+    def work():
+        r = ar.route_experts(x, 6, live=live, renormalize=True)
+        return [*r, ar.route_experts_grad(x, r, w, v, v, live=live, renormalize=True)]
+
+    fast = work()
+
+    class Ctypes:
+        def __getattr__(self, name):
+            return getattr(B.lib(), "argreduce_" + name)
+
+    monkeypatch.setattr(module, "_call", Ctypes())
+    for a, b in zip(fast, work()):
+        assert torch.equal(a, b)
+
+
 def test_expert_numbers_beyond_the_row():
     """Bad numbers in what is passed back make no access out of range."""
     announce("route bad experts")
