@@ -92,7 +92,8 @@ struct JoinLds {
     uint16_t near[kBeamLists];  // lists whose heads can be among the width best
     uint16_t entries[kBeamLists];
     uint16_t list[kBeamMax];    // of the r-th best head
-    uint32_t close, bound, count;
+    uint32_t least[kSliceThreads / kWave];  // of each wavefront's candidates
+    uint32_t close, bound, count, picked;
 };
 // What can be among the width best, at most entry j of the list whose head is the r-th best where r + j < width: in LDS
 // that the launch sizes (beam_cands).
@@ -102,12 +103,14 @@ __host__ __device__ inline uint32_t beam_room(uint32_t width) {
 }
 struct Cands {
     uint64_t *value, *key;
+    uint16_t* picked;  // numbers of those that are ranked
     uint8_t* beam;
     __device__ Cands(uint64_t* lds, uint32_t width) {
         const uint32_t n = beam_room(width);
         value = lds;
         key = lds + n;
-        beam = reinterpret_cast<uint8_t*>(lds + 2 * n);
+        picked = reinterpret_cast<uint16_t*>(lds + 2 * n);
+        beam = reinterpret_cast<uint8_t*>(picked + n);
     }
     __device__ Cand get(uint32_t i) const { return {value[i], key[i], beam[i]}; }
     __device__ void put(uint32_t i, const Cand& c) const {
@@ -116,7 +119,7 @@ struct Cands {
         beam[i] = static_cast<uint8_t>(c.beam);
     }
 };
-inline size_t beam_cands(uint32_t width) { return static_cast<size_t>(beam_room(width)) * 17; }
+inline size_t beam_cands(uint32_t width) { return static_cast<size_t>(beam_room(width)) * 19; }
 
 // Outputs of all groups, one after another: parents, tokens (int64), scores (float), ended (bytes).
 struct BeamOut {
@@ -256,7 +259,7 @@ __device__ inline void join(JoinLds& L, const Cands& cands, const Step& a, const
         rows(Int<32>{});
     else
         rows(Int<64>{});
-    if (tid == 0) L.count = 0;
+    if (tid == 0) L.count = L.picked = 0;
     if (tid < kBeamMax) L.list[tid] = kNoList;
     __syncthreads();
     Cand head{0, 0, 0};
@@ -331,15 +334,45 @@ __device__ inline void join(JoinLds& L, const Cands& cands, const Step& a, const
         }
         __syncthreads();
     }
+    // Of many, those are ranked that reach the smallest of the bounds that an even share of the width best reaches
+    // among each wavefront's (200 ranked candidates took 20 us).
+    const uint32_t all = L.count;
+    uint32_t n = all;
+    if (all > kWave) {
+        constexpr uint32_t kWaves = T / kWave;
+        const uint32_t each = (width + kWaves - 1) / kWaves, wave = tid / kWave;
+        const auto least = [&](auto words) {
+            constexpr int P = decltype(words)::value;
+            uint32_t o[P], some = 0;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const uint32_t at = tid % kWave * kWaves + wave + i * T;
+                o[i] = at < all ? high_of(cands.value[at]) : 0;
+                some += __popcll(__ballot(o[i] != 0));
+            }
+            return some < each ? 0 : bisect(o, each, each + each / 4 + 1);
+        };
+        constexpr uint32_t kMost = kBeamMax * (kBeamMax + 1) / 2;
+        const uint32_t mine = all <= T ? least(Int<1>{}) : least(Int<(kMost + T - 1) / T>{});
+        if (tid % kWave == 0) L.least[wave] = mine;
+        __syncthreads();
+        uint32_t enough = L.least[0];
+#pragma unroll
+        for (uint32_t i = 1; i < kWaves; ++i) enough = L.least[i] < enough ? L.least[i] : enough;
+        for (uint32_t i = tid; i < all; i += T)
+            if (high_of(cands.value[i]) >= enough) cands.picked[atomicAdd(&L.picked, 1u)] = static_cast<uint16_t>(i);
+        __syncthreads();
+        n = L.picked;
+    }
+    const auto ranked = [&](uint32_t i) { return cands.get(all > kWave ? cands.picked[i] : i); };
     // ranks: several lanes count for a candidate, each over its share of the others
-    const uint32_t n = L.count;
     const size_t first = static_cast<size_t>(a.g) * width;
     const uint32_t lg = n <= T / 16 ? 4 : n <= T / 8 ? 3 : n <= T / 4 ? 2 : n <= T / 2 ? 1 : 0;
     for (uint32_t i = tid >> lg; i < n; i += T >> lg) {
-        const Cand c = cands.get(i);
+        const Cand c = ranked(i);
         uint32_t rank = 0;
 #pragma unroll 2
-        for (uint32_t j = tid & ((1u << lg) - 1); j < n; j += 1u << lg) rank += cands.get(j).above(c) ? 1 : 0;
+        for (uint32_t j = tid & ((1u << lg) - 1); j < n; j += 1u << lg) rank += ranked(j).above(c) ? 1 : 0;
         rank = lanes_sum_u32(rank, lg);
         if ((tid & ((1u << lg) - 1)) == 0 && rank < width) out.put(first + rank, c, a.end_token);
     }
@@ -433,9 +466,15 @@ __global__ __launch_bounds__(kSliceThreads) void k_beam_join(uint64_t scores, ui
 // that k / 4 lanes of each wavefront reach; what reaches that, less than 2 k as a rule, is collected and ranked by
 // counting. (By a bound for k of each wavefront alone, 16 best of 6300 elements took 9000 cycles more.)
 
-constexpr int kSliceWaves = kSliceThreads / kWave;
-constexpr int kSliceCap = 1024;  // keys that a workgroup collects, an even share by each wavefront
-static_assert(kSliceCap >= kSliceWaves * kBeamMax, "the k best of each wavefront fit");
+template <int W>
+struct SliceLds {
+    static constexpr uint32_t kCap = 256;  // keys that a wavefront collects
+    static_assert(kCap >= kBeamMax, "the k best of each wavefront fit");
+    Stat stat[W];
+    uint32_t bound[W], total;
+    uint64_t best[W][kBeamMax];
+    uint64_t buf[W * kCap];
+};
 
 // A vector as the compiler does not know it: what was made of it before is not kept in registers.
 template <typename Vec>
@@ -553,17 +592,129 @@ __device__ inline uint32_t wave_best(const typename Fmt::Vec (&q)[NV], uint32_t 
     return taken;
 }
 
-// One slice of up to NV vectors per lane.
+// One slice of up to NV vectors per lane, by W wavefronts.
+template <typename Fmt, int NV, int W>
+__device__ inline void hold_slice(SliceLds<W>& L, const SliceJob& j, const Scratch& w, uint64_t x, uint32_t stride,
+                                  float k_hi) {
+    constexpr int VW = Fmt::VW, T = W * kWave;
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const RowSpan<Fmt> sp(row_ptr<Fmt>(addr<const void>(x), j.row, stride), j.cols);
+    const uint32_t n = part_vecs(span_max<Fmt>(j.cols), j.parts);  // the row's last vector is in the last slices
+    const uint32_t first = j.part * n, vecs = sp.vb + (j.cols % VW ? 1 : 0);
+    const uint32_t last = first < vecs ? (vecs - first < n ? vecs : first + n) : first;
+    typename Fmt::Vec q[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const uint32_t v = first + tid + u * T;
+        q[u] = masked16<Fmt>();
+        if (v < last) {
+            if (v < sp.vb) {
+                q[u] = sp.load_whole(v);
+            } else {
+                q[u] = sp.load_tail();
+            }
+        }
+    }
+    Stat a;
+    a.init();
+    float most = -__builtin_huge_valf();  // the lane's maximum
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float e[VW];
+        Fmt::unpack(q[u], e);
+        most = max_f(most, max_of(e));
+    }
+    a.m = lanes_max<kWave>(max_f(most, kLowest));
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float e[VW];
+        Fmt::unpack(anew(q[u]), e);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            const float z = (e[i] - a.m) * k_hi;
+            const float p = exp2_f(z);
+            a.s += p;
+            a.h = fmaf(p, max_f(z, kZFloor), a.h);
+        }
+    }
+    a.s = lanes_sum<kWave>(a.s);
+    a.h = lanes_sum<kWave>(a.h);
+    const uint32_t enough = a.s > 0.0f ? wave_bound<Fmt>(most, (j.width + W - 1) / W) : 0;
+    if (lane == 0) {
+        L.stat[wave] = a;
+        L.bound[wave] = enough;
+    }
+    if (tid == 0) L.total = 0;
+    __syncthreads();
+    uint32_t bound = L.bound[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) bound = L.bound[w] < bound ? L.bound[w] : bound;
+    if (bound == 0) bound = wave_bound<Fmt>(most, j.width);  // a wavefront with next to nothing
+    bound <<= kLowBits<Fmt>;
+    const float tau = bound > order_of(kLowest) ? value_of(bound) : kLowest;
+    const uint32_t pos = (first + tid) * VW;
+    // the lanes' hits, and those of the lanes before each
+    Hits<Fmt, NV> hits(q, a.s > 0.0f ? tau : __builtin_nanf(""));
+    uint32_t at = hits.count;
+#pragma unroll
+    for (int off = 1; off < kWave; off *= 2) {
+        const uint32_t other = __shfl_up(at, off);
+        at += lane >= off ? other : 0;
+    }
+    const uint32_t many = __builtin_amdgcn_readlane(at, kWave - 1);
+    at -= hits.count;
+    uint32_t place = 0;
+    if (many <= L.kCap) {
+        if (lane == 0) place = atomicAdd(&L.total, many);
+        at += __builtin_amdgcn_readfirstlane(place);
+        hits.each(q, pos, T * VW, [&](uint64_t key) { L.buf[at++] = key; });
+    } else {  // ties
+        const uint32_t n = wave_best<Fmt, NV>(q, pos, T * VW, j.width, L.best[wave], lane);
+        team_sync<kWave>();
+        if (lane == 0) place = atomicAdd(&L.total, n);
+        place = __builtin_amdgcn_readfirstlane(place);
+        if (static_cast<uint32_t>(lane) < n) L.buf[place + lane] = L.best[wave][lane];
+    }
+    __syncthreads();
+    // every thread merges the four statistics
+    Stat all = L.stat[0];
+#pragma unroll
+    for (int x = 1; x < W; ++x) {
+        Stat o = L.stat[x];
+        const float to = max_f(all.m, o.m);
+        all.move<true>(to, k_hi);
+        o.move<true>(to, k_hi);
+        all.s += o.s;
+        all.h += o.h;
+    }
+    // ranks: several lanes count for a key, each over its share of the others
+    const uint32_t total = L.total;
+    const bool ok = all.s > 0.0f;
+    const uint32_t lg = total <= 16 ? 4 : total <= 32 ? 3 : total <= 64 ? 2 : total <= 128 ? 1 : 0;
+    for (uint32_t i = tid >> lg; ok && i < total; i += T >> lg) {
+        const uint64_t key = L.buf[i];
+        uint32_t rank = 0;
+#pragma unroll 4
+        for (uint32_t y = tid & ((1u << lg) - 1); y < total; y += 1u << lg) rank += L.buf[y] > key ? 1 : 0;
+        rank = lanes_sum_u32(rank, lg);
+        if ((tid & ((1u << lg) - 1)) == 0 && rank < j.width)
+            store_part(w.lists + static_cast<size_t>(j.list()) * j.width + rank, key);
+    }
+    if (tid == 0) {
+        store_part(w.slices + 2 * j.list(), two(all.m, __float_as_uint(all.s)));
+        store_part(w.slices + 2 * j.list() + 1, two(all.h, ok ? (total < j.width ? total : j.width) : 0));
+    }
+}
+
+// Few slices: the last one joins.
 template <typename Fmt, int NV>
 __global__ __launch_bounds__(kSliceThreads) void k_beam_slice(uint64_t x, uint64_t scores, uint64_t ended,
                                                               uint64_t scratch, uint64_t out, uint32_t stride,
                                                               uint32_t end_token, float k_hi, uint32_t nonce) {
-    constexpr int VW = Fmt::VW;
-    __shared__ Stat s_stat[kSliceWaves];
-    __shared__ uint32_t s_bound[kSliceWaves], s_total, s_found;
-    __shared__ uint64_t s_best[kSliceWaves][kBeamMax];
+    __shared__ uint32_t s_found;
     __shared__ union Lds {
-        uint64_t buf[kSliceCap];
+        SliceLds<kSliceThreads / kWave> slice;
         JoinLds join;
         __device__ Lds() {}
     } lds;
@@ -571,118 +722,18 @@ __global__ __launch_bounds__(kSliceThreads) void k_beam_slice(uint64_t x, uint64
     const SliceJob j(x, scores, ended, scratch, end_token);
     const Scratch w(addr<uint8_t>(scratch), j.groups, j.step.g, j.beams * j.parts, j.width);
     const uint64_t generation = load_part(w.generation);
-    const int tid = threadIdx.x, lane = tid % kWave;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    auto& buf = lds.buf;
-    if (j.on()) {
-        const RowSpan<Fmt> sp(row_ptr<Fmt>(addr<const void>(x), j.row, stride), j.cols);
-        const uint32_t n = part_vecs(span_max<Fmt>(j.cols), j.parts);  // the row's last vector is in the last slices
-        const uint32_t first = j.part * n, vecs = sp.vb + (j.cols % VW ? 1 : 0);
-        const uint32_t last = first < vecs ? (vecs - first < n ? vecs : first + n) : first;
-        typename Fmt::Vec q[NV];
-#pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            const uint32_t v = first + tid + u * kSliceThreads;
-            q[u] = masked16<Fmt>();
-            if (v < last) {
-                if (v < sp.vb) {
-                    q[u] = sp.load_whole(v);
-                } else {
-                    q[u] = sp.load_tail();
-                }
-            }
-        }
-        Stat a;
-        a.init();
-        float most = -__builtin_huge_valf();  // the lane's maximum
-#pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            float e[VW];
-            Fmt::unpack(q[u], e);
-            most = max_f(most, max_of(e));
-        }
-        a.m = lanes_max<kWave>(max_f(most, kLowest));
-#pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            float e[VW];
-            Fmt::unpack(anew(q[u]), e);
-#pragma unroll
-            for (int i = 0; i < VW; ++i) {
-                const float z = (e[i] - a.m) * k_hi;
-                const float p = exp2_f(z);
-                a.s += p;
-                a.h = fmaf(p, max_f(z, kZFloor), a.h);
-            }
-        }
-        a.s = lanes_sum<kWave>(a.s);
-        a.h = lanes_sum<kWave>(a.h);
-        const uint32_t enough = a.s > 0.0f ? wave_bound<Fmt>(most, (j.width + kSliceWaves - 1) / kSliceWaves) : 0;
-        if (lane == 0) {
-            s_stat[wave] = a;
-            s_bound[wave] = enough;
-        }
-        if (tid == 0) s_total = 0;
-        __syncthreads();
-        uint32_t bound = s_bound[0];
-#pragma unroll
-        for (int w = 1; w < kSliceWaves; ++w) bound = s_bound[w] < bound ? s_bound[w] : bound;
-        if (bound == 0) bound = wave_bound<Fmt>(most, j.width);  // a wavefront with next to nothing
-        bound <<= kLowBits<Fmt>;
-        const float tau = bound > order_of(kLowest) ? value_of(bound) : kLowest;
-        const uint32_t pos = (first + tid) * VW;
-        // the lanes' hits, and those of the lanes before each
-        Hits<Fmt, NV> hits(q, a.s > 0.0f ? tau : __builtin_nanf(""));
-        uint32_t at = hits.count;
-#pragma unroll
-        for (int off = 1; off < kWave; off *= 2) {
-            const uint32_t other = __shfl_up(at, off);
-            at += lane >= off ? other : 0;
-        }
-        const uint32_t many = __builtin_amdgcn_readlane(at, kWave - 1);
-        at -= hits.count;
-        uint32_t place = 0;
-        if (many <= kSliceCap / kSliceWaves) {
-            if (lane == 0) place = atomicAdd(&s_total, many);
-            at += __builtin_amdgcn_readfirstlane(place);
-            hits.each(q, pos, kSliceThreads * VW, [&](uint64_t key) { buf[at++] = key; });
-        } else {  // ties
-            const uint32_t n = wave_best<Fmt, NV>(q, pos, kSliceThreads * VW, j.width, s_best[wave], lane);
-            team_sync<kWave>();
-            if (lane == 0) place = atomicAdd(&s_total, n);
-            place = __builtin_amdgcn_readfirstlane(place);
-            if (static_cast<uint32_t>(lane) < n) buf[place + lane] = s_best[wave][lane];
-        }
-        __syncthreads();
-        // every thread merges the four statistics
-        Stat all = s_stat[0];
-#pragma unroll
-        for (int x = 1; x < kSliceWaves; ++x) {
-            Stat o = s_stat[x];
-            const float to = max_f(all.m, o.m);
-            all.move<true>(to, k_hi);
-            o.move<true>(to, k_hi);
-            all.s += o.s;
-            all.h += o.h;
-        }
-        // ranks: several lanes count for a key, each over its share of the others
-        const uint32_t total = s_total;
-        const bool ok = all.s > 0.0f;
-        const uint32_t lg = total <= 16 ? 4 : total <= 32 ? 3 : total <= 64 ? 2 : total <= 128 ? 1 : 0;
-        for (uint32_t i = tid >> lg; ok && i < total; i += kSliceThreads >> lg) {
-            const uint64_t key = buf[i];
-            uint32_t rank = 0;
-#pragma unroll 4
-            for (uint32_t y = tid & ((1u << lg) - 1); y < total; y += 1u << lg) rank += buf[y] > key ? 1 : 0;
-            rank = lanes_sum_u32(rank, lg);
-            if ((tid & ((1u << lg) - 1)) == 0 && rank < j.width)
-                store_part(w.lists + static_cast<size_t>(j.list()) * j.width + rank, key);
-        }
-        if (tid == 0) {
-            store_part(w.slices + 2 * j.list(), two(all.m, __float_as_uint(all.s)));
-            store_part(w.slices + 2 * j.list() + 1, two(all.h, ok ? (total < j.width ? total : j.width) : 0));
-        }
-    }
+    if (j.on()) hold_slice<Fmt, NV>(lds.slice, j, w, x, stride, k_hi);
     join_if_last<kSliceThreads>(lds.join, s_cands, &s_found, j, w, generation, nonce, k_hi, out);
+}
+
+// Many rows of up to 512 vectors: a wavefront each, and the join is a launch of its own.
+template <typename Fmt, int NV>
+__global__ __launch_bounds__(kWave) void k_beam_rows(uint64_t x, uint64_t scores, uint64_t ended, uint64_t scratch,
+                                                         uint32_t stride, float k_hi) {
+    __shared__ SliceLds<1> s_slice;
+    const SliceJob j(x, scores, ended, scratch, kNoEnd);
+    const Scratch w(addr<uint8_t>(scratch), j.groups, j.step.g, j.beams * j.parts, j.width);
+    if (j.on()) hold_slice<Fmt, NV>(s_slice, j, w, x, stride, k_hi);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1046,11 +1097,20 @@ hipError_t launch_beam_step(const BeamPlan& plan, const BeamArgs& a, uint8_t* sc
                 default: return units(Int<64>{}, Int<2>{});
             }
         }
-        switch (plan.held) {
-            case 1: return slice(k_beam_slice<Fmt, 1>);
-            case 2: return slice(k_beam_slice<Fmt, 2>);
-            case 4: return slice(k_beam_slice<Fmt, 4>);
-            case 8: return slice(k_beam_slice<Fmt, 8>);
+        if (plan.held > 0) {
+            const auto held = [&](auto vecs) {
+                constexpr int NV = decltype(vecs)::value;
+                if (plan.joins)
+                    slice(k_beam_slice<Fmt, NV>);
+                else
+                    scan(k_beam_rows<Fmt, NV>);
+            };
+            switch (plan.held) {
+                case 1: return held(Int<1>{});
+                case 2: return held(Int<2>{});
+                case 4: return held(Int<4>{});
+                default: return held(Int<8>{});
+            }
         }
         switch (plan.team) {
             case 256: return scan(k_beam_scan<Fmt, 256>);

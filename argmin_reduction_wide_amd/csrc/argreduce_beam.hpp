@@ -21,6 +21,7 @@ struct BeamPlan {
     int team;             // SUBWAVE: lanes per row, 4 to 128; else threads that scan one slice
     int parts;            // BLOCK, SPLIT: slices per row, each with a list of candidates of its own
     int held;             // 16-byte vectors per lane held in registers: 1, 2, 4, 8, or 0 (a slice in one pass)
+    bool joins;           // whether the scanning kernel joins the lists, too
     int64_t grid_blocks;  // workgroups of the (scanning) kernel
     int64_t device_threads;
     size_t scratch_bytes; // including 15 bytes of alignment slack; 0 if none needed

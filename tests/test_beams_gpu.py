@@ -122,6 +122,23 @@ def test_every_path(capacity, dtype, cap, groups, beams, cols):
         check(x, make_scores(rng, groups, beams), width, 0.9)
 
 
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("beams,cols,width", [(5, 520, 3), (12, 1031, 24), (3, 1999, 64), (12, 2056, 12), (7, 4090, 20),
+                                              (64, 515, 64), (5, 64 * 32 + 1, 7)])
+def test_a_wavefront_per_row(capacity, dtype, beams, cols, width):
+    """Rows of up to 512 vectors, more of them than the (simulated) device has compute units; a join of up to 64 lists
+    that all count, and of hundreds of candidates."""
+    capacity(2048)
+    announce(f"beam_step {dtype} rows by wavefronts [3,{beams},{cols}] width {width}")
+    rng = np.random.default_rng(cols)
+    plan = B.argreduce_beam_plan(3, beams, cols, dtype, width)
+    assert plan["block_threads"] == 64 or cols * (4 if dtype == "f32" else 2) > 16 * 512 or plan["path"] == B.PATH_SUBWAVE
+    wide = torch.full((3, beams, cols + 5), float("nan"), dtype=DT[dtype], device="cuda")
+    wide[..., :cols] = make_logits(rng, 3, beams, cols, dtype)
+    ended = torch.from_numpy(rng.random((3, beams)) < 0.3).cuda()
+    check(wide[..., :cols], make_scores(rng, 3, beams), width, 0.8, ended, cols - 1)
+
+
 @pytest.mark.parametrize("cap", [2048, 256 * 2048])
 @pytest.mark.parametrize("cols", [40, 500, 3000, 140000])
 def test_tied_rows(capacity, cap, cols):
