@@ -161,6 +161,28 @@ __device__ inline void sort8(typename K::T* a) {
     for (int i = 0; i < 19; ++i) exchange<K>(a[kPairs[i][0]], a[kPairs[i][1]]);
 }
 
+template <typename K, int L>
+__device__ inline void sort(typename K::T (&a)[L]) {
+    static_assert(L == 8 || L == 16, "lists of eight or sixteen");
+    sort8<K>(a);
+    if constexpr (L == 16) {
+        sort8<K>(a + 8);
+        typename K::T hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            hi[i] = K::max(a[i], a[15 - i]);
+            lo[i] = K::min(a[i], a[15 - i]);
+        }
+        sort_merged<K, 8>(hi);
+        sort_merged<K, 8>(lo);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a[i] = hi[i];
+            a[8 + i] = lo[i];
+        }
+    }
+}
+
 // The L largest of a lane's N keys, sorted.
 template <typename K, int L, int N>
 __device__ inline void best_of_lane(const typename K::T (&key)[N], typename K::T (&best)[L]) {
@@ -173,13 +195,12 @@ __device__ inline void best_of_lane(const typename K::T (&key)[N], typename K::T
             best[0] = K::max(best[0], key[i]);
         }
     } else {
-        static_assert(L == 8, "lists of two or eight");
 #pragma unroll
         for (int j = 0; j < N; j += L) {
             typename K::T part[L];
 #pragma unroll
             for (int i = 0; i < L; ++i) part[i] = j + i < N ? key[j + i] : K::kNone;
-            sort8<K>(part);
+            sort<K, L>(part);
             if (j == 0) {
 #pragma unroll
                 for (int i = 0; i < L; ++i) best[i] = part[i];
@@ -400,7 +421,7 @@ __device__ inline void finish(JoinLds& L, const Totals& out, double both, Tail t
 }
 
 // G lanes per token, NV vectors each: vector v of the token in lane v % G. L: the length of the lists that
-// are merged (2 or 8), or 0 for more choices than that, which are taken one by one.
+// are merged (2, 8 or 16), or 0 for more choices than that, which are taken one by one (16 of [16,4096,256] bf16: 43 us).
 // Tags: experts in x, top (and 0x8000: renormalize) in live, workgroups per group in weights, nonce in
 // (chosen, scratch).
 template <typename Fmt, int G, int NV, int L>
@@ -811,6 +832,8 @@ hipError_t launch_route(const RoutePlan& plan, const RouteArgs& a, const uint8_t
                 go(Int<2>{});
             else if (a.top <= 8)
                 go(Int<8>{});
+            else if (a.top <= 16)
+                go(Int<16>{});
             else
                 go(Int<0>{});
         });

@@ -102,6 +102,18 @@ def test_route_and_gradient(dtype, experts):
         check(x[:1], top, dtype, None, not renormalize, rng)
 
 
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("experts", [9, 16, 17, 33, 64, 127, 256, 300, 512, 1000])
+def test_nine_and_more_choices(dtype, experts):
+    """Lists of up to sixteen and, above that, choices taken one by one; rows with fewer logits than choices."""
+    rng = np.random.default_rng(experts + 5)
+    for top in sorted({9, min(15, experts), min(16, experts), min(17, experts)}):
+        announce(f"route {dtype} experts={experts} top={top}")
+        x = make_logits(rng, 2, 21, experts, dtype)
+        x[0, 3:6, 5:] = -INF
+        check(x, top, dtype, None, top % 2 == 0, rng)
+
+
 @pytest.mark.parametrize("cap", [2048, 256 * 2048])
 @pytest.mark.parametrize("tokens", [1, 2, 63, 700])
 def test_tokens_over_workgroups(capacity, cap, tokens):
