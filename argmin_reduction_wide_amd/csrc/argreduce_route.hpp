@@ -13,7 +13,7 @@ namespace argreduce {
 constexpr int kExpertsMax = 1024;  // experts of a router (ARGREDUCE_EXPERTS_MAX)
 constexpr int kRouteTopMax = 64;   // experts chosen per token (ARGREDUCE_ROUTE_TOP_MAX)
 
-constexpr int kRouteThreads = 256;  // of a workgroup
+constexpr int kRouteThreads = 512;  // of a workgroup
 constexpr uint32_t kRouteSet = 64;  // workgroups whose sums one of them adds up
 
 // A token's logits lie in `lanes` lanes of a wavefront, `vecs` vectors of 16 bytes each.

@@ -20,16 +20,17 @@ int check_route(int dtype, int64_t groups, int64_t tokens, int64_t experts) {
 }
 
 // Tokens up to this many (of all groups) take up to 16 lanes each, more of them up to 8, as long as a lane has no
-// more than four vectors. Forward and gradient of [16,4096,256] bf16 with 8 experts per token, us: 8 lanes 27.3 and
-// 23.6, 16 lanes 29.0 and 23.2, 32 lanes 42.6 and 30.5; [16,4096,128] 18.6 and 15.3, 22.2 and 17.7; [16,4096,64]
-// f16 with 2 (8 vectors) 12.0 by 8 lanes, 13.0 by 4, 15.9 by 2; but [1,300,256] 11.2 and 8.1 by 8, 9.6 and 5.6 by 16.
+// more than four vectors. Forward of [16,4096,256] bf16 with 8 experts per token, us: 8 lanes 27.3, 16 lanes 29.0, 32
+// lanes 42.6; [16,4096,128] 18.6, 22.2; [16,4096,64] f16 with 2 (8 vectors) 12.0 by 8 lanes, 13.0 by 4, 15.9 by 2; but
+// [1,300,256] 11.2 by 8, 9.6 by 16, and its gradient 8.1 and 5.6.
 constexpr int64_t kFewTokens = 4096;
-// Workgroups per CU, of all groups together: forward 2 ([16,4096,256] 27.3 us, with 3 of them 30.4, with 4
-// 33.8: more sums to join), gradient 4 ([16,4096,64] f16 11.4, with 2 14.5).
-constexpr int64_t kForwardPerCu = 2, kGradPerCu = 4;
-// Tokens of a group that one workgroup goes through by itself, in rounds: nothing to join then ([1,32,256] bf16
-// 6.1 us, with four workgroups 7.8).
-constexpr int64_t kAloneRounds = 4;
+// Workgroups of 512 threads per CU, of all groups together: forward 1 ([16,4096,256] bf16 24.8 us, with 2 of them
+// 32.5: more sums to join; with 2 of 256 threads 25.1, [8,4096,512] 25.2 and 31.0), gradient 2 ([16,4096,256] 17.8 us,
+// with 4 of them 20.4).
+constexpr int64_t kForwardPerCu = 1, kGradPerCu = 2;
+// Tokens of a group that one workgroup goes through by itself, in rounds: nothing to join then ([1,32,256] bf16 in one
+// round 5.4 us, over four workgroups 7.8).
+constexpr int64_t kAloneRounds = 2;
 
 int make_route_plan(int dtype, int64_t groups, int64_t tokens, int64_t experts, bool grad, RoutePlan* p) {
     int rc = check_route(dtype, groups, tokens, experts);
