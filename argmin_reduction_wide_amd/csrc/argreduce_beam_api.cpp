@@ -8,8 +8,9 @@
 namespace argreduce {
 namespace {
 
-// Slices of at least this many vectors: two for each of 256 lanes.
-constexpr int64_t kLeastSlice = 512;
+// Slices of at least this many vectors, two for each of 256 lanes, where rows are few ([8,4,32000] bf16 10.5 us, of
+// twice as many 10.9), and of at least so many where they are more than the CUs.
+constexpr int64_t kLeastSlice = 512, kLongSlice = 4000;
 
 int check_beams(int64_t groups, int64_t beams, int64_t cols, int dtype) {
     if (logits_elem_size(dtype) == 0) return ARGREDUCE_ERR_UNSUPPORTED_DTYPE;
@@ -30,7 +31,8 @@ int make_beam_plan(int dtype, int64_t groups, int64_t beams, int64_t cols, int w
     const int64_t rows = std::max<int64_t>(1, groups * beams);
     const int64_t cus = std::max<int64_t>(1, cap / kThreadsPerCu);
     const int64_t vecs = span_vecs(cols, logits_elem_size(dtype));
-    // A wavefront per group, if its beams' rows are units of at most eight vectors per lane.
+    // A wavefront per group, if its beams' rows are units of at most eight vectors per lane: [2048,4,64] f16 5.5 us, by
+    // a wavefront per row and a join 18.3; [100,8,100] f32 8 and 10.8, [2000,8,500] f16 (eight vectors) 26.6 and 29.9.
     const int64_t whole = ceil_div(cols * logits_elem_size(dtype), 16);  // vectors of a row from its first element
     const int64_t lanes = std::max<int64_t>(4, next_pow2(whole));
     const int64_t units = next_pow2(lanes <= 64 ? ceil_div(beams, 64 / lanes) : beams * 2);
@@ -47,7 +49,11 @@ int make_beam_plan(int dtype, int64_t groups, int64_t beams, int64_t cols, int w
     // no more than the CUs, rows of at most 512 by a wavefront each where they are more: [2000,12,1000] f16 43 us
     // instead of 116 in one pass by 256 threads, [2000,8,4000] bf16 65 and 84, [64,8,1000] 10.7 and 12.7; but longer
     // ones by 256 threads held [1000,8,10000] bf16 in 109 us instead of 60.
-    const int64_t parts = std::min({ceil_div(vecs, kLeastSlice), std::max<int64_t>(1, cus / rows), kBeamLists / beams});
+    // More and longer rows are cut until the slices are six per CU: [300,1,128256] f16 27.9 us in four slices, 41 in one,
+    // [400,2,260000] 97 and 110; but [256,8,128256] bf16 110 in four and 103 in one.
+    const int64_t parts =
+        rows <= cus ? std::min({ceil_div(vecs, kLeastSlice), cus / rows, kBeamLists / beams})
+                    : std::max<int64_t>(1, std::min({vecs / kLongSlice, ceil_div(6 * cus, rows), kBeamLists / beams}));
     const int64_t slice = parts > 1 ? ceil_div(vecs, parts) : whole;
     p->path = parts > 1 ? ARGREDUCE_PATH_SPLIT : ARGREDUCE_PATH_BLOCK;
     p->joins = rows <= cus && slice <= kSliceVecs * kSliceThreads;
@@ -55,7 +61,10 @@ int make_beam_plan(int dtype, int64_t groups, int64_t beams, int64_t cols, int w
         p->team = p->joins ? kSliceThreads : 64;
         p->held = static_cast<int>(next_pow2(ceil_div(slice, p->team)));
     } else {
-        p->team = slice > 2048 && rows * 1024 <= cap ? 1024 : slice > 4096 ? 512 : 256;
+        // One slice or less per CU: 1024 threads ([20,10,50000] f32 19.7 us, 25 with 256). Two, or six rows or more and
+        // long ones: 512 ([30,12,25000] f16 22.0, 23.2 with 256; [256,8,128256] bf16 103 and 110; but [1000,8,10000]
+        // 97 and 60, [200,5,32001] f16 31.8 and 27.0).
+        p->team = rows <= cus ? 1024 : rows * parts <= 2 * cus || (rows >= 6 * cus && slice > kLongSlice) ? 512 : 256;
     }
     p->parts = static_cast<int>(parts);
     p->grid_blocks = rows * parts;
