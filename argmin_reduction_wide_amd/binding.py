@@ -1,8 +1,8 @@
 """Python binding of the HIP library ``libargreduce.so`` (argument marshalling only).
 
-ctypes loads the library and serves every entry point; the three reduction calls and the
-logits operators (torch functions in ``logits.py``) go through a small CPython fast-call
-module (``_argreduce_fast``, built beside the library) when it is present, because a ctypes
+ctypes loads the library and serves every entry point; the three reduction calls, the logits
+operators, beam search and expert routing (torch functions in ``logits.py``, ``beams.py`` and
+``routing.py``) go through a small CPython fast-call module (``_argreduce_fast``, built beside the library) when it is present, because a ctypes
 call with nine converted arguments costs about as much host time as the GPU spends on a
 small reduction.
 

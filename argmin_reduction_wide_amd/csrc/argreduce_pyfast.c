@@ -1,5 +1,5 @@
-/* CPython fast-call entry points for the reduction calls (and the launch-floor hooks) of
- * libargreduce.so.
+/* CPython fast-call entry points for the reduction calls, the logits operators, beam search and
+ * expert routing (and the launch-floor hooks) of libargreduce.so.
  *
  * Argument marshalling only, like the ctypes binding it sits beside: each function takes
  * the C ABI's arguments as Python ints (device pointers, enum codes, sizes, the stream

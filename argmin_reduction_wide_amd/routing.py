@@ -14,9 +14,9 @@ import torch
 from torch.autograd import forward_ad as _forward_ad
 
 from . import binding as B
-from .beams import _contiguous
+from .beams import _contiguous, _results
 from .logits import (_F32, _I64, _Calls, _check_grad, _device, _elsewhere, _new_grad, _refuse_tangent, _rows, _same,
-                     _scratch, _stream, _tuple)
+                     _stream, _tuple)
 
 EXPERTS_MAX = 1024   # experts of a router (ARGREDUCE_EXPERTS_MAX)
 ROUTE_TOP_MAX = 64   # experts chosen per token (ARGREDUCE_ROUTE_TOP_MAX)
@@ -76,15 +76,13 @@ def _route(logits, top, live, renormalize, scratch, apart=False) -> RouteExperts
     shape = lead + (tokens, top)
     # totals (counts, tokens: 8 bytes each, balance and z: 4 each, one after another), experts (8) and weights (4)
     per, n = groups * (experts + 2), groups * tokens * top
-    out = torch.empty(per + n + (0 if apart else (n + 1) // 2), dtype=_I64, device=device)
+    need = _call.route_scratch_bytes(groups, tokens, experts, code)
+    out, sptr, sbytes, scratch = _results(per + n + (0 if apart else (n + 1) // 2), need, "argreduce_route", scratch,
+                                          device)
     strides, floats = _contiguous(shape), out.view(_F32)
     totals = out.as_strided((per,), (1,))
     chosen = out.as_strided(shape, strides, per)
     weights = torch.empty(shape, dtype=_F32, device=device) if apart else floats.as_strided(shape, strides, 2 * (per + n))
-    need = _call.route_scratch_bytes(groups, tokens, experts, code)
-    sptr = sbytes = 0
-    if need or scratch is not None:
-        sptr, sbytes, scratch = _scratch(need, "argreduce_route", scratch, device)
     rc = _call.route(logits.data_ptr(), code, groups, tokens, experts, stride,
                      0 if live is None else live.data_ptr(), top, bool(renormalize), weights.data_ptr(),
                      chosen.data_ptr(), totals.data_ptr(), sptr, sbytes, _stream(device.index))
