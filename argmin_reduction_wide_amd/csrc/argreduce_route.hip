@@ -13,8 +13,8 @@
 //
 // A token's logits lie in the registers of a group of G lanes, and a lane's columns are the same for
 // all tokens, so that it sums p of its own columns in registers; choices are counted in LDS. A workgroup
-// leaves one word of sums per expert in scratch, and the last one of a group adds them up. No atomics on floats: results do not depend on the order in which
-// workgroups run.
+// leaves one word of sums per expert in scratch, and the last one of a group adds them up. No atomics on
+// floats: results do not depend on the order in which workgroups run.
 #include <hip/hip_runtime.h>
 
 #include "argreduce_launch.hpp"
@@ -341,7 +341,8 @@ struct JoinLds {
 
 // Adds up n <= kRouteSet partials: each(expert, sum, count) by the threads of the workgroup in turn, in teams that
 // take a share of the partials each where there are fewer experts than threads; kBatch loads of a thread at
-// once (32 would take registers from the tokens' part: 157 instead of 72). Returns the sums of z and of the tokens, in the first wavefront.
+// once (32 would take registers from the tokens' part: 157 instead of 72). Returns the sums of z and of the
+// tokens, in the first wavefront.
 constexpr uint32_t kBatch = 16;
 struct Tail {
     double z, tokens;
@@ -424,7 +425,8 @@ __device__ inline void finish(JoinLds& L, const Totals& out, double both, Tail t
 // 14.5 more for each further 65536 tokens. What bounds it is arithmetic, some 1000 vector instructions per eight
 // tokens, half of them the lists' exchanges, and 10 us of launch, first loads, sums and the last workgroup's join.
 // G lanes per token, NV vectors each: vector v of the token in lane v % G. L: the length of the lists that
-// are merged (2, 8 or 16), or 0 for more choices than that, which are taken one by one (16 of [16,4096,256] bf16: 43 us).
+// are merged (2, 8 or 16), or 0 for more choices than that, which are taken one by one (16 of [16,4096,256] bf16:
+// 43 us, by lists 28.5).
 // Tags: experts in x, top (and 0x8000: renormalize) in live, workgroups per group in weights, nonce in
 // (chosen, scratch).
 template <typename Fmt, int G, int NV, int L>
