@@ -312,6 +312,37 @@ def test_same_bits_streams_and_graphs(groups, beams, cols, width):
         assert same(graphs[i % 2][1], want[i % 2])
 
 
+def test_graphs_that_share_a_scratch():
+    """Steps and routings of several shapes in one scratch, captured and eager in turn, one stream."""
+    announce("one scratch for graphs of several calls")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    scratch = torch.randint(0, 256, (1 << 21,), dtype=torch.uint8, device="cuda", generator=gen)
+    calls = []
+    for groups, beams, cols, width in ((1, 4, 32000, 4), (3, 4, 40000, 8), (2, 8, 3000, 20), (300, 3, 700, 3)):
+        x = torch.randn(groups, beams, cols, device="cuda", generator=gen)
+        s = torch.rand(groups, beams, device="cuda", generator=gen)
+        calls.append(lambda x=x, s=s, w=width: ar.beam_step(x, s, w, scratch=scratch)[:3])
+    for tokens, experts in ((4001, 64), (700, 300)):
+        x = torch.randn(2, tokens, experts, device="cuda", generator=gen)
+        calls.append(lambda x=x: ar.route_experts(x, 4, scratch=scratch)[:6])
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    graphs = []
+    for f in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            r = f()
+        graphs.append((graph, r))
+    for i in (0, 4, 1, 1, 2, 5, 3, 0, 0, 5, 4, 2, 1, 3, 0):
+        for t in graphs[i][1]:
+            t.zero_()
+        graphs[i][0].replay()
+        graphs[(i + 1) % len(graphs)][0].replay()
+        eager = calls[i]()
+        for a, b, c in zip(graphs[i][1], want[i], eager):
+            assert torch.equal(a, b) and torch.equal(c, b), i
+
+
 def test_outputs_may_be_written_over():
     announce("beam_step outputs")
     x, s = torch.randn(3, 4, 100, device="cuda"), torch.zeros(3, 4, device="cuda")
