@@ -728,7 +728,7 @@ __global__ __launch_bounds__(kSliceThreads) void k_beam_slice(uint64_t x, uint64
     join_if_last<kSliceThreads>(lds.join, s_cands, &s_found, j, w, generation, nonce, k_hi, out);
 }
 
-// Many rows of up to 512 vectors: a wavefront each, and the join is a launch of its own. [2000,12,1000] f16 28 us and 15
+// Many rows of up to 512 vectors: a wavefront each, and the join is a launch of its own. [2000,12,1000] f16 28 us and 14
 // for the join; arithmetic bounds it, 33 vector instructions' time per logit.
 template <typename Fmt, int NV>
 __global__ __launch_bounds__(kWave) void k_beam_rows(uint64_t x, uint64_t scores, uint64_t ended, uint64_t scratch,
@@ -1117,6 +1117,7 @@ hipError_t launch_beam_step(const BeamPlan& plan, const BeamArgs& a, uint8_t* sc
             }
         }
         switch (plan.team) {
+            case 64: return scan(k_beam_scan<Fmt, 64>);
             case 256: return scan(k_beam_scan<Fmt, 256>);
             case 512: return scan(k_beam_scan<Fmt, 512>);
             default: return scan(k_beam_scan<Fmt, 1024>);

@@ -45,26 +45,35 @@ int make_beam_plan(int dtype, int64_t groups, int64_t beams, int64_t cols, int w
         p->grid_blocks = ceil_div(std::max<int64_t>(1, groups), kBlock / 64);
         return grid_too_large(p->grid_blocks, kBlock) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
     }
-    // Slices of rows too few to give every CU one. Slices of at most 2048 vectors are held in registers where they are
-    // no more than the CUs, rows of at most 512 by a wavefront each where they are more: [2000,12,1000] f16 43 us
-    // instead of 116 in one pass by 256 threads, [2000,8,4000] bf16 65 and 84, [64,8,1000] 10.7 and 12.7; but longer
-    // ones by 256 threads held [1000,8,10000] bf16 in 109 us instead of 60.
-    // More and longer rows are cut until the slices are six per CU: [300,1,128256] f16 27.9 us in four slices, 41 in one,
-    // [400,2,260000] 97 and 110; but [256,8,128256] bf16 110 in four and 103 in one.
+    // Slices of rows too few to give every CU one. More and longer rows are cut until the slices are six per CU:
+    // [300,1,128256] f16 27.9 us in four slices, 41 in one, [400,2,260000] 97 and 110; but [256,8,128256] bf16 110 in
+    // four and 103 in one.
     const int64_t parts =
         rows <= cus ? std::min({ceil_div(vecs, kLeastSlice), cus / rows, kBeamLists / beams})
                     : std::max<int64_t>(1, std::min({vecs / kLongSlice, ceil_div(6 * cus, rows), kBeamLists / beams}));
     const int64_t slice = parts > 1 ? ceil_div(vecs, parts) : whole;
     p->path = parts > 1 ? ARGREDUCE_PATH_SPLIT : ARGREDUCE_PATH_BLOCK;
+    // Slices of at most 2048 vectors are held in registers where they are no more than the CUs, rows of at most 512 (256
+    // where they are many) by a wavefront each where they are more: [2000,12,1000] f16 43 us instead of 116 in one pass
+    // by 256 threads and 47 by a wavefront, [100,8,3500] 13.7 and 17.2 by a wavefront; but [2000,8,4000] bf16 66 and 54,
+    // and held by 256 threads [1000,8,10000] 109 instead of 60.
     p->joins = rows <= cus && slice <= kSliceVecs * kSliceThreads;
-    if (p->joins || slice <= kSliceVecs * 64) {
+    const bool many = rows >= 16 * cus;
+    if (p->joins || slice <= (many ? 4 : kSliceVecs) * 64) {
         p->team = p->joins ? kSliceThreads : 64;
         p->held = static_cast<int>(next_pow2(ceil_div(slice, p->team)));
     } else {
         // One slice or less per CU: 1024 threads ([20,10,50000] f32 19.7 us, 25 with 256). Two, or six rows or more and
         // long ones: 512 ([30,12,25000] f16 22.0, 23.2 with 256; [256,8,128256] bf16 103 and 110; but [1000,8,10000]
-        // 97 and 60, [200,5,32001] f16 31.8 and 27.0).
-        p->team = rows <= cus ? 1024 : rows * parts <= 2 * cus || (rows >= 6 * cus && slice > kLongSlice) ? 512 : 256;
+        // 97 and 60, [200,5,32001] f16 31.8 and 27.0). Many short ones: a wavefront, few of whose steps wait for others
+        // ([2000,8,6000] f16 58 us, 90 with 256, [1000,8,10000] bf16 51 and 60, [1000,8,20000] f16 81 and 87; but
+        // [250,4,10000] 20.5 and 16.3).
+        if (rows <= cus)
+            p->team = 1024;
+        else if (many && slice <= 2560)
+            p->team = 64;
+        else
+            p->team = rows * parts <= 2 * cus || (rows >= 6 * cus && slice > kLongSlice) ? 512 : 256;
     }
     p->parts = static_cast<int>(parts);
     p->grid_blocks = rows * parts;

@@ -139,6 +139,23 @@ def test_a_wavefront_per_row(capacity, dtype, beams, cols, width):
     check(wide[..., :cols], make_scores(rng, 3, beams), width, 0.8, ended, cols - 1)
 
 
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("beams,cols,width", [(8, 4090, 8), (6, 9001, 24), (16, 2100, 64), (12, 20400, 5)])
+def test_many_rows_in_one_pass(capacity, dtype, beams, cols, width):
+    """Longer rows, sixteen and more per compute unit of the (simulated) device: a wavefront each, in one pass."""
+    capacity(2048)
+    announce(f"beam_step {dtype} many rows in one pass [3,{beams},{cols}] width {width}")
+    rng = np.random.default_rng(cols)
+    plan = B.argreduce_beam_plan(3, beams, cols, dtype, width)
+    vecs = -(-cols * (4 if dtype == "f32" else 2) // 16)
+    assert plan["block_threads"] == 64 or vecs > 2560
+    wide = torch.full((3, beams, cols + 5), float("nan"), dtype=DT[dtype], device="cuda")
+    wide[..., :cols] = make_logits(rng, 3, beams, cols, dtype)
+    wide[0, :, :cols - 1:2] = 1.0  # ties
+    ended = torch.from_numpy(rng.random((3, beams)) < 0.3).cuda()
+    check(wide[..., :cols], make_scores(rng, 3, beams), width, 0.8, ended, cols - 1)
+
+
 @pytest.mark.parametrize("cap", [2048, 256 * 2048])
 @pytest.mark.parametrize("cols", [40, 500, 3000, 140000])
 def test_tied_rows(capacity, cap, cols):
