@@ -171,18 +171,17 @@ __device__ inline Cand finished(float score, uint32_t b, uint32_t end_token) {
     return {order64(static_cast<double>(score)), key_of(0.0f, end_token), b};
 }
 
-// Scratch: generation and owner of every group, a slot for every slice (arrive), slices, lists.
+// Scratch: an owner for every group (in 16 bytes), a slot for every slice (arrive), slices, lists.
 struct Scratch {
-    uint64_t *generation, *owner, *slots;  // of the group
-    uint64_t *slices, *lists;              // of the group: two words, and width words each
+    uint64_t *owner, *slots;   // of the group
+    uint64_t *slices, *lists;  // of the group: two words, and width words each
     static size_t bytes(int64_t groups, int64_t lists, int width) {
         return 8 * static_cast<size_t>(groups) * (2 + static_cast<size_t>(lists) * (3 + width));
     }
     __device__ Scratch(uint8_t* p, uint32_t groups, uint32_t g, uint32_t lists_, uint32_t width) {
         uint64_t* w = reinterpret_cast<uint64_t*>(p);
         const size_t all = static_cast<size_t>(groups) * lists_, mine = static_cast<size_t>(g) * lists_;
-        generation = w + g;
-        owner = w + groups + g;
+        owner = w + 2 * static_cast<size_t>(g);
         slots = w + 2 * static_cast<size_t>(groups) + mine;
         slices = w + 2 * static_cast<size_t>(groups) + all + 2 * mine;
         lists = w + 2 * static_cast<size_t>(groups) + 3 * all + mine * width;
@@ -407,10 +406,10 @@ struct SliceJob {
 // After a slice's words are stored: the group's last workgroup joins its lists.
 template <int T>
 __device__ inline void join_if_last(JoinLds& L, uint64_t* cands, uint32_t* found, const SliceJob& j, const Scratch& w,
-                                    uint64_t generation, uint32_t nonce, float k_hi, uint64_t out) {
-    if (!arrive(w.slots, w.owner, j.list(), j.beams * j.parts, arrival_tag(nonce, generation), found)) return;
+                                    uint32_t nonce, float k_hi, uint64_t out) {
+    if (!arrive(w.slots, w.owner, j.list(), j.beams * j.parts, arrival_tag(nonce), found)) return;
     join<T>(L, Cands(cands, j.width), j.step, w, Scale(k_hi, tag(out)), BeamOut(addr<uint8_t>(out), j.groups, j.width));
-    if (threadIdx.x == 0) store_part(w.generation, generation + 1);
+    leave<T>(w.slots, j.beams * j.parts);
 }
 
 // One slice of a row per workgroup, in one pass; the join is a launch of its own (its registers would halve the
@@ -723,9 +722,8 @@ __global__ __launch_bounds__(kSliceThreads) void k_beam_slice(uint64_t x, uint64
     extern __shared__ uint64_t s_cands[];
     const SliceJob j(x, scores, ended, scratch, end_token);
     const Scratch w(addr<uint8_t>(scratch), j.groups, j.step.g, j.beams * j.parts, j.width);
-    const uint64_t generation = load_part(w.generation);
     if (j.on()) hold_slice<Fmt, NV>(lds.slice, j, w, x, stride, k_hi);
-    join_if_last<kSliceThreads>(lds.join, s_cands, &s_found, j, w, generation, nonce, k_hi, out);
+    join_if_last<kSliceThreads>(lds.join, s_cands, &s_found, j, w, nonce, k_hi, out);
 }
 
 // Many rows of up to 512 vectors: a wavefront each, and the join is a launch of its own. [2000,12,1000] f16 28 us and 14

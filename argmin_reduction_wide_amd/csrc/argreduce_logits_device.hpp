@@ -787,9 +787,10 @@ __device__ inline typename Fmt::Vec pack(const float (&g)[Fmt::VW]) {
 // all of them comes after all parts. Several can find it, and the first of them to put the tag into the
 // owner's word is the one. The parts are read with load_part.
 //
-// The tag is one of 2^64 made from the call's nonce and a generation word in scratch, which the last
-// workgroup moves on and all others have read before: a graph's replay, whose nonce is that of its
-// capture, has another tag than the replay before it.
+// The tag is made from the call's nonce, and the replays of a captured call have one nonce, so no word may hold
+// the tag before its launch puts it there: the last workgroup clears the slots when it is done (leave), and the
+// first one clears the owner before its slot can be seen, and with it all slots. What other kernels leave in this
+// memory between two replays then does not matter, nor what of it they leave as it was: none of it is the tag.
 //
 // Parts and slots are agent-scope accesses, which pass the L2 caches of the XCDs; a store is done when its
 // wavefront's count of memory operations says so (vmcnt), so that no cache has to be written back.
@@ -804,8 +805,9 @@ __device__ inline T load_part(const T* p) {
 }
 __device__ inline void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-__device__ inline uint64_t arrival_tag(uint32_t nonce, uint64_t generation) {
-    uint64_t v = generation + 0x9e3779b97f4a7c15ull * (nonce | uint64_t{1} << 32);
+// One of 2^64 (and never 0).
+__device__ inline uint64_t arrival_tag(uint32_t nonce) {
+    uint64_t v = 0x9e3779b97f4a7c15ull * (nonce | uint64_t{1} << 32);
     v = (v ^ (v >> 30)) * 0xbf58476d1ce4e5b9ull;
     v = (v ^ (v >> 27)) * 0x94d049bb133111ebull;
     return v ^ (v >> 31);
@@ -814,6 +816,7 @@ __device__ inline uint64_t arrival_tag(uint32_t nonce, uint64_t generation) {
 // Called by the whole workgroup after its last store_part; `found` is in LDS. Whether it is the last of n.
 __device__ inline bool arrive(uint64_t* slots, uint64_t* owner, uint32_t mine, uint32_t n, uint64_t tag,
                               uint32_t* found) {
+    if (mine == 0 && threadIdx.x == 0) store_part(owner, uint64_t{0});
     stores_done();
     __syncthreads();
     if (threadIdx.x < kWave) {
@@ -829,6 +832,11 @@ __device__ inline bool arrive(uint64_t* slots, uint64_t* owner, uint32_t mine, u
     }
     __syncthreads();
     return *found != 0;
+}
+// Called by the T threads of the last workgroup, once all n slots hold the tag.
+template <int T>
+__device__ inline void leave(uint64_t* slots, uint32_t n) {
+    for (uint32_t i = threadIdx.x; i < n; i += T) store_part(slots + i, uint64_t{0});
 }
 
 // ---------------------------------------------------------------------------------------

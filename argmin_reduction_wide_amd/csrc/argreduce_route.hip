@@ -311,20 +311,18 @@ __device__ inline uint64_t word(float sum, uint32_t count) { return static_cast<
 __device__ inline float sum_of(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
 __device__ inline uint32_t count_of(uint64_t w) { return static_cast<uint32_t>(w >> 32); }
 
-// A group's words in scratch: its generation; owners and slots of its sets, and an owner and slots of the
-// group where there are several sets (arrive); partials of workgroups and of sets.
+// A group's words in scratch: owners and slots of its sets, and an owner and slots of the group where there are
+// several sets (arrive); partials of workgroups and of sets.
 struct Group {
-    uint64_t* generation;
     uint64_t *owners, *slots, *last, *set_slots, *partials, *set_partials;
     __host__ __device__ static uint32_t sets(uint32_t blocks) { return (blocks + kRouteSet - 1) / kRouteSet; }
     __host__ __device__ static size_t words(uint32_t experts, uint32_t blocks) {
         const uint32_t n = sets(blocks);
-        return 2 + n + (blocks + n) * (1 + static_cast<size_t>(experts) + 1);
+        return 1 + n + (blocks + n) * (1 + static_cast<size_t>(experts) + 1);
     }
     __device__ Group(uint8_t* scratch, uint32_t g, uint32_t experts, uint32_t blocks) {
         const uint32_t n = sets(blocks);
-        generation = reinterpret_cast<uint64_t*>(scratch) + g * words(experts, blocks);
-        owners = generation + 1;
+        owners = reinterpret_cast<uint64_t*>(scratch) + g * words(experts, blocks);
         slots = owners + n;
         last = slots + blocks;
         set_slots = last + 1;
@@ -452,7 +450,6 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(uint64_t x, uint64_t li
     const int lane = threadIdx.x % G;
     const uint8_t* live = addr<const uint8_t>(live_);
     const Group group(addr<uint8_t>(scratch), g, experts, blocks);
-    const uint64_t generation = blocks > 1 ? load_part(group.generation) : 0;
     for (int i = threadIdx.x; i < G * N; i += kRouteThreads) s_cnt[i] = 0;
     __syncthreads();
     float sum[N], z = 0.0f;
@@ -608,7 +605,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(uint64_t x, uint64_t li
     }
     if (blocks == 1) return finish(s_join, out, both, {zs, static_cast<double>(ns)}, g, experts, top);
     if (threadIdx.x == 0) store_part(part + experts, word(zs, ns));
-    const uint64_t launch_tag = arrival_tag(tags(chosen, scratch), generation);
+    const uint64_t launch_tag = arrival_tag(tags(chosen, scratch));
     const uint32_t set = b / kRouteSet, sets = Group::sets(blocks), from = set * kRouteSet;
     const uint32_t many = blocks - from < kRouteSet ? blocks - from : kRouteSet;
     if (!arrive(group.slots + from, group.owners + set, b - from, many, launch_tag, &s_found)) return;
@@ -629,7 +626,8 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(uint64_t x, uint64_t li
         both += static_cast<double>(times) * share;
     });
     finish(s_join, out, both, tail, g, experts, top);
-    if (threadIdx.x == 0) store_part(group.generation, generation + 1);
+    leave<kRouteThreads>(group.slots, blocks);
+    if (sets > 1) leave<kRouteThreads>(group.set_slots, sets);
 }
 
 // A row is read once and kept. In LDS lies, per team and expert, per_balance c_j, and while a token is worked on also
