@@ -53,7 +53,7 @@ int make_route_plan(int dtype, int64_t groups, int64_t tokens, int64_t experts, 
     p->grid_blocks = groups1 * p->blocks;
     if (!grad)
         p->scratch_bytes = blocks == 1 ? 0 : 15 + static_cast<size_t>(groups1) * route_group_bytes(experts, p->blocks);
-    return grid_too_large(p->grid_blocks, kBlock) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
+    return grid_too_large(p->grid_blocks, kRouteThreads) ? ARGREDUCE_ERR_TOO_WIDE : ARGREDUCE_OK;
 }
 
 // The checks of both directions.
@@ -92,9 +92,9 @@ ARGREDUCE_EXPORT int argreduce_route_plan(int64_t groups, int64_t tokens, int64_
     out->path = ARGREDUCE_PATH_SUBWAVE;
     out->lanes_per_row = p.lanes;
     out->blocks_per_row = 1;
-    out->block_threads = static_cast<int32_t>(kBlock);
+    out->block_threads = kRouteThreads;
     out->grid_blocks = p.grid_blocks;
-    out->outputs_per_block = static_cast<int32_t>(kBlock) / p.lanes;
+    out->outputs_per_block = kRouteThreads / p.lanes;
     out->grid_rows = p.grid_blocks * out->outputs_per_block;
     out->unroll = p.vecs;
     out->device_threads = p.device_threads;
