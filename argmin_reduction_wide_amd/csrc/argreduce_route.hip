@@ -305,11 +305,31 @@ __device__ inline void softmax(float (&e)[N], float& m, float& s) {
 // Sums over the tokens of a group: one partial per workgroup, joined by the last of up to kRouteSet
 // workgroups; of more than that, the sets' partials by the last set's.
 
-// A partial: a word per expert (the sum of its probabilities, and how often it was chosen above it), one for
-// the sum of z and the number of tokens above it.
-__device__ inline uint64_t word(float sum, uint32_t count) { return static_cast<uint64_t>(count) << 32 | __float_as_uint(sum); }
-__device__ inline float sum_of(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
-__device__ inline uint32_t count_of(uint64_t w) { return static_cast<uint32_t>(w >> 32); }
+// A partial: per expert the sum of its probabilities and how often it was chosen, and one more column for the sum of
+// z and the number of tokens. A workgroup's has a word per column, the sum in binary32 below the number; a set's, of
+// sums that more than binary32 holds, two. kBatch: columns that a thread loads at once, 16 words (32 would take
+// registers from the tokens' part: 157 instead of 72).
+struct BlockPart {
+    static constexpr uint32_t kWords = 1, kBatch = 16;
+    uint64_t w;
+    __device__ static BlockPart load(const uint64_t* p) { return {load_part(p)}; }
+    __device__ static void store(uint64_t* p, float sum, uint32_t count) {
+        store_part(p, static_cast<uint64_t>(count) << 32 | __float_as_uint(sum));
+    }
+    __device__ double sum() const { return static_cast<double>(__uint_as_float(static_cast<uint32_t>(w))); }
+    __device__ uint32_t count() const { return static_cast<uint32_t>(w >> 32); }
+};
+struct SetPart {
+    static constexpr uint32_t kWords = 2, kBatch = 8;
+    uint64_t s, n;
+    __device__ static SetPart load(const uint64_t* p) { return {load_part(p), load_part(p + 1)}; }
+    __device__ static void store(uint64_t* p, double sum, uint32_t count) {
+        store_part(p, __builtin_bit_cast(uint64_t, sum));
+        store_part(p + 1, static_cast<uint64_t>(count));
+    }
+    __device__ double sum() const { return __builtin_bit_cast(double, s); }
+    __device__ uint32_t count() const { return static_cast<uint32_t>(n); }
+};
 
 // A group's words in scratch: owners and slots of its sets, and an owner and slots of the group where there are
 // several sets (arrive); partials of workgroups and of sets.
@@ -318,7 +338,8 @@ struct Group {
     __host__ __device__ static uint32_t sets(uint32_t blocks) { return (blocks + kRouteSet - 1) / kRouteSet; }
     __host__ __device__ static size_t words(uint32_t experts, uint32_t blocks) {
         const uint32_t n = sets(blocks);
-        return 1 + n + (blocks + n) * (1 + static_cast<size_t>(experts) + 1);
+        const size_t columns = static_cast<size_t>(experts) + 1;
+        return 1 + n + (blocks + n) + (BlockPart::kWords * blocks + SetPart::kWords * n) * columns;
     }
     __device__ Group(uint8_t* scratch, uint32_t g, uint32_t experts, uint32_t blocks) {
         const uint32_t n = sets(blocks);
@@ -338,19 +359,21 @@ struct JoinLds {
 };
 
 // Adds up n <= kRouteSet partials: each(expert, sum, count) by the threads of the workgroup in turn, in teams that
-// take a share of the partials each where there are fewer experts than threads; kBatch loads of a thread at
-// once (32 would take registers from the tokens' part: 157 instead of 72). Returns the sums of z and of the
+// take a share of the partials each where there are fewer experts than threads. Returns the sums of z and of the
 // tokens, in the first wavefront.
-constexpr uint32_t kBatch = 16;
 struct Tail {
-    double z, tokens;
+    double z;
+    uint32_t tokens;
 };
-template <typename Each>
+template <typename Part, typename Each>
 __device__ inline Tail add_up(JoinLds& L, const uint64_t* partials, uint32_t n, uint32_t experts, Each each) {
-    const uint32_t columns = experts + 1;
-    static_assert(kRouteSet <= kWave, "a lane for each partial's last word");
-    uint64_t tail = 0;
-    if (threadIdx.x < n) tail = load_part(partials + static_cast<size_t>(threadIdx.x) * columns + experts);
+    constexpr uint32_t kBatch = Part::kBatch;
+    static_assert(kRouteSet <= kWave, "a lane for each partial's last column");
+    const auto part = [&](uint32_t b, uint32_t c) {
+        return Part::load(partials + Part::kWords * (static_cast<size_t>(b) * (experts + 1) + c));
+    };
+    Part tail{};
+    if (threadIdx.x < n) tail = part(threadIdx.x, experts);
     uint32_t wide = kRouteThreads / 8;
     while (wide < kRouteThreads && wide < experts) wide *= 2;
     const uint32_t teams = kRouteThreads / wide, team = threadIdx.x / wide;
@@ -361,16 +384,16 @@ __device__ inline Tail add_up(JoinLds& L, const uint64_t* partials, uint32_t n, 
         if (c < experts) {
 #pragma unroll 1
             for (uint32_t b0 = team; b0 < n; b0 += kBatch * teams) {
-                uint64_t w[kBatch];
+                Part w[kBatch];
 #pragma unroll
                 for (uint32_t i = 0; i < kBatch; ++i) {
                     const uint32_t b = b0 + i * teams;
-                    w[i] = b < n ? load_part(partials + static_cast<size_t>(b) * columns + c) : 0;
+                    w[i] = b < n ? part(b, c) : Part{};
                 }
 #pragma unroll
                 for (uint32_t i = 0; i < kBatch; ++i) {
-                    share += static_cast<double>(sum_of(w[i]));
-                    times += count_of(w[i]);
+                    share += w[i].sum();
+                    times += w[i].count();
                 }
             }
         }
@@ -387,7 +410,7 @@ __device__ inline Tail add_up(JoinLds& L, const uint64_t* partials, uint32_t n, 
         }
         if (team == 0 && c < experts) each(c, share, times);
     }
-    return {lanes_sum64(static_cast<double>(sum_of(tail))), lanes_sum64(static_cast<double>(count_of(tail)))};
+    return {lanes_sum64(tail.sum()), static_cast<uint32_t>(lanes_sum64(static_cast<double>(tail.count())))};
 }
 
 // Totals of all groups, one after another: counts (int64 [groups, experts]), tokens (int64 [groups]),
@@ -413,7 +436,7 @@ __device__ inline void finish(JoinLds& L, const Totals& out, double both, Tail t
         both = 0.0;
         for (int i = 0; i < kRouteThreads / kWave; ++i) both += L.red[i];
         const double n = tail.tokens;
-        out.tokens[g] = static_cast<int64_t>(n);
+        out.tokens[g] = tail.tokens;
         out.balance[g] = n > 0.0 ? static_cast<float>(both * experts / (top * n * n)) : 0.0f;
         out.z[g] = n > 0.0 ? static_cast<float>(tail.z / n) : 0.0f;
     }
@@ -593,7 +616,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(uint64_t x, uint64_t li
             counts[c] = times;
             both += static_cast<double>(times) * static_cast<double>(total);
         } else {
-            store_part(part + c, word(total, times));
+            BlockPart::store(part + c, total, times);
         }
     }
     float zs = 0.0f;
@@ -603,28 +626,29 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(uint64_t x, uint64_t li
         zs += s_z[i];
         ns += s_n[i];
     }
-    if (blocks == 1) return finish(s_join, out, both, {zs, static_cast<double>(ns)}, g, experts, top);
-    if (threadIdx.x == 0) store_part(part + experts, word(zs, ns));
+    if (blocks == 1) return finish(s_join, out, both, {zs, ns}, g, experts, top);
+    if (threadIdx.x == 0) BlockPart::store(part + experts, zs, ns);
     const uint64_t launch_tag = arrival_tag(tags(chosen, scratch));
     const uint32_t set = b / kRouteSet, sets = Group::sets(blocks), from = set * kRouteSet;
     const uint32_t many = blocks - from < kRouteSet ? blocks - from : kRouteSet;
     if (!arrive(group.slots + from, group.owners + set, b - from, many, launch_tag, &s_found)) return;
     const uint64_t* ours = group.partials + static_cast<size_t>(from) * (experts + 1);
-    uint32_t last = many;
-    if (sets > 1) {
-        uint64_t* to = group.set_partials + static_cast<size_t>(set) * (experts + 1);
-        const Tail tail = add_up(s_join, ours, many, experts, [&](uint32_t c, double share, uint32_t times) {
-            store_part(to + c, word(static_cast<float>(share), times));
-        });
-        if (threadIdx.x == 0) store_part(to + experts, word(static_cast<float>(tail.z), static_cast<uint32_t>(tail.tokens)));
-        if (!arrive(group.set_slots, group.last, set, sets, launch_tag, &s_found)) return;
-        ours = group.set_partials;
-        last = sets;
-    }
-    const Tail tail = add_up(s_join, ours, last, experts, [&](uint32_t c, double share, uint32_t times) {
+    const auto total = [&](uint32_t c, double share, uint32_t times) {
         counts[c] = times;
         both += static_cast<double>(times) * share;
-    });
+    };
+    Tail tail;
+    if (sets == 1) {
+        tail = add_up<BlockPart>(s_join, ours, many, experts, total);
+    } else {
+        uint64_t* to = group.set_partials + SetPart::kWords * (static_cast<size_t>(set) * (experts + 1));
+        tail = add_up<BlockPart>(s_join, ours, many, experts, [&](uint32_t c, double share, uint32_t times) {
+            SetPart::store(to + SetPart::kWords * c, share, times);
+        });
+        if (threadIdx.x == 0) SetPart::store(to + SetPart::kWords * experts, tail.z, tail.tokens);
+        if (!arrive(group.set_slots, group.last, set, sets, launch_tag, &s_found)) return;
+        tail = add_up<SetPart>(s_join, group.set_partials, sets, experts, total);
+    }
     finish(s_join, out, both, tail, g, experts, top);
     leave<kRouteThreads>(group.slots, blocks);
     if (sets > 1) leave<kRouteThreads>(group.set_slots, sets);
