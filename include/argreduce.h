@@ -463,8 +463,9 @@ int argreduce_beam_step(const void *x, argreduce_dtype_t dtype, int64_t groups, 
                         int64_t cols, int64_t row_stride, const float *scores, const uint8_t *ended,
                         int64_t end_token, double temperature, int32_t width, void *out, void *scratch,
                         size_t scratch_bytes, void *stream);
-/* The plan of argreduce_beam_step: SUBWAVE (a wavefront per row), BLOCK or SPLIT; blocks_per_row is the
- * number of slices of a row. */
+/* The plan of argreduce_beam_step: SUBWAVE (a wavefront per group of beams, four to a workgroup), BLOCK (a
+ * workgroup per row, or with block_threads 64 a wavefront per row) or SPLIT (a workgroup per slice, blocks_per_row
+ * slices to a row). */
 int argreduce_beam_plan(int64_t groups, int64_t beams, int64_t cols, argreduce_dtype_t dtype, int32_t width,
                         argreduce_plan_t *plan);
 

@@ -42,3 +42,23 @@ def test_routings_of_too_many_groups_are_refused(lib, groups, tokens):
     for h in (lib, B.fast()):
         assert h.argreduce_route(*route) == -3
         assert h.argreduce_route_grad(*grad) == (-3 if tokens else 0)
+
+
+def test_step_paths_are_what_the_header_says(lib):
+    text = " ".join(open(B.LIB_PATH.replace("libargreduce.so", "../include/argreduce.h")).read().split()).replace("* ", "")
+    at = text.index("The plan of argreduce_beam_step")
+    text = text[at:text.index("*/", at)]
+    for words in ("SUBWAVE (a wavefront per group of beams, four to a workgroup)", "block_threads 64 a wavefront per row",
+                  "SPLIT (a workgroup per slice"):
+        assert words in text
+    p = B.argreduce_beam_plan(2048, 4, 64, "f16", 4)
+    assert (p["path"], p["block_threads"], p["grid_blocks"], p["scratch_bytes"]) == (B.PATH_SUBWAVE, 256, 512, 0)
+    assert p["outputs_per_block"] == 16  # rows of four groups
+    p = B.argreduce_beam_plan(2000, 12, 1000, "f16", 12)
+    assert (p["path"], p["block_threads"], p["grid_blocks"]) == (B.PATH_BLOCK, 64, 24000)
+    p = B.argreduce_beam_plan(2000, 8, 6000, "f16", 8)
+    assert (p["path"], p["block_threads"], p["grid_blocks"]) == (B.PATH_BLOCK, 64, 16000)
+    p = B.argreduce_beam_plan(256, 8, 128256, "bf16", 8)
+    assert (p["path"], p["block_threads"], p["grid_blocks"]) == (B.PATH_BLOCK, 512, 2048)
+    p = B.argreduce_beam_plan(1, 8, 202048, "bf16", 16)
+    assert p["path"] == B.PATH_SPLIT and p["grid_blocks"] == 8 * p["blocks_per_row"]
