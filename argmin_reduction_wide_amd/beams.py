@@ -93,10 +93,11 @@ def beam_step(logits, scores, width: Optional[int] = None, *, temperature: float
     strides = _contiguous(shape)
     parents = out.as_strided(shape, strides)
     tokens = out.as_strided(shape, strides, n)
-    values = out.view(_F32).as_strided(shape, strides, 4 * n)
+    # (.data: to autograd a tensor of its own, whose writes are no writes to parents and tokens)
+    values = out.view(_F32).as_strided(shape, strides, 4 * n).data
     flags = None
     if end_token is not None:
-        flags = out.view(torch.bool).as_strided(shape, strides, 20 * n)
+        flags = out.view(torch.bool).as_strided(shape, strides, 20 * n).data
     return _tuple(BeamStep, (values, parents, tokens, flags))
 
 

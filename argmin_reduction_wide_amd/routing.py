@@ -28,7 +28,8 @@ class RouteExperts(NamedTuple):
     """What route_experts returns, for logits [..., tokens, experts]: weights (float32) and experts
     (int64), [..., tokens, top]; counts (int64 [..., experts]), how many tokens chose each expert; tokens
     (int64 [...]), how many there are; the losses balance and z (float32 [...]). ``totals`` is what
-    route_experts_grad takes; without autograd counts, tokens, balance and z lie in its memory."""
+    route_experts_grad takes; without autograd counts, tokens, balance and z lie in its memory, and to autograd an
+    in-place write to any result but the weights is one to all others but the weights."""
 
     weights: torch.Tensor
     experts: torch.Tensor
@@ -82,7 +83,9 @@ def _route(logits, top, live, renormalize, scratch, apart=False) -> RouteExperts
     strides, floats = _contiguous(shape), out.view(_F32)
     totals = out.as_strided((per,), (1,))
     chosen = out.as_strided(shape, strides, per)
-    weights = torch.empty(shape, dtype=_F32, device=device) if apart else floats.as_strided(shape, strides, 2 * (per + n))
+    # (.data: to autograd a tensor of its own, whose writes are no writes to the experts)
+    weights = torch.empty(shape, dtype=_F32, device=device) if apart else \
+        floats.as_strided(shape, strides, 2 * (per + n)).data
     rc = _call.route(logits.data_ptr(), code, groups, tokens, experts, stride,
                      0 if live is None else live.data_ptr(), top, bool(renormalize), weights.data_ptr(),
                      chosen.data_ptr(), totals.data_ptr(), sptr, sbytes, _stream(device.index))
