@@ -174,8 +174,13 @@ class BeamStates:
     positions, heads, size] are both fine, and so are slices of longer caches.
 
     The tensors are held, not copied: they must keep their memory (no ``resize_`` or ``set_``), and may
-    share no memory with each other. Made once, outside of a graph capture; a graph that captured a
-    reordering reads this object's memory, which must live as long as the graph."""
+    share no memory with each other. Autograd does not see the move: a state that a graph has saved must
+    not be reordered before that graph's backward pass.
+
+    Made once, outside of a graph capture: it checks the tensors on the host and copies a table of them to the
+    GPU, and waits for that (21 us for one tensor, 77 for 16, 201 for 48). A program whose caches are new tensors
+    in every step pays it in every step. A graph that captured a reordering reads this object's memory, which
+    must live as long as the graph."""
 
     def __init__(self, states, *, dim: Optional[int] = None):
         states = [states] if isinstance(states, torch.Tensor) else list(states)

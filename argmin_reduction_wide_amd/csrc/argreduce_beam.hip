@@ -708,8 +708,9 @@ __device__ inline void hold_slice(SliceLds<W>& L, const SliceJob& j, const Scrat
     }
 }
 
-// Few slices: the last one joins. Latencies bound it: [1,4,32000] f32 10.1 us, [1,8,202048] bf16 13.2, [16,5,32001] f16
-// 12.8, where the launch takes 2.8, the arrival about 3 and the join 3; with the join as a launch of its own 15 to 17.
+// Few slices: the last one joins. Latencies bound it: [1,4,32000] f32 10.2 us captured (kernel trace 10.3), [1,8,202048]
+// bf16 13.2 (13.6), [16,5,32001] f16 12.8 (13.1), where the launch takes 2.8, the arrival about 3 and the join 3; with the
+// join as a launch of its own 15 to 17.
 template <typename Fmt, int NV>
 __global__ __launch_bounds__(kSliceThreads) void k_beam_slice(uint64_t x, uint64_t scores, uint64_t ended,
                                                               uint64_t scratch, uint64_t out, uint32_t stride,
