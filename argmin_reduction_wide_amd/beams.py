@@ -56,7 +56,7 @@ def beam_step(logits, scores, width: Optional[int] = None, *, temperature: float
     code, rows, cols, stride = _rows(logits)
     if logits.dim() < 2:
         raise ValueError("logits need dimensions for beams and columns")
-    lead = logits.shape[:-1]
+    lead = tuple(logits.shape)[:-1]  # (a slice or sum of torch's own sizes takes five times as long)
     beams = lead[-1]
     if not 1 <= beams <= BEAM_MAX:
         raise ValueError(f"a group must have 1..{BEAM_MAX} beams; got {beams}")
@@ -91,9 +91,9 @@ def beam_step(logits, scores, width: Optional[int] = None, *, temperature: float
                                    f"row_stride={stride}, width={width})")
     shape = lead[:-1] + (width,)
     strides = _contiguous(shape)
+    # (.data: to autograd tensors of their own, so that a write to one is no write to another)
     parents = out.as_strided(shape, strides)
-    tokens = out.as_strided(shape, strides, n)
-    # (.data: to autograd a tensor of its own, whose writes are no writes to parents and tokens)
+    tokens = out.as_strided(shape, strides, n).data
     values = out.view(_F32).as_strided(shape, strides, 4 * n).data
     flags = None
     if end_token is not None:
@@ -121,6 +121,8 @@ def _contiguous(shape):
         return (shape[1] * shape[2], shape[2], 1)
     if d == 2:
         return (shape[1], 1)
+    if d == 1:
+        return (1,)
     strides, n = [], 1
     for s in reversed(shape):
         strides.append(n)

@@ -28,8 +28,8 @@ class RouteExperts(NamedTuple):
     """What route_experts returns, for logits [..., tokens, experts]: weights (float32) and experts
     (int64), [..., tokens, top]; counts (int64 [..., experts]), how many tokens chose each expert; tokens
     (int64 [...]), how many there are; the losses balance and z (float32 [...]). ``totals`` is what
-    route_experts_grad takes; without autograd counts, tokens, balance and z lie in its memory, and to autograd an
-    in-place write to any result but the weights is one to all others but the weights."""
+    route_experts_grad takes; without autograd counts, tokens, balance and z lie in its memory, and an in-place write
+    to one of the five is one to all of them for autograd."""
 
     weights: torch.Tensor
     experts: torch.Tensor
@@ -49,7 +49,8 @@ def _router(logits, top):
         raise ValueError(f"a router must have 1..{EXPERTS_MAX} experts; got {experts}")
     if not 1 <= top <= min(experts, ROUTE_TOP_MAX):
         raise ValueError(f"top must lie in 1..{min(experts, ROUTE_TOP_MAX)}; got {top}")
-    lead, tokens = logits.shape[:-2], logits.shape[-2]
+    shape = tuple(logits.shape)  # (a slice or sum of torch's own sizes takes five times as long)
+    lead, tokens = shape[:-2], shape[-2]
     groups = 1
     for n in lead:
         groups *= n
@@ -82,8 +83,8 @@ def _route(logits, top, live, renormalize, scratch, apart=False) -> RouteExperts
                                           device)
     strides, floats = _contiguous(shape), out.view(_F32)
     totals = out.as_strided((per,), (1,))
-    chosen = out.as_strided(shape, strides, per)
-    # (.data: to autograd a tensor of its own, whose writes are no writes to the experts)
+    # (.data: to autograd tensors of their own, so that a write to one is no write to another)
+    chosen = out.as_strided(shape, strides, per).data
     weights = torch.empty(shape, dtype=_F32, device=device) if apart else \
         floats.as_strided(shape, strides, 2 * (per + n)).data
     rc = _call.route(logits.data_ptr(), code, groups, tokens, experts, stride,
@@ -93,9 +94,9 @@ def _route(logits, top, live, renormalize, scratch, apart=False) -> RouteExperts
         raise B.ArgreduceError(rc, f"argreduce_route(groups={groups}, tokens={tokens}, experts={experts}, "
                                    f"row_stride={stride}, top={top})")
     n = groups * experts
-    each = _contiguous(lead)
+    each, columns = _contiguous(lead), lead + (experts,)
     return _tuple(RouteExperts, (
-        weights, chosen, out.as_strided(lead + (experts,), _contiguous(lead + (experts,))),
+        weights, chosen, out.as_strided(columns, _contiguous(columns)),
         out.as_strided(lead, each, n), floats.as_strided(lead, each, 2 * (n + groups)),
         floats.as_strided(lead, each, 2 * n + 3 * groups), totals))
 

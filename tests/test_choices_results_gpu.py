@@ -65,3 +65,28 @@ def test_weights_times_a_parameter_in_place():
     assert not any(t.requires_grad for t in (r.experts, r.counts, r.tokens, r.balance, r.z, r.totals))
     r.weights.sum().backward()
     assert torch.equal(scale.grad, want.sum((0, 1)))
+
+
+def test_tokens_written_after_the_parents_were_used():
+    announce("beam_step: tokens in place after a gather by the parents")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for cols in (50, 9000):
+        x, s = torch.randn(2, 4, cols, device="cuda", generator=g), torch.zeros(2, 4, device="cuda")
+        hidden = torch.randn(2, 4, 5, device="cuda", generator=g).requires_grad_()
+        r = ar.beam_step(x, s)
+        want = torch.zeros(2, 4, device="cuda").scatter_add_(1, r.parents, torch.ones(2, 4, device="cuda"))
+        out = hidden.gather(1, r.parents[..., None].expand(2, 4, 5))
+        r.tokens.clamp_(min=3)
+        out.sum().backward()
+        assert torch.equal(hidden.grad, want[..., None].expand(2, 4, 5))
+
+
+def test_experts_written_after_the_counts_were_used():
+    announce("route_experts: experts in place after a product with the counts")
+    x = torch.randn(2, 30, 16, device="cuda")
+    load = torch.ones(2, 16, device="cuda", requires_grad=True)
+    r = ar.route_experts(x, 3)
+    out = load * r.counts
+    r.experts.clamp_(min=1)
+    out.sum().backward()
+    assert torch.equal(load.grad, r.counts.float())
