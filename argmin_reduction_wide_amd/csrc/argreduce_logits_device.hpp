@@ -784,13 +784,14 @@ __device__ inline typename Fmt::Vec pack(const float (&g)[Fmt::VW]) {
 // Which workgroup of a launch is the last of several to be done with its part, so that it can join the
 // parts: nothing waits, and the words in scratch may hold anything before. Every workgroup stores its part
 // with store_part, then the launch's tag into its own slot, and then reads all slots: who finds the tag in
-// all of them comes after all parts. Several can find it, and the first of them to put the tag into the
-// owner's word is the one. The parts are read with load_part.
+// all of them comes after all parts. Several can find it, and the first of them to put the tag's complement into
+// the owner's word is the one. The parts are read with load_part.
 //
 // The tag is made from the call's nonce, and the replays of a captured call have one nonce, so no word may hold
-// the tag before its launch puts it there: the last workgroup clears the slots when it is done (leave), and the
-// first one clears the owner before its slot can be seen, and with it all slots. What other kernels leave in this
-// memory between two replays then does not matter, nor what of it they leave as it was: none of it is the tag.
+// the tag before its launch puts it there: the last workgroup clears the slots when it is done (leave), so that
+// no launch leaves the tag in any word, and the first one clears the owner before its slot can be seen, and with
+// it all slots. What other kernels leave in this memory between two replays then does not matter, nor what of it
+// they leave as it was or copy from elsewhere: none of it is the tag.
 //
 // Parts and slots are agent-scope accesses, which pass the L2 caches of the XCDs; a store is done when its
 // wavefront's count of memory operations says so (vmcnt), so that no cache has to be written back.
@@ -805,7 +806,7 @@ __device__ inline T load_part(const T* p) {
 }
 __device__ inline void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// One of 2^64 (and never 0).
+// A nonce as one of 2^64 words (never 0).
 __device__ inline uint64_t arrival_tag(uint32_t nonce) {
     uint64_t v = 0x9e3779b97f4a7c15ull * (nonce | uint64_t{1} << 32);
     v = (v ^ (v >> 30)) * 0xbf58476d1ce4e5b9ull;
@@ -826,7 +827,7 @@ __device__ inline bool arrive(uint64_t* slots, uint64_t* owner, uint32_t mine, u
         for (uint32_t i = threadIdx.x; i < n; i += kWave) there &= load_part(slots + i) == tag;
         bool one = __ballot(!there) == 0;
         if (threadIdx.x == 0) {
-            if (one) one = __hip_atomic_exchange(owner, tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != tag;
+            if (one) one = __hip_atomic_exchange(owner, ~tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != ~tag;
             *found = one ? 1 : 0;
         }
     }

@@ -52,8 +52,9 @@ class Launch:
         if not there:
             return False
         yield
-        before, self.mem[owner] = self.mem[owner], tag
-        return before != tag
+        taken = tag if self.counted else -TAG
+        before, self.mem[owner] = self.mem[owner], taken
+        return before != taken
 
     def workgroup(self, b):
         yield
@@ -131,6 +132,8 @@ def replays(blocks, most, kind, counted, seed, count):
             mem[a:b] = [CONSTANT] * (b - a)
         elif kind == "garbage":
             mem[:] = [rng.getrandbits(64) for _ in range(size)]
+        elif kind == "copies of its words":
+            mem[:] = [rng.choice(mem) for _ in range(size)]
         elif kind == "as it was":
             snapshot = list(mem) if snapshot is None else snapshot
             mem[:] = snapshot
@@ -138,7 +141,7 @@ def replays(blocks, most, kind, counted, seed, count):
 
 
 SHAPES = [(2, None), (5, None), (16, None), (40, None), (9, 4), (30, 8)]
-KINDS = ["nothing", "word 0", "a prefix", "a range", "garbage", "as it was"]
+KINDS = ["nothing", "word 0", "a prefix", "a range", "garbage", "copies of its words", "as it was"]
 
 
 @pytest.mark.parametrize("kind", KINDS)

@@ -92,3 +92,20 @@ def test_results_dropped_inside_of_a_graph(name):
             others = [torch.full((words,), 5, dtype=torch.int64, device="cuda") for _ in range(4)]
         replay_and_compare(make, call, graph, static, results, (name, words))
         assert all((t == 5).all() for t in others)
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_scratch_moved_within_itself_between_replays(name):
+    """What a launch has left in one word of scratch, another one holds at the next replay."""
+    make, call, need, groups = CALLS[name]()
+    for shift in (8, 16, 8 * groups, 16 * groups, need // 16 * 8):
+        announce(f"{name} scratch moved on by {shift} of {need} bytes in the graph")
+        static = make(torch.Generator(device="cuda").manual_seed(1))
+        scratch = torch.full((need + 16,), 3, dtype=torch.uint8, device="cuda")
+        call(static)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            results = call(static, scratch)
+            scratch.copy_(scratch.roll(shift))
+        replay_and_compare(make, call, graph, static, results, (name, shift))
